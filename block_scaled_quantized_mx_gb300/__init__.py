@@ -45,7 +45,9 @@ EXPORTS = ("mx_data_bytes", "mx_scale_bytes", "mx_quantize", "mx_gemm",
            "gemm_f16_workspace_bytes", "gemm_f16_splitk",
            "mx_gemm_splitk_noalloc", "mx_last_error",
            "mx_selftest_wait_timeout", "mx_scales_to_rowmajor",
-           "mx_status_string", "mx_version", "mx_set_tile_width")
+           "mx_status_string", "mx_version", "mx_set_tile_width",
+           "mx_kv_extend", "mx_kv_truncate", "mx_kv_append",
+           "mx_kv_attention_workspace_bytes", "mx_kv_attention")
 
 
 class MXError(RuntimeError):
@@ -64,6 +66,15 @@ class CMXTensor(ctypes.Structure):
 class CEpilogue(ctypes.Structure):
     """Mirror of struct mx_epilogue."""
     _fields_ = [("bias", ctypes.c_void_p), ("act", ctypes.c_int32)]
+
+
+class CKVCache(ctypes.Structure):
+    """Mirror of struct mx_kv_cache."""
+    _fields_ = [("k_data", ctypes.c_void_p), ("v_data", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("fmt", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("pages", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("d", ctypes.c_int64)]
 
 
 _lib = None
@@ -147,6 +158,21 @@ def lib() -> ctypes.CDLL:
     L.mx_version.argtypes = []
     L.mx_set_tile_width.restype = i32
     L.mx_set_tile_width.argtypes = [i32]
+    pc = ctypes.POINTER(CKVCache)
+    L.mx_kv_extend.restype = i32
+    L.mx_kv_extend.argtypes = [p, p, i64, p, i64, i64, p, i64, p, i32, p, p, p,
+                               i64, p, p]
+    L.mx_kv_truncate.restype = i32
+    L.mx_kv_truncate.argtypes = [p, p, i64, p, i64, i64, p, i64, p, i32, p, p,
+                                 p]
+    L.mx_kv_append.restype = i32
+    L.mx_kv_append.argtypes = [pc, p, p, i32, i64, i64, i64, i64, i64, p, p]
+    L.mx_kv_attention_workspace_bytes.restype = sz
+    L.mx_kv_attention_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    L.mx_kv_attention.restype = i32
+    L.mx_kv_attention.argtypes = [p, i32, i64, i64, i64, i64, pc, p, i64, i64,
+                                  p, p, i64, i64, p, i32, i64, i64, i32, i64,
+                                  ctypes.c_float, p, sz, p]
     _lib = L
     return L
 
@@ -493,6 +519,243 @@ def flash_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
 def flash_attention_workspace_bytes(BH: int, Lq: int, Lk: int, d: int) -> int:
     """Bytes of workspace flash_attention splits into (0: no split)."""
     return int(lib().flash_attention_workspace_bytes(BH, Lq, Lk, d))
+
+
+@dataclass
+class KVCache:
+    """An 8-bit paged key/value cache: code planes (uint8, pages x heads x page
+    x d), one UE8M0 scale byte for each page and head (uint8, pages x heads),
+    and the element format (E4M3, E5M2 or INT8)."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scales: torch.Tensor
+    v_scales: torch.Tensor
+    fmt: int
+
+    def __post_init__(self):
+        shape = self.k.shape
+        if len(shape) != 4 or self.v.shape != shape:
+            raise ValueError("k and v must be pages x heads x page x d")
+        if self.k_scales.shape != shape[:2] or self.v_scales.shape != shape[:2]:
+            raise ValueError("scales must be pages x heads")
+        for t in (self.k, self.v, self.k_scales, self.v_scales):
+            if t.dtype != torch.uint8 or not t.is_contiguous():
+                raise ValueError("a cache's planes are contiguous uint8 tensors")
+        pages, heads, page, d = shape
+        self._c = CKVCache(self.k.data_ptr(), self.v.data_ptr(),
+                           self.k_scales.data_ptr(), self.v_scales.data_ptr(),
+                           self.fmt, page, pages, heads, d)
+
+    def c(self) -> CKVCache:
+        c = self._c
+        if c.k_data != self.k.data_ptr() or c.v_data != self.v.data_ptr() or \
+                c.k_scales != self.k_scales.data_ptr() or \
+                c.v_scales != self.v_scales.data_ptr() or c.fmt != self.fmt:
+            self.__post_init__()                 # a plane was replaced
+        return self._c
+
+
+def empty_kv_cache(fmt: int, pages: int, heads: int, page: int, d: int,
+                   device="cuda") -> KVCache:
+    """A cache of uninitialised pages: a page means nothing until its first
+    token is appended."""
+    def u8(*shape):
+        return torch.empty(shape, dtype=torch.uint8, device=device)
+    return KVCache(u8(pages, heads, page, d), u8(pages, heads, page, d),
+                   u8(pages, heads), u8(pages, heads), fmt)
+
+
+@dataclass
+class KVPlan:
+    """What mx_kv_extend gives: the requests' new lengths, the offsets of
+    their new tokens, the tokens' slots, and [free pages, requests refused]."""
+    lens: torch.Tensor
+    cu: torch.Tensor
+    slots: torch.Tensor
+    counts: torch.Tensor
+
+
+@dataclass
+class KVCut:
+    """What mx_kv_truncate gives: the new lengths, and [free pages, pages the
+    stack had no room for]."""
+    lens: torch.Tensor
+    counts: torch.Tensor
+
+
+def _int32(t: torch.Tensor, name: str, n: int | None = None):
+    if t.dtype != torch.int32 or not t.is_cuda or t.dim() != 1 or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 1-D int32 CUDA tensor")
+    if n is not None and t.shape[0] < n:
+        raise ValueError(f"{name} must hold {n} values")
+
+
+def _check_table(table: torch.Tensor, requests: int):
+    if table.dtype != torch.int32 or not table.is_cuda or table.dim() != 2 or \
+            table.shape[0] < requests:
+        raise ValueError("table must be a 2-D int32 CUDA tensor with a row for "
+                         "each request")
+    if table.shape[1] > 1 and table.stride(1) != 1:
+        raise ValueError("table must have a unit inner stride")
+
+
+def _row_stride(table: torch.Tensor) -> int:
+    # the stride of a dimension of size 1 means nothing
+    return table.stride(0) if table.shape[0] > 1 else max(table.stride(0),
+                                                          table.shape[1])
+
+
+def mx_kv_extend(lens: torch.Tensor, new_tokens: torch.Tensor,
+                 table: torch.Tensor, stack: torch.Tensor, count: torch.Tensor,
+                 page: int, max_tokens: int, out: KVPlan | None = None,
+                 stream=None) -> KVPlan:
+    """Room for new tokens: pages from the stack of free ones into the
+    requests' rows of the block table (in place), and every new token's slot.
+    lens, new_tokens: int32, one per request; table: int32, requests x width;
+    stack, count: the free pages' ids and, in count[0], their number;
+    max_tokens: the most new tokens there may be (the length of slots).  A
+    request that finds no room, and every one behind it, is refused whole."""
+    B = lens.shape[0]
+    _int32(lens, "lens")
+    _int32(new_tokens, "new_tokens", B)
+    _int32(stack, "stack")
+    _int32(count, "count", 1)
+    _check_table(table, B)
+    if out is None:
+        e = lens.new_empty
+        out = KVPlan(e(B), e(B + 1), e(max_tokens, dtype=torch.int64), e(2))
+    else:
+        _int32(out.lens, "out.lens", B)
+        _int32(out.cu, "out.cu", B + 1)
+        _int32(out.counts, "out.counts", 2)
+        if out.slots.dtype != torch.int64 or not out.slots.is_cuda or \
+                not out.slots.is_contiguous() or out.slots.numel() < max_tokens:
+            raise ValueError("out.slots must hold max_tokens int64 values")
+    _check(lib().mx_kv_extend(
+        lens.data_ptr(), new_tokens.data_ptr(), B, table.data_ptr(),
+        _row_stride(table), table.shape[1], stack.data_ptr(), stack.shape[0],
+        count.data_ptr(), page, out.lens.data_ptr(), out.cu.data_ptr(),
+        out.slots.data_ptr(), max_tokens, out.counts.data_ptr(),
+        _stream(stream)), "mx_kv_extend")
+    return out
+
+
+def mx_kv_truncate(lens: torch.Tensor, keep: torch.Tensor, table: torch.Tensor,
+                   stack: torch.Tensor, count: torch.Tensor, page: int,
+                   out: KVCut | None = None, stream=None) -> KVCut:
+    """Drop tokens from the ends of requests: request b keeps keep[b] of its
+    tokens (0: it is finished).  Pages that become free go back on the stack
+    (in place) and their table entries become -1; an mx_kv_extend by as many
+    tokens hands out the same pages again."""
+    B = lens.shape[0]
+    _int32(lens, "lens")
+    _int32(keep, "keep", B)
+    _int32(stack, "stack")
+    _int32(count, "count", 1)
+    _check_table(table, B)
+    if out is None:
+        out = KVCut(lens.new_empty(B), lens.new_empty(2))
+    else:
+        _int32(out.lens, "out.lens", B)
+        _int32(out.counts, "out.counts", 2)
+    _check(lib().mx_kv_truncate(
+        lens.data_ptr(), keep.data_ptr(), B, table.data_ptr(),
+        _row_stride(table), table.shape[1], stack.data_ptr(), stack.shape[0],
+        count.data_ptr(), page, out.lens.data_ptr(), out.counts.data_ptr(),
+        _stream(stream)), "mx_kv_truncate")
+    return out
+
+
+def _kv_dtype(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in (torch.float16, torch.bfloat16) or not t.is_cuda or \
+            t.dim() != 3:
+        raise ValueError(f"{name} must be a tokens x heads x d fp16 or bf16 "
+                         "CUDA tensor")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must have a unit inner stride")
+    return DT_F16 if t.dtype == torch.float16 else DT_BF16
+
+
+def _kv_strides(t: torch.Tensor) -> tuple[int, int]:
+    # strides of dimensions of size 1 mean nothing
+    return (t.stride(0) if t.shape[0] > 1 else 0,
+            t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def mx_kv_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor,
+                 slots: torch.Tensor, stream=None) -> KVCache:
+    """Quantize new keys and values (tokens x heads x d, fp16 or bf16) into the
+    cache, in place, at their slots (int64, one per token; negative: none).
+    One power-of-two scale covers a page and head: where new tokens need a
+    larger one than the page has, the codes already there are rounded again."""
+    dt = _kv_dtype(K, "K")
+    if V.dtype != K.dtype or V.shape != K.shape:
+        raise ValueError("K and V must have one shape and type")
+    _kv_dtype(V, "V")
+    T = K.shape[0]
+    c = cache.c()
+    if K.shape[1] != c.heads or K.shape[2] != c.d:
+        raise ValueError("K and V must have the cache's heads and d")
+    if slots.dtype != torch.int64 or not slots.is_cuda or slots.dim() != 1 or \
+            not slots.is_contiguous() or slots.shape[0] < T:
+        raise ValueError("slots must be a contiguous int64 CUDA tensor, one "
+                         "for each token")
+    (kt, kh), (vt, vh) = _kv_strides(K), _kv_strides(V)
+    _check(lib().mx_kv_append(ctypes.byref(c), K.data_ptr(), V.data_ptr(), dt,
+                              T, kt, kh, vt, vh, slots.data_ptr(),
+                              _stream(stream)), "mx_kv_append")
+    return cache
+
+
+@functools.lru_cache(maxsize=1024)
+def kv_attention_workspace_bytes(q_heads: int, heads: int, d: int,
+                                 max_q: int) -> int:
+    """Bytes of workspace with which mx_kv_attention spreads a request's keys
+    over many SMs; the same for all lengths and numbers of requests."""
+    return int(lib().mx_kv_attention_workspace_bytes(q_heads, heads, d, max_q))
+
+
+def mx_kv_attention(Q: torch.Tensor, cache: KVCache, table: torch.Tensor,
+                    lens: torch.Tensor, cu: torch.Tensor, max_q: int,
+                    causal: bool = True, window: int = 0,
+                    scale: float | None = None, out_dtype=None,
+                    out: torch.Tensor | None = None, stream=None,
+                    workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of the requests' last tokens over the cache.  Q: tokens x
+    heads x d, fp16 or bf16, the rows of request b being cu[b] .. cu[b+1];
+    lens: the requests' lengths, those rows included; max_q: the most rows
+    any request has (or more).  causal: a row sees no key behind its own
+    position; window > 0: and only the last `window` of those.  scale
+    defaults to 1/sqrt(d), out_dtype to Q's.  With a device `workspace`
+    (uint8, kv_attention_workspace_bytes() long) a request's keys are spread
+    over many SMs.  Rows that belong to no request are not written."""
+    dt = _kv_dtype(Q, "Q")
+    T, Hq, d = Q.shape
+    c = cache.c()
+    if d != c.d or Hq % c.heads:
+        raise ValueError("Q must have the cache's d and a multiple of its heads")
+    B = lens.shape[0]
+    _int32(lens, "lens")
+    _int32(cu, "cu", B + 1)
+    _check_table(table, B)
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=out_dtype or Q.dtype,
+                          device=Q.device)
+    elif (out.shape != Q.shape or not out.is_cuda or out.stride(2) != 1
+          or (out_dtype is not None and out.dtype != out_dtype)):
+        raise ValueError("out must be a CUDA tensor of Q's shape and of type "
+                         "out_dtype, with a unit inner stride")
+    odt = _out_code(out.dtype, (torch.float32, torch.bfloat16, torch.float16))
+    (qt, qh), (ot, oh) = _kv_strides(Q), _kv_strides(out)
+    _check(lib().mx_kv_attention(
+        Q.data_ptr(), dt, T, Hq, qt, qh, ctypes.byref(c), table.data_ptr(),
+        _row_stride(table), table.shape[1], lens.data_ptr(), cu.data_ptr(), B,
+        max_q, out.data_ptr(), odt, ot, oh, int(bool(causal)), int(window),
+        1.0 / float(d) ** 0.5 if scale is None else float(scale),
+        workspace.data_ptr() if workspace is not None else None,
+        _nbytes(workspace), _stream(stream)), "mx_kv_attention")
+    return out
 
 
 def mx_last_error(stream=None) -> int:

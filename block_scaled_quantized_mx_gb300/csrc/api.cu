@@ -11,6 +11,7 @@
 
 #include "mx.h"
 #include "common.cuh"
+#include "kv_common.cuh"
 
 namespace {
 
@@ -301,6 +302,168 @@ mx_status flash_attention_splitkv(const void* Q, const void* K, const void* V, v
                    stream);
 }
 
+namespace {
+
+bool is_page(int32_t page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+
+mx_status check_cache(const mx_kv_cache* c, mxk::KvCache* out) {
+  if (!c) return MX_ERR_INVALID_ARG;
+  if (c->fmt != MX_FMT_E4M3 && c->fmt != MX_FMT_E5M2 && c->fmt != MX_FMT_INT8)
+    return MX_ERR_INVALID_ARG;
+  if (!is_page(c->page) || (c->d != 64 && c->d != 128)) return MX_ERR_SHAPE;
+  if (c->heads < 1 || c->heads > 65535 || c->pages < 1 ||
+      c->pages > kMaxDim / (c->heads * c->page))
+    return MX_ERR_SHAPE;
+  if (!c->k_data || !c->v_data || !c->k_scales || !c->v_scales) return MX_ERR_INVALID_ARG;
+  if (!aligned16(c->k_data) || !aligned16(c->v_data)) return MX_ERR_ALIGN;
+  out->k = static_cast<uint8_t*>(c->k_data);
+  out->v = static_cast<uint8_t*>(c->v_data);
+  out->k_scales = c->k_scales;
+  out->v_scales = c->v_scales;
+  out->fmt = c->fmt;
+  out->page = c->page;
+  out->pages = c->pages;
+  out->heads = c->heads;
+  out->d = c->d;
+  return MX_OK;
+}
+
+// Token and head strides of a tokens x heads x d operand of 16- or 32-bit
+// elements: multiples of 8, heads not overlapping (a stride is free where
+// there is only one of its kind).
+mx_status check_strides(int64_t tokens, int64_t heads, int64_t ts, int64_t hs, int64_t d) {
+  if (ts % 8 || hs % 8) return MX_ERR_SHAPE;
+  if (heads > 1 && hs < d) return MX_ERR_SHAPE;
+  if (tokens > 1 && ts < d) return MX_ERR_SHAPE;
+  return MX_OK;
+}
+
+mx_status check_pages_call(int64_t requests, int64_t stride, int64_t width, int64_t stack_size,
+                           int32_t page) {
+  if (!is_page(page)) return MX_ERR_SHAPE;
+  if (requests < 0 || requests > 16384 || width < 1 || stride < width || stack_size < 0 ||
+      width > kMaxDim || stride > kMaxDim || stack_size > kMaxDim)
+    return MX_ERR_SHAPE;
+  return MX_OK;
+}
+
+}  // namespace
+
+mx_status mx_kv_extend(const int32_t* lens, const int32_t* new_tokens, int64_t requests,
+                       int32_t* table, int64_t table_stride, int64_t table_width,
+                       const int32_t* stack, int64_t stack_size, const int32_t* count,
+                       int32_t page, int32_t* lens_out, int32_t* cu, int64_t* slots,
+                       int64_t max_tokens, int32_t* counts_out, void* stream) {
+  mx_status s = check_pages_call(requests, table_stride, table_width, stack_size, page);
+  if (s != MX_OK) return s;
+  if (max_tokens < 0 || max_tokens > kMaxDim) return MX_ERR_SHAPE;
+  if (requests > 0 && (!lens || !new_tokens || !table || !lens_out)) return MX_ERR_INVALID_ARG;
+  if ((stack_size > 0 && !stack) || (max_tokens > 0 && !slots) || !count || !cu || !counts_out)
+    return MX_ERR_INVALID_ARG;
+  if ((s = check_device()) != MX_OK) return s;
+  return from_cuda(mxk::launch_kv_extend(lens, new_tokens, requests, table, table_stride,
+                                         table_width, stack, stack_size, count, page, lens_out,
+                                         cu, slots, max_tokens, counts_out,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+mx_status mx_kv_truncate(const int32_t* lens, const int32_t* keep, int64_t requests,
+                         int32_t* table, int64_t table_stride, int64_t table_width,
+                         int32_t* stack, int64_t stack_size, const int32_t* count, int32_t page,
+                         int32_t* lens_out, int32_t* counts_out, void* stream) {
+  mx_status s = check_pages_call(requests, table_stride, table_width, stack_size, page);
+  if (s != MX_OK) return s;
+  if (requests > 0 && (!lens || !keep || !table || !lens_out)) return MX_ERR_INVALID_ARG;
+  if ((stack_size > 0 && !stack) || !count || !counts_out) return MX_ERR_INVALID_ARG;
+  if ((s = check_device()) != MX_OK) return s;
+  return from_cuda(mxk::launch_kv_truncate(lens, keep, requests, table, table_stride,
+                                           table_width, stack, stack_size, count, page, lens_out,
+                                           counts_out, static_cast<cudaStream_t>(stream)));
+}
+
+mx_status mx_kv_append(const mx_kv_cache* cache, const void* K, const void* V, int32_t dtype,
+                       int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
+                       int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots,
+                       void* stream) {
+  mxk::KvCache c;
+  mx_status s = check_cache(cache, &c);
+  if (s != MX_OK) return s;
+  if (dtype != MX_DT_F16 && dtype != MX_DT_BF16) return MX_ERR_INVALID_ARG;
+  if (tokens < 0 || tokens > kMaxDim) return MX_ERR_SHAPE;
+  if (tokens == 0) return MX_OK;
+  if (!K || !V || !slots) return MX_ERR_INVALID_ARG;
+  if ((s = check_strides(tokens, c.heads, k_token_stride, k_head_stride, c.d)) != MX_OK) return s;
+  if ((s = check_strides(tokens, c.heads, v_token_stride, v_head_stride, c.d)) != MX_OK) return s;
+  if (!aligned16(K) || !aligned16(V)) return MX_ERR_ALIGN;
+  if ((s = check_device()) != MX_OK) return s;
+  return from_cuda(mxk::launch_kv_append(c, K, V, dtype, tokens, k_token_stride, k_head_stride,
+                                         v_token_stride, v_head_stride, slots,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+size_t mx_kv_attention_workspace_bytes(int64_t q_heads, int64_t heads, int64_t d, int64_t max_q) {
+  if (heads < 1 || heads > 65535 || q_heads < 1 || q_heads % heads || (d != 64 && d != 128) ||
+      max_q < 1 || max_q > kMaxDim)
+    return 0;
+  if (check_device() != MX_OK) return 0;
+  return mxk::kv_attention_workspace_bytes(q_heads, heads, d, max_q);
+}
+
+mx_status mx_kv_attention(const void* Q, int32_t dtype, int64_t tokens, int64_t q_heads,
+                          int64_t q_token_stride, int64_t q_head_stride,
+                          const mx_kv_cache* cache, const int32_t* table, int64_t table_stride,
+                          int64_t table_width, const int32_t* lens, const int32_t* cu,
+                          int64_t requests, int64_t max_q, void* O, int32_t o_dtype,
+                          int64_t o_token_stride, int64_t o_head_stride, int32_t causal,
+                          int64_t window, float scale, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  mxk::KvAttn a{};
+  mx_status s = check_cache(cache, &a.cache);
+  if (s != MX_OK) return s;
+  if (dtype != MX_DT_F16 && dtype != MX_DT_BF16) return MX_ERR_INVALID_ARG;
+  if (o_dtype != MX_DT_F32 && o_dtype != MX_DT_BF16 && o_dtype != MX_DT_F16)
+    return MX_ERR_INVALID_ARG;
+  if (!(scale == scale) || scale > 3.0e38f || scale < -3.0e38f) return MX_ERR_INVALID_ARG;
+  if ((causal != 0 && causal != 1) || window < 0) return MX_ERR_INVALID_ARG;
+  const int64_t d = a.cache.d;
+  if (q_heads < 1 || q_heads % a.cache.heads) return MX_ERR_SHAPE;
+  // rows of one cache head are counted in 32 bits
+  if (tokens < 0 || tokens > kMaxDim / (q_heads / a.cache.heads)) return MX_ERR_SHAPE;
+  if (requests < 0 || requests > kMaxDim || max_q < 0 || max_q > kMaxDim) return MX_ERR_SHAPE;
+  if (table_width < 1 || table_stride < table_width || table_width > kMaxDim ||
+      table_stride > kMaxDim)
+    return MX_ERR_SHAPE;
+  if (tokens == 0 || requests == 0) return MX_OK;
+  if (!Q || !O || !table || !lens || !cu) return MX_ERR_INVALID_ARG;
+  if ((s = check_strides(tokens, q_heads, q_token_stride, q_head_stride, d)) != MX_OK) return s;
+  if ((s = check_strides(tokens, q_heads, o_token_stride, o_head_stride, d)) != MX_OK) return s;
+  if (!aligned16(Q) || !aligned16(O) || (workspace && !aligned16(workspace))) return MX_ERR_ALIGN;
+  if ((s = check_device()) != MX_OK) return s;
+  a.Q = Q;
+  a.dtype = dtype;
+  a.tokens = tokens;
+  a.q_heads = q_heads;
+  a.q_ts = q_token_stride;
+  a.q_hs = q_head_stride;
+  a.table = table;
+  a.table_stride = table_stride;
+  a.width = table_width;
+  a.lens = lens;
+  a.cu = cu;
+  a.requests = requests;
+  a.max_q = max_q;
+  a.O = O;
+  a.o_dtype = o_dtype;
+  a.o_ts = o_token_stride;
+  a.o_hs = o_head_stride;
+  a.causal = causal;
+  a.window = window;
+  a.scale = scale;
+  a.ws = workspace;
+  a.ws_bytes = workspace_bytes;
+  return from_cuda(mxk::launch_kv_attention(a, static_cast<cudaStream_t>(stream)));
+}
+
 mx_status gemm_f16(const void* A, const void* B, float* C, int32_t ab_dtype, int64_t M,
                    int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc,
                    void* stream) {
@@ -336,12 +499,13 @@ mx_status mx_last_error(void* stream) {
   cudaError_t e3 = cudaSuccess, e4 = cudaSuccess;
   const unsigned c = mxk::fetch_and_clear_status_dq(&e3);
   const unsigned d = mxk::fetch_and_clear_status_attn(&e4);
-  cudaError_t e5 = cudaSuccess;
+  cudaError_t e5 = cudaSuccess, e6 = cudaSuccess;
   const unsigned f = mxk::fetch_and_clear_status_dqd(&e5);
+  const unsigned g = mxk::fetch_and_clear_status_kv(&e6);
   if (e1 != cudaSuccess || e2 != cudaSuccess || e3 != cudaSuccess || e4 != cudaSuccess ||
-      e5 != cudaSuccess)
+      e5 != cudaSuccess || e6 != cudaSuccess)
     return MX_ERR_CUDA;
-  if ((a | b | c | d | f) & mxk::STATUS_TIMEOUT) return MX_ERR_TIMEOUT;
+  if ((a | b | c | d | f | g) & mxk::STATUS_TIMEOUT) return MX_ERR_TIMEOUT;
   return MX_OK;
 }
 

@@ -412,6 +412,161 @@ mx_status gemm_f16_splitk(const void* A, const void* B, float* C,
 mx_status mx_gemm_splitk_noalloc(const mx_tensor* A, const mx_tensor* B, void* C,
                                  int32_t c_dtype, int64_t ldc, void* stream);
 
+/*
+ * The 8-bit paged key/value cache.
+ *
+ * A cache holds `pages` pages of `page` tokens for each of `heads` heads of d
+ * values, keys and values apart.  The codes of one page and head lie together:
+ * the code of (page p, head h, token t of the page, value i) is byte
+ * ((p * heads + h) * page + t) * d + i of the plane; its scale is the UE8M0 byte
+ * p * heads + h (value 2^(c - 127), 0xFF = NaN): one scale for each block of
+ * `page` tokens and head.  An element's value is code * scale.
+ *
+ *   k_data, v_data      device, pages * heads * page * d bytes, 16-byte aligned
+ *   k_scales, v_scales  device, pages * heads bytes
+ *   fmt                 MX_FMT_E4M3, MX_FMT_E5M2 or MX_FMT_INT8
+ *   page                16, 32, 64 or 128
+ *   d                   64 or 128;  heads 1 .. 65535;  pages >= 1, with
+ *                       pages * heads * page < 2^31
+ * A request's tokens live in the pages that its row of the block table names
+ * (int32, entry j: the page of tokens j * page ..), in order; -1 where there is
+ * none.  A slot (int64) names one token's place: page id * page + offset.
+ */
+typedef struct mx_kv_cache {
+  void* k_data;
+  void* v_data;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+  int32_t fmt;
+  int32_t page;
+  int64_t pages;
+  int64_t heads;
+  int64_t d;
+} mx_kv_cache;
+
+/*
+ * mx_kv_extend -- give requests room for new tokens: pages from the stack of
+ * free pages into the block tables, and the slot of every new token.
+ *
+ * Request b holds lens[b] tokens and gets new_tokens[b] more.  Of the pages
+ * that the requests need, in request order, the i-th is stack[count - 1 - i].
+ * A request with a negative length or count, or with more tokens than its
+ * row of the table has room for, is refused by itself; the first other
+ * request that the free pages or max_tokens do not suffice for, and every
+ * request behind it, is refused too.  A refused request keeps its length and
+ * gets no tokens; nothing is half done.
+ *
+ *   lens, new_tokens  device, int32, requests entries
+ *   table             device, int32, requests rows of table_width entries,
+ *                     table_stride apart; new entries are written
+ *   stack, count      device, int32: the ids of the free pages (stack_size
+ *                     entries, the first *count of them free), and *count
+ *   lens_out          device, int32, requests entries: the new lengths
+ *   cu                device, int32, requests + 1 entries: cu[b] the first of
+ *                     request b's tokens among all new tokens, cu[requests]
+ *                     their number (what mx_kv_attention takes)
+ *   slots             device, int64, max_tokens entries: the new tokens'
+ *                     slots in that order, -1 behind the last
+ *   counts_out        device, int32, 2 entries: free pages left, requests
+ *                     refused
+ * lens_out may be lens, and counts_out may be count.  requests <= 16384.
+ */
+mx_status mx_kv_extend(const int32_t* lens, const int32_t* new_tokens, int64_t requests,
+                       int32_t* table, int64_t table_stride, int64_t table_width,
+                       const int32_t* stack, int64_t stack_size, const int32_t* count,
+                       int32_t page, int32_t* lens_out, int32_t* cu, int64_t* slots,
+                       int64_t max_tokens, int32_t* counts_out, void* stream);
+
+/*
+ * mx_kv_truncate -- drop tokens from the ends of requests (drafted tokens that
+ * were rejected; keep 0 for a finished request).  Request b keeps
+ * min(max(keep[b], 0), lens[b]) tokens; the pages behind them go back on the
+ * stack and their table entries become -1.  Of the n pages freed (in request
+ * order, then table order) the i-th is written to stack[count + n - 1 - i], so
+ * that an mx_kv_extend by as many tokens hands out the same pages again.
+ * counts_out: free pages, and pages that the stack had no room for (0 when
+ * stack_size is the cache's number of pages).  The rest as above.
+ */
+mx_status mx_kv_truncate(const int32_t* lens, const int32_t* keep, int64_t requests,
+                         int32_t* table, int64_t table_stride, int64_t table_width,
+                         int32_t* stack, int64_t stack_size, const int32_t* count, int32_t page,
+                         int32_t* lens_out, int32_t* counts_out, void* stream);
+
+/*
+ * mx_kv_append -- quantize new keys and values into the cache.
+ *
+ * Let e be the OCP MX scale code (the rule of mx_quantize, over a block of all
+ * the tokens that this call adds to a page of one head).  A page whose first
+ * token is among them gets the scale s = e.  One that already held tokens
+ * gets s = max(s_old, e), and if that is larger than s_old the codes in front
+ * of the new tokens are rounded again, to nearest even, under the new scale.
+ * New codes are x * 2^(127 - s), rounded to nearest even and saturated.  A NaN
+ * or an infinity among the new values makes s 0xFF (NaN) and the new codes
+ * 0; the page stays NaN until its first token is written anew.
+ *
+ *   K, V    device, tokens x heads x d of dtype (MX_DT_BF16 / MX_DT_F16): the
+ *           value (t, h, i) at element t * token_stride + h * head_stride + i;
+ *           16-byte aligned, strides multiples of 8 elements
+ *   slots   device, int64, one per token; a slot that is negative or lies
+ *           beyond the cache writes nothing
+ * The tokens that a call adds to one page must be neighbours in slots with
+ * consecutive slots (as mx_kv_extend makes them): a page is written by the
+ * run of tokens that begins in it.
+ */
+mx_status mx_kv_append(const mx_kv_cache* cache, const void* K, const void* V, int32_t dtype,
+                       int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
+                       int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots,
+                       void* stream);
+
+/*
+ * mx_kv_attention -- attention of new queries over the cache.
+ *
+ * Rows cu[b] .. cu[b + 1] - 1 of Q are the last n = cu[b + 1] - cu[b] tokens of
+ * request b, whose length lens[b] counts them: row cu[b] + i stands at position
+ * p = lens[b] - n + i.  Query head h reads cache head h / (q_heads / heads):
+ *   o = sum_j w_j v_j,  w = softmax over the visible j of scale * q . k_j
+ * Visible are j < lens[b], with `causal` j <= p, with window > 0 also
+ * j > p - window.  A row that sees nothing is 0.
+ *
+ *   Q        device, tokens x q_heads x d of dtype (MX_DT_BF16 / MX_DT_F16), at
+ *            element t * q_token_stride + h * q_head_stride; O likewise, of
+ *            o_dtype (MX_DT_F32, MX_DT_BF16, MX_DT_F16).  16-byte aligned,
+ *            strides multiples of 8 elements.  Rows outside every request are
+ *            not written.
+ *   table    device, int32, requests rows of table_width entries.  Entries
+ *            behind a request's last page (and, with a window, pages that no
+ *            row sees) are never followed; a page id outside the cache makes
+ *            the rows that see it NaN.
+ *   lens, cu device, int32, requests and requests + 1 entries
+ *   max_q    the largest n of any request, or more (picks the kernel; results
+ *            are right for any value)
+ *   q_heads  a multiple of the cache's heads
+ *   scale    finite
+ * The scores, sums and outputs accumulate in fp32; probabilities are rounded
+ * to f16 before the product with V, whose codes are exact in f16, so each
+ * weight is off by at most 2^-11 relative; Q's values below 2^-14 of their
+ * row's largest are rounded to 2^-25 of it.  Codes that stand for NaN or
+ * infinity (which mx_kv_append never writes) reach every row that shares a
+ * tile with them.
+ *
+ *   workspace  device, 16-byte aligned, caller-owned scratch of at least
+ *              mx_kv_attention_workspace_bytes() bytes, as for the K-split
+ *              calls (contents on entry do not matter; not shared by calls
+ *              that run at the same time).  With it the keys of one request
+ *              are spread over many SMs; NULL or a smaller size: they are not.
+ * mx_kv_attention_workspace_bytes does not depend on lengths or the number of
+ * requests; 0 on bad arguments or without a compute capability 10.3 device.
+ */
+size_t mx_kv_attention_workspace_bytes(int64_t q_heads, int64_t heads, int64_t d, int64_t max_q);
+mx_status mx_kv_attention(const void* Q, int32_t dtype, int64_t tokens, int64_t q_heads,
+                          int64_t q_token_stride, int64_t q_head_stride,
+                          const mx_kv_cache* cache, const int32_t* table, int64_t table_stride,
+                          int64_t table_width, const int32_t* lens, const int32_t* cu,
+                          int64_t requests, int64_t max_q, void* O, int32_t o_dtype,
+                          int64_t o_token_stride, int64_t o_head_stride, int32_t causal,
+                          int64_t window, float scale, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
 /* Synchronize the stream, then return (and clear) the first error recorded
  * by a kernel of this library on the current device: MX_OK,
  * MX_ERR_TIMEOUT, or MX_ERR_CUDA if the synchronization itself failed. */
