@@ -171,9 +171,6 @@ bool plain_epilogue(const Epilogue& e) {
 
 }  // namespace
 
-// The same tags for the other kernels whose units are split (kvattn.cu).
-unsigned long long next_split_tag() { return next_tag(); }
-
 static PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (!fn) {

@@ -161,7 +161,4 @@ inline bool kv_tensor_map(CUtensorMap* m, const void* p, const KvCache& c) {
                       c.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-// A launch's tag for the counters of split units (gemm.cu).
-unsigned long long next_split_tag();
-
 }  // namespace mxk

@@ -1,4 +1,5 @@
-// kvattn.cu -- attention over the 8-bit paged key/value cache.
+// kvattn.cu -- attention over the 8-bit paged key/value cache, for few query
+// rows per request (single tokens, drafts).
 //
 //   x_ij = scale * q_i . k_j,  o_i = sum_j softmax_j(x_ij) v_j
 // over the keys j that query i may see (j < length, not behind its own
@@ -9,36 +10,43 @@
 // a stream over pages that never widens them in memory:
 //   * work is cut evenly, not by request: the key tiles of every (request,
 //     row tile, cache head) form one list and each CTA takes an equal
-//     stretch of it, two CTAs per SM.  A long request is spread over many
-//     CTAs, many short ones share one;
-//   * a producer warp reads the block table and loads each page's P x d codes
-//     with one TMA box (swizzled, so that the reads below are free of bank
-//     conflicts), three tiles of 128 keys ahead; pages that a request does
-//     not have are not loaded;
-//   * four warps each take 32 keys of a tile, with their own running maximum
-//     and sum (no barrier per tile): codes become f16 in registers (exact for
-//     all three formats) and feed mma.sync m16n8k16, up to 16 rows (tokens x
-//     heads of the group) against 8 keys.  The contraction order is permuted
-//     so that a lane's 32 consecutive codes of a key are its share of the B
-//     operand: no transposition in memory for K, a byte permute for V;
+//     stretch of it.  A long request is spread over many CTAs, many short
+//     ones share one;
+//   * a producer warp walks the stretch: it brings the rows of Q to f16, reads
+//     the block table and loads each page's P x d codes with one TMA box
+//     (swizzled, so that the reads below are free of bank conflicts), ahead of
+//     the consumers; pages that a request does not have are not loaded;
+//   * four consumer warps each take 32 keys of a 128-key tile, with their own
+//     running maximum and sum (no barrier per tile): codes become f16 in
+//     registers (exact for all three formats) and feed mma.sync m16n8k16 with
+//     the keys (S = K Q^T) and then V's columns (O = V^T P) as the 16 rows
+//     and the query rows as the 8 columns.  The contraction order is permuted
+//     so that a lane's consecutive codes of a key are its share of the
+//     operand: K needs no transposition, V a byte permute, P one movmatrix;
 //   * page scales never touch the codes: K's multiplies the score, V's the
 //     probability, which as a power of two is exact.
-// The scores and the tensor work of 16 rows need a few percent of the tensor
-// rate, so mma.sync suffices here; long query runs go to kvprompt.cu.
+// With rows as the narrow side of the product, eight rows (a group of up to
+// eight heads) cost half the products, exponentials and registers of sixteen:
+// the kernel comes with 8 rows (three CTAs an SM) and 16 (two CTAs).
 //
 // Precision.  Q is brought to f16 with a power of two per row (so that its
 // largest value is in [1, 2): what f16 drops is 2^-25 of it, as fp32
 // accumulation would), scores, sums and outputs accumulate in fp32, and P is
-// rounded to f16 (relative 2^-11 of each weight at most).  P carries V's scale relative to the largest
-// so far: p 2^(7 + s - s_max), at most 2^15 with the exponentials' slack of
-// 2^8, so that a page whose values are 2^20 smaller than another's still
-// contributes with full precision.
+// rounded to f16 (relative 2^-11 of each weight at most).  P carries V's scale
+// relative to the largest so far: p 2^(7 + s - s_max), at most 2^15 with the
+// exponentials' slack of 2^8, so that a page whose values are 2^20 smaller than
+// another's still contributes with full precision.
 //
 // A unit cut between CTAs leaves its parts (un-normalised O, maximum, sum) in
-// the workspace; the CTA that completes the unit's count adds them in CTA
-// order, so results do not depend on timing.  Every wait is bounded.
+// the workspace, and a second, small kernel joins them in a fixed order.  It
+// is launched as a programmatic dependent, so that its start-up hides behind
+// the first.  (Counting the parts' arrivals in memory and letting the last
+// one join them took 27 us after the last tile with 57 CTAs to a unit, 131072
+// keys in 8 cache heads: every arrival waited for its turn on the counter,
+// and one CTA did all the adding.)  Every wait is bounded.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "common.cuh"
@@ -55,29 +63,68 @@ __device__ unsigned int g_status_kv = 0;
 
 constexpr int KA_TK = 128;                 // keys per tile
 constexpr int KA_WARPS = 4;                // consumer warps
-constexpr int KA_KW = KA_TK / KA_WARPS;    // keys of a tile per warp
-constexpr int KA_THREADS = 32 * (KA_WARPS + 1);
-constexpr int KA_ROWS = 16;                // rows of a unit
+constexpr int KA_KW = KA_TK / KA_WARPS;    // keys of a tile per warp: two steps of 16
+constexpr int KA_CONS = 32 * KA_WARPS;
+constexpr int KA_THREADS = KA_CONS + 32;
 constexpr int KA_MAX_PAGES = KA_TK / 16;   // pages in a tile
 constexpr float KA_LAZY = 8.0f;            // slack of the exponentials' reference point
 constexpr int KA_P_EXP = 7;                // P is scaled by 2^7: at most 2^(7 + 8) in f16
+constexpr int KA_RED = 36;                 // floats per row of the staging: 32, padded
 
-template <int D>
+// CTAs per SM of the 8-row (NR = 1) and the 16-row (NR = 2) kernel.
+template <int NR>
+constexpr int ka_ctas_per_sm() {
+  return NR == 1 ? 3 : 2;
+}
+
+// What the producer says about a segment: one CTA's part of a unit.
+template <int ROWS>
+struct KaSeg {
+  int tile, count;             // first key tile, number (0: no more segments)
+  int len;                     // the request's length
+  int live;                    // rows of the unit that exist
+  int all_lo, all_hi;          // keys that every live row sees: no mask needed
+  int any_lo, any_hi;          // keys that some row sees
+  int part;                    // the unit is shared with other CTAs
+  int slot;                    // workspace slot of the part
+  float fr[ROWS];              // scale * log2 e * the row's power of two
+  int lo[ROWS], hi[ROWS];      // keys [lo, hi) that the row sees
+  long long out[ROWS];         // the row's first element of O
+};
+
+// A unit that begins in this CTA's stretch and goes on in others': what the
+// joining kernel needs (live 0: there is none).
+template <int ROWS>
+struct KaJoin {
+  int live;                    // rows
+  int parts;                   // CTAs that share it: this one and the next ones
+  int first_slot;              // this CTA's slot; the others use their first
+  int pad;
+  long long out[ROWS];         // the rows' first elements of O
+};
+
+template <int D, int NR>
 struct KaSmem {
+  static constexpr int ROWS = 8 * NR;
   static constexpr int TILE = KA_TK * D;               // codes of one tile of K or V
-  static constexpr int STAGES = 98304 / (2 * TILE);    // 3 (d 128) or 6 (d 64)
-  static constexpr int RING = STAGES * 2 * TILE;
-  // staging of the warps' O: [warp][row][32 columns]
+  static constexpr int RING = NR == 1 ? 65536 : 98304;
+  static constexpr int STAGES = RING / (2 * TILE);
+  // staging of the warps' O: [warp][8 rows][KA_RED]
   static constexpr int RED_OFF = RING;
-  static constexpr int RED_BYTES = KA_WARPS * KA_ROWS * 32 * 4;
-  static constexpr int ML_OFF = RED_OFF + RED_BYTES;   // m, l, e: [3][warp][row]
-  static constexpr int PG_OFF = ML_OFF + 3 * KA_WARPS * KA_ROWS * 4;
-  static constexpr int PG_STAGE = KA_MAX_PAGES * 8;    // per page: K scale, V exponent
+  static constexpr int RED_BYTES = KA_WARPS * 8 * KA_RED * 4;
+  // Q fragments, two slots of [row tile][D / 32][lane] x 16 bytes
+  static constexpr int Q_OFF = RED_OFF + RED_BYTES;
+  static constexpr int Q_SLOT = NR * (D / 32) * 512;
+  static constexpr int SEG_OFF = Q_OFF + 2 * Q_SLOT;
+  static constexpr int SEG_BYTES = (sizeof(KaSeg<ROWS>) + 15) / 16 * 16;
+  static constexpr int ML_OFF = SEG_OFF + 2 * SEG_BYTES;     // m, l: [2][warp][row], e: [warp]
+  static constexpr int PG_OFF = ML_OFF + 2 * KA_WARPS * ROWS * 4 + 16;
+  static constexpr int PG_STAGE = KA_MAX_PAGES * 8;          // per page: K scale, V exponent
   static constexpr int BAR_OFF = PG_OFF + STAGES * PG_STAGE;
-  static constexpr int MISC_OFF = BAR_OFF + STAGES * 16;
-  static constexpr int TOTAL = MISC_OFF + 64;
+  static constexpr int MISC_OFF = BAR_OFF + STAGES * 16 + 32;
+  static constexpr int TOTAL = MISC_OFF + 128;
   static constexpr int ALLOC = TOTAL + 1024;
-  static_assert(2 * (ALLOC + 1024) <= 233472, "two CTAs per SM");
+  static_assert(ka_ctas_per_sm<NR>() * (ALLOC + 1024) <= 233472, "CTAs per SM");
 };
 
 struct KaArgs {
@@ -89,9 +136,8 @@ struct KaArgs {
   int o_dtype;
   float scale_log2e;
   int skip_rows;               // requests with more rows than this are another kernel's
-  float* ws;                   // parts: [2 CTAs' slots][16 rows][D], then m, l: [slot][2][16]
-  unsigned long long* ctr;
-  unsigned long long tag;
+  float* ws;                   // two slots per CTA: [rows][D] of O, then m[rows], l[rows]
+  uint8_t* joins;              // one KaJoin per CTA, behind the slots
 };
 
 __device__ __forceinline__ void ka_timeout(volatile int* abort, unsigned site) {
@@ -108,95 +154,110 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Count one arrival (see the K-split's counters in the GEMM: tag << 16 |
-// count, a word with another tag counts as zero, completion leaves zero).
-__device__ __forceinline__ int ka_arrive(unsigned long long* ctr, unsigned long long tag,
-                                         int target) {
-  unsigned long long v = 0ull;
-  for (int i = 0; i < (1 << 16); ++i) {
-    const unsigned long long cnt = ((v >> 16) == tag) ? (v & 0xFFFFull) : 0ull;
-    const unsigned long long nv =
-        (cnt + 1 == static_cast<unsigned long long>(target)) ? 0ull : (tag << 16) | (cnt + 1);
-    const unsigned long long old = atomicCAS(ctr, v, nv);
-    if (old == v) return static_cast<int>(cnt + 1);
-    v = old;
-  }
-  return -1;
-}
-
 // One request's share of the work list.
 struct KaReq {
   KvReq r;
-  int tiles;                   // key tiles of each of its units
+  int tiles;                   // key tiles of each of its units, and one for its overhead
   int tile0;                   // its first tile
   int row_tiles;
   long long units;             // row tiles x cache heads; 0: nothing for this kernel
 };
 
+template <int ROWS>
 __device__ __forceinline__ KaReq ka_request(const KaArgs& a, int b) {
   KaReq q;
   q.r = kv_request(a.v, b);
   const long long rows = static_cast<long long>(q.r.n) * a.v.group;
   const int first = kv_first_key(a.v, q.r, 0);
   q.tile0 = first / KA_TK;
-  q.tiles = max(1, (q.r.len + KA_TK - 1) / KA_TK - q.tile0);
-  q.row_tiles = rows > a.skip_rows ? 0 : static_cast<int>((rows + KA_ROWS - 1) / KA_ROWS);
+  q.tiles = 1 + max(1, (q.r.len + KA_TK - 1) / KA_TK - q.tile0);
+  q.row_tiles = rows > a.skip_rows ? 0 : static_cast<int>((rows + ROWS - 1) / ROWS);
   q.units = static_cast<long long>(q.row_tiles) * a.v.heads;
   return q;
 }
 
-// The walk over one CTA's stretch of the list; every role runs it alike.
+// The walk over one CTA's stretch of the list.  Each unit stands in it with
+// its tiles behind one entry more, for the time it takes to begin and end a
+// unit (about that of a tile): without it a stretch of many short units took
+// 68 us where the median took 43 (48 requests of 0 to 6000 keys, window 2048).
+template <int ROWS>
 struct KaWalk {
-  long long w, w1;             // next tile of the list, end of the stretch
-  long long base;              // first tile of request b
+  long long w, w1;             // next entry of the list, end of the stretch
+  long long base;              // first entry of request b
   int b;
   KaReq q;
   // the current segment
   int head, row_tile, tile, count;
   bool begins, ends;
-  long long unit_start, unit_end;
+  long long unit_start, unit_end;   // the unit's first tile's entry, its end
 
   __device__ __forceinline__ bool next(const KaArgs& a) {
-    if (w >= w1) return false;
-    while (w >= base + q.units * q.tiles) {
-      base += q.units * q.tiles;
-      if (++b >= a.v.requests) return false;
-      q = ka_request(a, b);
+    while (w < w1) {
+      while (w >= base + q.units * q.tiles) {
+        base += q.units * q.tiles;
+        if (++b >= a.v.requests) return false;
+        q = ka_request<ROWS>(a, b);
+      }
+      const long long u = (w - base) / q.tiles;
+      int t = static_cast<int>((w - base) - u * q.tiles);   // 0: the extra entry
+      if (t == 0) {
+        t = 1;
+        if (++w >= w1) return false;          // the unit's tiles are the next CTA's
+      }
+      head = static_cast<int>(u % a.v.heads);
+      row_tile = static_cast<int>(u / a.v.heads);
+      unit_start = base + u * q.tiles + 1;
+      unit_end = unit_start + q.tiles - 1;
+      tile = q.tile0 + t - 1;
+      count = static_cast<int>(min(static_cast<long long>(q.tiles - t), w1 - w));
+      begins = t == 1;
+      ends = t + count == q.tiles;
+      w += count;
+      return true;
     }
-    const long long u = (w - base) / q.tiles;
-    const int t = static_cast<int>((w - base) - u * q.tiles);
-    head = static_cast<int>(u % a.v.heads);
-    row_tile = static_cast<int>(u / a.v.heads);
-    unit_start = base + u * q.tiles;
-    unit_end = unit_start + q.tiles;
-    tile = q.tile0 + t;
-    count = static_cast<int>(min(static_cast<long long>(q.tiles - t), w1 - w));
-    begins = t == 0;
-    ends = t + count == q.tiles;
-    w += count;
-    return true;
+    return false;
   }
 };
 
-template <int FMT, int D>
-__global__ void __launch_bounds__(KA_THREADS, 2)
+// movmatrix: the 8 x 8 matrix of 16-bit elements held a row per four lanes,
+// transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t r) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(r));
+  return d;
+}
+
+// All consumer threads' verdict: true if it is true for each of them.
+__device__ __forceinline__ bool ka_all(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "n"(KA_CONS)
+      : "memory");
+  return r != 0;
+}
+
+template <int FMT, int D, int NR>
+__global__ void __launch_bounds__(KA_THREADS, ka_ctas_per_sm<NR>())
 kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const KaArgs a) {
-  using L = KaSmem<D>;
+  using L = KaSmem<D, NR>;
+  constexpr int ROWS = L::ROWS;
+  using Seg = KaSeg<ROWS>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
-  float* red = reinterpret_cast<float*>(gbase + L::RED_OFF);
-  float* sm_m = reinterpret_cast<float*>(gbase + L::ML_OFF);
-  float* sm_l = sm_m + KA_WARPS * KA_ROWS;
-  int* sm_e = reinterpret_cast<int*>(sm_l + KA_WARPS * KA_ROWS);
   const uint32_t bar_full = base + L::BAR_OFF, bar_empty = bar_full + 8 * L::STAGES;
+  const uint32_t bar_seg = bar_empty + 8 * L::STAGES, bar_seg_empty = bar_seg + 16;
   volatile int* abort = reinterpret_cast<volatile int*>(gbase + L::MISC_OFF);
-  int* sm_flag = reinterpret_cast<int*>(gbase + L::MISC_OFF + 4);
-  int* sm_b = reinterpret_cast<int*>(gbase + L::MISC_OFF + 8);
   long long* sm_base = reinterpret_cast<long long*>(gbase + L::MISC_OFF + 16);
-  long long* sm_scan = reinterpret_cast<long long*>(gbase + L::MISC_OFF + 24);   // 5 warps
+  long long* sm_scan = reinterpret_cast<long long*>(gbase + L::MISC_OFF + 24);   // [5]
+  KaReq* sm_req = reinterpret_cast<KaReq*>(gbase + L::MISC_OFF + 64);
+  int* sm_b = reinterpret_cast<int*>(gbase + L::MISC_OFF + 64 + sizeof(KaReq));
+  static_assert(sizeof(KaReq) <= 56, "fits");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
@@ -204,8 +265,11 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
       mbar_init(bar_full + 8 * i, 2);
       mbar_init(bar_empty + 8 * i, KA_WARPS);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_seg + 8 * i, 1);
+      mbar_init(bar_seg_empty + 8 * i, KA_WARPS);
+    }
     *abort = 0;
-    *sm_b = -1;
     fence_mbar_init();
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
@@ -214,9 +278,10 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
   const int per = (a.v.requests + KA_THREADS - 1) / KA_THREADS;
   const int rb0 = min(a.v.requests, tid * per), rb1 = min(a.v.requests, rb0 + per);
   long long mine = 0;
+  KaReq last{};
   for (int b = rb0; b < rb1; ++b) {
-    const KaReq q = ka_request(a, b);
-    mine += q.units * q.tiles;
+    last = ka_request<ROWS>(a, b);
+    mine += last.units * last.tiles;
   }
   long long incl = mine;
 #pragma unroll
@@ -233,15 +298,21 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
   }
   const long long ctas = min(static_cast<long long>(gridDim.x), total);
   const long long cta = blockIdx.x;
-  if (cta >= ctas) return;                   // the whole CTA: nothing was started
-  long long w0 = total * cta / ctas, w1 = total * (cta + 1) / ctas;
+  KaJoin<ROWS>* join = reinterpret_cast<KaJoin<ROWS>*>(a.joins) + cta;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (cta >= ctas) {                         // the whole CTA: nothing was started
+    if (a.ws != nullptr && tid == 0) join->live = 0;
+    return;
+  }
+  const long long w0 = total * cta / ctas, w1 = total * (cta + 1) / ctas;
   if (w0 >= before && w0 < before + mine) {
     long long p = before;
     for (int b = rb0; b < rb1; ++b) {
-      const KaReq q = ka_request(a, b);
+      const KaReq q = per == 1 ? last : ka_request<ROWS>(a, b);
       const long long n = q.units * q.tiles;
       if (w0 < p + n) {
         *sm_b = b;
+        *sm_req = q;
         *sm_base = p;
         break;
       }
@@ -249,44 +320,166 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
     }
   }
   __syncthreads();
-  KaWalk walk;
-  walk.b = *sm_b;
-  walk.base = *sm_base;
-  walk.q = ka_request(a, walk.b);
-  walk.w = w0;
-  walk.w1 = w1;
-  if (a.ws == nullptr) {
-    // units stay whole: the CTA in whose stretch a unit begins takes all of it
-    const long long t = walk.q.tiles;
-    const long long lo = walk.base + (w0 - walk.base + t - 1) / t * t;
-    walk.w = lo;                             // may be the next request's first
-  }
 
   if (warp == KA_WARPS) {
     // ------------------------------------------------------------ producer
-    int it = 0;
-    bool ok = true;
+    KaWalk<ROWS> walk;
+    walk.b = *sm_b;
+    walk.base = *sm_base;
+    walk.q = *sm_req;
+    walk.w = w0;
+    walk.w1 = w1;
+    const bool whole = a.ws == nullptr;
+    if (whole) {
+      // units stay whole: the CTA in whose stretch a unit begins takes all of it
+      const long long t = walk.q.tiles;
+      walk.w = walk.base + (w0 - walk.base + t - 1) / t * t;   // may be the next request's first
+    } else if (lane == 0) {
+      join->live = 0;
+    }
+    const int g = lane >> 2, t4 = lane & 3;
+    int it = 0, seg_it = 0;
+    bool ok = true, first = true;
     while (ok) {
-      if (a.ws == nullptr) {
-        if (walk.w >= w1) break;
+      bool more;
+      if (whole) {
+        more = walk.w < w1;
         walk.w1 = 0x7FFFFFFFFFFFFFFFll;
+        more = more && walk.next(a);
+      } else {
+        more = walk.next(a);
       }
-      if (!walk.next(a)) break;
-      const int len = walk.q.r.len, shift = a.v.page_shift;
+      const int ss = seg_it & 1;
+      Seg* seg = reinterpret_cast<Seg*>(gbase + L::SEG_OFF + ss * L::SEG_BYTES);
+      if (!mbar_wait(bar_seg_empty + 8 * ss, ((seg_it >> 1) & 1) ^ 1, abort)) {
+        if (lane == 0) ka_timeout(abort, 0x41);
+        ok = false;
+        break;
+      }
+      ++seg_it;
+      if (!more) {
+        if (lane == 0) {
+          seg->count = 0;
+          mbar_arrive(bar_seg + 8 * ss);
+        }
+        break;
+      }
+      const KvReq rq = walk.q.r;
+      const int rows = rq.n * a.v.group;
+      const int len = rq.len, shift = a.v.page_shift;
       const int per_tile = KA_TK >> shift;
       const int* row = a.v.table + static_cast<long long>(walk.b) * a.v.table_stride;
+      // a tile's pages, one per lane: its id, or -1 where the request has
+      // none and for an id outside the cache (whose keys are NaN); read one
+      // tile ahead
+      auto page_of = [&](int i) {
+        const int key0 = (walk.tile + i) * KA_TK;
+        int id = -1;
+        if (i < walk.count && lane < per_tile && key0 + (lane << shift) < len)
+          id = row[(key0 >> shift) + lane];
+        return id;
+      };
+      int next_id = page_of(0);
+      // ---- the rows: what they see, and Q as the B operand's fragments: lane
+      // (g, t) holds row g's values [D/4 t, D/4 (t + 1))
+      int all_lo = 0, all_hi = 0x7FFFFFFF, any_lo = 0x7FFFFFFF, any_hi = 0;
+      long long out_of_lane = 0;
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+        const int rr = 8 * nr + g, r = walk.row_tile * ROWS + rr;
+        const bool live = r < rows;
+        const int token = live ? r / a.v.group : 0;
+        const int qh = walk.head * a.v.group + (live ? r - token * a.v.group : 0);
+        const uint16_t* src = a.Q + (rq.q0 + token) * a.q_ts + qh * a.q_hs + t4 * (D / 4);
+        uint32_t w[D / 8];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (live) v = *reinterpret_cast<const uint4*>(src + 8 * c);
+          w[4 * c] = v.x;
+          w[4 * c + 1] = v.y;
+          w[4 * c + 2] = v.z;
+          w[4 * c + 3] = v.w;
+        }
+        const int lo = live ? kv_first_key(a.v, rq, token) : 0;
+        const int hi = live ? kv_end_key(a.v, rq, token) : 0;
+        if (live) {
+          all_lo = max(all_lo, lo);
+          all_hi = min(all_hi, hi);
+          if (hi > lo) {
+            any_lo = min(any_lo, lo);
+            any_hi = max(any_hi, hi);
+          }
+        }
+        // a power of two that brings the row's largest value into [1, 2)
+        float down = 1.0f, up = 1.0f;
+        if (a.bf16) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int e = 0; e < D / 8; ++e)
+            top = max(top, max((w[e] << 16) & 0x7FFFFFFFu, w[e] & 0x7FFF0000u));
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+          kv_row_factors(top, down, up);
+#pragma unroll
+          for (int e = 0; e < D / 8; ++e)
+            w[e] = cvt_f16x2(__uint_as_float(w[e] << 16) * down,
+                             __uint_as_float(w[e] & 0xFFFF0000u) * down);
+        }
+        uint4* qs = reinterpret_cast<uint4*>(gbase + L::Q_OFF + ss * L::Q_SLOT) +
+                    nr * (D / 32) * 32 + lane;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+          qs[32 * c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        const long long out = (rq.q0 + token) * a.o_ts + qh * a.o_hs;
+        if (t4 == 0) {
+          seg->fr[rr] = a.scale_log2e * up;
+          seg->lo[rr] = lo;
+          seg->hi[rr] = hi;
+          seg->out[rr] = out;
+        }
+        // lane r of the warp keeps row r's
+        const long long of = __shfl_sync(0xFFFFFFFFu, out, 4 * (lane & 7));
+        if ((lane >> 3) == nr) out_of_lane = of;
+      }
+      all_lo = __reduce_max_sync(0xFFFFFFFFu, all_lo);
+      all_hi = __reduce_min_sync(0xFFFFFFFFu, all_hi);
+      any_lo = __reduce_min_sync(0xFFFFFFFFu, any_lo);
+      any_hi = __reduce_max_sync(0xFFFFFFFFu, any_hi);
+      if (lane == 0) {
+        seg->tile = walk.tile;
+        seg->count = walk.count;
+        seg->len = rq.len;
+        seg->live = min(ROWS, rows - walk.row_tile * ROWS);
+        seg->all_lo = all_lo;
+        seg->all_hi = all_hi;
+        seg->any_lo = any_lo;
+        seg->any_hi = any_hi;
+        seg->part = !(walk.begins && walk.ends);
+        // the CTA's first segment and its last can be parts
+        seg->slot = static_cast<int>(2 * cta + (first ? 0 : 1));
+      }
+      // the unit goes on in other CTAs (stretch c is [total c / ctas, total
+      // (c + 1) / ctas)): say what joins it
+      if (walk.begins && !walk.ends) {
+        if (lane == 0) {
+          join->live = min(ROWS, rows - walk.row_tile * ROWS);
+          join->parts = static_cast<int>((walk.unit_end * ctas - 1) / total - cta + 1);
+          join->first_slot = static_cast<int>(2 * cta + (first ? 0 : 1));
+        }
+        if (lane < ROWS) join->out[lane] = out_of_lane;
+      }
+      first = false;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_seg + 8 * ss);
+
+      // ---- the tiles
       for (int i = 0; i < walk.count; ++i, ++it) {
         const int st = it % L::STAGES;
-        const int key0 = (walk.tile + i) * KA_TK;
-        // the tile's pages, one per lane: its id, or -1 where the request has
-        // none; -2 for an id outside the cache, which makes the page NaN
-        int id = -1;
-        if (lane < per_tile && key0 + (lane << shift) < len) {
-          id = row[(key0 >> shift) + lane];
-          if (id < 0 || id >= a.v.pages) id = -2;
-        }
+        const int id = next_id < a.v.pages ? next_id : -1;
+        next_id = page_of(i + 1);
         if (!mbar_wait(bar_empty + 8 * st, ((it / L::STAGES) & 1) ^ 1, abort)) {
-          if (lane == 0) ka_timeout(abort, 0x41);
+          if (lane == 0) ka_timeout(abort, 0x42);
           ok = false;
           break;
         }
@@ -331,185 +524,183 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
 
   // ------------------------------------------------------------ consumers
   const int g = lane >> 2, t4 = lane & 3;
-  constexpr int STEPS = D / 16;               // 16-value steps of the contraction
+  constexpr int STEPS = D / 16;               // 16-value steps of S's contraction
   constexpr int CHUNKS = D / 64;              // 16-byte chunks of a key per lane
-  constexpr int NT = D / 8;                   // output column tiles
-  int it = 0;
+  constexpr int MT = D / 16;                  // 16-column tiles of O
+  float* red = reinterpret_cast<float*>(gbase + L::RED_OFF);
+  float* sm_m = reinterpret_cast<float*>(gbase + L::ML_OFF);
+  float* sm_l = sm_m + KA_WARPS * ROWS;
+  int* sm_e = reinterpret_cast<int*>(sm_l + KA_WARPS * ROWS);
+  int it = 0, seg_it = 0;
   bool ok = true;
-  const bool whole = a.ws == nullptr;
   while (true) {
-    if (whole) {
-      if (walk.w >= w1) break;
-      walk.w1 = 0x7FFFFFFFFFFFFFFFll;
+    const int ss = seg_it & 1;
+    if (ok && !mbar_wait(bar_seg + 8 * ss, (seg_it >> 1) & 1, abort)) {
+      if (lane == 0) ka_timeout(abort, 0x43);
+      ok = false;
     }
-    const long long seg_w = walk.w;
-    if (!walk.next(a)) break;
-    const KvReq rq = walk.q.r;
-    const int rows = rq.n * a.v.group;        // all rows of the request and cache head
-    // ---- this lane's two rows: what they see, and Q as A fragments
-    int lo[2], hi[2];
-    uint32_t qf[STEPS][4];
-    float fr[2];
+    ok = ka_all(ok);
+    if (!ok) break;
+    ++seg_it;
+    const Seg* seg = reinterpret_cast<const Seg*>(gbase + L::SEG_OFF + ss * L::SEG_BYTES);
+    const int count = seg->count;
+    if (count == 0) break;
+    const int tile0 = seg->tile, len = seg->len;
+    const int all_lo = seg->all_lo, all_hi = seg->all_hi, any_lo = seg->any_lo, any_hi = seg->any_hi;
+    // B fragments of Q, and the lane's rows of S^T: 8 nr + 2 t + e
+    uint32_t qf[NR][D / 8];
+    float fr[NR][2], m[NR][2], l[NR][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = walk.row_tile * KA_ROWS + g + 8 * h;
-      const bool live = r < rows;
-      const int token = live ? r / a.v.group : 0;
-      lo[h] = live ? kv_first_key(a.v, rq, token) : 0;
-      hi[h] = live ? kv_end_key(a.v, rq, token) : 0;
-      const int qh = walk.head * a.v.group + (live ? r - token * a.v.group : 0);
-      const uint16_t* src = a.Q + (rq.q0 + token) * a.q_ts + qh * a.q_hs + t4 * (D / 4);
-      uint32_t w[D / 8];
+    for (int nr = 0; nr < NR; ++nr) {
+      const uint4* qs = reinterpret_cast<const uint4*>(gbase + L::Q_OFF + ss * L::Q_SLOT) +
+                        nr * (D / 32) * 32 + lane;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (live) v = *reinterpret_cast<const uint4*>(src + 8 * c);
-        w[4 * c] = v.x;
-        w[4 * c + 1] = v.y;
-        w[4 * c + 2] = v.z;
-        w[4 * c + 3] = v.w;
+        const uint4 v = qs[32 * c];
+        qf[nr][4 * c] = v.x;
+        qf[nr][4 * c + 1] = v.y;
+        qf[nr][4 * c + 2] = v.z;
+        qf[nr][4 * c + 3] = v.w;
       }
-      // a power of two that brings the row's largest value into [1, 2)
-      float down = 1.0f, up = 1.0f;
-      if (a.bf16) {
-        uint32_t top = 0;
 #pragma unroll
-        for (int e = 0; e < D / 8; ++e) top = max(top, max((w[e] << 16) & 0x7FFFFFFFu, w[e] & 0x7FFF0000u));
-        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        kv_row_factors(top, down, up);
-#pragma unroll
-        for (int e = 0; e < D / 8; ++e)
-          w[e] = cvt_f16x2(__uint_as_float(w[e] << 16) * down,
-                           __uint_as_float(w[e] & 0xFFFF0000u) * down);
-      }
-      fr[h] = a.scale_log2e * up;
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s) {
-        qf[s][h] = w[2 * s];
-        qf[s][2 + h] = w[2 * s + 1];
+      for (int e = 0; e < 2; ++e) {
+        fr[nr][e] = seg->fr[8 * nr + 2 * t4 + e];
+        m[nr][e] = -INFINITY;
+        l[nr][e] = 0.0f;
       }
     }
-    // keys that every live row of the warp sees need no mask
-    int all_lo = max(lo[0], lo[1]), all_hi = min(hi[0] ? hi[0] : 0x7FFFFFFF, hi[1] ? hi[1] : 0x7FFFFFFF);
-    {
-      const int r0 = walk.row_tile * KA_ROWS + g;
-      if (r0 < rows && hi[0] == 0) all_hi = 0;
-      if (r0 + 8 < rows && hi[1] == 0) all_hi = 0;
-    }
-    all_lo = __reduce_max_sync(0xFFFFFFFFu, all_lo);
-    all_hi = __reduce_min_sync(0xFFFFFFFFu, all_hi);
-    const int any_hi = __reduce_max_sync(0xFFFFFFFFu, max(hi[0], hi[1]));
-    const int any_lo = __reduce_min_sync(
-        0xFFFFFFFFu, min(hi[0] ? lo[0] : 0x7FFFFFFF, hi[1] ? lo[1] : 0x7FFFFFFF));
-
-    float o[NT][4];
+    float o[MT][NR][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][nr][e] = 0.0f;
     int ve = 0;                               // V's reference exponent
-    for (int i = 0; i < walk.count; ++i, ++it) {
+    for (int i = 0; i < count; ++i, ++it) {
       const int st = it % L::STAGES;
       if (ok && !mbar_wait(bar_full + 8 * st, (it / L::STAGES) & 1, abort)) {
-        if (lane == 0) ka_timeout(abort, 0x42);
+        if (lane == 0) ka_timeout(abort, 0x44);
         ok = false;
       }
       ok = __all_sync(0xFFFFFFFFu, ok);
-      const int key0 = (walk.tile + i) * KA_TK + warp * KA_KW;
+      const int key0 = (tile0 + i) * KA_TK + warp * KA_KW;
       if (ok && key0 < any_hi && key0 + KA_KW > any_lo) {
         const uint32_t kt = base + st * 2 * L::TILE;
         const uint32_t vt = kt + L::TILE;
         const uint2* pg = reinterpret_cast<const uint2*>(gbase + L::PG_OFF + st * L::PG_STAGE);
         const bool masked = key0 < all_lo || key0 + KA_KW > all_hi;
-        // ---- scores: four tiles of 8 keys
-        float x[4][4];
+        // ---- scores of two tiles of 16 keys: x[.][.][2 h + e] is key g + 8 h
+        // and row 2 t + e
+        float x[2][NR][4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
+        for (int s = 0; s < 2; ++s) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[n][e] = 0.0f;
-          const int key = warp * KA_KW + 8 * n + g;   // this lane's key in the tile
+          for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[s][nr][e] = 0.0f;
+          const int key = warp * KA_KW + 16 * s + g;   // and key + 8: the same swizzle
 #pragma unroll
           for (int c = 0; c < CHUNKS; ++c) {
             const int chunk = CHUNKS * t4 + c;
             const int sw = D == 128 ? (chunk ^ (key & 7)) : (chunk ^ ((key >> 1) & 3));
-            const uint4 k4 = ld_shared_v4(kt + key * D + sw * 16);
-            const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
+            const uint4 ka = ld_shared_v4(kt + key * D + sw * 16);
+            const uint4 kb = ld_shared_v4(kt + (key + 8) * D + sw * 16);
+            const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-              uint32_t b0, b1;
-              kv_f16_pairs<FMT>(w[s], b0, b1);
-              mma_16816(x[n], qf[4 * c + s], b0, b1);
+            for (int q = 0; q < 4; ++q) {
+              uint32_t f[4];
+              kv_f16_pairs<FMT>(wa[q], f[0], f[2]);
+              kv_f16_pairs<FMT>(wb[q], f[1], f[3]);
+#pragma unroll
+              for (int nr = 0; nr < NR; ++nr)
+                mma_16816(x[s][nr], f, qf[nr][2 * (4 * c + q)], qf[nr][2 * (4 * c + q) + 1]);
             }
           }
         }
         // ---- log2 units, mask, running maximum
         int vnew = ve;
-        float mx[2] = {-INFINITY, -INFINITY};
+        float mx[NR][2];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const uint2 page = pg[(warp * KA_KW + 8 * n) >> a.v.page_shift];
-          const float kf = __uint_as_float(page.x);
-          if (page.y < 0xFFu) vnew = max(vnew, static_cast<int>(page.y));
+        for (int nr = 0; nr < NR; ++nr) mx[nr][0] = mx[nr][1] = -INFINITY;
+        uint2 page[2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int h = e >> 1;
-            float y = x[n][e] * (fr[h] * kf);
-            if (masked) {
-              const int j = key0 + 8 * n + 2 * t4 + (e & 1);
-              if (j < lo[h] || j >= hi[h]) y = -INFINITY;
+        for (int s = 0; s < 2; ++s) {
+          page[s] = pg[(warp * KA_KW + 16 * s) >> a.v.page_shift];
+          if (page[s].y < 0xFFu) vnew = max(vnew, static_cast<int>(page[s].y));
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float f = fr[nr][e] * __uint_as_float(page[s].x);
+              float y0 = x[s][nr][e] * f, y1 = x[s][nr][2 + e] * f;
+              if (masked) {
+                const int lo = seg->lo[8 * nr + 2 * t4 + e], hi = seg->hi[8 * nr + 2 * t4 + e];
+                const int j = key0 + 16 * s + g;
+                if (j < lo || j >= hi) y0 = -INFINITY;
+                if (j + 8 < lo || j + 8 >= hi) y1 = -INFINITY;
+              }
+              x[s][nr][e] = y0;
+              x[s][nr][2 + e] = y1;
+              mx[nr][e] = fmaxf(mx[nr][e], fmaxf(y0, y1));
             }
-            x[n][e] = y;
-            mx[h] = fmaxf(mx[h], y);
-          }
         }
         bool moved = vnew != ve;
-        float alpha[2];
+        float alpha[NR][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 1));
-          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 2));
-          const float mn = mx[h] > m[h] + KA_LAZY ? mx[h] : m[h];
-          alpha[h] = mn == m[h] ? 1.0f : ex2_approx(m[h] - mn);
-          moved |= mn != m[h];
-          m[h] = mn;
-          l[h] *= alpha[h];
-        }
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float v = mx[nr][e];
+            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+            const float mn = v > m[nr][e] + KA_LAZY ? v : m[nr][e];
+            alpha[nr][e] = mn == m[nr][e] ? 1.0f : ex2_approx(m[nr][e] - mn);
+            moved |= mn != m[nr][e];
+            m[nr][e] = mn;
+          }
         if (__any_sync(0xFFFFFFFFu, moved)) {
           const float vf = kv_exp2i(ve - vnew);
-          const float f0 = alpha[0] * vf, f1 = alpha[1] * vf;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            o[n][0] *= f0;
-            o[n][1] *= f0;
-            o[n][2] *= f1;
-            o[n][3] *= f1;
-          }
           ve = vnew;
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr) {
+            const float f0 = alpha[nr][0] * vf, f1 = alpha[nr][1] * vf;
+            l[nr][0] *= alpha[nr][0];
+            l[nr][1] *= alpha[nr][1];
+#pragma unroll
+            for (int c = 0; c < MT; ++c) {
+              o[c][nr][0] *= f0;
+              o[c][nr][1] *= f1;
+              o[c][nr][2] *= f0;
+              o[c][nr][3] *= f1;
+            }
+          }
         }
         // ---- probabilities and the product with V: two steps of 16 keys
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const int kk = warp * KA_KW + 16 * s;
-          const int code = static_cast<int>(pg[kk >> a.v.page_shift].y);
+          const int code = static_cast<int>(page[s].y);
           const float vf = code == 0xFF || code < 0 ? __uint_as_float(0x7FC00000u)
                                                     : kv_exp2i(KA_P_EXP + code - ve);
-          uint32_t pa[4];
+          uint32_t pb[NR][2];
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float x0 = x[2 * s + n][2 * h], x1 = x[2 * s + n][2 * h + 1];
-              float p0 = ex2_approx(x0 - m[h]), p1 = ex2_approx(x1 - m[h]);
-              float q0 = p0 * vf, q1 = p1 * vf;
-              if (masked) {
-                const int j = key0 + 16 * s + 8 * n + 2 * t4;
-                if (j < lo[h] || j >= hi[h]) p0 = q0 = 0.0f;
-                if (j + 1 < lo[h] || j + 1 >= hi[h]) p1 = q1 = 0.0f;
+              float p[2], q[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                p[e] = ex2_approx(x[s][nr][2 * h + e] - m[nr][e]);
+                q[e] = p[e] * vf;
+                if (masked) {
+                  const int j = key0 + 16 * s + g + 8 * h;
+                  if (j < seg->lo[8 * nr + 2 * t4 + e] || j >= seg->hi[8 * nr + 2 * t4 + e])
+                    p[e] = q[e] = 0.0f;
+                }
+                l[nr][e] += p[e];
               }
-              l[h] += p0 + p1;
-              pa[2 * n + h] = cvt_f16x2(q0, q1);
+              pb[nr][h] = transpose8(cvt_f16x2(q[0], q[1]));
             }
           // codes of keys 2t, 2t + 1, 2t + 8, 2t + 9 of the step; those that
           // were not loaded, or lie behind the request's end, count as zero
@@ -517,7 +708,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
           uint32_t vw[4][W];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int key = kk + 2 * t4 + (r & 1) + 8 * (r >> 1);
+            const int key = warp * KA_KW + 16 * s + 2 * t4 + (r & 1) + 8 * (r >> 1);
             if constexpr (D == 128) {
               const uint4 v = ld_shared_v4(vt + key * D + ((g ^ (key & 7)) << 4));
               vw[r][0] = v.x;
@@ -531,25 +722,29 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
               vw[r][1] = v.y;
             }
           }
-          if (code < 0 || key0 + 16 * s + 16 > rq.len) {
+          if (code < 0 || key0 + 16 * s + 16 > len) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const int j = key0 + 16 * s + 2 * t4 + (r & 1) + 8 * (r >> 1);
-              if (code < 0 || j >= rq.len)
+              if (code < 0 || j >= len)
 #pragma unroll
                 for (int e = 0; e < W; ++e) vw[r][e] = 0u;
             }
           }
 #pragma unroll
           for (int e = 0; e < W; ++e) {
-            // zip two keys' bytes: columns 4e .. 4e + 3 as pairs of keys
-            uint32_t b0[4], b1[4];
-            kv_f16_pairs<FMT>(__byte_perm(vw[0][e], vw[1][e], 0x5140), b0[0], b0[1]);
-            kv_f16_pairs<FMT>(__byte_perm(vw[0][e], vw[1][e], 0x7362), b0[2], b0[3]);
-            kv_f16_pairs<FMT>(__byte_perm(vw[2][e], vw[3][e], 0x5140), b1[0], b1[1]);
-            kv_f16_pairs<FMT>(__byte_perm(vw[2][e], vw[3][e], 0x7362), b1[2], b1[3]);
+            // zip two keys' bytes: columns 4e .. 4e + 3 as pairs of keys; two
+            // columns make the 16 rows of an operand (lane g: columns of chunk g)
+            uint32_t f0[4], f1[4];
+            kv_f16_pairs<FMT>(__byte_perm(vw[0][e], vw[1][e], 0x5140), f0[0], f0[1]);
+            kv_f16_pairs<FMT>(__byte_perm(vw[2][e], vw[3][e], 0x5140), f0[2], f0[3]);
+            kv_f16_pairs<FMT>(__byte_perm(vw[0][e], vw[1][e], 0x7362), f1[0], f1[1]);
+            kv_f16_pairs<FMT>(__byte_perm(vw[2][e], vw[3][e], 0x7362), f1[2], f1[3]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) mma_16816(o[4 * e + c], pa, b0[c], b1[c]);
+            for (int nr = 0; nr < NR; ++nr) {
+              mma_16816(o[2 * e][nr], f0, pb[nr][0], pb[nr][1]);
+              mma_16816(o[2 * e + 1][nr], f1, pb[nr][0], pb[nr][1]);
+            }
           }
         }
       }
@@ -559,150 +754,186 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
 
     // ---- the four warps' results as one
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 2);
-      if (t4 == 0) {
-        sm_m[warp * KA_ROWS + g + 8 * h] = m[h];
-        sm_l[warp * KA_ROWS + g + 8 * h] = l[h];
-        sm_e[warp * KA_ROWS + g + 8 * h] = ve;
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float v = l[nr][e];
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+        if (g == 0) {
+          sm_m[warp * ROWS + 8 * nr + 2 * t4 + e] = m[nr][e];
+          sm_l[warp * ROWS + 8 * nr + 2 * t4 + e] = v;
+        }
       }
-    }
-    kv_bar_sync(1, 32 * KA_WARPS);
-    // weight of this warp's two rows relative to the common reference, with
-    // O brought to true units in the end: 2^(e - 127 - KA_P_EXP)
-    float wgt[2];
+    if (lane == 0) sm_e[warp] = ve;
+    kv_bar_sync(1, KA_CONS);
     int top_e = 0;
 #pragma unroll
-    for (int w = 0; w < KA_WARPS; ++w) top_e = max(top_e, sm_e[w * KA_ROWS]);
+    for (int w = 0; w < KA_WARPS; ++w) top_e = max(top_e, sm_e[w]);
+    // weight of this warp's rows relative to the common reference
+    float wgt[NR][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float M = -INFINITY;
+    for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-      for (int w = 0; w < KA_WARPS; ++w) M = fmaxf(M, sm_m[w * KA_ROWS + g + 8 * h]);
-      wgt[h] = (m[h] == M ? 1.0f : ex2_approx(m[h] - M)) * kv_exp2i(ve - top_e);
-    }
-    // the row this thread adds up, and its sum
-    const int rr = tid >> 3;                  // 0..15
-    float M = -INFINITY, lsum = 0.0f;
+      for (int e = 0; e < 2; ++e) {
+        float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < KA_WARPS; ++w) M = fmaxf(M, sm_m[w * KA_ROWS + rr]);
+        for (int w = 0; w < KA_WARPS; ++w) M = fmaxf(M, sm_m[w * ROWS + 8 * nr + 2 * t4 + e]);
+        wgt[nr][e] = (m[nr][e] == M ? 1.0f : ex2_approx(m[nr][e] - M)) * kv_exp2i(ve - top_e);
+      }
+    const bool part = seg->part;
+    const int live = seg->live;
+    float* slot = a.ws + static_cast<long long>(seg->slot) * (ROWS * (D + 2));
 #pragma unroll
-    for (int w = 0; w < KA_WARPS; ++w) {
-      const float mw = sm_m[w * KA_ROWS + rr];
-      lsum += sm_l[w * KA_ROWS + rr] * (mw == M ? 1.0f : ex2_approx(mw - M));
-    }
-    const bool part = !(walk.begins && walk.ends);
-    const int r = walk.row_tile * KA_ROWS + rr;
-    const bool live = r < rows;
-    const float inv = lsum == 0.0f ? 0.0f : 1.0f / lsum;
-    const int slot = static_cast<int>(2 * cta + (seg_w == w0 ? 0 : 1));
-    float* part_o = a.ws + static_cast<long long>(slot) * (KA_ROWS * (D + 2)) + rr * D;
-    const int token = live ? r / a.v.group : 0;
-    const int qh = walk.head * a.v.group + (live ? r - token * a.v.group : 0);
-    const long long out0 = (rq.q0 + token) * a.o_ts + qh * a.o_hs;
-    // rounds over 4 (of the lane's D / 4) columns at a time: lane (g, t) holds
-    // columns [D/4 t, D/4 (t + 1)), the first half of them in accumulators 0, 2
+    for (int nr = 0; nr < NR; ++nr) {
+      if (8 * nr >= live) break;
+      // the row that a thread of the first two warps adds up, and its sum
+      const int rr = 8 * nr + ((tid >> 3) & 7), c8 = tid & 7;
+      const bool adds = tid < 64 && rr < live;
+      float M = -INFINITY, lsum = 0.0f;
 #pragma unroll
-    for (int rd = 0; rd < NT / 4; ++rd) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float4 v;
-          v.x = o[4 * rd][2 * h + half] * wgt[h];
-          v.y = o[4 * rd + 1][2 * h + half] * wgt[h];
-          v.z = o[4 * rd + 2][2 * h + half] * wgt[h];
-          v.w = o[4 * rd + 3][2 * h + half] * wgt[h];
-          *reinterpret_cast<float4*>(red + (warp * KA_ROWS + g + 8 * h) * 32 + 8 * t4 + 4 * half) = v;
-        }
-      kv_bar_sync(1, 32 * KA_WARPS);
-      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      const int c8 = tid & 7;                 // 4 columns: lane t = c8 / 2, half c8 & 1
+      for (int w = 0; w < KA_WARPS; ++w) M = fmaxf(M, sm_m[w * ROWS + rr]);
 #pragma unroll
       for (int w = 0; w < KA_WARPS; ++w) {
-        const float4 v = *reinterpret_cast<const float4*>(red + (w * KA_ROWS + rr) * 32 + 4 * c8);
-        s.x += v.x;
-        s.y += v.y;
-        s.z += v.z;
-        s.w += v.w;
+        const float mw = sm_m[w * ROWS + rr];
+        lsum += sm_l[w * ROWS + rr] * (mw == M ? 1.0f : ex2_approx(mw - M));
       }
-      if (live) {
-        const int col = (D / 4) * (c8 >> 1) + (D / 8) * (c8 & 1) + 4 * rd;
-        // to true units: 2^(top_e - 127), and the 2^KA_P_EXP out of P
-        const float f = kv_scale_value(static_cast<uint32_t>(top_e));
-        s.x = s.x * (1.0f / (1 << KA_P_EXP)) * f;
-        s.y = s.y * (1.0f / (1 << KA_P_EXP)) * f;
-        s.z = s.z * (1.0f / (1 << KA_P_EXP)) * f;
-        s.w = s.w * (1.0f / (1 << KA_P_EXP)) * f;
-        if (part) {
-          *reinterpret_cast<float4*>(part_o + col) = s;
-        } else {
-          s.x *= inv;
-          s.y *= inv;
-          s.z *= inv;
-          s.w *= inv;
-          kv_store4(a.O, a.o_dtype, out0 + col, s);
+      const float inv = lsum == 0.0f ? 0.0f : 1.0f / lsum;
+      const long long out = seg->out[rr];
+      // rounds over 4 columns of each of the 8 chunks
+#pragma unroll
+      for (int rd = 0; rd < D / 32; ++rd) {
+        if (rd + nr > 0) kv_bar_sync(1, KA_CONS);    // the staging has been read
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float4*>(red + (warp * 8 + 2 * t4 + e) * KA_RED + 4 * g) =
+              make_float4(o[2 * rd][nr][e] * wgt[nr][e], o[2 * rd][nr][2 + e] * wgt[nr][e],
+                          o[2 * rd + 1][nr][e] * wgt[nr][e], o[2 * rd + 1][nr][2 + e] * wgt[nr][e]);
+        kv_bar_sync(1, KA_CONS);
+        if (adds) {
+          float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+          for (int w = 0; w < KA_WARPS; ++w) {
+            const float4 v =
+                *reinterpret_cast<const float4*>(red + (w * 8 + (rr & 7)) * KA_RED + 4 * c8);
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+          }
+          const int col = (D / 8) * c8 + 4 * rd;
+          // to true units: 2^(top_e - 127), and the 2^KA_P_EXP out of P
+          const float f = kv_scale_value(static_cast<uint32_t>(top_e));
+          s.x = s.x * (1.0f / (1 << KA_P_EXP)) * f;
+          s.y = s.y * (1.0f / (1 << KA_P_EXP)) * f;
+          s.z = s.z * (1.0f / (1 << KA_P_EXP)) * f;
+          s.w = s.w * (1.0f / (1 << KA_P_EXP)) * f;
+          if (part) {
+            *reinterpret_cast<float4*>(slot + rr * D + col) = s;
+          } else {
+            s.x *= inv;
+            s.y *= inv;
+            s.z *= inv;
+            s.w *= inv;
+            kv_store4(a.O, a.o_dtype, out + col, s);
+          }
         }
       }
-      kv_bar_sync(1, 32 * KA_WARPS);
-    }
-    if (!part) continue;
-    float* part_ml = a.ws + static_cast<long long>(slot) * (KA_ROWS * (D + 2)) + KA_ROWS * D;
-    if ((tid & 7) == 0) {
-      part_ml[rr] = M;
-      part_ml[KA_ROWS + rr] = lsum;
-    }
-    __threadfence();
-    kv_bar_sync(1, 32 * KA_WARPS);
-    // which CTAs share this unit: stretch c is [total c / ctas, total (c+1) / ctas)
-    const long long c0 = ((walk.unit_start + 1) * ctas - 1) / total;
-    const long long c1 = (walk.unit_end * ctas - 1) / total;
-    if (tid == 0)
-      *sm_flag = ka_arrive(a.ctr + c0, a.tag, static_cast<int>(c1 - c0 + 1)) ==
-                 static_cast<int>(c1 - c0 + 1);
-    kv_bar_sync(1, 32 * KA_WARPS);
-    if (!*sm_flag) continue;
-    __threadfence();
-    // this CTA came last: the parts in CTA order
-    if (live) {
-      const int c8 = tid & 7;
-      const long long first = total * c0 / ctas == walk.unit_start ? 2 * c0 : 2 * c0 + 1;
-      auto at = [&](long long c) {
-        return a.ws + (c == c0 ? first : 2 * c) * (KA_ROWS * (D + 2));
-      };
-      float top = -INFINITY;
-      for (long long c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(at(c) + KA_ROWS * D + rr));
-      float ls = 0.0f;
-      float4 acc[D / 32];
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (long long c = c0; c <= c1; ++c) {
-        const float* p = at(c);
-        const float mc = __ldcg(p + KA_ROWS * D + rr);
-        const float f = mc == top ? 1.0f : ex2_approx(mc - top);
-        ls = fmaf(f, __ldcg(p + KA_ROWS * (D + 1) + rr), ls);
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) {
-          const float4 v = ld_global_cg_f4(p + rr * D + 32 * e + 4 * c8);
-          acc[e].x = fmaf(f, v.x, acc[e].x);
-          acc[e].y = fmaf(f, v.y, acc[e].y);
-          acc[e].z = fmaf(f, v.z, acc[e].z);
-          acc[e].w = fmaf(f, v.w, acc[e].w);
-        }
+      if (part && adds && c8 == 0) {
+        slot[ROWS * D + rr] = M;
+        slot[ROWS * (D + 1) + rr] = lsum;
       }
-      const float fin = ls == 0.0f ? 0.0f : 1.0f / ls;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_seg_empty + 8 * ss);
+  }
+
+}
+
+// Join the parts of the unit that begins in main CTA blockIdx.x's stretch:
+// M = max m_p, O = sum 2^(m_p - M) O_p / sum 2^(m_p - M) l_p, parts in CTA
+// order.  One block per (unit, 32 columns); a thread takes a row and four
+// columns, and where a unit has few rows, groups of threads share its parts.
+// Reads of the parts go around L1 (another kernel wrote them).
+constexpr int KJ_THREADS = 128;
+template <int D, int ROWS>
+__global__ void __launch_bounds__(KJ_THREADS)
+kv_join_kernel(const float* __restrict__ ws, const KaJoin<ROWS>* joins, void* O, int o_dtype) {
+  constexpr int BATCH = 64, J = KJ_THREADS / ROWS;
+  constexpr long long PART = ROWS * (D + 2);
+  __shared__ float sm_w[BATCH * ROWS];
+  __shared__ float sm_r[J * ROWS];
+  __shared__ float4 sm_acc[KJ_THREADS];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const KaJoin<ROWS>* join = joins + blockIdx.x;
+  const int live = __ldcg(&join->live);
+  if (live == 0) return;
+  const int n = __ldcg(&join->parts);
+  const float* first = ws + __ldcg(&join->first_slot) * PART;
+  const float* rest = ws + 2ll * blockIdx.x * PART;    // part p > 0: slot 2 (CTA + p)
+  auto at = [&](int p) { return p == 0 ? first : rest + 2 * p * PART; };
+  const int tid = threadIdx.x;
+  // thread (r, j) looks after row r of parts j, j + J, ..
+  const int r = tid & (ROWS - 1), j = tid / ROWS;
+  float top = -INFINITY;
+  for (int p = j; p < n; p += J) top = fmaxf(top, __ldcg(at(p) + ROWS * D + r));
+  sm_r[j * ROWS + r] = top;
+  __syncthreads();
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) {
-        float4 v = acc[e];
-        v.x *= fin;
-        v.y *= fin;
-        v.z *= fin;
-        v.w *= fin;
-        kv_store4(a.O, a.o_dtype, out0 + 32 * e + 4 * c8, v);
+  for (int i = 0; i < J; ++i) top = fmaxf(top, sm_r[i * ROWS + r]);
+  const int items = live * 8;                          // (row, 4 columns)
+  int groups = 1;
+  while (groups * 2 * items <= KJ_THREADS) groups *= 2;
+  const int grp = tid / items;                         // >= groups: no part of the sum
+  const int row = (tid - grp * items) >> 3;
+  const int col = 32 * blockIdx.y + 4 * (tid & 7);
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float ls = 0.0f;
+  for (int p0 = 0; p0 < n; p0 += BATCH) {
+    const int batch = min(BATCH, n - p0);
+    __syncthreads();                                   // sm_r and the last batch are read
+    for (int p = j; p < batch; p += J) {
+      const float* part = at(p0 + p) + ROWS * D + r;
+      const float mp = __ldcg(part), lp = __ldcg(part + ROWS);
+      const float w = mp == top ? 1.0f : ex2_approx(mp - top);
+      sm_w[p * ROWS + r] = w;
+      ls = fmaf(w, lp, ls);
+    }
+    __syncthreads();
+    if (grp < groups) {
+#pragma unroll 8
+      for (int p = grp; p < batch; p += groups) {
+        const float w = sm_w[p * ROWS + row];
+        const float4 v = ld_global_cg_f4(at(p0 + p) + row * D + col);
+        acc.x = fmaf(w, v.x, acc.x);
+        acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z);
+        acc.w = fmaf(w, v.w, acc.w);
       }
     }
   }
+  __syncthreads();
+  sm_r[j * ROWS + r] = ls;
+  sm_acc[tid] = acc;
+  __syncthreads();
+  if (tid >= items) return;
+  for (int i = 1; i < groups; ++i) {
+    const float4 u = sm_acc[i * items + tid];
+    acc.x += u.x;
+    acc.y += u.y;
+    acc.z += u.z;
+    acc.w += u.w;
+  }
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < J; ++i) sum += sm_r[i * ROWS + row];
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  acc.x *= inv;
+  acc.y *= inv;
+  acc.z *= inv;
+  acc.w *= inv;
+  kv_store4(O, o_dtype, __ldcg(&join->out[row]) + col, acc);
 }
 
 int ka_sm_count() {
@@ -712,40 +943,59 @@ int ka_sm_count() {
   return n;
 }
 
-constexpr int64_t part_bytes(int64_t d) { return KA_ROWS * (d + 2) * 4; }
-
-// Two slots per CTA, then a counter per CTA.
-size_t ka_ws_bytes(int64_t d, int64_t ctas) {
-  return static_cast<size_t>(ctas * 2 * part_bytes(d) + ctas * 8);
+// The workspace of a launch: two slots per CTA (rows x (d + 2) floats), then
+// a KaJoin per CTA.
+int64_t ka_slot_bytes(int64_t d, int nr) { return 8 * nr * (d + 2) * 4; }
+int ka_ctas(int nr, int sms) { return (nr == 1 ? ka_ctas_per_sm<1>() : ka_ctas_per_sm<2>()) * sms; }
+size_t ka_ws_bytes(int64_t d, int nr, int sms) {
+  const size_t join = nr == 1 ? sizeof(KaJoin<8>) : sizeof(KaJoin<16>);
+  return static_cast<size_t>(ka_ctas(nr, sms)) * (2 * ka_slot_bytes(d, nr) + join);
 }
 
-template <int FMT, int D>
-cudaError_t ka_run(const CUtensorMap& tk, const CUtensorMap& tv, const KaArgs& a, int ctas,
+template <int FMT, int D, int NR>
+cudaError_t ka_run(const CUtensorMap& tk, const CUtensorMap& tv, const KaArgs& a, int sms,
                    cudaStream_t st) {
-  auto kern = kv_attention_kernel<FMT, D>;
+  auto kern = kv_attention_kernel<FMT, D, NR>;
+  using L = KaSmem<D, NR>;
   static std::atomic<bool> attr_set[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !attr_set[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, KaSmem<D>::ALLOC);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
   }
-  kern<<<ctas, KA_THREADS, KaSmem<D>::ALLOC, st>>>(tk, tv, a);
-  return cudaGetLastError();
+  const int ctas = ka_ctas(NR, sms);
+  kern<<<ctas, KA_THREADS, L::ALLOC, st>>>(tk, tv, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.ws == nullptr) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, D / 32);
+  cfg.blockDim = dim3(KJ_THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, 8 * NR>, static_cast<const float*>(a.ws),
+                            reinterpret_cast<const KaJoin<8 * NR>*>(a.joins), a.O, a.o_dtype);
 }
 
 template <int FMT>
-cudaError_t ka_run_d(int64_t d, const CUtensorMap& tk, const CUtensorMap& tv, const KaArgs& a,
-                     int ctas, cudaStream_t st) {
-  return d == 64 ? ka_run<FMT, 64>(tk, tv, a, ctas, st) : ka_run<FMT, 128>(tk, tv, a, ctas, st);
+cudaError_t ka_run_f(int64_t d, int nr, const CUtensorMap& tk, const CUtensorMap& tv,
+                     const KaArgs& a, int sms, cudaStream_t st) {
+  if (d == 64)
+    return nr == 1 ? ka_run<FMT, 64, 1>(tk, tv, a, sms, st) : ka_run<FMT, 64, 2>(tk, tv, a, sms, st);
+  return nr == 1 ? ka_run<FMT, 128, 1>(tk, tv, a, sms, st) : ka_run<FMT, 128, 2>(tk, tv, a, sms, st);
 }
 
 }  // namespace
 
 size_t kv_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t max_q) {
-  return ka_ws_bytes(d, 2 * ka_sm_count());
+  const int sms = ka_sm_count();
+  return std::max(ka_ws_bytes(d, 1, sms), ka_ws_bytes(d, 2, sms));
 }
 
 cudaError_t launch_kv_attention(const KvAttn& q, cudaStream_t st) {
@@ -762,20 +1012,20 @@ cudaError_t launch_kv_attention(const KvAttn& q, cudaStream_t st) {
   a.o_dtype = q.o_dtype;
   a.scale_log2e = q.scale * 1.4426950408889634f;
   a.skip_rows = 0x7FFFFFFF;
-  const int ctas = 2 * ka_sm_count();
-  if (ctas <= 0) return cudaErrorInvalidValue;
-  if (q.ws && q.ws_bytes >= ka_ws_bytes(c.d, ctas)) {
+  const int sms = ka_sm_count();
+  if (sms <= 0) return cudaErrorInvalidValue;
+  // eight rows where the rows that one request has for a cache head fit
+  const int nr = q.max_q * a.v.group <= 8 ? 1 : 2;
+  if (q.ws && q.ws_bytes >= ka_ws_bytes(c.d, nr, sms)) {
     a.ws = static_cast<float*>(q.ws);
-    a.ctr = reinterpret_cast<unsigned long long*>(static_cast<char*>(q.ws) +
-                                                  ctas * 2 * part_bytes(c.d));
-    a.tag = next_split_tag();
+    a.joins = static_cast<uint8_t*>(q.ws) + ka_ctas(nr, sms) * 2 * ka_slot_bytes(c.d, nr);
   }
   CUtensorMap tk, tv;
   if (!kv_tensor_map(&tk, c.k, c) || !kv_tensor_map(&tv, c.v, c)) return cudaErrorInvalidValue;
   switch (c.fmt) {
-    case FMT_E4M3: return ka_run_d<FMT_E4M3>(c.d, tk, tv, a, ctas, st);
-    case FMT_E5M2: return ka_run_d<FMT_E5M2>(c.d, tk, tv, a, ctas, st);
-    default: return ka_run_d<FMT_INT8>(c.d, tk, tv, a, ctas, st);
+    case FMT_E4M3: return ka_run_f<FMT_E4M3>(c.d, nr, tk, tv, a, sms, st);
+    case FMT_E5M2: return ka_run_f<FMT_E5M2>(c.d, nr, tk, tv, a, sms, st);
+    default: return ka_run_f<FMT_INT8>(c.d, nr, tk, tv, a, sms, st);
   }
 }
 
