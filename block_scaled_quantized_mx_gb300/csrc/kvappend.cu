@@ -73,7 +73,7 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
 
 // NP: 16-byte loads per thread that cover a whole page of one head.
 template <int FMT, int NP>
-__global__ void __launch_bounds__(AP_THREADS) kv_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(AP_THREADS, NP == 16 ? 4 : 8) kv_append_kernel(const AppendArgs a) {
   __shared__ uint32_t sm_max[AP_THREADS / 32];
   __shared__ int sm_len;
   __shared__ uint32_t sm_begin[4];          // one bit per token of the segment

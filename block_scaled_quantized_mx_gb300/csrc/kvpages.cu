@@ -15,13 +15,13 @@
 //
 // A few KB in, a slot (8 bytes) per token out: the launch and a chain of
 // dependent reads bound it, not bandwidth.  So it is one launch with no
-// scratch memory and no atomics on global memory: every CTA of one cluster
-// scans all requests for itself (two integer prefix sums over B lengths read
-// from L2), and only the filling of tables and slots is divided.  The
-// cluster barrier stands between the last read of an input and the first
-// write of an output, so outputs may overwrite their inputs.  One CTA for
-// small steps; eight (the portable cluster limit) where there are thousands
-// of slots to write.
+// scratch memory and no atomics on global memory: every CTA scans all
+// requests for itself (two integer prefix sums over B lengths read from L2),
+// and only the filling of tables and slots is divided.  A page id is read
+// once per 32 blocks and passed on by shuffles.  Where an output overwrites an
+// input, the CTAs are one cluster (of at most eight, the portable limit) with
+// its barrier between the last read of an input and the first write of an
+// output; otherwise there are as many as the slots keep busy.
 #include <cstdint>
 
 #include "common.cuh"
@@ -35,6 +35,7 @@ namespace {
 constexpr int PG_THREADS = 512;
 constexpr int PG_WARPS = PG_THREADS / 32;
 constexpr int PG_CLUSTER = 8;
+constexpr int PG_MAX_CTAS = 128;
 
 // Sum of two values over the block's threads before this one (exclusive), in
 // thread order; `all` receives the block's totals.  Uses `sm` (2 x PG_WARPS).
@@ -58,15 +59,23 @@ __device__ __forceinline__ Pair block_scan(Pair v, long long* sm, Pair& all) {
     sm[2 * warp + 1] = s.b;
   }
   __syncthreads();
-  Pair before{0, 0};
-  all = Pair{0, 0};
-  for (int w = 0; w < PG_WARPS; ++w) {
-    if (w == warp) before = all;
-    all.a += sm[2 * w];
-    all.b += sm[2 * w + 1];
+  // every warp scans the warps' totals for itself
+  static_assert(PG_WARPS <= 32, "one total per lane");
+  Pair t{lane < PG_WARPS ? sm[2 * lane] : 0, lane < PG_WARPS ? sm[2 * lane + 1] : 0};
+#pragma unroll
+  for (int d = 1; d < PG_WARPS; d <<= 1) {
+    const long long ua = __shfl_up_sync(0xFFFFFFFFu, t.a, d);
+    const long long ub = __shfl_up_sync(0xFFFFFFFFu, t.b, d);
+    if (lane >= d) {
+      t.a += ua;
+      t.b += ub;
+    }
   }
-  __syncthreads();
-  return Pair{before.a + s.a - v.a, before.b + s.b - v.b};
+  all.a = __shfl_sync(0xFFFFFFFFu, t.a, PG_WARPS - 1);
+  all.b = __shfl_sync(0xFFFFFFFFu, t.b, PG_WARPS - 1);
+  const long long ba = __shfl_sync(0xFFFFFFFFu, t.a, warp ? warp - 1 : 0);
+  const long long bb = __shfl_sync(0xFFFFFFFFu, t.b, warp ? warp - 1 : 0);
+  return Pair{(warp ? ba : 0) + s.a - v.a, (warp ? bb : 0) + s.b - v.b};
 }
 
 struct PagesArgs {
@@ -85,16 +94,11 @@ struct PagesArgs {
   long long* slots;
   long long max_tokens;
   int* counts_out;
+  int in_place;             // an output overwrites an input: the CTAs are a cluster
 };
 
 __device__ __forceinline__ long long blocks_of(long long tokens, int shift) {
   return (tokens + (1ll << shift) - 1) >> shift;
-}
-
-__device__ __forceinline__ uint32_t cluster_nctas() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
-  return r;
 }
 
 __global__ void __launch_bounds__(PG_THREADS) kv_extend_kernel(const PagesArgs a) {
@@ -115,25 +119,24 @@ __global__ void __launch_bounds__(PG_THREADS) kv_extend_kernel(const PagesArgs a
     sm_cut = B;
     sm_served = 0;
   }
-  // need and new tokens of request b; false for a request that is refused on
-  // its own: a negative length or count, or more tokens than a table row holds
-  auto request = [&](int b, int& len, long long& need, long long& fresh) {
-    len = a.lens[b];
-    fresh = a.change[b];
-    const bool ok = len >= 0 && fresh >= 0 && len + fresh <= capacity;
-    if (!ok) fresh = 0;
-    need = ok ? blocks_of(len + fresh, a.page_shift) - blocks_of(len, a.page_shift) : 0;
-    return ok;
-  };
+  // Each request's need and new tokens, kept in the arrays that later hold its
+  // first page and first token; -1 new tokens for a request that is refused
+  // on its own: a negative length or count, or more tokens than a table row
+  // holds.
   Pair mine{0, 0}, all;
   for (int b = b0; b < b1; ++b) {
-    int len;
-    long long need, fresh;
-    request(b, len, need, fresh);
+    const int len = a.lens[b];
+    const long long fresh = a.change[b];
+    const bool ok = len >= 0 && fresh >= 0 && len + fresh <= capacity && len + fresh <= 0x7FFFFFFF;
+    const long long need =
+        ok ? blocks_of(len + fresh, a.page_shift) - blocks_of(len, a.page_shift) : 0;
+    sm_len[b] = len;
+    sm_cu[b] = ok ? static_cast<int>(fresh) : -1;
+    sm_rank[b] = static_cast<int>(need);
     mine.a += need;
-    mine.b += fresh;
+    mine.b += ok ? fresh : 0;
   }
-  Pair at = block_scan(mine, sm_scan, all);
+  const Pair at = block_scan(mine, sm_scan, all);
   if (tid == 0) {
     sm_total[0] = all.a;
     sm_total[1] = all.b;
@@ -142,11 +145,8 @@ __global__ void __launch_bounds__(PG_THREADS) kv_extend_kernel(const PagesArgs a
   {
     Pair p = at;
     for (int b = b0; b < b1; ++b) {
-      int len;
-      long long need, fresh;
-      request(b, len, need, fresh);
-      p.a += need;
-      p.b += fresh;
+      p.a += sm_rank[b];
+      p.b += max(0, sm_cu[b]);
       if (p.a > avail || p.b > a.max_tokens) {
         atomicMin(&sm_cut, b);
         break;
@@ -159,19 +159,16 @@ __global__ void __launch_bounds__(PG_THREADS) kv_extend_kernel(const PagesArgs a
     Pair p = at;
     int served = 0;
     for (int b = b0; b < b1; ++b) {
-      int len;
-      long long need, fresh;
-      const bool ok = request(b, len, need, fresh);
+      const int need = sm_rank[b], fresh = sm_cu[b];
       if (b == cut) {
         sm_total[0] = p.a;
         sm_total[1] = p.b;
       }
       sm_cu[b] = b <= cut ? static_cast<int>(p.b) : -1;   // -1: the total, filled in below
       sm_rank[b] = static_cast<int>(b <= cut ? p.a : 0);
-      sm_len[b] = len;
       p.a += need;
-      p.b += fresh;
-      served += ok && b < cut;
+      p.b += max(0, fresh);
+      served += fresh >= 0 && b < cut;
     }
     if (served) atomicAdd(&sm_served, served);
   }
@@ -182,8 +179,8 @@ __global__ void __launch_bounds__(PG_THREADS) kv_extend_kernel(const PagesArgs a
     if (b > cut) sm_cu[b] = total;
   if (tid == 0) sm_cu[B] = total;
   __syncthreads();
-  cluster_sync();                           // every CTA has read its inputs
-  const int rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(cluster_nctas());
+  if (a.in_place) cluster_sync();           // every CTA has read its inputs
+  const int rank = blockIdx.x, ctas = gridDim.x;
   for (int b = rank * PG_THREADS + tid; b <= B; b += ctas * PG_THREADS) {
     a.cu[b] = sm_cu[b];
     if (b < B) a.lens_out[b] = sm_len[b] + (sm_cu[b + 1] - sm_cu[b]);
@@ -202,12 +199,28 @@ __global__ void __launch_bounds__(PG_THREADS) kv_extend_kernel(const PagesArgs a
     const long long had = blocks_of(len, a.page_shift);
     const long long has = blocks_of(static_cast<long long>(len) + n, a.page_shift);
     const int* top = a.stack + (avail - 1 - sm_rank[b]);
-    for (long long j = had + lane; j < has; j += 32) row[j] = top[had - j];
-    for (int i = lane; i < n; i += 32) {
-      const long long pos = static_cast<long long>(len) + i;
-      const long long j = pos >> a.page_shift;
-      const long long page = j < had ? row[j] : top[had - j];
-      a.slots[first + i] = page * P + (pos & (P - 1));
+    // 32 blocks at a time, a page id per lane: a partly filled last block's
+    // from the table, new ones from the stack (one load for up to 32 P tokens)
+    const long long end = static_cast<long long>(len) + n;
+    for (long long j0 = len >> a.page_shift; j0 < has; j0 += 32) {
+      const long long j = j0 + lane;
+      int page = -1;
+      if (j < had) {
+        page = row[j];
+      } else if (j < has) {
+        page = top[had - j];
+        row[j] = page;
+      }
+      const long long p0 = j0 << a.page_shift;
+      const long long from = p0 > len ? p0 : len;
+      const long long to = min(end, p0 + (32ll << a.page_shift));
+      for (long long t = from; t < to; t += 32) {
+        const long long pos = t + lane;
+        const int id = __shfl_sync(0xFFFFFFFFu, page,
+                                   static_cast<int>((pos >> a.page_shift) - j0) & 31);
+        if (pos < to)
+          a.slots[first + (pos - len)] = static_cast<long long>(id) * P + (pos & (P - 1));
+      }
     }
   }
   for (long long t = total + rank * PG_THREADS + tid; t < a.max_tokens; t += ctas * PG_THREADS)
@@ -242,8 +255,8 @@ __global__ void __launch_bounds__(PG_THREADS) kv_truncate_kernel(const PagesArgs
     at.a += blocks_in_row(sm_len[b]) - blocks_in_row(sm_keep[b]);
   }
   __syncthreads();
-  cluster_sync();                           // every CTA has read its inputs
-  const int rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(cluster_nctas());
+  if (a.in_place) cluster_sync();           // every CTA has read its inputs
+  const int rank = blockIdx.x, ctas = gridDim.x;
   for (int b = rank * PG_THREADS + tid; b < B; b += ctas * PG_THREADS) a.lens_out[b] = sm_keep[b];
   if (rank == 0 && tid == 0) {
     const long long n = count + all.a;
@@ -262,22 +275,37 @@ __global__ void __launch_bounds__(PG_THREADS) kv_truncate_kernel(const PagesArgs
   }
 }
 
-cudaError_t launch_pages(void (*kern)(const PagesArgs), const PagesArgs& a, size_t smem,
-                         bool cluster, cudaStream_t st) {
+cudaError_t launch_pages(void (*kern)(const PagesArgs), PagesArgs& a, size_t smem,
+                         cudaStream_t st) {
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(
         kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  const unsigned ctas = cluster ? PG_CLUSTER : 1;
+  const char* in[3] = {reinterpret_cast<const char*>(a.lens),
+                       reinterpret_cast<const char*>(a.change),
+                       reinterpret_cast<const char*>(a.count)};
+  const int64_t in_bytes[3] = {4ll * a.requests, 4ll * a.requests, 4};
+  const char* out[3] = {reinterpret_cast<const char*>(a.lens_out),
+                        reinterpret_cast<const char*>(a.counts_out),
+                        reinterpret_cast<const char*>(a.cu)};
+  const int64_t out_bytes[3] = {4ll * a.requests, 8, a.cu ? 4ll * (a.requests + 1) : 0};
+  a.in_place = 0;
+  for (int i = 0; i < 3; ++i)
+    for (int o = 0; o < 3; ++o)
+      if (in[i] < out[o] + out_bytes[o] && out[o] < in[i] + in_bytes[i]) a.in_place = 1;
+  // a warp for every 4 requests or 128 slots
+  const int64_t want = (a.requests / 4 + a.max_tokens / 128) / PG_WARPS;
+  const int64_t most = a.in_place ? PG_CLUSTER : PG_MAX_CTAS;
+  const int64_t ctas = want < 1 ? 1 : (want > most ? most : (a.in_place ? PG_CLUSTER : want));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(PG_THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.x = a.in_place ? static_cast<unsigned>(ctas) : 1;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
@@ -308,8 +336,7 @@ cudaError_t launch_kv_extend(const int* lens, const int* fresh, int64_t requests
   a.slots = reinterpret_cast<long long*>(slots);
   a.max_tokens = max_tokens;
   a.counts_out = counts_out;
-  return launch_pages(kv_extend_kernel, a, (3 * requests + 1) * sizeof(int),
-                      requests + max_tokens > 4096, st);
+  return launch_pages(kv_extend_kernel, a, (3 * requests + 1) * sizeof(int), st);
 }
 
 cudaError_t launch_kv_truncate(const int* lens, const int* keep, int64_t requests, int* table,
@@ -329,7 +356,7 @@ cudaError_t launch_kv_truncate(const int* lens, const int* keep, int64_t request
   a.requests = static_cast<int>(requests);
   a.lens_out = lens_out;
   a.counts_out = counts_out;
-  return launch_pages(kv_truncate_kernel, a, 3 * requests * sizeof(int), requests > 512, st);
+  return launch_pages(kv_truncate_kernel, a, 3 * requests * sizeof(int), st);
 }
 
 }  // namespace mxk
