@@ -499,11 +499,11 @@ mx_status mx_last_error(void* stream) {
   cudaError_t e3 = cudaSuccess, e4 = cudaSuccess;
   const unsigned c = mxk::fetch_and_clear_status_dq(&e3);
   const unsigned d = mxk::fetch_and_clear_status_attn(&e4);
-  cudaError_t e5 = cudaSuccess, e6 = cudaSuccess;
+  cudaError_t e5 = cudaSuccess, e6 = cudaSuccess, e7 = cudaSuccess;
   const unsigned f = mxk::fetch_and_clear_status_dqd(&e5);
-  const unsigned g = mxk::fetch_and_clear_status_kv(&e6);
+  const unsigned g = mxk::fetch_and_clear_status_kv(&e6) | mxk::fetch_and_clear_status_kvp(&e7);
   if (e1 != cudaSuccess || e2 != cudaSuccess || e3 != cudaSuccess || e4 != cudaSuccess ||
-      e5 != cudaSuccess || e6 != cudaSuccess)
+      e5 != cudaSuccess || e6 != cudaSuccess || e7 != cudaSuccess)
     return MX_ERR_CUDA;
   if ((a | b | c | d | f | g) & mxk::STATUS_TIMEOUT) return MX_ERR_TIMEOUT;
   return MX_OK;

@@ -73,4 +73,11 @@ size_t kv_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t d
 cudaError_t launch_kv_attention(const KvAttn& a, cudaStream_t st);
 unsigned fetch_and_clear_status_kv(cudaError_t* err);
 
+// Its kernel for many rows per request (kvprompt.cu), up to
+// kv_prompt_max_requests() requests.
+int64_t kv_prompt_max_requests();
+size_t kv_prompt_workspace_bytes(int64_t d, int sms);
+cudaError_t launch_kv_prompt(const KvAttn& a, int sms, cudaStream_t st);
+unsigned fetch_and_clear_status_kvp(cudaError_t* err);
+
 }  // namespace mxk

@@ -135,7 +135,6 @@ struct KaArgs {
   int bf16;
   int o_dtype;
   float scale_log2e;
-  int skip_rows;               // requests with more rows than this are another kernel's
   float* ws;                   // two slots per CTA: [rows][D] of O, then m[rows], l[rows]
   uint8_t* joins;              // one KaJoin per CTA, behind the slots
 };
@@ -171,7 +170,7 @@ __device__ __forceinline__ KaReq ka_request(const KaArgs& a, int b) {
   const int first = kv_first_key(a.v, q.r, 0);
   q.tile0 = first / KA_TK;
   q.tiles = 1 + max(1, (q.r.len + KA_TK - 1) / KA_TK - q.tile0);
-  q.row_tiles = rows > a.skip_rows ? 0 : static_cast<int>((rows + ROWS - 1) / ROWS);
+  q.row_tiles = static_cast<int>((rows + ROWS - 1) / ROWS);
   q.units = static_cast<long long>(q.row_tiles) * a.v.heads;
   return q;
 }
@@ -993,13 +992,26 @@ cudaError_t ka_run_f(int64_t d, int nr, const CUtensorMap& tk, const CUtensorMap
 
 }  // namespace
 
+namespace {
+
+// More rows of one request and cache head than this go to the prompt kernel.
+constexpr int64_t KA_MOST_ROWS = 16;
+bool many_rows(int64_t max_q, int64_t group) { return max_q * group > KA_MOST_ROWS; }
+
+}  // namespace
+
 size_t kv_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t max_q) {
   const int sms = ka_sm_count();
-  return std::max(ka_ws_bytes(d, 1, sms), ka_ws_bytes(d, 2, sms));
+  const size_t few = std::max(ka_ws_bytes(d, 1, sms), ka_ws_bytes(d, 2, sms));
+  return many_rows(max_q, q_heads / kv_heads) ? std::max(few, kv_prompt_workspace_bytes(d, sms)) : few;
 }
 
 cudaError_t launch_kv_attention(const KvAttn& q, cudaStream_t st) {
   const KvCache& c = q.cache;
+  const int sms = ka_sm_count();
+  if (sms <= 0) return cudaErrorInvalidValue;
+  if (many_rows(q.max_q, q.q_heads / c.heads) && q.requests <= kv_prompt_max_requests())
+    return launch_kv_prompt(q, sms, st);
   KaArgs a{};
   a.v = kv_view(q);
   a.Q = static_cast<const uint16_t*>(q.Q);
@@ -1011,9 +1023,6 @@ cudaError_t launch_kv_attention(const KvAttn& q, cudaStream_t st) {
   a.bf16 = q.dtype == DT_BF16;
   a.o_dtype = q.o_dtype;
   a.scale_log2e = q.scale * 1.4426950408889634f;
-  a.skip_rows = 0x7FFFFFFF;
-  const int sms = ka_sm_count();
-  if (sms <= 0) return cudaErrorInvalidValue;
   // eight rows where the rows that one request has for a cache head fit
   const int nr = q.max_q * a.v.group <= 8 ? 1 : 2;
   if (q.ws && q.ws_bytes >= ka_ws_bytes(c.d, nr, sms)) {

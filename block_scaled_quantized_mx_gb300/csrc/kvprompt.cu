@@ -1,0 +1,1105 @@
+// kvprompt.cu -- attention over the 8-bit paged key/value cache for many query
+// rows per request (prompts and their chunks): the formula, the masks and the
+// precision of kvattn.cu, on the fifth-generation tensor core.
+//
+// Bound: the 16-bit tensor rate, 4 d flop per row and visible key.  One CTA
+// per SM; a unit is 256 rows of one request and cache head (row r is token
+// r / group, head r % group of the group, so that all heads of a group share
+// the converted keys), in two tiles of 128 that take turns on the tensor core
+// as in attention.cu.  What differs from dense attention:
+//   * K and V come as codes.  Warp 0 reads the block table and loads blocks of
+//     128 keys page by page with TMA into one slot for K and one for V; warps
+//     0, 2 and 3 take a slot's codes into registers (which frees the slot for
+//     the next block at once), turn them into f16 -- exactly, for all three
+//     formats -- and write the swizzled operand tiles, two deep each.  The
+//     conversion of a block serves both tiles and, through the rows' order,
+//     all heads of the group;
+//   * page scales stay out of the operands: K's is a factor of the scores of
+//     its 16 .. 128 keys, applied with the softmax scale in the exponent's FMA;
+//     V's, a power of two relative to the largest so far, is added to the
+//     exponent, so P carries it exactly and the row sums take it out again;
+//   * rows are converted once per unit: the thread that owns a row brings it
+//     to f16 with a power of two of its own, and keeps its mask bounds;
+//   * the units are cut evenly over the SMs, as in kvattn.cu: a stretch of the
+//     list of all (request, row tile, cache head, key block)s per CTA, each
+//     unit standing with some entries more for what it costs to begin and end
+//     one; parts of units go to the workspace and a second kernel joins them.
+// Tensor memory as in attention.cu: S (then P) of tile t in columns [256 t,
+// 256 t + 128), its O behind.  Every mbarrier wait is bounded.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "common.cuh"
+#include "gemm_common.cuh"
+#include "kv_common.cuh"
+#include "kv_kernel.cuh"
+#include "ptx.cuh"
+
+namespace mxk {
+
+namespace {
+
+__device__ unsigned int g_status_kvp = 0;
+
+constexpr int KP_BQ = 128;                 // rows per tile
+constexpr int KP_ROWS = 2 * KP_BQ;         // rows of a unit
+constexpr int KP_BK = 128;                 // keys per block
+constexpr int KP_THREADS = 384;            // warpgroup 0, two softmax warpgroups
+constexpr int KP_WARPS = KP_THREADS / 32;
+constexpr int KP_CONV = 96;                // converting threads: warps 0, 2, 3
+// Registers: launched at 168; 96 * 128 + 200 * 256 = 63488 <= 384 * 168.
+constexpr int KP_REGS_LOW = 96;
+constexpr int KP_REGS_HIGH = 200;
+constexpr int KP_TMEM_COLS = 512;
+constexpr float KP_LAZY = 8.0f;            // slack of the exponentials' reference point
+constexpr int KP_P_EXP = 7;                // P is scaled by 2^7: at most 2^(7 + 8) in f16
+constexpr int KP_OVER = 4;                 // entries of a unit besides its blocks
+constexpr int KP_PG = 8;                   // blocks whose page data is kept
+constexpr int KP_MAX_REQUESTS = 16384;
+
+// One block's pages: per 16 keys at most one page.
+struct KpPages {
+  float kf[8];                             // K's scale (NaN: none or a NaN page)
+  int ve[8];                               // V's scale code, 0xFF NaN, -1 not loaded
+};
+
+// One CTA's part of a unit, as every role sees it.
+struct KpSeg {
+  int count;                               // key blocks (0: no more segments)
+  int block;                               // the first
+  int len;                                 // the request's length
+  int n;                                   // its tokens
+  long long q0;                            // its first row of Q
+  int row0;                                // the unit's first row
+  int head;
+  int slot;                                // workspace slot, -1: not a part
+  int pad;
+};
+
+// A unit that begins in this CTA's stretch and goes on in others'.
+struct KpJoin {
+  int live;                                // rows (0: there is none)
+  int parts;                               // CTAs that share it
+  int first_slot;                          // this CTA's slot; the others use their first
+  int head;
+  int row0;
+  int pad;
+  long long q0;
+};
+
+// The key blocks of row tile rt of a request: [first, first + count).
+__device__ __forceinline__ int kp_blocks(const KvView& v, const KvReq& r, int rt, int& first) {
+  const int rows = r.n * v.group;
+  const int t0 = rt * KP_ROWS / v.group;
+  const int t1 = (min(rows, (rt + 1) * KP_ROWS) - 1) / v.group;
+  const int lo = kv_first_key(v, r, t0), hi = kv_end_key(v, r, t1);
+  first = lo / KP_BK;
+  const int n = hi > lo ? (hi + KP_BK - 1) / KP_BK - first : 0;
+  return n > 0 ? n : 1;
+}
+__device__ __forceinline__ int kp_row_tiles(const KvView& v, const KvReq& r) {
+  return (r.n * v.group + KP_ROWS - 1) / KP_ROWS;
+}
+
+// The walk over one CTA's stretch of the list: groups of units (request, row
+// tile), in each the cache heads, each with KP_OVER entries and its blocks.
+struct KpWalk {
+  long long w, w1;
+  long long base;              // first entry of the group
+  int b, rt, tiles;            // request, row tile, the request's row tiles
+  int blocks, block0;          // of each unit of the group
+  KvReq r;
+  int head, block, count;
+  bool begins, ends;
+  long long unit_start, unit_end;
+
+  __device__ __forceinline__ void enter(const KvView& v) {   // b, rt -> the rest
+    r = kv_request(v, b);
+    tiles = kp_row_tiles(v, r);
+    if (rt < tiles) blocks = kp_blocks(v, r, rt, block0);
+  }
+  __device__ __forceinline__ bool next(const KvView& v) {
+    while (w < w1) {
+      while (w >= base + static_cast<long long>(v.heads) * (KP_OVER + blocks)) {
+        base += static_cast<long long>(v.heads) * (KP_OVER + blocks);
+        if (++rt < tiles) {
+          blocks = kp_blocks(v, r, rt, block0);
+          continue;
+        }
+        rt = 0;
+        do {
+          if (++b >= v.requests) return false;
+          enter(v);
+        } while (tiles == 0);
+      }
+      const int c = KP_OVER + blocks;
+      head = static_cast<int>((w - base) / c);
+      const long long unit = base + static_cast<long long>(head) * c;
+      unit_start = unit + KP_OVER;
+      unit_end = unit + c;
+      if (w < unit_start) {
+        w = unit_start;
+        if (w >= w1) return false;           // the unit's blocks are the next CTA's
+      }
+      const int t = static_cast<int>(w - unit_start);
+      block = block0 + t;
+      count = static_cast<int>(min(static_cast<long long>(blocks - t), w1 - w));
+      begins = t == 0;
+      ends = t + count == blocks;
+      w += count;
+      return true;
+    }
+    return false;
+  }
+};
+
+template <int D>
+struct KpSmem {
+  static constexpr int REGION = 128 * 128;
+  static constexpr int Q_BYTES = (D / 64) * REGION;
+  static constexpr int K_BYTES = (D / 64) * REGION;
+  static constexpr int V_BYTES = 2 * (D / 64) * 8192;
+  static constexpr int RAW_BYTES = KP_BK * D;
+  static constexpr int Q_OFF = 0;
+  static constexpr int K_OFF = Q_OFF + 2 * Q_BYTES;
+  static constexpr int V_OFF = K_OFF + 2 * K_BYTES;
+  static constexpr int RAW_OFF = V_OFF + 2 * V_BYTES;    // K's slot, V's slot
+  static constexpr int PG_OFF = RAW_OFF + 2 * RAW_BYTES;
+  static constexpr int SEG_OFF = PG_OFF + KP_PG * static_cast<int>(sizeof(KpPages));
+  static constexpr int BAR_OFF = SEG_OFF + 2 * static_cast<int>(sizeof(KpSeg));
+  // q_full[2], k_full[2], v_full[2], k_empty[2], v_empty[2], s_full[2],
+  // p_full[2 tiles][2 halves], o_done[2], raw_full[2], raw_empty[2],
+  // seg_full[2], seg_empty[2], pg_full[8]
+  static constexpr int BARS = 2 + 8 + 2 + 4 + 2 + 8 + KP_PG;
+  static constexpr int MISC_OFF = BAR_OFF + BARS * 8;
+  static constexpr int WALK_OFF = MISC_OFF + 16;
+  static constexpr int TOTAL = WALK_OFF + static_cast<int>(sizeof(KpWalk));
+  static constexpr int ALLOC = TOTAL + 1024;
+  static_assert(ALLOC <= 232448, "shared memory budget");
+  static_assert(K_OFF + 2 * K_BYTES >= (KP_MAX_REQUESTS + 1) * 4 - 4, "the plan's array fits");
+};
+
+struct KpArgs {
+  KvView v;
+  const uint16_t* Q;
+  void* O;
+  long long q_ts, q_hs, o_ts, o_hs;
+  int bf16;
+  int o_dtype;
+  float scale_log2e;
+  float* ws;                               // two slots per CTA: 256 x D of O, m[256], l[256]
+  KpJoin* joins;                           // one per CTA
+};
+
+__device__ __forceinline__ void kp_timeout(volatile int* abort, unsigned site) {
+  *abort = 1;
+  atomicOr(&g_status_kvp, STATUS_TIMEOUT | site);
+}
+
+// kind::f16 instruction descriptor: D f32, A and B f16, A K-major, B K-major
+// (b_mn = 0) or MN-major (1), N >> 3 at bit 17, M = 128.
+__device__ __forceinline__ uint32_t kp_idesc(uint32_t n, uint32_t b_mn) {
+  return (1u << 4) | (b_mn << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// The MMA warp runs its loop with all 32 lanes (warp-uniform descriptors); one
+// elected lane issues.
+__device__ __forceinline__ void kp_mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t id,
+                                          uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void kp_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
+                                          uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void kp_commit(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          bar)
+      : "memory");
+}
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Exclusive prefix sum over the block's threads, and the total.
+__device__ __forceinline__ long long kp_scan(long long v, long long* sm, long long& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long s = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long u = __shfl_up_sync(0xFFFFFFFFu, s, d);
+    if (lane >= d) s += u;
+  }
+  if (lane == 31) sm[warp] = s;
+  __syncthreads();
+  long long before = 0;
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < KP_WARPS; ++w) {
+    if (w < warp) before += sm[w];
+    all += sm[w];
+  }
+  __syncthreads();
+  return before + s - v;
+}
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(KP_THREADS, 1)
+kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                 const KpArgs a) {
+  using L = KpSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const uint32_t bar_q = base + L::BAR_OFF;
+  const uint32_t bar_k = bar_q + 16;
+  const uint32_t bar_v = bar_k + 16;
+  const uint32_t bar_k_empty = bar_v + 16;
+  const uint32_t bar_v_empty = bar_k_empty + 16;
+  const uint32_t bar_s_full = bar_v_empty + 16;
+  const uint32_t bar_p_full = bar_s_full + 16;     // [tile][half]
+  const uint32_t bar_o_done = bar_p_full + 32;
+  const uint32_t bar_raw = bar_o_done + 16;        // [K, V]
+  const uint32_t bar_raw_empty = bar_raw + 16;
+  const uint32_t bar_seg = bar_raw_empty + 16;
+  const uint32_t bar_seg_empty = bar_seg + 16;
+  const uint32_t bar_pg = bar_seg_empty + 16;      // [KP_PG]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::MISC_OFF);
+  volatile int* abort = reinterpret_cast<volatile int*>(gbase + L::MISC_OFF + 4);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // ---- the list: row tiles of each request, then entries of each row tile
+  // (in the operand regions, which nothing uses yet)
+  KpWalk* walk = reinterpret_cast<KpWalk*>(gbase + L::WALK_OFF);   // warp 0's, kept by lane 0
+  long long total, w0, ctas;
+  {
+    int* sm_rt = reinterpret_cast<int*>(gbase);                        // requests + 1
+    long long* sm_scan = reinterpret_cast<long long*>(gbase + L::RAW_OFF);
+    const int B = a.v.requests;
+    const int per = (B + KP_THREADS - 1) / KP_THREADS;
+    const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+    long long mine = 0, tiles;
+    for (int b = b0; b < b1; ++b) mine += kp_row_tiles(a.v, kv_request(a.v, b));
+    long long at = kp_scan(mine, sm_scan, tiles);
+    for (int b = b0; b < b1; ++b) {
+      sm_rt[b] = static_cast<int>(at);
+      at += kp_row_tiles(a.v, kv_request(a.v, b));
+    }
+    __syncthreads();
+    const long long tper = (tiles + KP_THREADS - 1) / KP_THREADS;
+    const long long f0 = min(tiles, tid * tper), f1 = min(tiles, f0 + tper);
+    // walks the row tiles [f0, f1): calls f(b, rt, request) for each
+    auto each = [&](auto f) {
+      if (f0 >= f1) return;
+      int lo = 0, hi = B - 1;                // the last request that begins at or before f0
+      while (lo < hi) {
+        const int m = (lo + hi + 1) >> 1;
+        if (sm_rt[m] <= f0) lo = m; else hi = m - 1;
+      }
+      int b = lo;
+      KvReq r = kv_request(a.v, b);
+      int rt = static_cast<int>(f0 - sm_rt[b]), n = kp_row_tiles(a.v, r);
+      for (long long i = f0; i < f1; ++i, ++rt) {
+        while (rt >= n) {
+          rt = 0;
+          r = kv_request(a.v, ++b);
+          n = kp_row_tiles(a.v, r);
+        }
+        if (!f(b, rt, r)) return;
+      }
+    };
+    mine = 0;
+    each([&](int, int rt, const KvReq& r) {
+      int first;
+      mine += static_cast<long long>(a.v.heads) * (KP_OVER + kp_blocks(a.v, r, rt, first));
+      return true;
+    });
+    long long before = kp_scan(mine, sm_scan, total);
+    ctas = min(static_cast<long long>(gridDim.x), total);
+    w0 = total * blockIdx.x / max(1ll, ctas);
+    if (blockIdx.x < ctas && w0 >= before && w0 < before + mine) {
+      long long p = before;
+      each([&](int b, int rt, const KvReq& r) {
+        int first;
+        const int blocks = kp_blocks(a.v, r, rt, first);
+        const long long n = static_cast<long long>(a.v.heads) * (KP_OVER + blocks);
+        if (w0 >= p + n) {
+          p += n;
+          return true;
+        }
+        KpWalk k;
+        k.w = w0;
+        k.w1 = total * (blockIdx.x + 1) / ctas;
+        k.base = p;
+        k.b = b;
+        k.rt = rt;
+        k.enter(a.v);
+        if (a.ws == nullptr) {
+          // units stay whole: the CTA in whose stretch a unit begins takes all of it
+          const long long c = KP_OVER + k.blocks;
+          k.w = p + (w0 - p + c - 1) / c * c;          // may be the next group's first
+        }
+        *walk = k;
+        return false;
+      });
+    }
+    __syncthreads();
+    KpJoin* join = a.joins ? a.joins + blockIdx.x : nullptr;
+    if (tid == 0 && join) join->live = 0;
+    if (blockIdx.x >= ctas) return;          // the whole CTA: nothing was started
+  }
+  // the regions go to their owners, TMA and the tensor core among them
+  fence_proxy_async_smem();
+  __syncthreads();
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_q + 8 * i, 4);
+      mbar_init(bar_k + 8 * i, 3);
+      mbar_init(bar_v + 8 * i, 3);
+      mbar_init(bar_k_empty + 8 * i, 1);
+      mbar_init(bar_v_empty + 8 * i, 1);
+      mbar_init(bar_s_full + 8 * i, 1);
+      mbar_init(bar_p_full + 16 * i, 4);
+      mbar_init(bar_p_full + 16 * i + 8, 4);
+      mbar_init(bar_o_done + 8 * i, 1);
+      mbar_init(bar_raw + 8 * i, 1);
+      mbar_init(bar_raw_empty + 8 * i, 3);
+      mbar_init(bar_seg + 8 * i, 1);
+      mbar_init(bar_seg_empty + 8 * i, 12);
+    }
+    for (int i = 0; i < KP_PG; ++i) mbar_init(bar_pg + 8 * i, 1);
+    *abort = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+  }
+  if (warp == 1) tmem_alloc_cg<1>(smem_u32(tmem_slot), KP_TMEM_COLS);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const KpSeg* segs = reinterpret_cast<const KpSeg*>(gbase + L::SEG_OFF);
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(KP_REGS_LOW));
+    if (warp != 1) {
+      // ---------------------------------------------------- loads, conversion
+      const int c0 = (warp == 0 ? 0 : warp - 1) * 32 + lane;      // 0 .. 95
+      constexpr int CPR = D / 16;                                 // 16-code chunks per row
+      constexpr int CHUNKS = KP_BK * CPR;
+      constexpr int IT = (CHUNKS + KP_CONV - 1) / KP_CONV;
+      const int shift = a.v.page_shift;
+      bool ok = true;
+      // -- warp 0's cursor of loads, one block ahead of the conversion
+      int ahead = 0;                         // blocks whose loads were issued
+      int issued[2] = {0, 0};                // of K, of V
+      int left = 0, at_block = 0, seg_out = 0, id = -1;
+      int len_ahead = 0, head_ahead = 0;
+      const int* row = nullptr;
+      bool more = true, first_seg = true;
+      // the next block's K (kv 0) or V (kv 1); publishes a segment as it enters it
+      auto issue = [&](int kv) {
+        if (!more || !ok) return;
+        if (kv == 0) {
+          if (left == 0) {
+            const int ss = seg_out & 1;
+            if (!mbar_wait(bar_seg_empty + 8 * ss, ((seg_out >> 1) & 1) ^ 1, abort)) {
+              if (lane == 0) kp_timeout(abort, 0x51);
+              ok = false;
+              return;
+            }
+            ++seg_out;
+            int found = 0;
+            if (lane == 0) {
+              if (a.ws != nullptr) {
+                found = walk->next(a.v);
+              } else if (walk->w < walk->w1) {
+                const long long w1 = walk->w1;
+                walk->w1 = 0x7FFFFFFFFFFFFFFFll;
+                found = walk->next(a.v);
+                walk->w1 = w1;
+              }
+              KpSeg* s = const_cast<KpSeg*>(segs) + ss;
+              s->count = found ? walk->count : 0;
+              if (found) {
+                s->block = walk->block;
+                s->len = walk->r.len;
+                s->n = walk->r.n;
+                s->q0 = walk->r.q0;
+                s->row0 = walk->rt * KP_ROWS;
+                s->head = walk->head;
+                const int slot = 2 * static_cast<int>(blockIdx.x) + (first_seg ? 0 : 1);
+                s->slot = walk->begins && walk->ends ? -1 : slot;
+                if (walk->begins && !walk->ends) {
+                  KpJoin* j = a.joins + blockIdx.x;
+                  j->live = min(KP_ROWS, walk->r.n * a.v.group - walk->rt * KP_ROWS);
+                  j->parts = static_cast<int>((walk->unit_end * ctas - 1) / total - blockIdx.x + 1);
+                  j->first_slot = slot;
+                  j->head = walk->head;
+                  j->row0 = walk->rt * KP_ROWS;
+                  j->q0 = walk->r.q0;
+                }
+              }
+              mbar_arrive(bar_seg + 8 * ss);
+            }
+            __syncwarp();
+            more = __shfl_sync(0xFFFFFFFFu, found, 0) != 0;
+            first_seg = false;
+            if (!more) return;
+            left = walk->count;
+            at_block = walk->block;
+            row = a.v.table + static_cast<long long>(walk->b) * a.v.table_stride;
+            len_ahead = walk->r.len;
+            head_ahead = walk->head;
+          }
+          // the block's pages, one per lane
+          const int key0 = at_block * KP_BK;
+          id = -1;
+          if (lane < (KP_BK >> shift) && key0 + (lane << shift) < len_ahead) {
+            id = row[(key0 >> shift) + lane];
+            if (id >= a.v.pages) id = -1;
+          }
+        }
+        if (!mbar_wait(bar_raw_empty + 8 * kv, (ahead & 1) ^ 1, abort)) {
+          if (lane == 0) kp_timeout(abort, 0x52);
+          ok = false;
+          return;
+        }
+        const unsigned have = __ballot_sync(0xFFFFFFFFu, id >= 0);
+        const uint32_t full = bar_raw + 8 * kv;
+        if (kv) ++issued[1]; else ++issued[0];
+        if (lane == 0)
+          mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(have)) * (D << shift));
+        __syncwarp();
+        if (id >= 0) {
+          const int y = static_cast<int>((static_cast<long long>(id) * a.v.heads + head_ahead) << shift);
+          tma_load_2d(base + L::RAW_OFF + kv * L::RAW_BYTES + lane * (D << shift),
+                      kv ? &tmV : &tmK, full, 0, y);
+        }
+        if (kv == 0) {
+          const int ps = ahead & (KP_PG - 1);
+          KpPages* pg = reinterpret_cast<KpPages*>(gbase + L::PG_OFF) + ps;
+          if (lane < (KP_BK >> shift)) {
+            float kf = __uint_as_float(0x7FC00000u);
+            int ve = -1;
+            if (id >= 0) {
+              const long long unit = static_cast<long long>(id) * a.v.heads + head_ahead;
+              kf = kv_scale_value(a.v.k_scales[unit]);
+              ve = a.v.v_scales[unit];
+            }
+            pg->kf[lane] = kf;
+            pg->ve[lane] = ve;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_pg + 8 * ps);
+        } else {
+          ++ahead;
+          ++at_block;
+          --left;
+        }
+      };
+      if (warp == 0) {
+        issue(0);
+        issue(1);
+      }
+      int bt = 0, seg_it = 0;
+      while (ok) {
+        const int ss = seg_it & 1;
+        if (!mbar_wait(bar_seg + 8 * ss, (seg_it >> 1) & 1, abort)) {
+          if (lane == 0) kp_timeout(abort, 0x53);
+          break;
+        }
+        ++seg_it;
+        const int count = segs[ss].count, len = segs[ss].len, block0 = segs[ss].block;
+        if (count == 0) break;
+        for (int j = 0; j < count && ok; ++j, ++bt) {
+          const int st = bt & 1, key0 = (block0 + j) * KP_BK;
+          const KpPages* pg = reinterpret_cast<const KpPages*>(gbase + L::PG_OFF) + (bt & (KP_PG - 1));
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            if (!mbar_wait(bar_raw + 8 * kv, bt & 1, abort) ||
+                !mbar_wait(bar_pg + 8 * (bt & (KP_PG - 1)), (bt / KP_PG) & 1, abort)) {
+              if (lane == 0) kp_timeout(abort, 0x54);
+              ok = false;
+              break;
+            }
+            uint4 w[IT];
+            const uint32_t src = base + L::RAW_OFF + kv * L::RAW_BYTES;
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+              const int ch = i * KP_CONV + c0, r = ch / CPR, c = ch % CPR;
+              if (ch < CHUNKS) {
+                const int sw = D == 128 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3));
+                w[i] = ld_shared_v4(src + r * D + sw * 16);
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_raw_empty + 8 * kv);
+            if (kv == 1 && key0 + KP_BK > len) {
+              // keys behind the request's end: zeros, whatever the page holds
+#pragma unroll
+              for (int i = 0; i < IT; ++i)
+                if (key0 + (i * KP_CONV + c0) / CPR >= len) w[i] = make_uint4(0, 0, 0, 0);
+            }
+            if (kv == 1) {
+              // and those of pages that were not loaded
+              bool gone = false;
+              for (int p = 0; p < (KP_BK >> shift); ++p) gone |= pg->ve[p] < 0;
+              if (gone) {
+#pragma unroll
+                for (int i = 0; i < IT; ++i) {
+                  const int r = (i * KP_CONV + c0) / CPR;
+                  if (r < KP_BK && pg->ve[r >> shift] < 0) w[i] = make_uint4(0, 0, 0, 0);
+                }
+              }
+            }
+            if (warp == 0) issue(kv);
+            if (!ok) break;
+            if (!mbar_wait((kv ? bar_v_empty : bar_k_empty) + 8 * st, ((bt >> 1) & 1) ^ 1, abort)) {
+              if (lane == 0) kp_timeout(abort, 0x55);
+              ok = false;
+              break;
+            }
+            const uint32_t dst = base + (kv ? L::V_OFF + st * L::V_BYTES : L::K_OFF + st * L::K_BYTES);
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+              const int ch = i * KP_CONV + c0, r = ch / CPR, c = ch % CPR;
+              if (ch < CHUNKS) {
+                // 16 codes: two 16-byte chunks of the f16 row, in 64-value
+                // regions (K: 128 keys; V: 64 keys) of 128-byte rows
+                uint32_t f[8];
+                kv_f16_pairs<FMT>(w[i].x, f[0], f[1]);
+                kv_f16_pairs<FMT>(w[i].y, f[2], f[3]);
+                kv_f16_pairs<FMT>(w[i].z, f[4], f[5]);
+                kv_f16_pairs<FMT>(w[i].w, f[6], f[7]);
+                const int q = 2 * (c & 3);
+                const uint32_t row =
+                    kv ? dst + (r >> 6) * (D / 64) * 8192 + (c >> 2) * 8192 + (r & 63) * 128
+                       : dst + (c >> 2) * L::REGION + r * 128;
+                const uint32_t a0 = row + ((q ^ (r & 7)) << 4), a1 = row + (((q + 1) ^ (r & 7)) << 4);
+                // the upper half of a row goes odd chunk first: the eight
+                // lanes of a row then hit eight different bank groups
+                if (c & 4) {
+                  st_shared_v4(a1, f[4], f[5], f[6], f[7]);
+                  st_shared_v4(a0, f[0], f[1], f[2], f[3]);
+                } else {
+                  st_shared_v4(a0, f[0], f[1], f[2], f[3]);
+                  st_shared_v4(a1, f[4], f[5], f[6], f[7]);
+                }
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive((kv ? bar_v : bar_k) + 8 * st);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_seg_empty + 8 * ss);
+      }
+      if (warp == 0) {
+        // the CTA may not retire before its copies have landed
+        for (int kv = 0; kv < 2; ++kv) {
+          const int n = kv ? issued[1] : issued[0];
+          if (n == 0) continue;
+          const long long t0 = clock64();
+          while (!mbar_try_wait(bar_raw + 8 * kv, (n - 1) & 1) &&
+                 clock64() - t0 < MXK_WAIT_LIMIT_CYCLES) {
+          }
+        }
+      }
+    } else {
+      // ------------------------------------------------------------ MMA issuer
+      const uint32_t id_qk = kp_idesc(KP_BK, 0);
+      const uint32_t id_pv = kp_idesc(D, 1);
+      const uint64_t dq0 = smem_desc(base + L::Q_OFF, 16, 1024, 2);
+      const uint64_t dk0 = smem_desc(base + L::K_OFF, 16, 1024, 2);
+      const uint64_t dv0 = smem_desc(base + L::V_OFF, 8192, 1024, 2);
+      int bt = 0, bt1 = 0, seg_it = 0, seg1 = 0;
+      bool ok = true;
+      while (ok) {
+        const int ss = seg_it & 1;
+        if (!mbar_wait(bar_seg + 8 * ss, (seg_it >> 1) & 1, abort)) {
+          kp_timeout(abort, 0x56);
+          break;
+        }
+        const int nkb = segs[ss].count;
+        if (nkb == 0) break;
+        const int live = segs[ss].n * a.v.group - segs[ss].row0;
+        const int tiles = live > KP_BQ ? 2 : 1;
+        ++seg_it;
+        // tile 1 sits a unit of up to 128 rows out: its barriers count its own
+        // units and blocks
+        for (int t = 0; t < tiles && ok; ++t) {
+          ok = mbar_wait(bar_q + 8 * t, (t ? seg1 : seg_it - 1) & 1, abort);
+          if (!ok) kp_timeout(abort, 0x57);
+        }
+        if (!ok) break;
+        tc_fence_after();
+        for (int j = 0; j <= nkb && ok; ++j) {
+          for (int t = 0; t < tiles && ok; ++t) {
+            const uint32_t s_t = tmem_base + 256 * t;
+            const uint32_t o_t = s_t + 128;
+            if (j >= 1) {
+              const int g = bt + j - 1, st = g & 1;
+              const uint32_t pp = ((t ? bt1 : bt) + j - 1) & 1;
+              if (!mbar_wait(bar_p_full + 16 * t, pp, abort) ||
+                  !mbar_wait(bar_v + 8 * st, (g >> 1) & 1, abort)) {
+                kp_timeout(abort, 0x58);
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < KP_BK / 16; ++kk) {
+                if (kk == KP_BK / 32) {
+                  if (!mbar_wait(bar_p_full + 16 * t + 8, pp, abort)) {
+                    kp_timeout(abort, 0x59);
+                    ok = false;
+                    break;
+                  }
+                  tc_fence_after();
+                }
+                const uint32_t boff = (kk >> 2) * (D / 64) * 8192 + (kk & 3) * 2048;
+                kp_mma_ts(o_t, s_t + 8 * kk,
+                          dv0 + static_cast<uint64_t>((st * L::V_BYTES + boff) >> 4), id_pv,
+                          (j > 1 || kk > 0) ? 1u : 0u);
+              }
+              if (!ok) break;
+              if (t == tiles - 1) kp_commit(bar_v_empty + 8 * st);
+            }
+            if (j < nkb) {
+              const int g = bt + j, st = g & 1;
+              if (!mbar_wait(bar_k + 8 * st, (g >> 1) & 1, abort)) {
+                kp_timeout(abort, 0x5a);
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * L::REGION + (kk & 3) * 32;
+                kp_mma_ss(s_t, dq0 + static_cast<uint64_t>((t * L::Q_BYTES + off) >> 4),
+                          dk0 + static_cast<uint64_t>((st * L::K_BYTES + off) >> 4), id_qk,
+                          kk > 0 ? 1u : 0u);
+              }
+              kp_commit(bar_s_full + 8 * t);
+              if (t == tiles - 1) kp_commit(bar_k_empty + 8 * st);
+            } else {
+              kp_commit(bar_o_done + 8 * t);
+            }
+          }
+        }
+        bt += nkb;
+        if (tiles == 2) {
+          bt1 += nkb;
+          ++seg1;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_seg_empty + 8 * ss);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(KP_REGS_HIGH));
+    // ------------------------------------------------------------ softmax
+    const int t = (warp - 4) >> 2;
+    const int quarter = warp & 3;
+    const int urow = KP_BQ * t + 32 * quarter + lane;       // row in the unit
+    const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + 256 * t;
+    const int shift = a.v.page_shift;
+    // blocks of the tile's own barriers (tile 1 may sit units out) and of all
+    int bt = 0, own = 0, own_seg = 0, seg_it = 0;
+    bool ok = true;
+    while (ok) {
+      const int ss = seg_it & 1;
+      if (!mbar_wait(bar_seg + 8 * ss, (seg_it >> 1) & 1, abort)) {
+        if (lane == 0) kp_timeout(abort, 0x5b);
+        break;
+      }
+      ++seg_it;
+      const KpSeg sg = segs[ss];
+      if (sg.count == 0) break;
+      const int rows = sg.n * a.v.group;
+      const bool works = rows - sg.row0 > KP_BQ * t;        // the tile has rows
+      // ---- this thread's row: Q to f16, its bounds and factor
+      const int row = sg.row0 + urow;
+      const bool live = row < rows;
+      const int token = live ? row / a.v.group : 0;
+      const int qh = sg.head * a.v.group + (live ? row - token * a.v.group : 0);
+      KvReq rq;
+      rq.q0 = sg.q0;
+      rq.n = sg.n;
+      rq.len = sg.len;
+      const int lo = live ? kv_first_key(a.v, rq, token) : 0;
+      const int hi = live ? kv_end_key(a.v, rq, token) : 0;
+      float up = 1.0f;
+      if (works) {
+        uint32_t w[D / 2];
+        const uint16_t* src = a.Q + (sg.q0 + token) * a.q_ts + qh * a.q_hs;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (live) v = *reinterpret_cast<const uint4*>(src + 8 * c);
+          w[4 * c] = v.x;
+          w[4 * c + 1] = v.y;
+          w[4 * c + 2] = v.z;
+          w[4 * c + 3] = v.w;
+        }
+        if (a.bf16) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int e = 0; e < D / 2; ++e)
+            top = max(top, max((w[e] << 16) & 0x7FFFFFFFu, w[e] & 0x7FFF0000u));
+          float down;
+          kv_row_factors(top, down, up);
+#pragma unroll
+          for (int e = 0; e < D / 2; ++e)
+            w[e] = cvt_f16x2(__uint_as_float(w[e] << 16) * down,
+                             __uint_as_float(w[e] & 0xFFFF0000u) * down);
+        }
+        const int r = 32 * quarter + lane;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          st_shared_v4(base + L::Q_OFF + t * L::Q_BYTES + (c >> 3) * L::REGION + r * 128 +
+                           (((c & 7) ^ (r & 7)) << 4),
+                       w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_q + 8 * t);
+      }
+      const float fr = a.scale_log2e * up;
+      // keys that every live row of this warp sees
+      const int all_lo = __reduce_max_sync(0xFFFFFFFFu, live ? lo : 0);
+      const int all_hi = __reduce_min_sync(0xFFFFFFFFu, live ? hi : 0x7FFFFFFF);
+
+      float m = -INFINITY, l = 0.0f;
+      int ev = 0;                              // V's reference exponent
+      for (int j = 0; j < sg.count && works; ++j, ++own) {
+        const int g = bt + j, key0 = (sg.block + j) * KP_BK;
+        if (!mbar_wait(bar_pg + 8 * (g & (KP_PG - 1)), (g / KP_PG) & 1, abort) ||
+            !mbar_wait(bar_s_full + 8 * t, own & 1, abort)) {
+          if (lane == 0) kp_timeout(abort, 0x5c);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const KpPages* pg = reinterpret_cast<const KpPages*>(gbase + L::PG_OFF) + (g & (KP_PG - 1));
+        uint32_t sv[KP_BK];
+#pragma unroll
+        for (int c = 0; c < KP_BK / 32; ++c)
+          tmem_ld_32x32b_x32(lane_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
+        int ev_new = ev;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          const int e = pg->ve[(16 * p) >> shift];
+          if (static_cast<unsigned>(e) < 0xFFu) ev_new = max(ev_new, e);
+        }
+        tmem_wait_ld();
+        // row maximum: of the raw scores of each 16 keys, times their factor
+        // (for a negative one, the minimum); a block that some row does not
+        // see whole is scaled and masked first
+        const bool masked = key0 < all_lo || key0 + KP_BK > all_hi;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          const float f = fr * pg->kf[(16 * p) >> shift];
+          float g0 = -INFINITY, g1 = -INFINITY;
+          if (!masked) {
+            if (fr >= 0.0f) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) {
+                g0 = max3(g0, __uint_as_float(sv[16 * p + e]), __uint_as_float(sv[16 * p + e + 1]));
+                g1 = max3(g1, __uint_as_float(sv[16 * p + e + 2]), __uint_as_float(sv[16 * p + e + 3]));
+              }
+              g0 = fmaxf(g0, g1);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) g0 = fmaxf(g0, -__uint_as_float(sv[16 * p + e]));
+              g0 = -g0;
+            }
+            mx = fmaxf(mx, g0 * f);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int k = key0 + 16 * p + e;
+              const float x = k >= lo && k < hi ? __uint_as_float(sv[16 * p + e]) * f : -INFINITY;
+              sv[16 * p + e] = __float_as_uint(x);
+              mx = fmaxf(mx, x);
+            }
+          }
+        }
+        const float m_new = mx > m + KP_LAZY ? mx : m;
+        const float alpha = m_new == m ? 1.0f : ex2_approx(m - m_new);
+        if (j >= 1 && __any_sync(0xFFFFFFFFu, m_new != m || ev_new != ev)) {
+          const float f = alpha * kv_exp2i(ev - ev_new);
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(lane_addr + 128 + 32 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st_32x32b_x32(lane_addr + 128 + 32 * c, o);
+          }
+        }
+        ev = ev_new;
+        l *= alpha;
+        m = m_new;
+        // p' = 2^(x - m + b), b = 7 + (V's exponent - the reference), rounded
+        // to f16 and written back over the scores; the sum takes b out again
+        const float m_use = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int c = 0; c < KP_BK / 32; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int p = 2 * c + h;
+            const int e8 = pg->ve[(16 * p) >> shift];
+            const bool nan = static_cast<unsigned>(e8) >= 0xFFu;
+            const int be = max(-60, KP_P_EXP + e8 - ev);
+            const float b = nan ? __uint_as_float(0x7FC00000u) : static_cast<float>(be);
+            const float f = masked ? 1.0f : fr * pg->kf[(16 * p) >> shift];
+            const float nm = b - m_use;
+            const uint64_t f2 = pack2(f, f), nm2 = pack2(nm, nm);
+            uint64_t sum = pack2(0.0f, 0.0f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float x0, x1;
+              unpack2(fma2(pack2(__uint_as_float(sv[16 * p + 2 * e]),
+                                 __uint_as_float(sv[16 * p + 2 * e + 1])),
+                           f2, nm2),
+                      x0, x1);
+              float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+              if (masked) {
+                if (__uint_as_float(sv[16 * p + 2 * e]) == -INFINITY) p0 = 0.0f;
+                if (__uint_as_float(sv[16 * p + 2 * e + 1]) == -INFINITY) p1 = 0.0f;
+              }
+              pk[8 * h + e] = cvt_f16x2(p0, p1);
+              sum = add2(sum, pack2(p0, p1));
+            }
+            float s0, s1;
+            unpack2(sum, s0, s1);
+            l = fmaf(s0 + s1, kv_exp2i(-be), l);
+          }
+          tmem_st_32x32b_x16(lane_addr + 16 * c, pk);
+          if (c == KP_BK / 64 - 1 || c == KP_BK / 32 - 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_p_full + 16 * t + (c == KP_BK / 32 - 1 ? 8 : 0));
+          }
+        }
+      }
+      bt += sg.count;
+      if (!ok) break;
+      if (works) {
+        if (!mbar_wait(bar_o_done + 8 * t, own_seg & 1, abort)) {
+          if (lane == 0) kp_timeout(abort, 0x5d);
+          break;
+        }
+        ++own_seg;
+        tc_fence_after();
+        // to true units: 2^(ev - 127), and the 2^KP_P_EXP out of P
+        const float unit = kv_scale_value(static_cast<uint32_t>(ev));
+        const float inv = (l == 0.0f ? 0.0f : 1.0f / l) * (1.0f / (1 << KP_P_EXP));
+        float* part = sg.slot >= 0 ? a.ws + static_cast<long long>(sg.slot) * (KP_ROWS * (D + 2)) : nullptr;
+        const long long out = (sg.q0 + token) * a.o_ts + qh * a.o_hs;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(lane_addr + 128 + 32 * c, o);
+          tmem_wait_ld();
+          if (!live) continue;
+          const float f = part ? 1.0f / (1 << KP_P_EXP) : inv;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 v = make_float4(__uint_as_float(o[4 * e]) * f * unit,
+                                         __uint_as_float(o[4 * e + 1]) * f * unit,
+                                         __uint_as_float(o[4 * e + 2]) * f * unit,
+                                         __uint_as_float(o[4 * e + 3]) * f * unit);
+            if (part)
+              *reinterpret_cast<float4*>(part + urow * D + 32 * c + 4 * e) = v;
+            else
+              kv_store4(a.O, a.o_dtype, out + 32 * c + 4 * e, v);
+          }
+        }
+        if (part && live) {
+          part[KP_ROWS * D + urow] = m;
+          part[KP_ROWS * (D + 1) + urow] = l;
+        }
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_seg_empty + 8 * ss);
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_cg<1>(tmem_base, KP_TMEM_COLS);
+  }
+}
+
+// Join the parts of the unit that begins in CTA blockIdx.x's stretch, in CTA
+// order (the merge of kvattn.cu): a thread per (row, four columns).
+constexpr int KPJ_THREADS = 256;
+template <int D>
+__global__ void __launch_bounds__(KPJ_THREADS)
+kv_prompt_join_kernel(const KpArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const KpJoin* join = a.joins + blockIdx.x;
+  const int live = __ldcg(&join->live);
+  const int at = blockIdx.y * KPJ_THREADS + threadIdx.x;
+  const int urow = at / (D / 4), col = 4 * (at % (D / 4));
+  if (urow >= live) return;
+  constexpr long long PART = KP_ROWS * (D + 2);
+  const int n = __ldcg(&join->parts);
+  const float* first = a.ws + __ldcg(&join->first_slot) * PART;
+  const float* rest = a.ws + 2ll * blockIdx.x * PART;
+  auto part = [&](int p) { return p == 0 ? first : rest + 2 * p * PART; };
+  float top = -INFINITY;
+#pragma unroll 4
+  for (int p = 0; p < n; ++p) top = fmaxf(top, __ldcg(part(p) + KP_ROWS * D + urow));
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float sum = 0.0f;
+#pragma unroll 4
+  for (int p = 0; p < n; ++p) {
+    const float mp = __ldcg(part(p) + KP_ROWS * D + urow);
+    const float lp = __ldcg(part(p) + KP_ROWS * (D + 1) + urow);
+    const float4 v = ld_global_cg_f4(part(p) + static_cast<long long>(urow) * D + col);
+    const float w = mp == top ? 1.0f : ex2_approx(mp - top);
+    sum = fmaf(w, lp, sum);
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int row = __ldcg(&join->row0) + urow;
+  const int token = row / a.v.group;
+  const long long out = (__ldcg(&join->q0) + token) * a.o_ts +
+                        (__ldcg(&join->head) * a.v.group + row - token * a.v.group) * a.o_hs + col;
+  kv_store4(a.O, a.o_dtype, out, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+}
+
+template <int FMT, int D>
+cudaError_t kp_run(const CUtensorMap& tk, const CUtensorMap& tv, const KpArgs& a, int sms,
+                   cudaStream_t st) {
+  auto kern = kv_prompt_kernel<FMT, D>;
+  using L = KpSmem<D>;
+  static std::atomic<bool> attr_set[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !attr_set[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
+    if (e != cudaSuccess) return e;
+    // setmaxnreg.inc waits for registers that the launch must have allocated
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs * KP_THREADS < KP_REGS_LOW * 128 + KP_REGS_HIGH * 256)
+      return cudaErrorInvalidConfiguration;
+    if (dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
+  }
+  kern<<<sms, KP_THREADS, L::ALLOC, st>>>(tk, tv, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.ws == nullptr) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sms, KP_ROWS * (D / 4) / KPJ_THREADS);
+  cfg.blockDim = dim3(KPJ_THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_prompt_join_kernel<D>, a);
+}
+
+}  // namespace
+
+int64_t kv_prompt_max_requests() { return KP_MAX_REQUESTS; }
+
+size_t kv_prompt_workspace_bytes(int64_t d, int sms) {
+  return static_cast<size_t>(sms) * (2 * KP_ROWS * (d + 2) * 4 + sizeof(KpJoin));
+}
+
+cudaError_t launch_kv_prompt(const KvAttn& q, int sms, cudaStream_t st) {
+  const KvCache& c = q.cache;
+  KpArgs a{};
+  a.v = kv_view(q);
+  a.Q = static_cast<const uint16_t*>(q.Q);
+  a.O = q.O;
+  a.q_ts = q.q_ts;
+  a.q_hs = q.q_hs;
+  a.o_ts = q.o_ts;
+  a.o_hs = q.o_hs;
+  a.bf16 = q.dtype == DT_BF16;
+  a.o_dtype = q.o_dtype;
+  a.scale_log2e = q.scale * 1.4426950408889634f;
+  if (q.ws && q.ws_bytes >= kv_prompt_workspace_bytes(c.d, sms)) {
+    a.ws = static_cast<float*>(q.ws);
+    a.joins = reinterpret_cast<KpJoin*>(static_cast<char*>(q.ws) +
+                                        static_cast<int64_t>(sms) * 2 * KP_ROWS * (c.d + 2) * 4);
+  }
+  CUtensorMap tk, tv;
+  if (!kv_tensor_map(&tk, c.k, c) || !kv_tensor_map(&tv, c.v, c)) return cudaErrorInvalidValue;
+  const bool d64 = c.d == 64;
+  switch (c.fmt) {
+    case FMT_E4M3:
+      return d64 ? kp_run<FMT_E4M3, 64>(tk, tv, a, sms, st) : kp_run<FMT_E4M3, 128>(tk, tv, a, sms, st);
+    case FMT_E5M2:
+      return d64 ? kp_run<FMT_E5M2, 64>(tk, tv, a, sms, st) : kp_run<FMT_E5M2, 128>(tk, tv, a, sms, st);
+    default:
+      return d64 ? kp_run<FMT_INT8, 64>(tk, tv, a, sms, st) : kp_run<FMT_INT8, 128>(tk, tv, a, sms, st);
+  }
+}
+
+unsigned fetch_and_clear_status_kvp(cudaError_t* err) {
+  unsigned v = 0, z = 0;
+  *err = cudaMemcpyFromSymbol(&v, g_status_kvp, sizeof(v));
+  if (*err == cudaSuccess) *err = cudaMemcpyToSymbol(g_status_kvp, &z, sizeof(z));
+  return v;
+}
+
+}  // namespace mxk

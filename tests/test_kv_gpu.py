@@ -469,6 +469,61 @@ def test_attention_without_rows():
     assert (out == 5).all()
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d,page", [(64, 16), (64, 128), (128, 16), (128, 32), (128, 64), (128, 128)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_attention_chunks(fmt, d, page, dtype):
+    """Chunks of prompts behind what is cached, whole and ragged row tiles
+    and key blocks, units of one tile and of two."""
+    s = Setup(fmt, page, 2, d, [300, 129, 64, 1, 520], [140, 33, 64, 1, 130], dtype=dtype, group=3)
+    for ws in (True, False):
+        s.check(ws=ws)
+    s.check(causal=False, out_dtype=F32)
+
+
+def test_attention_chunks_alone_and_many():
+    """One unit over all SMs; more units than SMs; units that alternate
+    between one tile and two in the same CTA."""
+    s = Setup(mx.E4M3, 64, 1, 128, [9000], [40], group=1)
+    a = s.check()
+    assert torch.equal(a, s.run())
+    s = Setup(mx.INT8, 16, 2, 64, [90 + i for i in range(90)], [60 + (37 * i) % 90 for i in range(90)], group=2)
+    s.check()
+    s.check(ws=False)
+
+
+def test_attention_chunks_of_special_values():
+    """Pages of very different size, growing scores, a negative scale, extreme
+    queries, a NaN page and one that is not in the cache, in the kernel for
+    many rows."""
+    s = Setup(mx.E4M3, 16, 2, 64, [300, 177], [90, 60], spread=14.0, group=2)
+    s.check(out_dtype=F32)
+    s.check(scale=-0.3, out_dtype=F32)
+    s.check(scale=-0.3, causal=False, window=70, out_dtype=F32)
+    t = Setup(mx.E4M3, 16, 1, 64, [800], [50], group=4)
+    order = torch.arange(800, device="cuda").float()
+    K = (torch.ones(800, 1, 64, device="cuda") * (order / 40)[:, None, None]).bfloat16()
+    slots = torch.tensor([int(t.table[0, j // 16]) * 16 + j % 16 for j in range(800)], device="cuda")
+    mx.mx_kv_append(t.cache, K, _tokens(800, 1, 64, BF, 9), slots)
+    t.q = torch.ones_like(t.q)
+    t.q[7] = 0
+    t.check(out_dtype=F32)
+    t.q[3] *= 1e30
+    t.q[4] *= 1e-30
+    t.check(scale=1e-31)
+    u = Setup(mx.E4M3, 16, 2, 64, [300, 100, 150], [40, 60, 33], group=2)
+    clean = u.run()
+    u.cache.v_scales[int(u.table[0, 17]), 1] = 255        # positions 272 ..: rows 12 .. of 40
+    u.table[1, 1] = -1
+    r = u.run()
+    assert torch.equal(r[:12], clean[:12]) and torch.equal(r[:40, :2], clean[:40, :2])
+    assert r[12:40, 2:].isnan().all() and r[40:100].isnan().all() and torch.equal(r[100:], clean[100:])
+    w = Setup(mx.E5M2, 16, 1, 128, [600], [40], seed=4)
+    want = w.run(window=60)
+    w.table[0, :30] = -1                                  # nobody sees before position 500
+    assert torch.equal(w.run(window=60), want)
+
+
 def test_attention_many_requests():
     """More requests than a CTA has threads, most with one token."""
     rng = np.random.default_rng(0)
@@ -476,6 +531,16 @@ def test_attention_many_requests():
     s = Setup(mx.INT8, 16, 1, 64, lens, [int(x) for x in rng.integers(0, 3, 700)], group=2)
     s.check()
     s.check(ws=False)
+    e = s.exact()                                # and by the kernel for many rows
+    assert (np.abs(_np(s.run(max_q=100).double()) - e[0]) <= _kv.bound(*e, BF)).all()
+
+
+def test_attention_max_q_only_picks_the_kernel():
+    s = Setup(mx.E4M3, 32, 2, 128, [0, 1, 77, 300, 500], [3, 1, 70, 1, 20], group=4)
+    e = s.exact()
+    for most in (1, 2, 70, 5000):
+        got = _np(s.run(max_q=most).double())
+        assert (np.abs(got - e[0]) <= _kv.bound(*e, BF)).all()
 
 
 def test_attention_far_offsets():
