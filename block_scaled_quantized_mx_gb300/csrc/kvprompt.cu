@@ -49,8 +49,8 @@ constexpr int KP_BK = 128;                 // keys per block
 constexpr int KP_THREADS = 384;            // warpgroup 0, two softmax warpgroups
 constexpr int KP_WARPS = KP_THREADS / 32;
 constexpr int KP_CONV = 96;                // converting threads: warps 0, 2, 3
-// Registers: launched at 168; 96 * 128 + 200 * 256 = 63488 <= 384 * 168.
-constexpr int KP_REGS_LOW = 96;
+// Registers: launched at 168; 104 * 128 + 200 * 256 = 64512 = 384 * 168.
+constexpr int KP_REGS_LOW = 104;
 constexpr int KP_REGS_HIGH = 200;
 constexpr int KP_TMEM_COLS = 512;
 constexpr float KP_LAZY = 8.0f;            // slack of the exponentials' reference point
@@ -59,10 +59,15 @@ constexpr int KP_OVER = 4;                 // entries of a unit besides its bloc
 constexpr int KP_PG = 8;                   // blocks whose page data is kept
 constexpr int KP_MAX_REQUESTS = 16384;
 
-// One block's pages: per 16 keys at most one page.
+// One block's scales, for each 16 of its keys.
 struct KpPages {
-  float kf[8];                             // K's scale (NaN: none or a NaN page)
-  int ve[8];                               // V's scale code, 0xFF NaN, -1 not loaded
+  struct {
+    float kf;                              // K's scale; NaN where K's or V's is NaN or no page is
+    int ve;                                // V's scale code; 0 there
+  } of[8];
+  int top;                                 // the largest ve
+  int gone;                                // a bit for each 16 keys whose page was not loaded
+  int pad[2];
 };
 
 // One CTA's part of a unit, as every role sees it.
@@ -160,7 +165,7 @@ struct KpSmem {
   static constexpr int REGION = 128 * 128;
   static constexpr int Q_BYTES = (D / 64) * REGION;
   static constexpr int K_BYTES = (D / 64) * REGION;
-  static constexpr int V_BYTES = 2 * (D / 64) * 8192;
+  static constexpr int V_BYTES = (D / 64) * REGION;
   static constexpr int RAW_BYTES = KP_BK * D;
   static constexpr int Q_OFF = 0;
   static constexpr int K_OFF = Q_OFF + 2 * Q_BYTES;
@@ -421,10 +426,34 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(KP_REGS_LOW));
     if (warp != 1) {
       // ---------------------------------------------------- loads, conversion
-      const int c0 = (warp == 0 ? 0 : warp - 1) * 32 + lane;      // 0 .. 95
-      constexpr int CPR = D / 16;                                 // 16-code chunks per row
-      constexpr int CHUNKS = KP_BK * CPR;
-      constexpr int IT = (CHUNKS + KP_CONV - 1) / KP_CONV;
+      // A step is 512 bytes of codes (4 rows of 128 or 8 of 64), 16 codes a
+      // lane; converting warp ci takes steps ci, ci + 3, ..  The lanes' places in
+      // a step keep both the reads of the swizzled codes and the writes of the
+      // swizzled f16 rows free of bank conflicts: eight consecutive lanes take
+      // the four lower chunks of one row and the four upper ones of the next.
+      const int ci = warp == 0 ? 0 : warp - 1;
+      constexpr int SROWS = 512 / D;                             // rows of a step
+      constexpr int STEPS = KP_BK / SROWS;
+      constexpr int IT = (STEPS + 2) / 3;
+      int rl, c;                                                 // row in the step, chunk
+      if constexpr (D == 128) {
+        rl = 2 * (lane >> 4) + (((lane >> 2) ^ (lane >> 3)) & 1);
+        c = (lane & 3) + (lane & 4);
+      } else {
+        rl = lane >> 2;
+        c = lane & 3;
+      }
+      // offsets of the first two of the warp's steps in the codes and in the
+      // f16 tile (whose rows are 128 bytes in regions of 64 values); a step's
+      // rows start at 0 or 4 mod 8, alternately (D 128), which is what the
+      // swizzles depend on.  Later steps lie 6 steps further each.
+      uint32_t from[2], to[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int step = ci + 3 * e, r = step * SROWS + rl;
+        from[e] = r * D + ((D == 128 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3))) << 4);
+        to[e] = (c >> 2) * L::REGION + r * 128 + (((2 * (c & 3)) ^ (r & 7)) << 4);
+      }
       const int shift = a.v.page_shift;
       bool ok = true;
       // -- warp 0's cursor of loads, one block ahead of the conversion
@@ -434,7 +463,19 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       int len_ahead = 0, head_ahead = 0;
       const int* row = nullptr;
       bool more = true, first_seg = true;
-      // the next block's K (kv 0) or V (kv 1); publishes a segment as it enters it
+      int next_id = -1;                      // the page of the block after this one
+      float kf = 0.0f;
+      int ve = 0;
+      auto page_of = [&](int block) {
+        const int key0 = block * KP_BK;
+        int p = -1;
+        if (lane < (KP_BK >> shift) && key0 + (lane << shift) < len_ahead)
+          p = row[(key0 >> shift) + lane];
+        return p;
+      };
+      // Loads the next block's K (kv 0) or V (kv 1); publishes a segment as it
+      // enters it.  The page ids are read a block ahead, and the scales that
+      // the K call asks for are used in the V call, so that neither waits.
       auto issue = [&](int kv) {
         if (!more || !ok) return;
         if (kv == 0) {
@@ -445,7 +486,6 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
               ok = false;
               return;
             }
-            ++seg_out;
             int found = 0;
             if (lane == 0) {
               if (a.ws != nullptr) {
@@ -479,6 +519,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
               }
               mbar_arrive(bar_seg + 8 * ss);
             }
+            ++seg_out;
             __syncwarp();
             more = __shfl_sync(0xFFFFFFFFu, found, 0) != 0;
             first_seg = false;
@@ -488,14 +529,11 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             row = a.v.table + static_cast<long long>(walk->b) * a.v.table_stride;
             len_ahead = walk->r.len;
             head_ahead = walk->head;
+            __syncwarp();                    // all lanes have read the walk
+            next_id = page_of(at_block);
           }
-          // the block's pages, one per lane
-          const int key0 = at_block * KP_BK;
-          id = -1;
-          if (lane < (KP_BK >> shift) && key0 + (lane << shift) < len_ahead) {
-            id = row[(key0 >> shift) + lane];
-            if (id >= a.v.pages) id = -1;
-          }
+          id = next_id < a.v.pages ? next_id : -1;
+          next_id = left > 1 ? page_of(at_block + 1) : -1;
         }
         if (!mbar_wait(bar_raw_empty + 8 * kv, (ahead & 1) ^ 1, abort)) {
           if (lane == 0) kp_timeout(abort, 0x52);
@@ -508,28 +546,40 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         if (lane == 0)
           mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(have)) * (D << shift));
         __syncwarp();
-        if (id >= 0) {
-          const int y = static_cast<int>((static_cast<long long>(id) * a.v.heads + head_ahead) << shift);
+        const long long unit = static_cast<long long>(id) * a.v.heads + head_ahead;
+        if (id >= 0)
           tma_load_2d(base + L::RAW_OFF + kv * L::RAW_BYTES + lane * (D << shift),
-                      kv ? &tmV : &tmK, full, 0, y);
-        }
+                      kv ? &tmV : &tmK, full, 0, static_cast<int>(unit << shift));
         if (kv == 0) {
+          kf = __uint_as_float(0x7FC00000u);
+          ve = 0xFF;
+          if (id >= 0) {
+            kf = kv_scale_value(a.v.k_scales[unit]);
+            ve = a.v.v_scales[unit];
+          }
+        } else {
           const int ps = ahead & (KP_PG - 1);
           KpPages* pg = reinterpret_cast<KpPages*>(gbase + L::PG_OFF) + ps;
-          if (lane < (KP_BK >> shift)) {
-            float kf = __uint_as_float(0x7FC00000u);
-            int ve = -1;
-            if (id >= 0) {
-              const long long unit = static_cast<long long>(id) * a.v.heads + head_ahead;
-              kf = kv_scale_value(a.v.k_scales[unit]);
-              ve = a.v.v_scales[unit];
-            }
-            pg->kf[lane] = kf;
-            pg->ve[lane] = ve;
+          if (ve == 0xFF) {
+            kf = __uint_as_float(0x7FC00000u);
+            ve = 0;
+          }
+          // lane i < 8 writes for keys 16 i ..: the page of lane 16 i >> shift
+          const int of = (16 * (lane & 7)) >> shift;
+          const float f = __shfl_sync(0xFFFFFFFFu, kf, of);
+          const int e = __shfl_sync(0xFFFFFFFFu, ve, of);
+          const int top = __reduce_max_sync(0xFFFFFFFFu, lane < 8 ? e : 0);
+          const unsigned gone = __ballot_sync(0xFFFFFFFFu, lane < 8 && !((have >> of) & 1));
+          if (lane < 8) {
+            pg->of[lane].kf = f;
+            pg->of[lane].ve = e;
+          }
+          if (lane == 0) {
+            pg->top = top;
+            pg->gone = static_cast<int>(gone);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_pg + 8 * ps);
-        } else {
           ++ahead;
           ++at_block;
           --left;
@@ -554,8 +604,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           const KpPages* pg = reinterpret_cast<const KpPages*>(gbase + L::PG_OFF) + (bt & (KP_PG - 1));
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
-            if (!mbar_wait(bar_raw + 8 * kv, bt & 1, abort) ||
-                !mbar_wait(bar_pg + 8 * (bt & (KP_PG - 1)), (bt / KP_PG) & 1, abort)) {
+            if (!mbar_wait(bar_raw + 8 * kv, bt & 1, abort)) {
               if (lane == 0) kp_timeout(abort, 0x54);
               ok = false;
               break;
@@ -563,30 +612,25 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             uint4 w[IT];
             const uint32_t src = base + L::RAW_OFF + kv * L::RAW_BYTES;
 #pragma unroll
-            for (int i = 0; i < IT; ++i) {
-              const int ch = i * KP_CONV + c0, r = ch / CPR, c = ch % CPR;
-              if (ch < CHUNKS) {
-                const int sw = D == 128 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3));
-                w[i] = ld_shared_v4(src + r * D + sw * 16);
-              }
-            }
+            for (int i = 0; i < IT; ++i)
+              if (i < IT - 1 || ci + 3 * i < STEPS)
+                w[i] = ld_shared_v4(src + from[i & 1] + (i >> 1) * 3072);
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_raw_empty + 8 * kv);
-            if (kv == 1 && key0 + KP_BK > len) {
-              // keys behind the request's end: zeros, whatever the page holds
-#pragma unroll
-              for (int i = 0; i < IT; ++i)
-                if (key0 + (i * KP_CONV + c0) / CPR >= len) w[i] = make_uint4(0, 0, 0, 0);
-            }
             if (kv == 1) {
-              // and those of pages that were not loaded
-              bool gone = false;
-              for (int p = 0; p < (KP_BK >> shift); ++p) gone |= pg->ve[p] < 0;
-              if (gone) {
+              if (!mbar_wait(bar_pg + 8 * (bt & (KP_PG - 1)), (bt / KP_PG) & 1, abort)) {
+                if (lane == 0) kp_timeout(abort, 0x54);
+                ok = false;
+                break;
+              }
+              // keys behind the request's end or in pages that were not
+              // loaded: zeros, whatever stands there
+              const unsigned gone = static_cast<unsigned>(pg->gone);
+              if (gone || key0 + KP_BK > len) {
 #pragma unroll
                 for (int i = 0; i < IT; ++i) {
-                  const int r = (i * KP_CONV + c0) / CPR;
-                  if (r < KP_BK && pg->ve[r >> shift] < 0) w[i] = make_uint4(0, 0, 0, 0);
+                  const int r = (ci + 3 * i) * SROWS + rl;
+                  if (key0 + r >= len || ((gone >> ((r >> 4) & 7)) & 1)) w[i] = make_uint4(0, 0, 0, 0);
                 }
               }
             }
@@ -600,29 +644,16 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             const uint32_t dst = base + (kv ? L::V_OFF + st * L::V_BYTES : L::K_OFF + st * L::K_BYTES);
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
-              const int ch = i * KP_CONV + c0, r = ch / CPR, c = ch % CPR;
-              if (ch < CHUNKS) {
-                // 16 codes: two 16-byte chunks of the f16 row, in 64-value
-                // regions (K: 128 keys; V: 64 keys) of 128-byte rows
+              if (i < IT - 1 || ci + 3 * i < STEPS) {
+                // 16 codes: two neighbouring 16-byte chunks of the f16 row
                 uint32_t f[8];
                 kv_f16_pairs<FMT>(w[i].x, f[0], f[1]);
                 kv_f16_pairs<FMT>(w[i].y, f[2], f[3]);
                 kv_f16_pairs<FMT>(w[i].z, f[4], f[5]);
                 kv_f16_pairs<FMT>(w[i].w, f[6], f[7]);
-                const int q = 2 * (c & 3);
-                const uint32_t row =
-                    kv ? dst + (r >> 6) * (D / 64) * 8192 + (c >> 2) * 8192 + (r & 63) * 128
-                       : dst + (c >> 2) * L::REGION + r * 128;
-                const uint32_t a0 = row + ((q ^ (r & 7)) << 4), a1 = row + (((q + 1) ^ (r & 7)) << 4);
-                // the upper half of a row goes odd chunk first: the eight
-                // lanes of a row then hit eight different bank groups
-                if (c & 4) {
-                  st_shared_v4(a1, f[4], f[5], f[6], f[7]);
-                  st_shared_v4(a0, f[0], f[1], f[2], f[3]);
-                } else {
-                  st_shared_v4(a0, f[0], f[1], f[2], f[3]);
-                  st_shared_v4(a1, f[4], f[5], f[6], f[7]);
-                }
+                const uint32_t at = dst + to[i & 1] + (i >> 1) * (6 * SROWS * 128);
+                st_shared_v4(at, f[0], f[1], f[2], f[3]);
+                st_shared_v4(at ^ 16, f[4], f[5], f[6], f[7]);
               }
             }
             fence_proxy_async_smem();
@@ -650,7 +681,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       const uint32_t id_pv = kp_idesc(D, 1);
       const uint64_t dq0 = smem_desc(base + L::Q_OFF, 16, 1024, 2);
       const uint64_t dk0 = smem_desc(base + L::K_OFF, 16, 1024, 2);
-      const uint64_t dv0 = smem_desc(base + L::V_OFF, 8192, 1024, 2);
+      const uint64_t dv0 = smem_desc(base + L::V_OFF, L::REGION, 1024, 2);
       int bt = 0, bt1 = 0, seg_it = 0, seg1 = 0;
       bool ok = true;
       while (ok) {
@@ -696,9 +727,8 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                   }
                   tc_fence_after();
                 }
-                const uint32_t boff = (kk >> 2) * (D / 64) * 8192 + (kk & 3) * 2048;
                 kp_mma_ts(o_t, s_t + 8 * kk,
-                          dv0 + static_cast<uint64_t>((st * L::V_BYTES + boff) >> 4), id_pv,
+                          dv0 + static_cast<uint64_t>((st * L::V_BYTES + kk * 2048) >> 4), id_pv,
                           (j > 1 || kk > 0) ? 1u : 0u);
               }
               if (!ok) break;
@@ -788,10 +818,14 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             top = max(top, max((w[e] << 16) & 0x7FFFFFFFu, w[e] & 0x7FFF0000u));
           float down;
           kv_row_factors(top, down, up);
+          if (a.scale_log2e < 0.0f) down = -down;
 #pragma unroll
           for (int e = 0; e < D / 2; ++e)
             w[e] = cvt_f16x2(__uint_as_float(w[e] << 16) * down,
                              __uint_as_float(w[e] & 0xFFFF0000u) * down);
+        } else if (a.scale_log2e < 0.0f) {
+#pragma unroll
+          for (int e = 0; e < D / 2; ++e) w[e] ^= 0x80008000u;
         }
         const int r = 32 * quarter + lane;
 #pragma unroll
@@ -803,7 +837,8 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_q + 8 * t);
       }
-      const float fr = a.scale_log2e * up;
+      // a negative scale has gone into Q: the factor of a score is never negative
+      const float fr = fabsf(a.scale_log2e) * up;
       // keys that every live row of this warp sees
       const int all_lo = __reduce_max_sync(0xFFFFFFFFu, live ? lo : 0);
       const int all_hi = __reduce_min_sync(0xFFFFFFFFu, live ? hi : 0x7FFFFFFF);
@@ -824,37 +859,27 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
         for (int c = 0; c < KP_BK / 32; ++c)
           tmem_ld_32x32b_x32(lane_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
-        int ev_new = ev;
-#pragma unroll
-        for (int p = 0; p < 8; ++p) {
-          const int e = pg->ve[(16 * p) >> shift];
-          if (static_cast<unsigned>(e) < 0xFFu) ev_new = max(ev_new, e);
-        }
+        const int ev_new = max(ev, pg->top);
         tmem_wait_ld();
-        // row maximum: of the raw scores of each 16 keys, times their factor
-        // (for a negative one, the minimum); a block that some row does not
-        // see whole is scaled and masked first
+        // row maximum: of the raw scores of each 16 keys, times their factor; a
+        // block that some row does not see whole is scaled and masked first
         const bool masked = key0 < all_lo || key0 + KP_BK > all_hi;
         float mx = -INFINITY;
+        if (!masked) {
 #pragma unroll
-        for (int p = 0; p < 8; ++p) {
-          const float f = fr * pg->kf[(16 * p) >> shift];
-          float g0 = -INFINITY, g1 = -INFINITY;
-          if (!masked) {
-            if (fr >= 0.0f) {
+          for (int p = 0; p < 8; ++p) {
+            float g0 = -INFINITY, g1 = -INFINITY;
 #pragma unroll
-              for (int e = 0; e < 16; e += 4) {
-                g0 = max3(g0, __uint_as_float(sv[16 * p + e]), __uint_as_float(sv[16 * p + e + 1]));
-                g1 = max3(g1, __uint_as_float(sv[16 * p + e + 2]), __uint_as_float(sv[16 * p + e + 3]));
-              }
-              g0 = fmaxf(g0, g1);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) g0 = fmaxf(g0, -__uint_as_float(sv[16 * p + e]));
-              g0 = -g0;
+            for (int e = 0; e < 16; e += 4) {
+              g0 = max3(g0, __uint_as_float(sv[16 * p + e]), __uint_as_float(sv[16 * p + e + 1]));
+              g1 = max3(g1, __uint_as_float(sv[16 * p + e + 2]), __uint_as_float(sv[16 * p + e + 3]));
             }
-            mx = fmaxf(mx, g0 * f);
-          } else {
+            mx = fmaxf(mx, fmaxf(g0, g1) * (fr * pg->of[p].kf));
+          }
+        } else {
+#pragma unroll
+          for (int p = 0; p < 8; ++p) {
+            const float f = fr * pg->of[p].kf;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const int k = key0 + 16 * p + e;
@@ -882,7 +907,8 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         l *= alpha;
         m = m_new;
         // p' = 2^(x - m + b), b = 7 + (V's exponent - the reference), rounded
-        // to f16 and written back over the scores; the sum takes b out again
+        // to f16 and written back over the scores; the sum takes b out again.
+        // Masked scores are -inf and stay it: b and m_use are finite.
         const float m_use = m == -INFINITY ? 0.0f : m;
 #pragma unroll
         for (int c = 0; c < KP_BK / 32; ++c) {
@@ -890,12 +916,10 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int p = 2 * c + h;
-            const int e8 = pg->ve[(16 * p) >> shift];
-            const bool nan = static_cast<unsigned>(e8) >= 0xFFu;
-            const int be = max(-60, KP_P_EXP + e8 - ev);
-            const float b = nan ? __uint_as_float(0x7FC00000u) : static_cast<float>(be);
-            const float f = masked ? 1.0f : fr * pg->kf[(16 * p) >> shift];
-            const float nm = b - m_use;
+            const int b = max(-60, pg->of[p].ve + (KP_P_EXP - ev));
+            const float f = masked ? 1.0f : fr * pg->of[p].kf;
+            // b as a float: 1.5 * 2^23 + b, less 1.5 * 2^23
+            const float nm = (__int_as_float(0x4B400000 + b) - 12582912.0f) - m_use;
             const uint64_t f2 = pack2(f, f), nm2 = pack2(nm, nm);
             uint64_t sum = pack2(0.0f, 0.0f);
 #pragma unroll
@@ -905,17 +929,13 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                                  __uint_as_float(sv[16 * p + 2 * e + 1])),
                            f2, nm2),
                       x0, x1);
-              float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-              if (masked) {
-                if (__uint_as_float(sv[16 * p + 2 * e]) == -INFINITY) p0 = 0.0f;
-                if (__uint_as_float(sv[16 * p + 2 * e + 1]) == -INFINITY) p1 = 0.0f;
-              }
+              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
               pk[8 * h + e] = cvt_f16x2(p0, p1);
               sum = add2(sum, pack2(p0, p1));
             }
             float s0, s1;
             unpack2(sum, s0, s1);
-            l = fmaf(s0 + s1, kv_exp2i(-be), l);
+            l = fmaf(s0 + s1, __int_as_float((127 - b) << 23), l);
           }
           tmem_st_32x32b_x16(lane_addr + 16 * c, pk);
           if (c == KP_BK / 64 - 1 || c == KP_BK / 32 - 1) {
