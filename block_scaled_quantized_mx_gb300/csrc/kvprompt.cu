@@ -7,13 +7,15 @@
 // r / group, head r % group of the group, so that all heads of a group share
 // the converted keys), in two tiles of 128 that take turns on the tensor core
 // as in attention.cu.  What differs from dense attention:
-//   * K and V come as codes.  Warp 0 reads the block table and loads blocks of
-//     128 keys page by page with TMA into one slot for K and one for V; warps
-//     0, 2 and 3 take a slot's codes into registers (which frees the slot for
-//     the next block at once), turn them into f16 -- exactly, for all three
-//     formats -- and write the swizzled operand tiles, two deep each.  The
-//     conversion of a block serves both tiles and, through the rows' order,
-//     all heads of the group;
+//   * K and V come as codes.  Warp 0 reads the block table and the scales,
+//     some blocks of 128 keys ahead; four warps read the codes from global
+//     memory straight into registers (a tile ahead: a converted chunk's
+//     registers take the next tile's codes at once), turn them into f16 --
+//     exactly, for all three formats -- and write the swizzled operand tiles,
+//     two deep each.  The conversion of a block serves both tiles and, through
+//     the rows' order, all heads of the group.  (Codes staged in shared memory
+//     by TMA cost its port 64 KB more a block, which the operands of the
+//     products already load by 192 KB, and a load's latency per tile.);
 //   * page scales stay out of the operands: K's is a factor of the scores of
 //     its 16 .. 128 keys, applied with the softmax scale in the exponent's FMA;
 //     V's, a power of two relative to the largest so far, is added to the
@@ -26,8 +28,6 @@
 //     one; parts of units go to the workspace and a second kernel joins them.
 // Tensor memory as in attention.cu: S (then P) of tile t in columns [256 t,
 // 256 t + 128), its O behind.  Every mbarrier wait is bounded.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <atomic>
 
@@ -46,12 +46,12 @@ __device__ unsigned int g_status_kvp = 0;
 constexpr int KP_BQ = 128;                 // rows per tile
 constexpr int KP_ROWS = 2 * KP_BQ;         // rows of a unit
 constexpr int KP_BK = 128;                 // keys per block
-constexpr int KP_THREADS = 384;            // warpgroup 0, two softmax warpgroups
+constexpr int KP_THREADS = 512;            // pages and MMA, two softmax warpgroups, conversion
 constexpr int KP_WARPS = KP_THREADS / 32;
-constexpr int KP_CONV = 96;                // converting threads: warps 0, 2, 3
-// Registers: launched at 168; 104 * 128 + 200 * 256 = 64512 = 384 * 168.
-constexpr int KP_REGS_LOW = 104;
-constexpr int KP_REGS_HIGH = 200;
+// Registers: launched at 128; 72 * 128 + 176 * 256 + 88 * 128 = 65536.
+constexpr int KP_REGS_LOW = 72;            // warpgroup 0
+constexpr int KP_REGS_SOFT = 176;          // warpgroups 1 and 2
+constexpr int KP_REGS_CONV = 88;           // warpgroup 3
 constexpr int KP_TMEM_COLS = 512;
 constexpr float KP_LAZY = 8.0f;            // slack of the exponentials' reference point
 constexpr int KP_P_EXP = 7;                // P is scaled by 2^7: at most 2^(7 + 8) in f16
@@ -59,15 +59,17 @@ constexpr int KP_OVER = 4;                 // entries of a unit besides its bloc
 constexpr int KP_PG = 8;                   // blocks whose page data is kept
 constexpr int KP_MAX_REQUESTS = 16384;
 
-// One block's scales, for each 16 of its keys.
+// One block: for each 16 of its keys the scales and where the codes are.
 struct KpPages {
   struct {
     float kf;                              // K's scale; NaN where K's or V's is NaN or no page is
     int ve;                                // V's scale code; 0 there
   } of[8];
-  int top;                                 // the largest ve
-  int gone;                                // a bit for each 16 keys whose page was not loaded
-  int pad[2];
+  long long at[8];                         // the 16 keys' first code in both planes, -1: no page
+  int top;                                 // the largest ve; -1: no block at all
+  int valid;                               // keys of the block in front of the request's end
+  int more;                                // another block follows
+  int pad;
 };
 
 // One CTA's part of a unit, as every role sees it.
@@ -164,37 +166,37 @@ template <int D>
 struct KpSmem {
   static constexpr int REGION = 128 * 128;
   static constexpr int Q_BYTES = (D / 64) * REGION;
-  static constexpr int K_BYTES = (D / 64) * REGION;
-  static constexpr int V_BYTES = (D / 64) * REGION;
-  static constexpr int RAW_BYTES = KP_BK * D;
+  static constexpr int K_BYTES = (D / 64) * REGION;       // V's tiles are alike
+  static constexpr int V_BYTES = K_BYTES;
   static constexpr int Q_OFF = 0;
   static constexpr int K_OFF = Q_OFF + 2 * Q_BYTES;
   static constexpr int V_OFF = K_OFF + 2 * K_BYTES;
-  static constexpr int RAW_OFF = V_OFF + 2 * V_BYTES;    // K's slot, V's slot
-  static constexpr int PG_OFF = RAW_OFF + 2 * RAW_BYTES;
+  static constexpr int PG_OFF = V_OFF + 2 * V_BYTES;
   static constexpr int SEG_OFF = PG_OFF + KP_PG * static_cast<int>(sizeof(KpPages));
   static constexpr int BAR_OFF = SEG_OFF + 2 * static_cast<int>(sizeof(KpSeg));
   // q_full[2], k_full[2], v_full[2], k_empty[2], v_empty[2], s_full[2],
-  // p_full[2 tiles][2 halves], o_done[2], raw_full[2], raw_empty[2],
-  // seg_full[2], seg_empty[2], pg_full[8]
-  static constexpr int BARS = 2 + 8 + 2 + 4 + 2 + 8 + KP_PG;
+  // p_full[2 tiles][2 halves], o_done[2], seg_full[2], seg_empty[2],
+  // pg_full[8], pg_empty[8]
+  static constexpr int BARS = 2 + 8 + 2 + 4 + 2 + 4 + 2 * KP_PG;
   static constexpr int MISC_OFF = BAR_OFF + BARS * 8;
   static constexpr int WALK_OFF = MISC_OFF + 16;
   static constexpr int TOTAL = WALK_OFF + static_cast<int>(sizeof(KpWalk));
   static constexpr int ALLOC = TOTAL + 1024;
   static_assert(ALLOC <= 232448, "shared memory budget");
-  static_assert(K_OFF + 2 * K_BYTES >= (KP_MAX_REQUESTS + 1) * 4 - 4, "the plan's array fits");
+  static_assert(V_OFF >= KP_MAX_REQUESTS * 4, "the plan's array fits before V");
 };
 
 struct KpArgs {
   KvView v;
   const uint16_t* Q;
+  const uint8_t* k;
+  const uint8_t* v_codes;
   void* O;
   long long q_ts, q_hs, o_ts, o_hs;
   int bf16;
   int o_dtype;
   float scale_log2e;
-  float* ws;                               // two slots per CTA: 256 x D of O, m[256], l[256]
+  float* ws;                               // two slots per CTA: O as [D / 4][256 rows][4], m[256], l[256]
   KpJoin* joins;                           // one per CTA
 };
 
@@ -283,8 +285,7 @@ __device__ __forceinline__ long long kp_scan(long long v, long long* sm, long lo
 
 template <int FMT, int D>
 __global__ void __launch_bounds__(KP_THREADS, 1)
-kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                 const KpArgs a) {
+kv_prompt_kernel(const KpArgs a) {
   using L = KpSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -298,11 +299,10 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   const uint32_t bar_s_full = bar_v_empty + 16;
   const uint32_t bar_p_full = bar_s_full + 16;     // [tile][half]
   const uint32_t bar_o_done = bar_p_full + 32;
-  const uint32_t bar_raw = bar_o_done + 16;        // [K, V]
-  const uint32_t bar_raw_empty = bar_raw + 16;
-  const uint32_t bar_seg = bar_raw_empty + 16;
+  const uint32_t bar_seg = bar_o_done + 16;
   const uint32_t bar_seg_empty = bar_seg + 16;
   const uint32_t bar_pg = bar_seg_empty + 16;      // [KP_PG]
+  const uint32_t bar_pg_empty = bar_pg + 8 * KP_PG;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::MISC_OFF);
   volatile int* abort = reinterpret_cast<volatile int*>(gbase + L::MISC_OFF + 4);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -314,7 +314,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   long long total, w0, ctas;
   {
     int* sm_rt = reinterpret_cast<int*>(gbase);                        // requests + 1
-    long long* sm_scan = reinterpret_cast<long long*>(gbase + L::RAW_OFF);
+    long long* sm_scan = reinterpret_cast<long long*>(gbase + L::PG_OFF);
     const int B = a.v.requests;
     const int per = (B + KP_THREADS - 1) / KP_THREADS;
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
@@ -388,31 +388,30 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     if (tid == 0 && join) join->live = 0;
     if (blockIdx.x >= ctas) return;          // the whole CTA: nothing was started
   }
-  // the regions go to their owners, TMA and the tensor core among them
+  // the regions go to their owners, the tensor core among them
   fence_proxy_async_smem();
   __syncthreads();
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar_q + 8 * i, 4);
-      mbar_init(bar_k + 8 * i, 3);
-      mbar_init(bar_v + 8 * i, 3);
+      mbar_init(bar_k + 8 * i, 4);
+      mbar_init(bar_v + 8 * i, 4);
       mbar_init(bar_k_empty + 8 * i, 1);
       mbar_init(bar_v_empty + 8 * i, 1);
       mbar_init(bar_s_full + 8 * i, 1);
       mbar_init(bar_p_full + 16 * i, 4);
       mbar_init(bar_p_full + 16 * i + 8, 4);
       mbar_init(bar_o_done + 8 * i, 1);
-      mbar_init(bar_raw + 8 * i, 1);
-      mbar_init(bar_raw_empty + 8 * i, 3);
       mbar_init(bar_seg + 8 * i, 1);
-      mbar_init(bar_seg_empty + 8 * i, 12);
+      mbar_init(bar_seg_empty + 8 * i, 9);
     }
-    for (int i = 0; i < KP_PG; ++i) mbar_init(bar_pg + 8 * i, 1);
+    for (int i = 0; i < KP_PG; ++i) {
+      mbar_init(bar_pg + 8 * i, 1);
+      mbar_init(bar_pg_empty + 8 * i, 12);
+    }
     *abort = 0;
     fence_mbar_init();
-    prefetch_tmap(&tmK);
-    prefetch_tmap(&tmV);
   }
   if (warp == 1) tmem_alloc_cg<1>(smem_u32(tmem_slot), KP_TMEM_COLS);
   __syncwarp();
@@ -424,258 +423,122 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(KP_REGS_LOW));
-    if (warp != 1) {
-      // ---------------------------------------------------- loads, conversion
-      // A step is 512 bytes of codes (4 rows of 128 or 8 of 64), 16 codes a
-      // lane; converting warp ci takes steps ci, ci + 3, ..  The lanes' places in
-      // a step keep both the reads of the swizzled codes and the writes of the
-      // swizzled f16 rows free of bank conflicts: eight consecutive lanes take
-      // the four lower chunks of one row and the four upper ones of the next.
-      const int ci = warp == 0 ? 0 : warp - 1;
-      constexpr int SROWS = 512 / D;                             // rows of a step
-      constexpr int STEPS = KP_BK / SROWS;
-      constexpr int IT = (STEPS + 2) / 3;
-      int rl, c;                                                 // row in the step, chunk
-      if constexpr (D == 128) {
-        rl = 2 * (lane >> 4) + (((lane >> 2) ^ (lane >> 3)) & 1);
-        c = (lane & 3) + (lane & 4);
-      } else {
-        rl = lane >> 2;
-        c = lane & 3;
-      }
-      // offsets of the first two of the warp's steps in the codes and in the
-      // f16 tile (whose rows are 128 bytes in regions of 64 values); a step's
-      // rows start at 0 or 4 mod 8, alternately (D 128), which is what the
-      // swizzles depend on.  Later steps lie 6 steps further each.
-      uint32_t from[2], to[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int step = ci + 3 * e, r = step * SROWS + rl;
-        from[e] = r * D + ((D == 128 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3))) << 4);
-        to[e] = (c >> 2) * L::REGION + r * 128 + (((2 * (c & 3)) ^ (r & 7)) << 4);
-      }
-      const int shift = a.v.page_shift;
-      bool ok = true;
-      // -- warp 0's cursor of loads, one block ahead of the conversion
-      int ahead = 0;                         // blocks whose loads were issued
-      int issued[2] = {0, 0};                // of K, of V
-      int left = 0, at_block = 0, seg_out = 0, id = -1;
-      int len_ahead = 0, head_ahead = 0;
-      const int* row = nullptr;
-      bool more = true, first_seg = true;
-      int next_id = -1;                      // the page of the block after this one
-      float kf = 0.0f;
-      int ve = 0;
-      auto page_of = [&](int block) {
-        const int key0 = block * KP_BK;
-        int p = -1;
-        if (lane < (KP_BK >> shift) && key0 + (lane << shift) < len_ahead)
-          p = row[(key0 >> shift) + lane];
-        return p;
+    if (warp == 0) {
+      // ------------------------------------------------- segments and pages
+      int bt = 0, seg_out = 0;
+      bool ok = true, first_seg = true, held = false;
+      KpPages* pages = reinterpret_cast<KpPages*>(gbase + L::PG_OFF);
+      // a block's data stay back until it is known whether another follows
+      auto release = [&](int more) {
+        if (!held) return;
+        const int ps = (bt - 1) & (KP_PG - 1);
+        if (lane == 0) {
+          pages[ps].more = more;
+          mbar_arrive(bar_pg + 8 * ps);
+        }
+        held = false;
       };
-      // Loads the next block's K (kv 0) or V (kv 1); publishes a segment as it
-      // enters it.  The page ids are read a block ahead, and the scales that
-      // the K call asks for are used in the V call, so that neither waits.
-      auto issue = [&](int kv) {
-        if (!more || !ok) return;
-        if (kv == 0) {
-          if (left == 0) {
-            const int ss = seg_out & 1;
-            if (!mbar_wait(bar_seg_empty + 8 * ss, ((seg_out >> 1) & 1) ^ 1, abort)) {
-              if (lane == 0) kp_timeout(abort, 0x51);
-              ok = false;
-              return;
-            }
-            int found = 0;
-            if (lane == 0) {
-              if (a.ws != nullptr) {
-                found = walk->next(a.v);
-              } else if (walk->w < walk->w1) {
-                const long long w1 = walk->w1;
-                walk->w1 = 0x7FFFFFFFFFFFFFFFll;
-                found = walk->next(a.v);
-                walk->w1 = w1;
-              }
-              KpSeg* s = const_cast<KpSeg*>(segs) + ss;
-              s->count = found ? walk->count : 0;
-              if (found) {
-                s->block = walk->block;
-                s->len = walk->r.len;
-                s->n = walk->r.n;
-                s->q0 = walk->r.q0;
-                s->row0 = walk->rt * KP_ROWS;
-                s->head = walk->head;
-                const int slot = 2 * static_cast<int>(blockIdx.x) + (first_seg ? 0 : 1);
-                s->slot = walk->begins && walk->ends ? -1 : slot;
-                if (walk->begins && !walk->ends) {
-                  KpJoin* j = a.joins + blockIdx.x;
-                  j->live = min(KP_ROWS, walk->r.n * a.v.group - walk->rt * KP_ROWS);
-                  j->parts = static_cast<int>((walk->unit_end * ctas - 1) / total - blockIdx.x + 1);
-                  j->first_slot = slot;
-                  j->head = walk->head;
-                  j->row0 = walk->rt * KP_ROWS;
-                  j->q0 = walk->r.q0;
-                }
-              }
-              mbar_arrive(bar_seg + 8 * ss);
-            }
-            ++seg_out;
-            __syncwarp();
-            more = __shfl_sync(0xFFFFFFFFu, found, 0) != 0;
-            first_seg = false;
-            if (!more) return;
-            left = walk->count;
-            at_block = walk->block;
-            row = a.v.table + static_cast<long long>(walk->b) * a.v.table_stride;
-            len_ahead = walk->r.len;
-            head_ahead = walk->head;
-            __syncwarp();                    // all lanes have read the walk
-            next_id = page_of(at_block);
-          }
-          id = next_id < a.v.pages ? next_id : -1;
-          next_id = left > 1 ? page_of(at_block + 1) : -1;
-        }
-        if (!mbar_wait(bar_raw_empty + 8 * kv, (ahead & 1) ^ 1, abort)) {
-          if (lane == 0) kp_timeout(abort, 0x52);
-          ok = false;
-          return;
-        }
-        const unsigned have = __ballot_sync(0xFFFFFFFFu, id >= 0);
-        const uint32_t full = bar_raw + 8 * kv;
-        if (kv) ++issued[1]; else ++issued[0];
-        if (lane == 0)
-          mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(have)) * (D << shift));
-        __syncwarp();
-        const long long unit = static_cast<long long>(id) * a.v.heads + head_ahead;
-        if (id >= 0)
-          tma_load_2d(base + L::RAW_OFF + kv * L::RAW_BYTES + lane * (D << shift),
-                      kv ? &tmV : &tmK, full, 0, static_cast<int>(unit << shift));
-        if (kv == 0) {
-          kf = __uint_as_float(0x7FC00000u);
-          ve = 0xFF;
-          if (id >= 0) {
-            kf = kv_scale_value(a.v.k_scales[unit]);
-            ve = a.v.v_scales[unit];
-          }
-        } else {
-          const int ps = ahead & (KP_PG - 1);
-          KpPages* pg = reinterpret_cast<KpPages*>(gbase + L::PG_OFF) + ps;
-          if (ve == 0xFF) {
-            kf = __uint_as_float(0x7FC00000u);
-            ve = 0;
-          }
-          // lane i < 8 writes for keys 16 i ..: the page of lane 16 i >> shift
-          const int of = (16 * (lane & 7)) >> shift;
-          const float f = __shfl_sync(0xFFFFFFFFu, kf, of);
-          const int e = __shfl_sync(0xFFFFFFFFu, ve, of);
-          const int top = __reduce_max_sync(0xFFFFFFFFu, lane < 8 ? e : 0);
-          const unsigned gone = __ballot_sync(0xFFFFFFFFu, lane < 8 && !((have >> of) & 1));
-          if (lane < 8) {
-            pg->of[lane].kf = f;
-            pg->of[lane].ve = e;
-          }
-          if (lane == 0) {
-            pg->top = top;
-            pg->gone = static_cast<int>(gone);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_pg + 8 * ps);
-          ++ahead;
-          ++at_block;
-          --left;
-        }
-      };
-      if (warp == 0) {
-        issue(0);
-        issue(1);
-      }
-      int bt = 0, seg_it = 0;
       while (ok) {
-        const int ss = seg_it & 1;
-        if (!mbar_wait(bar_seg + 8 * ss, (seg_it >> 1) & 1, abort)) {
-          if (lane == 0) kp_timeout(abort, 0x53);
+        const int ss = seg_out & 1;
+        int found = 0;
+        if (lane == 0) {
+          if (a.ws != nullptr) {
+            found = walk->next(a.v);
+          } else if (walk->w < walk->w1) {
+            const long long w1 = walk->w1;
+            walk->w1 = 0x7FFFFFFFFFFFFFFFll;
+            found = walk->next(a.v);
+            walk->w1 = w1;
+          }
+        }
+        __syncwarp();
+        found = __shfl_sync(0xFFFFFFFFu, found, 0);
+        release(found);
+        if (!found && bt == 0 && lane == 0) {
+          // a stretch without blocks: the converting warps wait for the first
+          pages[0].top = -1;
+          mbar_arrive(bar_pg);
+        }
+        if (!mbar_wait(bar_seg_empty + 8 * ss, ((seg_out >> 1) & 1) ^ 1, abort)) {
+          if (lane == 0) kp_timeout(abort, 0x51);
           break;
         }
-        ++seg_it;
-        const int count = segs[ss].count, len = segs[ss].len, block0 = segs[ss].block;
-        if (count == 0) break;
-        for (int j = 0; j < count && ok; ++j, ++bt) {
-          const int st = bt & 1, key0 = (block0 + j) * KP_BK;
-          const KpPages* pg = reinterpret_cast<const KpPages*>(gbase + L::PG_OFF) + (bt & (KP_PG - 1));
-#pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv) {
-            if (!mbar_wait(bar_raw + 8 * kv, bt & 1, abort)) {
-              if (lane == 0) kp_timeout(abort, 0x54);
-              ok = false;
-              break;
+        if (lane == 0) {
+          KpSeg* s = const_cast<KpSeg*>(segs) + ss;
+          s->count = found ? walk->count : 0;
+          if (found) {
+            s->block = walk->block;
+            s->len = walk->r.len;
+            s->n = walk->r.n;
+            s->q0 = walk->r.q0;
+            s->row0 = walk->rt * KP_ROWS;
+            s->head = walk->head;
+            const int slot = 2 * static_cast<int>(blockIdx.x) + (first_seg ? 0 : 1);
+            s->slot = walk->begins && walk->ends ? -1 : slot;
+            if (walk->begins && !walk->ends) {
+              KpJoin* j = a.joins + blockIdx.x;
+              j->live = min(KP_ROWS, walk->r.n * a.v.group - walk->rt * KP_ROWS);
+              j->parts = static_cast<int>((walk->unit_end * ctas - 1) / total - blockIdx.x + 1);
+              j->first_slot = slot;
+              j->head = walk->head;
+              j->row0 = walk->rt * KP_ROWS;
+              j->q0 = walk->r.q0;
             }
-            uint4 w[IT];
-            const uint32_t src = base + L::RAW_OFF + kv * L::RAW_BYTES;
-#pragma unroll
-            for (int i = 0; i < IT; ++i)
-              if (i < IT - 1 || ci + 3 * i < STEPS)
-                w[i] = ld_shared_v4(src + from[i & 1] + (i >> 1) * 3072);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_raw_empty + 8 * kv);
-            if (kv == 1) {
-              if (!mbar_wait(bar_pg + 8 * (bt & (KP_PG - 1)), (bt / KP_PG) & 1, abort)) {
-                if (lane == 0) kp_timeout(abort, 0x54);
-                ok = false;
-                break;
-              }
-              // keys behind the request's end or in pages that were not
-              // loaded: zeros, whatever stands there
-              const unsigned gone = static_cast<unsigned>(pg->gone);
-              if (gone || key0 + KP_BK > len) {
-#pragma unroll
-                for (int i = 0; i < IT; ++i) {
-                  const int r = (ci + 3 * i) * SROWS + rl;
-                  if (key0 + r >= len || ((gone >> ((r >> 4) & 7)) & 1)) w[i] = make_uint4(0, 0, 0, 0);
-                }
-              }
-            }
-            if (warp == 0) issue(kv);
-            if (!ok) break;
-            if (!mbar_wait((kv ? bar_v_empty : bar_k_empty) + 8 * st, ((bt >> 1) & 1) ^ 1, abort)) {
-              if (lane == 0) kp_timeout(abort, 0x55);
-              ok = false;
-              break;
-            }
-            const uint32_t dst = base + (kv ? L::V_OFF + st * L::V_BYTES : L::K_OFF + st * L::K_BYTES);
-#pragma unroll
-            for (int i = 0; i < IT; ++i) {
-              if (i < IT - 1 || ci + 3 * i < STEPS) {
-                // 16 codes: two neighbouring 16-byte chunks of the f16 row
-                uint32_t f[8];
-                kv_f16_pairs<FMT>(w[i].x, f[0], f[1]);
-                kv_f16_pairs<FMT>(w[i].y, f[2], f[3]);
-                kv_f16_pairs<FMT>(w[i].z, f[4], f[5]);
-                kv_f16_pairs<FMT>(w[i].w, f[6], f[7]);
-                const uint32_t at = dst + to[i & 1] + (i >> 1) * (6 * SROWS * 128);
-                st_shared_v4(at, f[0], f[1], f[2], f[3]);
-                st_shared_v4(at ^ 16, f[4], f[5], f[6], f[7]);
-              }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive((kv ? bar_v : bar_k) + 8 * st);
           }
+          mbar_arrive(bar_seg + 8 * ss);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_seg_empty + 8 * ss);
-      }
-      if (warp == 0) {
-        // the CTA may not retire before its copies have landed
-        for (int kv = 0; kv < 2; ++kv) {
-          const int n = kv ? issued[1] : issued[0];
-          if (n == 0) continue;
-          const long long t0 = clock64();
-          while (!mbar_try_wait(bar_raw + 8 * kv, (n - 1) & 1) &&
-                 clock64() - t0 < MXK_WAIT_LIMIT_CYCLES) {
+        ++seg_out;
+        first_seg = false;
+        if (!found) break;
+        const int count = walk->count, block0 = walk->block, len = walk->r.len, head = walk->head;
+        const int* row = a.v.table + static_cast<long long>(walk->b) * a.v.table_stride;
+        __syncwarp();                          // all lanes have read the walk
+        const int shift = a.v.page_shift;
+        // the page of 16 keys, one per lane; -1: none, or outside the cache
+        auto page_of = [&](int j) {
+          const int key = (block0 + j) * KP_BK + 16 * lane;
+          return j < count && lane < 8 && key < len ? row[key >> shift] : -1;
+        };
+        int next_id = page_of(0);
+        for (int j = 0; j < count; ++j) {
+          int id = next_id;
+          next_id = page_of(j + 1);            // a block ahead
+          if (id >= a.v.pages) id = -1;
+          long long at = -1;
+          float kf = __uint_as_float(0x7FC00000u);
+          int ve = 0;
+          if (id >= 0) {
+            const long long unit = static_cast<long long>(id) * a.v.heads + head;
+            const uint32_t kc = a.v.k_scales[unit], vc = a.v.v_scales[unit];
+            at = ((unit << shift) + ((16 * lane) & ((1 << shift) - 1))) * D;
+            if (kc != 0xFFu && vc != 0xFFu) {
+              kf = kv_scale_value(kc);
+              ve = static_cast<int>(vc);
+            }
           }
+          release(1);
+          const int ps = bt & (KP_PG - 1);
+          if (!mbar_wait(bar_pg_empty + 8 * ps, ((bt / KP_PG) & 1) ^ 1, abort)) {
+            if (lane == 0) kp_timeout(abort, 0x52);
+            ok = false;
+            break;
+          }
+          if (lane < 8) {
+            pages[ps].of[lane].kf = kf;
+            pages[ps].of[lane].ve = ve;
+            pages[ps].at[lane] = at;
+          }
+          const int top = __reduce_max_sync(0xFFFFFFFFu, ve);
+          if (lane == 0) {
+            pages[ps].top = top;
+            pages[ps].valid = len - (block0 + j) * KP_BK;
+          }
+          __syncwarp();
+          held = true;
+          ++bt;
         }
       }
-    } else {
+    } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
       const uint32_t id_qk = kp_idesc(KP_BK, 0);
       const uint32_t id_pv = kp_idesc(D, 1);
@@ -765,14 +628,105 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         if (lane == 0) mbar_arrive(bar_seg_empty + 8 * ss);
       }
     }
+  } else if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(KP_REGS_CONV));
+    // ------------------------------------------------------------ conversion
+    // A step is 512 bytes of codes (4 rows of 128 or 8 of 64), 16 codes a
+    // lane; warp ci takes steps ci, ci + 4, ..: all its steps start at the
+    // same row mod 8, and each lies within 16 keys.  For d 128 eight
+    // consecutive lanes take the four lower chunks of one row and the four
+    // upper ones of the next, which keeps the swizzled writes (two 16-byte
+    // chunks of f16 a lane) free of bank conflicts.
+    const int ci = warp - 12;
+    constexpr int SROWS = 512 / D;
+    constexpr int IT = KP_BK / SROWS / 4;
+    int rl, c;                               // row in the step, chunk of the row
+    if constexpr (D == 128) {
+      rl = 2 * (lane >> 4) + (((lane >> 2) ^ (lane >> 3)) & 1);
+      c = lane & 7;
+    } else {
+      rl = lane >> 2;
+      c = lane & 3;
+    }
+    const int r0 = ci * SROWS + rl;          // the lane's row in the warp's first step
+    const uint32_t to = (c >> 2) * L::REGION + r0 * 128 + (((2 * (c & 3)) ^ (r0 & 7)) << 4);
+    // its place in the 16 keys that step i lies in: number (i * 4 * SROWS + r0) / 16
+    const int from = (r0 & 15) * D + 16 * c;
+    const KpPages* pages = reinterpret_cast<const KpPages*>(gbase + L::PG_OFF);
+    uint4 w[IT];                             // the next tile's codes
+    auto load = [&](const uint8_t* plane, long long at) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (at >= 0)
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                     : "l"(plane + at + from));
+      return x;
+    };
+    auto store = [&](uint32_t dst, int i, const uint4& x) {
+      uint32_t f[8];
+      kv_f16_pairs<FMT>(x.x, f[0], f[1]);
+      kv_f16_pairs<FMT>(x.y, f[2], f[3]);
+      kv_f16_pairs<FMT>(x.z, f[4], f[5]);
+      kv_f16_pairs<FMT>(x.w, f[6], f[7]);
+      const uint32_t p = dst + to + i * (4 * SROWS * 128);
+      st_shared_v4(p, f[0], f[1], f[2], f[3]);
+      st_shared_v4(p ^ 16, f[4], f[5], f[6], f[7]);
+    };
+    // the table's data of the block that is loaded next
+    auto pages_of = [&](int b) -> const KpPages* {
+      if (!mbar_wait(bar_pg + 8 * (b & (KP_PG - 1)), (b / KP_PG) & 1, abort)) {
+        if (lane == 0) kp_timeout(abort, 0x53);
+        return nullptr;
+      }
+      return pages + (b & (KP_PG - 1));
+    };
+    const KpPages* pg = pages_of(0);
+    if (pg && pg->top < 0) pg = nullptr;     // there are none
+    if (pg) {
+#pragma unroll
+      for (int i = 0; i < IT; ++i) w[i] = load(a.k, pg->at[(i * 4 * SROWS + r0) >> 4]);
+    }
+    // tiles in the order K, V of each block; a chunk's registers take the next
+    // tile's codes as soon as it is converted
+#pragma unroll 1
+    for (int tile = 0; pg; ++tile) {
+      const int kv = tile & 1, bt = tile >> 1, st = bt & 1;
+      const KpPages* next = pg;              // of the next tile: V, or the next block's K
+      if (kv == 1 && pg->more == 0) {
+        next = nullptr;
+      } else if (kv == 1) {
+        next = pages_of(bt + 1);
+        if (!next) break;
+      }
+      const uint8_t* plane = kv ? a.k : a.v_codes;
+      const uint32_t dst = base + (kv ? L::V_OFF : L::K_OFF) + st * L::K_BYTES;
+      // keys behind the request's end count as zeros in V, whatever stands there
+      const int valid = kv ? pg->valid : KP_BK;
+      if (!mbar_wait((kv ? bar_v_empty : bar_k_empty) + 8 * st, ((bt >> 1) & 1) ^ 1, abort)) {
+        if (lane == 0) kp_timeout(abort, 0x54);
+        break;
+      }
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        if (i * 4 * SROWS + r0 >= valid) w[i] = make_uint4(0, 0, 0, 0);
+        store(dst, i, w[i]);
+        if (next) w[i] = load(plane, next->at[(i * 4 * SROWS + r0) >> 4]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive((kv ? bar_v : bar_k) + 8 * st);
+        if (kv) mbar_arrive(bar_pg_empty + 8 * (bt & (KP_PG - 1)));
+      }
+      pg = next;
+    }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(KP_REGS_HIGH));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(KP_REGS_SOFT));
     // ------------------------------------------------------------ softmax
     const int t = (warp - 4) >> 2;
     const int quarter = warp & 3;
     const int urow = KP_BQ * t + 32 * quarter + lane;       // row in the unit
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + 256 * t;
-    const int shift = a.v.page_shift;
     // blocks of the tile's own barriers (tile 1 may sit units out) and of all
     int bt = 0, own = 0, own_seg = 0, seg_it = 0;
     bool ok = true;
@@ -783,25 +737,27 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         break;
       }
       ++seg_it;
-      const KpSeg sg = segs[ss];
-      if (sg.count == 0) break;
-      const int rows = sg.n * a.v.group;
-      const bool works = rows - sg.row0 > KP_BQ * t;        // the tile has rows
+      const int count = segs[ss].count, key00 = segs[ss].block * KP_BK;
+      if (count == 0) break;
+      const bool works = segs[ss].n * a.v.group - segs[ss].row0 > KP_BQ * t;   // the tile has rows
       // ---- this thread's row: Q to f16, its bounds and factor
-      const int row = sg.row0 + urow;
-      const bool live = row < rows;
-      const int token = live ? row / a.v.group : 0;
-      const int qh = sg.head * a.v.group + (live ? row - token * a.v.group : 0);
-      KvReq rq;
-      rq.q0 = sg.q0;
-      rq.n = sg.n;
-      rq.len = sg.len;
-      const int lo = live ? kv_first_key(a.v, rq, token) : 0;
-      const int hi = live ? kv_end_key(a.v, rq, token) : 0;
+      bool live;
+      int lo, hi;
       float up = 1.0f;
+      {
+      KvReq rq;
+      rq.q0 = segs[ss].q0;
+      rq.n = segs[ss].n;
+      rq.len = segs[ss].len;
+      const int row = segs[ss].row0 + urow;
+      live = row < rq.n * a.v.group;
+      const int token = live ? row / a.v.group : 0;
+      const int qh = segs[ss].head * a.v.group + (live ? row - token * a.v.group : 0);
+      lo = live ? kv_first_key(a.v, rq, token) : 0;
+      hi = live ? kv_end_key(a.v, rq, token) : 0;
       if (works) {
         uint32_t w[D / 2];
-        const uint16_t* src = a.Q + (sg.q0 + token) * a.q_ts + qh * a.q_hs;
+        const uint16_t* src = a.Q + (rq.q0 + token) * a.q_ts + qh * a.q_hs;
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
           uint4 v = make_uint4(0, 0, 0, 0);
@@ -837,6 +793,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_q + 8 * t);
       }
+      }
       // a negative scale has gone into Q: the factor of a score is never negative
       const float fr = fabsf(a.scale_log2e) * up;
       // keys that every live row of this warp sees
@@ -845,53 +802,69 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 
       float m = -INFINITY, l = 0.0f;
       int ev = 0;                              // V's reference exponent
-      for (int j = 0; j < sg.count && works; ++j, ++own) {
-        const int g = bt + j, key0 = (sg.block + j) * KP_BK;
-        if (!mbar_wait(bar_pg + 8 * (g & (KP_PG - 1)), (g / KP_PG) & 1, abort) ||
-            !mbar_wait(bar_s_full + 8 * t, own & 1, abort)) {
+      for (int j = 0; j < count; ++j) {
+        const int g = bt + j, key0 = key00 + j * KP_BK, ps = g & (KP_PG - 1);
+        if (!mbar_wait(bar_pg + 8 * ps, (g / KP_PG) & 1, abort) ||
+            (works && !mbar_wait(bar_s_full + 8 * t, own & 1, abort))) {
           if (lane == 0) kp_timeout(abort, 0x5c);
           ok = false;
           break;
         }
+        if (!works) {                          // the tile has no rows: only say so
+          if (lane == 0) mbar_arrive(bar_pg_empty + 8 * ps);
+          continue;
+        }
+        ++own;
         tc_fence_after();
-        const KpPages* pg = reinterpret_cast<const KpPages*>(gbase + L::PG_OFF) + (g & (KP_PG - 1));
-        uint32_t sv[KP_BK];
-#pragma unroll
-        for (int c = 0; c < KP_BK / 32; ++c)
-          tmem_ld_32x32b_x32(lane_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
+        const KpPages* pg = reinterpret_cast<const KpPages*>(gbase + L::PG_OFF) + ps;
         const int ev_new = max(ev, pg->top);
-        tmem_wait_ld();
-        // row maximum: of the raw scores of each 16 keys, times their factor; a
-        // block that some row does not see whole is scaled and masked first
+        // Row maximum: of the raw scores of each 16 keys, times their factor.
+        // A block that some row does not see whole is scaled and masked first:
+        // what is hidden may stand in a page whose factor is NaN.  The scores
+        // are read 32 at a time, a load ahead, here and again for the
+        // exponentials, in loops: unrolled with all 128 in registers, the code
+        // of the roles crowded the MMA warp's out of the instruction cache.
         const bool masked = key0 < all_lo || key0 + KP_BK > all_hi;
-        float mx = -INFINITY;
-        if (!masked) {
+        // scales keys 32 c .. 32 c + 31 and hides what the row does not see
+        auto hide = [&](uint32_t (&x)[32], int c) {
+          const int k0 = key0 + 32 * c;
+          const float f0 = fr * pg->of[2 * c].kf, f1 = fr * pg->of[2 * c + 1].kf;
 #pragma unroll
-          for (int p = 0; p < 8; ++p) {
+          for (int e = 0; e < 32; ++e) {
+            const float y = __uint_as_float(x[e]) * (e < 16 ? f0 : f1);
+            x[e] = k0 + e >= lo && k0 + e < hi ? __float_as_uint(y) : 0xFF800000u;   // -inf
+          }
+        };
+        float mx = -INFINITY;
+        auto top_of = [&](uint32_t (&x)[32], int c) {
+          if (masked) hide(x, c);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
             float g0 = -INFINITY, g1 = -INFINITY;
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
-              g0 = max3(g0, __uint_as_float(sv[16 * p + e]), __uint_as_float(sv[16 * p + e + 1]));
-              g1 = max3(g1, __uint_as_float(sv[16 * p + e + 2]), __uint_as_float(sv[16 * p + e + 3]));
+              g0 = max3(g0, __uint_as_float(x[16 * h + e]), __uint_as_float(x[16 * h + e + 1]));
+              g1 = max3(g1, __uint_as_float(x[16 * h + e + 2]), __uint_as_float(x[16 * h + e + 3]));
             }
-            mx = fmaxf(mx, fmaxf(g0, g1) * (fr * pg->of[p].kf));
+            mx = fmaxf(mx, fmaxf(g0, g1) * (masked ? 1.0f : fr * pg->of[2 * c + h].kf));
           }
-        } else {
-#pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            const float f = fr * pg->of[p].kf;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int k = key0 + 16 * p + e;
-              const float x = k >= lo && k < hi ? __uint_as_float(sv[16 * p + e]) * f : -INFINITY;
-              sv[16 * p + e] = __float_as_uint(x);
-              mx = fmaxf(mx, x);
-            }
-          }
+        };
+        uint32_t sa[32], sb[32];
+        tmem_ld_32x32b_x32(lane_addr, sa);
+#pragma unroll 1
+        for (int c = 0; c < 4; c += 2) {
+          tmem_wait_ld();
+          tmem_ld_32x32b_x32(lane_addr + 32 * c + 32, sb);
+          top_of(sa, c);
+          tmem_wait_ld();
+          // the next two; at the end the first 32 again, for the exponentials
+          tmem_ld_32x32b_x32(lane_addr + ((32 * c + 64) & 127), sa);
+          top_of(sb, c + 1);
         }
         const float m_new = mx > m + KP_LAZY ? mx : m;
         const float alpha = m_new == m ? 1.0f : ex2_approx(m - m_new);
         if (j >= 1 && __any_sync(0xFFFFFFFFu, m_new != m || ev_new != ev)) {
+          tmem_wait_ld();                      // sa's load
           const float f = alpha * kv_exp2i(ev - ev_new);
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -908,10 +881,10 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         m = m_new;
         // p' = 2^(x - m + b), b = 7 + (V's exponent - the reference), rounded
         // to f16 and written back over the scores; the sum takes b out again.
-        // Masked scores are -inf and stay it: b and m_use are finite.
+        // Hidden scores are -inf and stay it: b and m_use are finite.
         const float m_use = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-        for (int c = 0; c < KP_BK / 32; ++c) {
+        auto exps = [&](uint32_t (&x)[32], int c) {
+          if (masked) hide(x, c);
           uint32_t pk[16];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -925,28 +898,39 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               float x0, x1;
-              unpack2(fma2(pack2(__uint_as_float(sv[16 * p + 2 * e]),
-                                 __uint_as_float(sv[16 * p + 2 * e + 1])),
+              unpack2(fma2(pack2(__uint_as_float(x[16 * h + 2 * e]),
+                                 __uint_as_float(x[16 * h + 2 * e + 1])),
                            f2, nm2),
                       x0, x1);
               const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
               pk[8 * h + e] = cvt_f16x2(p0, p1);
               sum = add2(sum, pack2(p0, p1));
             }
-            float s0, s1;
-            unpack2(sum, s0, s1);
-            l = fmaf(s0 + s1, __int_as_float((127 - b) << 23), l);
+            float a0, a1;
+            unpack2(sum, a0, a1);
+            l = fmaf(a0 + a1, __int_as_float((127 - b) << 23), l);
           }
           tmem_st_32x32b_x16(lane_addr + 16 * c, pk);
-          if (c == KP_BK / 64 - 1 || c == KP_BK / 32 - 1) {
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_p_full + 16 * t + (c == KP_BK / 32 - 1 ? 8 : 0));
-          }
+        };
+        auto written = [&](int half) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_p_full + 16 * t + 8 * half);
+        };
+#pragma unroll 1
+        for (int c = 0; c < 4; c += 2) {
+          tmem_wait_ld();
+          tmem_ld_32x32b_x32(lane_addr + 32 * c + 32, sb);
+          exps(sa, c);
+          tmem_wait_ld();
+          if (c == 0) tmem_ld_32x32b_x32(lane_addr + 64, sa);
+          exps(sb, c + 1);
+          written(c >> 1);                     // 64 keys of P: their product may start
         }
+        if (lane == 0) mbar_arrive(bar_pg_empty + 8 * ps);
       }
-      bt += sg.count;
+      bt += count;
       if (!ok) break;
       if (works) {
         if (!mbar_wait(bar_o_done + 8 * t, own_seg & 1, abort)) {
@@ -958,25 +942,54 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         // to true units: 2^(ev - 127), and the 2^KP_P_EXP out of P
         const float unit = kv_scale_value(static_cast<uint32_t>(ev));
         const float inv = (l == 0.0f ? 0.0f : 1.0f / l) * (1.0f / (1 << KP_P_EXP));
-        float* part = sg.slot >= 0 ? a.ws + static_cast<long long>(sg.slot) * (KP_ROWS * (D + 2)) : nullptr;
-        const long long out = (sg.q0 + token) * a.o_ts + qh * a.o_hs;
+        // (read again rather than kept in registers over the blocks)
+        const volatile KpSeg* sg = segs + ss;
+        float* part = sg->slot >= 0 ? a.ws + static_cast<long long>(sg->slot) * (KP_ROWS * (D + 2)) : nullptr;
+        const int row = sg->row0 + urow, token = row / a.v.group;
+        const long long out =
+            (sg->q0 + token) * a.o_ts + (sg->head * a.v.group + row - token * a.v.group) * a.o_hs;
+        // rows of O 32 bytes at a time where they are that aligned
+        const bool by32 = ((reinterpret_cast<uintptr_t>(a.O) |
+                            static_cast<uintptr_t>(out * (a.o_dtype == DT_F32 ? 4 : 2))) & 31) == 0;
+        const float f = part ? 1.0f / (1 << KP_P_EXP) : inv;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld_32x32b_x32(lane_addr + 128 + 32 * c, o);
           tmem_wait_ld();
           if (!live) continue;
-          const float f = part ? 1.0f / (1 << KP_P_EXP) : inv;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 v = make_float4(__uint_as_float(o[4 * e]) * f * unit,
-                                         __uint_as_float(o[4 * e + 1]) * f * unit,
-                                         __uint_as_float(o[4 * e + 2]) * f * unit,
-                                         __uint_as_float(o[4 * e + 3]) * f * unit);
-            if (part)
-              *reinterpret_cast<float4*>(part + urow * D + 32 * c + 4 * e) = v;
-            else
-              kv_store4(a.O, a.o_dtype, out + 32 * c + 4 * e, v);
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f * unit);
+          if (part) {
+            // lanes hold consecutive rows: whole lines of [column][row]
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<uint4*>(part)[(8 * c + e) * KP_ROWS + urow] =
+                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          } else if (a.o_dtype == DT_F32) {
+            float* dst = static_cast<float*>(a.O) + out + 32 * c;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<uint4*>(dst)[e] =
+                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          } else {
+            uint16_t* dst = static_cast<uint16_t*>(a.O) + out + 32 * c;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float x0 = __uint_as_float(o[16 * h + 2 * e]);
+                const float x1 = __uint_as_float(o[16 * h + 2 * e + 1]);
+                w[e] = a.o_dtype == DT_BF16 ? cvt_bf16x2(x0, x1) : cvt_f16x2(x0, x1);
+              }
+              if (by32) {
+                st_global_v8(dst + 16 * h, w);
+              } else {
+                reinterpret_cast<uint4*>(dst + 16 * h)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                reinterpret_cast<uint4*>(dst + 16 * h)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+              }
+            }
           }
         }
         if (part && live) {
@@ -1008,8 +1021,11 @@ kv_prompt_join_kernel(const KpArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const KpJoin* join = a.joins + blockIdx.x;
   const int live = __ldcg(&join->live);
-  const int at = blockIdx.y * KPJ_THREADS + threadIdx.x;
-  const int urow = at / (D / 4), col = 4 * (at % (D / 4));
+  // a warp takes two rows and 64 columns: whole sectors of the parts, whose
+  // rows stand side by side, and 128 bytes or more of each row of O
+  const int warp = (blockIdx.y * KPJ_THREADS + threadIdx.x) >> 5, lane = threadIdx.x & 31;
+  const int urow = 2 * (warp / (D / 64)) + (lane & 1);
+  const int col = 64 * (warp % (D / 64)) + 4 * (lane >> 1);
   if (urow >= live) return;
   constexpr long long PART = KP_ROWS * (D + 2);
   const int n = __ldcg(&join->parts);
@@ -1025,7 +1041,7 @@ kv_prompt_join_kernel(const KpArgs a) {
   for (int p = 0; p < n; ++p) {
     const float mp = __ldcg(part(p) + KP_ROWS * D + urow);
     const float lp = __ldcg(part(p) + KP_ROWS * (D + 1) + urow);
-    const float4 v = ld_global_cg_f4(part(p) + static_cast<long long>(urow) * D + col);
+    const float4 v = ld_global_cg_f4(part(p) + static_cast<long long>(col) * KP_ROWS + 4 * urow);
     const float w = mp == top ? 1.0f : ex2_approx(mp - top);
     sum = fmaf(w, lp, sum);
     acc.x = fmaf(w, v.x, acc.x);
@@ -1042,8 +1058,7 @@ kv_prompt_join_kernel(const KpArgs a) {
 }
 
 template <int FMT, int D>
-cudaError_t kp_run(const CUtensorMap& tk, const CUtensorMap& tv, const KpArgs& a, int sms,
-                   cudaStream_t st) {
+cudaError_t kp_run(const KpArgs& a, int sms, cudaStream_t st) {
   auto kern = kv_prompt_kernel<FMT, D>;
   using L = KpSmem<D>;
   static std::atomic<bool> attr_set[64] = {};
@@ -1057,11 +1072,11 @@ cudaError_t kp_run(const CUtensorMap& tk, const CUtensorMap& tv, const KpArgs& a
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, kern);
     if (e != cudaSuccess) return e;
-    if (fa.numRegs * KP_THREADS < KP_REGS_LOW * 128 + KP_REGS_HIGH * 256)
+    if (fa.numRegs * KP_THREADS < KP_REGS_LOW * 128 + KP_REGS_SOFT * 256 + KP_REGS_CONV * 128)
       return cudaErrorInvalidConfiguration;
     if (dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
   }
-  kern<<<sms, KP_THREADS, L::ALLOC, st>>>(tk, tv, a);
+  kern<<<sms, KP_THREADS, L::ALLOC, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.ws == nullptr) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1089,6 +1104,8 @@ cudaError_t launch_kv_prompt(const KvAttn& q, int sms, cudaStream_t st) {
   KpArgs a{};
   a.v = kv_view(q);
   a.Q = static_cast<const uint16_t*>(q.Q);
+  a.k = c.k;
+  a.v_codes = c.v;
   a.O = q.O;
   a.q_ts = q.q_ts;
   a.q_hs = q.q_hs;
@@ -1102,16 +1119,14 @@ cudaError_t launch_kv_prompt(const KvAttn& q, int sms, cudaStream_t st) {
     a.joins = reinterpret_cast<KpJoin*>(static_cast<char*>(q.ws) +
                                         static_cast<int64_t>(sms) * 2 * KP_ROWS * (c.d + 2) * 4);
   }
-  CUtensorMap tk, tv;
-  if (!kv_tensor_map(&tk, c.k, c) || !kv_tensor_map(&tv, c.v, c)) return cudaErrorInvalidValue;
   const bool d64 = c.d == 64;
   switch (c.fmt) {
     case FMT_E4M3:
-      return d64 ? kp_run<FMT_E4M3, 64>(tk, tv, a, sms, st) : kp_run<FMT_E4M3, 128>(tk, tv, a, sms, st);
+      return d64 ? kp_run<FMT_E4M3, 64>(a, sms, st) : kp_run<FMT_E4M3, 128>(a, sms, st);
     case FMT_E5M2:
-      return d64 ? kp_run<FMT_E5M2, 64>(tk, tv, a, sms, st) : kp_run<FMT_E5M2, 128>(tk, tv, a, sms, st);
+      return d64 ? kp_run<FMT_E5M2, 64>(a, sms, st) : kp_run<FMT_E5M2, 128>(a, sms, st);
     default:
-      return d64 ? kp_run<FMT_INT8, 64>(tk, tv, a, sms, st) : kp_run<FMT_INT8, 128>(tk, tv, a, sms, st);
+      return d64 ? kp_run<FMT_INT8, 64>(a, sms, st) : kp_run<FMT_INT8, 128>(a, sms, st);
   }
 }
 
