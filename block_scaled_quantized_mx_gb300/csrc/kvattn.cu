@@ -368,17 +368,69 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
       const int len = rq.len, shift = a.v.page_shift;
       const int per_tile = KA_TK >> shift;
       const int* row = a.v.table + static_cast<long long>(walk.b) * a.v.table_stride;
-      // a tile's pages, one per lane: its id, or -1 where the request has
-      // none and for an id outside the cache (whose keys are NaN); read one
-      // tile ahead
+      // A tile's pages: lanes 0 .. 7 look after their keys, 8 .. 15 after their
+      // values.  A page's id is -1 where the request has none and for an id
+      // outside the cache (whose keys are NaN).  Ids are read two tiles ahead
+      // and scales one, so that no tile waits for either.
+      const int slot = lane & 7;
+      const bool is_v = (lane & 8) != 0;
+      const uint8_t* scales = is_v ? a.v.v_scales : a.v.k_scales;
       auto page_of = [&](int i) {
         const int key0 = (walk.tile + i) * KA_TK;
         int id = -1;
-        if (i < walk.count && lane < per_tile && key0 + (lane << shift) < len)
-          id = row[(key0 >> shift) + lane];
-        return id;
+        if (i < walk.count && lane < 16 && slot < per_tile && key0 + (slot << shift) < len)
+          id = row[(key0 >> shift) + slot];
+        return id < a.v.pages ? id : -1;
       };
-      int next_id = page_of(0);
+      auto scale_of = [&](int id) -> uint32_t {
+        return id >= 0 ? scales[static_cast<long long>(id) * a.v.heads + walk.head] : 0xFFu;
+      };
+      int id0 = page_of(0), id1 = page_of(1);
+      uint32_t code = scale_of(id0);
+      // loads tile i of the segment
+      auto load = [&](int i) {
+        const int st = it % L::STAGES;
+        const int id2 = page_of(i + 2);
+        const uint32_t next_code = scale_of(id1);
+        if (!mbar_wait(bar_empty + 8 * st, ((it / L::STAGES) & 1) ^ 1, abort)) {
+          if (lane == 0) ka_timeout(abort, 0x42);
+          return false;
+        }
+        const unsigned have = __ballot_sync(0xFFFFFFFFu, id0 >= 0);
+        const uint32_t full = bar_full + 8 * st;
+        if (lane == 0)
+          mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(have)) * (D << shift));
+        __syncwarp();
+        if (id0 >= 0) {
+          const int y =
+              static_cast<int>((static_cast<long long>(id0) * a.v.heads + walk.head) << shift);
+          tma_load_2d(base + st * 2 * L::TILE + (is_v ? L::TILE : 0) + slot * (D << shift),
+                      is_v ? &tmV : &tmK, full, 0, y);
+        }
+        // K's scale as a factor; V's as its code, 0xFF for NaN and -1 for a page
+        // that was not loaded (its codes must not be used)
+        if (lane < 16 && slot < per_tile) {
+          uint32_t* pg = reinterpret_cast<uint32_t*>(gbase + L::PG_OFF + st * L::PG_STAGE);
+          pg[2 * slot + (is_v ? 1 : 0)] =
+              is_v ? (id0 >= 0 ? code : 0xFFFFFFFFu) : __float_as_uint(kv_scale_value(code));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full);
+        id0 = id1;
+        id1 = id2;
+        code = next_code;
+        ++it;
+        return true;
+      };
+      // the CTA's first tiles are on their way before its first rows are
+      // prepared: the ring is empty
+      int loaded = 0;
+      if (it == 0)
+        while (loaded < min(walk.count, L::STAGES) && ok) {
+          ok = load(loaded);
+          ++loaded;
+        }
+      if (!ok) break;
       // ---- the rows: what they see, and Q as the B operand's fragments: lane
       // (g, t) holds row g's values [D/4 t, D/4 (t + 1))
       int all_lo = 0, all_hi = 0x7FFFFFFF, any_lo = 0x7FFFFFFF, any_hi = 0;
@@ -472,44 +524,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_seg + 8 * ss);
 
-      // ---- the tiles
-      for (int i = 0; i < walk.count; ++i, ++it) {
-        const int st = it % L::STAGES;
-        const int id = next_id < a.v.pages ? next_id : -1;
-        next_id = page_of(i + 1);
-        if (!mbar_wait(bar_empty + 8 * st, ((it / L::STAGES) & 1) ^ 1, abort)) {
-          if (lane == 0) ka_timeout(abort, 0x42);
-          ok = false;
-          break;
-        }
-        const unsigned have = __ballot_sync(0xFFFFFFFFu, id >= 0);
-        const uint32_t full = bar_full + 8 * st;
-        if (lane == 0)
-          mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(have)) * 2u * (D << shift));
-        __syncwarp();
-        if (id >= 0) {
-          const uint32_t dst = base + st * 2 * L::TILE + lane * (D << shift);
-          const int y = static_cast<int>((static_cast<long long>(id) * a.v.heads + walk.head)
-                                         << shift);
-          tma_load_2d(dst, &tmK, full, 0, y);
-          tma_load_2d(dst + L::TILE, &tmV, full, 0, y);
-        }
-        if (lane < per_tile) {
-          // K's scale as a factor; V's as its code, 0xFF for NaN and -1 for
-          // a page that was not loaded (its codes must not be used)
-          float kf = __uint_as_float(0x7FC00000u);
-          int ve = -1;
-          if (id >= 0) {
-            const long long unit = static_cast<long long>(id) * a.v.heads + walk.head;
-            kf = kv_scale_value(a.v.k_scales[unit]);
-            ve = a.v.v_scales[unit];
-          }
-          uint2* pg = reinterpret_cast<uint2*>(gbase + L::PG_OFF + st * L::PG_STAGE) + lane;
-          *pg = make_uint2(__float_as_uint(kf), static_cast<uint32_t>(ve));
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full);
-      }
+      for (int i = loaded; i < walk.count && ok; ++i) ok = load(i);
     }
     // the CTA may not retire before its copies have landed
     for (int i = max(0, it - L::STAGES); i < it; ++i) {
