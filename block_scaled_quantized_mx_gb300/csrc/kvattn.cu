@@ -16,7 +16,7 @@
 //     the block table and loads each page's P x d codes with one TMA box
 //     (swizzled, so that the reads below are free of bank conflicts), ahead of
 //     the consumers; pages that a request does not have are not loaded;
-//   * four consumer warps each take 32 keys of a 128-key tile, with their own
+//   * four consumer warps each take a quarter of a tile's keys, with their own
 //     running maximum and sum (no barrier per tile): codes become f16 in
 //     registers (exact for all three formats) and feed mma.sync m16n8k16 with
 //     the keys (S = K Q^T) and then V's columns (O = V^T P) as the 16 rows
@@ -61,15 +61,19 @@ namespace {
 
 __device__ unsigned int g_status_kv = 0;
 
-constexpr int KA_TK = 128;                 // keys per tile
 constexpr int KA_WARPS = 4;                // consumer warps
-constexpr int KA_KW = KA_TK / KA_WARPS;    // keys of a tile per warp: two steps of 16
 constexpr int KA_CONS = 32 * KA_WARPS;
 constexpr int KA_THREADS = KA_CONS + 32;
-constexpr int KA_MAX_PAGES = KA_TK / 16;   // pages in a tile
 constexpr float KA_LAZY = 8.0f;            // slack of the exponentials' reference point
 constexpr int KA_P_EXP = 7;                // P is scaled by 2^7: at most 2^(7 + 8) in f16
 constexpr int KA_RED = 36;                 // floats per row of the staging: 32, padded
+
+// Keys per tile: 16 KB of codes of K and as many of V.  (128 keys of 64 values a
+// tile left each warp 32 short keys between two waits.)
+template <int D>
+constexpr int ka_tk() {
+  return D == 64 ? 256 : 128;
+}
 
 // CTAs per SM of the 8-row (NR = 1) and the 16-row (NR = 2) kernel.
 template <int NR>
@@ -106,7 +110,9 @@ struct KaJoin {
 template <int D, int NR>
 struct KaSmem {
   static constexpr int ROWS = 8 * NR;
-  static constexpr int TILE = KA_TK * D;               // codes of one tile of K or V
+  static constexpr int TK = ka_tk<D>();
+  static constexpr int MAX_PAGES = TK / 16;            // pages in a tile
+  static constexpr int TILE = TK * D;                  // codes of one tile of K or V
   static constexpr int RING = NR == 1 ? 65536 : 98304;
   static constexpr int STAGES = RING / (2 * TILE);
   // staging of the warps' O: [warp][8 rows][KA_RED]
@@ -119,7 +125,7 @@ struct KaSmem {
   static constexpr int SEG_BYTES = (sizeof(KaSeg<ROWS>) + 15) / 16 * 16;
   static constexpr int ML_OFF = SEG_OFF + 2 * SEG_BYTES;     // m, l: [2][warp][row], e: [warp]
   static constexpr int PG_OFF = ML_OFF + 2 * KA_WARPS * ROWS * 4 + 16;
-  static constexpr int PG_STAGE = KA_MAX_PAGES * 8;          // per page: K scale, V exponent
+  static constexpr int PG_STAGE = MAX_PAGES * 8;             // per page: K scale, V exponent
   static constexpr int BAR_OFF = PG_OFF + STAGES * PG_STAGE;
   static constexpr int MISC_OFF = BAR_OFF + STAGES * 16 + 32;
   static constexpr int TOTAL = MISC_OFF + 128;
@@ -153,6 +159,12 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// a / b for a >= 0, b > 0; 32-bit where both fit, which is several times faster.
+__device__ __forceinline__ long long ka_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // One request's share of the work list.
 struct KaReq {
   KvReq r;
@@ -162,14 +174,14 @@ struct KaReq {
   long long units;             // row tiles x cache heads; 0: nothing for this kernel
 };
 
-template <int ROWS>
+template <int ROWS, int TK>
 __device__ __forceinline__ KaReq ka_request(const KaArgs& a, int b) {
   KaReq q;
   q.r = kv_request(a.v, b);
   const long long rows = static_cast<long long>(q.r.n) * a.v.group;
   const int first = kv_first_key(a.v, q.r, 0);
-  q.tile0 = first / KA_TK;
-  q.tiles = 1 + max(1, (q.r.len + KA_TK - 1) / KA_TK - q.tile0);
+  q.tile0 = first / TK;
+  q.tiles = 1 + max(1, (q.r.len + TK - 1) / TK - q.tile0);
   q.row_tiles = static_cast<int>((rows + ROWS - 1) / ROWS);
   q.units = static_cast<long long>(q.row_tiles) * a.v.heads;
   return q;
@@ -179,7 +191,7 @@ __device__ __forceinline__ KaReq ka_request(const KaArgs& a, int b) {
 // its tiles behind one entry more, for the time it takes to begin and end a
 // unit (about that of a tile): without it a stretch of many short units took
 // 68 us where the median took 43 (48 requests of 0 to 6000 keys, window 2048).
-template <int ROWS>
+template <int ROWS, int TK>
 struct KaWalk {
   long long w, w1;             // next entry of the list, end of the stretch
   long long base;              // first entry of request b
@@ -195,16 +207,16 @@ struct KaWalk {
       while (w >= base + q.units * q.tiles) {
         base += q.units * q.tiles;
         if (++b >= a.v.requests) return false;
-        q = ka_request<ROWS>(a, b);
+        q = ka_request<ROWS, TK>(a, b);
       }
-      const long long u = (w - base) / q.tiles;
+      const long long u = ka_div(w - base, q.tiles);
       int t = static_cast<int>((w - base) - u * q.tiles);   // 0: the extra entry
       if (t == 0) {
         t = 1;
         if (++w >= w1) return false;          // the unit's tiles are the next CTA's
       }
-      head = static_cast<int>(u % a.v.heads);
-      row_tile = static_cast<int>(u / a.v.heads);
+      row_tile = static_cast<int>(ka_div(u, a.v.heads));
+      head = static_cast<int>(u - static_cast<long long>(row_tile) * a.v.heads);
       unit_start = base + u * q.tiles + 1;
       unit_end = unit_start + q.tiles - 1;
       tile = q.tile0 + t - 1;
@@ -243,7 +255,7 @@ __global__ void __launch_bounds__(KA_THREADS, ka_ctas_per_sm<NR>())
 kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const KaArgs a) {
   using L = KaSmem<D, NR>;
-  constexpr int ROWS = L::ROWS;
+  constexpr int ROWS = L::ROWS, TK = L::TK, KW = TK / KA_WARPS, KS = KW / 16;
   using Seg = KaSeg<ROWS>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -279,7 +291,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
   long long mine = 0;
   KaReq last{};
   for (int b = rb0; b < rb1; ++b) {
-    last = ka_request<ROWS>(a, b);
+    last = ka_request<ROWS, TK>(a, b);
     mine += last.units * last.tiles;
   }
   long long incl = mine;
@@ -303,11 +315,14 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
     if (a.ws != nullptr && tid == 0) join->live = 0;
     return;
   }
-  const long long w0 = total * cta / ctas, w1 = total * (cta + 1) / ctas;
+  // the first `longer` CTAs take one entry more than the others
+  const long long share = ka_div(total, ctas), longer = total - share * ctas;
+  const long long w0 = cta * share + min(cta, longer);
+  const long long w1 = w0 + share + (cta < longer ? 1 : 0);
   if (w0 >= before && w0 < before + mine) {
     long long p = before;
     for (int b = rb0; b < rb1; ++b) {
-      const KaReq q = per == 1 ? last : ka_request<ROWS>(a, b);
+      const KaReq q = per == 1 ? last : ka_request<ROWS, TK>(a, b);
       const long long n = q.units * q.tiles;
       if (w0 < p + n) {
         *sm_b = b;
@@ -322,7 +337,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
 
   if (warp == KA_WARPS) {
     // ------------------------------------------------------------ producer
-    KaWalk<ROWS> walk;
+    KaWalk<ROWS, TK> walk;
     walk.b = *sm_b;
     walk.base = *sm_base;
     walk.q = *sm_req;
@@ -366,19 +381,34 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
       const KvReq rq = walk.q.r;
       const int rows = rq.n * a.v.group;
       const int len = rq.len, shift = a.v.page_shift;
-      const int per_tile = KA_TK >> shift;
+      const int per_tile = TK >> shift;
+      // the rows' raw values, on their way before anything waits
+      uint4 raw_q[NR][D / 32];
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+        const int r = walk.row_tile * ROWS + 8 * nr + g;
+        const bool live = r < rows;
+        const int token = live ? r / a.v.group : 0;
+        const int qh = walk.head * a.v.group + (live ? r - token * a.v.group : 0);
+        const uint16_t* src = a.Q + (rq.q0 + token) * a.q_ts + qh * a.q_hs + t4 * (D / 4);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          raw_q[nr][c] = make_uint4(0, 0, 0, 0);
+          if (live) raw_q[nr][c] = *reinterpret_cast<const uint4*>(src + 8 * c);
+        }
+      }
       const int* row = a.v.table + static_cast<long long>(walk.b) * a.v.table_stride;
-      // A tile's pages: lanes 0 .. 7 look after their keys, 8 .. 15 after their
-      // values.  A page's id is -1 where the request has none and for an id
+      // A tile's pages: the first MAX_PAGES lanes look after their keys, the next
+      // after their values.  A page's id is -1 where the request has none and for an id
       // outside the cache (whose keys are NaN).  Ids are read two tiles ahead
       // and scales one, so that no tile waits for either.
-      const int slot = lane & 7;
-      const bool is_v = (lane & 8) != 0;
+      const int slot = lane & (L::MAX_PAGES - 1);
+      const bool is_v = (lane & L::MAX_PAGES) != 0;
       const uint8_t* scales = is_v ? a.v.v_scales : a.v.k_scales;
       auto page_of = [&](int i) {
-        const int key0 = (walk.tile + i) * KA_TK;
+        const int key0 = (walk.tile + i) * TK;
         int id = -1;
-        if (i < walk.count && lane < 16 && slot < per_tile && key0 + (slot << shift) < len)
+        if (i < walk.count && lane < 2 * L::MAX_PAGES && slot < per_tile && key0 + (slot << shift) < len)
           id = row[(key0 >> shift) + slot];
         return id < a.v.pages ? id : -1;
       };
@@ -409,7 +439,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
         }
         // K's scale as a factor; V's as its code, 0xFF for NaN and -1 for a page
         // that was not loaded (its codes must not be used)
-        if (lane < 16 && slot < per_tile) {
+        if (lane < 2 * L::MAX_PAGES && slot < per_tile) {
           uint32_t* pg = reinterpret_cast<uint32_t*>(gbase + L::PG_OFF + st * L::PG_STAGE);
           pg[2 * slot + (is_v ? 1 : 0)] =
               is_v ? (id0 >= 0 ? code : 0xFFFFFFFFu) : __float_as_uint(kv_scale_value(code));
@@ -441,12 +471,10 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
         const bool live = r < rows;
         const int token = live ? r / a.v.group : 0;
         const int qh = walk.head * a.v.group + (live ? r - token * a.v.group : 0);
-        const uint16_t* src = a.Q + (rq.q0 + token) * a.q_ts + qh * a.q_hs + t4 * (D / 4);
         uint32_t w[D / 8];
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (live) v = *reinterpret_cast<const uint4*>(src + 8 * c);
+          const uint4 v = raw_q[nr][c];
           w[4 * c] = v.x;
           w[4 * c + 1] = v.y;
           w[4 * c + 2] = v.z;
@@ -510,12 +538,14 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
         // the CTA's first segment and its last can be parts
         seg->slot = static_cast<int>(2 * cta + (first ? 0 : 1));
       }
-      // the unit goes on in other CTAs (stretch c is [total c / ctas, total
-      // (c + 1) / ctas)): say what joins it
+      // the unit goes on in other CTAs: say what joins it
       if (walk.begins && !walk.ends) {
         if (lane == 0) {
           join->live = min(ROWS, rows - walk.row_tile * ROWS);
-          join->parts = static_cast<int>((walk.unit_end * ctas - 1) / total - cta + 1);
+          const long long last = walk.unit_end - 1, edge = longer * (share + 1);
+          const long long c1 =
+              last < edge ? ka_div(last, share + 1) : longer + ka_div(last - edge, share);
+          join->parts = static_cast<int>(c1 - cta + 1);
           join->first_slot = static_cast<int>(2 * cta + (first ? 0 : 1));
         }
         if (lane < ROWS) join->out[lane] = out_of_lane;
@@ -598,22 +628,22 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
         ok = false;
       }
       ok = __all_sync(0xFFFFFFFFu, ok);
-      const int key0 = (tile0 + i) * KA_TK + warp * KA_KW;
-      if (ok && key0 < any_hi && key0 + KA_KW > any_lo) {
+      const int key0 = (tile0 + i) * TK + warp * KW;
+      if (ok && key0 < any_hi && key0 + KW > any_lo) {
         const uint32_t kt = base + st * 2 * L::TILE;
         const uint32_t vt = kt + L::TILE;
         const uint2* pg = reinterpret_cast<const uint2*>(gbase + L::PG_OFF + st * L::PG_STAGE);
-        const bool masked = key0 < all_lo || key0 + KA_KW > all_hi;
-        // ---- scores of two tiles of 16 keys: x[.][.][2 h + e] is key g + 8 h
+        const bool masked = key0 < all_lo || key0 + KW > all_hi;
+        // ---- scores of the warp's steps of 16 keys: x[.][.][2 h + e] is key g + 8 h
         // and row 2 t + e
-        float x[2][NR][4];
+        float x[KS][NR][4];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < KS; ++s) {
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[s][nr][e] = 0.0f;
-          const int key = warp * KA_KW + 16 * s + g;   // and key + 8: the same swizzle
+          const int key = warp * KW + 16 * s + g;   // and key + 8: the same swizzle
 #pragma unroll
           for (int c = 0; c < CHUNKS; ++c) {
             const int chunk = CHUNKS * t4 + c;
@@ -637,10 +667,10 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
         float mx[NR][2];
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) mx[nr][0] = mx[nr][1] = -INFINITY;
-        uint2 page[2];
+        uint2 page[KS];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          page[s] = pg[(warp * KA_KW + 16 * s) >> a.v.page_shift];
+        for (int s = 0; s < KS; ++s) {
+          page[s] = pg[(warp * KW + 16 * s) >> a.v.page_shift];
           if (page[s].y < 0xFFu) vnew = max(vnew, static_cast<int>(page[s].y));
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr)
@@ -691,9 +721,9 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
             }
           }
         }
-        // ---- probabilities and the product with V: two steps of 16 keys
+        // ---- probabilities and the product with V, a step of 16 keys at a time
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < KS; ++s) {
           const int code = static_cast<int>(page[s].y);
           const float vf = code == 0xFF || code < 0 ? __uint_as_float(0x7FC00000u)
                                                     : kv_exp2i(KA_P_EXP + code - ve);
@@ -722,7 +752,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
           uint32_t vw[4][W];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int key = warp * KA_KW + 16 * s + 2 * t4 + (r & 1) + 8 * (r >> 1);
+            const int key = warp * KW + 16 * s + 2 * t4 + (r & 1) + 8 * (r >> 1);
             if constexpr (D == 128) {
               const uint4 v = ld_shared_v4(vt + key * D + ((g ^ (key & 7)) << 4));
               vw[r][0] = v.x;
