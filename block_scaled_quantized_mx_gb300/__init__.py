@@ -584,27 +584,38 @@ class KVCut:
     counts: torch.Tensor
 
 
-def _int32(t: torch.Tensor, name: str, n: int | None = None):
-    if t.dtype != torch.int32 or not t.is_cuda or t.dim() != 1 or \
+# The cache's calls take a few microseconds on the GPU in a decoding step, less
+# than careful Python around them: shapes and strides are read once, and
+# dtypes looked up in tables.
+_i32 = torch.int32
+_KV_DTYPES = {torch.float16: DT_F16, torch.bfloat16: DT_BF16}
+_KV_OUT_DTYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16,
+                  torch.float16: DT_F16}
+
+
+def _int32(t: torch.Tensor, name: str, n: int = 0) -> int:
+    """Checks a vector of int32 values; its address."""
+    if t.dtype is not _i32 or not t.is_cuda or t.dim() != 1 or \
             not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous 1-D int32 CUDA tensor")
-    if n is not None and t.shape[0] < n:
+    if t.numel() < n:
         raise ValueError(f"{name} must hold {n} values")
+    return t.data_ptr()
 
 
-def _check_table(table: torch.Tensor, requests: int):
-    if table.dtype != torch.int32 or not table.is_cuda or table.dim() != 2 or \
-            table.shape[0] < requests:
+def _table(table: torch.Tensor, requests: int) -> tuple[int, int, int]:
+    """Checks a block table; its address, row stride and width."""
+    shape, stride = table.shape, table.stride()
+    if table.dtype is not _i32 or not table.is_cuda or len(shape) != 2 or \
+            shape[0] < requests:
         raise ValueError("table must be a 2-D int32 CUDA tensor with a row for "
                          "each request")
-    if table.shape[1] > 1 and table.stride(1) != 1:
+    width = shape[1]
+    if width > 1 and stride[1] != 1:
         raise ValueError("table must have a unit inner stride")
-
-
-def _row_stride(table: torch.Tensor) -> int:
     # the stride of a dimension of size 1 means nothing
-    return table.stride(0) if table.shape[0] > 1 else max(table.stride(0),
-                                                          table.shape[1])
+    return (table.data_ptr(),
+            stride[0] if shape[0] > 1 else max(stride[0], width), width)
 
 
 def mx_kv_extend(lens: torch.Tensor, new_tokens: torch.Tensor,
@@ -618,11 +629,11 @@ def mx_kv_extend(lens: torch.Tensor, new_tokens: torch.Tensor,
     max_tokens: the most new tokens there may be (the length of slots).  A
     request that finds no room, and every one behind it, is refused whole."""
     B = lens.shape[0]
-    _int32(lens, "lens")
-    _int32(new_tokens, "new_tokens", B)
-    _int32(stack, "stack")
-    _int32(count, "count", 1)
-    _check_table(table, B)
+    p_lens = _int32(lens, "lens")
+    p_new = _int32(new_tokens, "new_tokens", B)
+    p_stack = _int32(stack, "stack")
+    p_count = _int32(count, "count", 1)
+    p_table, stride, width = _table(table, B)
     if out is None:
         e = lens.new_empty
         out = KVPlan(e(B), e(B + 1), e(max_tokens, dtype=torch.int64), e(2))
@@ -634,9 +645,8 @@ def mx_kv_extend(lens: torch.Tensor, new_tokens: torch.Tensor,
                 not out.slots.is_contiguous() or out.slots.numel() < max_tokens:
             raise ValueError("out.slots must hold max_tokens int64 values")
     _check(lib().mx_kv_extend(
-        lens.data_ptr(), new_tokens.data_ptr(), B, table.data_ptr(),
-        _row_stride(table), table.shape[1], stack.data_ptr(), stack.shape[0],
-        count.data_ptr(), page, out.lens.data_ptr(), out.cu.data_ptr(),
+        p_lens, p_new, B, p_table, stride, width, p_stack, stack.numel(),
+        p_count, page, out.lens.data_ptr(), out.cu.data_ptr(),
         out.slots.data_ptr(), max_tokens, out.counts.data_ptr(),
         _stream(stream)), "mx_kv_extend")
     return out
@@ -650,38 +660,35 @@ def mx_kv_truncate(lens: torch.Tensor, keep: torch.Tensor, table: torch.Tensor,
     (in place) and their table entries become -1; an mx_kv_extend by as many
     tokens hands out the same pages again."""
     B = lens.shape[0]
-    _int32(lens, "lens")
-    _int32(keep, "keep", B)
-    _int32(stack, "stack")
-    _int32(count, "count", 1)
-    _check_table(table, B)
+    p_lens = _int32(lens, "lens")
+    p_keep = _int32(keep, "keep", B)
+    p_stack = _int32(stack, "stack")
+    p_count = _int32(count, "count", 1)
+    p_table, stride, width = _table(table, B)
     if out is None:
         out = KVCut(lens.new_empty(B), lens.new_empty(2))
     else:
         _int32(out.lens, "out.lens", B)
         _int32(out.counts, "out.counts", 2)
     _check(lib().mx_kv_truncate(
-        lens.data_ptr(), keep.data_ptr(), B, table.data_ptr(),
-        _row_stride(table), table.shape[1], stack.data_ptr(), stack.shape[0],
-        count.data_ptr(), page, out.lens.data_ptr(), out.counts.data_ptr(),
+        p_lens, p_keep, B, p_table, stride, width, p_stack, stack.numel(),
+        p_count, page, out.lens.data_ptr(), out.counts.data_ptr(),
         _stream(stream)), "mx_kv_truncate")
     return out
 
 
-def _kv_dtype(t: torch.Tensor, name: str) -> int:
-    if t.dtype not in (torch.float16, torch.bfloat16) or not t.is_cuda or \
-            t.dim() != 3:
+def _kv_tensor(t: torch.Tensor, name: str):
+    """Checks a tokens x heads x d tensor; its type's code, shape, token stride
+    and head stride (0 for a dimension of size 1, whose stride means
+    nothing)."""
+    dt, shape, stride = _KV_DTYPES.get(t.dtype), t.shape, t.stride()
+    if dt is None or not t.is_cuda or len(shape) != 3:
         raise ValueError(f"{name} must be a tokens x heads x d fp16 or bf16 "
                          "CUDA tensor")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    if stride[2] != 1 and shape[2] > 1:
         raise ValueError(f"{name} must have a unit inner stride")
-    return DT_F16 if t.dtype == torch.float16 else DT_BF16
-
-
-def _kv_strides(t: torch.Tensor) -> tuple[int, int]:
-    # strides of dimensions of size 1 mean nothing
-    return (t.stride(0) if t.shape[0] > 1 else 0,
-            t.stride(1) if t.shape[1] > 1 else 0)
+    return (dt, shape, stride[0] if shape[0] > 1 else 0,
+            stride[1] if shape[1] > 1 else 0)
 
 
 def mx_kv_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor,
@@ -690,19 +697,18 @@ def mx_kv_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor,
     cache, in place, at their slots (int64, one per token; negative: none).
     One power-of-two scale covers a page and head: where new tokens need a
     larger one than the page has, the codes already there are rounded again."""
-    dt = _kv_dtype(K, "K")
-    if V.dtype != K.dtype or V.shape != K.shape:
+    dt, shape, kt, kh = _kv_tensor(K, "K")
+    vdt, vshape, vt, vh = _kv_tensor(V, "V")
+    if vdt != dt or vshape != shape:
         raise ValueError("K and V must have one shape and type")
-    _kv_dtype(V, "V")
-    T = K.shape[0]
+    T, heads, d = shape
     c = cache.c()
-    if K.shape[1] != c.heads or K.shape[2] != c.d:
+    if heads != c.heads or d != c.d:
         raise ValueError("K and V must have the cache's heads and d")
     if slots.dtype != torch.int64 or not slots.is_cuda or slots.dim() != 1 or \
-            not slots.is_contiguous() or slots.shape[0] < T:
+            not slots.is_contiguous() or slots.numel() < T:
         raise ValueError("slots must be a contiguous int64 CUDA tensor, one "
                          "for each token")
-    (kt, kh), (vt, vh) = _kv_strides(K), _kv_strides(V)
     _check(lib().mx_kv_append(ctypes.byref(c), K.data_ptr(), V.data_ptr(), dt,
                               T, kt, kh, vt, vh, slots.data_ptr(),
                               _stream(stream)), "mx_kv_append")
@@ -731,30 +737,34 @@ def mx_kv_attention(Q: torch.Tensor, cache: KVCache, table: torch.Tensor,
     defaults to 1/sqrt(d), out_dtype to Q's.  With a device `workspace`
     (uint8, kv_attention_workspace_bytes() long) a request's keys are spread
     over many SMs.  Rows that belong to no request are not written."""
-    dt = _kv_dtype(Q, "Q")
-    T, Hq, d = Q.shape
+    dt, shape, qt, qh = _kv_tensor(Q, "Q")
+    T, Hq, d = shape
     c = cache.c()
     if d != c.d or Hq % c.heads:
         raise ValueError("Q must have the cache's d and a multiple of its heads")
     B = lens.shape[0]
-    _int32(lens, "lens")
-    _int32(cu, "cu", B + 1)
-    _check_table(table, B)
+    p_lens = _int32(lens, "lens")
+    p_cu = _int32(cu, "cu", B + 1)
+    p_table, stride, width = _table(table, B)
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=out_dtype or Q.dtype,
-                          device=Q.device)
-    elif (out.shape != Q.shape or not out.is_cuda or out.stride(2) != 1
+        out = torch.empty(shape, dtype=out_dtype or Q.dtype, device=Q.device)
+        ot, oh = Hq * d, d
+    elif (out.shape != shape or not out.is_cuda or out.stride(2) != 1
           or (out_dtype is not None and out.dtype != out_dtype)):
         raise ValueError("out must be a CUDA tensor of Q's shape and of type "
                          "out_dtype, with a unit inner stride")
-    odt = _out_code(out.dtype, (torch.float32, torch.bfloat16, torch.float16))
-    (qt, qh), (ot, oh) = _kv_strides(Q), _kv_strides(out)
+    else:
+        ot = out.stride(0) if T > 1 else 0
+        oh = out.stride(1) if Hq > 1 else 0
+    odt = _KV_OUT_DTYPES.get(out.dtype)
+    if odt is None:
+        raise ValueError("out_dtype must be float32, bfloat16 or float16, not "
+                         f"{out.dtype}")
     _check(lib().mx_kv_attention(
-        Q.data_ptr(), dt, T, Hq, qt, qh, ctypes.byref(c), table.data_ptr(),
-        _row_stride(table), table.shape[1], lens.data_ptr(), cu.data_ptr(), B,
-        max_q, out.data_ptr(), odt, ot, oh, int(bool(causal)), int(window),
-        1.0 / float(d) ** 0.5 if scale is None else float(scale),
-        workspace.data_ptr() if workspace is not None else None,
+        Q.data_ptr(), dt, T, Hq, qt, qh, ctypes.byref(c), p_table, stride,
+        width, p_lens, p_cu, B, max_q, out.data_ptr(), odt, ot, oh,
+        1 if causal else 0, window, d ** -0.5 if scale is None else scale,
+        None if workspace is None else workspace.data_ptr(),
         _nbytes(workspace), _stream(stream)), "mx_kv_attention")
     return out
 
