@@ -26,8 +26,17 @@
 //     list of all (request, row tile, cache head, key block)s per CTA, each
 //     unit standing with some entries more for what it costs to begin and end
 //     one; parts of units go to the workspace and a second kernel joins them.
-// Tensor memory as in attention.cu: S (then P) of tile t in columns [256 t,
-// 256 t + 128), its O behind.  Every mbarrier wait is bounded.
+//   * Q stands in tensor memory beside the scores: the product S = Q K^T then
+//     reads only K from shared memory.  With Q there too, that product alone
+//     asks for all of the port's 128 bytes a clock, and the conversion's writes
+//     wait for it.  Scores go 64 keys at a time (there is no room for 128);
+//     a block's operands, of 128 keys, serve two such steps.
+// Tensor memory, tile t: its scores (then P) in columns [256 t, 256 t + 64), Q
+// in [256 t + 64, 256 t + 64 + d / 2), O in [256 t + 128, 256 t + 128 + d).
+// Ordering: the MMA warp issues a step's P V before the next step's scores,
+// and a commit covers every earlier operation of its thread: once scores are
+// complete so is the product that read P and accumulated into O.  Every
+// mbarrier wait is bounded.
 #include <algorithm>
 #include <atomic>
 
@@ -46,6 +55,7 @@ __device__ unsigned int g_status_kvp = 0;
 constexpr int KP_BQ = 128;                 // rows per tile
 constexpr int KP_ROWS = 2 * KP_BQ;         // rows of a unit
 constexpr int KP_BK = 128;                 // keys per block
+constexpr int KP_HK = 64;                  // keys per step of the softmax, two to a block
 constexpr int KP_THREADS = 512;            // pages and MMA, two softmax warpgroups, conversion
 constexpr int KP_WARPS = KP_THREADS / 32;
 // Registers: launched at 128; 72 * 128 + 176 * 256 + 88 * 128 = 65536.
@@ -57,6 +67,7 @@ constexpr float KP_LAZY = 8.0f;            // slack of the exponentials' referen
 constexpr int KP_P_EXP = 7;                // P is scaled by 2^7: at most 2^(7 + 8) in f16
 constexpr int KP_OVER = 4;                 // entries of a unit besides its blocks
 constexpr int KP_PG = 8;                   // blocks whose page data is kept
+constexpr int KP_STAGES = 3;               // tiles of K, and of V
 constexpr int KP_MAX_REQUESTS = 16384;
 
 // One block: for each 16 of its keys the scales and where the codes are.
@@ -165,25 +176,22 @@ struct KpWalk {
 template <int D>
 struct KpSmem {
   static constexpr int REGION = 128 * 128;
-  static constexpr int Q_BYTES = (D / 64) * REGION;
   static constexpr int K_BYTES = (D / 64) * REGION;       // V's tiles are alike
   static constexpr int V_BYTES = K_BYTES;
-  static constexpr int Q_OFF = 0;
-  static constexpr int K_OFF = Q_OFF + 2 * Q_BYTES;
-  static constexpr int V_OFF = K_OFF + 2 * K_BYTES;
-  static constexpr int PG_OFF = V_OFF + 2 * V_BYTES;
+  static constexpr int K_OFF = 0;
+  static constexpr int V_OFF = K_OFF + KP_STAGES * K_BYTES;
+  static constexpr int PG_OFF = V_OFF + KP_STAGES * V_BYTES;
   static constexpr int SEG_OFF = PG_OFF + KP_PG * static_cast<int>(sizeof(KpPages));
   static constexpr int BAR_OFF = SEG_OFF + 2 * static_cast<int>(sizeof(KpSeg));
-  // q_full[2], k_full[2], v_full[2], k_empty[2], v_empty[2], s_full[2],
-  // p_full[2 tiles][2 halves], o_done[2], seg_full[2], seg_empty[2],
-  // pg_full[8], pg_empty[8]
-  static constexpr int BARS = 2 + 8 + 2 + 4 + 2 + 4 + 2 * KP_PG;
+  // k_full, v_full, k_empty, v_empty [stages]; q_full, s_full, p_full, o_done
+  // [tile]; seg_full[2], seg_empty[2], pg_full[8], pg_empty[8]
+  static constexpr int BARS = 4 * KP_STAGES + 8 + 4 + 2 * KP_PG;
   static constexpr int MISC_OFF = BAR_OFF + BARS * 8;
   static constexpr int WALK_OFF = MISC_OFF + 16;
   static constexpr int TOTAL = WALK_OFF + static_cast<int>(sizeof(KpWalk));
   static constexpr int ALLOC = TOTAL + 1024;
   static_assert(ALLOC <= 232448, "shared memory budget");
-  static_assert(V_OFF >= KP_MAX_REQUESTS * 4, "the plan's array fits before V");
+  static_assert(PG_OFF >= KP_MAX_REQUESTS * 4, "the plan's array fits in the operand tiles");
 };
 
 struct KpArgs {
@@ -211,22 +219,64 @@ __device__ __forceinline__ uint32_t kp_idesc(uint32_t n, uint32_t b_mn) {
   return (1u << 4) | (b_mn << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// The MMA warp runs its loop with all 32 lanes (warp-uniform descriptors); one
-// elected lane issues.
-__device__ __forceinline__ void kp_mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t id,
-                                          uint32_t acc) {
+// Whole products in one statement each.  The MMA warp runs them with all 32
+// lanes, so that the descriptors stay warp-uniform, and one elected lane
+// issues; the election and the predicates are made once per product, and of
+// the descriptors only the low words (start addresses) move.  Issued one by
+// one, with an election each, the instructions around them took longer than
+// the products.
+//
+// Both products read their first operand from tensor memory (16 values of a
+// row are 8 columns).  S = Q K^T: D / 16 steps of 16 along the 128-byte rows of
+// K, whose regions of 64 values lie 16 KB apart.
+template <int D>
+__device__ __forceinline__ void kp_issue_s(uint32_t d, uint32_t q, uint64_t b, uint32_t id) {
+  const uint32_t b0 = static_cast<uint32_t>(b), b1 = static_cast<uint32_t>(b >> 32);
   asm volatile(
-      "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a_tmem), "l"(b), "r"(id), "r"(acc)
+      "{\n\t.reg .pred e, no, yes;\n\t.reg .b32 x, y;\n\t.reg .b64 db;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 no, 0, 0;\n\tsetp.eq.b32 yes, 0, 0;\n\t"
+      "add.u32 x, %1, 0;\n\tadd.u32 y, %2, 0;\n\tmov.b64 db, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, no;\n\t"
+      "add.u32 x, %1, 8;\n\tadd.u32 y, %2, 2;\n\tmov.b64 db, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, yes;\n\t"
+      "add.u32 x, %1, 16;\n\tadd.u32 y, %2, 4;\n\tmov.b64 db, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, yes;\n\t"
+      "add.u32 x, %1, 24;\n\tadd.u32 y, %2, 6;\n\tmov.b64 db, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, yes;\n\t"
+      "}" ::"r"(d), "r"(q), "r"(b0), "r"(b1), "r"(id)
       : "memory");
+  if constexpr (D == 128)
+    asm volatile(
+        "{\n\t.reg .pred e, yes;\n\t.reg .b32 x, y;\n\t.reg .b64 db;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.eq.b32 yes, 0, 0;\n\t"
+        "add.u32 x, %1, 32;\n\tadd.u32 y, %2, 1024;\n\tmov.b64 db, {y, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, yes;\n\t"
+        "add.u32 x, %1, 40;\n\tadd.u32 y, %2, 1026;\n\tmov.b64 db, {y, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, yes;\n\t"
+        "add.u32 x, %1, 48;\n\tadd.u32 y, %2, 1028;\n\tmov.b64 db, {y, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, yes;\n\t"
+        "add.u32 x, %1, 56;\n\tadd.u32 y, %2, 1030;\n\tmov.b64 db, {y, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, yes;\n\t"
+        "}" ::"r"(d), "r"(q), "r"(b0), "r"(b1), "r"(id)
+        : "memory");
 }
-__device__ __forceinline__ void kp_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
-                                          uint32_t acc) {
+// O += P V over 64 keys: four steps, V's rows 2 KB apart per step; acc 0: O is
+// overwritten.
+__device__ __forceinline__ void kp_issue_pv(uint32_t d, uint32_t p, uint64_t b, uint32_t id,
+                                            uint32_t acc) {
+  const uint32_t b0 = static_cast<uint32_t>(b), b1 = static_cast<uint32_t>(b >> 32);
   asm volatile(
-      "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(acc)
+      "{\n\t.reg .pred e, first, yes;\n\t.reg .b32 x, y;\n\t.reg .b64 db;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 first, %5, 0;\n\tsetp.eq.b32 yes, 0, 0;\n\t"
+      "add.u32 x, %1, 0;\n\tadd.u32 y, %2, 0;\n\tmov.b64 db, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, first;\n\t"
+      "add.u32 x, %1, 8;\n\tadd.u32 y, %2, 128;\n\tmov.b64 db, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, yes;\n\t"
+      "add.u32 x, %1, 16;\n\tadd.u32 y, %2, 256;\n\tmov.b64 db, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, yes;\n\t"
+      "add.u32 x, %1, 24;\n\tadd.u32 y, %2, 384;\n\tmov.b64 db, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, yes;\n\t"
+      "}" ::"r"(d), "r"(p), "r"(b0), "r"(b1), "r"(id), "r"(acc)
       : "memory");
 }
 __device__ __forceinline__ void kp_commit(uint32_t bar) {
@@ -291,14 +341,14 @@ kv_prompt_kernel(const KpArgs a) {
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
-  const uint32_t bar_q = base + L::BAR_OFF;
-  const uint32_t bar_k = bar_q + 16;
-  const uint32_t bar_v = bar_k + 16;
-  const uint32_t bar_k_empty = bar_v + 16;
-  const uint32_t bar_v_empty = bar_k_empty + 16;
-  const uint32_t bar_s_full = bar_v_empty + 16;
-  const uint32_t bar_p_full = bar_s_full + 16;     // [tile][half]
-  const uint32_t bar_o_done = bar_p_full + 32;
+  const uint32_t bar_k = base + L::BAR_OFF;
+  const uint32_t bar_v = bar_k + 8 * KP_STAGES;
+  const uint32_t bar_k_empty = bar_v + 8 * KP_STAGES;
+  const uint32_t bar_v_empty = bar_k_empty + 8 * KP_STAGES;
+  const uint32_t bar_q = bar_v_empty + 8 * KP_STAGES;
+  const uint32_t bar_s_full = bar_q + 16;
+  const uint32_t bar_p_full = bar_s_full + 16;
+  const uint32_t bar_o_done = bar_p_full + 16;
   const uint32_t bar_seg = bar_o_done + 16;
   const uint32_t bar_seg_empty = bar_seg + 16;
   const uint32_t bar_pg = bar_seg_empty + 16;      // [KP_PG]
@@ -393,15 +443,16 @@ kv_prompt_kernel(const KpArgs a) {
   __syncthreads();
 
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar_q + 8 * i, 4);
+    for (int i = 0; i < KP_STAGES; ++i) {
       mbar_init(bar_k + 8 * i, 4);
       mbar_init(bar_v + 8 * i, 4);
       mbar_init(bar_k_empty + 8 * i, 1);
       mbar_init(bar_v_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_q + 8 * i, 4);
       mbar_init(bar_s_full + 8 * i, 1);
-      mbar_init(bar_p_full + 16 * i, 4);
-      mbar_init(bar_p_full + 16 * i + 8, 4);
+      mbar_init(bar_p_full + 8 * i, 4);
       mbar_init(bar_o_done + 8 * i, 1);
       mbar_init(bar_seg + 8 * i, 1);
       mbar_init(bar_seg_empty + 8 * i, 9);
@@ -540,12 +591,11 @@ kv_prompt_kernel(const KpArgs a) {
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
-      const uint32_t id_qk = kp_idesc(KP_BK, 0);
+      const uint32_t id_qk = kp_idesc(KP_HK, 0);
       const uint32_t id_pv = kp_idesc(D, 1);
-      const uint64_t dq0 = smem_desc(base + L::Q_OFF, 16, 1024, 2);
       const uint64_t dk0 = smem_desc(base + L::K_OFF, 16, 1024, 2);
       const uint64_t dv0 = smem_desc(base + L::V_OFF, L::REGION, 1024, 2);
-      int bt = 0, bt1 = 0, seg_it = 0, seg1 = 0;
+      int bt = 0, seg_it = 0, seg1 = 0;      // blocks, units, tile 1's units
       bool ok = true;
       while (ok) {
         const int ss = seg_it & 1;
@@ -559,71 +609,53 @@ kv_prompt_kernel(const KpArgs a) {
         const int tiles = live > KP_BQ ? 2 : 1;
         ++seg_it;
         // tile 1 sits a unit of up to 128 rows out: its barriers count its own
-        // units and blocks
+        // units (steps are even in number per unit)
         for (int t = 0; t < tiles && ok; ++t) {
           ok = mbar_wait(bar_q + 8 * t, (t ? seg1 : seg_it - 1) & 1, abort);
           if (!ok) kp_timeout(abort, 0x57);
         }
         if (!ok) break;
         tc_fence_after();
-        for (int j = 0; j <= nkb && ok; ++j) {
-          for (int t = 0; t < tiles && ok; ++t) {
-            const uint32_t s_t = tmem_base + 256 * t;
-            const uint32_t o_t = s_t + 128;
-            if (j >= 1) {
-              const int g = bt + j - 1, st = g & 1;
-              const uint32_t pp = ((t ? bt1 : bt) + j - 1) & 1;
-              if (!mbar_wait(bar_p_full + 16 * t, pp, abort) ||
-                  !mbar_wait(bar_v + 8 * st, (g >> 1) & 1, abort)) {
-                kp_timeout(abort, 0x58);
+        // step h: P_h V_h, then the next step's scores over P_h
+        const int steps = 2 * nkb;
+#pragma unroll 1
+        for (int h = -1; h < steps && ok; ++h) {
+          const int n = h + 1;
+          const int sv = (bt + (h >> 1)) % KP_STAGES, sk = (bt + (n >> 1)) % KP_STAGES;
+          const uint64_t dv = dv0 + static_cast<uint64_t>((sv * L::V_BYTES + (h & 1) * 8192) >> 4);
+          const uint64_t dk = dk0 + static_cast<uint64_t>((sk * L::K_BYTES + (n & 1) * 8192) >> 4);
+          if (h >= 0 && !(h & 1))
+            ok = mbar_wait(bar_v + 8 * sv, ((bt + (h >> 1)) / KP_STAGES) & 1, abort);
+          if (n < steps && !(n & 1))
+            ok = ok && mbar_wait(bar_k + 8 * sk, ((bt + (n >> 1)) / KP_STAGES) & 1, abort);
+          if (!ok) {
+            kp_timeout(abort, 0x58);
+            break;
+          }
+#pragma unroll 1
+          for (int t = 0; t < tiles; ++t) {
+            const uint32_t s_t = tmem_base + 256 * t;        // S, then P; Q behind it, then O
+            if (h >= 0) {
+              if (!mbar_wait(bar_p_full + 8 * t, h & 1, abort)) {
+                kp_timeout(abort, 0x59);
                 ok = false;
                 break;
               }
               tc_fence_after();
-#pragma unroll
-              for (int kk = 0; kk < KP_BK / 16; ++kk) {
-                if (kk == KP_BK / 32) {
-                  if (!mbar_wait(bar_p_full + 16 * t + 8, pp, abort)) {
-                    kp_timeout(abort, 0x59);
-                    ok = false;
-                    break;
-                  }
-                  tc_fence_after();
-                }
-                kp_mma_ts(o_t, s_t + 8 * kk,
-                          dv0 + static_cast<uint64_t>((st * L::V_BYTES + kk * 2048) >> 4), id_pv,
-                          (j > 1 || kk > 0) ? 1u : 0u);
-              }
-              if (!ok) break;
-              if (t == tiles - 1) kp_commit(bar_v_empty + 8 * st);
+              kp_issue_pv(s_t + 128, s_t, dv, id_pv, h > 0 ? 1u : 0u);
+              if (n == steps) kp_commit(bar_o_done + 8 * t);
             }
-            if (j < nkb) {
-              const int g = bt + j, st = g & 1;
-              if (!mbar_wait(bar_k + 8 * st, (g >> 1) & 1, abort)) {
-                kp_timeout(abort, 0x5a);
-                ok = false;
-                break;
-              }
+            if (n < steps) {
               tc_fence_after();
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * L::REGION + (kk & 3) * 32;
-                kp_mma_ss(s_t, dq0 + static_cast<uint64_t>((t * L::Q_BYTES + off) >> 4),
-                          dk0 + static_cast<uint64_t>((st * L::K_BYTES + off) >> 4), id_qk,
-                          kk > 0 ? 1u : 0u);
-              }
+              kp_issue_s<D>(s_t, s_t + 64, dk, id_qk);
               kp_commit(bar_s_full + 8 * t);
-              if (t == tiles - 1) kp_commit(bar_k_empty + 8 * st);
-            } else {
-              kp_commit(bar_o_done + 8 * t);
             }
           }
+          if (h >= 0 && (h & 1)) kp_commit(bar_v_empty + 8 * sv);
+          if (n < steps && (n & 1)) kp_commit(bar_k_empty + 8 * sk);
         }
         bt += nkb;
-        if (tiles == 2) {
-          bt1 += nkb;
-          ++seg1;
-        }
+        seg1 += tiles - 1;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_seg_empty + 8 * ss);
       }
@@ -690,7 +722,7 @@ kv_prompt_kernel(const KpArgs a) {
     // tile's codes as soon as it is converted
 #pragma unroll 1
     for (int tile = 0; pg; ++tile) {
-      const int kv = tile & 1, bt = tile >> 1, st = bt & 1;
+      const int kv = tile & 1, bt = tile >> 1, st = bt % KP_STAGES;
       const KpPages* next = pg;              // of the next tile: V, or the next block's K
       if (kv == 1 && pg->more == 0) {
         next = nullptr;
@@ -702,7 +734,7 @@ kv_prompt_kernel(const KpArgs a) {
       const uint32_t dst = base + (kv ? L::V_OFF : L::K_OFF) + st * L::K_BYTES;
       // keys behind the request's end count as zeros in V, whatever stands there
       const int valid = kv ? pg->valid : KP_BK;
-      if (!mbar_wait((kv ? bar_v_empty : bar_k_empty) + 8 * st, ((bt >> 1) & 1) ^ 1, abort)) {
+      if (!mbar_wait((kv ? bar_v_empty : bar_k_empty) + 8 * st, ((bt / KP_STAGES) & 1) ^ 1, abort)) {
         if (lane == 0) kp_timeout(abort, 0x54);
         break;
       }
@@ -727,8 +759,7 @@ kv_prompt_kernel(const KpArgs a) {
     const int quarter = warp & 3;
     const int urow = KP_BQ * t + 32 * quarter + lane;       // row in the unit
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + 256 * t;
-    // blocks of the tile's own barriers (tile 1 may sit units out) and of all
-    int bt = 0, own = 0, own_seg = 0, seg_it = 0;
+    int bt = 0, own_seg = 0, seg_it = 0;     // blocks, the tile's own units, all units
     bool ok = true;
     while (ok) {
       const int ss = seg_it & 1;
@@ -783,13 +814,13 @@ kv_prompt_kernel(const KpArgs a) {
 #pragma unroll
           for (int e = 0; e < D / 2; ++e) w[e] ^= 0x80008000u;
         }
-        const int r = 32 * quarter + lane;
+        // the row's D / 2 columns behind the scores
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          st_shared_v4(base + L::Q_OFF + t * L::Q_BYTES + (c >> 3) * L::REGION + r * 128 +
-                           (((c & 7) ^ (r & 7)) << 4),
-                       w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-        fence_proxy_async_smem();
+        for (int c = 0; c < D / 64; ++c)
+          tmem_st_32x32b_x32(lane_addr + 64 + 32 * c,
+                             *reinterpret_cast<const uint32_t(*)[32]>(w + 32 * c));
+        tmem_wait_st();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_q + 8 * t);
       }
@@ -802,77 +833,70 @@ kv_prompt_kernel(const KpArgs a) {
 
       float m = -INFINITY, l = 0.0f;
       int ev = 0;                              // V's reference exponent
-      for (int j = 0; j < count; ++j) {
-        const int g = bt + j, key0 = key00 + j * KP_BK, ps = g & (KP_PG - 1);
+#pragma unroll 1
+      for (int h = 0; h < 2 * count; ++h) {
+        const int g = bt + (h >> 1), ps = g & (KP_PG - 1);
+        const int key0 = key00 + KP_HK * h;
         if (!mbar_wait(bar_pg + 8 * ps, (g / KP_PG) & 1, abort) ||
-            (works && !mbar_wait(bar_s_full + 8 * t, own & 1, abort))) {
+            (works && !mbar_wait(bar_s_full + 8 * t, h & 1, abort))) {
           if (lane == 0) kp_timeout(abort, 0x5c);
           ok = false;
           break;
         }
         if (!works) {                          // the tile has no rows: only say so
-          if (lane == 0) mbar_arrive(bar_pg_empty + 8 * ps);
+          if (lane == 0 && (h & 1)) mbar_arrive(bar_pg_empty + 8 * ps);
           continue;
         }
-        ++own;
         tc_fence_after();
         const KpPages* pg = reinterpret_cast<const KpPages*>(gbase + L::PG_OFF) + ps;
+        const int p0 = 4 * (h & 1);            // the step's first 16 keys in the block
         const int ev_new = max(ev, pg->top);
+        uint32_t x0[32], x1[32];
+        tmem_ld_32x32b_x32(lane_addr, x0);
+        tmem_ld_32x32b_x32(lane_addr + 32, x1);
+        tmem_wait_ld();
         // Row maximum: of the raw scores of each 16 keys, times their factor.
-        // A block that some row does not see whole is scaled and masked first:
-        // what is hidden may stand in a page whose factor is NaN.  The scores
-        // are read 32 at a time, a load ahead, here and again for the
-        // exponentials, in loops: unrolled with all 128 in registers, the code
-        // of the roles crowded the MMA warp's out of the instruction cache.
-        const bool masked = key0 < all_lo || key0 + KP_BK > all_hi;
-        // scales keys 32 c .. 32 c + 31 and hides what the row does not see
-        auto hide = [&](uint32_t (&x)[32], int c) {
-          const int k0 = key0 + 32 * c;
-          const float f0 = fr * pg->of[2 * c].kf, f1 = fr * pg->of[2 * c + 1].kf;
+        // A step that some row does not see whole is scaled and masked first:
+        // what is hidden may stand in a page whose factor is NaN.
+        const bool masked = key0 < all_lo || key0 + KP_HK > all_hi;
+        float f[4];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float y = __uint_as_float(x[e]) * (e < 16 ? f0 : f1);
-            x[e] = k0 + e >= lo && k0 + e < hi ? __float_as_uint(y) : 0xFF800000u;   // -inf
+        for (int p = 0; p < 4; ++p) f[p] = fr * pg->of[p0 + p].kf;
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < KP_HK; ++e) {
+            uint32_t& x = e < 32 ? x0[e & 31] : x1[e & 31];
+            const float y = __uint_as_float(x) * f[e >> 4];
+            x = key0 + e >= lo && key0 + e < hi ? __float_as_uint(y) : 0xFF800000u;   // -inf
           }
-        };
+#pragma unroll
+          for (int p = 0; p < 4; ++p) f[p] = 1.0f;
+        }
         float mx = -INFINITY;
-        auto top_of = [&](uint32_t (&x)[32], int c) {
-          if (masked) hide(x, c);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float g0 = -INFINITY, g1 = -INFINITY;
+        for (int p = 0; p < 4; ++p) {
+          const uint32_t(&x)[32] = p < 2 ? x0 : x1;
+          float g0 = -INFINITY, g1 = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              g0 = max3(g0, __uint_as_float(x[16 * h + e]), __uint_as_float(x[16 * h + e + 1]));
-              g1 = max3(g1, __uint_as_float(x[16 * h + e + 2]), __uint_as_float(x[16 * h + e + 3]));
-            }
-            mx = fmaxf(mx, fmaxf(g0, g1) * (masked ? 1.0f : fr * pg->of[2 * c + h].kf));
+          for (int e = 0; e < 16; e += 4) {
+            const int i = 16 * (p & 1) + e;
+            g0 = max3(g0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+            g1 = max3(g1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
           }
-        };
-        uint32_t sa[32], sb[32];
-        tmem_ld_32x32b_x32(lane_addr, sa);
-#pragma unroll 1
-        for (int c = 0; c < 4; c += 2) {
-          tmem_wait_ld();
-          tmem_ld_32x32b_x32(lane_addr + 32 * c + 32, sb);
-          top_of(sa, c);
-          tmem_wait_ld();
-          // the next two; at the end the first 32 again, for the exponentials
-          tmem_ld_32x32b_x32(lane_addr + ((32 * c + 64) & 127), sa);
-          top_of(sb, c + 1);
+          mx = fmaxf(mx, fmaxf(g0, g1) * f[p]);
         }
         const float m_new = mx > m + KP_LAZY ? mx : m;
         const float alpha = m_new == m ? 1.0f : ex2_approx(m - m_new);
-        if (j >= 1 && __any_sync(0xFFFFFFFFu, m_new != m || ev_new != ev)) {
-          tmem_wait_ld();                      // sa's load
-          const float f = alpha * kv_exp2i(ev - ev_new);
+        if (h >= 1 && __any_sync(0xFFFFFFFFu, m_new != m || ev_new != ev)) {
+          // (the product that last wrote O ended before these scores did)
+          const float by = alpha * kv_exp2i(ev - ev_new);
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
             tmem_ld_32x32b_x32(lane_addr + 128 + 32 * c, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
             tmem_st_32x32b_x32(lane_addr + 128 + 32 * c, o);
           }
         }
@@ -883,52 +907,42 @@ kv_prompt_kernel(const KpArgs a) {
         // to f16 and written back over the scores; the sum takes b out again.
         // Hidden scores are -inf and stay it: b and m_use are finite.
         const float m_use = m == -INFINITY ? 0.0f : m;
-        auto exps = [&](uint32_t (&x)[32], int c) {
-          if (masked) hide(x, c);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t(&x)[32] = c ? x1 : x0;
           uint32_t pk[16];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int p = 2 * c + h;
-            const int b = max(-60, pg->of[p].ve + (KP_P_EXP - ev));
-            const float f = masked ? 1.0f : fr * pg->of[p].kf;
+          for (int q = 0; q < 2; ++q) {
+            const int p = 2 * c + q;
+            const int b = max(-60, pg->of[p0 + p].ve + (KP_P_EXP - ev));
             // b as a float: 1.5 * 2^23 + b, less 1.5 * 2^23
             const float nm = (__int_as_float(0x4B400000 + b) - 12582912.0f) - m_use;
-            const uint64_t f2 = pack2(f, f), nm2 = pack2(nm, nm);
+            const uint64_t f2 = pack2(f[p], f[p]), nm2 = pack2(nm, nm);
             uint64_t sum = pack2(0.0f, 0.0f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              float x0, x1;
-              unpack2(fma2(pack2(__uint_as_float(x[16 * h + 2 * e]),
-                                 __uint_as_float(x[16 * h + 2 * e + 1])),
+              float y0, y1;
+              unpack2(fma2(pack2(__uint_as_float(x[16 * q + 2 * e]),
+                                 __uint_as_float(x[16 * q + 2 * e + 1])),
                            f2, nm2),
-                      x0, x1);
-              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-              pk[8 * h + e] = cvt_f16x2(p0, p1);
-              sum = add2(sum, pack2(p0, p1));
+                      y0, y1);
+              const float e0 = ex2_approx(y0), e1 = ex2_approx(y1);
+              pk[8 * q + e] = cvt_f16x2(e0, e1);
+              sum = add2(sum, pack2(e0, e1));
             }
             float a0, a1;
             unpack2(sum, a0, a1);
             l = fmaf(a0 + a1, __int_as_float((127 - b) << 23), l);
           }
           tmem_st_32x32b_x16(lane_addr + 16 * c, pk);
-        };
-        auto written = [&](int half) {
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_p_full + 16 * t + 8 * half);
-        };
-#pragma unroll 1
-        for (int c = 0; c < 4; c += 2) {
-          tmem_wait_ld();
-          tmem_ld_32x32b_x32(lane_addr + 32 * c + 32, sb);
-          exps(sa, c);
-          tmem_wait_ld();
-          if (c == 0) tmem_ld_32x32b_x32(lane_addr + 64, sa);
-          exps(sb, c + 1);
-          written(c >> 1);                     // 64 keys of P: their product may start
         }
-        if (lane == 0) mbar_arrive(bar_pg_empty + 8 * ps);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar_p_full + 8 * t);
+          if (h & 1) mbar_arrive(bar_pg_empty + 8 * ps);
+        }
       }
       bt += count;
       if (!ok) break;
