@@ -1039,8 +1039,14 @@ cudaError_t ka_run_f(int64_t d, int nr, const CUtensorMap& tk, const CUtensorMap
 
 namespace {
 
-// More rows of one request and cache head than this go to the prompt kernel.
-constexpr int64_t KA_MOST_ROWS = 16;
+// Which kernel: the one in this file reads a request's keys once per 16 rows of
+// a cache head, the prompt kernel once per 256 but with more to set up and a
+// longer way from one step to the next.  Measured with 8 cache heads of 128
+// values (this kernel against the prompt kernel): 32 rows, 1 request of 2000
+// keys 14 against 21 us, of 32000 37 against 45, 16 requests of 6000 87
+// against 96, 64 of 6000 455 against 331; 48 rows, 1 of 32000 48 against 45,
+// 16 of 6000 134 against 106, 64 of 6000 676 against 353.
+constexpr int64_t KA_MOST_ROWS = 32;
 bool many_rows(int64_t max_q, int64_t group) { return max_q * group > KA_MOST_ROWS; }
 
 }  // namespace

@@ -7,15 +7,14 @@
 // r / group, head r % group of the group, so that all heads of a group share
 // the converted keys), in two tiles of 128 that take turns on the tensor core
 // as in attention.cu.  What differs from dense attention:
-//   * K and V come as codes.  Warp 0 reads the block table and the scales,
-//     some blocks of 128 keys ahead; four warps read the codes from global
-//     memory straight into registers (a tile ahead: a converted chunk's
-//     registers take the next tile's codes at once), turn them into f16 --
-//     exactly, for all three formats -- and write the swizzled operand tiles,
-//     two deep each.  The conversion of a block serves both tiles and, through
-//     the rows' order, all heads of the group.  (Codes staged in shared memory
-//     by TMA cost its port 64 KB more a block, which the operands of the
-//     products already load by 192 KB, and a load's latency per tile.);
+//   * K and V come as codes.  Warp 0 reads the block table and the scales and
+//     loads the codes of blocks of 128 keys page by page with TMA, up to three
+//     blocks ahead; four warps turn them into f16 -- exactly, for all three
+//     formats -- and write the swizzled operand tiles, two deep each.  The
+//     conversion of a block serves both tiles and, through the rows' order, all
+//     heads of the group.  (Read from global memory straight into the
+//     converting warps' registers, a tile ahead, a block took 2.2 us to convert,
+//     whatever its products took.)
 //   * page scales stay out of the operands: K's is a factor of the scores of
 //     its 16 .. 128 keys, applied with the softmax scale in the exponent's FMA;
 //     V's, a power of two relative to the largest so far, is added to the
@@ -37,6 +36,8 @@
 // and a commit covers every earlier operation of its thread: once scores are
 // complete so is the product that read P and accumulated into O.  Every
 // mbarrier wait is bounded.
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <atomic>
 
@@ -67,20 +68,20 @@ constexpr float KP_LAZY = 8.0f;            // slack of the exponentials' referen
 constexpr int KP_P_EXP = 7;                // P is scaled by 2^7: at most 2^(7 + 8) in f16
 constexpr int KP_OVER = 4;                 // entries of a unit besides its blocks
 constexpr int KP_PG = 8;                   // blocks whose page data is kept
-constexpr int KP_STAGES = 3;               // tiles of K, and of V
+constexpr int KP_STAGES = 2;               // f16 tiles of K, and of V
+constexpr int KP_RAW = 6;                  // tiles of codes, K and V in turn
 constexpr int KP_MAX_REQUESTS = 16384;
 
-// One block: for each 16 of its keys the scales and where the codes are.
+// One block: the scales of each 16 of its keys, and what there is of it.
 struct KpPages {
   struct {
     float kf;                              // K's scale; NaN where K's or V's is NaN or no page is
     int ve;                                // V's scale code; 0 there
   } of[8];
-  long long at[8];                         // the 16 keys' first code in both planes, -1: no page
   int top;                                 // the largest ve; -1: no block at all
   int valid;                               // keys of the block in front of the request's end
   int more;                                // another block follows
-  int pad;
+  int gone;                                // a bit for each 16 keys whose page was not loaded
 };
 
 // One CTA's part of a unit, as every role sees it.
@@ -180,12 +181,15 @@ struct KpSmem {
   static constexpr int V_BYTES = K_BYTES;
   static constexpr int K_OFF = 0;
   static constexpr int V_OFF = K_OFF + KP_STAGES * K_BYTES;
-  static constexpr int PG_OFF = V_OFF + KP_STAGES * V_BYTES;
+  static constexpr int RAW_BYTES = KP_BK * D;
+  static constexpr int RAW_OFF = V_OFF + KP_STAGES * V_BYTES;
+  static constexpr int PG_OFF = RAW_OFF + KP_RAW * RAW_BYTES;
   static constexpr int SEG_OFF = PG_OFF + KP_PG * static_cast<int>(sizeof(KpPages));
   static constexpr int BAR_OFF = SEG_OFF + 2 * static_cast<int>(sizeof(KpSeg));
   // k_full, v_full, k_empty, v_empty [stages]; q_full, s_full, p_full, o_done
-  // [tile]; seg_full[2], seg_empty[2], pg_full[8], pg_empty[8]
-  static constexpr int BARS = 4 * KP_STAGES + 8 + 4 + 2 * KP_PG;
+  // [tile]; seg_full[2], seg_empty[2], pg_full[8], pg_empty[8]; raw_full,
+  // raw_empty [KP_RAW]
+  static constexpr int BARS = 4 * KP_STAGES + 8 + 4 + 2 * KP_PG + 2 * KP_RAW;
   static constexpr int MISC_OFF = BAR_OFF + BARS * 8;
   static constexpr int WALK_OFF = MISC_OFF + 16;
   static constexpr int TOTAL = WALK_OFF + static_cast<int>(sizeof(KpWalk));
@@ -197,8 +201,6 @@ struct KpSmem {
 struct KpArgs {
   KvView v;
   const uint16_t* Q;
-  const uint8_t* k;
-  const uint8_t* v_codes;
   void* O;
   long long q_ts, q_hs, o_ts, o_hs;
   int bf16;
@@ -335,7 +337,8 @@ __device__ __forceinline__ long long kp_scan(long long v, long long* sm, long lo
 
 template <int FMT, int D>
 __global__ void __launch_bounds__(KP_THREADS, 1)
-kv_prompt_kernel(const KpArgs a) {
+kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                 const KpArgs a) {
   using L = KpSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -353,6 +356,8 @@ kv_prompt_kernel(const KpArgs a) {
   const uint32_t bar_seg_empty = bar_seg + 16;
   const uint32_t bar_pg = bar_seg_empty + 16;      // [KP_PG]
   const uint32_t bar_pg_empty = bar_pg + 8 * KP_PG;
+  const uint32_t bar_raw = bar_pg_empty + 8 * KP_PG;
+  const uint32_t bar_raw_empty = bar_raw + 8 * KP_RAW;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::MISC_OFF);
   volatile int* abort = reinterpret_cast<volatile int*>(gbase + L::MISC_OFF + 4);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -438,7 +443,7 @@ kv_prompt_kernel(const KpArgs a) {
     if (tid == 0 && join) join->live = 0;
     if (blockIdx.x >= ctas) return;          // the whole CTA: nothing was started
   }
-  // the regions go to their owners, the tensor core among them
+  // the regions go to their owners, TMA and the tensor core among them
   fence_proxy_async_smem();
   __syncthreads();
 
@@ -461,8 +466,14 @@ kv_prompt_kernel(const KpArgs a) {
       mbar_init(bar_pg + 8 * i, 1);
       mbar_init(bar_pg_empty + 8 * i, 12);
     }
+    for (int i = 0; i < KP_RAW; ++i) {
+      mbar_init(bar_raw + 8 * i, 1);
+      mbar_init(bar_raw_empty + 8 * i, 4);
+    }
     *abort = 0;
     fence_mbar_init();
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
   }
   if (warp == 1) tmem_alloc_cg<1>(smem_u32(tmem_slot), KP_TMEM_COLS);
   __syncwarp();
@@ -476,7 +487,7 @@ kv_prompt_kernel(const KpArgs a) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(KP_REGS_LOW));
     if (warp == 0) {
       // ------------------------------------------------- segments and pages
-      int bt = 0, seg_out = 0;
+      int bt = 0, seg_out = 0, raw_it = 0;
       bool ok = true, first_seg = true, held = false;
       KpPages* pages = reinterpret_cast<KpPages*>(gbase + L::PG_OFF);
       // a block's data stay back until it is known whether another follows
@@ -555,13 +566,12 @@ kv_prompt_kernel(const KpArgs a) {
           int id = next_id;
           next_id = page_of(j + 1);            // a block ahead
           if (id >= a.v.pages) id = -1;
-          long long at = -1;
+          long long unit = 0;
           float kf = __uint_as_float(0x7FC00000u);
           int ve = 0;
           if (id >= 0) {
-            const long long unit = static_cast<long long>(id) * a.v.heads + head;
+            unit = static_cast<long long>(id) * a.v.heads + head;
             const uint32_t kc = a.v.k_scales[unit], vc = a.v.v_scales[unit];
-            at = ((unit << shift) + ((16 * lane) & ((1 << shift) - 1))) * D;
             if (kc != 0xFFu && vc != 0xFFu) {
               kf = kv_scale_value(kc);
               ve = static_cast<int>(vc);
@@ -577,16 +587,44 @@ kv_prompt_kernel(const KpArgs a) {
           if (lane < 8) {
             pages[ps].of[lane].kf = kf;
             pages[ps].of[lane].ve = ve;
-            pages[ps].at[lane] = at;
           }
           const int top = __reduce_max_sync(0xFFFFFFFFu, ve);
+          const unsigned gone = __ballot_sync(0xFFFFFFFFu, lane < 8 && id < 0);
           if (lane == 0) {
+            pages[ps].gone = static_cast<int>(gone);
             pages[ps].top = top;
             pages[ps].valid = len - (block0 + j) * KP_BK;
           }
           __syncwarp();
           held = true;
           ++bt;
+          // the codes: a box per page, by the lane of its first 16 keys
+          const bool loads = id >= 0 && ((16 * lane) & ((1 << shift) - 1)) == 0;
+          const unsigned boxes = __popc(__ballot_sync(0xFFFFFFFFu, loads));
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const int slot = raw_it % KP_RAW;
+            if (!mbar_wait(bar_raw_empty + 8 * slot, ((raw_it / KP_RAW) & 1) ^ 1, abort)) {
+              if (lane == 0) kp_timeout(abort, 0x5e);
+              ok = false;
+              break;
+            }
+            const uint32_t full = bar_raw + 8 * slot;
+            if (lane == 0) mbar_arrive_expect_tx(full, boxes * (D << shift));
+            __syncwarp();
+            if (loads)
+              tma_load_2d(base + L::RAW_OFF + slot * L::RAW_BYTES + 16 * lane * D,
+                          kv ? &tmV : &tmK, full, 0, static_cast<int>(unit << shift));
+            ++raw_it;
+          }
+          if (!ok) break;
+        }
+      }
+      // the CTA may not retire before its copies have landed
+      for (int i = max(0, raw_it - KP_RAW); i < raw_it; ++i) {
+        const long long t0 = clock64();
+        while (!mbar_try_wait(bar_raw + 8 * (i % KP_RAW), (i / KP_RAW) & 1) &&
+               clock64() - t0 < MXK_WAIT_LIMIT_CYCLES) {
         }
       }
     } else if (warp == 1) {
@@ -682,29 +720,9 @@ kv_prompt_kernel(const KpArgs a) {
     }
     const int r0 = ci * SROWS + rl;          // the lane's row in the warp's first step
     const uint32_t to = (c >> 2) * L::REGION + r0 * 128 + (((2 * (c & 3)) ^ (r0 & 7)) << 4);
-    // its place in the 16 keys that step i lies in: number (i * 4 * SROWS + r0) / 16
-    const int from = (r0 & 15) * D + 16 * c;
+    const uint32_t from = r0 * D + ((D == 128 ? (c ^ (r0 & 7)) : (c ^ ((r0 >> 1) & 3))) << 4);
     const KpPages* pages = reinterpret_cast<const KpPages*>(gbase + L::PG_OFF);
-    uint4 w[IT];                             // the next tile's codes
-    auto load = [&](const uint8_t* plane, long long at) {
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (at >= 0)
-        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                     : "l"(plane + at + from));
-      return x;
-    };
-    auto store = [&](uint32_t dst, int i, const uint4& x) {
-      uint32_t f[8];
-      kv_f16_pairs<FMT>(x.x, f[0], f[1]);
-      kv_f16_pairs<FMT>(x.y, f[2], f[3]);
-      kv_f16_pairs<FMT>(x.z, f[4], f[5]);
-      kv_f16_pairs<FMT>(x.w, f[6], f[7]);
-      const uint32_t p = dst + to + i * (4 * SROWS * 128);
-      st_shared_v4(p, f[0], f[1], f[2], f[3]);
-      st_shared_v4(p ^ 16, f[4], f[5], f[6], f[7]);
-    };
-    // the table's data of the block that is loaded next
+    // a block's data, once they are there
     auto pages_of = [&](int b) -> const KpPages* {
       if (!mbar_wait(bar_pg + 8 * (b & (KP_PG - 1)), (b / KP_PG) & 1, abort)) {
         if (lane == 0) kp_timeout(abort, 0x53);
@@ -714,43 +732,54 @@ kv_prompt_kernel(const KpArgs a) {
     };
     const KpPages* pg = pages_of(0);
     if (pg && pg->top < 0) pg = nullptr;     // there are none
-    if (pg) {
-#pragma unroll
-      for (int i = 0; i < IT; ++i) w[i] = load(a.k, pg->at[(i * 4 * SROWS + r0) >> 4]);
-    }
-    // tiles in the order K, V of each block; a chunk's registers take the next
-    // tile's codes as soon as it is converted
+    // tiles in the order K, V of each block
 #pragma unroll 1
     for (int tile = 0; pg; ++tile) {
-      const int kv = tile & 1, bt = tile >> 1, st = bt % KP_STAGES;
-      const KpPages* next = pg;              // of the next tile: V, or the next block's K
-      if (kv == 1 && pg->more == 0) {
-        next = nullptr;
-      } else if (kv == 1) {
-        next = pages_of(bt + 1);
-        if (!next) break;
+      const int kv = tile & 1, bt = tile >> 1, st = bt % KP_STAGES, slot = tile % KP_RAW;
+      if (!mbar_wait(bar_raw + 8 * slot, (tile / KP_RAW) & 1, abort)) {
+        if (lane == 0) kp_timeout(abort, 0x5f);
+        break;
       }
-      const uint8_t* plane = kv ? a.k : a.v_codes;
-      const uint32_t dst = base + (kv ? L::V_OFF : L::K_OFF) + st * L::K_BYTES;
-      // keys behind the request's end count as zeros in V, whatever stands there
-      const int valid = kv ? pg->valid : KP_BK;
+      uint4 w[IT];
+#pragma unroll
+      for (int i = 0; i < IT; ++i)
+        w[i] = ld_shared_v4(base + L::RAW_OFF + slot * L::RAW_BYTES + from + i * 2048);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_raw_empty + 8 * slot);
+      // keys of V behind the request's end or in pages that were not loaded
+      // count as zeros, whatever stands there
+      if (kv && (pg->valid < KP_BK || pg->gone)) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          const int r = i * 4 * SROWS + r0;
+          if (r >= pg->valid || ((pg->gone >> (r >> 4)) & 1)) w[i] = make_uint4(0, 0, 0, 0);
+        }
+      }
       if (!mbar_wait((kv ? bar_v_empty : bar_k_empty) + 8 * st, ((bt / KP_STAGES) & 1) ^ 1, abort)) {
         if (lane == 0) kp_timeout(abort, 0x54);
         break;
       }
+      const uint32_t dst = base + (kv ? L::V_OFF : L::K_OFF) + st * L::K_BYTES + to;
 #pragma unroll
       for (int i = 0; i < IT; ++i) {
-        if (i * 4 * SROWS + r0 >= valid) w[i] = make_uint4(0, 0, 0, 0);
-        store(dst, i, w[i]);
-        if (next) w[i] = load(plane, next->at[(i * 4 * SROWS + r0) >> 4]);
+        uint32_t f[8];
+        kv_f16_pairs<FMT>(w[i].x, f[0], f[1]);
+        kv_f16_pairs<FMT>(w[i].y, f[2], f[3]);
+        kv_f16_pairs<FMT>(w[i].z, f[4], f[5]);
+        kv_f16_pairs<FMT>(w[i].w, f[6], f[7]);
+        const uint32_t p = dst + i * (4 * SROWS * 128);
+        st_shared_v4(p, f[0], f[1], f[2], f[3]);
+        st_shared_v4(p ^ 16, f[4], f[5], f[6], f[7]);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive((kv ? bar_v : bar_k) + 8 * st);
-        if (kv) mbar_arrive(bar_pg_empty + 8 * (bt & (KP_PG - 1)));
+      if (lane == 0) mbar_arrive((kv ? bar_v : bar_k) + 8 * st);
+      if (kv) {
+        const bool more = pg->more != 0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_pg_empty + 8 * (bt & (KP_PG - 1)));
+        pg = more ? pages_of(bt + 1) : nullptr;
       }
-      pg = next;
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(KP_REGS_SOFT));
@@ -1072,7 +1101,8 @@ kv_prompt_join_kernel(const KpArgs a) {
 }
 
 template <int FMT, int D>
-cudaError_t kp_run(const KpArgs& a, int sms, cudaStream_t st) {
+cudaError_t kp_run(const CUtensorMap& tk, const CUtensorMap& tv, const KpArgs& a, int sms,
+                   cudaStream_t st) {
   auto kern = kv_prompt_kernel<FMT, D>;
   using L = KpSmem<D>;
   static std::atomic<bool> attr_set[64] = {};
@@ -1090,7 +1120,7 @@ cudaError_t kp_run(const KpArgs& a, int sms, cudaStream_t st) {
       return cudaErrorInvalidConfiguration;
     if (dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
   }
-  kern<<<sms, KP_THREADS, L::ALLOC, st>>>(a);
+  kern<<<sms, KP_THREADS, L::ALLOC, st>>>(tk, tv, a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.ws == nullptr) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1118,8 +1148,6 @@ cudaError_t launch_kv_prompt(const KvAttn& q, int sms, cudaStream_t st) {
   KpArgs a{};
   a.v = kv_view(q);
   a.Q = static_cast<const uint16_t*>(q.Q);
-  a.k = c.k;
-  a.v_codes = c.v;
   a.O = q.O;
   a.q_ts = q.q_ts;
   a.q_hs = q.q_hs;
@@ -1133,14 +1161,16 @@ cudaError_t launch_kv_prompt(const KvAttn& q, int sms, cudaStream_t st) {
     a.joins = reinterpret_cast<KpJoin*>(static_cast<char*>(q.ws) +
                                         static_cast<int64_t>(sms) * 2 * KP_ROWS * (c.d + 2) * 4);
   }
+  CUtensorMap tk, tv;
+  if (!kv_tensor_map(&tk, c.k, c) || !kv_tensor_map(&tv, c.v, c)) return cudaErrorInvalidValue;
   const bool d64 = c.d == 64;
   switch (c.fmt) {
     case FMT_E4M3:
-      return d64 ? kp_run<FMT_E4M3, 64>(a, sms, st) : kp_run<FMT_E4M3, 128>(a, sms, st);
+      return d64 ? kp_run<FMT_E4M3, 64>(tk, tv, a, sms, st) : kp_run<FMT_E4M3, 128>(tk, tv, a, sms, st);
     case FMT_E5M2:
-      return d64 ? kp_run<FMT_E5M2, 64>(a, sms, st) : kp_run<FMT_E5M2, 128>(a, sms, st);
+      return d64 ? kp_run<FMT_E5M2, 64>(tk, tv, a, sms, st) : kp_run<FMT_E5M2, 128>(tk, tv, a, sms, st);
     default:
-      return d64 ? kp_run<FMT_INT8, 64>(a, sms, st) : kp_run<FMT_INT8, 128>(a, sms, st);
+      return d64 ? kp_run<FMT_INT8, 64>(tk, tv, a, sms, st) : kp_run<FMT_INT8, 128>(tk, tv, a, sms, st);
   }
 }
 

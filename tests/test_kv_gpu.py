@@ -554,10 +554,33 @@ def test_attention_far_offsets():
     mx.mx_kv_append(c, K, V, slots)
     q = _tokens(1, 4, d, BF, 3)
     r = mx.mx_kv_attention(q, c, _i32([table]), _i32([n]), _i32([0, 1]), 1)
+    chunk = _tokens(40, 4, d, BF, 4)             # the kernel for many rows
+    rc = mx.mx_kv_attention(chunk, c, _i32([table]), _i32([n]), _i32([0, 40]), 40)
     small = mx.KVCache(*(x[table].contiguous() for x in (c.k, c.v, c.k_scales, c.v_scales)), mx.E4M3)
     k, v, ks, vs = _planes(small)
     e = _kv.attention(_np(q.double()), k, v, ks, vs, mx.E4M3, np.array([[0, 1, 2, 3]]), [n], [0, 1], d ** -0.5)
     assert (np.abs(_np(r.double()) - e[0]) <= _kv.bound(*e, BF)).all()
+    e = _kv.attention(_np(chunk.double()), k, v, ks, vs, mx.E4M3, np.array([[0, 1, 2, 3]]), [n], [0, 40], d ** -0.5)
+    assert (np.abs(_np(rc.double()) - e[0]) <= _kv.bound(*e, BF)).all()
+
+
+def test_attention_of_more_requests_than_the_prompt_kernel_plans():
+    """Beyond 16384 requests every call goes through the kernel for few rows."""
+    B = 16390
+    lens, news = [1 + i % 3 for i in range(B)], [1] * B
+    lens[-1], news[-1] = 60, 40
+    s = Setup(mx.INT8, 16, 1, 64, lens, news, group=1)
+    s.check()
+
+
+def test_extend_the_most_requests():
+    rng = np.random.default_rng(3)
+    lens, new, table, stack = _pages_case(rng, 16384, 16, 3, 2, 40000)
+    want_table = table.copy()
+    want = _kv.extend(lens, new, want_table, stack, len(stack), 16, 33000)
+    p, t = _extend(lens, new, table, stack, len(stack), 16, 33000)
+    assert (_np(p.lens).tolist(), _np(p.cu).tolist(), _np(p.slots).tolist(), _np(p.counts).tolist()) == want
+    assert (_np(t) == want_table).all()
 
 
 def test_a_step_in_a_graph_and_on_another_stream():
