@@ -744,8 +744,6 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
       for (int i = 0; i < IT; ++i)
         w[i] = ld_shared_v4(base + L::RAW_OFF + slot * L::RAW_BYTES + from + i * 2048);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_raw_empty + 8 * slot);
       // keys of V behind the request's end or in pages that were not loaded
       // count as zeros, whatever stands there
       if (kv && (pg->valid < KP_BK || pg->gone)) {
@@ -773,7 +771,12 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive((kv ? bar_v : bar_k) + 8 * st);
+      if (lane == 0) {
+        mbar_arrive((kv ? bar_v : bar_k) + 8 * st);
+        // only now, with the codes converted and so in registers beyond doubt:
+        // arrived right behind the loads, the next copy could overtake them
+        mbar_arrive(bar_raw_empty + 8 * slot);
+      }
       if (kv) {
         const bool more = pg->more != 0;
         __syncwarp();

@@ -524,6 +524,63 @@ def test_attention_chunks_of_special_values():
     assert torch.equal(w.run(window=60), want)
 
 
+def _check_large(q_len, kv, hq, heads, d, page, fmt, dtype, window=0, requests=1):
+    """At the sizes of real prompts: the formula in 64 bits on the GPU for all
+    rows, the bound of tests/_kv.py, and the same bits in every run (a race
+    between roles that small sizes never lose shows here)."""
+    c = mx.empty_kv_cache(fmt, requests * -(-kv // page), heads, page, d)
+    g = torch.Generator().manual_seed(kv)
+    table = torch.randperm(c.k.shape[0], generator=g).to(torch.int32).view(requests, -1).cuda()
+    pos = torch.arange(kv, device="cuda")
+    slots = torch.cat([t.long()[pos // page] * page + pos % page for t in table])
+    n = requests * kv
+    mx.mx_kv_append(c, _tokens(n, heads, d, dtype, 1), _tokens(n, heads, d, dtype, 2), slots)
+    Q = _tokens(requests * q_len, hq, d, dtype, 3)
+    lens, cu = _i32([kv] * requests), _i32([q_len * i for i in range(requests + 1)])
+    ws = torch.empty(mx.kv_attention_workspace_bytes(hq, heads, d, q_len), dtype=torch.uint8, device="cuda")
+    for w in (ws, None):
+        runs = [mx.mx_kv_attention(Q, c, table, lens, cu, q_len, window=window, workspace=w) for _ in range(6)]
+        torch.cuda.synchronize()
+        assert mx.mx_last_error() == 0
+        assert all(torch.equal(r, runs[0]) for r in runs)
+        codes = torch.tensor(_kv.TABLES[fmt], device="cuda")
+        for b in range(requests):
+            at = kv - q_len + torch.arange(q_len, device="cuda")[:, None]
+            see = (pos <= at) & ((pos > at - window) if window else True)
+            for h in range(heads):
+                def plane(x, s):
+                    ids = table[b].long()
+                    e = torch.exp2(s[ids, h].double() - 127)[:, None, None]
+                    return (codes[x[ids, h].long()] * e).view(-1, d)[:kv]
+                k, v = plane(c.k, c.k_scales), plane(c.v, c.v_scales)
+                G = hq // heads
+                q = Q[b * q_len:(b + 1) * q_len, h * G:(h + 1) * G].double().transpose(0, 1)
+                x = (q @ k.T * d ** -0.5).masked_fill(~see, -math.inf)
+                p = torch.softmax(x, -1)
+                out, sv = p @ v, p @ v.abs()
+                ab = (q.abs() @ k.abs().T).masked_fill(~see, 0).amax(-1, keepdim=True)
+                qm = q.abs().amax(-1, keepdim=True) * k.abs().sum(-1).max()
+                ex = d ** -0.5 * ((d + 4) * ab + 0.5 * qm) * 2.0 ** -24
+                e = [t.cpu().numpy() for t in (out, sv, ex, see.sum(-1)[None, :, None].double(),
+                                               v.abs().max()[None, None, None])]
+                got = runs[0][b * q_len:(b + 1) * q_len, h * G:(h + 1) * G].double().transpose(0, 1)
+                assert (np.abs(_np(got) - e[0]) <= _kv.bound(*e, dtype)).all()
+
+
+@pytest.mark.parametrize("case", [
+    (2048, 2048, 32, 8, 128, 64, mx.E4M3, BF), (2048, 2500, 16, 16, 64, 16, mx.INT8, HF),
+    (1500, 4000, 8, 2, 128, 128, mx.E5M2, BF, 900), (700, 1900, 12, 4, 128, 32, mx.INT8, HF, 0, 5)])
+def test_attention_large_chunks(case):
+    _check_large(*case)
+
+
+@pytest.mark.parametrize("case", [
+    (1, 20000, 32, 8, 128, 64, mx.E4M3, BF, 0, 3), (4, 9000, 16, 4, 128, 16, mx.INT8, HF, 5000, 9),
+    (1, 7000, 8, 8, 64, 32, mx.E5M2, HF, 0, 20)])
+def test_attention_large_decode(case):
+    _check_large(*case)
+
+
 def test_attention_many_requests():
     """More requests than a CTA has threads, most with one token."""
     rng = np.random.default_rng(0)
