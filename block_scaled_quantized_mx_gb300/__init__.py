@@ -593,6 +593,13 @@ _KV_OUT_DTYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16,
                   torch.float16: DT_F16}
 
 
+# An uninitialised tensor on the current GPU: (shape, strides, dtype).  The
+# allocator's entry without the operator dispatch around it, whose code a
+# kernel launch between two calls pushes out of the host's caches: 3.6 us
+# instead of 7 in a decoding step.
+_empty_cuda = torch._C._dynamo.guards._empty_strided_cuda
+
+
 def _int32(t: torch.Tensor, name: str, n: int = 0) -> int:
     """Checks a vector of int32 values; its address."""
     if t.dtype is not _i32 or not t.is_cuda or t.dim() != 1 or \
@@ -635,8 +642,11 @@ def mx_kv_extend(lens: torch.Tensor, new_tokens: torch.Tensor,
     p_count = _int32(count, "count", 1)
     p_table, stride, width = _table(table, B)
     if out is None:
-        e = lens.new_empty
-        out = KVPlan(e(B), e(B + 1), e(max_tokens, dtype=torch.int64), e(2))
+        one = (1,)
+        out = KVPlan(_empty_cuda((B,), one, _i32),
+                     _empty_cuda((B + 1,), one, _i32),
+                     _empty_cuda((max_tokens,), one, torch.int64),
+                     _empty_cuda((2,), one, _i32))
     else:
         _int32(out.lens, "out.lens", B)
         _int32(out.cu, "out.cu", B + 1)
@@ -666,7 +676,7 @@ def mx_kv_truncate(lens: torch.Tensor, keep: torch.Tensor, table: torch.Tensor,
     p_count = _int32(count, "count", 1)
     p_table, stride, width = _table(table, B)
     if out is None:
-        out = KVCut(lens.new_empty(B), lens.new_empty(2))
+        out = KVCut(_empty_cuda((B,), (1,), _i32), _empty_cuda((2,), (1,), _i32))
     else:
         _int32(out.lens, "out.lens", B)
         _int32(out.counts, "out.counts", 2)
@@ -747,8 +757,8 @@ def mx_kv_attention(Q: torch.Tensor, cache: KVCache, table: torch.Tensor,
     p_cu = _int32(cu, "cu", B + 1)
     p_table, stride, width = _table(table, B)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or Q.dtype, device=Q.device)
         ot, oh = Hq * d, d
+        out = _empty_cuda((T, Hq, d), (ot, oh, 1), out_dtype or Q.dtype)
     elif (out.shape != shape or not out.is_cuda or out.stride(2) != 1
           or (out_dtype is not None and out.dtype != out_dtype)):
         raise ValueError("out must be a CUDA tensor of Q's shape and of type "
