@@ -427,8 +427,8 @@ mx_status mx_kv_attention(const void* Q, int32_t dtype, int64_t tokens, int64_t 
   if ((causal != 0 && causal != 1) || window < 0) return MX_ERR_INVALID_ARG;
   const int64_t d = a.cache.d;
   if (q_heads < 1 || q_heads % a.cache.heads) return MX_ERR_SHAPE;
-  // rows of one cache head are counted in 32 bits
-  if (tokens < 0 || tokens > kMaxDim / (q_heads / a.cache.heads)) return MX_ERR_SHAPE;
+  // rows of one cache head are counted in 32 bits, rounded up to whole tiles
+  if (tokens < 0 || tokens > (kMaxDim - 1024) / (q_heads / a.cache.heads)) return MX_ERR_SHAPE;
   if (requests < 0 || requests > kMaxDim || max_q < 0 || max_q > kMaxDim) return MX_ERR_SHAPE;
   if (table_width < 1 || table_stride < table_width || table_width > kMaxDim ||
       table_stride > kMaxDim)

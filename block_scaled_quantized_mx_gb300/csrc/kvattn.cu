@@ -44,6 +44,11 @@
 // one join them took 27 us after the last tile with 57 CTAs to a unit, 131072
 // keys in 8 cache heads: every arrival waited for its turn on the counter,
 // and one CTA did all the adding.)  Every wait is bounded.
+//
+// Measured: 64 requests of 8192 keys (32 heads on 8 cache heads of 128, E4M3)
+// 168 us, 6.4 TB/s, 0.94 of the copy rate; one of 131072 keys 55 us, of which
+// about 10 are the start and the join; 256 of up to 4096 keys, a head of 64 to
+// each cache head, int8, pages of 16, 205 us, 5.3 TB/s.
 #include <cudaTypedefs.h>
 
 #include <algorithm>

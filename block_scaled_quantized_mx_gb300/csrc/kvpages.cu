@@ -22,6 +22,9 @@
 // input, the CTAs are one cluster (of at most eight, the portable limit) with
 // its barrier between the last read of an input and the first write of an
 // output; otherwise there are as many as the slots keep busy.
+// Measured, truncate and extend together: 64 requests 7.4 us; 2048 requests, a
+// tenth of them with whole prompts (200000 new tokens), 14.7 us (with a page
+// read per token and eight CTAs 39).
 #include <cstdint>
 
 #include "common.cuh"

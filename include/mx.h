@@ -2,7 +2,7 @@
  * mx.h -- C ABI of the GB300 (sm_103a) MX block-scaled / FP16 GEMM library
  * (libmx_gb300.so).
  *
- * Three operations, all launched asynchronously on the caller's CUDA stream:
+ * Its operations, all launched asynchronously on the caller's CUDA stream:
  *
  *   mx_quantize  fp32 matrix -> MX tensor (E4M3, E5M2 or E2M1 data plane plus
  *                a UE8M0 scale plane, one scale per 32 consecutive K elements)
@@ -13,6 +13,8 @@
  *   *_fused      the same products with bias and GELU applied to the fp32
  *                accumulator in the epilogue, and mx_gemm_fused_quantize,
  *                which also quantizes C to an MX tensor for the next layer
+ *   mx_kv_*      an 8-bit paged key/value cache: its block tables and slots,
+ *                the quantizing write, and attention over it
  *
  * Where these come from.  The quantized tensor as one object holding a data
  * plane and a scale plane, the scale format ("FP8 E8M0") and the block of 32
@@ -555,7 +557,10 @@ mx_status mx_kv_append(const mx_kv_cache* cache, const void* K, const void* V, i
  *              that run at the same time).  With it the keys of one request
  *              are spread over many SMs; NULL or a smaller size: they are not.
  * mx_kv_attention_workspace_bytes does not depend on lengths or the number of
- * requests; 0 on bad arguments or without a compute capability 10.3 device.
+ * requests (about 7 MB, or 40 MB where max_q * q_heads / heads > 32 and d = 128); 0
+ * on bad arguments or without a compute capability 10.3 device.  The two
+ * kernels and the two modes sum in different orders: results can differ
+ * between them in the last bits, and are the same from run to run.
  */
 size_t mx_kv_attention_workspace_bytes(int64_t q_heads, int64_t heads, int64_t d, int64_t max_q);
 mx_status mx_kv_attention(const void* Q, int32_t dtype, int64_t tokens, int64_t q_heads,
