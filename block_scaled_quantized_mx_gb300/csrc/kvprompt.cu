@@ -989,6 +989,10 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
         ++own_seg;
         tc_fence_after();
+        // a row that saw keys and adds up to nothing had only scores of -infinity:
+        // 0 / 0, not the 0 of a row that sees none
+        if (l == 0.0f && max(lo, key00) < min(hi, key00 + KP_BK * count))
+          l = __uint_as_float(0x7FC00000u);
         // to true units: 2^(ev - 127), and the 2^KP_P_EXP out of P
         const float unit = kv_scale_value(static_cast<uint32_t>(ev));
         const float inv = (l == 0.0f ? 0.0f : 1.0f / l) * (1.0f / (1 << KP_P_EXP));

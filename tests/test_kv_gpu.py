@@ -435,6 +435,26 @@ def test_attention_masked_lowest_and_infinite_queries():
     assert torch.equal(r[0, 1], clean[0, 1]) and torch.equal(r[1, 0], clean[1, 0]) and torch.equal(r[2], clean[2])
 
 
+@pytest.mark.parametrize("news", [[1, 2], [40, 70]])
+@pytest.mark.parametrize("ws", [True, False])
+def test_attention_scores_of_minus_infinity(news, ws):
+    """A row whose every score is -infinity is 0 / 0 in both kernels; one that
+    sees no key is 0, and the rows beside them stay as they were."""
+    s = Setup(mx.E4M3, 16, 1, 64, [500, 700], news, dtype=HF, group=2)
+    s.cache.k[..., 5] = 0x38            # 1.0 at value 5 of every key
+    clean = s.run(window=100, ws=ws)
+    s.q[0, 1, 5] = -math.inf
+    s.q[-1, 0, 5] = -math.inf
+    r = s.run(window=100, ws=ws)
+    assert r[0, 1].isnan().all() and r[-1, 0].isnan().all()
+    clean[0, 1] = r[0, 1] = 0
+    clean[-1, 0] = r[-1, 0] = 0
+    assert torch.equal(r, clean)
+    s.lens = [n // 2 - 1 for n in news]                   # the first rows see nothing
+    s.q[0, :, 5] = -math.inf
+    assert (s.run(ws=ws)[0] == 0).all()
+
+
 def test_attention_strided_and_offsets_beyond_requests():
     """Q and O inside wider tensors; cu that leaves rows to nobody, goes down
     or beyond Q; lengths beyond the table."""
