@@ -149,6 +149,22 @@ __device__ __forceinline__ void kv_store4(void* O, int o_dtype, long long at, fl
   }
 }
 
+// Eight consecutive outputs at element `at`.
+__device__ __forceinline__ void kv_store8(void* O, int o_dtype, long long at, const float (&v)[8]) {
+  if (o_dtype == DT_F32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(O) + at);
+    p[0] = make_float4(v[0], v[1], v[2], v[3]);
+    p[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    const bool bf = o_dtype == DT_BF16;
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(O) + at) =
+        make_uint4(bf ? cvt_bf16x2(v[0], v[1]) : cvt_f16x2(v[0], v[1]),
+                   bf ? cvt_bf16x2(v[2], v[3]) : cvt_f16x2(v[2], v[3]),
+                   bf ? cvt_bf16x2(v[4], v[5]) : cvt_f16x2(v[4], v[5]),
+                   bf ? cvt_bf16x2(v[6], v[7]) : cvt_f16x2(v[6], v[7]));
+  }
+}
+
 // One box of the K or V plane: the P x d codes of a page of one head, rows
 // swizzled over 128 bytes (d 128) or 64 (d 64).
 inline bool kv_tensor_map(CUtensorMap* m, const void* p, const KvCache& c) {

@@ -8,8 +8,8 @@
 // the converted keys), in two tiles of 128 that take turns on the tensor core
 // as in attention.cu.  What differs from dense attention:
 //   * K and V come as codes.  Warp 0 reads the block table and the scales and
-//     loads the codes of blocks of 128 keys page by page with TMA, up to three
-//     blocks ahead; four warps turn them into f16 -- exactly, for all three
+//     loads the codes of blocks of 128 keys page by page with TMA, a block ahead
+//     (d 128; three for d 64); four warps turn them into f16 -- exactly, for all three
 //     formats -- and write the swizzled operand tiles, two deep each.  The
 //     conversion of a block serves both tiles and, through the rows' order, all
 //     heads of the group.  (Read from global memory straight into the
@@ -20,24 +20,30 @@
 //     V's, a power of two relative to the largest so far, is added to the
 //     exponent, so P carries it exactly and the row sums take it out again;
 //   * rows are converted once per unit: the thread that owns a row brings it
-//     to f16 with a power of two of its own, and keeps its mask bounds;
+//     to f16 with a power of two of its own, and keeps its mask bounds.  The next
+//     unit's go to shared memory before this unit's O is read and written, so
+//     that its first scores are under way meanwhile (231 us -> 227);
 //   * the units are cut evenly over the SMs, as in kvattn.cu: a stretch of the
 //     list of all (request, row tile, cache head, key block)s per CTA, each
 //     unit standing with some entries more for what it costs to begin and end
 //     one; parts of units go to the workspace and a second kernel joins them.
-//   * Q stands in tensor memory beside the scores, which leaves 64 KB of shared
-//     memory to the staged codes.  Scores then go 64 keys at a time (there is
-//     no room for 128 of each tile); a block's operands, of 128 keys, serve
-//     two such steps.
+//   * scores go 64 keys at a time into two buffers per tile, so that a tile's
+//     next scores do not wait for its softmax, and each tile has an issuing warp
+//     of its own: one warp spends ~850 clocks on the waits and instructions of a
+//     tile's step, the tensor core ~620 (one buffer and one warp, with Q in
+//     tensor memory: 237 us against 231; two buffers and one warp: 248; one
+//     buffer of 128 keys: 240).
 // A 2048-token chunk over 8192 keys (32 heads on 8 cache heads of 128) takes
-// 235 us, 0.53 of the measured bf16 rate: the tensor core is busy 46 % of the
-// time, no other pipe more, and a step waits on the step before it.
-// Tensor memory, tile t: its scores (then P) in columns [256 t, 256 t + 64), Q
-// in [256 t + 64, 256 t + 64 + d / 2), O in [256 t + 128, 256 t + 128 + d).
-// Ordering: the MMA warp issues a step's P V before the next step's scores,
-// and a commit covers every earlier operation of its thread: once scores are
-// complete so is the product that read P and accumulated into O.  Every
-// mbarrier wait is bounded.
+// 219 us, 0.57 of the measured bf16 rate.  Of these the join takes ~11 and
+// beginning and ending units ~20; a block of 128 keys for both tiles ~3700
+// clocks, where its products alone need 2480 (in steps of 64 keys a product of
+// Q K^T takes 48 clocks, not 32).  With no conversion and no exponentials it
+// would still be ~3300: hand-offs between the roles.
+// Tensor memory, tile t: its score buffers (then P) in columns [256 t, 256 t + 64)
+// and [256 t + 64, 256 t + 128), O in [256 t + 128, 256 t + 128 + d).
+// Ordering: an issuing warp issues P V of step h before the scores of step h + 2,
+// and a commit covers every earlier operation of its thread: once those scores
+// are complete so is that product.  Every mbarrier wait is bounded.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -59,7 +65,7 @@ constexpr int KP_BQ = 128;                 // rows per tile
 constexpr int KP_ROWS = 2 * KP_BQ;         // rows of a unit
 constexpr int KP_BK = 128;                 // keys per block
 constexpr int KP_HK = 64;                  // keys per step of the softmax, two to a block
-constexpr int KP_THREADS = 512;            // pages and MMA, two softmax warpgroups, conversion
+constexpr int KP_THREADS = 512;            // pages and issuers, two softmax warpgroups, conversion
 constexpr int KP_WARPS = KP_THREADS / 32;
 // Registers: launched at 128; 72 * 128 + 176 * 256 + 88 * 128 = 65536.
 constexpr int KP_REGS_LOW = 72;            // warpgroup 0
@@ -73,7 +79,6 @@ constexpr int KP_P_EXP = 7;                // P is scaled by 2^7: at most 2^(7 +
 constexpr int KP_OVER = 4;
 constexpr int KP_PG = 8;                   // blocks whose page data is kept
 constexpr int KP_STAGES = 2;               // f16 tiles of K, and of V
-constexpr int KP_RAW = 6;                  // tiles of codes, K and V in turn
 constexpr int KP_MAX_REQUESTS = 16384;
 
 // One block: the scales of each 16 of its keys, and what there is of it.
@@ -181,19 +186,22 @@ struct KpWalk {
 template <int D>
 struct KpSmem {
   static constexpr int REGION = 128 * 128;
+  static constexpr int Q_BYTES = (D / 64) * REGION;
   static constexpr int K_BYTES = (D / 64) * REGION;       // V's tiles are alike
   static constexpr int V_BYTES = K_BYTES;
-  static constexpr int K_OFF = 0;
+  static constexpr int RAW = D == 64 ? 6 : 2;             // tiles of codes, K and V in turn
+  static constexpr int Q_OFF = 0;
+  static constexpr int K_OFF = Q_OFF + 2 * Q_BYTES;
   static constexpr int V_OFF = K_OFF + KP_STAGES * K_BYTES;
   static constexpr int RAW_BYTES = KP_BK * D;
   static constexpr int RAW_OFF = V_OFF + KP_STAGES * V_BYTES;
-  static constexpr int PG_OFF = RAW_OFF + KP_RAW * RAW_BYTES;
+  static constexpr int PG_OFF = RAW_OFF + RAW * RAW_BYTES;
   static constexpr int SEG_OFF = PG_OFF + KP_PG * static_cast<int>(sizeof(KpPages));
   static constexpr int BAR_OFF = SEG_OFF + 2 * static_cast<int>(sizeof(KpSeg));
-  // k_full, v_full, k_empty, v_empty [stages]; q_full, s_full, p_full, o_done
-  // [tile]; seg_full[2], seg_empty[2], pg_full[8], pg_empty[8]; raw_full,
-  // raw_empty [KP_RAW]
-  static constexpr int BARS = 4 * KP_STAGES + 8 + 4 + 2 * KP_PG + 2 * KP_RAW;
+  // k_full, v_full, k_empty, v_empty [stages]; q_full, o_done [tile],
+  // s_full, p_full [tile][buffer]; seg_full[2], seg_empty[2], pg_full[8], pg_empty[8];
+  // raw_full, raw_empty [RAW]
+  static constexpr int BARS = 4 * KP_STAGES + 12 + 4 + 2 * KP_PG + 2 * RAW;
   static constexpr int MISC_OFF = BAR_OFF + BARS * 8;
   static constexpr int WALK_OFF = MISC_OFF + 16;
   static constexpr int TOTAL = WALK_OFF + static_cast<int>(sizeof(KpWalk));
@@ -210,7 +218,8 @@ struct KpArgs {
   int bf16;
   int o_dtype;
   float scale_log2e;
-  float* ws;                               // two slots per CTA: O as [D / 4][256 rows][4], m[256], l[256]
+  float* ws;                               // two slots per CTA: O as [D / 8][256 rows][8], m[256], l[256];
+                                           // 32-byte aligned
   KpJoin* joins;                           // one per CTA
 };
 
@@ -225,49 +234,48 @@ __device__ __forceinline__ uint32_t kp_idesc(uint32_t n, uint32_t b_mn) {
   return (1u << 4) | (b_mn << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// Whole products in one statement each.  The MMA warp runs them with all 32
+// Whole products in one statement each.  An issuing warp runs them with all 32
 // lanes, so that the descriptors stay warp-uniform, and one elected lane
 // issues; the election and the predicates are made once per product, and of
 // the descriptors only the low words (start addresses) move.  Issued one by
 // one, with an election each, the instructions around them took longer than
 // the products.
 //
-// Both products read their first operand from tensor memory (16 values of a
-// row are 8 columns).  S = Q K^T: D / 16 steps of 16 along the 128-byte rows of
-// K, whose regions of 64 values lie 16 KB apart.
+// S = Q K^T: D / 16 steps of 16 along rows of 128-byte regions 16 KB apart.
 template <int D>
-__device__ __forceinline__ void kp_issue_s(uint32_t d, uint32_t q, uint64_t b, uint32_t id) {
+__device__ __forceinline__ void kp_issue_s(uint32_t d, uint64_t a, uint64_t b, uint32_t id) {
+  const uint32_t a0 = static_cast<uint32_t>(a), a1 = static_cast<uint32_t>(a >> 32);
   const uint32_t b0 = static_cast<uint32_t>(b), b1 = static_cast<uint32_t>(b >> 32);
   asm volatile(
-      "{\n\t.reg .pred e, no, yes;\n\t.reg .b32 x, y;\n\t.reg .b64 db;\n\t"
+      "{\n\t.reg .pred e, no, yes;\n\t.reg .b32 x, y;\n\t.reg .b64 da, db;\n\t"
       "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 no, 0, 0;\n\tsetp.eq.b32 yes, 0, 0;\n\t"
-      "add.u32 x, %1, 0;\n\tadd.u32 y, %2, 0;\n\tmov.b64 db, {y, %3};\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, no;\n\t"
-      "add.u32 x, %1, 8;\n\tadd.u32 y, %2, 2;\n\tmov.b64 db, {y, %3};\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, yes;\n\t"
-      "add.u32 x, %1, 16;\n\tadd.u32 y, %2, 4;\n\tmov.b64 db, {y, %3};\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, yes;\n\t"
-      "add.u32 x, %1, 24;\n\tadd.u32 y, %2, 6;\n\tmov.b64 db, {y, %3};\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, yes;\n\t"
-      "}" ::"r"(d), "r"(q), "r"(b0), "r"(b1), "r"(id)
+      "add.u32 x, %1, 0;\n\tadd.u32 y, %3, 0;\n\tmov.b64 da, {x, %2};\n\tmov.b64 db, {y, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, no;\n\t"
+      "add.u32 x, %1, 2;\n\tadd.u32 y, %3, 2;\n\tmov.b64 da, {x, %2};\n\tmov.b64 db, {y, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, yes;\n\t"
+      "add.u32 x, %1, 4;\n\tadd.u32 y, %3, 4;\n\tmov.b64 da, {x, %2};\n\tmov.b64 db, {y, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, yes;\n\t"
+      "add.u32 x, %1, 6;\n\tadd.u32 y, %3, 6;\n\tmov.b64 da, {x, %2};\n\tmov.b64 db, {y, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, yes;\n\t"
+      "}" ::"r"(d), "r"(a0), "r"(a1), "r"(b0), "r"(b1), "r"(id)
       : "memory");
   if constexpr (D == 128)
     asm volatile(
-        "{\n\t.reg .pred e, yes;\n\t.reg .b32 x, y;\n\t.reg .b64 db;\n\t"
+        "{\n\t.reg .pred e, yes;\n\t.reg .b32 x, y;\n\t.reg .b64 da, db;\n\t"
         "elect.sync _|e, 0xffffffff;\n\tsetp.eq.b32 yes, 0, 0;\n\t"
-        "add.u32 x, %1, 32;\n\tadd.u32 y, %2, 1024;\n\tmov.b64 db, {y, %3};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, yes;\n\t"
-        "add.u32 x, %1, 40;\n\tadd.u32 y, %2, 1026;\n\tmov.b64 db, {y, %3};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, yes;\n\t"
-        "add.u32 x, %1, 48;\n\tadd.u32 y, %2, 1028;\n\tmov.b64 db, {y, %3};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, yes;\n\t"
-        "add.u32 x, %1, 56;\n\tadd.u32 y, %2, 1030;\n\tmov.b64 db, {y, %3};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, yes;\n\t"
-        "}" ::"r"(d), "r"(q), "r"(b0), "r"(b1), "r"(id)
+      "add.u32 x, %1, 1024;\n\tadd.u32 y, %3, 1024;\n\tmov.b64 da, {x, %2};\n\tmov.b64 db, {y, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, yes;\n\t"
+      "add.u32 x, %1, 1026;\n\tadd.u32 y, %3, 1026;\n\tmov.b64 da, {x, %2};\n\tmov.b64 db, {y, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, yes;\n\t"
+      "add.u32 x, %1, 1028;\n\tadd.u32 y, %3, 1028;\n\tmov.b64 da, {x, %2};\n\tmov.b64 db, {y, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, yes;\n\t"
+      "add.u32 x, %1, 1030;\n\tadd.u32 y, %3, 1030;\n\tmov.b64 da, {x, %2};\n\tmov.b64 db, {y, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, yes;\n\t"
+        "}" ::"r"(d), "r"(a0), "r"(a1), "r"(b0), "r"(b1), "r"(id)
         : "memory");
 }
-// O += P V over 64 keys: four steps, V's rows 2 KB apart per step; acc 0: O is
-// overwritten.
+// O += P V over 64 keys: four steps, P in tensor memory, V's rows 2 KB apart
+// per step; acc 0: O is overwritten.
 __device__ __forceinline__ void kp_issue_pv(uint32_t d, uint32_t p, uint64_t b, uint32_t id,
                                             uint32_t acc) {
   const uint32_t b0 = static_cast<uint32_t>(b), b1 = static_cast<uint32_t>(b >> 32);
@@ -353,15 +361,15 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   const uint32_t bar_k_empty = bar_v + 8 * KP_STAGES;
   const uint32_t bar_v_empty = bar_k_empty + 8 * KP_STAGES;
   const uint32_t bar_q = bar_v_empty + 8 * KP_STAGES;
-  const uint32_t bar_s_full = bar_q + 16;
-  const uint32_t bar_p_full = bar_s_full + 16;
-  const uint32_t bar_o_done = bar_p_full + 16;
-  const uint32_t bar_seg = bar_o_done + 16;
+  const uint32_t bar_o_done = bar_q + 16;
+  const uint32_t bar_s_full = bar_o_done + 16;
+  const uint32_t bar_p_full = bar_s_full + 32;
+  const uint32_t bar_seg = bar_p_full + 32;
   const uint32_t bar_seg_empty = bar_seg + 16;
   const uint32_t bar_pg = bar_seg_empty + 16;      // [KP_PG]
   const uint32_t bar_pg_empty = bar_pg + 8 * KP_PG;
   const uint32_t bar_raw = bar_pg_empty + 8 * KP_PG;
-  const uint32_t bar_raw_empty = bar_raw + 8 * KP_RAW;
+  const uint32_t bar_raw_empty = bar_raw + 8 * L::RAW;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::MISC_OFF);
   volatile int* abort = reinterpret_cast<volatile int*>(gbase + L::MISC_OFF + 4);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -455,22 +463,24 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     for (int i = 0; i < KP_STAGES; ++i) {
       mbar_init(bar_k + 8 * i, 4);
       mbar_init(bar_v + 8 * i, 4);
-      mbar_init(bar_k_empty + 8 * i, 1);
-      mbar_init(bar_v_empty + 8 * i, 1);
+      mbar_init(bar_k_empty + 8 * i, 2);
+      mbar_init(bar_v_empty + 8 * i, 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar_q + 8 * i, 4);
-      mbar_init(bar_s_full + 8 * i, 1);
-      mbar_init(bar_p_full + 8 * i, 4);
       mbar_init(bar_o_done + 8 * i, 1);
+      mbar_init(bar_s_full + 16 * i, 1);
+      mbar_init(bar_s_full + 16 * i + 8, 1);
+      mbar_init(bar_p_full + 16 * i, 4);
+      mbar_init(bar_p_full + 16 * i + 8, 4);
       mbar_init(bar_seg + 8 * i, 1);
-      mbar_init(bar_seg_empty + 8 * i, 9);
+      mbar_init(bar_seg_empty + 8 * i, 10);
     }
     for (int i = 0; i < KP_PG; ++i) {
       mbar_init(bar_pg + 8 * i, 1);
       mbar_init(bar_pg_empty + 8 * i, 12);
     }
-    for (int i = 0; i < KP_RAW; ++i) {
+    for (int i = 0; i < L::RAW; ++i) {
       mbar_init(bar_raw + 8 * i, 1);
       mbar_init(bar_raw_empty + 8 * i, 4);
     }
@@ -563,25 +573,34 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         // the page of 16 keys, one per lane; -1: none, or outside the cache
         auto page_of = [&](int j) {
           const int key = (block0 + j) * KP_BK + 16 * lane;
-          return j < count && lane < 8 && key < len ? row[key >> shift] : -1;
+          const int id = j < count && lane < 8 && key < len ? row[key >> shift] : -1;
+          return id < a.v.pages ? id : -1;
         };
-        int next_id = page_of(0);
+        // Ids are read two blocks ahead and scales one: nothing here waits for either.
+        int id1 = page_of(0), id2 = page_of(1);
+        uint32_t kc1 = 0xFFu, vc1 = 0xFFu;
+        auto scales_of = [&](int id) {
+          kc1 = vc1 = 0xFFu;
+          if (id >= 0) {
+            const long long unit = static_cast<long long>(id) * a.v.heads + head;
+            kc1 = a.v.k_scales[unit];
+            vc1 = a.v.v_scales[unit];
+          }
+        };
+        scales_of(id1);
         for (int j = 0; j < count; ++j) {
-          int id = next_id;
-          next_id = page_of(j + 1);            // a block ahead
-          if (id >= a.v.pages) id = -1;
-          long long unit = 0;
+          const int id = id1;
+          const uint32_t kc = kc1, vc = vc1;
+          id1 = id2;
+          id2 = page_of(j + 2);
+          scales_of(id1);
+          const long long unit = id >= 0 ? static_cast<long long>(id) * a.v.heads + head : 0;
           float kf = __uint_as_float(0x7FC00000u);
           int ve = 0;
-          if (id >= 0) {
-            unit = static_cast<long long>(id) * a.v.heads + head;
-            const uint32_t kc = a.v.k_scales[unit], vc = a.v.v_scales[unit];
-            if (kc != 0xFFu && vc != 0xFFu) {
-              kf = kv_scale_value(kc);
-              ve = static_cast<int>(vc);
-            }
+          if (kc != 0xFFu && vc != 0xFFu) {
+            kf = kv_scale_value(kc);
+            ve = static_cast<int>(vc);
           }
-          release(1);
           const int ps = bt & (KP_PG - 1);
           if (!mbar_wait(bar_pg_empty + 8 * ps, ((bt / KP_PG) & 1) ^ 1, abort)) {
             if (lane == 0) kp_timeout(abort, 0x52);
@@ -600,15 +619,16 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             pages[ps].valid = len - (block0 + j) * KP_BK;
           }
           __syncwarp();
-          held = true;
           ++bt;
+          held = true;
+          if (j + 1 < count) release(1);       // (of the last one: when the next segment is known)
           // the codes: a box per page, by the lane of its first 16 keys
           const bool loads = id >= 0 && ((16 * lane) & ((1 << shift) - 1)) == 0;
           const unsigned boxes = __popc(__ballot_sync(0xFFFFFFFFu, loads));
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            const int slot = raw_it % KP_RAW;
-            if (!mbar_wait(bar_raw_empty + 8 * slot, ((raw_it / KP_RAW) & 1) ^ 1, abort)) {
+            const int slot = raw_it % L::RAW;
+            if (!mbar_wait(bar_raw_empty + 8 * slot, ((raw_it / L::RAW) & 1) ^ 1, abort)) {
               if (lane == 0) kp_timeout(abort, 0x5e);
               ok = false;
               break;
@@ -625,19 +645,22 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
       }
       // the CTA may not retire before its copies have landed
-      for (int i = max(0, raw_it - KP_RAW); i < raw_it; ++i) {
+      for (int i = max(0, raw_it - L::RAW); i < raw_it; ++i) {
         const long long t0 = clock64();
-        while (!mbar_try_wait(bar_raw + 8 * (i % KP_RAW), (i / KP_RAW) & 1) &&
+        while (!mbar_try_wait(bar_raw + 8 * (i % L::RAW), (i / L::RAW) & 1) &&
                clock64() - t0 < MXK_WAIT_LIMIT_CYCLES) {
         }
       }
-    } else if (warp == 1) {
-      // ------------------------------------------------------------ MMA issuer
+    } else if (warp <= 2) {
+      // ------------------------------------------------- MMA issuer of tile t
+      const int t = warp - 1;
       const uint32_t id_qk = kp_idesc(KP_HK, 0);
       const uint32_t id_pv = kp_idesc(D, 1);
+      const uint64_t dq = smem_desc(base + L::Q_OFF + t * L::Q_BYTES, 16, 1024, 2);
       const uint64_t dk0 = smem_desc(base + L::K_OFF, 16, 1024, 2);
       const uint64_t dv0 = smem_desc(base + L::V_OFF, L::REGION, 1024, 2);
-      int bt = 0, seg_it = 0, seg1 = 0;      // blocks, units, tile 1's units
+      const uint32_t s_full = bar_s_full + 16 * t, p_full = bar_p_full + 16 * t;
+      int bt = 0, seg_it = 0, own = 0, own_b = 0;   // blocks, units; units and blocks of the tile
       bool ok = true;
       while (ok) {
         const int ss = seg_it & 1;
@@ -647,57 +670,62 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
         const int nkb = segs[ss].count;
         if (nkb == 0) break;
-        const int live = segs[ss].n * a.v.group - segs[ss].row0;
-        const int tiles = live > KP_BQ ? 2 : 1;
+        // tile 1 sits a unit of up to 128 rows out: it only hands the blocks back
+        const bool works = segs[ss].n * a.v.group - segs[ss].row0 > KP_BQ * t;
         ++seg_it;
-        // tile 1 sits a unit of up to 128 rows out: its barriers count its own
-        // units (steps are even in number per unit)
-        for (int t = 0; t < tiles && ok; ++t) {
-          ok = mbar_wait(bar_q + 8 * t, (t ? seg1 : seg_it - 1) & 1, abort);
-          if (!ok) kp_timeout(abort, 0x57);
-        }
-        if (!ok) break;
-        tc_fence_after();
-        // step h: P_h V_h, then the next step's scores over P_h
-        const int steps = 2 * nkb;
-#pragma unroll 1
-        for (int h = -1; h < steps && ok; ++h) {
-          const int n = h + 1;
-          const int sv = (bt + (h >> 1)) % KP_STAGES, sk = (bt + (n >> 1)) % KP_STAGES;
-          const uint64_t dv = dv0 + static_cast<uint64_t>((sv * L::V_BYTES + (h & 1) * 8192) >> 4);
-          const uint64_t dk = dk0 + static_cast<uint64_t>((sk * L::K_BYTES + (n & 1) * 8192) >> 4);
-          if (h >= 0 && !(h & 1))
-            ok = mbar_wait(bar_v + 8 * sv, ((bt + (h >> 1)) / KP_STAGES) & 1, abort);
-          if (n < steps && !(n & 1))
-            ok = ok && mbar_wait(bar_k + 8 * sk, ((bt + (n >> 1)) / KP_STAGES) & 1, abort);
-          if (!ok) {
-            kp_timeout(abort, 0x58);
+        if (works) {
+          if (!mbar_wait(bar_q + 8 * t, own & 1, abort)) {
+            kp_timeout(abort, 0x57);
             break;
           }
+          ++own;
+          tc_fence_after();
+        }
+        // step h: P_h V_h, then the scores of step h + 2 into the same buffer.  The
+        // commit behind the two says that both are done: scores h + 2 complete,
+        // and O with P_h V_h in it (which is all that the last two say, the very
+        // last at its own barrier: the next unit's scores may follow at once).
+        const int steps = 2 * nkb;
 #pragma unroll 1
-          for (int t = 0; t < tiles; ++t) {
-            const uint32_t s_t = tmem_base + 256 * t;        // S, then P; Q behind it, then O
-            if (h >= 0) {
-              if (!mbar_wait(bar_p_full + 8 * t, h & 1, abort)) {
-                kp_timeout(abort, 0x59);
-                ok = false;
-                break;
-              }
+        for (int h = -2; h < steps; ++h) {
+          const int n = h + 2, buf = h & 1;
+          const int gv = bt + (h >> 1), gk = bt + (n >> 1);
+          const int sv = gv % KP_STAGES, sk = gk % KP_STAGES;
+          const uint32_t s_t = tmem_base + 256 * t + KP_HK * buf;
+          if (h >= 0) {
+            if (!buf) ok = mbar_wait(bar_v + 8 * sv, (gv / KP_STAGES) & 1, abort);
+            if (works) {
+              ok = ok && mbar_wait(p_full + 8 * buf, (own_b + (h >> 1)) & 1, abort);
+              if (!ok) break;
               tc_fence_after();
-              kp_issue_pv(s_t + 128, s_t, dv, id_pv, h > 0 ? 1u : 0u);
-              if (n == steps) kp_commit(bar_o_done + 8 * t);
-            }
-            if (n < steps) {
-              tc_fence_after();
-              kp_issue_s<D>(s_t, s_t + 64, dk, id_qk);
-              kp_commit(bar_s_full + 8 * t);
+              kp_issue_pv(tmem_base + 256 * t + 128, s_t,
+                          dv0 + static_cast<uint64_t>((sv * L::V_BYTES + buf * 8192) >> 4), id_pv,
+                          h > 0 ? 1u : 0u);
             }
           }
-          if (h >= 0 && (h & 1)) kp_commit(bar_v_empty + 8 * sv);
-          if (n < steps && (n & 1)) kp_commit(bar_k_empty + 8 * sk);
+          if (n < steps) {
+            if (!buf) ok = ok && mbar_wait(bar_k + 8 * sk, (gk / KP_STAGES) & 1, abort);
+            if (!ok) break;
+            if (works) {
+              tc_fence_after();
+              kp_issue_s<D>(s_t, dq,
+                            dk0 + static_cast<uint64_t>((sk * L::K_BYTES + buf * 8192) >> 4), id_qk);
+            }
+          }
+          if (works) kp_commit(n <= steps ? s_full + 8 * buf : bar_o_done + 8 * t);
+          if (buf) {
+            if (works) {
+              if (h >= 0) kp_commit(bar_v_empty + 8 * sv);
+              if (n < steps) kp_commit(bar_k_empty + 8 * sk);
+            } else if (lane == 0) {
+              if (h >= 0) mbar_arrive(bar_v_empty + 8 * sv);
+              if (n < steps) mbar_arrive(bar_k_empty + 8 * sk);
+            }
+          }
         }
+        if (!ok) kp_timeout(abort, 0x58);
         bt += nkb;
-        seg1 += tiles - 1;
+        if (works) own_b += nkb;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_seg_empty + 8 * ss);
       }
@@ -739,8 +767,8 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     // tiles in the order K, V of each block
 #pragma unroll 1
     for (int tile = 0; pg; ++tile) {
-      const int kv = tile & 1, bt = tile >> 1, st = bt % KP_STAGES, slot = tile % KP_RAW;
-      if (!mbar_wait(bar_raw + 8 * slot, (tile / KP_RAW) & 1, abort)) {
+      const int kv = tile & 1, bt = tile >> 1, st = bt % KP_STAGES, slot = tile % L::RAW;
+      if (!mbar_wait(bar_raw + 8 * slot, (tile / L::RAW) & 1, abort)) {
         if (lane == 0) kp_timeout(abort, 0x5f);
         break;
       }
@@ -795,40 +823,45 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     const int quarter = warp & 3;
     const int urow = KP_BQ * t + 32 * quarter + lane;       // row in the unit
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + 256 * t;
-    int bt = 0, own_seg = 0, seg_it = 0;     // blocks, the tile's own units, all units
-    bool ok = true;
-    while (ok) {
+    // blocks; the tile's own units and, per score buffer, its steps; all units
+    int bt = 0, own_seg = 0, own0 = 0, own1 = 0, seg_it = 0;
+    const uint32_t s_full = bar_s_full + 16 * t;
+    bool ok = true, live = false, works = false;
+    int lo = 0, hi = 0, count = 0, key00 = 0;
+    float fr = 0.0f, m = -INFINITY, l = 0.0f;
+    int ev = 0;                                // V's reference exponent
+    while (true) {
+      // ---- the next unit's rows, before this unit's are written: its first
+      // scores are on their way meanwhile.  (Q is free: the last scores are done.)
       const int ss = seg_it & 1;
       if (!mbar_wait(bar_seg + 8 * ss, (seg_it >> 1) & 1, abort)) {
         if (lane == 0) kp_timeout(abort, 0x5b);
         break;
       }
-      ++seg_it;
-      const int count = segs[ss].count, key00 = segs[ss].block * KP_BK;
-      if (count == 0) break;
-      const bool works = segs[ss].n * a.v.group - segs[ss].row0 > KP_BQ * t;   // the tile has rows
-      // ---- this thread's row: Q to f16, its bounds and factor
-      bool live;
-      int lo, hi;
+      const int next_count = segs[ss].count;
+      const bool next_works = next_count != 0 && segs[ss].n * a.v.group - segs[ss].row0 > KP_BQ * t;
+      bool next_live = false;
+      int next_lo = 0, next_hi = 0;
       float up = 1.0f;
-      {
+      if (next_count != 0) {
+      // this thread's row: Q to f16, its bounds and factor
       KvReq rq;
       rq.q0 = segs[ss].q0;
       rq.n = segs[ss].n;
       rq.len = segs[ss].len;
       const int row = segs[ss].row0 + urow;
-      live = row < rq.n * a.v.group;
-      const int token = live ? row / a.v.group : 0;
-      const int qh = segs[ss].head * a.v.group + (live ? row - token * a.v.group : 0);
-      lo = live ? kv_first_key(a.v, rq, token) : 0;
-      hi = live ? kv_end_key(a.v, rq, token) : 0;
-      if (works) {
+      next_live = row < rq.n * a.v.group;
+      const int token = next_live ? row / a.v.group : 0;
+      const int qh = segs[ss].head * a.v.group + (next_live ? row - token * a.v.group : 0);
+      next_lo = next_live ? kv_first_key(a.v, rq, token) : 0;
+      next_hi = next_live ? kv_end_key(a.v, rq, token) : 0;
+      if (next_works) {
         uint32_t w[D / 2];
         const uint16_t* src = a.Q + (rq.q0 + token) * a.q_ts + qh * a.q_hs;
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
           uint4 v = make_uint4(0, 0, 0, 0);
-          if (live) v = *reinterpret_cast<const uint4*>(src + 8 * c);
+          if (next_live) v = *reinterpret_cast<const uint4*>(src + 8 * c);
           w[4 * c] = v.x;
           w[4 * c + 1] = v.y;
           w[4 * c + 2] = v.z;
@@ -850,31 +883,115 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
           for (int e = 0; e < D / 2; ++e) w[e] ^= 0x80008000u;
         }
-        // the row's D / 2 columns behind the scores
+        const int r = 32 * quarter + lane;
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          tmem_st_32x32b_x32(lane_addr + 64 + 32 * c,
-                             *reinterpret_cast<const uint32_t(*)[32]>(w + 32 * c));
-        tmem_wait_st();
-        tc_fence_before();
+        for (int c = 0; c < D / 8; ++c)
+          st_shared_v4(base + L::Q_OFF + t * L::Q_BYTES + (c >> 3) * L::REGION + r * 128 +
+                           (((c & 7) ^ (r & 7)) << 4),
+                       w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_q + 8 * t);
       }
       }
+      // ---- this unit's rows (none before the first unit)
+      if (works) {
+        if (!mbar_wait(bar_o_done + 8 * t, own_seg & 1, abort)) {
+          if (lane == 0) kp_timeout(abort, 0x5d);
+          break;
+        }
+        ++own_seg;
+        tc_fence_after();
+        // a row that saw keys and adds up to nothing had only scores of -infinity:
+        // 0 / 0, not the 0 of a row that sees none
+        if (l == 0.0f && max(lo, key00) < min(hi, key00 + KP_BK * count))
+          l = __uint_as_float(0x7FC00000u);
+        // to true units: 2^(ev - 127), and the 2^KP_P_EXP out of P
+        const float unit = kv_scale_value(static_cast<uint32_t>(ev));
+        const float inv = (l == 0.0f ? 0.0f : 1.0f / l) * (1.0f / (1 << KP_P_EXP));
+        // (read again rather than kept in registers over the blocks)
+        const volatile KpSeg* sg = segs + (ss ^ 1);
+        float* part = sg->slot >= 0 ? a.ws + static_cast<long long>(sg->slot) * (KP_ROWS * (D + 2)) : nullptr;
+        const int row = sg->row0 + urow, token = row / a.v.group;
+        const long long out =
+            (sg->q0 + token) * a.o_ts + (sg->head * a.v.group + row - token * a.v.group) * a.o_hs;
+        // rows of O 32 bytes at a time where they are that aligned
+        const bool by32 = ((reinterpret_cast<uintptr_t>(a.O) |
+                            static_cast<uintptr_t>(out * (a.o_dtype == DT_F32 ? 4 : 2))) & 31) == 0;
+        const float f = part ? 1.0f / (1 << KP_P_EXP) : inv;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(lane_addr + 128 + 32 * c, o);
+          tmem_wait_ld();
+          if (!live) continue;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f * unit);
+          if (part) {
+            // lanes hold consecutive rows: whole lines of [8 columns][row][column]
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              st_global_v8(part + ((4 * c + e) * KP_ROWS + urow) * 8,
+                           *reinterpret_cast<const uint32_t(*)[8]>(o + 8 * e));
+          } else if (a.o_dtype == DT_F32) {
+            float* dst = static_cast<float*>(a.O) + out + 32 * c;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<uint4*>(dst)[e] =
+                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          } else {
+            uint16_t* dst = static_cast<uint16_t*>(a.O) + out + 32 * c;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float x0 = __uint_as_float(o[16 * h + 2 * e]);
+                const float x1 = __uint_as_float(o[16 * h + 2 * e + 1]);
+                w[e] = a.o_dtype == DT_BF16 ? cvt_bf16x2(x0, x1) : cvt_f16x2(x0, x1);
+              }
+              if (by32) {
+                st_global_v8(dst + 16 * h, w);
+              } else {
+                reinterpret_cast<uint4*>(dst + 16 * h)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                reinterpret_cast<uint4*>(dst + 16 * h)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+              }
+            }
+          }
+        }
+        if (part && live) {
+          part[KP_ROWS * D + urow] = m;
+          part[KP_ROWS * (D + 1) + urow] = l;
+        }
+        tc_fence_before();
+      }
+      if (seg_it > 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_seg_empty + 8 * (ss ^ 1));
+      }
+      ++seg_it;
+      if (next_count == 0) break;
+      live = next_live;
+      works = next_works;
+      lo = next_lo;
+      hi = next_hi;
+      count = next_count;
+      key00 = segs[ss].block * KP_BK;
       // a negative scale has gone into Q: the factor of a score is never negative
-      const float fr = fabsf(a.scale_log2e) * up;
+      fr = fabsf(a.scale_log2e) * up;
       // keys that every live row of this warp sees
       const int all_lo = __reduce_max_sync(0xFFFFFFFFu, live ? lo : 0);
       const int all_hi = __reduce_min_sync(0xFFFFFFFFu, live ? hi : 0x7FFFFFFF);
 
-      float m = -INFINITY, l = 0.0f;
-      int ev = 0;                              // V's reference exponent
+      m = -INFINITY;
+      l = 0.0f;
+      ev = 0;
 #pragma unroll 1
       for (int h = 0; h < 2 * count; ++h) {
         const int g = bt + (h >> 1), ps = g & (KP_PG - 1);
         const int key0 = key00 + KP_HK * h;
         if (!mbar_wait(bar_pg + 8 * ps, (g / KP_PG) & 1, abort) ||
-            (works && !mbar_wait(bar_s_full + 8 * t, h & 1, abort))) {
+            (works && !mbar_wait(s_full + 8 * (h & 1), ((h & 1 ? own1 : own0) + (h >> 1)) & 1, abort))) {
           if (lane == 0) kp_timeout(abort, 0x5c);
           ok = false;
           break;
@@ -888,8 +1005,9 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         const int p0 = 4 * (h & 1);            // the step's first 16 keys in the block
         const int ev_new = max(ev, pg->top);
         uint32_t x0[32], x1[32];
-        tmem_ld_32x32b_x32(lane_addr, x0);
-        tmem_ld_32x32b_x32(lane_addr + 32, x1);
+        const uint32_t s_at = lane_addr + KP_HK * (h & 1);
+        tmem_ld_32x32b_x32(s_at, x0);
+        tmem_ld_32x32b_x32(s_at + 32, x1);
         tmem_wait_ld();
         // Row maximum: of the raw scores of each 16 keys, times their factor.
         // A step that some row does not see whole is scaled and masked first:
@@ -924,7 +1042,14 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         const float m_new = mx > m + KP_LAZY ? mx : m;
         const float alpha = m_new == m ? 1.0f : ex2_approx(m - m_new);
         if (h >= 1 && __any_sync(0xFFFFFFFFu, m_new != m || ev_new != ev)) {
-          // (the product that last wrote O ended before these scores did)
+          // the product that last wrote O, of the step before, is done when the
+          // next step's scores are
+          if (!mbar_wait(s_full + 8 * (~h & 1), ((h & 1 ? own0 : own1) + ((h + 1) >> 1)) & 1, abort)) {
+            if (lane == 0) kp_timeout(abort, 0x5a);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
           const float by = alpha * kv_exp2i(ev - ev_new);
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -970,90 +1095,27 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             unpack2(sum, a0, a1);
             l = fmaf(a0 + a1, __int_as_float((127 - b) << 23), l);
           }
-          tmem_st_32x32b_x16(lane_addr + 16 * c, pk);
+          tmem_st_32x32b_x16(s_at + 16 * c, pk);
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(bar_p_full + 8 * t);
+          mbar_arrive(bar_p_full + 16 * t + 8 * (h & 1));
           if (h & 1) mbar_arrive(bar_pg_empty + 8 * ps);
         }
       }
       bt += count;
       if (!ok) break;
       if (works) {
-        if (!mbar_wait(bar_o_done + 8 * t, own_seg & 1, abort)) {
-          if (lane == 0) kp_timeout(abort, 0x5d);
+        // the phase behind the last scores of buffer 0, before the next unit's
+        if (!mbar_wait(s_full, (own0 + count) & 1, abort)) {
+          if (lane == 0) kp_timeout(abort, 0x5a);
           break;
         }
-        ++own_seg;
-        tc_fence_after();
-        // a row that saw keys and adds up to nothing had only scores of -infinity:
-        // 0 / 0, not the 0 of a row that sees none
-        if (l == 0.0f && max(lo, key00) < min(hi, key00 + KP_BK * count))
-          l = __uint_as_float(0x7FC00000u);
-        // to true units: 2^(ev - 127), and the 2^KP_P_EXP out of P
-        const float unit = kv_scale_value(static_cast<uint32_t>(ev));
-        const float inv = (l == 0.0f ? 0.0f : 1.0f / l) * (1.0f / (1 << KP_P_EXP));
-        // (read again rather than kept in registers over the blocks)
-        const volatile KpSeg* sg = segs + ss;
-        float* part = sg->slot >= 0 ? a.ws + static_cast<long long>(sg->slot) * (KP_ROWS * (D + 2)) : nullptr;
-        const int row = sg->row0 + urow, token = row / a.v.group;
-        const long long out =
-            (sg->q0 + token) * a.o_ts + (sg->head * a.v.group + row - token * a.v.group) * a.o_hs;
-        // rows of O 32 bytes at a time where they are that aligned
-        const bool by32 = ((reinterpret_cast<uintptr_t>(a.O) |
-                            static_cast<uintptr_t>(out * (a.o_dtype == DT_F32 ? 4 : 2))) & 31) == 0;
-        const float f = part ? 1.0f / (1 << KP_P_EXP) : inv;
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld_32x32b_x32(lane_addr + 128 + 32 * c, o);
-          tmem_wait_ld();
-          if (!live) continue;
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f * unit);
-          if (part) {
-            // lanes hold consecutive rows: whole lines of [column][row]
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              reinterpret_cast<uint4*>(part)[(8 * c + e) * KP_ROWS + urow] =
-                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          } else if (a.o_dtype == DT_F32) {
-            float* dst = static_cast<float*>(a.O) + out + 32 * c;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              reinterpret_cast<uint4*>(dst)[e] =
-                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          } else {
-            uint16_t* dst = static_cast<uint16_t*>(a.O) + out + 32 * c;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t w[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float x0 = __uint_as_float(o[16 * h + 2 * e]);
-                const float x1 = __uint_as_float(o[16 * h + 2 * e + 1]);
-                w[e] = a.o_dtype == DT_BF16 ? cvt_bf16x2(x0, x1) : cvt_f16x2(x0, x1);
-              }
-              if (by32) {
-                st_global_v8(dst + 16 * h, w);
-              } else {
-                reinterpret_cast<uint4*>(dst + 16 * h)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                reinterpret_cast<uint4*>(dst + 16 * h)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-              }
-            }
-          }
-        }
-        if (part && live) {
-          part[KP_ROWS * D + urow] = m;
-          part[KP_ROWS * (D + 1) + urow] = l;
-        }
-        tc_fence_before();
+        own0 += count + 1;
+        own1 += count;
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_seg_empty + 8 * ss);
     }
   }
 
@@ -1067,48 +1129,71 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 }
 
 // Join the parts of the unit that begins in CTA blockIdx.x's stretch, in CTA
-// order (the merge of kvattn.cu): a thread per (row, four columns).
+// order: M = max m_p, O = sum 2^(m_p - M) O_p / sum 2^(m_p - M) l_p, with the M so
+// far carried along, so that no load waits for a maximum.  A thread takes
+// eight columns of KPJ_R rows, the lanes four rows of eight such chunks: whole
+// lines of the parts, whose rows stand side by side in 32 bytes, and of O.  (With
+// four columns side by side, half sectors of 16 lines a load, the 2048-token
+// chunk took 226 us instead of 219; one or four rows a thread: 219, 223.)
 constexpr int KPJ_THREADS = 256;
+constexpr int KPJ_R = 2;                       // rows of a thread
 template <int D>
 __global__ void __launch_bounds__(KPJ_THREADS)
 kv_prompt_join_kernel(const KpArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const KpJoin* join = a.joins + blockIdx.x;
   const int live = __ldcg(&join->live);
-  // a warp takes two rows and 64 columns: whole sectors of the parts, whose
-  // rows stand side by side, and 128 bytes or more of each row of O
   const int warp = (blockIdx.y * KPJ_THREADS + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  const int urow = 2 * (warp / (D / 64)) + (lane & 1);
-  const int col = 64 * (warp % (D / 64)) + 4 * (lane >> 1);
-  if (urow >= live) return;
+  const int r0 = 4 * KPJ_R * (warp / (D / 64)) + (lane & 3);
+  const int col = 64 * (warp % (D / 64)) + 8 * (lane >> 2);
+  if (r0 >= live) return;
   constexpr long long PART = KP_ROWS * (D + 2);
   const int n = __ldcg(&join->parts);
   const float* first = a.ws + __ldcg(&join->first_slot) * PART;
   const float* rest = a.ws + 2ll * blockIdx.x * PART;
-  auto part = [&](int p) { return p == 0 ? first : rest + 2 * p * PART; };
-  float top = -INFINITY;
-#pragma unroll 4
-  for (int p = 0; p < n; ++p) top = fmaxf(top, __ldcg(part(p) + KP_ROWS * D + urow));
-  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float sum = 0.0f;
-#pragma unroll 4
-  for (int p = 0; p < n; ++p) {
-    const float mp = __ldcg(part(p) + KP_ROWS * D + urow);
-    const float lp = __ldcg(part(p) + KP_ROWS * (D + 1) + urow);
-    const float4 v = ld_global_cg_f4(part(p) + static_cast<long long>(col) * KP_ROWS + 4 * urow);
-    const float w = mp == top ? 1.0f : ex2_approx(mp - top);
-    sum = fmaf(w, lp, sum);
-    acc.x = fmaf(w, v.x, acc.x);
-    acc.y = fmaf(w, v.y, acc.y);
-    acc.z = fmaf(w, v.z, acc.z);
-    acc.w = fmaf(w, v.w, acc.w);
+  const int row0 = __ldcg(&join->row0), head = __ldcg(&join->head);
+  const long long q0 = __ldcg(&join->q0);
+  float top[KPJ_R], sum[KPJ_R], acc[KPJ_R][8];
+#pragma unroll
+  for (int i = 0; i < KPJ_R; ++i) {
+    top[i] = -INFINITY;
+    sum[i] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[i][e] = 0.0f;
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const int row = __ldcg(&join->row0) + urow;
-  const int token = row / a.v.group;
-  const long long out = (__ldcg(&join->q0) + token) * a.o_ts +
-                        (__ldcg(&join->head) * a.v.group + row - token * a.v.group) * a.o_hs + col;
-  kv_store4(a.O, a.o_dtype, out, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+#pragma unroll 2
+  for (int p = 0; p < n; ++p) {
+    const float* part = p == 0 ? first : rest + 2 * p * PART;
+    float mp[KPJ_R], lp[KPJ_R], v[KPJ_R][8];
+#pragma unroll
+    for (int i = 0; i < KPJ_R; ++i) {
+      const int r = min(r0 + 4 * i, live - 1);           // (a row too many is not stored)
+      mp[i] = __ldcg(part + KP_ROWS * D + r);
+      lp[i] = __ldcg(part + KP_ROWS * (D + 1) + r);
+      ld_global_cg_v8(part + (col / 8 * KP_ROWS + r) * 8, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < KPJ_R; ++i) {
+      const float t = fmaxf(top[i], mp[i]);
+      const float before = top[i] == t ? 1.0f : ex2_approx(top[i] - t);
+      const float w = mp[i] == t ? 1.0f : ex2_approx(mp[i] - t);
+      top[i] = t;
+      sum[i] = fmaf(w, lp[i], sum[i] * before);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[i][e] = fmaf(w, v[i][e], acc[i][e] * before);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < KPJ_R; ++i) {
+    if (r0 + 4 * i >= live) break;
+    const float inv = sum[i] == 0.0f ? 0.0f : 1.0f / sum[i];
+    const int row = row0 + r0 + 4 * i, token = row / a.v.group;
+    const long long out =
+        (q0 + token) * a.o_ts + (head * a.v.group + row - token * a.v.group) * a.o_hs + col;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[i][e] *= inv;
+    kv_store8(a.O, a.o_dtype, out, acc[i]);
+  }
 }
 
 template <int FMT, int D>
@@ -1135,7 +1220,7 @@ cudaError_t kp_run(const CUtensorMap& tk, const CUtensorMap& tv, const KpArgs& a
   e = cudaGetLastError();
   if (e != cudaSuccess || a.ws == nullptr) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sms, KP_ROWS * (D / 4) / KPJ_THREADS);
+  cfg.gridDim = dim3(sms, KP_ROWS * (D / 8) / (KPJ_THREADS * KPJ_R));
   cfg.blockDim = dim3(KPJ_THREADS);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -1151,7 +1236,7 @@ cudaError_t kp_run(const CUtensorMap& tk, const CUtensorMap& tv, const KpArgs& a
 int64_t kv_prompt_max_requests() { return KP_MAX_REQUESTS; }
 
 size_t kv_prompt_workspace_bytes(int64_t d, int sms) {
-  return static_cast<size_t>(sms) * (2 * KP_ROWS * (d + 2) * 4 + sizeof(KpJoin));
+  return static_cast<size_t>(sms) * (2 * KP_ROWS * (d + 2) * 4 + sizeof(KpJoin)) + 16;
 }
 
 cudaError_t launch_kv_prompt(const KvAttn& q, int sms, cudaStream_t st) {
@@ -1168,9 +1253,10 @@ cudaError_t launch_kv_prompt(const KvAttn& q, int sms, cudaStream_t st) {
   a.o_dtype = q.o_dtype;
   a.scale_log2e = q.scale * 1.4426950408889634f;
   if (q.ws && q.ws_bytes >= kv_prompt_workspace_bytes(c.d, sms)) {
-    a.ws = static_cast<float*>(q.ws);
-    a.joins = reinterpret_cast<KpJoin*>(static_cast<char*>(q.ws) +
-                                        static_cast<int64_t>(sms) * 2 * KP_ROWS * (c.d + 2) * 4);
+    // the parts from a 32-byte boundary on
+    char* ws = static_cast<char*>(q.ws) + (reinterpret_cast<uintptr_t>(q.ws) & 16);
+    a.ws = reinterpret_cast<float*>(ws);
+    a.joins = reinterpret_cast<KpJoin*>(ws + static_cast<int64_t>(sms) * 2 * KP_ROWS * (c.d + 2) * 4);
   }
   CUtensorMap tk, tv;
   if (!kv_tensor_map(&tk, c.k, c) || !kv_tensor_map(&tv, c.v, c)) return cudaErrorInvalidValue;

@@ -208,6 +208,15 @@ __device__ __forceinline__ float4 ld_global_cg_f4(const float* p) {
   return v;
 }
 
+// 32-byte aligned.
+__device__ __forceinline__ void ld_global_cg_v8(const float* p, float (&v)[8]) {
+  asm volatile("ld.global.cg.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                 "=f"(v[6]), "=f"(v[7])
+               : "l"(p)
+               : "memory");
+}
+
 // ------------------------------------------------------------------ tcgen05
 
 // true in exactly one lane of the (converged) warp: the lowest active one
