@@ -46,9 +46,9 @@
 // and one CTA did all the adding.)  Every wait is bounded.
 //
 // Measured: 64 requests of 8192 keys (32 heads on 8 cache heads of 128, E4M3)
-// 168 us, 6.4 TB/s, 0.94 of the copy rate; one of 131072 keys 55 us, of which
-// about 10 are the start and the join; 256 of up to 4096 keys, a head of 64 to
-// each cache head, int8, pages of 16, 205 us, 5.3 TB/s.
+// 168 us, 6.4 TB/s, 0.94 of the copy rate; one of 131072 keys 50 us, of which
+// about 7 are the start and the join; 256 of up to 4096 keys, a head of 64 to
+// each cache head, int8, pages of 16, 204 us, 5.3 TB/s.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -901,88 +901,100 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
 }
 
 // Join the parts of the unit that begins in main CTA blockIdx.x's stretch:
-// M = max m_p, O = sum 2^(m_p - M) O_p / sum 2^(m_p - M) l_p, parts in CTA
-// order.  One block per (unit, 32 columns); a thread takes a row and four
-// columns, and where a unit has few rows, groups of threads share its parts.
+// M = max m_p, O = sum 2^(m_p - M) O_p / sum 2^(m_p - M) l_p.  One block per (unit,
+// 32 columns); a thread takes a row and four columns of every groups-th part,
+// with the M so far carried along, so that no load waits for a maximum, and
+// the groups' sums meet in shared memory, in order.  Latency bounds it: two
+// reads in a row, what to join and the parts.  (With the maxima read first, then
+// the weights, then the parts, one request of 131072 keys took 54.5 us, now 50.2;
+// batches of eight parts 49.2, but 48 requests of four drafts 53.7 instead of
+// 52.6; 256 threads, which leave the main kernel's last CTAs less room, 58.)
 // Reads of the parts go around L1 (another kernel wrote them).
 constexpr int KJ_THREADS = 128;
 template <int D, int ROWS>
 __global__ void __launch_bounds__(KJ_THREADS)
 kv_join_kernel(const float* __restrict__ ws, const KaJoin<ROWS>* joins, void* O, int o_dtype) {
-  constexpr int BATCH = 64, J = KJ_THREADS / ROWS;
+  constexpr int BATCH = 4, GROUPS = 16;
   constexpr long long PART = ROWS * (D + 2);
-  __shared__ float sm_w[BATCH * ROWS];
-  __shared__ float sm_r[J * ROWS];
+  __shared__ float sm_m[KJ_THREADS], sm_l[KJ_THREADS];
   __shared__ float4 sm_acc[KJ_THREADS];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const KaJoin<ROWS>* join = joins + blockIdx.x;
-  const int live = __ldcg(&join->live);
+  const int4 head = __ldcg(reinterpret_cast<const int4*>(join));
+  const int live = head.x, n = head.y;
   if (live == 0) return;
-  const int n = __ldcg(&join->parts);
-  const float* first = ws + __ldcg(&join->first_slot) * PART;
-  const float* rest = ws + 2ll * blockIdx.x * PART;    // part p > 0: slot 2 (CTA + p)
-  auto at = [&](int p) { return p == 0 ? first : rest + 2 * p * PART; };
   const int tid = threadIdx.x;
-  // thread (r, j) looks after row r of parts j, j + J, ..
-  const int r = tid & (ROWS - 1), j = tid / ROWS;
-  float top = -INFINITY;
-  for (int p = j; p < n; p += J) top = fmaxf(top, __ldcg(at(p) + ROWS * D + r));
-  sm_r[j * ROWS + r] = top;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < J; ++i) top = fmaxf(top, sm_r[i * ROWS + r]);
   const int items = live * 8;                          // (row, 4 columns)
-  int groups = 1;
-  while (groups * 2 * items <= KJ_THREADS) groups *= 2;
+  const int groups = min(min(KJ_THREADS / items, GROUPS), n);
   const int grp = tid / items;                         // >= groups: no part of the sum
   const int row = (tid - grp * items) >> 3;
   const int col = 32 * blockIdx.y + 4 * (tid & 7);
+  const long long out = __ldcg(&join->out[row]);
+  const float* first = ws + head.z * PART;
+  const float* rest = ws + 2ll * blockIdx.x * PART;    // part p > 0: slot 2 (CTA + p)
+  float top = -INFINITY, sum = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float ls = 0.0f;
-  for (int p0 = 0; p0 < n; p0 += BATCH) {
-    const int batch = min(BATCH, n - p0);
-    __syncthreads();                                   // sm_r and the last batch are read
-    for (int p = j; p < batch; p += J) {
-      const float* part = at(p0 + p) + ROWS * D + r;
-      const float mp = __ldcg(part), lp = __ldcg(part + ROWS);
-      const float w = mp == top ? 1.0f : ex2_approx(mp - top);
-      sm_w[p * ROWS + r] = w;
-      ls = fmaf(w, lp, ls);
-    }
-    __syncthreads();
-    if (grp < groups) {
-#pragma unroll 8
-      for (int p = grp; p < batch; p += groups) {
-        const float w = sm_w[p * ROWS + row];
-        const float4 v = ld_global_cg_f4(at(p0 + p) + row * D + col);
-        acc.x = fmaf(w, v.x, acc.x);
-        acc.y = fmaf(w, v.y, acc.y);
-        acc.z = fmaf(w, v.z, acc.z);
-        acc.w = fmaf(w, v.w, acc.w);
+  if (grp < groups)
+    for (int p0 = grp; p0 < n; p0 += BATCH * groups) {
+      float m[BATCH], l[BATCH];
+      float4 v[BATCH];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int p = p0 + i * groups;
+        if (p >= n) break;
+        const float* part = p == 0 ? first : rest + 2 * p * PART;
+        m[i] = __ldcg(part + ROWS * D + row);
+        l[i] = __ldcg(part + ROWS * (D + 1) + row);
+        v[i] = ld_global_cg_f4(part + row * D + col);
       }
+      float t = top;
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i)
+        if (p0 + i * groups < n) t = fmaxf(t, m[i]);
+      const float before = top == t ? 1.0f : ex2_approx(top - t);
+      top = t;
+      sum *= before;
+      acc.x *= before;
+      acc.y *= before;
+      acc.z *= before;
+      acc.w *= before;
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i)
+        if (p0 + i * groups < n) {
+          const float w = m[i] == t ? 1.0f : ex2_approx(m[i] - t);
+          sum = fmaf(w, l[i], sum);
+          acc.x = fmaf(w, v[i].x, acc.x);
+          acc.y = fmaf(w, v[i].y, acc.y);
+          acc.z = fmaf(w, v[i].z, acc.z);
+          acc.w = fmaf(w, v[i].w, acc.w);
+        }
     }
-  }
-  __syncthreads();
-  sm_r[j * ROWS + r] = ls;
+  sm_m[tid] = top;
+  sm_l[tid] = sum;
   sm_acc[tid] = acc;
   __syncthreads();
   if (tid >= items) return;
-  for (int i = 1; i < groups; ++i) {
+  float t = top;
+  for (int i = 1; i < groups; ++i) t = fmaxf(t, sm_m[i * items + tid]);
+  sum = 0.0f;
+  acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int i = 0; i < groups; ++i) {
+    const float mi = sm_m[i * items + tid];
+    const float w = mi == t ? 1.0f : ex2_approx(mi - t);
     const float4 u = sm_acc[i * items + tid];
-    acc.x += u.x;
-    acc.y += u.y;
-    acc.z += u.z;
-    acc.w += u.w;
+    sum = fmaf(w, sm_l[i * items + tid], sum);
+    acc.x = fmaf(w, u.x, acc.x);
+    acc.y = fmaf(w, u.y, acc.y);
+    acc.z = fmaf(w, u.z, acc.z);
+    acc.w = fmaf(w, u.w, acc.w);
   }
-  float sum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < J; ++i) sum += sm_r[i * ROWS + row];
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   acc.x *= inv;
   acc.y *= inv;
   acc.z *= inv;
   acc.w *= inv;
-  kv_store4(O, o_dtype, __ldcg(&join->out[row]) + col, acc);
+  kv_store4(O, o_dtype, out + col, acc);
 }
 
 int ka_sm_count() {
