@@ -74,8 +74,9 @@ constexpr int KP_REGS_CONV = 88;           // warpgroup 3
 constexpr int KP_TMEM_COLS = 512;
 constexpr float KP_LAZY = 8.0f;            // slack of the exponentials' reference point
 constexpr int KP_P_EXP = 7;                // P is scaled by 2^7: at most 2^(7 + 8) in f16
-// Entries of a unit besides its blocks: with 1, 2, 4 and 8 the 2048-token chunk
-// took 242, 239, 237 and 241 us and eight ragged chunks 80, 68, 65 and 72.
+// Entries of a unit besides its blocks: with 1, 2, 4 and 8 eight ragged chunks
+// took 80, 68, 65 and 72 us when the 2048-token chunk took 242, 239, 237 and 241
+// (now 219 with 2, 3, 4 and 6 alike).
 constexpr int KP_OVER = 4;
 constexpr int KP_PG = 8;                   // blocks whose page data is kept
 constexpr int KP_STAGES = 2;               // f16 tiles of K, and of V
