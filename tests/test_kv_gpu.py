@@ -479,6 +479,21 @@ def test_attention_strided_and_offsets_beyond_requests():
     assert s.run().shape == want.shape
 
 
+@pytest.mark.parametrize("news", [[1], [60]])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_workspace_alignment(news, d):
+    """A workspace of exactly the stated size, 16-byte aligned and no more."""
+    s = Setup(mx.E4M3, 64, 2, d, [5000], news, group=2)
+    want = s.run()
+    n = mx.kv_attention_workspace_bytes(4, 2, d, news[0])
+    guard = torch.full((n + 64,), 0x5A, dtype=torch.uint8, device="cuda")
+    got = mx.mx_kv_attention(s.q, s.cache, _i32(s.table), _i32(s.lens), _i32(s.cu), news[0],
+                             workspace=guard[16:16 + n])
+    torch.cuda.synchronize()
+    assert mx.mx_last_error() == 0 and torch.equal(got, want)
+    assert (guard[:16] == 0x5A).all() and (guard[16 + n:] == 0x5A).all()
+
+
 def test_attention_without_rows():
     s = Setup(mx.E4M3, 16, 2, 64, [10, 0], [0, 0], spare=2)
     q = torch.empty(0, 4, 64, dtype=BF, device="cuda")
