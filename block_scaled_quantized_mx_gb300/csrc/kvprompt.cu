@@ -713,7 +713,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                             dk0 + static_cast<uint64_t>((sk * L::K_BYTES + buf * 8192) >> 4), id_qk);
             }
           }
-          if (works) kp_commit(n <= steps ? s_full + 8 * buf : bar_o_done + 8 * t);
+          if (works && n <= steps) kp_commit(s_full + 8 * buf);
           if (buf) {
             if (works) {
               if (h >= 0) kp_commit(bar_v_empty + 8 * sv);
@@ -723,6 +723,8 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
               if (n < steps) mbar_arrive(bar_k_empty + 8 * sk);
             }
           }
+          // O's word comes last: who has heard it may leave
+          if (works && n > steps) kp_commit(bar_o_done + 8 * t);
         }
         if (!ok) kp_timeout(abort, 0x58);
         bt += nkb;
