@@ -847,55 +847,55 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       int next_lo = 0, next_hi = 0;
       float up = 1.0f;
       if (next_count != 0) {
-      // this thread's row: Q to f16, its bounds and factor
-      KvReq rq;
-      rq.q0 = segs[ss].q0;
-      rq.n = segs[ss].n;
-      rq.len = segs[ss].len;
-      const int row = segs[ss].row0 + urow;
-      next_live = row < rq.n * a.v.group;
-      const int token = next_live ? row / a.v.group : 0;
-      const int qh = segs[ss].head * a.v.group + (next_live ? row - token * a.v.group : 0);
-      next_lo = next_live ? kv_first_key(a.v, rq, token) : 0;
-      next_hi = next_live ? kv_end_key(a.v, rq, token) : 0;
-      if (next_works) {
-        uint32_t w[D / 2];
-        const uint16_t* src = a.Q + (rq.q0 + token) * a.q_ts + qh * a.q_hs;
+        // this thread's row: Q to f16, its bounds and factor
+        KvReq rq;
+        rq.q0 = segs[ss].q0;
+        rq.n = segs[ss].n;
+        rq.len = segs[ss].len;
+        const int row = segs[ss].row0 + urow;
+        next_live = row < rq.n * a.v.group;
+        const int token = next_live ? row / a.v.group : 0;
+        const int qh = segs[ss].head * a.v.group + (next_live ? row - token * a.v.group : 0);
+        next_lo = next_live ? kv_first_key(a.v, rq, token) : 0;
+        next_hi = next_live ? kv_end_key(a.v, rq, token) : 0;
+        if (next_works) {
+          uint32_t w[D / 2];
+          const uint16_t* src = a.Q + (rq.q0 + token) * a.q_ts + qh * a.q_hs;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (next_live) v = *reinterpret_cast<const uint4*>(src + 8 * c);
-          w[4 * c] = v.x;
-          w[4 * c + 1] = v.y;
-          w[4 * c + 2] = v.z;
-          w[4 * c + 3] = v.w;
+          for (int c = 0; c < D / 8; ++c) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (next_live) v = *reinterpret_cast<const uint4*>(src + 8 * c);
+            w[4 * c] = v.x;
+            w[4 * c + 1] = v.y;
+            w[4 * c + 2] = v.z;
+            w[4 * c + 3] = v.w;
+          }
+          if (a.bf16) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < D / 2; ++e)
+              top = max(top, max((w[e] << 16) & 0x7FFFFFFFu, w[e] & 0x7FFF0000u));
+            float down;
+            kv_row_factors(top, down, up);
+            if (a.scale_log2e < 0.0f) down = -down;
+#pragma unroll
+            for (int e = 0; e < D / 2; ++e)
+              w[e] = cvt_f16x2(__uint_as_float(w[e] << 16) * down,
+                               __uint_as_float(w[e] & 0xFFFF0000u) * down);
+          } else if (a.scale_log2e < 0.0f) {
+#pragma unroll
+            for (int e = 0; e < D / 2; ++e) w[e] ^= 0x80008000u;
+          }
+          const int r = 32 * quarter + lane;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c)
+            st_shared_v4(base + L::Q_OFF + t * L::Q_BYTES + (c >> 3) * L::REGION + r * 128 +
+                             (((c & 7) ^ (r & 7)) << 4),
+                         w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_q + 8 * t);
         }
-        if (a.bf16) {
-          uint32_t top = 0;
-#pragma unroll
-          for (int e = 0; e < D / 2; ++e)
-            top = max(top, max((w[e] << 16) & 0x7FFFFFFFu, w[e] & 0x7FFF0000u));
-          float down;
-          kv_row_factors(top, down, up);
-          if (a.scale_log2e < 0.0f) down = -down;
-#pragma unroll
-          for (int e = 0; e < D / 2; ++e)
-            w[e] = cvt_f16x2(__uint_as_float(w[e] << 16) * down,
-                             __uint_as_float(w[e] & 0xFFFF0000u) * down);
-        } else if (a.scale_log2e < 0.0f) {
-#pragma unroll
-          for (int e = 0; e < D / 2; ++e) w[e] ^= 0x80008000u;
-        }
-        const int r = 32 * quarter + lane;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          st_shared_v4(base + L::Q_OFF + t * L::Q_BYTES + (c >> 3) * L::REGION + r * 128 +
-                           (((c & 7) ^ (r & 7)) << 4),
-                       w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_q + 8 * t);
-      }
       }
       // ---- this unit's rows (none before the first unit)
       if (works) {
