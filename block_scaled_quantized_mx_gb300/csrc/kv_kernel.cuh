@@ -94,6 +94,17 @@ __device__ __forceinline__ float kv_exp2i(int e) {
   return e < -126 ? 0.0f : __uint_as_float(static_cast<uint32_t>(min(e, 127) + 127) << 23);
 }
 
+// The maximum that a part states for a row whose scores it saw are all
+// -infinity: they weigh nothing beside any finite score of another part, and
+// where no part has one the row is 0 / 0.  (A row that a part shows no key has -infinity.)
+constexpr float KV_ALL_MINUS_INF = -3.402823466e38f;
+
+// 1 / (the sum of a row's weights): 0 for a row that saw no key, NaN for one
+// whose every score was -infinity.
+__device__ __forceinline__ float kv_inverse(float sum, bool saw_keys) {
+  return sum != 0.0f ? 1.0f / sum : saw_keys ? __uint_as_float(0x7FC00000u) : 0.0f;
+}
+
 // For a row whose largest |value| has the bit pattern `top`: powers of two
 // that bring it into [1, 2) and back.  Rows of zeros, infinities and NaN
 // stay as they are.

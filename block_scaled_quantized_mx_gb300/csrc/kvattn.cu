@@ -726,6 +726,12 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
             }
           }
         }
+        // (scores of -infinity weigh nothing, also where there is no other yet)
+        float m_use[NR][2];
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) m_use[nr][e] = m[nr][e] == -INFINITY ? 0.0f : m[nr][e];
         // ---- probabilities and the product with V, a step of 16 keys at a time
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
@@ -740,7 +746,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
               float p[2], q[2];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                p[e] = ex2_approx(x[s][nr][2 * h + e] - m[nr][e]);
+                p[e] = ex2_approx(x[s][nr][2 * h + e] - m_use[nr][e]);
                 q[e] = p[e] * vf;
                 if (masked) {
                   const int j = key0 + 16 * s + g + 8 * h;
@@ -848,7 +854,9 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
         const float mw = sm_m[w * ROWS + rr];
         lsum += sm_l[w * ROWS + rr] * (mw == M ? 1.0f : ex2_approx(mw - M));
       }
-      const float inv = lsum == 0.0f ? 0.0f : 1.0f / lsum;
+      const bool saw = max(seg->lo[rr], seg->tile * TK) < min(seg->hi[rr], (seg->tile + seg->count) * TK);
+      const float inv = kv_inverse(lsum, saw);
+      if (lsum == 0.0f && saw) M = KV_ALL_MINUS_INF;
       const long long out = seg->out[rr];
       // rounds over 4 columns of each of the 8 chunks
 #pragma unroll
@@ -989,7 +997,7 @@ kv_join_kernel(const float* __restrict__ ws, const KaJoin<ROWS>* joins, void* O,
     acc.z = fmaf(w, u.z, acc.z);
     acc.w = fmaf(w, u.w, acc.w);
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const float inv = kv_inverse(sum, t != -INFINITY);
   acc.x *= inv;
   acc.y *= inv;
   acc.z *= inv;

@@ -905,13 +905,11 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
         ++own_seg;
         tc_fence_after();
-        // a row that saw keys and adds up to nothing had only scores of -infinity:
-        // 0 / 0, not the 0 of a row that sees none
-        if (l == 0.0f && max(lo, key00) < min(hi, key00 + KP_BK * count))
-          l = __uint_as_float(0x7FC00000u);
+        // a row that saw keys and adds up to nothing had only scores of -infinity
+        const bool saw = max(lo, key00) < min(hi, key00 + KP_BK * count);
         // to true units: 2^(ev - 127), and the 2^KP_P_EXP out of P
         const float unit = kv_scale_value(static_cast<uint32_t>(ev));
-        const float inv = (l == 0.0f ? 0.0f : 1.0f / l) * (1.0f / (1 << KP_P_EXP));
+        const float inv = kv_inverse(l, saw) * (1.0f / (1 << KP_P_EXP));
         // (read again rather than kept in registers over the blocks)
         const volatile KpSeg* sg = segs + (ss ^ 1);
         float* part = sg->slot >= 0 ? a.ws + static_cast<long long>(sg->slot) * (KP_ROWS * (D + 2)) : nullptr;
@@ -963,7 +961,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           }
         }
         if (part && live) {
-          part[KP_ROWS * D + urow] = m;
+          part[KP_ROWS * D + urow] = l == 0.0f && saw ? KV_ALL_MINUS_INF : m;
           part[KP_ROWS * (D + 1) + urow] = l;
         }
         tc_fence_before();
@@ -1189,7 +1187,7 @@ kv_prompt_join_kernel(const KpArgs a) {
 #pragma unroll
   for (int i = 0; i < KPJ_R; ++i) {
     if (r0 + 4 * i >= live) break;
-    const float inv = sum[i] == 0.0f ? 0.0f : 1.0f / sum[i];
+    const float inv = kv_inverse(sum[i], top[i] != -INFINITY);
     const int row = row0 + r0 + 4 * i, token = row / a.v.group;
     const long long out =
         (q0 + token) * a.o_ts + (head * a.v.group + row - token * a.v.group) * a.o_hs + col;
