@@ -94,15 +94,63 @@ __device__ __forceinline__ float kv_exp2i(int e) {
   return e < -126 ? 0.0f : __uint_as_float(static_cast<uint32_t>(min(e, 127) + 127) << 23);
 }
 
-// The maximum that a part states for a row whose scores it saw are all
-// -infinity: they weigh nothing beside any finite score of another part, and
-// where no part has one the row is 0 / 0.  (A row that a part shows no key has -infinity.)
-constexpr float KV_ALL_MINUS_INF = -3.402823466e38f;
+// A row's running maximum before its first score above -infinity.  Finite, so that
+// x_j - m stays -infinity for scores of -infinity, hidden or real: they weigh
+// nothing, whatever comes beside them.  A part states it for a row that saw such
+// scores only, and -infinity for a row that saw none: where no part has another
+// maximum, the first is 0 / 0 and the second 0.
+constexpr float KV_NO_MAX = -3.402823466e38f;
 
 // 1 / (the sum of a row's weights): 0 for a row that saw no key, NaN for one
 // whose every score was -infinity.
 __device__ __forceinline__ float kv_inverse(float sum, bool saw_keys) {
   return sum != 0.0f ? 1.0f / sum : saw_keys ? __uint_as_float(0x7FC00000u) : 0.0f;
+}
+
+// The exponents of P.  A row's weights are 2^(x_j - m), and V's pages have scales
+// 2^(e_j - 127) of any size, so that neither the largest weight nor the largest
+// scale says which products matter.  P is rounded to f16 as
+//   2^(x_j - m + e_j - v + 7),
+// where v is at least the largest x_j - m + e_j of the keys that the row itself
+// sees, less KV_LAZY, and at most that rounded up: the product that weighs most
+// stands between 2^6 and 2^15.  Keys that a row does not see, and pages of large
+// values that it gives no weight, leave the others' precision alone.  m and v are
+// whole numbers: moving either is exact, and so is what the sum of the weights
+// takes out again, 2^(e_j - v + 7).
+constexpr float KV_LAZY = 8.0f;            // slack of m and of v
+constexpr int KV_P_EXP = 7;
+constexpr float KV_NO_V = -300.0f;         // v of a row that has seen nothing: below every other
+
+// m for a row whose next scores are x_top at most.
+__device__ __forceinline__ float kv_next_m(float m, float x_top) {
+  return x_top > m + KV_LAZY ? ceilf(x_top) : m;
+}
+// v for a row whose m moved by dm = m_old - m_new, to the next keys' largest
+// x_j - m_new + e_j.
+__device__ __forceinline__ float kv_next_v(float v, float dm, float top) {
+  const float r = fmaxf(v + dm, KV_NO_V);
+  return top > r + KV_LAZY ? ceilf(top) : r;
+}
+
+// What O, in units of 2^v_old at m_old, is multiplied by when they become v and m.
+__device__ __forceinline__ float kv_move_o(float m_old, float m_new, float v_old, float v_new) {
+  return ex2_approx((m_old - m_new) + (v_old - v_new));
+}
+
+// e_j - v + 7 of a page.  Below 2^-60 P is 0 in f16 whatever it is exactly, and
+// the sum still gets the weight.
+__device__ __forceinline__ float kv_p_shift(float e, float v) {
+  return fmaxf(e - v + static_cast<float>(KV_P_EXP), -60.0f);
+}
+
+// 2^-b for such a whole number b (0 beyond 126: weights of less than 2^-110).
+__device__ __forceinline__ float kv_unshift(float b) { return ex2_approx(-b); }
+
+// The unit of O, 2^(v - 127 - 7), as two factors: v goes from -16 to 262.
+__device__ __forceinline__ void kv_o_unit(float v, float& f0, float& f1) {
+  const int e = static_cast<int>(v) - 127 - KV_P_EXP, half = e >> 1;
+  f0 = kv_exp2i(half);
+  f1 = kv_exp2i(e - half);
 }
 
 // For a row whose largest |value| has the bit pattern `top`: powers of two

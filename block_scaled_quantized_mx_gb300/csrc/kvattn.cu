@@ -23,19 +23,18 @@
 //     and the query rows as the 8 columns.  The contraction order is permuted
 //     so that a lane's consecutive codes of a key are its share of the
 //     operand: K needs no transposition, V a byte permute, P one movmatrix;
-//   * page scales never touch the codes: K's multiplies the score, V's the
-//     probability, which as a power of two is exact.
+//   * page scales never touch the codes: K's multiplies the score, V's goes into
+//     the probability's exponent, which as a power of two is exact.
 // With rows as the narrow side of the product, eight rows (a group of up to
 // eight heads) cost half the products, exponentials and registers of sixteen:
 // the kernel comes with 8 rows (three CTAs an SM) and 16 (two CTAs).
 //
 // Precision.  Q is brought to f16 with a power of two per row (so that its
 // largest value is in [1, 2): what f16 drops is 2^-25 of it, as fp32
-// accumulation would), scores, sums and outputs accumulate in fp32, and P is
-// rounded to f16 (relative 2^-11 of each weight at most).  P carries V's scale
-// relative to the largest so far: p 2^(7 + s - s_max), at most 2^15 with the
-// exponentials' slack of 2^8, so that a page whose values are 2^20 smaller than
-// another's still contributes with full precision.
+// accumulation would), scores, sums and outputs accumulate in fp32, and P, with
+// V's scale in its exponent (kv_kernel.cuh), is rounded to f16: relative 2^-11 of
+// a weight, or 2^-28 of the row's largest product of a weight and a scale (2^-25 of
+// P that is 2^3 at least for that product).
 //
 // A unit cut between CTAs leaves its parts (un-normalised O, maximum, sum) in
 // the workspace, and a second, small kernel joins them in a fixed order.  It
@@ -69,8 +68,10 @@ __device__ unsigned int g_status_kv = 0;
 constexpr int KA_WARPS = 4;                // consumer warps
 constexpr int KA_CONS = 32 * KA_WARPS;
 constexpr int KA_THREADS = KA_CONS + 32;
-constexpr float KA_LAZY = 8.0f;            // slack of the exponentials' reference point
-constexpr int KA_P_EXP = 7;                // P is scaled by 2^7: at most 2^(7 + 8) in f16
+// V's scales within 2^3 of each other count as the largest of them in a step: the
+// row's largest product is then 2^3 instead of 2^6 at least, still 2^17 above
+// the smallest normal f16.
+constexpr int KA_ALIKE = 3;
 constexpr int KA_RED = 36;                 // floats per row of the staging: 32, padded
 
 // Keys per tile: 16 KB of codes of K and as many of V.  (128 keys of 64 values a
@@ -96,7 +97,7 @@ struct KaSeg {
   int any_lo, any_hi;          // keys that some row sees
   int part;                    // the unit is shared with other CTAs
   int slot;                    // workspace slot of the part
-  float fr[ROWS];              // scale * log2 e * the row's power of two
+  alignas(8) float fr[ROWS];   // scale * log2 e * the row's power of two
   int lo[ROWS], hi[ROWS];      // keys [lo, hi) that the row sees
   long long out[ROWS];         // the row's first element of O
 };
@@ -128,8 +129,8 @@ struct KaSmem {
   static constexpr int Q_SLOT = NR * (D / 32) * 512;
   static constexpr int SEG_OFF = Q_OFF + 2 * Q_SLOT;
   static constexpr int SEG_BYTES = (sizeof(KaSeg<ROWS>) + 15) / 16 * 16;
-  static constexpr int ML_OFF = SEG_OFF + 2 * SEG_BYTES;     // m, l: [2][warp][row], e: [warp]
-  static constexpr int PG_OFF = ML_OFF + 2 * KA_WARPS * ROWS * 4 + 16;
+  static constexpr int ML_OFF = SEG_OFF + 2 * SEG_BYTES;     // (m, v): [warp][row]; l: [warp][row]
+  static constexpr int PG_OFF = ML_OFF + 3 * KA_WARPS * ROWS * 4;
   static constexpr int PG_STAGE = MAX_PAGES * 8;             // per page: K scale, V exponent
   static constexpr int BAR_OFF = PG_OFF + STAGES * PG_STAGE;
   static constexpr int MISC_OFF = BAR_OFF + STAGES * 16 + 32;
@@ -241,6 +242,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t r) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(r));
   return d;
+}
+
+// The maximum of a row's values over the warp's keys (the lanes of one t).
+__device__ __forceinline__ float ka_over_keys(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+  return fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
 }
 
 // All consumer threads' verdict: true if it is true for each of them.
@@ -442,12 +450,15 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
           tma_load_2d(base + st * 2 * L::TILE + (is_v ? L::TILE : 0) + slot * (D << shift),
                       is_v ? &tmV : &tmK, full, 0, y);
         }
-        // K's scale as a factor; V's as its code, 0xFF for NaN and -1 for a page
-        // that was not loaded (its codes must not be used)
+        // K's scale as a factor, NaN where V's is (the two halves of the lanes tell
+        // each other); V's as its code, -1 for a page that was not loaded (its
+        // codes must not be used)
+        const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, code, L::MAX_PAGES);
         if (lane < 2 * L::MAX_PAGES && slot < per_tile) {
           uint32_t* pg = reinterpret_cast<uint32_t*>(gbase + L::PG_OFF + st * L::PG_STAGE);
           pg[2 * slot + (is_v ? 1 : 0)] =
-              is_v ? (id0 >= 0 ? code : 0xFFFFFFFFu) : __float_as_uint(kv_scale_value(code));
+              is_v ? (id0 >= 0 ? code : 0xFFFFFFFFu)
+                   : __float_as_uint(kv_scale_value(other == 0xFFu ? 0xFFu : code));
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(full);
@@ -577,9 +588,8 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
   constexpr int CHUNKS = D / 64;              // 16-byte chunks of a key per lane
   constexpr int MT = D / 16;                  // 16-column tiles of O
   float* red = reinterpret_cast<float*>(gbase + L::RED_OFF);
-  float* sm_m = reinterpret_cast<float*>(gbase + L::ML_OFF);
-  float* sm_l = sm_m + KA_WARPS * ROWS;
-  int* sm_e = reinterpret_cast<int*>(sm_l + KA_WARPS * ROWS);
+  float2* sm_mv = reinterpret_cast<float2*>(gbase + L::ML_OFF);
+  float* sm_l = reinterpret_cast<float*>(sm_mv + KA_WARPS * ROWS);
   int it = 0, seg_it = 0;
   bool ok = true;
   while (true) {
@@ -596,25 +606,45 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
     if (count == 0) break;
     const int tile0 = seg->tile, len = seg->len;
     const int all_lo = seg->all_lo, all_hi = seg->all_hi, any_lo = seg->any_lo, any_hi = seg->any_hi;
-    // B fragments of Q, and the lane's rows of S^T: 8 nr + 2 t + e
+    // The lane's rows of S^T are 8 nr + 2 t + e.  B fragments of Q, and the rows'
+    // factors: with 16 rows read for each tile, where keeping them cost spills
+    // (48 requests of four drafts 56 us, now 51).
     uint32_t qf[NR][D / 8];
-    float fr[NR][2], m[NR][2], l[NR][2];
+    float fr[NR][2];
+    auto read_q = [&] {
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+        const uint4* qs = reinterpret_cast<const uint4*>(gbase + L::Q_OFF + ss * L::Q_SLOT) +
+                          nr * (D / 32) * 32 + lane;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          const uint4 w = qs[32 * c];
+          qf[nr][4 * c] = w.x;
+          qf[nr][4 * c + 1] = w.y;
+          qf[nr][4 * c + 2] = w.z;
+          qf[nr][4 * c + 3] = w.w;
+        }
+      }
+    };
+    auto read_fr = [&] {
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+        const float2 u = *reinterpret_cast<const float2*>(seg->fr + 8 * nr + 2 * t4);
+        fr[nr][0] = u.x;
+        fr[nr][1] = u.y;
+      }
+    };
+    if constexpr (NR == 1) {
+      read_q();
+      read_fr();
+    }
+    float m[NR][2], l[NR][2], v[NR][2];       // v: P's and O's exponent
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
-      const uint4* qs = reinterpret_cast<const uint4*>(gbase + L::Q_OFF + ss * L::Q_SLOT) +
-                        nr * (D / 32) * 32 + lane;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        const uint4 v = qs[32 * c];
-        qf[nr][4 * c] = v.x;
-        qf[nr][4 * c + 1] = v.y;
-        qf[nr][4 * c + 2] = v.z;
-        qf[nr][4 * c + 3] = v.w;
-      }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        fr[nr][e] = seg->fr[8 * nr + 2 * t4 + e];
-        m[nr][e] = -INFINITY;
+        m[nr][e] = KV_NO_MAX;
+        v[nr][e] = KV_NO_V;
         l[nr][e] = 0.0f;
       }
     }
@@ -625,7 +655,6 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
       for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][nr][e] = 0.0f;
-    int ve = 0;                               // V's reference exponent
     for (int i = 0; i < count; ++i, ++it) {
       const int st = it % L::STAGES;
       if (ok && !mbar_wait(bar_full + 8 * st, (it / L::STAGES) & 1, abort)) {
@@ -639,6 +668,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
         const uint32_t vt = kt + L::TILE;
         const uint2* pg = reinterpret_cast<const uint2*>(gbase + L::PG_OFF + st * L::PG_STAGE);
         const bool masked = key0 < all_lo || key0 + KW > all_hi;
+        if constexpr (NR == 2) read_q();
         // ---- scores of the warp's steps of 16 keys: x[.][.][2 h + e] is key g + 8 h
         // and row 2 t + e
         float x[KS][NR][4];
@@ -668,15 +698,19 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
           }
         }
         // ---- log2 units, mask, running maximum
-        int vnew = ve;
+        int v_top = -1, v_low = 255;
         float mx[NR][2];
+        if constexpr (NR == 2) read_fr();
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) mx[nr][0] = mx[nr][1] = -INFINITY;
         uint2 page[KS];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
           page[s] = pg[(warp * KW + 16 * s) >> a.v.page_shift];
-          if (page[s].y < 0xFFu) vnew = max(vnew, static_cast<int>(page[s].y));
+          if (page[s].y < 0xFFu) {
+            v_top = max(v_top, static_cast<int>(page[s].y));
+            v_low = min(v_low, static_cast<int>(page[s].y));
+          }
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
@@ -694,69 +728,82 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
               mx[nr][e] = fmaxf(mx[nr][e], fmaxf(y0, y1));
             }
         }
-        bool moved = vnew != ve;
-        float alpha[NR][2];
+        // v's condition with the step's largest scale, whether a row sees it or not;
+        // what it moves to knows better
+        bool moves = false;
+        float x_top[NR][2];
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float v = mx[nr][e];
-            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
-            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
-            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
-            const float mn = v > m[nr][e] + KA_LAZY ? v : m[nr][e];
-            alpha[nr][e] = mn == m[nr][e] ? 1.0f : ex2_approx(m[nr][e] - mn);
-            moved |= mn != m[nr][e];
-            m[nr][e] = mn;
+            x_top[nr][e] = ka_over_keys(mx[nr][e]);
+            const float over = x_top[nr][e] - m[nr][e];
+            moves |= over > KV_LAZY || over + (static_cast<float>(v_top) - v[nr][e]) > KV_LAZY;
           }
-        if (__any_sync(0xFFFFFFFFu, moved)) {
-          const float vf = kv_exp2i(ve - vnew);
-          ve = vnew;
+        if (__any_sync(0xFFFFFFFFu, moves)) {
+          const bool alike = v_top - v_low <= KA_ALIKE;
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr) {
-            const float f0 = alpha[nr][0] * vf, f1 = alpha[nr][1] * vf;
-            l[nr][0] *= alpha[nr][0];
-            l[nr][1] *= alpha[nr][1];
+            float by[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float mn = kv_next_m(m[nr][e], x_top[nr][e]);
+              float t = x_top[nr][e] - mn + static_cast<float>(v_top);
+              if (!alike) {
+                t = -INFINITY;
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+                  if (page[s].y < 0xFFu)
+                    t = fmaxf(t, fmaxf(x[s][nr][e], x[s][nr][2 + e]) - mn +
+                                     static_cast<float>(page[s].y));
+                t = ka_over_keys(t);
+              }
+              const float vn = kv_next_v(v[nr][e], m[nr][e] - mn, t);
+              by[e] = kv_move_o(m[nr][e], mn, v[nr][e], vn);
+              l[nr][e] *= ex2_approx(m[nr][e] - mn);
+              m[nr][e] = mn;
+              v[nr][e] = vn;
+            }
 #pragma unroll
             for (int c = 0; c < MT; ++c) {
-              o[c][nr][0] *= f0;
-              o[c][nr][1] *= f1;
-              o[c][nr][2] *= f0;
-              o[c][nr][3] *= f1;
+              o[c][nr][0] *= by[0];
+              o[c][nr][1] *= by[1];
+              o[c][nr][2] *= by[0];
+              o[c][nr][3] *= by[1];
             }
           }
         }
-        // (scores of -infinity weigh nothing, also where there is no other yet)
-        float m_use[NR][2];
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) m_use[nr][e] = m[nr][e] == -INFINITY ? 0.0f : m[nr][e];
         // ---- probabilities and the product with V, a step of 16 keys at a time
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
           const int code = static_cast<int>(page[s].y);
-          const float vf = code == 0xFF || code < 0 ? __uint_as_float(0x7FC00000u)
-                                                    : kv_exp2i(KA_P_EXP + code - ve);
+          const float ve = static_cast<float>(code);
           uint32_t pb[NR][2];
 #pragma unroll
-          for (int nr = 0; nr < NR; ++nr)
+          for (int nr = 0; nr < NR; ++nr) {
+            float nm[2], back[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float b = kv_p_shift(ve, v[nr][e]);
+              nm[e] = b - m[nr][e];
+              back[e] = kv_unshift(b);
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              float p[2], q[2];
+              float q[2];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                p[e] = ex2_approx(x[s][nr][2 * h + e] - m_use[nr][e]);
-                q[e] = p[e] * vf;
+                q[e] = ex2_approx(x[s][nr][2 * h + e] + nm[e]);
                 if (masked) {
                   const int j = key0 + 16 * s + g + 8 * h;
                   if (j < seg->lo[8 * nr + 2 * t4 + e] || j >= seg->hi[8 * nr + 2 * t4 + e])
-                    p[e] = q[e] = 0.0f;
+                    q[e] = 0.0f;
                 }
-                l[nr][e] += p[e];
+                l[nr][e] = fmaf(q[e], back[e], l[nr][e]);
               }
               pb[nr][h] = transpose8(cvt_f16x2(q[0], q[1]));
             }
+          }
           // codes of keys 2t, 2t + 1, 2t + 8, 2t + 9 of the step; those that
           // were not loaded, or lie behind the request's end, count as zero
           constexpr int W = D / 32;            // 32-bit words of a key per lane
@@ -812,31 +859,42 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
     for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float v = l[nr][e];
-        v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
-        v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
-        v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+        float sum = l[nr][e];
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 4);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
         if (g == 0) {
-          sm_m[warp * ROWS + 8 * nr + 2 * t4 + e] = m[nr][e];
-          sm_l[warp * ROWS + 8 * nr + 2 * t4 + e] = v;
+          sm_mv[warp * ROWS + 8 * nr + 2 * t4 + e] = make_float2(m[nr][e], v[nr][e]);
+          sm_l[warp * ROWS + 8 * nr + 2 * t4 + e] = sum;
         }
       }
-    if (lane == 0) sm_e[warp] = ve;
     kv_bar_sync(1, KA_CONS);
-    int top_e = 0;
+    // the maximum of a row's m over the warps, and of its units 2^v at that m
+    auto common = [&](const float2 (&mv)[KA_WARPS], float& M, float& V) {
+      M = V = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < KA_WARPS; ++w) top_e = max(top_e, sm_e[w]);
-    // weight of this warp's rows relative to the common reference
+      for (int w = 0; w < KA_WARPS; ++w) M = fmaxf(M, mv[w].x);
+#pragma unroll
+      for (int w = 0; w < KA_WARPS; ++w) V = fmaxf(V, mv[w].y + (mv[w].x - M));
+    };
+    // weight of this warp's rows relative to the common references
     float wgt[NR][2];
 #pragma unroll
-    for (int nr = 0; nr < NR; ++nr)
+    for (int nr = 0; nr < NR; ++nr) {
+      float2 mv[2][KA_WARPS];
+#pragma unroll
+      for (int w = 0; w < KA_WARPS; ++w) {
+        const float4 u = *reinterpret_cast<const float4*>(sm_mv + w * ROWS + 8 * nr + 2 * t4);
+        mv[0][w] = make_float2(u.x, u.y);
+        mv[1][w] = make_float2(u.z, u.w);
+      }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < KA_WARPS; ++w) M = fmaxf(M, sm_m[w * ROWS + 8 * nr + 2 * t4 + e]);
-        wgt[nr][e] = (m[nr][e] == M ? 1.0f : ex2_approx(m[nr][e] - M)) * kv_exp2i(ve - top_e);
+        float M, V;
+        common(mv[e], M, V);
+        wgt[nr][e] = kv_move_o(m[nr][e], M, v[nr][e], V);
       }
+    }
     const bool part = seg->part;
     const int live = seg->live;
     float* slot = a.ws + static_cast<long long>(seg->slot) * (ROWS * (D + 2));
@@ -846,17 +904,19 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
       // the row that a thread of the first two warps adds up, and its sum
       const int rr = 8 * nr + ((tid >> 3) & 7), c8 = tid & 7;
       const bool adds = tid < 64 && rr < live;
-      float M = -INFINITY, lsum = 0.0f;
+      float M, V, unit0, unit, lsum = 0.0f;
+      float2 mv[KA_WARPS];
 #pragma unroll
-      for (int w = 0; w < KA_WARPS; ++w) M = fmaxf(M, sm_m[w * ROWS + rr]);
+      for (int w = 0; w < KA_WARPS; ++w) mv[w] = sm_mv[w * ROWS + rr];
+      common(mv, M, V);
+      kv_o_unit(V, unit0, unit);
 #pragma unroll
       for (int w = 0; w < KA_WARPS; ++w) {
-        const float mw = sm_m[w * ROWS + rr];
-        lsum += sm_l[w * ROWS + rr] * (mw == M ? 1.0f : ex2_approx(mw - M));
+        lsum += sm_l[w * ROWS + rr] * ex2_approx(mv[w].x - M);
       }
       const bool saw = max(seg->lo[rr], seg->tile * TK) < min(seg->hi[rr], (seg->tile + seg->count) * TK);
-      const float inv = kv_inverse(lsum, saw);
-      if (lsum == 0.0f && saw) M = KV_ALL_MINUS_INF;
+      if (!part) unit0 *= kv_inverse(lsum, saw);
+      if (!saw) M = -INFINITY;
       const long long out = seg->out[rr];
       // rounds over 4 columns of each of the 8 chunks
 #pragma unroll
@@ -880,21 +940,14 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
             s.w += v.w;
           }
           const int col = (D / 8) * c8 + 4 * rd;
-          // to true units: 2^(top_e - 127), and the 2^KA_P_EXP out of P
-          const float f = kv_scale_value(static_cast<uint32_t>(top_e));
-          s.x = s.x * (1.0f / (1 << KA_P_EXP)) * f;
-          s.y = s.y * (1.0f / (1 << KA_P_EXP)) * f;
-          s.z = s.z * (1.0f / (1 << KA_P_EXP)) * f;
-          s.w = s.w * (1.0f / (1 << KA_P_EXP)) * f;
-          if (part) {
+          s.x = s.x * unit0 * unit;
+          s.y = s.y * unit0 * unit;
+          s.z = s.z * unit0 * unit;
+          s.w = s.w * unit0 * unit;
+          if (part)
             *reinterpret_cast<float4*>(slot + rr * D + col) = s;
-          } else {
-            s.x *= inv;
-            s.y *= inv;
-            s.z *= inv;
-            s.w *= inv;
+          else
             kv_store4(a.O, a.o_dtype, out + col, s);
-          }
         }
       }
       if (part && adds && c8 == 0) {

@@ -17,8 +17,9 @@
 //     6000 keys took 352 us against 331.)
 //   * page scales stay out of the operands: K's is a factor of the scores of
 //     its 16 .. 128 keys, applied with the softmax scale in the exponent's FMA;
-//     V's, a power of two relative to the largest so far, is added to the
-//     exponent, so P carries it exactly and the row sums take it out again;
+//     V's, a power of two, is added to the exponent relative to the row's own
+//     reference (kv_kernel.cuh), so P carries it exactly and the row sums take
+//     it out again;
 //   * rows are converted once per unit: the thread that owns a row brings it
 //     to f16 with a power of two of its own, and keeps its mask bounds.  The next
 //     unit's go to shared memory before this unit's O is read and written, so
@@ -72,8 +73,6 @@ constexpr int KP_REGS_LOW = 72;            // warpgroup 0
 constexpr int KP_REGS_SOFT = 176;          // warpgroups 1 and 2
 constexpr int KP_REGS_CONV = 88;           // warpgroup 3
 constexpr int KP_TMEM_COLS = 512;
-constexpr float KP_LAZY = 8.0f;            // slack of the exponentials' reference point
-constexpr int KP_P_EXP = 7;                // P is scaled by 2^7: at most 2^(7 + 8) in f16
 // Entries of a unit besides its blocks: with 1, 2, 4 and 8 eight ragged chunks
 // took 80, 68, 65 and 72 us when the 2048-token chunk took 242, 239, 237 and 241
 // (now 219 with 2, 3, 4 and 6 alike).
@@ -86,9 +85,9 @@ constexpr int KP_MAX_REQUESTS = 16384;
 struct KpPages {
   struct {
     float kf;                              // K's scale; NaN where K's or V's is NaN or no page is
-    int ve;                                // V's scale code; 0 there
+    float ve;                              // V's scale code; 0 there
   } of[8];
-  int top;                                 // the largest ve; -1: no block at all
+  float top;                               // the largest ve; -1: no block at all
   int valid;                               // keys of the block in front of the request's end
   int more;                                // another block follows
   int gone;                                // a bit for each 16 keys whose page was not loaded
@@ -533,7 +532,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         release(found);
         if (!found && bt == 0 && lane == 0) {
           // a stretch without blocks: the converting warps wait for the first
-          pages[0].top = -1;
+          pages[0].top = -1.0f;
           mbar_arrive(bar_pg);
         }
         if (!mbar_wait(bar_seg_empty + 8 * ss, ((seg_out >> 1) & 1) ^ 1, abort)) {
@@ -597,10 +596,10 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           scales_of(id1);
           const long long unit = id >= 0 ? static_cast<long long>(id) * a.v.heads + head : 0;
           float kf = __uint_as_float(0x7FC00000u);
-          int ve = 0;
+          float ve = 0.0f;
           if (kc != 0xFFu && vc != 0xFFu) {
             kf = kv_scale_value(kc);
-            ve = static_cast<int>(vc);
+            ve = static_cast<float>(vc);
           }
           const int ps = bt & (KP_PG - 1);
           if (!mbar_wait(bar_pg_empty + 8 * ps, ((bt / KP_PG) & 1) ^ 1, abort)) {
@@ -612,7 +611,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             pages[ps].of[lane].kf = kf;
             pages[ps].of[lane].ve = ve;
           }
-          const int top = __reduce_max_sync(0xFFFFFFFFu, ve);
+          const float top = static_cast<float>(__reduce_max_sync(0xFFFFFFFFu, static_cast<int>(ve)));
           const unsigned gone = __ballot_sync(0xFFFFFFFFu, lane < 8 && id < 0);
           if (lane == 0) {
             pages[ps].gone = static_cast<int>(gone);
@@ -766,7 +765,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       return pages + (b & (KP_PG - 1));
     };
     const KpPages* pg = pages_of(0);
-    if (pg && pg->top < 0) pg = nullptr;     // there are none
+    if (pg && pg->top < 0.0f) pg = nullptr;  // there are none
     // tiles in the order K, V of each block
 #pragma unroll 1
     for (int tile = 0; pg; ++tile) {
@@ -831,8 +830,8 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     const uint32_t s_full = bar_s_full + 16 * t;
     bool ok = true, live = false, works = false;
     int lo = 0, hi = 0, count = 0, key00 = 0;
-    float fr = 0.0f, m = -INFINITY, l = 0.0f;
-    int ev = 0;                                // V's reference exponent
+    float fr = 0.0f, m = KV_NO_MAX, l = 0.0f;
+    float v = KV_NO_V;                         // P's and O's exponent: kv_kernel.cuh
     while (true) {
       // ---- the next unit's rows, before this unit's are written: its first
       // scores are on their way meanwhile.  (Q is free: the last scores are done.)
@@ -907,9 +906,8 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         tc_fence_after();
         // a row that saw keys and adds up to nothing had only scores of -infinity
         const bool saw = max(lo, key00) < min(hi, key00 + KP_BK * count);
-        // to true units: 2^(ev - 127), and the 2^KP_P_EXP out of P
-        const float unit = kv_scale_value(static_cast<uint32_t>(ev));
-        const float inv = kv_inverse(l, saw) * (1.0f / (1 << KP_P_EXP));
+        float unit0, unit;
+        kv_o_unit(v, unit0, unit);
         // (read again rather than kept in registers over the blocks)
         const volatile KpSeg* sg = segs + (ss ^ 1);
         float* part = sg->slot >= 0 ? a.ws + static_cast<long long>(sg->slot) * (KP_ROWS * (D + 2)) : nullptr;
@@ -919,7 +917,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         // rows of O 32 bytes at a time where they are that aligned
         const bool by32 = ((reinterpret_cast<uintptr_t>(a.O) |
                             static_cast<uintptr_t>(out * (a.o_dtype == DT_F32 ? 4 : 2))) & 31) == 0;
-        const float f = part ? 1.0f / (1 << KP_P_EXP) : inv;
+        const float f = part ? unit0 : unit0 * kv_inverse(l, saw);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -961,7 +959,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           }
         }
         if (part && live) {
-          part[KP_ROWS * D + urow] = l == 0.0f && saw ? KV_ALL_MINUS_INF : m;
+          part[KP_ROWS * D + urow] = saw ? m : -INFINITY;
           part[KP_ROWS * (D + 1) + urow] = l;
         }
         tc_fence_before();
@@ -984,9 +982,9 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       const int all_lo = __reduce_max_sync(0xFFFFFFFFu, live ? lo : 0);
       const int all_hi = __reduce_min_sync(0xFFFFFFFFu, live ? hi : 0x7FFFFFFF);
 
-      m = -INFINITY;
+      m = KV_NO_MAX;
       l = 0.0f;
-      ev = 0;
+      v = KV_NO_V;
 #pragma unroll 1
       for (int h = 0; h < 2 * count; ++h) {
         const int g = bt + (h >> 1), ps = g & (KP_PG - 1);
@@ -1004,7 +1002,6 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         tc_fence_after();
         const KpPages* pg = reinterpret_cast<const KpPages*>(gbase + L::PG_OFF) + ps;
         const int p0 = 4 * (h & 1);            // the step's first 16 keys in the block
-        const int ev_new = max(ev, pg->top);
         uint32_t x0[32], x1[32];
         const uint32_t s_at = lane_addr + KP_HK * (h & 1);
         tmem_ld_32x32b_x32(s_at, x0);
@@ -1027,7 +1024,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
           for (int p = 0; p < 4; ++p) f[p] = 1.0f;
         }
-        float mx = -INFINITY;
+        float mx = -INFINITY, gx[4];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           const uint32_t(&x)[32] = p < 2 ? x0 : x1;
@@ -1038,37 +1035,45 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             g0 = max3(g0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
             g1 = max3(g1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
           }
-          mx = fmaxf(mx, fmaxf(g0, g1) * f[p]);
+          gx[p] = fmaxf(g0, g1) * f[p];
+          mx = fmaxf(mx, gx[p]);
         }
-        const float m_new = mx > m + KP_LAZY ? mx : m;
-        const float alpha = m_new == m ? 1.0f : ex2_approx(m - m_new);
-        if (h >= 1 && __any_sync(0xFFFFFFFFu, m_new != m || ev_new != ev)) {
-          // the product that last wrote O, of the step before, is done when the
-          // next step's scores are
-          if (!mbar_wait(s_full + 8 * (~h & 1), ((h & 1 ? own0 : own1) + ((h + 1) >> 1)) & 1, abort)) {
-            if (lane == 0) kp_timeout(abort, 0x5a);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const float by = alpha * kv_exp2i(ev - ev_new);
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(lane_addr + 128 + 32 * c, o);
-            tmem_wait_ld();
+        // v's condition with the block's largest scale, whether the row sees it or
+        // not; what it moves to knows better
+        const float over = mx - m;
+        if (__any_sync(0xFFFFFFFFu, over > KV_LAZY || over + (pg->top - v) > KV_LAZY)) {
+          const float m_new = kv_next_m(m, mx);
+          float tv = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
-            tmem_st_32x32b_x32(lane_addr + 128 + 32 * c, o);
+          for (int p = 0; p < 4; ++p) tv = fmaxf(tv, (gx[p] - m_new) + pg->of[p0 + p].ve);
+          const float v_new = kv_next_v(v, m - m_new, tv);
+          if (h >= 1 && __any_sync(0xFFFFFFFFu, m_new != m || v_new != v)) {
+            // the product that last wrote O, of the step before, is done when the
+            // next step's scores are
+            if (!mbar_wait(s_full + 8 * (~h & 1), ((h & 1 ? own0 : own1) + ((h + 1) >> 1)) & 1, abort)) {
+              if (lane == 0) kp_timeout(abort, 0x5a);
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const float by = kv_move_o(m, m_new, v, v_new);
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(lane_addr + 128 + 32 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
+              tmem_st_32x32b_x32(lane_addr + 128 + 32 * c, o);
+            }
           }
+          l *= ex2_approx(m - m_new);
+          m = m_new;
+          v = v_new;
         }
-        ev = ev_new;
-        l *= alpha;
-        m = m_new;
-        // p' = 2^(x - m + b), b = 7 + (V's exponent - the reference), rounded
+        // p' = 2^(x - m + b), b = 7 + (V's exponent - v), rounded
         // to f16 and written back over the scores; the sum takes b out again.
-        // Hidden scores are -inf and stay it: b and m_use are finite.
-        const float m_use = m == -INFINITY ? 0.0f : m;
+        // Hidden scores are -inf and stay it: b and m are finite.
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const uint32_t(&x)[32] = c ? x1 : x0;
@@ -1076,9 +1081,8 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const int p = 2 * c + q;
-            const int b = max(-60, pg->of[p0 + p].ve + (KP_P_EXP - ev));
-            // b as a float: 1.5 * 2^23 + b, less 1.5 * 2^23
-            const float nm = (__int_as_float(0x4B400000 + b) - 12582912.0f) - m_use;
+            const float b = kv_p_shift(pg->of[p0 + p].ve, v);
+            const float nm = b - m;
             const uint64_t f2 = pack2(f[p], f[p]), nm2 = pack2(nm, nm);
             uint64_t sum = pack2(0.0f, 0.0f);
 #pragma unroll
@@ -1094,7 +1098,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             }
             float a0, a1;
             unpack2(sum, a0, a1);
-            l = fmaf(a0 + a1, __int_as_float((127 - b) << 23), l);
+            l = fmaf(a0 + a1, kv_unshift(b), l);
           }
           tmem_st_32x32b_x16(s_at + 16 * c, pk);
         }

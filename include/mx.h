@@ -545,9 +545,11 @@ mx_status mx_kv_append(const mx_kv_cache* cache, const void* K, const void* V, i
  *   q_heads  a multiple of the cache's heads
  *   scale    finite
  * The scores, sums and outputs accumulate in fp32; probabilities are rounded
- * to f16 before the product with V, whose codes are exact in f16, so each
- * weight is off by at most 2^-11 relative; Q's values below 2^-14 of their
- * row's largest are rounded to 2^-25 of it.  Codes that stand for NaN or
+ * to f16 before the product with V, whose codes are exact in f16: a weight w_j
+ * whose key's page has V's scale s_j is off by at most 2^-11 w_j or, if that is
+ * more, by 2^-28 / s_j times the row's largest w_k s_k (k over the keys that the
+ * row sees: what it does not see changes nothing); Q's values below 2^-14 of
+ * their row's largest are rounded to 2^-25 of it.  Codes that stand for NaN or
  * infinity (which mx_kv_append never writes) reach every row that shares a
  * tile with them.
  *

@@ -125,3 +125,43 @@ def test_keys_of_minus_infinity_beside_others(n, rows, ws, page):
     s.cache.k_scales.fill_(254)
     got = s.run(ws=ws)
     assert np.isnan(got[0, 1]).all()
+
+
+@pytest.mark.parametrize("n,rows", FEW + MANY)
+@pytest.mark.parametrize("ws", [True, False])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("fmt", [mx.E4M3, mx.INT8])
+def test_large_values_of_no_weight(n, rows, ws, page, fmt):
+    """Values of 2^33 in every third page, with weights of e^-40: what the
+    other pages give has to survive beside them."""
+    far = (np.arange(n) // page) % 3 == 1
+    key, value = _noise(n) * 0.05 + 2.5, _noise(n, seed=2)
+    key[far] -= 5.0
+    value[far] *= 2.0 ** 33
+    s = One(n, rows, page, key, value, torch.ones(rows * 2, D), fmt=fmt)
+    out, tol = s.exact()
+    assert (np.abs(out) > 4 * tol).mean() > 0.5            # the bound can tell them from zero
+    assert (np.abs(s.run(ws=ws) - out) <= tol).all()
+
+
+@pytest.mark.parametrize("n,rows", [(259, 5), (6003, 5), (300, 40), (9000, 70)])
+@pytest.mark.parametrize("ws", [True, False])
+@pytest.mark.parametrize("up", [12, 40, 90])
+def test_large_values_that_a_row_does_not_see(n, rows, ws, up):
+    """The last page's values are 2^up times the others': rows in front of it
+    do not know it.  The same in front of a window that begins inside a page
+    and behind whole ones."""
+    page = 16
+    s = One(n, rows, page, _noise(n), _noise(n, seed=2), _noise(rows * 2, seed=3))
+    s.cache.v_scales[int(s.ids[-1])] += up
+    out, tol = s.exact()
+    before = n - rows + np.arange(rows) < (n - 1) // page * page
+    assert before.any() and not before.all()
+    got = s.run(ws=ws)
+    assert (np.abs(got - out) <= tol).all()
+    s.cache.v_scales[int(s.ids[-1])] -= up
+    window = 50
+    first = n - rows + 1 - window
+    s.cache.v_scales[torch.from_numpy(s.ids[:first // page])] += up
+    out, tol = s.exact(window=window)
+    assert (np.abs(s.run(window=window, ws=ws) - out) <= tol).all()
