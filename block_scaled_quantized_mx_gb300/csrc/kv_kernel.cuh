@@ -84,6 +84,14 @@ __device__ __forceinline__ int kv_end_key(const KvView& v, const KvReq& r, int i
   return p > 0 ? p : 0;
 }
 
+// Whether the table entry of key j's page is followed: the page begins in front of
+// the request's end and does not end in front of `first`, the first key that any
+// row sees.  (A page behind the window may belong to another request by now,
+// whatever the table still says.)
+__device__ __forceinline__ bool kv_follows(const KvView& v, const KvReq& r, int first, int j) {
+  return j < r.len && ((j >> v.page_shift) + 1) << v.page_shift > first;
+}
+
 // A scale code as a factor: 2^(c - 127); 0xFF is NaN.
 __device__ __forceinline__ float kv_scale_value(uint32_t c) {
   return __uint_as_float(c == 0 ? 0x00400000u : c == 0xFFu ? 0x7FC00000u : (c << 23));

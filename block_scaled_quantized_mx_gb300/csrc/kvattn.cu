@@ -393,7 +393,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
       }
       const KvReq rq = walk.q.r;
       const int rows = rq.n * a.v.group;
-      const int len = rq.len, shift = a.v.page_shift;
+      const int shift = a.v.page_shift;
       const int per_tile = TK >> shift;
       // the rows' raw values, on their way before anything waits
       uint4 raw_q[NR][D / 32];
@@ -417,11 +417,13 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
       // and scales one, so that no tile waits for either.
       const int slot = lane & (L::MAX_PAGES - 1);
       const bool is_v = (lane & L::MAX_PAGES) != 0;
+      const int first_key = kv_first_key(a.v, rq, walk.row_tile * ROWS / a.v.group);
       const uint8_t* scales = is_v ? a.v.v_scales : a.v.k_scales;
       auto page_of = [&](int i) {
         const int key0 = (walk.tile + i) * TK;
         int id = -1;
-        if (i < walk.count && lane < 2 * L::MAX_PAGES && slot < per_tile && key0 + (slot << shift) < len)
+        if (i < walk.count && lane < 2 * L::MAX_PAGES && slot < per_tile &&
+            kv_follows(a.v, rq, first_key, key0 + (slot << shift)))
           id = row[(key0 >> shift) + slot];
         return id < a.v.pages ? id : -1;
       };

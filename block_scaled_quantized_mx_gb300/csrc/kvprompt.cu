@@ -566,14 +566,17 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         ++seg_out;
         first_seg = false;
         if (!found) break;
-        const int count = walk->count, block0 = walk->block, len = walk->r.len, head = walk->head;
+        const int count = walk->count, block0 = walk->block, head = walk->head;
+        const KvReq rq = walk->r;
         const int* row = a.v.table + static_cast<long long>(walk->b) * a.v.table_stride;
-        __syncwarp();                          // all lanes have read the walk
         const int shift = a.v.page_shift;
+        const int first_key = kv_first_key(a.v, rq, walk->rt * KP_ROWS / a.v.group);
+        __syncwarp();                          // all lanes have read the walk
         // the page of 16 keys, one per lane; -1: none, or outside the cache
         auto page_of = [&](int j) {
           const int key = (block0 + j) * KP_BK + 16 * lane;
-          const int id = j < count && lane < 8 && key < len ? row[key >> shift] : -1;
+          const bool follows = j < count && lane < 8 && kv_follows(a.v, rq, first_key, key);
+          const int id = follows ? row[key >> shift] : -1;
           return id < a.v.pages ? id : -1;
         };
         // Ids are read two blocks ahead and scales one: nothing here waits for either.
@@ -616,7 +619,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           if (lane == 0) {
             pages[ps].gone = static_cast<int>(gone);
             pages[ps].top = top;
-            pages[ps].valid = len - (block0 + j) * KP_BK;
+            pages[ps].valid = rq.len - (block0 + j) * KP_BK;
           }
           __syncwarp();
           ++bt;

@@ -165,3 +165,21 @@ def test_large_values_that_a_row_does_not_see(n, rows, ws, up):
     s.cache.v_scales[torch.from_numpy(s.ids[:first // page])] += up
     out, tol = s.exact(window=window)
     assert (np.abs(s.run(window=window, ws=ws) - out) <= tol).all()
+
+
+@pytest.mark.parametrize("n,rows,window", [(250, 1, 100), (6000, 3, 990), (300, 40, 70), (9000, 70, 100)])
+@pytest.mark.parametrize("ws", [True, False])
+@pytest.mark.parametrize("fmt", [mx.E4M3, mx.E5M2])
+def test_pages_in_front_of_the_window_are_not_followed(n, rows, window, ws, fmt):
+    """Pages that no row sees may belong to another request by now, whatever
+    the table still says: NaN codes and any scale in them change no bit."""
+    page = 16
+    s = One(n, rows, page, _noise(n), _noise(n, seed=2), _noise(rows * 2, seed=3), fmt=fmt)
+    want = s.run(window=window, ws=ws)
+    out, tol = s.exact(window=window)
+    assert (np.abs(want - out) <= tol).all()
+    gone = torch.from_numpy(s.ids[:(n - rows + 1 - window) // page])
+    for code, scale in ((0x7F, 254), (0x7F, 255), (0x00, 254)):
+        s.cache.k[gone] = s.cache.v[gone] = code
+        s.cache.k_scales[gone] = s.cache.v_scales[gone] = scale
+        assert np.array_equal(s.run(window=window, ws=ws), want)
