@@ -546,13 +546,20 @@ class KVCache:
         self._c = CKVCache(self.k.data_ptr(), self.v.data_ptr(),
                            self.k_scales.data_ptr(), self.v_scales.data_ptr(),
                            self.fmt, page, pages, heads, d)
+        self._of = self._planes()
+
+    def _planes(self):
+        """All that the C struct follows from."""
+        k, v, ks, vs = self.k, self.v, self.k_scales, self.v_scales
+        return (self.fmt, k.data_ptr(), v.data_ptr(), ks.data_ptr(),
+                vs.data_ptr(), k.shape, v.shape, ks.shape, vs.shape,
+                k.is_contiguous(), v.is_contiguous(), ks.is_contiguous(),
+                vs.is_contiguous(), k.dtype, v.dtype, ks.dtype, vs.dtype)
 
     def c(self) -> CKVCache:
-        c = self._c
-        if c.k_data != self.k.data_ptr() or c.v_data != self.v.data_ptr() or \
-                c.k_scales != self.k_scales.data_ptr() or \
-                c.v_scales != self.v_scales.data_ptr() or c.fmt != self.fmt:
-            self.__post_init__()                 # a plane was replaced
+        """The planes as they are now, checked again if any of them changed."""
+        if self._of != self._planes():
+            self.__post_init__()
         return self._c
 
 
