@@ -542,6 +542,9 @@ class KVCache:
         for t in (self.k, self.v, self.k_scales, self.v_scales):
             if t.dtype != torch.uint8 or not t.is_contiguous():
                 raise ValueError("a cache's planes are contiguous uint8 tensors")
+        # one GPU's memory: the calls ask, a cache on the host may be kept
+        self._gpu = self.k.is_cuda and all(
+            t.device == self.k.device for t in (self.v, self.k_scales, self.v_scales))
         pages, heads, page, d = shape
         self._c = CKVCache(self.k.data_ptr(), self.v.data_ptr(),
                            self.k_scales.data_ptr(), self.v_scales.data_ptr(),
@@ -561,6 +564,13 @@ class KVCache:
         if self._of != self._planes():
             self.__post_init__()
         return self._c
+
+    def on_gpu(self) -> CKVCache:
+        """c(), for a call that follows its addresses on the GPU."""
+        c = self.c()
+        if not self._gpu:
+            raise ValueError("a cache's planes must be CUDA tensors of one GPU")
+        return c
 
 
 def empty_kv_cache(fmt: int, pages: int, heads: int, page: int, d: int,
@@ -714,12 +724,12 @@ def mx_kv_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor,
     cache, in place, at their slots (int64, one per token; negative: none).
     One power-of-two scale covers a page and head: where new tokens need a
     larger one than the page has, the codes already there are rounded again."""
+    c = cache.on_gpu()
     dt, shape, kt, kh = _kv_tensor(K, "K")
     vdt, vshape, vt, vh = _kv_tensor(V, "V")
     if vdt != dt or vshape != shape:
         raise ValueError("K and V must have one shape and type")
     T, heads, d = shape
-    c = cache.c()
     if heads != c.heads or d != c.d:
         raise ValueError("K and V must have the cache's heads and d")
     if slots.dtype != torch.int64 or not slots.is_cuda or slots.dim() != 1 or \
@@ -754,9 +764,9 @@ def mx_kv_attention(Q: torch.Tensor, cache: KVCache, table: torch.Tensor,
     defaults to 1/sqrt(d), out_dtype to Q's.  With a device `workspace`
     (uint8, kv_attention_workspace_bytes() long) a request's keys are spread
     over many SMs.  Rows that belong to no request are not written."""
+    c = cache.on_gpu()
     dt, shape, qt, qh = _kv_tensor(Q, "Q")
     T, Hq, d = shape
-    c = cache.c()
     if d != c.d or Hq % c.heads:
         raise ValueError("Q must have the cache's d and a multiple of its heads")
     B = lens.shape[0]

@@ -57,3 +57,14 @@ def test_planes_that_no_longer_belong_together_are_refused(change):
     change(cache)
     with pytest.raises(ValueError):
         cache.c()
+
+
+def test_a_cache_in_host_memory_is_refused():
+    """Before anything else of the call is looked at: K, V and Q may well be
+    on the GPU."""
+    cache, q = _cache(), torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    i = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="planes must be CUDA"):
+        mx.mx_kv_append(cache, q, q, torch.zeros(2, dtype=torch.int64))
+    with pytest.raises(ValueError, match="planes must be CUDA"):
+        mx.mx_kv_attention(q, cache, i.view(3, 1), i[:2], i, 1)
