@@ -764,6 +764,9 @@ def mx_kv_attention(Q: torch.Tensor, cache: KVCache, table: torch.Tensor,
     defaults to 1/sqrt(d), out_dtype to Q's.  With a device `workspace`
     (uint8, kv_attention_workspace_bytes() long) a request's keys are spread
     over many SMs.  Rows that belong to no request are not written."""
+    if workspace is not None and not (workspace.is_cuda and
+                                      workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
     c = cache.on_gpu()
     dt, shape, qt, qh = _kv_tensor(Q, "Q")
     T, Hq, d = shape

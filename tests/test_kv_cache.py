@@ -68,3 +68,26 @@ def test_a_cache_in_host_memory_is_refused():
         mx.mx_kv_append(cache, q, q, torch.zeros(2, dtype=torch.int64))
     with pytest.raises(ValueError, match="planes must be CUDA"):
         mx.mx_kv_attention(q, cache, i.view(3, 1), i[:2], i, 1)
+
+
+def test_a_workspace_in_host_memory_is_refused():
+    cache, q = _cache(), torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    i = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="workspace"):
+        mx.mx_kv_attention(q, cache, i.view(3, 1), i[:2], i, 1, workspace=_u8(1 << 20))
+
+
+@pytest.mark.gpu
+def test_a_workspace_that_holds_less_than_it_says_is_refused():
+    mx.build()
+    cache = mx.empty_kv_cache(mx.E4M3, 8, 2, 16, 64)
+    q = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device="cuda")
+    i = torch.zeros(3, dtype=torch.int32, device="cuda")
+    few = torch.zeros(16, dtype=torch.uint8, device="cuda")
+    for ws in (few.expand(1 << 20, 16), few[::2], few.cpu()):
+        with pytest.raises(ValueError, match="workspace"):
+            mx.mx_kv_attention(q, cache, i.view(3, 1), i[:2], i, 1, workspace=ws)
+    with pytest.raises(ValueError, match="planes must be CUDA"):
+        mx.mx_kv_attention(q, _cache(), i.view(3, 1), i[:2], i, 1)
+    with pytest.raises(ValueError, match="planes must be CUDA"):
+        mx.mx_kv_append(_cache(), q, q, torch.zeros(2, dtype=torch.int64, device="cuda"))
