@@ -551,6 +551,13 @@ class KVCache:
                            self.fmt, page, pages, heads, d)
         self._of = self._planes()
 
+    def __getstate__(self):                      # copies have addresses of their own
+        return {f: getattr(self, f) for f in self.__dataclass_fields__}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self.__post_init__()
+
     def _planes(self):
         """All that the C struct follows from."""
         k, v, ks, vs = self.k, self.v, self.k_scales, self.v_scales

@@ -91,3 +91,16 @@ def test_a_workspace_that_holds_less_than_it_says_is_refused():
         mx.mx_kv_attention(q, _cache(), i.view(3, 1), i[:2], i, 1)
     with pytest.raises(ValueError, match="planes must be CUDA"):
         mx.mx_kv_append(_cache(), q, q, torch.zeros(2, dtype=torch.int64, device="cuda"))
+
+
+def test_a_cache_can_be_copied():
+    """deepcopy and pickle give a cache of its own planes."""
+    cache = _cache()
+    cache.k[3] = 7
+    for other in (copy.deepcopy(cache), pickle.loads(pickle.dumps(cache))):
+        assert torch.equal(other.k, cache.k) and other.fmt == cache.fmt
+        c = other.c()
+        assert c.k_data == other.k.data_ptr() != cache.k.data_ptr() and _says(c) == (8, 2, 16, 64)
+    shallow = copy.copy(cache)
+    shallow.k = cache.k.clone()
+    assert cache.c().k_data == cache.k.data_ptr() and shallow.c().k_data == shallow.k.data_ptr()
