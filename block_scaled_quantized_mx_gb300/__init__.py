@@ -620,8 +620,24 @@ _KV_OUT_DTYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16,
 # An uninitialised tensor on the current GPU: (shape, strides, dtype).  The
 # allocator's entry without the operator dispatch around it, whose code a
 # kernel launch between two calls pushes out of the host's caches: 3.6 us
-# instead of 7 in a decoding step.
-_empty_cuda = torch._C._dynamo.guards._empty_strided_cuda
+# instead of 7 in a decoding step.  It is not public: None where torch lacks it.
+try:
+    _direct_empty = torch._C._dynamo.guards._empty_strided_cuda
+except AttributeError:
+    _direct_empty = None
+
+
+def _allocator(like: torch.Tensor):
+    """What makes a call's outputs, on the operands' GPU: the direct entry where
+    that is the current one, torch.empty_strided on another, without that entry
+    and where torch is to fill what nothing writes."""
+    if _direct_empty is not None and \
+            like.get_device() == torch.cuda.current_device() and \
+            not torch.are_deterministic_algorithms_enabled():
+        return _direct_empty
+    device = like.device
+    return lambda shape, strides, dtype: torch.empty_strided(
+        shape, strides, dtype=dtype, device=device)
 
 
 def _int32(t: torch.Tensor, name: str, n: int = 0) -> int:
@@ -666,11 +682,10 @@ def mx_kv_extend(lens: torch.Tensor, new_tokens: torch.Tensor,
     p_count = _int32(count, "count", 1)
     p_table, stride, width = _table(table, B)
     if out is None:
-        one = (1,)
-        out = KVPlan(_empty_cuda((B,), one, _i32),
-                     _empty_cuda((B + 1,), one, _i32),
-                     _empty_cuda((max_tokens,), one, torch.int64),
-                     _empty_cuda((2,), one, _i32))
+        one, empty = (1,), _allocator(lens)
+        out = KVPlan(empty((B,), one, _i32), empty((B + 1,), one, _i32),
+                     empty((max_tokens,), one, torch.int64),
+                     empty((2,), one, _i32))
     else:
         _int32(out.lens, "out.lens", B)
         _int32(out.cu, "out.cu", B + 1)
@@ -700,7 +715,8 @@ def mx_kv_truncate(lens: torch.Tensor, keep: torch.Tensor, table: torch.Tensor,
     p_count = _int32(count, "count", 1)
     p_table, stride, width = _table(table, B)
     if out is None:
-        out = KVCut(_empty_cuda((B,), (1,), _i32), _empty_cuda((2,), (1,), _i32))
+        empty = _allocator(lens)
+        out = KVCut(empty((B,), (1,), _i32), empty((2,), (1,), _i32))
     else:
         _int32(out.lens, "out.lens", B)
         _int32(out.counts, "out.counts", 2)
@@ -785,7 +801,7 @@ def mx_kv_attention(Q: torch.Tensor, cache: KVCache, table: torch.Tensor,
     p_table, stride, width = _table(table, B)
     if out is None:
         ot, oh = Hq * d, d
-        out = _empty_cuda((T, Hq, d), (ot, oh, 1), out_dtype or Q.dtype)
+        out = _allocator(Q)((T, Hq, d), (ot, oh, 1), out_dtype or Q.dtype)
     elif (out.shape != shape or not out.is_cuda or out.stride(2) != 1
           or (out_dtype is not None and out.dtype != out_dtype)):
         raise ValueError("out must be a CUDA tensor of Q's shape and of type "

@@ -104,3 +104,63 @@ def test_a_cache_can_be_copied():
     shallow = copy.copy(cache)
     shallow.k = cache.k.clone()
     assert cache.c().k_data == cache.k.data_ptr() and shallow.c().k_data == shallow.k.data_ptr()
+
+
+def test_the_package_imports_without_torch_s_private_allocator():
+    """The direct entry of the allocator is a saving, not a need."""
+    code = ("import torch; del torch._C._dynamo.guards._empty_strided_cuda; "
+            "import block_scaled_quantized_mx_gb300 as mx; print(len(mx.EXPORTS))")
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT, timeout=300)
+
+
+class _On:
+    """A tensor's device, as the choice of an allocator sees it."""
+
+    def __init__(self, index):
+        self.device = torch.device("cuda", index)
+
+    def get_device(self):
+        return self.device.index
+
+
+def test_outputs_are_made_where_the_operands_are(monkeypatch):
+    """The direct entry knows the current device only and fills nothing."""
+    made = []
+    monkeypatch.setattr(mx, "_direct_empty", lambda *a: made.append(("direct",) + a))
+    monkeypatch.setattr(torch, "empty_strided", lambda *a, **k: made.append((k["device"].index,) + a))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    make = lambda t: mx._allocator(t)((2, 3), (3, 1), torch.int32)  # noqa: E731
+    make(_On(0))
+    make(_On(1))
+    monkeypatch.setattr(torch, "are_deterministic_algorithms_enabled", lambda: True)
+    make(_On(0))
+    monkeypatch.setattr(torch, "are_deterministic_algorithms_enabled", lambda: False)
+    monkeypatch.setattr(mx, "_direct_empty", None)
+    make(_On(0))
+    assert [m[0] for m in made] == ["direct", 1, 0, 0] and all(m[1:3] == ((2, 3), (3, 1)) for m in made)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("direct", [True, False])
+def test_outputs_of_each_allocator(direct, monkeypatch):
+    mx.build()
+    if not direct:
+        monkeypatch.setattr(mx, "_direct_empty", None)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table, stack = torch.full((2, 3), -1, **i32), torch.tensor([4, 3, 2, 1], **i32)
+    lens, count = torch.tensor([0, 0], **i32), torch.tensor([4], **i32)
+    plan = mx.mx_kv_extend(lens, torch.tensor([17, 3], **i32), table, stack, count, 16, 24)
+    assert plan.lens.tolist() == [17, 3] and plan.cu.tolist() == [0, 17, 20] and plan.counts.tolist() == [1, 0]
+    assert plan.slots.tolist() == [16 + i for i in range(16)] + [32, 48, 49, 50] + [-1] * 4
+    cut = mx.mx_kv_truncate(plan.lens, torch.tensor([1, 0], **i32), table, stack, plan.counts, 16)
+    assert cut.lens.tolist() == [1, 0] and cut.counts.tolist() == [3, 0]
+    q = torch.ones(3, 2, 64, dtype=torch.float16, device="cuda")
+    cache = mx.empty_kv_cache(mx.E4M3, 4, 2, 16, 64)
+    args = (q, cache, table, torch.tensor([0, 0], **i32), torch.tensor([0, 1, 2], **i32), 1)
+    o = mx.mx_kv_attention(*args, out_dtype=torch.float32)
+    assert o.shape == (3, 2, 64) and o.is_contiguous() and o.dtype == torch.float32 and (o[:2] == 0).all()
+    torch.use_deterministic_algorithms(True)
+    try:                                         # rows of no request: as torch fills what nothing wrote
+        assert mx.mx_kv_attention(*args)[2].isnan().all()
+    finally:
+        torch.use_deterministic_algorithms(False)
