@@ -765,7 +765,6 @@ def mx_kv_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor,
     return cache
 
 
-@functools.lru_cache(maxsize=1024)
 def kv_attention_workspace_bytes(q_heads: int, heads: int, d: int,
                                  max_q: int) -> int:
     """Bytes of workspace with which mx_kv_attention spreads a request's keys

@@ -164,3 +164,17 @@ def test_outputs_of_each_allocator(direct, monkeypatch):
         assert mx.mx_kv_attention(*args)[2].isnan().all()
     finally:
         torch.use_deterministic_algorithms(False)
+
+
+def test_the_workspace_s_size_is_asked_of_the_device_at_hand(monkeypatch):
+    """It follows from the current device, and is 0 on one that the library
+    does not run on: an answer for one is none for another."""
+    answers = iter([0, 5, 9])
+
+    class Lib:
+        @staticmethod
+        def mx_kv_attention_workspace_bytes(*a):
+            return next(answers)
+
+    monkeypatch.setattr(mx, "lib", lambda: Lib)
+    assert [mx.kv_attention_workspace_bytes(24, 3, 64, 11) for _ in range(3)] == [0, 5, 9]
