@@ -4,7 +4,9 @@
 //   truncate  request b keeps keep_b of its len_b tokens; the pages behind
 //             them go back on the stack and their table entries become -1.
 //             Of the n pages freed (request order, then block order) the i-th
-//             lands at stack[count + n - 1 - i].
+//             lands at stack[count + n - 1 - i].  An entry that is -1 already (a
+//             page given back before) frees none: the scan counts entries as it
+//             finds them, not as lengths make them.
 //   extend    request b gets new_b tokens: pages for blocks ceil(len_b / P) ..
 //             ceil((len_b + new_b) / P) - 1 -- the i-th handed out (request
 //             order) is stack[count - 1 - i] -- and for each new token its
@@ -14,17 +16,22 @@
 // find the same pages again.
 //
 // A few KB in, a slot (8 bytes) per token out: the launch and a chain of
-// dependent reads bound it, not bandwidth.  So it is one launch with no
-// scratch memory and no atomics on global memory: every CTA scans all
-// requests for itself (two integer prefix sums over B lengths read from L2),
-// and only the filling of tables and slots is divided.  A page id is read
-// once per 32 blocks and passed on by shuffles.  Where an output overwrites an
-// input, the CTAs are one cluster (of at most eight, the portable limit) with
-// its barrier between the last read of an input and the first write of an
-// output; otherwise there are as many as the slots keep busy.
-// Measured, truncate and extend together: 64 requests 7.4 us; 2048 requests, a
-// tenth of them with whole prompts (200000 new tokens), 14.7 us (with a page
-// read per token and eight CTAs 39).
+// dependent reads bound it, not bandwidth.  So each is one launch with no
+// scratch memory and no atomics on global memory.
+//   extend    every CTA scans all requests for itself (two integer prefix sums
+//             over B lengths read from L2), and only the filling of tables and
+//             slots is divided.  A page id is read once per 32 blocks and passed
+//             on by shuffles.  Where an output overwrites an input, the CTAs are
+//             one cluster (of at most eight, the portable limit) with its
+//             barrier between the last read of an input and the first write
+//             of an output; otherwise there are as many as the slots keep busy.
+//   truncate  the table is an input that is always overwritten, and pages must be
+//             counted as they are found, so the CTAs of a cluster share the
+//             requests out, and read each other's totals.
+// Measured, truncate and extend together: 64 requests 7.2 us; 2048 requests, a
+// tenth of them with whole prompts (200000 new tokens), 16.4 us (with a page
+// read per token and eight CTAs 39; with truncate's pages taken from the lengths,
+// holes and all, 14.5; with every one of its CTAs counting all rows 27).
 #include <cstdint>
 
 #include "common.cuh"
@@ -230,13 +237,30 @@ __global__ void __launch_bounds__(PG_THREADS) kv_extend_kernel(const PagesArgs a
     a.slots[t] = -1;
 }
 
+// Rows that lose up to PG_SHORT blocks (dropped drafts) are looked after by a
+// thread each, longer ones (finished requests) by a warp, with PG_BATCH loads of
+// a lane on their way for each of PG_ROWS rows.
+constexpr int PG_SHORT = 2;
+constexpr int PG_BATCH = 4;
+constexpr int PG_ROWS = 4;
+
+// The requests of each of `ctas` CTAs.
+__host__ __device__ __forceinline__ int pages_share(int requests, int ctas) {
+  return (requests + ctas - 1) / ctas;
+}
+
 __global__ void __launch_bounds__(PG_THREADS) kv_truncate_kernel(const PagesArgs a) {
-  extern __shared__ int sm_req[];           // per request: first page freed, lengths before and after
+  // per request: first page freed, lengths before and after, a short row's entries
+  extern __shared__ int sm_req[];
   __shared__ long long sm_scan[2 * PG_WARPS];
-  const int B = a.requests, tid = threadIdx.x;
+  __shared__ long long sm_total;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x, ctas = gridDim.x, share = pages_share(a.requests, ctas);
+  const int first = min(a.requests, rank * share), B = min(share, a.requests - first);
   int* sm_rank = sm_req;
-  int* sm_len = sm_rank + B;
-  int* sm_keep = sm_len + B;
+  int* sm_len = sm_rank + share;
+  int* sm_keep = sm_len + share;
+  int* sm_page = sm_keep + share;           // [PG_SHORT][share]
   const int per = (B + PG_THREADS - 1) / PG_THREADS;
   const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
   long long count = *a.count;
@@ -245,62 +269,158 @@ __global__ void __launch_bounds__(PG_THREADS) kv_truncate_kernel(const PagesArgs
     const long long n = blocks_of(tokens < 0 ? 0 : tokens, a.page_shift);
     return n < a.width ? n : a.width;
   };
-  Pair mine{0, 0}, all;
+  auto row_of = [&](int b) { return a.table + static_cast<long long>(first + b) * a.table_stride; };
+  // the blocks that a request loses: from j0 on
+  auto blocks = [&](int b, long long& j0) {
+    j0 = blocks_in_row(sm_keep[b]);
+    return static_cast<int>(blocks_in_row(sm_len[b]) - j0);
+  };
+  // The pages among them, per request.  Short rows: each thread for its own.
   for (int b = b0; b < b1; ++b) {
-    const int len = a.lens[b], keep = max(0, min(a.change[b], len));
+    const int len = a.lens[first + b], keep = max(0, min(a.change[first + b], len));
     sm_len[b] = len;
     sm_keep[b] = len < 0 ? len : keep;
-    mine.a += blocks_in_row(len) - blocks_in_row(keep);
-  }
-  Pair at = block_scan(mine, sm_scan, all);
-  for (int b = b0; b < b1; ++b) {
-    sm_rank[b] = static_cast<int>(at.a);
-    at.a += blocks_in_row(sm_len[b]) - blocks_in_row(sm_keep[b]);
+    long long j0;
+    const int n = blocks(b, j0);
+    int pages = 0;
+    if (n <= PG_SHORT) {
+#pragma unroll
+      for (int i = 0; i < PG_SHORT; ++i) {
+        const int page = i < n ? row_of(b)[j0 + i] : -1;
+        sm_page[i * share + b] = page;
+        pages += page >= 0;
+      }
+    }
+    sm_rank[b] = n <= PG_SHORT ? pages : -1;
   }
   __syncthreads();
-  if (a.in_place) cluster_sync();           // every CTA has read its inputs
-  const int rank = blockIdx.x, ctas = gridDim.x;
-  for (int b = rank * PG_THREADS + tid; b < B; b += ctas * PG_THREADS) a.lens_out[b] = sm_keep[b];
+  // Long ones: a warp looks after the requests whose number is its own modulo the
+  // warps, so that neighbours (which often end together) go to different ones.
+  auto each_long = [&](auto f) {
+    for (int base = warp; base < B; base += 32 * PG_WARPS) {
+      const int mine = base + lane * PG_WARPS;
+      long long j0;
+      uint32_t bits = __ballot_sync(0xFFFFFFFFu, mine < B && blocks(mine, j0) > PG_SHORT);
+      f(base, bits);
+    }
+  };
+  each_long([&](int base, uint32_t bits) {
+    while (bits) {
+      int b[PG_ROWS], n[PG_ROWS], pages[PG_ROWS], most = 0;
+      long long j0[PG_ROWS];
+#pragma unroll
+      for (int u = 0; u < PG_ROWS; ++u) {
+        n[u] = pages[u] = 0;
+        b[u] = -1;
+        if (bits) {
+          b[u] = base + (__ffs(bits) - 1) * PG_WARPS;
+          bits &= bits - 1;
+          n[u] = blocks(b[u], j0[u]);
+        }
+        most = max(most, n[u]);
+      }
+      for (int k = lane; k < most; k += 32 * PG_BATCH) {
+        int page[PG_ROWS][PG_BATCH];
+#pragma unroll
+        for (int u = 0; u < PG_ROWS; ++u)
+#pragma unroll
+          for (int i = 0; i < PG_BATCH; ++i)
+            page[u][i] = k + 32 * i < n[u] ? row_of(b[u])[j0[u] + k + 32 * i] : -1;
+#pragma unroll
+        for (int u = 0; u < PG_ROWS; ++u)
+#pragma unroll
+          for (int i = 0; i < PG_BATCH; ++i) pages[u] += page[u][i] >= 0;
+      }
+#pragma unroll
+      for (int u = 0; u < PG_ROWS; ++u) {
+        const int all = __reduce_add_sync(0xFFFFFFFFu, pages[u]);
+        if (lane == 0 && b[u] >= 0) sm_rank[b[u]] = all;
+      }
+    }
+  });
+  __syncthreads();
+  Pair mine{0, 0}, all;
+  for (int b = b0; b < b1; ++b) mine.a += sm_rank[b];
+  Pair at = block_scan(mine, sm_scan, all);
+  for (int b = b0; b < b1; ++b) {
+    const int n = sm_rank[b];
+    sm_rank[b] = static_cast<int>(at.a);
+    at.a += n;
+  }
+  long long total = all.a, before = 0;
+  if (ctas > 1) {
+    if (tid == 0) sm_total = all.a;
+    cluster_sync();                         // every CTA has read its inputs and counted its pages
+    total = lane < ctas ? ld_shared_cluster_s64(map_to_cta(smem_u32(&sm_total), lane)) : 0;
+    before = lane < rank ? total : 0;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
+      before += __shfl_xor_sync(0xFFFFFFFFu, before, d);
+    }
+    cluster_arrive();
+  } else {
+    __syncthreads();
+  }
+  for (int b = tid; b < B; b += PG_THREADS) a.lens_out[first + b] = sm_keep[b];
   if (rank == 0 && tid == 0) {
-    const long long n = count + all.a;
+    const long long n = count + total;
     a.counts_out[0] = static_cast<int>(n < a.stack_size ? n : a.stack_size);
     a.counts_out[1] = static_cast<int>(n < a.stack_size ? 0 : n - a.stack_size);
   }
-  const int warp = tid >> 5, lane = tid & 31;
-  for (int b = rank * PG_WARPS + warp; b < B; b += ctas * PG_WARPS) {
-    const long long j0 = blocks_in_row(sm_keep[b]), j1 = blocks_in_row(sm_len[b]);
-    int* row = a.table + static_cast<long long>(b) * a.table_stride;
-    for (long long j = j0 + lane; j < j1; j += 32) {
-      const long long to = count + all.a - 1 - (sm_rank[b] + (j - j0));
-      if (to < a.stack_size) a.stack[to] = row[j];
-      row[j] = -1;
+  const long long top = count + total - 1 - before;
+  auto push = [&](int page, int i) {
+    if (top - i < a.stack_size) a.stack[top - i] = page;
+  };
+  for (int b = tid; b < B; b += PG_THREADS) {
+    long long j0;
+    const int n = blocks(b, j0);
+    if (n > PG_SHORT) continue;
+    int i_th = sm_rank[b];
+#pragma unroll
+    for (int i = 0; i < PG_SHORT; ++i) {
+      const int page = sm_page[i * share + b];
+      if (page >= 0) {
+        push(page, i_th++);
+        row_of(b)[j0 + i] = -1;
+      }
     }
   }
+  each_long([&](int base, uint32_t bits) {
+    for (; bits; bits &= bits - 1) {
+      const int b = base + (__ffs(bits) - 1) * PG_WARPS;
+      long long j0;
+      const int n = blocks(b, j0);
+      int i_th = sm_rank[b];
+      int* row = row_of(b) + j0;
+      for (int k0 = 0; k0 < n; k0 += 32 * PG_BATCH) {
+        const int k = k0 + lane;
+        int page[PG_BATCH];
+#pragma unroll
+        for (int i = 0; i < PG_BATCH; ++i) page[i] = k + 32 * i < n ? row[k + 32 * i] : -1;
+#pragma unroll
+        for (int i = 0; i < PG_BATCH; ++i) {
+          const uint32_t have = __ballot_sync(0xFFFFFFFFu, page[i] >= 0);
+          if (page[i] >= 0) {
+            push(page[i], i_th + __popc(have & ((1u << lane) - 1u)));
+            row[k + 32 * i] = -1;
+          }
+          i_th += __popc(have);
+        }
+      }
+    }
+  });
+  __syncwarp();
+  if (ctas > 1) cluster_wait();             // nobody reads this CTA's total any more
 }
 
-cudaError_t launch_pages(void (*kern)(const PagesArgs), PagesArgs& a, size_t smem,
-                         cudaStream_t st) {
+cudaError_t launch_pages(void (*kern)(const PagesArgs), const PagesArgs& a, int64_t ctas,
+                         size_t smem, cudaStream_t st) {
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(
         kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  const char* in[3] = {reinterpret_cast<const char*>(a.lens),
-                       reinterpret_cast<const char*>(a.change),
-                       reinterpret_cast<const char*>(a.count)};
-  const int64_t in_bytes[3] = {4ll * a.requests, 4ll * a.requests, 4};
-  const char* out[3] = {reinterpret_cast<const char*>(a.lens_out),
-                        reinterpret_cast<const char*>(a.counts_out),
-                        reinterpret_cast<const char*>(a.cu)};
-  const int64_t out_bytes[3] = {4ll * a.requests, 8, a.cu ? 4ll * (a.requests + 1) : 0};
-  a.in_place = 0;
-  for (int i = 0; i < 3; ++i)
-    for (int o = 0; o < 3; ++o)
-      if (in[i] < out[o] + out_bytes[o] && out[o] < in[i] + in_bytes[i]) a.in_place = 1;
-  // a warp for every 4 requests or 128 slots
-  const int64_t want = (a.requests / 4 + a.max_tokens / 128) / PG_WARPS;
-  const int64_t most = a.in_place ? PG_CLUSTER : PG_MAX_CTAS;
-  const int64_t ctas = want < 1 ? 1 : (want > most ? most : (a.in_place ? PG_CLUSTER : want));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(PG_THREADS);
@@ -339,7 +459,20 @@ cudaError_t launch_kv_extend(const int* lens, const int* fresh, int64_t requests
   a.slots = reinterpret_cast<long long*>(slots);
   a.max_tokens = max_tokens;
   a.counts_out = counts_out;
-  return launch_pages(kv_extend_kernel, a, (3 * requests + 1) * sizeof(int), st);
+  const char* in[3] = {reinterpret_cast<const char*>(lens), reinterpret_cast<const char*>(fresh),
+                       reinterpret_cast<const char*>(count)};
+  const int64_t in_bytes[3] = {4 * requests, 4 * requests, 4};
+  const char* out[3] = {reinterpret_cast<const char*>(lens_out),
+                        reinterpret_cast<const char*>(counts_out), reinterpret_cast<const char*>(cu)};
+  const int64_t out_bytes[3] = {4 * requests, 8, 4 * (requests + 1)};
+  for (int i = 0; i < 3; ++i)
+    for (int o = 0; o < 3; ++o)
+      if (in[i] < out[o] + out_bytes[o] && out[o] < in[i] + in_bytes[i]) a.in_place = 1;
+  // a warp for every 4 requests or 128 slots
+  const int64_t want = (requests / 4 + max_tokens / 128) / PG_WARPS;
+  const int64_t most = a.in_place ? PG_CLUSTER : PG_MAX_CTAS;
+  const int64_t ctas = want < 1 ? 1 : (want > most || a.in_place ? most : want);
+  return launch_pages(kv_extend_kernel, a, ctas, (3 * requests + 1) * sizeof(int), st);
 }
 
 cudaError_t launch_kv_truncate(const int* lens, const int* keep, int64_t requests, int* table,
@@ -359,7 +492,11 @@ cudaError_t launch_kv_truncate(const int* lens, const int* keep, int64_t request
   a.requests = static_cast<int>(requests);
   a.lens_out = lens_out;
   a.counts_out = counts_out;
-  return launch_pages(kv_truncate_kernel, a, 3 * requests * sizeof(int), st);
+  a.in_place = 1;                           // the table
+  // one CTA where its threads have a request each: a cluster's barriers take
+  // longer than sharing out saves
+  const int ctas = requests <= PG_THREADS ? 1 : PG_CLUSTER;
+  return launch_pages(kv_truncate_kernel, a, ctas, (3 + PG_SHORT) * pages_share(a.requests, ctas) * sizeof(int), st);
 }
 
 }  // namespace mxk

@@ -483,9 +483,11 @@ mx_status mx_kv_extend(const int32_t* lens, const int32_t* new_tokens, int64_t r
  * mx_kv_truncate -- drop tokens from the ends of requests (drafted tokens that
  * were rejected; keep 0 for a finished request).  Request b keeps
  * min(max(keep[b], 0), lens[b]) tokens; the pages behind them go back on the
- * stack and their table entries become -1.  Of the n pages freed (in request
- * order, then table order) the i-th is written to stack[count + n - 1 - i], so
- * that an mx_kv_extend by as many tokens hands out the same pages again.
+ * stack and their table entries become -1; an entry that is negative already
+ * (a page given back before, in front of a window) frees none.  Of the n pages
+ * freed (in request order, then table order) the i-th is written to
+ * stack[count + n - 1 - i], so that an mx_kv_extend by as many tokens hands out
+ * the same pages again.
  * counts_out: free pages, and pages that the stack had no room for (0 when
  * stack_size is the cache's number of pages).  The rest as above.
  */
