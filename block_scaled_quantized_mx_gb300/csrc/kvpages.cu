@@ -32,6 +32,7 @@
 // tenth of them with whole prompts (200000 new tokens), 16.4 us (with a page
 // read per token and eight CTAs 39; with truncate's pages taken from the lengths,
 // holes and all, 14.5; with every one of its CTAs counting all rows 27).
+#include <atomic>
 #include <cstdint>
 
 #include "common.cuh"
@@ -46,6 +47,8 @@ constexpr int PG_THREADS = 512;
 constexpr int PG_WARPS = PG_THREADS / 32;
 constexpr int PG_CLUSTER = 8;
 constexpr int PG_MAX_CTAS = 128;
+constexpr int PG_MAX_REQUESTS = 16384;
+constexpr int PG_SMEM_FREE = 48 * 1024;     // shared memory that a launch gets unasked
 
 // Sum of two values over the block's threads before this one (exclusive), in
 // thread order; `all` receives the block's totals.  Uses `sm` (2 x PG_WARPS).
@@ -416,11 +419,6 @@ __global__ void __launch_bounds__(PG_THREADS) kv_truncate_kernel(const PagesArgs
 
 cudaError_t launch_pages(void (*kern)(const PagesArgs), const PagesArgs& a, int64_t ctas,
                          size_t smem, cudaStream_t st) {
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(PG_THREADS);
@@ -472,7 +470,22 @@ cudaError_t launch_kv_extend(const int* lens, const int* fresh, int64_t requests
   const int64_t want = (requests / 4 + max_tokens / 128) / PG_WARPS;
   const int64_t most = a.in_place ? PG_CLUSTER : PG_MAX_CTAS;
   const int64_t ctas = want < 1 ? 1 : (want > most || a.in_place ? most : want);
-  return launch_pages(kv_extend_kernel, a, ctas, (3 * requests + 1) * sizeof(int), st);
+  const size_t smem = (3 * requests + 1) * sizeof(int);
+  if (smem > PG_SMEM_FREE) {
+    // the limit belongs to the kernel, not to the launch: once, to the most that
+    // any call needs, so that calls on several host threads leave each other theirs
+    constexpr int most_smem = (3 * PG_MAX_REQUESTS + 1) * sizeof(int);
+    static std::atomic<bool> set[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !set[dev].load(std::memory_order_relaxed)) {
+      e = cudaFuncSetAttribute(kv_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem);
+      if (e != cudaSuccess) return e;
+      if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
+    }
+  }
+  return launch_pages(kv_extend_kernel, a, ctas, smem, st);
 }
 
 cudaError_t launch_kv_truncate(const int* lens, const int* keep, int64_t requests, int* table,
@@ -496,6 +509,7 @@ cudaError_t launch_kv_truncate(const int* lens, const int* keep, int64_t request
   // one CTA where its threads have a request each: a cluster's barriers take
   // longer than sharing out saves
   const int ctas = requests <= PG_THREADS ? 1 : PG_CLUSTER;
+  static_assert((3 + PG_SHORT) * PG_MAX_REQUESTS / PG_CLUSTER * sizeof(int) <= PG_SMEM_FREE, "");
   return launch_pages(kv_truncate_kernel, a, ctas, (3 + PG_SHORT) * pages_share(a.requests, ctas) * sizeof(int), st);
 }
 

@@ -84,3 +84,37 @@ def test_truncate_where_the_stack_has_no_room_for_all():
     cut = mx.mx_kv_truncate(_i32([64, 64]), _i32([0, 0]), table, stack, _i32([2]), 16)
     # freed: 3 4 5 6 7 8; the i-th to stack[7 - i], of which there are four
     assert cut.counts.tolist() == [4, 4] and stack.tolist() == [0, 1, 8, 7] and (table == -1).all()
+
+
+def test_extend_from_two_threads():
+    """Calls of very different size at the same time: neither changes what the
+    other may launch."""
+    import threading
+
+    wrong = []
+
+    def calls(B, times):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                lens, new = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.ones(B, dtype=torch.int32, device="cuda")
+                table, stack = torch.full((B, 1), -1, dtype=torch.int32, device="cuda"), _i32(np.arange(B))
+                count = _i32([B])
+                plan = mx.mx_kv_extend(lens, new, table, stack, count, 16, B)
+                call, args = mx.lib().mx_kv_extend, (
+                    lens.data_ptr(), new.data_ptr(), B, table.data_ptr(), 1, 1, stack.data_ptr(), B,
+                    count.data_ptr(), 16, plan.lens.data_ptr(), plan.cu.data_ptr(), plan.slots.data_ptr(), B,
+                    plan.counts.data_ptr(), stream.cuda_stream)
+                status = [call(*args) for _ in range(times)]
+                stream.synchronize()
+                assert set(status) == {0}
+                assert plan.counts.tolist() == [0, 0] and (plan.slots == (B - 1 - torch.arange(B).cuda()) * 16).all()
+        except Exception as e:  # noqa: BLE001 -- shown below, by the thread that can fail the test
+            wrong.append((B, repr(e)))
+
+    threads = [threading.Thread(target=calls, args=a) for a in ((16384, 20000), (5000, 20000), (9000, 20000))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
