@@ -84,6 +84,28 @@ __device__ __forceinline__ int kv_end_key(const KvView& v, const KvReq& r, int i
   return p > 0 ? p : 0;
 }
 
+// The list of all requests' row tiles (`rows` rows each), and the request of a
+// tile in it.  Starts are kept in 32 bits.  Rows of Q that belong to one request
+// each make `most` tiles at most, a last one that is not full for every request
+// included; offsets that go up and down may name rows again and again, in any
+// number: the list then ends at `most`, and so do the starts.
+struct KvTileList {
+  long long most;
+  __host__ __device__ KvTileList(long long tokens, int group, int rows, int requests)
+      : most((tokens * group + rows - 1) / rows + requests) {}
+  __host__ __device__ long long clip(long long at) const { return at < most ? at : most; }
+  __host__ __device__ int start(long long at) const { return static_cast<int>(clip(at)); }
+  // the last of the requests that begins at or before tile f < clip(their sum)
+  static __host__ __device__ int request(const int* starts, int requests, long long f) {
+    int lo = 0, hi = requests - 1;
+    while (lo < hi) {
+      const int m = (lo + hi + 1) >> 1;
+      if (starts[m] <= f) lo = m; else hi = m - 1;
+    }
+    return lo;
+  }
+};
+
 // Whether the table entry of key j's page is followed: the page begins in front of
 // the request's end and does not end in front of `first`, the first key that any
 // row sees.  (A page behind the window may belong to another request by now,

@@ -383,27 +383,24 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     int* sm_rt = reinterpret_cast<int*>(gbase);                        // requests + 1
     long long* sm_scan = reinterpret_cast<long long*>(gbase + L::PG_OFF);
     const int B = a.v.requests;
+    const KvTileList list(a.v.tokens, a.v.group, KP_ROWS, B);
     const int per = (B + KP_THREADS - 1) / KP_THREADS;
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
     long long mine = 0, tiles;
     for (int b = b0; b < b1; ++b) mine += kp_row_tiles(a.v, kv_request(a.v, b));
     long long at = kp_scan(mine, sm_scan, tiles);
     for (int b = b0; b < b1; ++b) {
-      sm_rt[b] = static_cast<int>(at);
+      sm_rt[b] = list.start(at);
       at += kp_row_tiles(a.v, kv_request(a.v, b));
     }
+    tiles = list.clip(tiles);
     __syncthreads();
     const long long tper = (tiles + KP_THREADS - 1) / KP_THREADS;
     const long long f0 = min(tiles, tid * tper), f1 = min(tiles, f0 + tper);
     // walks the row tiles [f0, f1): calls f(b, rt, request) for each
     auto each = [&](auto f) {
       if (f0 >= f1) return;
-      int lo = 0, hi = B - 1;                // the last request that begins at or before f0
-      while (lo < hi) {
-        const int m = (lo + hi + 1) >> 1;
-        if (sm_rt[m] <= f0) lo = m; else hi = m - 1;
-      }
-      int b = lo;
+      int b = KvTileList::request(sm_rt, B, f0);
       KvReq r = kv_request(a.v, b);
       int rt = static_cast<int>(f0 - sm_rt[b]), n = kp_row_tiles(a.v, r);
       for (long long i = f0; i < f1; ++i, ++rt) {
