@@ -564,7 +564,7 @@ class KVCache:
         return (self.fmt, k.data_ptr(), v.data_ptr(), ks.data_ptr(),
                 vs.data_ptr(), k.shape, v.shape, ks.shape, vs.shape,
                 k.is_contiguous(), v.is_contiguous(), ks.is_contiguous(),
-                vs.is_contiguous(), k.dtype, v.dtype, ks.dtype, vs.dtype)
+                vs.is_contiguous())
 
     def c(self) -> CKVCache:
         """The planes as they are now, checked again if any of them changed."""

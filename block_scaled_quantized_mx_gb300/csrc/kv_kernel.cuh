@@ -119,11 +119,6 @@ __device__ __forceinline__ float kv_scale_value(uint32_t c) {
   return __uint_as_float(c == 0 ? 0x00400000u : c == 0xFFu ? 0x7FC00000u : (c << 23));
 }
 
-// 2^e; zero below 2^-126 (what it would multiply is beyond fp32 of the rest).
-__device__ __forceinline__ float kv_exp2i(int e) {
-  return e < -126 ? 0.0f : __uint_as_float(static_cast<uint32_t>(min(e, 127) + 127) << 23);
-}
-
 // A row's running maximum before its first score above -infinity.  Finite, so that
 // x_j - m stays -infinity for scores of -infinity, hidden or real: they weigh
 // nothing, whatever comes beside them.  A part states it for a row that saw such
@@ -144,16 +139,18 @@ __device__ __forceinline__ float kv_inverse(float sum, bool saw_keys) {
 // where v is at least the largest x_j - m + e_j of the keys that the row itself
 // sees, less KV_LAZY, and at most that rounded up: the product that weighs most
 // stands between 2^6 and 2^15.  Keys that a row does not see, and pages of large
-// values that it gives no weight, leave the others' precision alone.  m and v are
-// whole numbers: moving either is exact, and so is what the sum of the weights
-// takes out again, 2^(e_j - v + 7).
+// values that it gives no weight, leave the others' precision alone.  The sum of
+// the weights takes 2^(e_j - v + 7) out again.  (m is a score, not one rounded to a
+// whole number: the key that it comes from, often most of the row's weight, then
+// has no rounding at all.  With m rounded up, outputs in f16 were off by 2.9e-4
+// instead of 2.4e-4.)
 constexpr float KV_LAZY = 8.0f;            // slack of m and of v
 constexpr int KV_P_EXP = 7;
 constexpr float KV_NO_V = -300.0f;         // v of a row that has seen nothing: below every other
 
 // m for a row whose next scores are x_top at most.
 __device__ __forceinline__ float kv_next_m(float m, float x_top) {
-  return x_top > m + KV_LAZY ? ceilf(x_top) : m;
+  return x_top > m + KV_LAZY ? x_top : m;
 }
 // v for a row whose m moved by dm = m_old - m_new, to the next keys' largest
 // x_j - m_new + e_j.
@@ -173,14 +170,14 @@ __device__ __forceinline__ float kv_p_shift(float e, float v) {
   return fmaxf(e - v + static_cast<float>(KV_P_EXP), -60.0f);
 }
 
-// 2^-b for such a whole number b (0 beyond 126: weights of less than 2^-110).
+// 2^-b of such a shift (0 beyond 126: weights of less than 2^-110).
 __device__ __forceinline__ float kv_unshift(float b) { return ex2_approx(-b); }
 
 // The unit of O, 2^(v - 127 - 7), as two factors: v goes from -16 to 262.
 __device__ __forceinline__ void kv_o_unit(float v, float& f0, float& f1) {
-  const int e = static_cast<int>(v) - 127 - KV_P_EXP, half = e >> 1;
-  f0 = kv_exp2i(half);
-  f1 = kv_exp2i(e - half);
+  const float e = v - static_cast<float>(127 + KV_P_EXP), half = floorf(0.5f * e);
+  f0 = ex2_approx(half);
+  f1 = ex2_approx(e - half);
 }
 
 // For a row whose largest |value| has the bit pattern `top`: powers of two
