@@ -13,7 +13,6 @@ from tests import _kv
 pytestmark = pytest.mark.gpu
 BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
 TOP = {mx.E4M3: 448.0, mx.E5M2: 57344.0, mx.INT8: 128.0}
-D = 64
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -24,12 +23,12 @@ def _built():
 
 class One:
     """One request of n keys in pages of `page` in a shuffled pool, one cache
-    head, `rows` new tokens and two query heads.  key(j) and value(j) give the
-    values of K and V as n x D arrays; the planes may be changed afterwards."""
+    head, `rows` new tokens and two query heads.  key and value: K and V as n x d
+    arrays; the planes may be changed afterwards."""
 
-    def __init__(self, n, rows, page, key, value, q, fmt=mx.E4M3, d=D, seed=0):
+    def __init__(self, n, rows, page, key, value, q, fmt=mx.E4M3, seed=0):
         g = torch.Generator().manual_seed(seed)
-        pages = -(-n // page)
+        pages, d = -(-n // page), key.shape[1]
         ids = torch.randperm(pages + 2, generator=g)[:pages]
         self.n, self.rows, self.page, self.fmt, self.d, self.ids = n, rows, page, fmt, d, ids.numpy()
         self.cache = mx.empty_kv_cache(fmt, pages + 2, 1, page, d)
@@ -93,7 +92,7 @@ class One:
         return out, tol
 
 
-def _noise(n, d=D, seed=1):
+def _noise(n, d, seed=1):
     return torch.randn(n, d, generator=torch.Generator().manual_seed(seed)).clamp(-4, 4)
 
 
@@ -104,16 +103,16 @@ FEW, MANY = [(250, 1), (6000, 3)], [(300, 40), (9000, 70)]
 
 @pytest.mark.parametrize("n,rows", FEW + MANY)
 @pytest.mark.parametrize("ws", [True, False])
-@pytest.mark.parametrize("page", [16, 64])
-def test_keys_of_minus_infinity_beside_others(n, rows, ws, page):
+@pytest.mark.parametrize("page,d", [(16, 64), (64, 64), (32, 128)])
+def test_keys_of_minus_infinity_beside_others(n, rows, ws, page, d):
     """Scores that overflow to -infinity weigh nothing where the row has
     finite ones, whoever else they share a warp, a segment or a part with."""
     far = np.arange(0, n // 2 // page * page)             # whole pages
     far = far[(far // page) % 7 != 3] if n > 1000 else far
-    key = _noise(n) * 0.1
+    key = _noise(n, d) * 0.1
     key[far] = -4.0
-    q = torch.ones(rows * 2, D) + 0.1 * _noise(rows * 2, seed=3)
-    s = One(n, rows, page, key, _noise(n, seed=2), q)
+    q = torch.ones(rows * 2, d) + 0.1 * _noise(rows * 2, d, seed=3)
+    s = One(n, rows, page, key, _noise(n, d, seed=2), q)
     s.cache.k_scales[torch.from_numpy(s.ids[np.unique(far // page)])] = 254      # -2^135 and below: -infinity
     out, tol = s.exact(skip=far)
     got = s.run(ws=ws)
@@ -121,7 +120,7 @@ def test_keys_of_minus_infinity_beside_others(n, rows, ws, page):
     # a row that has no finite score at all is NaN still, and alone in it
     s.q[0, 1] = 0
     s.q[0, 1, 5] = 1
-    s.cache.k.view(-1, D)[:, 5] = 0xFE                    # -448
+    s.cache.k.view(-1, d)[:, 5] = 0xFE                    # -448
     s.cache.k_scales.fill_(254)
     got = s.run(ws=ws)
     assert np.isnan(got[0, 1]).all()
@@ -129,16 +128,16 @@ def test_keys_of_minus_infinity_beside_others(n, rows, ws, page):
 
 @pytest.mark.parametrize("n,rows", FEW + MANY)
 @pytest.mark.parametrize("ws", [True, False])
-@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("page,d", [(16, 64), (64, 64), (16, 128), (32, 128)])
 @pytest.mark.parametrize("fmt", [mx.E4M3, mx.INT8])
-def test_large_values_of_no_weight(n, rows, ws, page, fmt):
+def test_large_values_of_no_weight(n, rows, ws, page, d, fmt):
     """Values of 2^33 in every third page, with weights of e^-40: what the
     other pages give has to survive beside them."""
     far = (np.arange(n) // page) % 3 == 1
-    key, value = _noise(n) * 0.05 + 2.5, _noise(n, seed=2)
-    key[far] -= 5.0
+    key, value = _noise(n, d) * 0.05 + 2.5, _noise(n, d, seed=2)
+    key[far] -= 5.0 if d == 64 else 5.0 * 2 ** -0.5
     value[far] *= 2.0 ** 33
-    s = One(n, rows, page, key, value, torch.ones(rows * 2, D), fmt=fmt)
+    s = One(n, rows, page, key, value, torch.ones(rows * 2, d), fmt=fmt)
     out, tol = s.exact()
     assert (np.abs(out) > 4 * tol).mean() > 0.5            # the bound can tell them from zero
     assert (np.abs(s.run(ws=ws) - out) <= tol).all()
@@ -147,12 +146,13 @@ def test_large_values_of_no_weight(n, rows, ws, page, fmt):
 @pytest.mark.parametrize("n,rows", [(259, 5), (6003, 5), (300, 40), (9000, 70)])
 @pytest.mark.parametrize("ws", [True, False])
 @pytest.mark.parametrize("up", [12, 40, 90])
-def test_large_values_that_a_row_does_not_see(n, rows, ws, up):
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_values_that_a_row_does_not_see(n, rows, ws, up, d):
     """The last page's values are 2^up times the others': rows in front of it
     do not know it.  The same in front of a window that begins inside a page
     and behind whole ones."""
     page = 16
-    s = One(n, rows, page, _noise(n), _noise(n, seed=2), _noise(rows * 2, seed=3))
+    s = One(n, rows, page, _noise(n, d), _noise(n, d, seed=2), _noise(rows * 2, d, seed=3))
     s.cache.v_scales[int(s.ids[-1])] += up
     out, tol = s.exact()
     before = n - rows + np.arange(rows) < (n - 1) // page * page
@@ -169,12 +169,12 @@ def test_large_values_that_a_row_does_not_see(n, rows, ws, up):
 
 @pytest.mark.parametrize("n,rows,window", [(250, 1, 100), (6000, 3, 990), (300, 40, 70), (9000, 70, 100)])
 @pytest.mark.parametrize("ws", [True, False])
-@pytest.mark.parametrize("fmt", [mx.E4M3, mx.E5M2])
-def test_pages_in_front_of_the_window_are_not_followed(n, rows, window, ws, fmt):
+@pytest.mark.parametrize("fmt,d", [(mx.E4M3, 64), (mx.E5M2, 64), (mx.E4M3, 128)])
+def test_pages_in_front_of_the_window_are_not_followed(n, rows, window, ws, fmt, d):
     """Pages that no row sees may belong to another request by now, whatever
     the table still says: NaN codes and any scale in them change no bit."""
     page = 16
-    s = One(n, rows, page, _noise(n), _noise(n, seed=2), _noise(rows * 2, seed=3), fmt=fmt)
+    s = One(n, rows, page, _noise(n, d), _noise(n, d, seed=2), _noise(rows * 2, d, seed=3), fmt=fmt)
     want = s.run(window=window, ws=ws)
     out, tol = s.exact(window=window)
     assert (np.abs(want - out) <= tol).all()
