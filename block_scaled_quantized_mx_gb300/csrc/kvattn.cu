@@ -1122,13 +1122,13 @@ namespace {
 // Which kernel: the one in this file reads a request's keys once per 16 rows of
 // a cache head, the prompt kernel once per 256 but with more to set up and a
 // longer way from one step to the next.  Measured with 8 cache heads of 128
-// values (this kernel against the prompt kernel): 32 rows, 1 request of 2000
-// keys 12 against 24 us, of 32000 35 against 44, 16 requests of 500 18 against
-// 22, of 6000 87 against 80, 64 of 6000 458 against 265; 48 rows, 1 of 32000 47
-// against 45, 16 of 500 22 against 22, of 6000 134 against 81, 64 of 6000 675
-// against 265.  With 64 values: 32 rows, 8 of 16000 77 against 90, 48 rows 106
-// against 91.  (Between 17 and 32 rows it depends on the lengths, which the
-// host does not know.)
+// values (this kernel with 16 rows a tile against the prompt kernel): 32 rows, 1
+// request of 2000 keys 14 against 24 us, of 32000 35 against 45, 16 requests of
+// 500 19 against 22, of 6000 76 against 82, 64 of 500 51 against 61, of 6000 259
+// against 271; 48 rows, 1 of 32000 44 against 45, 16 of 500 24 against 22, of
+// 6000 106 against 82, 64 of 6000 378 against 272.  With 64 values: 32 rows, 8 of
+// 16000 69 against 91, 64 of 2000 85 against 102, 48 rows 97 against 94, 118
+// against 103.
 constexpr int64_t KA_MOST_ROWS = 32;
 bool many_rows(int64_t max_q, int64_t group) { return max_q * group > KA_MOST_ROWS; }
 

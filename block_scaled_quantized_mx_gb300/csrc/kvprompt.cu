@@ -35,7 +35,7 @@
 //     tensor memory: 237 us against 231; two buffers and one warp: 248; one
 //     buffer of 128 keys: 240).
 // A 2048-token chunk over 8192 keys (32 heads on 8 cache heads of 128) takes
-// 219 us, 0.57 of the measured bf16 rate.  Of these the join takes ~11 and
+// 217 us, 0.58 of the measured bf16 rate.  Of these the join takes ~11 and
 // beginning and ending units ~20; a block of 128 keys for both tiles ~3700
 // clocks, where its products alone need 2480 (in steps of 64 keys a product of
 // Q K^T takes 48 clocks, not 32).  With no conversion and no exponentials it

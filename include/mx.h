@@ -561,8 +561,9 @@ mx_status mx_kv_append(const mx_kv_cache* cache, const void* K, const void* V, i
  *              that run at the same time).  With it the keys of one request
  *              are spread over many SMs; NULL or a smaller size: they are not.
  * mx_kv_attention_workspace_bytes does not depend on lengths or the number of
- * requests (about 7 MB, or 40 MB where max_q * q_heads / heads > 32 and d = 128); 0
- * on bad arguments or without a compute capability 10.3 device.  The two
+ * requests (5 MB for d = 128 and 3 for d = 64; 40 and 21 where
+ * max_q * q_heads / heads > 32); 0 on bad arguments or without a compute
+ * capability 10.3 device.  The two
  * kernels and the two modes sum in different orders: results can differ
  * between them in the last bits, and are the same from run to run.
  */
