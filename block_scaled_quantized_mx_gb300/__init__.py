@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 from dataclasses import dataclass
 
@@ -47,7 +48,8 @@ EXPORTS = ("mx_data_bytes", "mx_scale_bytes", "mx_quantize", "mx_gemm",
            "mx_selftest_wait_timeout", "mx_scales_to_rowmajor",
            "mx_status_string", "mx_version", "mx_set_tile_width",
            "mx_kv_extend", "mx_kv_truncate", "mx_kv_append",
-           "mx_kv_attention_workspace_bytes", "mx_kv_attention")
+           "mx_kv_attention_workspace_bytes", "mx_kv_attention",
+           "mx_rmsnorm_quantize", "mx_dequantize", "mx_rope")
 
 
 class MXError(RuntimeError):
@@ -75,6 +77,16 @@ class CKVCache(ctypes.Structure):
                 ("fmt", ctypes.c_int32), ("page", ctypes.c_int32),
                 ("pages", ctypes.c_int64), ("heads", ctypes.c_int64),
                 ("d", ctypes.c_int64)]
+
+
+class CRopeOperand(ctypes.Structure):
+    """Mirror of struct mx_rope_operand."""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p),
+                ("heads", ctypes.c_int64),
+                ("x_token_stride", ctypes.c_int64),
+                ("x_head_stride", ctypes.c_int64),
+                ("y_token_stride", ctypes.c_int64),
+                ("y_head_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -173,6 +185,15 @@ def lib() -> ctypes.CDLL:
     L.mx_kv_attention.argtypes = [p, i32, i64, i64, i64, i64, pc, p, i64, i64,
                                   p, p, i64, i64, p, i32, i64, i64, i32, i64,
                                   ctypes.c_float, p, sz, p]
+    L.mx_rmsnorm_quantize.restype = i32
+    L.mx_rmsnorm_quantize.argtypes = [p, i32, i64, p, i32, i64, p,
+                                      ctypes.c_float, p, i64, pt, p]
+    L.mx_dequantize.restype = i32
+    L.mx_dequantize.argtypes = [pt, p, i32, i64, p]
+    pr = ctypes.POINTER(CRopeOperand)
+    L.mx_rope.restype = i32
+    L.mx_rope.argtypes = [pr, pr, i32, i64, i64, p, i64, ctypes.c_float, p, p,
+                          p, i64, i32, i32, p]
     _lib = L
     return L
 
@@ -520,6 +541,180 @@ def flash_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
 def flash_attention_workspace_bytes(BH: int, Lq: int, Lk: int, d: int) -> int:
     """Bytes of workspace flash_attention splits into (0: no split)."""
     return int(lib().flash_attention_workspace_bytes(BH, Lq, Lk, d))
+
+
+def _same_gpu(*tensors):
+    """A call's operands lie in the current GPU's memory, on whose stream it
+    runs."""
+    for t in tensors:
+        if t is not None and not (t.is_cuda and
+                                  t.get_device() == torch.cuda.current_device()):
+            raise ValueError("operands must be CUDA tensors of the current GPU")
+
+
+def _matrix(t: torch.Tensor, name: str, rows=None, cols=None):
+    """Checks a 2-D floating operand; its type's code, address and row stride."""
+    dt = _KV_OUT_DTYPES.get(t.dtype)
+    if dt is None or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D fp32, fp16 or bf16 tensor")
+    if rows is not None and tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} must be {rows} x {cols}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have a unit inner stride")
+    return dt, t.data_ptr() if t.numel() else None, t.stride(0)
+
+
+def mx_rmsnorm_quantize(X: torch.Tensor, weight: torch.Tensor, fmt: int,
+                        residual: torch.Tensor | None = None,
+                        eps: float = 1e-6,
+                        residual_out: torch.Tensor | None = None,
+                        out: MXTensor | None = None, stream=None):
+    """h = X + residual and the MX tensor (E4M3, E5M2 or E2M1) of
+    h / sqrt(mean(h^2) + eps) * weight, norm and mean along a row, in one pass.
+    X and residual: rows x K of fp32, fp16 or bf16, K a multiple of 32 up to
+    32768; weight: K fp32 values.  Returns (the MX tensor, h in residual's type);
+    without a residual (the MX tensor, None).  residual_out may be residual or X
+    itself."""
+    xdt, px, ldx = _matrix(X, "X")
+    rows, K = X.shape
+    if weight.dtype != torch.float32 or weight.dim() != 1 or \
+            not weight.is_contiguous() or weight.numel() != K:
+        raise ValueError("weight must be K contiguous float32 values")
+    _same_gpu(X, weight, residual, residual_out)
+    rdt, pr, ldr, po, ldo = 0, None, 0, None, 0
+    if residual is not None:
+        rdt, pr, ldr = _matrix(residual, "residual", rows, K)
+        if residual_out is None:
+            residual_out = torch.empty((rows, K), dtype=residual.dtype,
+                                       device=X.device)
+        odt, po, ldo = _matrix(residual_out, "residual_out", rows, K)
+        if odt != rdt:
+            raise ValueError("residual_out must be of residual's type")
+    elif residual_out is not None:
+        raise ValueError("there is no residual to write")
+    if out is None:
+        out = empty_mx(fmt, rows, K, X.device)
+    _check_mx(out, "out", fmt, rows, K)
+    _same_gpu(out.data, out.scales)
+    ct = out.c()
+    _check(lib().mx_rmsnorm_quantize(
+        px, xdt, ldx, pr, rdt, ldr, weight.data_ptr(), eps, po, ldo,
+        ctypes.byref(ct), _stream(stream)), "mx_rmsnorm_quantize")
+    return out, residual_out
+
+
+def mx_dequantize(A: MXTensor, out_dtype=torch.float32,
+                  out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values of an MX tensor of any format as an outer x K matrix."""
+    dt = _out_code(out_dtype, (torch.float32, torch.bfloat16, torch.float16))
+    _check_mx(A, "A")
+    _same_gpu(A.data, A.scales, out)
+    if out is None:
+        out = torch.empty((A.outer, A.K), dtype=out_dtype, device=A.data.device)
+    _check_out(out, A.outer, A.K, out_dtype)
+    ca = A.c()
+    _check(lib().mx_dequantize(ctypes.byref(ca),
+                               out.data_ptr() if out.numel() else None, dt,
+                               out.stride(0), _stream(stream)), "mx_dequantize")
+    return out
+
+
+@dataclass
+class Rope:
+    """Rotary frequencies: freq (int64 on the GPU, rot / 2), pair i's turns a
+    position in units of 2^-64 turn, and the factor of cosines and sines."""
+    freq: torch.Tensor
+    factor: float = 1.0
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "parts",
+                     factor: float = 1.0, original: int = 0, slow: float = 1.0,
+                     fast: float = 32.0, device="cuda") -> Rope:
+    """base^(-2 i / rot) radians a position for pair i of rot / 2, scaled for
+    contexts `factor` times as long as the `original` (factor 1: not at all):
+      linear  every frequency divided by factor
+      base    the base raised so that the slowest pair's is divided by factor
+      parts   pairs that turn `fast` times or more in `original` positions keep
+              theirs, those that turn `slow` times or less have it divided, in
+              between in proportion; cosines and sines times 1 + 0.1 ln factor"""
+    if rot < 16 or rot % 16:
+        raise ValueError("rot must be a multiple of 16")
+    if not base > 1.0 or not 1.0 <= factor < math.inf:
+        raise ValueError("base must be above 1, factor 1 or more")
+    if scaling not in ("linear", "base", "parts"):
+        raise ValueError("scaling must be linear, base or parts")
+    if scaling == "base":
+        base = base * factor ** (rot / (rot - 2))
+    f = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+    by = 1.0
+    if scaling == "linear":
+        f = [x / factor for x in f]
+    elif scaling == "parts" and factor != 1.0:
+        if original < 1 or not slow < fast:
+            raise ValueError("parts needs the original length, and slow < fast")
+        keep = [min(1.0, max(0.0, (original * x / (2 * math.pi) - slow) /
+                             (fast - slow))) for x in f]
+        f = [x * k + x / factor * (1.0 - k) for x, k in zip(f, keep)]
+        by = 1.0 + 0.1 * math.log(factor)
+    # below 2^62: a frequency is 1 radian at most
+    turns = [round(x / (2 * math.pi) * 2.0 ** 64) for x in f]
+    return Rope(torch.tensor(turns, dtype=torch.int64, device=device), by)
+
+
+def _rope_operand(x: torch.Tensor, y: torch.Tensor, name: str) -> CRopeOperand:
+    dt, shape, xt, xh = _kv_tensor(x, name)
+    ydt, yshape, yt, yh = _kv_tensor(y, "out")
+    if ydt != dt or yshape != shape:
+        raise ValueError(f"out must have {name}'s shape and type")
+    return CRopeOperand(x.data_ptr() if x.numel() else None,
+                        y.data_ptr() if y.numel() else None, shape[1],
+                        xt, xh, yt, yh)
+
+
+def mx_rope(Q: torch.Tensor, K: torch.Tensor | None, rope: Rope,
+            positions: torch.Tensor | None = None,
+            lens: torch.Tensor | None = None, cu: torch.Tensor | None = None,
+            neighbours: bool = False, backward: bool = False, out=None,
+            stream=None):
+    """Rotary positions of Q and K (tokens x heads x d, fp16 or bf16; K may be
+    None), of the first 2 * len(rope.freq) values of each head.  Positions: int32,
+    one per token, or the requests' lens and cu (mx_kv_extend's plan), tokens
+    of no request not being written.  Pairs are an element of the first half and its
+    like of the second, or `neighbours`.  backward: the transposed map, for
+    gradients.  out: (Q's, K's) outputs, which may be Q and K themselves.
+    Returns both."""
+    freq = rope.freq
+    if freq.dtype != torch.int64 or freq.dim() != 1 or not freq.is_contiguous():
+        raise ValueError("rope.freq must be a contiguous 1-D int64 tensor")
+    T, _, d = Q.shape
+    if K is not None and (K.dtype != Q.dtype or K.shape[0] != T or
+                          K.shape[2] != d):
+        raise ValueError("Q and K must have one type, tokens and d")
+    requests, p_pos, p_lens, p_cu = 0, None, None, None
+    if positions is not None:
+        p_pos = _int32(positions, "positions", T)
+    elif lens is None or cu is None:
+        raise ValueError("positions, or lens and cu, must be given")
+    else:
+        requests = lens.shape[0]
+        p_lens, p_cu = _int32(lens, "lens"), _int32(cu, "cu", requests + 1)
+    if out is None:
+        empty = _allocator(Q)
+        out = tuple(None if t is None else
+                    empty((T, t.shape[1], d), (t.shape[1] * d, d, 1), t.dtype)
+                    for t in (Q, K))
+    oq, ok = out
+    _same_gpu(Q, K, freq, positions, lens, cu, oq, ok)
+    a = _rope_operand(Q, oq, "Q")
+    b = None
+    if K is not None:
+        b = ctypes.byref(_rope_operand(K, ok, "K"))
+    _check(lib().mx_rope(
+        ctypes.byref(a), b, _KV_DTYPES[Q.dtype], T, d, freq.data_ptr(),
+        2 * freq.numel(), rope.factor, p_pos, p_lens, p_cu, requests,
+        1 if neighbours else 0, 1 if backward else 0, _stream(stream)),
+        "mx_rope")
+    return oq, ok
 
 
 @dataclass

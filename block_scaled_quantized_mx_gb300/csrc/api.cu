@@ -12,6 +12,7 @@
 #include "mx.h"
 #include "common.cuh"
 #include "kv_common.cuh"
+#include "layer_common.cuh"
 
 namespace {
 
@@ -462,6 +463,110 @@ mx_status mx_kv_attention(const void* Q, int32_t dtype, int64_t tokens, int64_t 
   a.ws = workspace;
   a.ws_bytes = workspace_bytes;
   return from_cuda(mxk::launch_kv_attention(a, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+bool is_dtype(int32_t t) { return t == MX_DT_F32 || t == MX_DT_BF16 || t == MX_DT_F16; }
+int64_t dtype_bytes(int32_t t) { return t == MX_DT_F32 ? 4 : 2; }
+
+// A row-major operand of rows x K values read or written 16 bytes at a time: its
+// row stride (free where there is one row).
+mx_status check_rows(const void* p, int32_t dtype, int64_t rows, int64_t K, int64_t ld) {
+  if (!p) return MX_ERR_INVALID_ARG;
+  if (rows > 1 && (ld < K || ld > kMaxDim || ld * dtype_bytes(dtype) % 16)) return MX_ERR_SHAPE;
+  if (!aligned16(p)) return MX_ERR_ALIGN;
+  return MX_OK;
+}
+
+}  // namespace
+
+mx_status mx_rmsnorm_quantize(const void* X, int32_t x_dtype, int64_t ldx, const void* residual,
+                              int32_t r_dtype, int64_t ldr, const float* weight, float eps,
+                              void* residual_out, int64_t ldo, const mx_tensor* out,
+                              void* stream) {
+  mx_status s = check_tensor(out);
+  if (s != MX_OK) return s;
+  if (is_int_fmt(out->fmt) || !is_dtype(x_dtype) || (residual && !is_dtype(r_dtype)))
+    return MX_ERR_INVALID_ARG;
+  if (!(eps >= 1e-30f) || eps > 3.0e38f) return MX_ERR_INVALID_ARG;
+  if (out->K > 32768) return MX_ERR_SHAPE;
+  if (out->outer == 0 || out->K == 0) return MX_OK;
+  if (!weight || (residual == nullptr) != (residual_out == nullptr)) return MX_ERR_INVALID_ARG;
+  if (!aligned16(weight)) return MX_ERR_ALIGN;
+  const int64_t rows = out->outer, K = out->K;
+  if ((s = check_rows(X, x_dtype, rows, K, ldx)) != MX_OK) return s;
+  if (residual) {
+    if ((s = check_rows(residual, r_dtype, rows, K, ldr)) != MX_OK) return s;
+    if ((s = check_rows(residual_out, r_dtype, rows, K, ldo)) != MX_OK) return s;
+  }
+  if ((s = check_device()) != MX_OK) return s;
+  return from_cuda(mxk::launch_rmsnorm_quantize(X, x_dtype, ldx, residual, r_dtype, ldr, weight, eps,
+                                                residual_out, ldo, out->fmt, rows, K, out->data,
+                                                out->scales, static_cast<cudaStream_t>(stream)));
+}
+
+mx_status mx_dequantize(const mx_tensor* A, void* out, int32_t dtype, int64_t ld, void* stream) {
+  mx_status s = check_tensor(A);
+  if (s != MX_OK) return s;
+  if (!is_dtype(dtype)) return MX_ERR_INVALID_ARG;
+  if (A->outer == 0 || A->K == 0) return MX_OK;
+  if ((s = check_rows(out, dtype, A->outer, A->K, ld)) != MX_OK) return s;
+  if ((s = check_device()) != MX_OK) return s;
+  return from_cuda(mxk::launch_dequantize(A->fmt, A->data, A->scales, A->outer, A->K, out, dtype, ld,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+mx_status mx_rope(const mx_rope_operand* a, const mx_rope_operand* b, int32_t dtype, int64_t tokens,
+                  int64_t d, const uint64_t* freq, int64_t rot, float factor,
+                  const int32_t* positions, const int32_t* lens, const int32_t* cu,
+                  int64_t requests, int32_t neighbours, int32_t backward, void* stream) {
+  if (!a) return MX_ERR_INVALID_ARG;
+  if (dtype != MX_DT_F16 && dtype != MX_DT_BF16) return MX_ERR_INVALID_ARG;
+  if ((neighbours != 0 && neighbours != 1) || (backward != 0 && backward != 1))
+    return MX_ERR_INVALID_ARG;
+  if (!(factor <= 3.0e38f && factor >= -3.0e38f)) return MX_ERR_INVALID_ARG;
+  if (d < 16 || d > 1024 || d % 8 || rot < 16 || rot > 512 || rot > d || rot % 16) return MX_ERR_SHAPE;
+  if (tokens < 0 || tokens > kMaxDim || requests < 0 || requests > kMaxDim) return MX_ERR_SHAPE;
+  mxk::RopeCall c{};
+  const mx_rope_operand* in[2] = {a, b};
+  mxk::RopeOperand* to[2] = {&c.a, &c.b};
+  for (int i = 0; i < 2; ++i) {
+    const mx_rope_operand* o = in[i];
+    if (!o) continue;
+    if (o->heads < 1 || o->heads > 65535) return MX_ERR_SHAPE;
+    if (tokens == 0) continue;
+    if (!o->x || !o->y) return MX_ERR_INVALID_ARG;
+    mx_status s = check_strides(tokens, o->heads, o->x_token_stride, o->x_head_stride, d);
+    if (s != MX_OK) return s;
+    s = check_strides(tokens, o->heads, o->y_token_stride, o->y_head_stride, d);
+    if (s != MX_OK) return s;
+    if (!aligned16(o->x) || !aligned16(o->y)) return MX_ERR_ALIGN;
+    to[i]->x = static_cast<const uint16_t*>(o->x);
+    to[i]->y = static_cast<uint16_t*>(o->y);
+    to[i]->x_ts = o->x_token_stride;
+    to[i]->x_hs = o->x_head_stride;
+    to[i]->y_ts = o->y_token_stride;
+    to[i]->y_hs = o->y_head_stride;
+    to[i]->heads = static_cast<int>(o->heads);
+  }
+  if (tokens == 0 || (!positions && requests == 0)) return MX_OK;
+  if (!freq || (!positions && (!lens || !cu))) return MX_ERR_INVALID_ARG;
+  mx_status s = check_device();
+  if (s != MX_OK) return s;
+  c.freq = freq;
+  c.positions = positions;
+  c.lens = lens;
+  c.cu = cu;
+  c.tokens = tokens;
+  c.requests = static_cast<int>(requests);
+  c.d = static_cast<int>(d);
+  c.rot = static_cast<int>(rot);
+  c.bf16 = dtype == MX_DT_BF16;
+  c.neighbours = neighbours;
+  c.backward = backward;
+  c.factor = factor;
+  return from_cuda(mxk::launch_rope(c, static_cast<cudaStream_t>(stream)));
 }
 
 mx_status gemm_f16(const void* A, const void* B, float* C, int32_t ab_dtype, int64_t M,

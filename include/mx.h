@@ -13,8 +13,12 @@
  *   *_fused      the same products with bias and GELU applied to the fp32
  *                accumulator in the epilogue, and mx_gemm_fused_quantize,
  *                which also quantizes C to an MX tensor for the next layer
+ *   mx_rmsnorm_quantize  residual addition, root-mean-square norm and MX
+ *                quantization in one pass; mx_dequantize, an MX tensor's values
+ *   mx_rope      rotary positions of queries and keys
  *   mx_kv_*      an 8-bit paged key/value cache: its block tables and slots,
- *                the quantizing write, and attention over it
+ *                pages that requests share, the quantizing write, and attention
+ *                over it
  *
  * Where these come from.  The quantized tensor as one object holding a data
  * plane and a scale plane, the scale format ("FP8 E8M0") and the block of 32
@@ -413,6 +417,85 @@ mx_status gemm_f16_splitk(const void* A, const void* B, float* C,
  */
 mx_status mx_gemm_splitk_noalloc(const mx_tensor* A, const mx_tensor* B, void* C,
                                  int32_t c_dtype, int64_t ldc, void* stream);
+
+/*
+ * mx_rmsnorm_quantize -- the A operand of a layer's next product from its
+ * residual stream, in one pass:
+ *   h = X + residual,  residual_out = h,
+ *   y[r][k] = h[r][k] / sqrt(mean_k h[r][k]^2 + eps) * weight[k],
+ * and out = the MX tensor that mx_quantize (MX_SRC_K_CONTIGUOUS) makes of y.
+ *
+ *   X             device, rows x K row-major, x_dtype (any mx_dtype); ldx >= K
+ *   residual      device, rows x K, r_dtype, ldr >= K; NULL: none (h = X)
+ *   residual_out  device, rows x K, r_dtype, ldo >= K: h rounded to r_dtype
+ *                 (the norm takes it before that rounding); NULL without a
+ *                 residual.  May be X or residual itself (same address, type and
+ *                 stride), and overlaps no other operand
+ *   weight        device, K fp32 values
+ *   eps           1e-30 or more
+ *   out           outer = rows, K up to 32768, E4M3, E5M2 or E2M1 (the formats that
+ *                 mx_gemm takes); the scales of rows that pad the last 128 are
+ *                 written as 0
+ * Pointers 16-byte aligned, row strides multiples of 16 bytes.  Sums are fp32.
+ * A NaN or an infinity in a row of h makes the scales of the blocks that it
+ * reaches 0xFF: all of the row's for a NaN, its own for an infinity (beside which
+ * the rest of the row is 0).
+ */
+mx_status mx_rmsnorm_quantize(const void* X, int32_t x_dtype, int64_t ldx, const void* residual,
+                              int32_t r_dtype, int64_t ldr, const float* weight, float eps,
+                              void* residual_out, int64_t ldo, const mx_tensor* out,
+                              void* stream);
+
+/*
+ * mx_dequantize -- the values of an MX tensor of any format as a plain outer x K
+ * row-major matrix: code * scale, exact in fp32 and rounded to nearest even in the
+ * 16-bit types (bf16 holds every value of every format for scales 2^-110 .. 2^110);
+ * NaN under a scale of 0xFF.
+ *
+ *   out    device, dtype (any mx_dtype), 16-byte aligned; ld >= K, a multiple of
+ *          16 bytes
+ */
+mx_status mx_dequantize(const mx_tensor* A, void* out, int32_t dtype, int64_t ld, void* stream);
+
+/* One tensor that mx_rope turns: element (token t, head h, i) of x at t *
+ * x_token_stride + h * x_head_stride + i, of y likewise; y may be x (with x's
+ * strides), and overlaps it in no other way.  16-byte aligned, strides
+ * multiples of 8 elements. */
+typedef struct mx_rope_operand {
+  const void* x;
+  void* y;
+  int64_t heads;
+  int64_t x_token_stride, x_head_stride;
+  int64_t y_token_stride, y_head_stride;
+} mx_rope_operand;
+
+/*
+ * mx_rope -- rotary positions: of each head's first `rot` values the pair (a, b)
+ * number i becomes
+ *   factor * (a cos t - b sin t, a sin t + b cos t),  t = 2 pi position freq[i] / 2^64,
+ * and the other values stay as they are.
+ *
+ *   a, b        what is turned, commonly queries and keys; b NULL: a alone.
+ *               dtype MX_DT_BF16 or MX_DT_F16, tokens x heads x d: d a multiple of 8
+ *               up to 1024, rot a multiple of 16 up to min(d, 512)
+ *   freq        device, rot / 2: pair i's turns for each position, in units of 2^-64
+ *               turn.  An angle is exact modulo one turn, at any position.
+ *   factor      finite (1, or the factor that goes with frequencies scaled for
+ *               long contexts)
+ *   positions   device, int32, one per token; or NULL, and
+ *   lens, cu    device, int32, requests and requests + 1 entries, as
+ *               mx_kv_extend gives them and mx_kv_attention takes them: token cu[b] + i
+ *               stands at lens[b] - (cu[b + 1] - cu[b]) + i.  Tokens of no request
+ *               are not written
+ *   neighbours  0: pair i is (i, i + rot / 2); 1: (2 i, 2 i + 1)
+ *   backward    0; 1: t negated -- the transposed map, which takes the outputs'
+ *               gradients to the inputs'
+ * Cosines, sines and products are fp32; outputs are rounded once.
+ */
+mx_status mx_rope(const mx_rope_operand* a, const mx_rope_operand* b, int32_t dtype, int64_t tokens,
+                  int64_t d, const uint64_t* freq, int64_t rot, float factor,
+                  const int32_t* positions, const int32_t* lens, const int32_t* cu,
+                  int64_t requests, int32_t neighbours, int32_t backward, void* stream);
 
 /*
  * The 8-bit paged key/value cache.
