@@ -49,7 +49,8 @@ EXPORTS = ("mx_data_bytes", "mx_scale_bytes", "mx_quantize", "mx_gemm",
            "mx_status_string", "mx_version", "mx_set_tile_width",
            "mx_kv_extend", "mx_kv_truncate", "mx_kv_append",
            "mx_kv_attention_workspace_bytes", "mx_kv_attention",
-           "mx_rmsnorm_quantize", "mx_dequantize", "mx_rope")
+           "mx_rmsnorm_quantize", "mx_dequantize", "mx_rope",
+           "mx_kv_fork", "mx_kv_own", "mx_kv_release")
 
 
 class MXError(RuntimeError):
@@ -194,6 +195,15 @@ def lib() -> ctypes.CDLL:
     L.mx_rope.restype = i32
     L.mx_rope.argtypes = [pr, pr, i32, i64, i64, p, i64, ctypes.c_float, p, p,
                           p, i64, i32, i32, p]
+    L.mx_kv_fork.restype = i32
+    L.mx_kv_fork.argtypes = [p, i64, p, p, p, i64, p, i64, i64, p, i64, i32, p,
+                             p, p]
+    L.mx_kv_own.restype = i32
+    L.mx_kv_own.argtypes = [pc, p, p, i64, p, i64, i64, p, i64, p, p, p, p, p,
+                            p]
+    L.mx_kv_release.restype = i32
+    L.mx_kv_release.argtypes = [p, p, i64, p, i64, i64, p, i64, p, p, i64, i32,
+                                p, p, p]
     _lib = L
     return L
 
@@ -803,6 +813,16 @@ class KVCut:
     counts: torch.Tensor
 
 
+@dataclass
+class KVOwn:
+    """What mx_kv_own gives: the new tokens that are allowed (0 for requests
+    refused), [page from, page to, tokens] of each request's copy (-1: none),
+    and [free pages, requests refused]."""
+    new_tokens: torch.Tensor
+    copies: torch.Tensor
+    counts: torch.Tensor
+
+
 # The cache's calls take a few microseconds on the GPU in a decoding step, less
 # than careful Python around them: shapes and strides are read once, and
 # dtypes looked up in tables.
@@ -919,6 +939,96 @@ def mx_kv_truncate(lens: torch.Tensor, keep: torch.Tensor, table: torch.Tensor,
         p_lens, p_keep, B, p_table, stride, width, p_stack, stack.numel(),
         p_count, page, out.lens.data_ptr(), out.counts.data_ptr(),
         _stream(stream)), "mx_kv_truncate")
+    return out
+
+
+def mx_kv_fork(lens: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
+               keep: torch.Tensor, table: torch.Tensor, refs: torch.Tensor,
+               page: int, out: KVCut | None = None, stream=None) -> KVCut:
+    """Request dst[i] becomes the first keep[i] tokens of request src[i] and
+    holds the same pages (table and refs in place).  refs: int32, one entry per
+    page, its holders beyond the first.  A dst must be empty; the first of several
+    forks that name it is served.  Returns the new lengths and [forks refused]."""
+    B, n = lens.shape[0], src.shape[0]
+    p_lens, p_src = _int32(lens, "lens"), _int32(src, "src")
+    p_dst, p_keep = _int32(dst, "dst", n), _int32(keep, "keep", n)
+    p_refs = _int32(refs, "refs")
+    p_table, stride, width = _table(table, B)
+    if out is None:
+        empty = _allocator(lens)
+        out = KVCut(empty((B,), (1,), _i32), empty((1,), (1,), _i32))
+    else:
+        _int32(out.lens, "out.lens", B)
+        _int32(out.counts, "out.counts", 1)
+    _same_gpu(lens, src, dst, keep, table, refs, out.lens, out.counts)
+    _check(lib().mx_kv_fork(
+        p_lens, B, p_src, p_dst, p_keep, n, p_table, stride, width, p_refs,
+        refs.numel(), page, out.lens.data_ptr(), out.counts.data_ptr(),
+        _stream(stream)), "mx_kv_fork")
+    return out
+
+
+def mx_kv_own(cache: KVCache, lens: torch.Tensor, new_tokens: torch.Tensor,
+              table: torch.Tensor, stack: torch.Tensor, count: torch.Tensor,
+              refs: torch.Tensor, out: KVOwn | None = None,
+              stream=None) -> KVOwn:
+    """Before mx_kv_extend: a request with new tokens whose partly filled last
+    page others hold too gets a copy of it on a page from the stack (cache, table
+    and refs in place), unless it is the last of the holders and all are about to
+    write.  The first that finds no page, and every one behind it, is
+    refused."""
+    c = cache.on_gpu()
+    B = lens.shape[0]
+    p_lens = _int32(lens, "lens")
+    p_new = _int32(new_tokens, "new_tokens", B)
+    p_stack = _int32(stack, "stack")
+    p_count = _int32(count, "count", 1)
+    p_refs = _int32(refs, "refs", c.pages)
+    p_table, stride, width = _table(table, B)
+    if out is None:
+        one, empty = (1,), _allocator(lens)
+        out = KVOwn(empty((B,), one, _i32), empty((B, 3), (3, 1), _i32),
+                    empty((2,), one, _i32))
+    else:
+        _int32(out.new_tokens, "out.new_tokens", B)
+        _int32(out.counts, "out.counts", 2)
+        if out.copies.dtype is not _i32 or not out.copies.is_contiguous() or \
+                out.copies.numel() < 3 * B:
+            raise ValueError("out.copies must hold 3 int32 values a request")
+    _same_gpu(cache.k, lens, new_tokens, table, stack, count, refs,
+              out.new_tokens, out.copies, out.counts)
+    _check(lib().mx_kv_own(
+        ctypes.byref(c), p_lens, p_new, B, p_table, stride, width, p_stack,
+        stack.numel(), p_count, p_refs, out.new_tokens.data_ptr(),
+        out.copies.data_ptr(), out.counts.data_ptr(), _stream(stream)),
+        "mx_kv_own")
+    return out
+
+
+def mx_kv_release(lens: torch.Tensor, keep: torch.Tensor, table: torch.Tensor,
+                  stack: torch.Tensor, count: torch.Tensor, refs: torch.Tensor,
+                  page: int, out: KVCut | None = None, stream=None) -> KVCut:
+    """mx_kv_truncate where pages may be shared (refs in place): a page that
+    others hold stays theirs, one that its last holder lets go goes back on the
+    stack."""
+    B = lens.shape[0]
+    p_lens = _int32(lens, "lens")
+    p_keep = _int32(keep, "keep", B)
+    p_stack = _int32(stack, "stack")
+    p_count = _int32(count, "count", 1)
+    p_refs = _int32(refs, "refs")
+    p_table, stride, width = _table(table, B)
+    if out is None:
+        empty = _allocator(lens)
+        out = KVCut(empty((B,), (1,), _i32), empty((2,), (1,), _i32))
+    else:
+        _int32(out.lens, "out.lens", B)
+        _int32(out.counts, "out.counts", 2)
+    _same_gpu(lens, keep, table, stack, count, refs, out.lens, out.counts)
+    _check(lib().mx_kv_release(
+        p_lens, p_keep, B, p_table, stride, width, p_stack, stack.numel(),
+        p_count, p_refs, refs.numel(), page, out.lens.data_ptr(),
+        out.counts.data_ptr(), _stream(stream)), "mx_kv_release")
     return out
 
 

@@ -382,6 +382,94 @@ mx_status mx_kv_truncate(const int32_t* lens, const int32_t* keep, int64_t reque
                                            counts_out, static_cast<cudaStream_t>(stream)));
 }
 
+mx_status mx_kv_release(const int32_t* lens, const int32_t* keep, int64_t requests, int32_t* table,
+                        int64_t table_stride, int64_t table_width, int32_t* stack,
+                        int64_t stack_size, const int32_t* count, int32_t* refs, int64_t pages,
+                        int32_t page, int32_t* lens_out, int32_t* counts_out, void* stream) {
+  mx_status s = check_pages_call(requests, table_stride, table_width, stack_size, page);
+  if (s != MX_OK) return s;
+  if (pages < 1 || pages > kMaxDim / page) return MX_ERR_SHAPE;
+  if (requests > 0 && (!lens || !keep || !table || !lens_out)) return MX_ERR_INVALID_ARG;
+  if ((stack_size > 0 && !stack) || !count || !counts_out || !refs) return MX_ERR_INVALID_ARG;
+  if ((s = check_device()) != MX_OK) return s;
+  mxk::KvShare q{};
+  q.lens = lens;
+  q.change = keep;
+  q.requests = requests;
+  q.table = table;
+  q.table_stride = table_stride;
+  q.width = table_width;
+  q.stack = stack;
+  q.stack_size = stack_size;
+  q.count = count;
+  q.refs = refs;
+  q.pages = pages;
+  q.page = page;
+  q.lens_out = lens_out;
+  q.counts_out = counts_out;
+  return from_cuda(mxk::launch_kv_release(q, static_cast<cudaStream_t>(stream)));
+}
+
+mx_status mx_kv_fork(const int32_t* lens, int64_t requests, const int32_t* src, const int32_t* dst,
+                     const int32_t* keep, int64_t forks, int32_t* table, int64_t table_stride,
+                     int64_t table_width, int32_t* refs, int64_t pages, int32_t page,
+                     int32_t* lens_out, int32_t* counts_out, void* stream) {
+  mx_status s = check_pages_call(requests, table_stride, table_width, 0, page);
+  if (s != MX_OK) return s;
+  if (pages < 1 || pages > kMaxDim / page || forks < 0 || forks > 16384) return MX_ERR_SHAPE;
+  if (requests > 0 && (!lens || !table || !lens_out)) return MX_ERR_INVALID_ARG;
+  if ((forks > 0 && (!src || !dst || !keep)) || !refs || !counts_out) return MX_ERR_INVALID_ARG;
+  if ((s = check_device()) != MX_OK) return s;
+  mxk::KvShare q{};
+  q.lens = lens;
+  q.change = keep;
+  q.requests = requests;
+  q.src = src;
+  q.dst = dst;
+  q.forks = forks;
+  q.table = table;
+  q.table_stride = table_stride;
+  q.width = table_width;
+  q.refs = refs;
+  q.pages = pages;
+  q.page = page;
+  q.lens_out = lens_out;
+  q.counts_out = counts_out;
+  return from_cuda(mxk::launch_kv_fork(q, static_cast<cudaStream_t>(stream)));
+}
+
+mx_status mx_kv_own(const mx_kv_cache* cache, const int32_t* lens, const int32_t* new_tokens,
+                    int64_t requests, int32_t* table, int64_t table_stride, int64_t table_width,
+                    const int32_t* stack, int64_t stack_size, const int32_t* count, int32_t* refs,
+                    int32_t* new_out, int32_t* copies, int32_t* counts_out, void* stream) {
+  mxk::KvCache c;
+  mx_status s = check_cache(cache, &c);
+  if (s != MX_OK) return s;
+  s = check_pages_call(requests, table_stride, table_width, stack_size, cache->page);
+  if (s != MX_OK) return s;
+  if (requests > 0 && (!lens || !new_tokens || !table || !new_out || !copies))
+    return MX_ERR_INVALID_ARG;
+  if ((stack_size > 0 && !stack) || !count || !refs || !counts_out) return MX_ERR_INVALID_ARG;
+  if ((s = check_device()) != MX_OK) return s;
+  mxk::KvShare q{};
+  q.lens = lens;
+  q.change = new_tokens;
+  q.requests = requests;
+  q.table = table;
+  q.table_stride = table_stride;
+  q.width = table_width;
+  q.stack = const_cast<int32_t*>(stack);     // own only reads it
+  q.stack_size = stack_size;
+  q.count = count;
+  q.refs = refs;
+  q.pages = c.pages;
+  q.page = c.page;
+  q.lens_out = new_out;
+  q.copies = copies;
+  q.counts_out = counts_out;
+  return from_cuda(mxk::launch_kv_own(c, q, static_cast<cudaStream_t>(stream)));
+}
+
 mx_status mx_kv_append(const mx_kv_cache* cache, const void* K, const void* V, int32_t dtype,
                        int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
                        int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots,

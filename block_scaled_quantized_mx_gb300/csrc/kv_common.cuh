@@ -40,6 +40,31 @@ cudaError_t launch_kv_truncate(const int* lens, const int* keep, int64_t request
                                int64_t stack_size, const int* count, int page, int* lens_out,
                                int* counts_out, cudaStream_t st);
 
+// Pages that several requests hold (kvshare.cu): refs counts a page's holders
+// beyond the first.
+struct KvShare {
+  const int* lens;
+  const int* change;          // release: tokens kept; fork: tokens shared; own: new tokens
+  int64_t requests;
+  const int* src;             // fork
+  const int* dst;
+  int64_t forks;
+  int* table;
+  int64_t table_stride, width;
+  int* stack;
+  int64_t stack_size;
+  const int* count;
+  int* refs;
+  int64_t pages;
+  int page;
+  int* lens_out;              // own: the new tokens that are allowed
+  int* copies;                // own: requests x (from, to, tokens)
+  int* counts_out;
+};
+cudaError_t launch_kv_release(const KvShare& q, cudaStream_t st);
+cudaError_t launch_kv_fork(const KvShare& q, cudaStream_t st);
+cudaError_t launch_kv_own(const KvCache& c, const KvShare& q, cudaStream_t st);
+
 // K and V: tokens x heads x d of dtype (DT_BF16 / DT_F16), strides in
 // elements; slots: one per token.
 cudaError_t launch_kv_append(const KvCache& c, const void* K, const void* V, int dtype,

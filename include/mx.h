@@ -580,6 +580,74 @@ mx_status mx_kv_truncate(const int32_t* lens, const int32_t* keep, int64_t reque
                          int32_t* lens_out, int32_t* counts_out, void* stream);
 
 /*
+ * Shared pages.  Several requests may hold a page -- samples of one prompt, a
+ * prompt's common beginning.  refs (device, int32, one entry per page of the cache)
+ * counts each page's holders beyond the first: 0 for free pages and for those that one
+ * request holds, so a cache begins with zeros, and mx_kv_extend, which hands out
+ * free pages, needs none of it.  Where pages may be shared
+ *   - mx_kv_fork makes a request hold another's pages,
+ *   - mx_kv_own goes before mx_kv_extend and mx_kv_append: it gives the requests that
+ *     are about to write a page that others hold too a copy of it,
+ *   - mx_kv_release takes mx_kv_truncate's place.
+ * mx_kv_attention needs nothing; mx_kv_attention_shared reads common pages once.
+ * All work on the GPU alone, give the same results from run to run, and ask
+ * requests <= 16384.
+ *
+ * mx_kv_fork -- request dst[i] becomes the first min(max(keep[i], 0),
+ * lens[src[i]]) tokens of request src[i], whose pages it holds too, a partly filled
+ * last one among them; an entry that is negative (a page given back in front of a
+ * window) is copied as it is.  A fork whose src or dst is no request, or the same one,
+ * or whose dst holds tokens already (lens[dst[i]] != 0) is refused, and so are all but the
+ * first of those left that name one dst.  Lengths are those before the call: a dst that is
+ * also a src is an empty src.
+ *
+ *   lens        device, int32, requests entries;  table as for mx_kv_extend
+ *   src, dst, keep  device, int32, forks entries;  forks <= 16384
+ *   refs        device, int32, `pages` entries, the cache's number of pages
+ *   lens_out    device, int32, requests entries: the new lengths; may be lens
+ *   counts_out  device, int32, 1 entry: forks refused
+ */
+mx_status mx_kv_fork(const int32_t* lens, int64_t requests, const int32_t* src, const int32_t* dst,
+                     const int32_t* keep, int64_t forks, int32_t* table, int64_t table_stride,
+                     int64_t table_width, int32_t* refs, int64_t pages, int32_t page,
+                     int32_t* lens_out, int32_t* counts_out, void* stream);
+
+/*
+ * mx_kv_own -- copy before write.  A request with new_tokens[b] > 0 whose last page
+ * is partly filled and held by others too gets a page from the stack -- the i-th that is
+ * handed out, in request order, is stack[count - 1 - i] -- with a copy of its tokens there and
+ * of its scales, and holds that one instead.  Where all holders of a page are such
+ * requests, the last of them keeps the page.  The first of them that finds no free page,
+ * and every one behind it, is refused: it keeps what it holds, and must get no tokens.
+ *
+ *   cache       its planes are written;  lens, new_tokens device, int32, requests entries
+ *   table, stack, count  as for mx_kv_extend;  refs one entry per page of the cache
+ *   new_out     device, int32, requests entries: new_tokens, 0 for the refused (what to
+ *               give mx_kv_extend); may be new_tokens
+ *   copies      device, int32, requests rows of 3: the page copied from, the page copied to
+ *               and the tokens copied, or -1 each
+ *   counts_out  device, int32, 2 entries: free pages left, requests refused; may be
+ *               count
+ */
+mx_status mx_kv_own(const mx_kv_cache* cache, const int32_t* lens, const int32_t* new_tokens,
+                    int64_t requests, int32_t* table, int64_t table_stride, int64_t table_width,
+                    const int32_t* stack, int64_t stack_size, const int32_t* count, int32_t* refs,
+                    int32_t* new_out, int32_t* copies, int32_t* counts_out, void* stream);
+
+/*
+ * mx_kv_release -- mx_kv_truncate where pages may be shared: a page that others hold
+ * too stays theirs and loses a holder; one that all its holders let go is freed, by
+ * the last of the requests that do so.  Of the n pages freed (in the order of the requests
+ * that free them, then table order) the i-th is written to stack[count + n - 1 - i].
+ * Page ids outside the cache are dropped.
+ *   refs        device, int32, `pages` entries;  the rest as for mx_kv_truncate
+ */
+mx_status mx_kv_release(const int32_t* lens, const int32_t* keep, int64_t requests, int32_t* table,
+                        int64_t table_stride, int64_t table_width, int32_t* stack,
+                        int64_t stack_size, const int32_t* count, int32_t* refs, int64_t pages,
+                        int32_t page, int32_t* lens_out, int32_t* counts_out, void* stream);
+
+/*
  * mx_kv_append -- quantize new keys and values into the cache.
  *
  * Let e be the OCP MX scale code (the rule of mx_quantize, over a block of all
