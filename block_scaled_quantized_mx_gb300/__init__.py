@@ -50,7 +50,8 @@ EXPORTS = ("mx_data_bytes", "mx_scale_bytes", "mx_quantize", "mx_gemm",
            "mx_kv_extend", "mx_kv_truncate", "mx_kv_append",
            "mx_kv_attention_workspace_bytes", "mx_kv_attention",
            "mx_rmsnorm_quantize", "mx_dequantize", "mx_rope",
-           "mx_kv_fork", "mx_kv_own", "mx_kv_release")
+           "mx_kv_fork", "mx_kv_own", "mx_kv_release",
+           "mx_kv_attention_shared_workspace_bytes", "mx_kv_attention_shared")
 
 
 class MXError(RuntimeError):
@@ -204,6 +205,13 @@ def lib() -> ctypes.CDLL:
     L.mx_kv_release.restype = i32
     L.mx_kv_release.argtypes = [p, p, i64, p, i64, i64, p, i64, p, p, i64, i32,
                                 p, p, p]
+    L.mx_kv_attention_shared_workspace_bytes.restype = sz
+    L.mx_kv_attention_shared_workspace_bytes.argtypes = [i64] * 7
+    L.mx_kv_attention_shared.restype = i32
+    L.mx_kv_attention_shared.argtypes = [p, i32, i64, i64, i64, i64, pc, p, i64,
+                                         i64, p, p, i64, i64, p, p, i64, p, i32,
+                                         i64, i64, i32, ctypes.c_float, p, sz,
+                                         p]
     _lib = L
     return L
 
@@ -1123,6 +1131,67 @@ def mx_kv_attention(Q: torch.Tensor, cache: KVCache, table: torch.Tensor,
         1 if causal else 0, window, d ** -0.5 if scale is None else scale,
         None if workspace is None else workspace.data_ptr(),
         _nbytes(workspace), _stream(stream)), "mx_kv_attention")
+    return out
+
+
+def kv_attention_shared_workspace_bytes(tokens: int, q_heads: int, heads: int,
+                                        d: int, max_q: int, requests: int,
+                                        groups: int) -> int:
+    """Bytes of workspace with which mx_kv_attention_shared reads a group's
+    common keys once; they grow with each argument."""
+    return int(lib().mx_kv_attention_shared_workspace_bytes(
+        tokens, q_heads, heads, d, max_q, requests, groups))
+
+
+def mx_kv_attention_shared(Q: torch.Tensor, cache: KVCache, table: torch.Tensor,
+                           lens: torch.Tensor, cu: torch.Tensor, max_q: int,
+                           groups: torch.Tensor, shared: torch.Tensor,
+                           causal: bool = True, scale: float | None = None,
+                           out_dtype=None, out: torch.Tensor | None = None,
+                           stream=None,
+                           workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """mx_kv_attention for requests that share their first tokens: group g is
+    the requests groups[g] .. groups[g + 1] (int32, one entry more than there are
+    groups), whose rows of the table begin with the same pages: up to shared[g] (or more)
+    tokens, read once for all.  With a device `workspace` (uint8,
+    kv_attention_shared_workspace_bytes() long); without one each request reads
+    its own."""
+    if workspace is not None and not (workspace.is_cuda and
+                                      workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    c = cache.on_gpu()
+    dt, shape, qt, qh = _kv_tensor(Q, "Q")
+    T, Hq, d = shape
+    if d != c.d or Hq % c.heads:
+        raise ValueError("Q must have the cache's d and a multiple of its heads")
+    B, n = lens.shape[0], groups.shape[0] - 1
+    if n < 0:
+        raise ValueError("groups must hold an entry more than there are groups")
+    p_lens = _int32(lens, "lens")
+    p_cu = _int32(cu, "cu", B + 1)
+    p_groups, p_shared = _int32(groups, "groups"), _int32(shared, "shared", n)
+    p_table, stride, width = _table(table, B)
+    if out is None:
+        ot, oh = Hq * d, d
+        out = _allocator(Q)((T, Hq, d), (ot, oh, 1), out_dtype or Q.dtype)
+    elif (out.shape != shape or not out.is_cuda or out.stride(2) != 1
+          or (out_dtype is not None and out.dtype != out_dtype)):
+        raise ValueError("out must be a CUDA tensor of Q's shape and of type "
+                         "out_dtype, with a unit inner stride")
+    else:
+        ot = out.stride(0) if T > 1 else 0
+        oh = out.stride(1) if Hq > 1 else 0
+    odt = _KV_OUT_DTYPES.get(out.dtype)
+    if odt is None:
+        raise ValueError("out_dtype must be float32, bfloat16 or float16, not "
+                         f"{out.dtype}")
+    _same_gpu(Q, cache.k, table, lens, cu, groups, shared, out, workspace)
+    _check(lib().mx_kv_attention_shared(
+        Q.data_ptr(), dt, T, Hq, qt, qh, ctypes.byref(c), p_table, stride,
+        width, p_lens, p_cu, B, max_q, p_groups, p_shared, n, out.data_ptr(),
+        odt, ot, oh, 1 if causal else 0, d ** -0.5 if scale is None else scale,
+        None if workspace is None else workspace.data_ptr(),
+        _nbytes(workspace), _stream(stream)), "mx_kv_attention_shared")
     return out
 
 

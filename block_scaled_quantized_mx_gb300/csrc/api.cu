@@ -498,15 +498,19 @@ size_t mx_kv_attention_workspace_bytes(int64_t q_heads, int64_t heads, int64_t d
   return mxk::kv_attention_workspace_bytes(q_heads, heads, d, max_q);
 }
 
-mx_status mx_kv_attention(const void* Q, int32_t dtype, int64_t tokens, int64_t q_heads,
-                          int64_t q_token_stride, int64_t q_head_stride,
-                          const mx_kv_cache* cache, const int32_t* table, int64_t table_stride,
-                          int64_t table_width, const int32_t* lens, const int32_t* cu,
-                          int64_t requests, int64_t max_q, void* O, int32_t o_dtype,
-                          int64_t o_token_stride, int64_t o_head_stride, int32_t causal,
-                          int64_t window, float scale, void* workspace, size_t workspace_bytes,
-                          void* stream) {
-  mxk::KvAttn a{};
+namespace {
+
+// The arguments of an attention call over the cache, checked, as the kernels take
+// them; *nothing: there is no row to compute.
+mx_status attention_call(const void* Q, int32_t dtype, int64_t tokens, int64_t q_heads,
+                         int64_t q_token_stride, int64_t q_head_stride, const mx_kv_cache* cache,
+                         const int32_t* table, int64_t table_stride, int64_t table_width,
+                         const int32_t* lens, const int32_t* cu, int64_t requests, int64_t max_q,
+                         void* O, int32_t o_dtype, int64_t o_token_stride, int64_t o_head_stride,
+                         int32_t causal, int64_t window, float scale, void* workspace,
+                         size_t workspace_bytes, mxk::KvAttn* out, bool* nothing) {
+  mxk::KvAttn& a = *out;
+  *nothing = false;
   mx_status s = check_cache(cache, &a.cache);
   if (s != MX_OK) return s;
   if (dtype != MX_DT_F16 && dtype != MX_DT_BF16) return MX_ERR_INVALID_ARG;
@@ -522,7 +526,10 @@ mx_status mx_kv_attention(const void* Q, int32_t dtype, int64_t tokens, int64_t 
   if (table_width < 1 || table_stride < table_width || table_width > kMaxDim ||
       table_stride > kMaxDim)
     return MX_ERR_SHAPE;
-  if (tokens == 0 || requests == 0) return MX_OK;
+  if (tokens == 0 || requests == 0) {
+    *nothing = true;
+    return MX_OK;
+  }
   if (!Q || !O || !table || !lens || !cu) return MX_ERR_INVALID_ARG;
   if ((s = check_strides(tokens, q_heads, q_token_stride, q_head_stride, d)) != MX_OK) return s;
   if ((s = check_strides(tokens, q_heads, o_token_stride, o_head_stride, d)) != MX_OK) return s;
@@ -550,7 +557,61 @@ mx_status mx_kv_attention(const void* Q, int32_t dtype, int64_t tokens, int64_t 
   a.scale = scale;
   a.ws = workspace;
   a.ws_bytes = workspace_bytes;
+  return MX_OK;
+}
+
+}  // namespace
+
+mx_status mx_kv_attention(const void* Q, int32_t dtype, int64_t tokens, int64_t q_heads,
+                          int64_t q_token_stride, int64_t q_head_stride,
+                          const mx_kv_cache* cache, const int32_t* table, int64_t table_stride,
+                          int64_t table_width, const int32_t* lens, const int32_t* cu,
+                          int64_t requests, int64_t max_q, void* O, int32_t o_dtype,
+                          int64_t o_token_stride, int64_t o_head_stride, int32_t causal,
+                          int64_t window, float scale, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  mxk::KvAttn a{};
+  bool nothing;
+  const mx_status s = attention_call(Q, dtype, tokens, q_heads, q_token_stride, q_head_stride, cache, table,
+                                     table_stride, table_width, lens, cu, requests, max_q, O, o_dtype,
+                                     o_token_stride, o_head_stride, causal, window, scale, workspace,
+                                     workspace_bytes, &a, &nothing);
+  if (s != MX_OK || nothing) return s;
   return from_cuda(mxk::launch_kv_attention(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t mx_kv_attention_shared_workspace_bytes(int64_t tokens, int64_t q_heads, int64_t heads,
+                                              int64_t d, int64_t max_q, int64_t requests,
+                                              int64_t groups) {
+  if (heads < 1 || heads > 65535 || q_heads < 1 || q_heads % heads || (d != 64 && d != 128) ||
+      max_q < 1 || max_q > kMaxDim || tokens < 1 || tokens > kMaxDim / q_heads || requests < 1 ||
+      requests > 16384 || groups < 1 || groups > 16384)
+    return 0;
+  if (check_device() != MX_OK) return 0;
+  return mxk::kv_attention_shared_workspace_bytes(tokens, q_heads, heads, d, max_q, requests, groups);
+}
+
+mx_status mx_kv_attention_shared(const void* Q, int32_t dtype, int64_t tokens, int64_t q_heads,
+                                 int64_t q_token_stride, int64_t q_head_stride,
+                                 const mx_kv_cache* cache, const int32_t* table,
+                                 int64_t table_stride, int64_t table_width, const int32_t* lens,
+                                 const int32_t* cu, int64_t requests, int64_t max_q,
+                                 const int32_t* groups, const int32_t* shared, int64_t n_groups,
+                                 void* O, int32_t o_dtype, int64_t o_token_stride,
+                                 int64_t o_head_stride, int32_t causal, float scale,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  if (n_groups < 0 || n_groups > 16384 || requests > 16384) return MX_ERR_SHAPE;
+  if (q_heads > 0 && tokens > kMaxDim / q_heads) return MX_ERR_SHAPE;
+  if (tokens > 0 && requests > 0 && n_groups > 0 && (!groups || !shared)) return MX_ERR_INVALID_ARG;
+  mxk::KvAttn a{};
+  bool nothing;
+  const mx_status s = attention_call(Q, dtype, tokens, q_heads, q_token_stride, q_head_stride, cache, table,
+                                     table_stride, table_width, lens, cu, requests, max_q, O, o_dtype,
+                                     o_token_stride, o_head_stride, causal, 0, scale, workspace,
+                                     workspace_bytes, &a, &nothing);
+  if (s != MX_OK || nothing) return s;
+  return from_cuda(mxk::launch_kv_attention_shared(a, mxk::KvGroups{groups, shared, n_groups},
+                                                   static_cast<cudaStream_t>(stream)));
 }
 
 namespace {

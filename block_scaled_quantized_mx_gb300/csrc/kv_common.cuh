@@ -98,11 +98,44 @@ size_t kv_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t d
 cudaError_t launch_kv_attention(const KvAttn& a, cudaStream_t st);
 unsigned fetch_and_clear_status_kv(cudaError_t* err);
 
+// Shared prefixes (kvshared.cu).  The keys that a group of requests has in common are
+// attended to by all of the group's rows in one pass, which leaves each row's state -- O
+// before the division, the reference m and the sum l -- in memory, a row for each (token,
+// query head); a second pass, over each request's own keys, takes it up.  Which of the
+// two a launch is:
+enum KvPass : int { KV_OWN = 0, KV_PREFIX = 1 };
+struct KvState {
+  float* o;                    // rows x d
+  float2* ml;                  // rows: m, l
+  int pass;
+};
+// What a pass needs besides (or instead of) the call's arguments: KvAttn's cu, lens,
+// requests and max_q are the pass's.
+struct KvPassArgs {
+  const int* start;            // each request's first key; null: 0
+  const int* row_of;           // each request's row of the table; null: its own
+  int cu_step;                 // a request's rows: cu[b * cu_step] .. cu[b * cu_step + 1]
+  KvState state;
+};
+// One of the passes: launched as a programmatic dependent, with the workspace's bytes below.
+size_t kv_pass_workspace_bytes(int64_t group, int64_t d, int64_t max_q);
+cudaError_t launch_kv_pass(const KvAttn& a, const KvPassArgs& pass, cudaStream_t st);
+
+// The call: requests groups[g] .. groups[g + 1] - 1 share their first shared[g] tokens.
+struct KvGroups {
+  const int* groups;
+  const int* shared;
+  int64_t n;
+};
+size_t kv_attention_shared_workspace_bytes(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d,
+                                           int64_t max_q, int64_t requests, int64_t groups);
+cudaError_t launch_kv_attention_shared(const KvAttn& a, const KvGroups& g, cudaStream_t st);
+
 // Its kernel for many rows per request (kvprompt.cu), up to
 // kv_prompt_max_requests() requests.
 int64_t kv_prompt_max_requests();
 size_t kv_prompt_workspace_bytes(int64_t d, int sms);
-cudaError_t launch_kv_prompt(const KvAttn& a, int sms, cudaStream_t st);
+cudaError_t launch_kv_prompt(const KvAttn& a, int sms, const KvPassArgs* pass, cudaStream_t st);
 unsigned fetch_and_clear_status_kvp(cudaError_t* err);
 
 }  // namespace mxk

@@ -2,6 +2,7 @@
 // 8-bit paged cache: what a request's rows may see, codes to f16, factors.
 #pragma once
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "gemm_common.cuh"
@@ -27,6 +28,10 @@ struct KvView {
   int capacity;                // tokens a table row holds
   int causal;
   int window;                  // 0: none
+  // Of the passes over shared prefixes (the kernels' SH variants) alone:
+  const int* start;            // each request's first key; null: 0
+  const int* row_of;           // each request's row of the table; null: its own
+  int cu_step;                 // a request's rows: cu[b * cu_step] .. cu[b * cu_step + 1]
 };
 
 inline KvView kv_view(const KvAttn& q) {
@@ -57,15 +62,28 @@ struct KvReq {
   int n;
   int len;
 };
+struct KvShReq : KvReq {
+  int start;                   // the first key
+};
 
-__device__ __forceinline__ KvReq kv_request(const KvView& v, int b) {
-  KvReq r;
-  long long s = v.cu[b], e = v.cu[b + 1];
+template <bool SH>
+__device__ __forceinline__ auto kv_request(const KvView& v, int b) {
+  std::conditional_t<SH, KvShReq, KvReq> r;
+  long long s, e;
+  if constexpr (SH) {
+    // (another kernel of the same call may have written these: around L1)
+    s = __ldcg(v.cu + static_cast<long long>(b) * v.cu_step);
+    e = __ldcg(v.cu + static_cast<long long>(b) * v.cu_step + 1);
+    r.start = v.start ? __ldcg(v.start + b) : 0;
+  } else {
+    s = v.cu[b];
+    e = v.cu[b + 1];
+  }
   s = s < 0 ? 0 : (s > v.tokens ? v.tokens : s);
   e = e < s ? s : (e > v.tokens ? v.tokens : e);
   r.q0 = s;
   r.n = static_cast<int>(e - s);
-  const int len = v.lens[b];
+  const int len = SH ? __ldcg(v.lens + b) : v.lens[b];
   r.len = len < 0 ? 0 : (len > v.capacity ? v.capacity : len);
   return r;
 }
@@ -73,6 +91,9 @@ __device__ __forceinline__ KvReq kv_request(const KvView& v, int b) {
 // Token i of a request stands at position len - n + i and sees keys
 // [first, end): all before its own and itself (causal), or all; with a
 // window only the last `window` up to its own position.
+__device__ __forceinline__ int kv_first_key(const KvView&, const KvShReq& r, int) {
+  return r.start;
+}
 __device__ __forceinline__ int kv_first_key(const KvView& v, const KvReq& r, int i) {
   if (v.window <= 0) return 0;
   const long long p = static_cast<long long>(r.len) - r.n + i + 1 - v.window;
@@ -130,6 +151,16 @@ constexpr float KV_NO_MAX = -3.402823466e38f;
 // whose every score was -infinity.
 __device__ __forceinline__ float kv_inverse(float sum, bool saw_keys) {
   return sum != 0.0f ? 1.0f / sum : saw_keys ? __uint_as_float(0x7FC00000u) : 0.0f;
+}
+
+// The two states' weights, for the sum of their O's divided by the sum of their l's.
+__device__ __forceinline__ void kv_join_states(float2 a, float2 b, float& wa, float& wb) {
+  const float t = fmaxf(a.x, b.x);
+  wa = a.x == t ? 1.0f : ex2_approx(a.x - t);
+  wb = b.x == t ? 1.0f : ex2_approx(b.x - t);
+  const float inv = kv_inverse(fmaf(wa, a.y, wb * b.y), t != -INFINITY);
+  wa *= inv;
+  wb *= inv;
 }
 
 // The exponents of P.  A row's weights are 2^(x_j - m), and V's pages have scales

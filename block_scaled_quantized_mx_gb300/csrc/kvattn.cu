@@ -88,8 +88,10 @@ constexpr int ka_ctas_per_sm() {
 }
 
 // What the producer says about a segment: one CTA's part of a unit.
+template <int ROWS, bool SH>
+struct KaSeg;
 template <int ROWS>
-struct KaSeg {
+struct KaSeg<ROWS, false> {
   int tile, count;             // first key tile, number (0: no more segments)
   int len;                     // the request's length
   int live;                    // rows of the unit that exist
@@ -101,19 +103,30 @@ struct KaSeg {
   int lo[ROWS], hi[ROWS];      // keys [lo, hi) that the row sees
   long long out[ROWS];         // the row's first element of O
 };
+template <int ROWS>
+struct KaSeg<ROWS, true> : KaSeg<ROWS, false> {
+  int row[ROWS];               // the row's state
+  int has_state;               // a prefix went before
+};
 
 // A unit that begins in this CTA's stretch and goes on in others': what the
 // joining kernel needs (live 0: there is none).
+template <int ROWS, bool SH>
+struct KaJoin;
 template <int ROWS>
-struct KaJoin {
+struct KaJoin<ROWS, false> {
   int live;                    // rows
   int parts;                   // CTAs that share it: this one and the next ones
   int first_slot;              // this CTA's slot; the others use their first
-  int pad;
+  int has_state;
   long long out[ROWS];         // the rows' first elements of O
 };
+template <int ROWS>
+struct KaJoin<ROWS, true> : KaJoin<ROWS, false> {
+  int row[ROWS];               // the rows' states
+};
 
-template <int D, int NR>
+template <int D, int NR, bool SH>
 struct KaSmem {
   static constexpr int ROWS = 8 * NR;
   static constexpr int TK = ka_tk<D>();
@@ -128,7 +141,7 @@ struct KaSmem {
   static constexpr int Q_OFF = RED_OFF + RED_BYTES;
   static constexpr int Q_SLOT = NR * (D / 32) * 512;
   static constexpr int SEG_OFF = Q_OFF + 2 * Q_SLOT;
-  static constexpr int SEG_BYTES = (sizeof(KaSeg<ROWS>) + 15) / 16 * 16;
+  static constexpr int SEG_BYTES = (sizeof(KaSeg<ROWS, SH>) + 15) / 16 * 16;
   static constexpr int ML_OFF = SEG_OFF + 2 * SEG_BYTES;     // (m, v): [warp][row]; l: [warp][row]
   static constexpr int PG_OFF = ML_OFF + 3 * KA_WARPS * ROWS * 4;
   static constexpr int PG_STAGE = MAX_PAGES * 8;             // per page: K scale, V exponent
@@ -149,6 +162,7 @@ struct KaArgs {
   float scale_log2e;
   float* ws;                   // two slots per CTA: [rows][D] of O, then m[rows], l[rows]
   uint8_t* joins;              // one KaJoin per CTA, behind the slots
+  KvState state;               // SH
 };
 
 __device__ __forceinline__ void ka_timeout(volatile int* abort, unsigned site) {
@@ -172,18 +186,19 @@ __device__ __forceinline__ long long ka_div(long long a, long long b) {
 }
 
 // One request's share of the work list.
+template <bool SH>
 struct KaReq {
-  KvReq r;
+  std::conditional_t<SH, KvShReq, KvReq> r;
   int tiles;                   // key tiles of each of its units, and one for its overhead
   int tile0;                   // its first tile
   int row_tiles;
   long long units;             // row tiles x cache heads; 0: nothing for this kernel
 };
 
-template <int ROWS, int TK>
-__device__ __forceinline__ KaReq ka_request(const KaArgs& a, int b) {
-  KaReq q;
-  q.r = kv_request(a.v, b);
+template <int ROWS, int TK, bool SH>
+__device__ __forceinline__ KaReq<SH> ka_request(const KaArgs& a, int b) {
+  KaReq<SH> q;
+  q.r = kv_request<SH>(a.v, b);
   const long long rows = static_cast<long long>(q.r.n) * a.v.group;
   const int first = kv_first_key(a.v, q.r, 0);
   q.tile0 = first / TK;
@@ -197,12 +212,12 @@ __device__ __forceinline__ KaReq ka_request(const KaArgs& a, int b) {
 // its tiles behind one entry more, for the time it takes to begin and end a
 // unit (about that of a tile): without it a stretch of many short units took
 // 68 us where the median took 43 (48 requests of 0 to 6000 keys, window 2048).
-template <int ROWS, int TK>
+template <int ROWS, int TK, bool SH>
 struct KaWalk {
   long long w, w1;             // next entry of the list, end of the stretch
   long long base;              // first entry of request b
   int b;
-  KaReq q;
+  KaReq<SH> q;
   // the current segment
   int head, row_tile, tile, count;
   bool begins, ends;
@@ -213,7 +228,7 @@ struct KaWalk {
       while (w >= base + q.units * q.tiles) {
         base += q.units * q.tiles;
         if (++b >= a.v.requests) return false;
-        q = ka_request<ROWS, TK>(a, b);
+        q = ka_request<ROWS, TK, SH>(a, b);
       }
       const long long u = ka_div(w - base, q.tiles);
       int t = static_cast<int>((w - base) - u * q.tiles);   // 0: the extra entry
@@ -263,13 +278,14 @@ __device__ __forceinline__ bool ka_all(bool v) {
   return r != 0;
 }
 
-template <int FMT, int D, int NR>
+template <int FMT, int D, int NR, bool SH>
 __global__ void __launch_bounds__(KA_THREADS, ka_ctas_per_sm<NR>())
 kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const KaArgs a) {
-  using L = KaSmem<D, NR>;
+  using L = KaSmem<D, NR, SH>;
   constexpr int ROWS = L::ROWS, TK = L::TK, KW = TK / KA_WARPS, KS = KW / 16;
-  using Seg = KaSeg<ROWS>;
+  using Seg = KaSeg<ROWS, SH>;
+  using Join = KaJoin<ROWS, SH>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -279,9 +295,9 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
   volatile int* abort = reinterpret_cast<volatile int*>(gbase + L::MISC_OFF);
   long long* sm_base = reinterpret_cast<long long*>(gbase + L::MISC_OFF + 16);
   long long* sm_scan = reinterpret_cast<long long*>(gbase + L::MISC_OFF + 24);   // [5]
-  KaReq* sm_req = reinterpret_cast<KaReq*>(gbase + L::MISC_OFF + 64);
-  int* sm_b = reinterpret_cast<int*>(gbase + L::MISC_OFF + 64 + sizeof(KaReq));
-  static_assert(sizeof(KaReq) <= 56, "fits");
+  KaReq<SH>* sm_req = reinterpret_cast<KaReq<SH>*>(gbase + L::MISC_OFF + 64);
+  int* sm_b = reinterpret_cast<int*>(gbase + L::MISC_OFF + 64 + sizeof(KaReq<SH>));
+  static_assert(sizeof(KaReq<SH>) <= 56, "fits");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
@@ -298,13 +314,18 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
+  // The prefix pass reads what the plan wrote; the other one's launch follows all of
+  // that, and it waits for the prefixes' states where it needs them (and before it
+  // ends, for what comes after it).
+  if constexpr (SH)
+    if (a.state.pass == KV_PREFIX) asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- the list: its length, and where this CTA's stretch begins
   const int per = (a.v.requests + KA_THREADS - 1) / KA_THREADS;
   const int rb0 = min(a.v.requests, tid * per), rb1 = min(a.v.requests, rb0 + per);
   long long mine = 0;
-  KaReq last{};
+  KaReq<SH> last{};
   for (int b = rb0; b < rb1; ++b) {
-    last = ka_request<ROWS, TK>(a, b);
+    last = ka_request<ROWS, TK, SH>(a, b);
     mine += last.units * last.tiles;
   }
   long long incl = mine;
@@ -322,10 +343,11 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
   }
   const long long ctas = min(static_cast<long long>(gridDim.x), total);
   const long long cta = blockIdx.x;
-  KaJoin<ROWS>* join = reinterpret_cast<KaJoin<ROWS>*>(a.joins) + cta;
+  Join* join = reinterpret_cast<Join*>(a.joins) + cta;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (cta >= ctas) {                         // the whole CTA: nothing was started
     if (a.ws != nullptr && tid == 0) join->live = 0;
+    if constexpr (SH) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
   // the first `longer` CTAs take one entry more than the others
@@ -335,7 +357,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
   if (w0 >= before && w0 < before + mine) {
     long long p = before;
     for (int b = rb0; b < rb1; ++b) {
-      const KaReq q = per == 1 ? last : ka_request<ROWS, TK>(a, b);
+      const KaReq<SH> q = per == 1 ? last : ka_request<ROWS, TK, SH>(a, b);
       const long long n = q.units * q.tiles;
       if (w0 < p + n) {
         *sm_b = b;
@@ -350,7 +372,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
 
   if (warp == KA_WARPS) {
     // ------------------------------------------------------------ producer
-    KaWalk<ROWS, TK> walk;
+    KaWalk<ROWS, TK, SH> walk;
     walk.b = *sm_b;
     walk.base = *sm_base;
     walk.q = *sm_req;
@@ -391,7 +413,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
         }
         break;
       }
-      const KvReq rq = walk.q.r;
+      const auto rq = walk.q.r;
       const int rows = rq.n * a.v.group;
       const int shift = a.v.page_shift;
       const int per_tile = TK >> shift;
@@ -410,7 +432,10 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
           if (live) raw_q[nr][c] = *reinterpret_cast<const uint4*>(src + 8 * c);
         }
       }
-      const int* row = a.v.table + static_cast<long long>(walk.b) * a.v.table_stride;
+      int table_row = walk.b;
+      if constexpr (SH)
+        if (a.v.row_of) table_row = __ldcg(a.v.row_of + walk.b);
+      const int* row = a.v.table + static_cast<long long>(table_row) * a.v.table_stride;
       // A tile's pages: the first MAX_PAGES lanes look after their keys, the next
       // after their values.  A page's id is -1 where the request has none and for an id
       // outside the cache (whose keys are NaN).  Ids are read two tiles ahead
@@ -483,6 +508,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
       // (g, t) holds row g's values [D/4 t, D/4 (t + 1))
       int all_lo = 0, all_hi = 0x7FFFFFFF, any_lo = 0x7FFFFFFF, any_hi = 0;
       long long out_of_lane = 0;
+      int row_of_lane = 0;
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) {
         const int rr = 8 * nr + g, r = walk.row_tile * ROWS + rr;
@@ -534,6 +560,13 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
           seg->lo[rr] = lo;
           seg->hi[rr] = hi;
           seg->out[rr] = out;
+          if constexpr (SH)
+            seg->row[rr] = static_cast<int>((rq.q0 + token) * (a.v.heads * a.v.group) + qh);
+        }
+        if constexpr (SH) {
+          const int own = static_cast<int>((rq.q0 + token) * (a.v.heads * a.v.group) + qh);
+          const int of = __shfl_sync(0xFFFFFFFFu, own, 4 * (lane & 7));
+          if ((lane >> 3) == nr) row_of_lane = of;
         }
         // lane r of the warp keeps row r's
         const long long of = __shfl_sync(0xFFFFFFFFu, out, 4 * (lane & 7));
@@ -555,6 +588,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
         seg->part = !(walk.begins && walk.ends);
         // the CTA's first segment and its last can be parts
         seg->slot = static_cast<int>(2 * cta + (first ? 0 : 1));
+        if constexpr (SH) seg->has_state = rq.start > 0;
       }
       // the unit goes on in other CTAs: say what joins it
       if (walk.begins && !walk.ends) {
@@ -565,8 +599,11 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
               last < edge ? ka_div(last, share + 1) : longer + ka_div(last - edge, share);
           join->parts = static_cast<int>(c1 - cta + 1);
           join->first_slot = static_cast<int>(2 * cta + (first ? 0 : 1));
+          if constexpr (SH) join->has_state = rq.start > 0;
         }
         if (lane < ROWS) join->out[lane] = out_of_lane;
+        if constexpr (SH)
+          if (lane < ROWS) join->row[lane] = row_of_lane;
       }
       first = false;
       __syncwarp();
@@ -581,6 +618,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
              clock64() - t0 < MXK_WAIT_LIMIT_CYCLES) {
       }
     }
+    if constexpr (SH) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
 
@@ -899,6 +937,13 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
     }
     const bool part = seg->part;
     const int live = seg->live;
+    // SH: the rows' states are what is written, or are to be joined with these
+    bool to_state = false, from_state = false;
+    if constexpr (SH) {
+      to_state = !part && a.state.pass == KV_PREFIX;
+      from_state = !part && a.state.pass == KV_OWN && seg->has_state;
+      if (from_state) asm volatile("griddepcontrol.wait;" ::: "memory");
+    }
     float* slot = a.ws + static_cast<long long>(seg->slot) * (ROWS * (D + 2));
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
@@ -917,9 +962,19 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
         lsum += sm_l[w * ROWS + rr] * ex2_approx(mv[w].x - M);
       }
       const bool saw = max(seg->lo[rr], seg->tile * TK) < min(seg->hi[rr], (seg->tile + seg->count) * TK);
-      if (!part) unit0 *= kv_inverse(lsum, saw);
+      if (!part && !to_state && !from_state) unit0 *= kv_inverse(lsum, saw);
       if (!saw) M = -INFINITY;
       const long long out = seg->out[rr];
+      float* state = nullptr;
+      float w_state = 0.0f, w_own = 1.0f;
+      if constexpr (SH)
+        if (adds && (to_state || from_state)) {
+          state = a.state.o + static_cast<long long>(seg->row[rr]) * D;
+          if (from_state)
+            kv_join_states(__ldcg(a.state.ml + seg->row[rr]), make_float2(M, lsum), w_state, w_own);
+          else if (c8 == 0)
+            a.state.ml[seg->row[rr]] = make_float2(M, lsum);
+        }
       // rounds over 4 columns of each of the 8 chunks
 #pragma unroll
       for (int rd = 0; rd < D / 32; ++rd) {
@@ -946,8 +1001,17 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
           s.y = s.y * unit0 * unit;
           s.z = s.z * unit0 * unit;
           s.w = s.w * unit0 * unit;
+          if (SH && from_state) {
+            const float4 p = ld_global_cg_f4(state + col);
+            s.x = s.x * w_own + p.x * w_state;
+            s.y = s.y * w_own + p.y * w_state;
+            s.z = s.z * w_own + p.z * w_state;
+            s.w = s.w * w_own + p.w * w_state;
+          }
           if (part)
             *reinterpret_cast<float4*>(slot + rr * D + col) = s;
+          else if (SH && to_state)
+            *reinterpret_cast<float4*>(state + col) = s;
           else
             kv_store4(a.O, a.o_dtype, out + col, s);
         }
@@ -974,15 +1038,17 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
 // 52.6; 256 threads, which leave the main kernel's last CTAs less room, 58.)
 // Reads of the parts go around L1 (another kernel wrote them).
 constexpr int KJ_THREADS = 128;
-template <int D, int ROWS>
+template <int D, int ROWS, bool SH>
 __global__ void __launch_bounds__(KJ_THREADS)
-kv_join_kernel(const float* __restrict__ ws, const KaJoin<ROWS>* joins, void* O, int o_dtype) {
+kv_join_kernel(const float* __restrict__ ws, const KaJoin<ROWS, SH>* joins, void* O, int o_dtype,
+               const KvState state) {
   constexpr int BATCH = 4, GROUPS = 16;
   constexpr long long PART = ROWS * (D + 2);
   __shared__ float sm_m[KJ_THREADS], sm_l[KJ_THREADS];
   __shared__ float4 sm_acc[KJ_THREADS];
+  if constexpr (SH) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const KaJoin<ROWS>* join = joins + blockIdx.x;
+  const KaJoin<ROWS, SH>* join = joins + blockIdx.x;
   const int4 head = __ldcg(reinterpret_cast<const int4*>(join));
   const int live = head.x, n = head.y;
   if (live == 0) return;
@@ -1052,6 +1118,23 @@ kv_join_kernel(const float* __restrict__ ws, const KaJoin<ROWS>* joins, void* O,
     acc.z = fmaf(w, u.z, acc.z);
     acc.w = fmaf(w, u.w, acc.w);
   }
+  if constexpr (SH) {
+    const long long at = __ldcg(&join->row[row]);
+    if (state.pass == KV_PREFIX) {
+      *reinterpret_cast<float4*>(state.o + at * D + col) = acc;
+      if (col == 0) state.ml[at] = make_float2(t, sum);
+      return;
+    }
+    if (head.w) {
+      float wp, wo;
+      kv_join_states(__ldcg(state.ml + at), make_float2(t, sum), wp, wo);
+      const float4 p = ld_global_cg_f4(state.o + at * D + col);
+      kv_store4(O, o_dtype, out + col,
+                make_float4(acc.x * wo + p.x * wp, acc.y * wo + p.y * wp, acc.z * wo + p.z * wp,
+                            acc.w * wo + p.w * wp));
+      return;
+    }
+  }
   const float inv = kv_inverse(sum, t != -INFINITY);
   acc.x *= inv;
   acc.y *= inv;
@@ -1071,16 +1154,18 @@ int ka_sm_count() {
 // a KaJoin per CTA.
 int64_t ka_slot_bytes(int64_t d, int nr) { return 8 * nr * (d + 2) * 4; }
 int ka_ctas(int nr, int sms) { return (nr == 1 ? ka_ctas_per_sm<1>() : ka_ctas_per_sm<2>()) * sms; }
-size_t ka_ws_bytes(int64_t d, int nr, int sms) {
-  const size_t join = nr == 1 ? sizeof(KaJoin<8>) : sizeof(KaJoin<16>);
+size_t ka_ws_bytes(int64_t d, int nr, int sms, bool sh) {
+  const size_t join = sh ? (nr == 1 ? sizeof(KaJoin<8, true>) : sizeof(KaJoin<16, true>))
+                         : (nr == 1 ? sizeof(KaJoin<8, false>) : sizeof(KaJoin<16, false>));
   return static_cast<size_t>(ka_ctas(nr, sms)) * (2 * ka_slot_bytes(d, nr) + join);
 }
 
-template <int FMT, int D, int NR>
+template <int FMT, int D, int NR, bool SH>
 cudaError_t ka_run(const CUtensorMap& tk, const CUtensorMap& tv, const KaArgs& a, int sms,
                    cudaStream_t st) {
-  auto kern = kv_attention_kernel<FMT, D, NR>;
-  using L = KaSmem<D, NR>;
+  auto kern = kv_attention_kernel<FMT, D, NR, SH>;
+  using L = KaSmem<D, NR, SH>;
+  using Join = KaJoin<8 * NR, SH>;
   static std::atomic<bool> attr_set[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1091,28 +1176,75 @@ cudaError_t ka_run(const CUtensorMap& tk, const CUtensorMap& tv, const KaArgs& a
     if (dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
   }
   const int ctas = ka_ctas(NR, sms);
-  kern<<<ctas, KA_THREADS, L::ALLOC, st>>>(tk, tv, a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || a.ws == nullptr) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, D / 32);
-  cfg.blockDim = dim3(KJ_THREADS);
-  cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = st;
   cfg.attrs = attr;
+  if constexpr (SH) {
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(KA_THREADS);
+    cfg.dynamicSmemBytes = L::ALLOC;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, tk, tv, a);
+    if (e != cudaSuccess) return e;
+  } else {
+    kern<<<ctas, KA_THREADS, L::ALLOC, st>>>(tk, tv, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || a.ws == nullptr) return e;
+  }
+  cfg.gridDim = dim3(ctas, D / 32);
+  cfg.blockDim = dim3(KJ_THREADS);
+  cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, 8 * NR>, static_cast<const float*>(a.ws),
-                            reinterpret_cast<const KaJoin<8 * NR>*>(a.joins), a.O, a.o_dtype);
+  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, 8 * NR, SH>, static_cast<const float*>(a.ws),
+                            reinterpret_cast<const Join*>(a.joins), a.O, a.o_dtype, a.state);
 }
 
-template <int FMT>
+template <int FMT, bool SH>
 cudaError_t ka_run_f(int64_t d, int nr, const CUtensorMap& tk, const CUtensorMap& tv,
                      const KaArgs& a, int sms, cudaStream_t st) {
   if (d == 64)
-    return nr == 1 ? ka_run<FMT, 64, 1>(tk, tv, a, sms, st) : ka_run<FMT, 64, 2>(tk, tv, a, sms, st);
-  return nr == 1 ? ka_run<FMT, 128, 1>(tk, tv, a, sms, st) : ka_run<FMT, 128, 2>(tk, tv, a, sms, st);
+    return nr == 1 ? ka_run<FMT, 64, 1, SH>(tk, tv, a, sms, st) : ka_run<FMT, 64, 2, SH>(tk, tv, a, sms, st);
+  return nr == 1 ? ka_run<FMT, 128, 1, SH>(tk, tv, a, sms, st) : ka_run<FMT, 128, 2, SH>(tk, tv, a, sms, st);
+}
+
+template <bool SH>
+cudaError_t ka_launch(const KvAttn& q, const KvPassArgs* pass, int sms, cudaStream_t st) {
+  const KvCache& c = q.cache;
+  KaArgs a{};
+  a.v = kv_view(q);
+  a.Q = static_cast<const uint16_t*>(q.Q);
+  a.O = q.O;
+  a.q_ts = q.q_ts;
+  a.q_hs = q.q_hs;
+  a.o_ts = q.o_ts;
+  a.o_hs = q.o_hs;
+  a.bf16 = q.dtype == DT_BF16;
+  a.o_dtype = q.o_dtype;
+  a.scale_log2e = q.scale * 1.4426950408889634f;
+  if constexpr (SH) {
+    a.v.start = pass->start;
+    a.v.row_of = pass->row_of;
+    a.v.cu_step = pass->cu_step;
+    a.state = pass->state;
+  }
+  // eight rows where the rows that one request has for a cache head fit
+  const int nr = q.max_q * a.v.group <= 8 ? 1 : 2;
+  if (q.ws && q.ws_bytes >= ka_ws_bytes(c.d, nr, sms, SH)) {
+    a.ws = static_cast<float*>(q.ws);
+    a.joins = static_cast<uint8_t*>(q.ws) + ka_ctas(nr, sms) * 2 * ka_slot_bytes(c.d, nr);
+  } else if (SH) {
+    return cudaErrorInvalidValue;             // the caller has seen to it
+  }
+  CUtensorMap tk, tv;
+  if (!kv_tensor_map(&tk, c.k, c) || !kv_tensor_map(&tv, c.v, c)) return cudaErrorInvalidValue;
+  switch (c.fmt) {
+    case FMT_E4M3: return ka_run_f<FMT_E4M3, SH>(c.d, nr, tk, tv, a, sms, st);
+    case FMT_E5M2: return ka_run_f<FMT_E5M2, SH>(c.d, nr, tk, tv, a, sms, st);
+    default: return ka_run_f<FMT_INT8, SH>(c.d, nr, tk, tv, a, sms, st);
+  }
 }
 
 }  // namespace
@@ -1132,44 +1264,38 @@ namespace {
 constexpr int64_t KA_MOST_ROWS = 32;
 bool many_rows(int64_t max_q, int64_t group) { return max_q * group > KA_MOST_ROWS; }
 
+size_t few_rows_bytes(int64_t d, int sms, bool sh) {
+  return std::max(ka_ws_bytes(d, 1, sms, sh), ka_ws_bytes(d, 2, sms, sh));
+}
+
 }  // namespace
 
 size_t kv_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t max_q) {
   const int sms = ka_sm_count();
-  const size_t few = std::max(ka_ws_bytes(d, 1, sms), ka_ws_bytes(d, 2, sms));
+  const size_t few = few_rows_bytes(d, sms, false);
   return many_rows(max_q, q_heads / kv_heads) ? std::max(few, kv_prompt_workspace_bytes(d, sms)) : few;
 }
 
 cudaError_t launch_kv_attention(const KvAttn& q, cudaStream_t st) {
-  const KvCache& c = q.cache;
   const int sms = ka_sm_count();
   if (sms <= 0) return cudaErrorInvalidValue;
-  if (many_rows(q.max_q, q.q_heads / c.heads) && q.requests <= kv_prompt_max_requests())
-    return launch_kv_prompt(q, sms, st);
-  KaArgs a{};
-  a.v = kv_view(q);
-  a.Q = static_cast<const uint16_t*>(q.Q);
-  a.O = q.O;
-  a.q_ts = q.q_ts;
-  a.q_hs = q.q_hs;
-  a.o_ts = q.o_ts;
-  a.o_hs = q.o_hs;
-  a.bf16 = q.dtype == DT_BF16;
-  a.o_dtype = q.o_dtype;
-  a.scale_log2e = q.scale * 1.4426950408889634f;
-  // eight rows where the rows that one request has for a cache head fit
-  const int nr = q.max_q * a.v.group <= 8 ? 1 : 2;
-  if (q.ws && q.ws_bytes >= ka_ws_bytes(c.d, nr, sms)) {
-    a.ws = static_cast<float*>(q.ws);
-    a.joins = static_cast<uint8_t*>(q.ws) + ka_ctas(nr, sms) * 2 * ka_slot_bytes(c.d, nr);
-  }
-  CUtensorMap tk, tv;
-  if (!kv_tensor_map(&tk, c.k, c) || !kv_tensor_map(&tv, c.v, c)) return cudaErrorInvalidValue;
-  switch (c.fmt) {
-    case FMT_E4M3: return ka_run_f<FMT_E4M3>(c.d, nr, tk, tv, a, sms, st);
-    case FMT_E5M2: return ka_run_f<FMT_E5M2>(c.d, nr, tk, tv, a, sms, st);
-    default: return ka_run_f<FMT_INT8>(c.d, nr, tk, tv, a, sms, st);
-  }
+  if (many_rows(q.max_q, q.q_heads / q.cache.heads) && q.requests <= kv_prompt_max_requests())
+    return launch_kv_prompt(q, sms, nullptr, st);
+  return ka_launch<false>(q, nullptr, sms, st);
+}
+
+size_t kv_pass_workspace_bytes(int64_t group, int64_t d, int64_t max_q) {
+  const int sms = ka_sm_count();
+  const size_t few = few_rows_bytes(d, sms, true);
+  const size_t n = many_rows(max_q, group) ? std::max(few, kv_prompt_workspace_bytes(d, sms)) : few;
+  return (n + 31) / 32 * 32;
+}
+
+cudaError_t launch_kv_pass(const KvAttn& q, const KvPassArgs& pass, cudaStream_t st) {
+  const int sms = ka_sm_count();
+  if (sms <= 0) return cudaErrorInvalidValue;
+  if (many_rows(q.max_q, q.q_heads / q.cache.heads)) return launch_kv_prompt(q, sms, &pass, st);
+  return ka_launch<true>(q, &pass, sms, st);
 }
 
 unsigned fetch_and_clear_status_kv(cudaError_t* err) {

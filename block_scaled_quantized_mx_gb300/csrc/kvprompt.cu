@@ -103,7 +103,7 @@ struct KpSeg {
   int row0;                                // the unit's first row
   int head;
   int slot;                                // workspace slot, -1: not a part
-  int pad;
+  int start;                               // SH: the request's first key
 };
 
 // A unit that begins in this CTA's stretch and goes on in others'.
@@ -113,12 +113,13 @@ struct KpJoin {
   int first_slot;                          // this CTA's slot; the others use their first
   int head;
   int row0;
-  int pad;
+  int has_state;                           // SH: a prefix went before
   long long q0;
 };
 
 // The key blocks of row tile rt of a request: [first, first + count).
-__device__ __forceinline__ int kp_blocks(const KvView& v, const KvReq& r, int rt, int& first) {
+template <class Req>
+__device__ __forceinline__ int kp_blocks(const KvView& v, const Req& r, int rt, int& first) {
   const int rows = r.n * v.group;
   const int t0 = rt * KP_ROWS / v.group;
   const int t1 = (min(rows, (rt + 1) * KP_ROWS) - 1) / v.group;
@@ -133,18 +134,19 @@ __device__ __forceinline__ int kp_row_tiles(const KvView& v, const KvReq& r) {
 
 // The walk over one CTA's stretch of the list: groups of units (request, row
 // tile), in each the cache heads, each with KP_OVER entries and its blocks.
+template <bool SH>
 struct KpWalk {
   long long w, w1;
   long long base;              // first entry of the group
   int b, rt, tiles;            // request, row tile, the request's row tiles
   int blocks, block0;          // of each unit of the group
-  KvReq r;
+  std::conditional_t<SH, KvShReq, KvReq> r;
   int head, block, count;
   bool begins, ends;
   long long unit_start, unit_end;
 
   __device__ __forceinline__ void enter(const KvView& v) {   // b, rt -> the rest
-    r = kv_request(v, b);
+    r = kv_request<SH>(v, b);
     tiles = kp_row_tiles(v, r);
     if (rt < tiles) blocks = kp_blocks(v, r, rt, block0);
   }
@@ -183,7 +185,7 @@ struct KpWalk {
   }
 };
 
-template <int D>
+template <int D, bool SH>
 struct KpSmem {
   static constexpr int REGION = 128 * 128;
   static constexpr int Q_BYTES = (D / 64) * REGION;
@@ -204,7 +206,7 @@ struct KpSmem {
   static constexpr int BARS = 4 * KP_STAGES + 12 + 4 + 2 * KP_PG + 2 * RAW;
   static constexpr int MISC_OFF = BAR_OFF + BARS * 8;
   static constexpr int WALK_OFF = MISC_OFF + 16;
-  static constexpr int TOTAL = WALK_OFF + static_cast<int>(sizeof(KpWalk));
+  static constexpr int TOTAL = WALK_OFF + static_cast<int>(sizeof(KpWalk<SH>));
   static constexpr int ALLOC = TOTAL + 1024;
   static_assert(ALLOC <= 232448, "shared memory budget");
   static_assert(PG_OFF >= KP_MAX_REQUESTS * 4, "the plan's array fits in the operand tiles");
@@ -221,6 +223,7 @@ struct KpArgs {
   float* ws;                               // two slots per CTA: O as [D / 8][256 rows][8], m[256], l[256];
                                            // 32-byte aligned
   KpJoin* joins;                           // one per CTA
+  KvState state;                           // SH
 };
 
 __device__ __forceinline__ void kp_timeout(volatile int* abort, unsigned site) {
@@ -347,11 +350,12 @@ __device__ __forceinline__ long long kp_scan(long long v, long long* sm, long lo
   return before + s - v;
 }
 
-template <int FMT, int D>
+template <int FMT, int D, bool SH>
 __global__ void __launch_bounds__(KP_THREADS, 1)
 kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                  const KpArgs a) {
-  using L = KpSmem<D>;
+  using L = KpSmem<D, SH>;
+  using Req = std::conditional_t<SH, KvShReq, KvReq>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -373,11 +377,16 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::MISC_OFF);
   volatile int* abort = reinterpret_cast<volatile int*>(gbase + L::MISC_OFF + 4);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // The prefix pass reads what the plan wrote, before others may follow; the other
+  // one's launch follows all of that, and it waits for the prefixes' states where it
+  // needs them (and before it ends, for what comes after it).
+  if constexpr (SH)
+    if (a.state.pass == KV_PREFIX) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- the list: row tiles of each request, then entries of each row tile
   // (in the operand regions, which nothing uses yet)
-  KpWalk* walk = reinterpret_cast<KpWalk*>(gbase + L::WALK_OFF);   // warp 0's, kept by lane 0
+  KpWalk<SH>* walk = reinterpret_cast<KpWalk<SH>*>(gbase + L::WALK_OFF);   // warp 0's, kept by lane 0
   long long total, w0, ctas;
   {
     int* sm_rt = reinterpret_cast<int*>(gbase);                        // requests + 1
@@ -387,11 +396,11 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     const int per = (B + KP_THREADS - 1) / KP_THREADS;
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
     long long mine = 0, tiles;
-    for (int b = b0; b < b1; ++b) mine += kp_row_tiles(a.v, kv_request(a.v, b));
+    for (int b = b0; b < b1; ++b) mine += kp_row_tiles(a.v, kv_request<SH>(a.v, b));
     long long at = kp_scan(mine, sm_scan, tiles);
     for (int b = b0; b < b1; ++b) {
       sm_rt[b] = list.start(at);
-      at += kp_row_tiles(a.v, kv_request(a.v, b));
+      at += kp_row_tiles(a.v, kv_request<SH>(a.v, b));
     }
     tiles = list.clip(tiles);
     __syncthreads();
@@ -401,19 +410,19 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     auto each = [&](auto f) {
       if (f0 >= f1) return;
       int b = KvTileList::request(sm_rt, B, f0);
-      KvReq r = kv_request(a.v, b);
+      Req r = kv_request<SH>(a.v, b);
       int rt = static_cast<int>(f0 - sm_rt[b]), n = kp_row_tiles(a.v, r);
       for (long long i = f0; i < f1; ++i, ++rt) {
         while (rt >= n) {
           rt = 0;
-          r = kv_request(a.v, ++b);
+          r = kv_request<SH>(a.v, ++b);
           n = kp_row_tiles(a.v, r);
         }
         if (!f(b, rt, r)) return;
       }
     };
     mine = 0;
-    each([&](int, int rt, const KvReq& r) {
+    each([&](int, int rt, const Req& r) {
       int first;
       mine += static_cast<long long>(a.v.heads) * (KP_OVER + kp_blocks(a.v, r, rt, first));
       return true;
@@ -423,7 +432,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     w0 = total * blockIdx.x / max(1ll, ctas);
     if (blockIdx.x < ctas && w0 >= before && w0 < before + mine) {
       long long p = before;
-      each([&](int b, int rt, const KvReq& r) {
+      each([&](int b, int rt, const Req& r) {
         int first;
         const int blocks = kp_blocks(a.v, r, rt, first);
         const long long n = static_cast<long long>(a.v.heads) * (KP_OVER + blocks);
@@ -431,7 +440,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           p += n;
           return true;
         }
-        KpWalk k;
+        KpWalk<SH> k;
         k.w = w0;
         k.w1 = total * (blockIdx.x + 1) / ctas;
         k.base = p;
@@ -450,7 +459,10 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     __syncthreads();
     KpJoin* join = a.joins ? a.joins + blockIdx.x : nullptr;
     if (tid == 0 && join) join->live = 0;
-    if (blockIdx.x >= ctas) return;          // the whole CTA: nothing was started
+    if (blockIdx.x >= ctas) {                // the whole CTA: nothing was started
+      if constexpr (SH) asm volatile("griddepcontrol.wait;" ::: "memory");
+      return;
+    }
   }
   // the regions go to their owners, TMA and the tensor core among them
   fence_proxy_async_smem();
@@ -546,6 +558,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             s->q0 = walk->r.q0;
             s->row0 = walk->rt * KP_ROWS;
             s->head = walk->head;
+            if constexpr (SH) s->start = walk->r.start;
             const int slot = 2 * static_cast<int>(blockIdx.x) + (first_seg ? 0 : 1);
             s->slot = walk->begins && walk->ends ? -1 : slot;
             if (walk->begins && !walk->ends) {
@@ -554,6 +567,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
               j->parts = static_cast<int>((walk->unit_end * ctas - 1) / total - blockIdx.x + 1);
               j->first_slot = slot;
               j->head = walk->head;
+              if constexpr (SH) j->has_state = walk->r.start > 0;
               j->row0 = walk->rt * KP_ROWS;
               j->q0 = walk->r.q0;
             }
@@ -564,8 +578,11 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         first_seg = false;
         if (!found) break;
         const int count = walk->count, block0 = walk->block, head = walk->head;
-        const KvReq rq = walk->r;
-        const int* row = a.v.table + static_cast<long long>(walk->b) * a.v.table_stride;
+        const Req rq = walk->r;
+        int table_row = walk->b;
+        if constexpr (SH)
+          if (a.v.row_of) table_row = __ldcg(a.v.row_of + table_row);
+        const int* row = a.v.table + static_cast<long long>(table_row) * a.v.table_stride;
         const int shift = a.v.page_shift;
         const int first_key = kv_first_key(a.v, rq, walk->rt * KP_ROWS / a.v.group);
         __syncwarp();                          // all lanes have read the walk
@@ -847,7 +864,8 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       float up = 1.0f;
       if (next_count != 0) {
         // this thread's row: Q to f16, its bounds and factor
-        KvReq rq;
+        Req rq;
+        if constexpr (SH) rq.start = segs[ss].start;
         rq.q0 = segs[ss].q0;
         rq.n = segs[ss].n;
         rq.len = segs[ss].len;
@@ -917,7 +935,25 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         // rows of O 32 bytes at a time where they are that aligned
         const bool by32 = ((reinterpret_cast<uintptr_t>(a.O) |
                             static_cast<uintptr_t>(out * (a.o_dtype == DT_F32 ? 4 : 2))) & 31) == 0;
-        const float f = part ? unit0 : unit0 * kv_inverse(l, saw);
+        // SH: the rows' states are what is written, or are to be joined with these
+        bool to_state = false;
+        float* state = nullptr;
+        float w_state = 0.0f, w_own = 1.0f;
+        if constexpr (SH) {
+          to_state = !part && a.state.pass == KV_PREFIX;
+          const bool from_state = !part && a.state.pass == KV_OWN && sg->start > 0;
+          const long long at = (sg->q0 + token) * (static_cast<long long>(a.v.heads) * a.v.group) +
+                               sg->head * a.v.group + row - token * a.v.group;
+          if (from_state) asm volatile("griddepcontrol.wait;" ::: "memory");
+          if ((to_state || from_state) && live) {
+            state = a.state.o + at * D;
+            if (from_state)
+              kv_join_states(__ldcg(a.state.ml + at), make_float2(saw ? m : -INFINITY, l), w_state, w_own);
+            else
+              a.state.ml[at] = make_float2(saw ? m : -INFINITY, l);
+          }
+        }
+        const float f = part || (SH && state) ? unit0 : unit0 * kv_inverse(l, saw);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -926,6 +962,24 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           if (!live) continue;
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f * unit);
+          if constexpr (SH) {
+            if (to_state) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                st_global_v8(state + 32 * c + 8 * e, *reinterpret_cast<const uint32_t(*)[8]>(o + 8 * e));
+              continue;
+            }
+            if (state) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 p = ld_global_cg_f4(state + 32 * c + 4 * e);
+                const float pp[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  o[4 * e + i] = __float_as_uint(__uint_as_float(o[4 * e + i]) * w_own + pp[i] * w_state);
+              }
+            }
+          }
           if (part) {
             // lanes hold consecutive rows: whole lines of [8 columns][row][column]
 #pragma unroll
@@ -1131,6 +1185,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     tc_fence_after();
     tmem_dealloc_cg<1>(tmem_base, KP_TMEM_COLS);
   }
+  if constexpr (SH) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Join the parts of the unit that begins in CTA blockIdx.x's stretch, in CTA
@@ -1142,9 +1197,10 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 // chunk took 226 us instead of 219; one or four rows a thread: 219, 223.)
 constexpr int KPJ_THREADS = 256;
 constexpr int KPJ_R = 2;                       // rows of a thread
-template <int D>
+template <int D, bool SH>
 __global__ void __launch_bounds__(KPJ_THREADS)
 kv_prompt_join_kernel(const KpArgs a) {
+  if constexpr (SH) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const KpJoin* join = a.joins + blockIdx.x;
   const int live = __ldcg(&join->live);
@@ -1158,6 +1214,7 @@ kv_prompt_join_kernel(const KpArgs a) {
   const float* rest = a.ws + 2ll * blockIdx.x * PART;
   const int row0 = __ldcg(&join->row0), head = __ldcg(&join->head);
   const long long q0 = __ldcg(&join->q0);
+  const int has_state = SH ? __ldcg(&join->has_state) : 0;
   float top[KPJ_R], sum[KPJ_R], acc[KPJ_R][8];
 #pragma unroll
   for (int i = 0; i < KPJ_R; ++i) {
@@ -1195,17 +1252,35 @@ kv_prompt_join_kernel(const KpArgs a) {
     const int row = row0 + r0 + 4 * i, token = row / a.v.group;
     const long long out =
         (q0 + token) * a.o_ts + (head * a.v.group + row - token * a.v.group) * a.o_hs + col;
+    if constexpr (SH) {
+      const long long at = (q0 + token) * (static_cast<long long>(a.v.heads) * a.v.group) +
+                           head * a.v.group + row - token * a.v.group;
+      if (a.state.pass == KV_PREFIX) {
+        kv_store8(a.state.o, DT_F32, at * D + col, acc[i]);
+        if (col == 0) a.state.ml[at] = make_float2(top[i], sum[i]);
+        continue;
+      }
+      if (has_state) {
+        float wp, wo, p[8];
+        kv_join_states(__ldcg(a.state.ml + at), make_float2(top[i], sum[i]), wp, wo);
+        ld_global_cg_v8(a.state.o + at * D + col, p);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[i][e] = acc[i][e] * wo + p[e] * wp;
+        kv_store8(a.O, a.o_dtype, out, acc[i]);
+        continue;
+      }
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[i][e] *= inv;
     kv_store8(a.O, a.o_dtype, out, acc[i]);
   }
 }
 
-template <int FMT, int D>
+template <int FMT, int D, bool SH>
 cudaError_t kp_run(const CUtensorMap& tk, const CUtensorMap& tv, const KpArgs& a, int sms,
                    cudaStream_t st) {
-  auto kern = kv_prompt_kernel<FMT, D>;
-  using L = KpSmem<D>;
+  auto kern = kv_prompt_kernel<FMT, D, SH>;
+  using L = KpSmem<D, SH>;
   static std::atomic<bool> attr_set[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1221,19 +1296,43 @@ cudaError_t kp_run(const CUtensorMap& tk, const CUtensorMap& tv, const KpArgs& a
       return cudaErrorInvalidConfiguration;
     if (dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
   }
-  kern<<<sms, KP_THREADS, L::ALLOC, st>>>(tk, tv, a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || a.ws == nullptr) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sms, KP_ROWS * (D / 8) / (KPJ_THREADS * KPJ_R));
-  cfg.blockDim = dim3(KPJ_THREADS);
-  cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = st;
   cfg.attrs = attr;
+  if constexpr (SH) {
+    cfg.gridDim = dim3(sms);
+    cfg.blockDim = dim3(KP_THREADS);
+    cfg.dynamicSmemBytes = L::ALLOC;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, tk, tv, a);
+    if (e != cudaSuccess) return e;
+  } else {
+    kern<<<sms, KP_THREADS, L::ALLOC, st>>>(tk, tv, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || a.ws == nullptr) return e;
+  }
+  cfg.gridDim = dim3(sms, KP_ROWS * (D / 8) / (KPJ_THREADS * KPJ_R));
+  cfg.blockDim = dim3(KPJ_THREADS);
+  cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_prompt_join_kernel<D>, a);
+  return cudaLaunchKernelEx(&cfg, kv_prompt_join_kernel<D, SH>, a);
+}
+
+template <bool SH>
+cudaError_t kp_run_f(const KvCache& c, const CUtensorMap& tk, const CUtensorMap& tv, const KpArgs& a,
+                     int sms, cudaStream_t st) {
+  const bool d64 = c.d == 64;
+  switch (c.fmt) {
+    case FMT_E4M3:
+      return d64 ? kp_run<FMT_E4M3, 64, SH>(tk, tv, a, sms, st) : kp_run<FMT_E4M3, 128, SH>(tk, tv, a, sms, st);
+    case FMT_E5M2:
+      return d64 ? kp_run<FMT_E5M2, 64, SH>(tk, tv, a, sms, st) : kp_run<FMT_E5M2, 128, SH>(tk, tv, a, sms, st);
+    default:
+      return d64 ? kp_run<FMT_INT8, 64, SH>(tk, tv, a, sms, st) : kp_run<FMT_INT8, 128, SH>(tk, tv, a, sms, st);
+  }
 }
 
 }  // namespace
@@ -1244,7 +1343,7 @@ size_t kv_prompt_workspace_bytes(int64_t d, int sms) {
   return static_cast<size_t>(sms) * (2 * KP_ROWS * (d + 2) * 4 + sizeof(KpJoin)) + 16;
 }
 
-cudaError_t launch_kv_prompt(const KvAttn& q, int sms, cudaStream_t st) {
+cudaError_t launch_kv_prompt(const KvAttn& q, int sms, const KvPassArgs* pass, cudaStream_t st) {
   const KvCache& c = q.cache;
   KpArgs a{};
   a.v = kv_view(q);
@@ -1263,17 +1362,16 @@ cudaError_t launch_kv_prompt(const KvAttn& q, int sms, cudaStream_t st) {
     a.ws = reinterpret_cast<float*>(ws);
     a.joins = reinterpret_cast<KpJoin*>(ws + static_cast<int64_t>(sms) * 2 * KP_ROWS * (c.d + 2) * 4);
   }
+  if (pass) {
+    if (a.ws == nullptr) return cudaErrorInvalidValue;   // the caller has seen to it
+    a.v.start = pass->start;
+    a.v.row_of = pass->row_of;
+    a.v.cu_step = pass->cu_step;
+    a.state = pass->state;
+  }
   CUtensorMap tk, tv;
   if (!kv_tensor_map(&tk, c.k, c) || !kv_tensor_map(&tv, c.v, c)) return cudaErrorInvalidValue;
-  const bool d64 = c.d == 64;
-  switch (c.fmt) {
-    case FMT_E4M3:
-      return d64 ? kp_run<FMT_E4M3, 64>(tk, tv, a, sms, st) : kp_run<FMT_E4M3, 128>(tk, tv, a, sms, st);
-    case FMT_E5M2:
-      return d64 ? kp_run<FMT_E5M2, 64>(tk, tv, a, sms, st) : kp_run<FMT_E5M2, 128>(tk, tv, a, sms, st);
-    default:
-      return d64 ? kp_run<FMT_INT8, 64>(tk, tv, a, sms, st) : kp_run<FMT_INT8, 128>(tk, tv, a, sms, st);
-  }
+  return pass ? kp_run_f<true>(c, tk, tv, a, sms, st) : kp_run_f<false>(c, tk, tv, a, sms, st);
 }
 
 unsigned fetch_and_clear_status_kvp(cudaError_t* err) {

@@ -728,6 +728,38 @@ mx_status mx_kv_attention(const void* Q, int32_t dtype, int64_t tokens, int64_t 
                           int64_t window, float scale, void* workspace, size_t workspace_bytes,
                           void* stream);
 
+/*
+ * mx_kv_attention_shared -- mx_kv_attention (without a window) for a batch in which
+ * requests share their first tokens: those are read, and their scores computed, once
+ * for all rows of a group.
+ *
+ *   groups     device, int32, n_groups + 1 entries: group g is the requests groups[g] ..
+ *              groups[g + 1] - 1.  Offsets outside 0 .. requests count as the nearest of
+ *              the two, one below an earlier one as that one; requests in front of the
+ *              first group and behind the last share nothing
+ *   shared     device, int32, n_groups entries: how many of its first tokens a group's
+ *              requests have in common, or more.  Shared are those in front of the first page
+ *              on which the requests' rows of the table differ, and in front of all of
+ *              the group's rows: any value gives the right results
+ *   workspace  as for mx_kv_attention, at least mx_kv_attention_shared_workspace_bytes()
+ *              bytes, which grow with each argument; NULL or a smaller size, or no groups:
+ *              every request reads its keys itself, as mx_kv_attention does
+ * requests and n_groups up to 16384, tokens * q_heads below 2^31.  The other arguments,
+ * results and bounds are those of mx_kv_attention, whose last bits may differ.
+ */
+size_t mx_kv_attention_shared_workspace_bytes(int64_t tokens, int64_t q_heads, int64_t heads,
+                                              int64_t d, int64_t max_q, int64_t requests,
+                                              int64_t groups);
+mx_status mx_kv_attention_shared(const void* Q, int32_t dtype, int64_t tokens, int64_t q_heads,
+                                 int64_t q_token_stride, int64_t q_head_stride,
+                                 const mx_kv_cache* cache, const int32_t* table,
+                                 int64_t table_stride, int64_t table_width, const int32_t* lens,
+                                 const int32_t* cu, int64_t requests, int64_t max_q,
+                                 const int32_t* groups, const int32_t* shared, int64_t n_groups,
+                                 void* O, int32_t o_dtype, int64_t o_token_stride,
+                                 int64_t o_head_stride, int32_t causal, float scale,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronize the stream, then return (and clear) the first error recorded
  * by a kernel of this library on the current device: MX_OK,
  * MX_ERR_TIMEOUT, or MX_ERR_CUDA if the synchronization itself failed. */

@@ -88,3 +88,41 @@ def test_restatement_by_hand():
     assert _share.release([20, 20, 17], [0, 16, 0], table, stack, 0, refs, 16) == ([0, 16, 0], [3, 0])
     # freed: 2 by request 0, 0 by request 1, 1 by request 2
     assert stack == [1, 0, 2, -1] and refs == [0, 0, 0, 0]
+
+
+def _shared(L, **kw):
+    a = dict(cache={}, Q=X, dtype=mx.DT_BF16, T=4, hq=8, qs=(1024, 128), table=X, stride=16, width=16, lens=X, cu=X, B=2, max_q=2,
+             groups=X, shared=X, n=1, O=X, odt=mx.DT_BF16, os=(1024, 128), causal=1, scale=0.1, ws=None, bytes=0)
+    a.update(kw)
+    c = _cache(**a["cache"])
+    return L.mx_kv_attention_shared(a["Q"], a["dtype"], a["T"], a["hq"], *a["qs"], ctypes.byref(c), a["table"], a["stride"], a["width"],
+                                    a["lens"], a["cu"], a["B"], a["max_q"], a["groups"], a["shared"], a["n"], a["O"], a["odt"],
+                                    *a["os"], a["causal"], a["scale"], a["ws"], a["bytes"], None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(cache=dict(fmt=mx.E2M1)), INVALID), (dict(cache=dict(d=96)), SHAPE), (dict(cache=dict(k_data=X + 8)), ALIGN),
+    (dict(dtype=mx.DT_F32), INVALID), (dict(odt=7), INVALID), (dict(hq=7), SHAPE), (dict(hq=0), SHAPE), (dict(causal=2), INVALID),
+    (dict(scale=float("nan")), INVALID), (dict(stride=8), SHAPE), (dict(width=0), SHAPE), (dict(B=-1), SHAPE), (dict(B=16385), SHAPE),
+    (dict(n=-1), SHAPE), (dict(n=16385), SHAPE), (dict(T=2 ** 29), SHAPE), (dict(groups=None), INVALID), (dict(shared=None), INVALID),
+    (dict(Q=None), INVALID), (dict(table=None), INVALID), (dict(cu=None), INVALID), (dict(lens=None), INVALID),
+    (dict(O=X + 8), ALIGN), (dict(qs=(1024, 100)), SHAPE), (dict(ws=X + 4, bytes=1 << 30), ALIGN), (dict(max_q=-1), SHAPE),
+    (dict(T=0), OK), (dict(B=0), OK)])
+def test_shared_attention_refuses(L, kw, want):
+    assert _shared(L, **kw) == want
+
+
+def test_shared_workspace_bytes_refuses(L):
+    f = L.mx_kv_attention_shared_workspace_bytes
+    for bad in ((4, 8, 3, 128, 1, 2, 1), (4, 8, 0, 128, 1, 2, 1), (4, 0, 1, 128, 1, 2, 1), (4, 8, 2, 80, 1, 2, 1),
+                (4, 8, 2, 128, 0, 2, 1), (0, 8, 2, 128, 1, 2, 1), (4, 8, 2, 128, 1, 0, 1), (4, 8, 2, 128, 1, 2, 0),
+                (4, 8, 2, 128, 1, 16385, 1), (4, 8, 2, 128, 1, 2, 16385), (2 ** 28, 8, 2, 128, 1, 2, 1)):
+        assert f(*bad) == 0
+
+
+def test_the_binding_of_shared_attention_refuses():
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)  # noqa: E731
+    cache = mx.KVCache(u8(4, 2, 16, 64), u8(4, 2, 16, 64), u8(4, 2), u8(4, 2), mx.E4M3)
+    i, q = torch.zeros(2, dtype=torch.int32), torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        mx.mx_kv_attention_shared(q, cache, i.view(2, 1), i, i, 1, i, i)

@@ -1,0 +1,275 @@
+"""mx_kv_attention_shared against the 64-bit restatement of attention over the
+cache, with mx_kv_attention's bound: the states of the two key sets are joined in
+fp32, a few roundings of 2^-24 among the 64 that the bound counts."""
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_quantized_mx_gb300 as mx
+from tests import _kv
+
+pytestmark = pytest.mark.gpu
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    mx.build()
+    mx.lib()
+
+
+def _i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+class Batch:
+    """groups: (common tokens, [(own tokens, rows) of each request]) each; common 0 for requests
+    that share nothing (they stand in no group if loose)."""
+
+    def __init__(self, groups, hq, heads, d, page, fmt=mx.E4M3, dtype=BF16, seed=0, spread=2.0):
+        rng = np.random.default_rng(seed)
+        lens, new, rows, ids = [], [], [], 0
+        for common, requests in groups:
+            lead = list(range(ids, ids + common // page))
+            ids += len(lead)
+            for own, n in requests:
+                total = common + own
+                k = -(-total // page) - len(lead)
+                rows.append(lead + list(range(ids, ids + k)))
+                ids += k
+                lens.append(total)
+                new.append(n)
+        pages = ids + 2
+        order = rng.permutation(pages)
+        self.width = max(1, max(len(r) for r in rows))
+        table = np.full((len(rows), self.width), -1, np.int32)
+        for b, r in enumerate(rows):
+            table[b, :len(r)] = order[r]
+        if fmt == mx.INT8:
+            k, v = (rng.integers(-128, 128, (pages, heads, page, d)).astype(np.int8).view(np.uint8) for _ in "kv")
+        else:
+            top = 0x7E if fmt == mx.E4M3 else 0x7B
+            k, v = (rng.integers(top // 3, top + 1, (pages, heads, page, d)).astype(np.uint8) | (rng.integers(0, 2, (pages, heads, page, d)) << 7).astype(np.uint8)
+                    for _ in "kv")
+        ref = {mx.E4M3: 127 - 8, mx.E5M2: 127 - 15, mx.INT8: 127 - 7}[fmt]
+        ks, vs = ((ref + np.rint(rng.normal(0, spread, (pages, heads)))).astype(np.uint8) for _ in "kv")
+        # pages that begin a request's own tokens hold the common rest too: the same values
+        for (common, requests), b0 in zip(groups, np.cumsum([0] + [len(r) for _, r in groups[:-1]])):
+            j, part = common // page, common % page
+            if part and len(requests) > 1:
+                p0 = table[b0, j]
+                for b in range(b0 + 1, b0 + len(requests)):
+                    p = table[b, j]
+                    for c, s in ((k, ks), (v, vs)):
+                        c[p, :, :part], s[p] = c[p0, :, :part], s[p0]
+        self.planes = k, v, ks, vs
+        self.fmt, self.heads, self.table, self.lens = fmt, heads, table, lens
+        self.cu = np.concatenate([[0], np.cumsum(new)])
+        self.most = max(new)
+        self.cache = mx.KVCache(*[torch.from_numpy(t).cuda() for t in self.planes], fmt)
+        self.q = (torch.randn(int(self.cu[-1]), hq, d, generator=torch.Generator().manual_seed(seed)) * 0.7).to(dtype)
+        self.edges = np.cumsum([0] + [len(r) for _, r in groups])
+        self.common = [c for c, _ in groups]
+
+    def workspace(self, n_groups=None):
+        T, hq, d = self.q.shape
+        n = mx.kv_attention_shared_workspace_bytes(T, hq, self.heads, d, self.most, len(self.lens), n_groups or len(self.common))
+        assert n > 0
+        return torch.empty(n, dtype=torch.uint8, device="cuda")
+
+    def run(self, groups=None, shared=None, ws=True, **kw):
+        groups = self.edges if groups is None else groups
+        shared = self.common if shared is None else shared
+        w = self.workspace(max(1, len(shared))) if ws is True else ws
+        return mx.mx_kv_attention_shared(self.q.cuda(), self.cache, _i32(self.table), _i32(self.lens), _i32(self.cu), self.most,
+                                         _i32(groups), _i32(shared), workspace=w, **kw)
+
+    def check(self, got, causal=True, scale=None):
+        d = self.q.shape[2]
+        e = _kv.attention(self.q.double().numpy(), *self.planes, self.fmt, self.table, self.lens, self.cu,
+                          d ** -0.5 if scale is None else scale, causal=causal)
+        bound = _kv.bound(*e, got.dtype)
+        err = np.abs(got.double().cpu().numpy() - e[0])
+        assert (err <= bound).all(), (err / np.maximum(bound, 1e-300)).max()
+        assert mx.mx_last_error() == 0
+
+
+CASES = [
+    # (groups, hq, heads, d, page, fmt, dtype)
+    ([(64, [(5, 1), (9, 1)])], 2, 2, 64, 16, mx.E4M3, BF16),
+    ([(128, [(1, 1)] * 4)], 8, 2, 128, 64, mx.E4M3, BF16),
+    ([(300, [(17, 1), (200, 1), (33, 2), (64, 0), (40, 4)])], 6, 2, 128, 32, mx.E5M2, F16),
+    ([(1, [(3, 1), (2, 2)]), (0, [(40, 1)]), (513, [(1, 1), (90, 1), (130, 1)])], 4, 4, 64, 128, mx.INT8, F16),
+    # many rows to a prefix, few to a request
+    ([(700, [(7 + 13 * i, 1 + i % 3) for i in range(21)])], 8, 2, 128, 64, mx.E4M3, BF16),
+    ([(700, [(7 + 13 * i, 1 + i % 3) for i in range(21)])], 8, 2, 64, 16, mx.INT8, F16),
+    ([(333, [(20, 1)] * 40), (0, [(50, 1), (60, 3)]), (256, [(9, 2)] * 9)], 4, 1, 128, 16, mx.E5M2, BF16),
+    # many rows to a request
+    ([(200, [(90, 40), (70, 66), (150, 1)])], 4, 2, 128, 64, mx.E4M3, BF16),
+    ([(128, [(300, 150), (131, 131)]), (0, [(97, 97)])], 2, 1, 64, 32, mx.INT8, F16),
+]
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+@pytest.mark.parametrize("out_dtype", [F32, None])
+@pytest.mark.parametrize("causal", [True, False])
+def test_against_64_bits(case, out_dtype, causal):
+    groups, hq, heads, d, page, fmt, dtype = CASES[case]
+    b = Batch(groups, hq, heads, d, page, fmt, dtype, seed=case)
+    got = b.run(causal=causal, out_dtype=out_dtype)
+    b.check(got, causal)
+    for _ in range(3):                           # the same bits from run to run
+        assert torch.equal(b.run(causal=causal, out_dtype=out_dtype), got)
+
+
+@pytest.mark.parametrize("case", [2, 4, 7])
+def test_without_a_workspace_and_without_groups(case):
+    groups, hq, heads, d, page, fmt, dtype = CASES[case]
+    b = Batch(groups, hq, heads, d, page, fmt, dtype, seed=case)
+    plain = mx.mx_kv_attention(b.q.cuda(), b.cache, _i32(b.table), _i32(b.lens), _i32(b.cu), b.most)
+    assert torch.equal(b.run(ws=None), plain)
+    b.check(b.run(ws=torch.empty(64, dtype=torch.uint8, device="cuda")))
+    b.check(b.run(groups=[0], shared=[]))
+    b.check(b.run(groups=[0], shared=[], ws=None))
+
+
+@pytest.mark.parametrize("groups,shared", [
+    ([0, 5], [10 ** 9]), ([0, 5], [-7]), ([0, 5], [0]), ([1, 4], [300]), ([0, 2, 5], [300, 100]), ([2, 1, 5], [300, 300]),
+    ([-9, 2, 99], [200, 300]), ([0, 1, 2, 3, 4, 5], [300] * 5), ([4, 5], [300]), ([0, 0, 5, 5], [1, 299, 3])])
+def test_any_offsets_give_the_same_answer(groups, shared):
+    """What a call says of prefixes changes no result."""
+    c = CASES[2]
+    b = Batch([(300, [(17, 1), (200, 1), (33, 2), (64, 0), (40, 4)])], *c[1:], seed=5)
+    b.check(b.run(groups=groups, shared=shared))
+
+
+def test_rows_that_stand_in_front_of_the_prefix():
+    """A request whose rows reach back into the common tokens: less is shared."""
+    b = Batch([(256, [(4, 60), (30, 1), (2, 2)])], 4, 2, 128, 32, seed=3)
+    b.check(b.run())
+    b = Batch([(64, [(1, 65), (3, 1)])], 4, 2, 64, 32, seed=3)   # nothing stands in front of all
+    b.check(b.run())
+
+
+def test_common_tokens_that_end_inside_a_page():
+    b = Batch([(300, [(17, 1), (9, 1), (100, 2)])], 4, 2, 64, 128, seed=1)
+    b.check(b.run())
+
+
+def test_strides_outputs_and_rows_of_no_request():
+    b = Batch(CASES[4][0], 8, 2, 128, 64, seed=9)
+    T = b.q.shape[0]
+    wide = torch.randn(T + 5, 3, 8, 136, device="cuda").to(BF16)
+    q = wide[:T + 5, 1, :, :128]
+    q[:T] = b.q.cuda()
+    out = torch.full((T + 5, 8, 160), 7.0, dtype=F16, device="cuda")[..., 16:144]
+    got = mx.mx_kv_attention_shared(q, b.cache, _i32(b.table), _i32(b.lens), _i32(b.cu), b.most, _i32(b.edges), _i32(b.common),
+                                    out=out, workspace=torch.empty(
+                                        mx.kv_attention_shared_workspace_bytes(T + 5, 8, 2, 128, b.most, len(b.lens), 1),
+                                        dtype=torch.uint8, device="cuda"))
+    b.check(got[:T])
+    assert (got[T:] == 7).all()
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_masked_and_weightless_keys(many):
+    """Prefixes whose scores are far below a request's own, and far above; scores of -infinity in one
+    set or both; a page with a NaN scale in one request's own keys."""
+    n = 12 if many else 2
+    for big in (1e4, -1e4):
+        b = Batch([(128, [(20 + i, 1) for i in range(n)])], 4, 1, 64, 16, seed=7, spread=0.0)
+        b.q[:] = 0
+        b.q[..., 0] = 1.0
+        k, v, ks, vs = [t.copy() for t in b.planes]
+        lead = b.table[0, :8]
+        k[..., 0] = 0
+        k[lead, ..., 0] = 0x7E if big > 0 else 0xFE     # +-448 times the scale below
+        ks[:] = 127 + 4
+        b.planes = k, v, ks, vs
+        b.cache = mx.KVCache(*[torch.from_numpy(t).cuda() for t in b.planes], b.fmt)
+        b.check(b.run(out_dtype=F32))
+    # -infinity in the prefix alone: it weighs nothing; in both: NaN
+    for both in (False, True):
+        b = Batch([(64, [(16, 1) for i in range(n)])], 4, 1, 64, 16, seed=8, spread=0.0, dtype=F16)
+        b.q[:] = 0
+        b.q[..., 0] = -60000.0
+        k, v, ks, vs = [t.copy() for t in b.planes]
+        k[..., 0] = 0
+        ks[:] = 127
+        lead = b.table[0, :4]
+        where = np.arange(len(ks)) if both else lead
+        k[where, ..., 0] = 0x7E
+        ks[where] = 250
+        b.planes = k, v, ks, vs
+        b.cache = mx.KVCache(*[torch.from_numpy(t).cuda() for t in b.planes], b.fmt)
+        got = b.run(out_dtype=F32)
+        if both:
+            assert torch.isnan(got).all()
+        else:
+            w = mx.mx_kv_attention(b.q.cuda(), b.cache, _i32(b.table[:, 4:]), _i32([16] * n), _i32(b.cu), 1, out_dtype=F32)
+            assert torch.isfinite(got).all() and ((got - w).abs() <= 2.0 ** -10 * w.abs().max()).all()
+    # a NaN page of one request's own
+    b = Batch([(64, [(16, 1) for i in range(n)])], 4, 1, 64, 16, seed=8)
+    k, v, ks, vs = [t.copy() for t in b.planes]
+    ks[b.table[1, 4]] = 255
+    b.cache = mx.KVCache(*[torch.from_numpy(t).cuda() for t in (k, v, ks, vs)], b.fmt)
+    got = b.run(out_dtype=F32)
+    assert torch.isnan(got[1]).all() and torch.isfinite(got[[i for i in range(n) if i != 1]]).all()
+    assert mx.mx_last_error() == 0
+
+
+def test_a_page_outside_the_cache():
+    b = Batch([(128, [(20, 1), (9, 1), (30, 1)])], 4, 2, 64, 16, seed=2)
+    right = b.table[0, 2]
+    b.table[:, 2] = 10 ** 6                      # in the prefix
+    assert torch.isnan(b.run(out_dtype=F32)).all()
+    b.table[1:, 2] = right                       # in one row alone: what the rows agree on is shared
+    got = b.run(out_dtype=F32)
+    assert torch.isnan(got[0]).all() and torch.isfinite(got[1:]).all()
+    b.table[0, 2] = right
+    b.table[2, 8] = -1
+    got = b.run(out_dtype=F32)
+    assert torch.isnan(got[2]).all() and torch.isfinite(got[:2]).all()
+
+
+def test_captured_and_on_another_stream():
+    b = Batch(CASES[6][0], 4, 1, 128, 16, mx.E5M2, seed=6)
+    args = (b.q.cuda(), b.cache, _i32(b.table), _i32(b.lens), _i32(b.cu), b.most, _i32(b.edges), _i32(b.common))
+    ws = b.workspace()
+    want = mx.mx_kv_attention_shared(*args, workspace=ws)
+    b.check(want)
+    out = torch.empty_like(want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        ws.fill_(255)                            # what stands in a workspace does not matter
+        mx.mx_kv_attention_shared(*args, out=out, workspace=ws)
+    side.synchronize()
+    assert torch.equal(out, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mx.mx_kv_attention_shared(*args, out=out, workspace=ws)
+        mx.mx_kv_attention_shared(*args, out=out, workspace=ws)
+    for fill in (0, 255):
+        ws.fill_(fill)
+        out.zero_()
+        graph.replay()
+        graph.replay()
+        assert torch.equal(out, want)
+    assert mx.mx_last_error() == 0
+
+
+def test_a_workspace_of_exactly_the_size_at_a_16_byte_boundary():
+    b = Batch(CASES[4][0], 8, 2, 128, 64, seed=4)
+    n = b.workspace().numel()
+    room = torch.full((n + 16 + 64,), 0x5A, dtype=torch.uint8, device="cuda")
+    for at in (0, 16):
+        room.fill_(0x5A)
+        b.check(b.run(ws=room[at:at + n]))
+        assert (room[:at] == 0x5A).all() and (room[at + n:] == 0x5A).all()
+
+
+@pytest.mark.parametrize("requests,q", [(64, 1), (13, 4)])
+def test_serving_sizes(requests, q):
+    b = Batch([(2048, [(q + (37 * i) % 256, q) for i in range(requests)])], 32, 8, 128, 64, seed=11)
+    b.check(b.run())
