@@ -561,25 +561,45 @@ def flash_attention_workspace_bytes(BH: int, Lq: int, Lk: int, d: int) -> int:
     return int(lib().flash_attention_workspace_bytes(BH, Lq, Lk, d))
 
 
-def _same_gpu(*tensors):
+def _one_gpu(*tensors) -> int:
     """A call's operands lie in the current GPU's memory, on whose stream it
-    runs."""
+    runs; that GPU."""
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and not (t.is_cuda and
-                                  t.get_device() == torch.cuda.current_device()):
-            raise ValueError("operands must be CUDA tensors of the current GPU")
+        if t is not None and t.get_device() != dev:
+            raise ValueError("operands must be CUDA tensors of one GPU")
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("operands must be CUDA tensors of the current GPU")
+    return dev
+
+
+def _empty(dev: int):
+    """_allocator on the current GPU."""
+    if _direct_empty is not None and \
+            not torch.are_deterministic_algorithms_enabled():
+        return _direct_empty
+    return lambda shape, strides, dtype: torch.empty_strided(
+        shape, strides, dtype=dtype, device=dev)
+
+
+def _stream_on(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None \
+        else _stream(stream)
 
 
 def _matrix(t: torch.Tensor, name: str, rows=None, cols=None):
     """Checks a 2-D floating operand; its type's code, address and row stride."""
-    dt = _KV_OUT_DTYPES.get(t.dtype)
-    if dt is None or t.dim() != 2:
+    dt, shape, stride = _KV_OUT_DTYPES.get(t.dtype), t.shape, t.stride()
+    if dt is None or len(shape) != 2:
         raise ValueError(f"{name} must be a 2-D fp32, fp16 or bf16 tensor")
-    if rows is not None and tuple(t.shape) != (rows, cols):
+    if rows is not None and (shape[0] != rows or shape[1] != cols):
         raise ValueError(f"{name} must be {rows} x {cols}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if stride[1] != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have a unit inner stride")
-    return dt, t.data_ptr() if t.numel() else None, t.stride(0)
+    return dt, t.data_ptr(), stride[0]
+
+
+_MX_A_FMTS = (E4M3, E2M1, E5M2)
 
 
 def mx_rmsnorm_quantize(X: torch.Tensor, weight: torch.Tensor, fmt: int,
@@ -595,45 +615,57 @@ def mx_rmsnorm_quantize(X: torch.Tensor, weight: torch.Tensor, fmt: int,
     itself."""
     xdt, px, ldx = _matrix(X, "X")
     rows, K = X.shape
-    if weight.dtype != torch.float32 or weight.dim() != 1 or \
+    if weight.dtype is not torch.float32 or weight.dim() != 1 or \
             not weight.is_contiguous() or weight.numel() != K:
         raise ValueError("weight must be K contiguous float32 values")
-    _same_gpu(X, weight, residual, residual_out)
+    dev = _one_gpu(X, weight, residual, residual_out)
+    empty = _empty(dev)
     rdt, pr, ldr, po, ldo = 0, None, 0, None, 0
     if residual is not None:
         rdt, pr, ldr = _matrix(residual, "residual", rows, K)
         if residual_out is None:
-            residual_out = torch.empty((rows, K), dtype=residual.dtype,
-                                       device=X.device)
-        odt, po, ldo = _matrix(residual_out, "residual_out", rows, K)
-        if odt != rdt:
-            raise ValueError("residual_out must be of residual's type")
+            residual_out = empty((rows, K), (K, 1), residual.dtype)
+            po, ldo = residual_out.data_ptr(), K
+        else:
+            odt, po, ldo = _matrix(residual_out, "residual_out", rows, K)
+            if odt != rdt:
+                raise ValueError("residual_out must be of residual's type")
     elif residual_out is not None:
         raise ValueError("there is no residual to write")
     if out is None:
-        out = empty_mx(fmt, rows, K, X.device)
-    _check_mx(out, "out", fmt, rows, K)
-    _same_gpu(out.data, out.scales)
-    ct = out.c()
+        if fmt not in _MX_A_FMTS or K % 32:
+            raise ValueError("fmt must be E4M3, E5M2 or E2M1, K a multiple of 32")
+        one, u8 = (1,), torch.uint8
+        out = MXTensor(empty((data_bytes(fmt, rows, K),), one, u8),
+                       empty((scale_bytes(rows, K),), one, u8), fmt, rows, K)
+    else:
+        _check_mx(out, "out", fmt, rows, K)
+        _one_gpu(X, out.data, out.scales)
+    ct = CMXTensor(out.data.data_ptr(), out.scales.data_ptr(), fmt, rows, K)
     _check(lib().mx_rmsnorm_quantize(
         px, xdt, ldx, pr, rdt, ldr, weight.data_ptr(), eps, po, ldo,
-        ctypes.byref(ct), _stream(stream)), "mx_rmsnorm_quantize")
+        ctypes.byref(ct), _stream_on(stream, dev)), "mx_rmsnorm_quantize")
     return out, residual_out
 
 
 def mx_dequantize(A: MXTensor, out_dtype=torch.float32,
                   out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The values of an MX tensor of any format as an outer x K matrix."""
-    dt = _out_code(out_dtype, (torch.float32, torch.bfloat16, torch.float16))
+    dt = _KV_OUT_DTYPES.get(out_dtype)
+    if dt is None:
+        raise ValueError("out_dtype must be float32, bfloat16 or float16, not "
+                         f"{out_dtype}")
     _check_mx(A, "A")
-    _same_gpu(A.data, A.scales, out)
+    dev = _one_gpu(A.data, A.scales, out)
+    rows, K = A.outer, A.K
     if out is None:
-        out = torch.empty((A.outer, A.K), dtype=out_dtype, device=A.data.device)
-    _check_out(out, A.outer, A.K, out_dtype)
+        out, ld = _empty(dev)((rows, K), (K, 1), out_dtype), K
+    else:
+        _check_out(out, rows, K, out_dtype)
+        ld = out.stride(0)
     ca = A.c()
-    _check(lib().mx_dequantize(ctypes.byref(ca),
-                               out.data_ptr() if out.numel() else None, dt,
-                               out.stride(0), _stream(stream)), "mx_dequantize")
+    _check(lib().mx_dequantize(ctypes.byref(ca), out.data_ptr(), dt, ld,
+                               _stream_on(stream, dev)), "mx_dequantize")
     return out
 
 
@@ -679,14 +711,19 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "parts",
     return Rope(torch.tensor(turns, dtype=torch.int64, device=device), by)
 
 
-def _rope_operand(x: torch.Tensor, y: torch.Tensor, name: str) -> CRopeOperand:
+def _rope_operand(x: torch.Tensor, y: torch.Tensor | None, name: str, empty):
+    """The struct of a tensor to turn, and its output."""
     dt, shape, xt, xh = _kv_tensor(x, name)
-    ydt, yshape, yt, yh = _kv_tensor(y, "out")
-    if ydt != dt or yshape != shape:
-        raise ValueError(f"out must have {name}'s shape and type")
-    return CRopeOperand(x.data_ptr() if x.numel() else None,
-                        y.data_ptr() if y.numel() else None, shape[1],
-                        xt, xh, yt, yh)
+    if y is None:
+        _, h, d = shape
+        yt, yh = h * d, d
+        y = empty(tuple(shape), (yt, yh, 1), x.dtype)
+    else:
+        ydt, yshape, yt, yh = _kv_tensor(y, "out")
+        if ydt != dt or yshape != shape:
+            raise ValueError(f"out must have {name}'s shape and type")
+    return dt, y, CRopeOperand(x.data_ptr(), y.data_ptr(), shape[1], xt, xh, yt,
+                               yh)
 
 
 def mx_rope(Q: torch.Tensor, K: torch.Tensor | None, rope: Rope,
@@ -702,12 +739,22 @@ def mx_rope(Q: torch.Tensor, K: torch.Tensor | None, rope: Rope,
     gradients.  out: (Q's, K's) outputs, which may be Q and K themselves.
     Returns both."""
     freq = rope.freq
-    if freq.dtype != torch.int64 or freq.dim() != 1 or not freq.is_contiguous():
+    if freq.dtype is not torch.int64 or freq.dim() != 1 or \
+            not freq.is_contiguous():
         raise ValueError("rope.freq must be a contiguous 1-D int64 tensor")
+    oq, ok = (None, None) if out is None else out
+    if out is not None and (oq is None or (ok is None) != (K is None)):
+        raise ValueError("out must hold an output for each of Q and K")
+    dev = _one_gpu(Q, K, freq, positions, lens, cu, oq, ok)
+    empty = _empty(dev)
+    dt, oq, a = _rope_operand(Q, oq, "Q", empty)
     T, _, d = Q.shape
-    if K is not None and (K.dtype != Q.dtype or K.shape[0] != T or
-                          K.shape[2] != d):
-        raise ValueError("Q and K must have one type, tokens and d")
+    b = None
+    if K is not None:
+        kdt, ok, cb = _rope_operand(K, ok, "K", empty)
+        if kdt != dt or K.shape[0] != T or K.shape[2] != d:
+            raise ValueError("Q and K must have one type, tokens and d")
+        b = ctypes.byref(cb)
     requests, p_pos, p_lens, p_cu = 0, None, None, None
     if positions is not None:
         p_pos = _int32(positions, "positions", T)
@@ -716,22 +763,10 @@ def mx_rope(Q: torch.Tensor, K: torch.Tensor | None, rope: Rope,
     else:
         requests = lens.shape[0]
         p_lens, p_cu = _int32(lens, "lens"), _int32(cu, "cu", requests + 1)
-    if out is None:
-        empty = _allocator(Q)
-        out = tuple(None if t is None else
-                    empty((T, t.shape[1], d), (t.shape[1] * d, d, 1), t.dtype)
-                    for t in (Q, K))
-    oq, ok = out
-    _same_gpu(Q, K, freq, positions, lens, cu, oq, ok)
-    a = _rope_operand(Q, oq, "Q")
-    b = None
-    if K is not None:
-        b = ctypes.byref(_rope_operand(K, ok, "K"))
     _check(lib().mx_rope(
-        ctypes.byref(a), b, _KV_DTYPES[Q.dtype], T, d, freq.data_ptr(),
-        2 * freq.numel(), rope.factor, p_pos, p_lens, p_cu, requests,
-        1 if neighbours else 0, 1 if backward else 0, _stream(stream)),
-        "mx_rope")
+        ctypes.byref(a), b, dt, T, d, freq.data_ptr(), 2 * freq.shape[0],
+        rope.factor, p_pos, p_lens, p_cu, requests, 1 if neighbours else 0,
+        1 if backward else 0, _stream_on(stream, dev)), "mx_rope")
     return oq, ok
 
 
@@ -962,17 +997,18 @@ def mx_kv_fork(lens: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
     p_dst, p_keep = _int32(dst, "dst", n), _int32(keep, "keep", n)
     p_refs = _int32(refs, "refs")
     p_table, stride, width = _table(table, B)
+    dev = _one_gpu(lens, src, dst, keep, table, refs)
     if out is None:
-        empty = _allocator(lens)
+        empty = _empty(dev)
         out = KVCut(empty((B,), (1,), _i32), empty((1,), (1,), _i32))
     else:
         _int32(out.lens, "out.lens", B)
         _int32(out.counts, "out.counts", 1)
-    _same_gpu(lens, src, dst, keep, table, refs, out.lens, out.counts)
+        _one_gpu(lens, out.lens, out.counts)
     _check(lib().mx_kv_fork(
         p_lens, B, p_src, p_dst, p_keep, n, p_table, stride, width, p_refs,
         refs.numel(), page, out.lens.data_ptr(), out.counts.data_ptr(),
-        _stream(stream)), "mx_kv_fork")
+        _stream_on(stream, dev)), "mx_kv_fork")
     return out
 
 
@@ -993,8 +1029,9 @@ def mx_kv_own(cache: KVCache, lens: torch.Tensor, new_tokens: torch.Tensor,
     p_count = _int32(count, "count", 1)
     p_refs = _int32(refs, "refs", c.pages)
     p_table, stride, width = _table(table, B)
+    dev = _one_gpu(lens, cache.k, new_tokens, table, stack, count, refs)
     if out is None:
-        one, empty = (1,), _allocator(lens)
+        one, empty = (1,), _empty(dev)
         out = KVOwn(empty((B,), one, _i32), empty((B, 3), (3, 1), _i32),
                     empty((2,), one, _i32))
     else:
@@ -1003,12 +1040,11 @@ def mx_kv_own(cache: KVCache, lens: torch.Tensor, new_tokens: torch.Tensor,
         if out.copies.dtype is not _i32 or not out.copies.is_contiguous() or \
                 out.copies.numel() < 3 * B:
             raise ValueError("out.copies must hold 3 int32 values a request")
-    _same_gpu(cache.k, lens, new_tokens, table, stack, count, refs,
-              out.new_tokens, out.copies, out.counts)
+        _one_gpu(lens, out.new_tokens, out.copies, out.counts)
     _check(lib().mx_kv_own(
         ctypes.byref(c), p_lens, p_new, B, p_table, stride, width, p_stack,
         stack.numel(), p_count, p_refs, out.new_tokens.data_ptr(),
-        out.copies.data_ptr(), out.counts.data_ptr(), _stream(stream)),
+        out.copies.data_ptr(), out.counts.data_ptr(), _stream_on(stream, dev)),
         "mx_kv_own")
     return out
 
@@ -1026,17 +1062,18 @@ def mx_kv_release(lens: torch.Tensor, keep: torch.Tensor, table: torch.Tensor,
     p_count = _int32(count, "count", 1)
     p_refs = _int32(refs, "refs")
     p_table, stride, width = _table(table, B)
+    dev = _one_gpu(lens, keep, table, stack, count, refs)
     if out is None:
-        empty = _allocator(lens)
+        empty = _empty(dev)
         out = KVCut(empty((B,), (1,), _i32), empty((2,), (1,), _i32))
     else:
         _int32(out.lens, "out.lens", B)
         _int32(out.counts, "out.counts", 2)
-    _same_gpu(lens, keep, table, stack, count, refs, out.lens, out.counts)
+        _one_gpu(lens, out.lens, out.counts)
     _check(lib().mx_kv_release(
         p_lens, p_keep, B, p_table, stride, width, p_stack, stack.numel(),
         p_count, p_refs, refs.numel(), page, out.lens.data_ptr(),
-        out.counts.data_ptr(), _stream(stream)), "mx_kv_release")
+        out.counts.data_ptr(), _stream_on(stream, dev)), "mx_kv_release")
     return out
 
 
@@ -1171,9 +1208,10 @@ def mx_kv_attention_shared(Q: torch.Tensor, cache: KVCache, table: torch.Tensor,
     p_cu = _int32(cu, "cu", B + 1)
     p_groups, p_shared = _int32(groups, "groups"), _int32(shared, "shared", n)
     p_table, stride, width = _table(table, B)
+    dev = _one_gpu(Q, cache.k, table, lens, cu, groups, shared, out, workspace)
     if out is None:
         ot, oh = Hq * d, d
-        out = _allocator(Q)((T, Hq, d), (ot, oh, 1), out_dtype or Q.dtype)
+        out = _empty(dev)((T, Hq, d), (ot, oh, 1), out_dtype or Q.dtype)
     elif (out.shape != shape or not out.is_cuda or out.stride(2) != 1
           or (out_dtype is not None and out.dtype != out_dtype)):
         raise ValueError("out must be a CUDA tensor of Q's shape and of type "
@@ -1185,13 +1223,12 @@ def mx_kv_attention_shared(Q: torch.Tensor, cache: KVCache, table: torch.Tensor,
     if odt is None:
         raise ValueError("out_dtype must be float32, bfloat16 or float16, not "
                          f"{out.dtype}")
-    _same_gpu(Q, cache.k, table, lens, cu, groups, shared, out, workspace)
     _check(lib().mx_kv_attention_shared(
         Q.data_ptr(), dt, T, Hq, qt, qh, ctypes.byref(c), p_table, stride,
         width, p_lens, p_cu, B, max_q, p_groups, p_shared, n, out.data_ptr(),
         odt, ot, oh, 1 if causal else 0, d ** -0.5 if scale is None else scale,
         None if workspace is None else workspace.data_ptr(),
-        _nbytes(workspace), _stream(stream)), "mx_kv_attention_shared")
+        _nbytes(workspace), _stream_on(stream, dev)), "mx_kv_attention_shared")
     return out
 
 

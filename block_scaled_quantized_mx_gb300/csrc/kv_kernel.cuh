@@ -74,7 +74,8 @@ __device__ __forceinline__ auto kv_request(const KvView& v, int b) {
     // (another kernel of the same call may have written these: around L1)
     s = __ldcg(v.cu + static_cast<long long>(b) * v.cu_step);
     e = __ldcg(v.cu + static_cast<long long>(b) * v.cu_step + 1);
-    r.start = v.start ? __ldcg(v.start + b) : 0;
+    const int start = v.start ? __ldcg(v.start + b) : 0;
+    r.start = start < 0 ? 0 : (start > v.capacity ? v.capacity : start);
   } else {
     s = v.cu[b];
     e = v.cu[b + 1];

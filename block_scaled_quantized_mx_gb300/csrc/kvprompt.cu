@@ -1197,10 +1197,9 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 // chunk took 226 us instead of 219; one or four rows a thread: 219, 223.)
 constexpr int KPJ_THREADS = 256;
 constexpr int KPJ_R = 2;                       // rows of a thread
-template <int D, bool SH>
+template <int D>
 __global__ void __launch_bounds__(KPJ_THREADS)
 kv_prompt_join_kernel(const KpArgs a) {
-  if constexpr (SH) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const KpJoin* join = a.joins + blockIdx.x;
   const int live = __ldcg(&join->live);
@@ -1214,7 +1213,6 @@ kv_prompt_join_kernel(const KpArgs a) {
   const float* rest = a.ws + 2ll * blockIdx.x * PART;
   const int row0 = __ldcg(&join->row0), head = __ldcg(&join->head);
   const long long q0 = __ldcg(&join->q0);
-  const int has_state = SH ? __ldcg(&join->has_state) : 0;
   float top[KPJ_R], sum[KPJ_R], acc[KPJ_R][8];
 #pragma unroll
   for (int i = 0; i < KPJ_R; ++i) {
@@ -1252,27 +1250,174 @@ kv_prompt_join_kernel(const KpArgs a) {
     const int row = row0 + r0 + 4 * i, token = row / a.v.group;
     const long long out =
         (q0 + token) * a.o_ts + (head * a.v.group + row - token * a.v.group) * a.o_hs + col;
-    if constexpr (SH) {
-      const long long at = (q0 + token) * (static_cast<long long>(a.v.heads) * a.v.group) +
-                           head * a.v.group + row - token * a.v.group;
-      if (a.state.pass == KV_PREFIX) {
-        kv_store8(a.state.o, DT_F32, at * D + col, acc[i]);
-        if (col == 0) a.state.ml[at] = make_float2(top[i], sum[i]);
-        continue;
-      }
-      if (has_state) {
-        float wp, wo, p[8];
-        kv_join_states(__ldcg(a.state.ml + at), make_float2(top[i], sum[i]), wp, wo);
-        ld_global_cg_v8(a.state.o + at * D + col, p);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[i][e] = acc[i][e] * wo + p[e] * wp;
-        kv_store8(a.O, a.o_dtype, out, acc[i]);
-        continue;
-      }
-    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[i][e] *= inv;
     kv_store8(a.O, a.o_dtype, out, acc[i]);
+  }
+}
+
+// The same for the passes over shared prefixes, whose units may be few and their parts
+// many -- 256 rows of 8 cache heads over 152 SMs make 8 units of 20 parts -- so that a CTA
+// per CTA of the main kernel leaves most of them without work.  Here the units are listed
+// first, and the CTAs share out pieces of 8 KPJ_R x 4 rows x 64 columns, a few rows a warp;
+// or, of units of more than KPS_FEW parts, of one warp's rows, whose parts the warps share
+// and join in shared memory, in order.
+constexpr int KPS_WARPS = KPJ_THREADS / 32;
+constexpr int KPS_MAX_CTAS = 512;              // of the main kernel
+constexpr int KPS_FEW = 4;
+template <int D>
+__global__ void __launch_bounds__(KPJ_THREADS)
+kv_prompt_states_kernel(const KpArgs a, const int main_ctas) {
+  __shared__ int sm_first[KPS_MAX_CTAS];       // per CTA of the main kernel: its unit's first piece
+  __shared__ int sm_scan[KPS_WARPS];
+  __shared__ float sm_acc[KPS_WARPS][KPJ_R][32][9];
+  __shared__ float2 sm_ml[KPS_WARPS][KPJ_R][32];
+  constexpr int COLS = D / 64;
+  constexpr long long PART = KP_ROWS * (D + 2);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto rows_of = [](int parts) { return 4 * KPJ_R * (parts > KPS_FEW ? 1 : KPS_WARPS); };
+  auto pieces_of = [&](int live, int parts) { return (live + rows_of(parts) - 1) / rows_of(parts) * COLS; };
+  // ---- the units' pieces
+  int at = 0;
+  for (int c0 = 0; c0 < main_ctas; c0 += KPJ_THREADS) {
+    const int c = c0 + tid;
+    int n = 0;
+    if (c < main_ctas) {
+      const int live = __ldcg(&a.joins[c].live);
+      if (live > 0) n = pieces_of(live, __ldcg(&a.joins[c].parts));
+    }
+    int s = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xFFFFFFFFu, s, d);
+      if (lane >= d) s += u;
+    }
+    if (lane == 31) sm_scan[warp] = s;
+    __syncthreads();
+    int before = at;
+    for (int w = 0; w < KPS_WARPS; ++w) {
+      if (w < warp) before += sm_scan[w];
+      at += sm_scan[w];
+    }
+    if (c < main_ctas) sm_first[c] = before + s - n;
+    __syncthreads();
+  }
+  const int total = at;
+  for (int piece = blockIdx.x; piece < total; piece += gridDim.x) {
+    // the last unit that begins at or before it and has pieces: of equal starts the last
+    int lo = 0, hi = main_ctas - 1;
+    while (lo < hi) {
+      const int m = (lo + hi + 1) >> 1;
+      if (sm_first[m] <= piece) lo = m; else hi = m - 1;
+    }
+    const KpJoin* join = a.joins + lo;
+    const int live = __ldcg(&join->live), n = __ldcg(&join->parts);
+    const int in = piece - sm_first[lo];
+    const bool many = n > KPS_FEW;
+    const int row0 = __ldcg(&join->row0), head = __ldcg(&join->head);
+    const long long q0 = __ldcg(&join->q0);
+    const bool to_state = a.state.pass == KV_PREFIX;
+    const bool from_state = !to_state && __ldcg(&join->has_state);
+    const int r0 = in / COLS * rows_of(n) + (many ? 0 : 4 * KPJ_R * warp) + (lane & 3);
+    const int col = 64 * (in % COLS) + 8 * (lane >> 2);
+    const float* first = a.ws + __ldcg(&join->first_slot) * PART;
+    const float* rest = a.ws + 2ll * lo * PART;
+    float top[KPJ_R], sum[KPJ_R], acc[KPJ_R][8];
+#pragma unroll
+    for (int i = 0; i < KPJ_R; ++i) {
+      top[i] = -INFINITY;
+      sum[i] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[i][e] = 0.0f;
+    }
+#pragma unroll 2
+    for (int p = many ? warp : 0; p < n; p += many ? KPS_WARPS : 1) {
+      const float* part = p == 0 ? first : rest + 2 * p * PART;
+      float mp[KPJ_R], lp[KPJ_R], v[KPJ_R][8];
+#pragma unroll
+      for (int i = 0; i < KPJ_R; ++i) {
+        const int r = min(r0 + 4 * i, live - 1);         // (a row too many is not stored)
+        mp[i] = __ldcg(part + KP_ROWS * D + r);
+        lp[i] = __ldcg(part + KP_ROWS * (D + 1) + r);
+        ld_global_cg_v8(part + (col / 8 * KP_ROWS + r) * 8, v[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < KPJ_R; ++i) {
+        const float t = fmaxf(top[i], mp[i]);
+        const float before = top[i] == t ? 1.0f : ex2_approx(top[i] - t);
+        const float w = mp[i] == t ? 1.0f : ex2_approx(mp[i] - t);
+        top[i] = t;
+        sum[i] = fmaf(w, lp[i], sum[i] * before);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[i][e] = fmaf(w, v[i][e], acc[i][e] * before);
+      }
+    }
+    // N columns from `col` of the unit's row r, as (t, l, o) has them
+    auto finish = [&](int r, int col, float t, float l, auto& o) {
+      constexpr int N = sizeof(o) / sizeof(float);
+      const int row = row0 + r, token = row / a.v.group;
+      const int qh = head * a.v.group + row - token * a.v.group;
+      const long long state = (q0 + token) * (static_cast<long long>(a.v.heads) * a.v.group) + qh;
+      float* so = a.state.o + state * D + col;
+      float wp = 0.0f, wo = 1.0f;
+      if (to_state) {
+        if (col == 0) a.state.ml[state] = make_float2(t, l);
+      } else if (from_state) {
+        kv_join_states(__ldcg(a.state.ml + state), make_float2(t, l), wp, wo);
+      } else {
+        wo = kv_inverse(l, t != -INFINITY);
+      }
+#pragma unroll
+      for (int e = 0; e < N; e += 2) {
+        float2 v = make_float2(o[e] * wo, o[e + 1] * wo);
+        if (from_state) {
+          const float2 p = __ldcg(reinterpret_cast<const float2*>(so + e));
+          v.x = fmaf(p.x, wp, v.x);
+          v.y = fmaf(p.y, wp, v.y);
+        }
+        const long long out = (q0 + token) * a.o_ts + qh * a.o_hs + col + e;
+        if (to_state)
+          *reinterpret_cast<float2*>(so + e) = v;
+        else if (a.o_dtype == DT_F32)
+          *reinterpret_cast<float2*>(static_cast<float*>(a.O) + out) = v;
+        else
+          *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.O) + out) =
+              a.o_dtype == DT_BF16 ? cvt_bf16x2(v.x, v.y) : cvt_f16x2(v.x, v.y);
+      }
+    };
+    if (!many) {
+#pragma unroll
+      for (int i = 0; i < KPJ_R; ++i)
+        if (r0 + 4 * i < live) finish(r0 + 4 * i, col, top[i], sum[i], acc[i]);
+      continue;
+    }
+    __syncthreads();                         // the shared arrays are free
+#pragma unroll
+    for (int i = 0; i < KPJ_R; ++i) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sm_acc[warp][i][lane][e] = acc[i][e];
+      sm_ml[warp][i][lane] = make_float2(top[i], sum[i]);
+    }
+    __syncthreads();
+    // a thread takes two columns of the 8 of one lane
+    static_assert(KPJ_THREADS == KPJ_R * 32 * 4, "two of eight columns a thread");
+    const int i = tid >> 7, of = (tid >> 2) & 31, e = 2 * (tid & 3);
+    const int r = in / COLS * rows_of(n) + (of & 3) + 4 * i;
+    if (r >= live) continue;
+    float t = -INFINITY, l = 0.0f, o[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < KPS_WARPS; ++w) t = fmaxf(t, sm_ml[w][i][of].x);
+#pragma unroll
+    for (int w = 0; w < KPS_WARPS; ++w) {
+      const float2 ml = sm_ml[w][i][of];
+      const float wgt = ml.x == t ? 1.0f : ex2_approx(ml.x - t);
+      l = fmaf(wgt, ml.y, l);
+      o[0] = fmaf(wgt, sm_acc[w][i][of][e], o[0]);
+      o[1] = fmaf(wgt, sm_acc[w][i][of][e + 1], o[1]);
+    }
+    finish(r, 64 * (in % COLS) + 8 * (of >> 2) + e, t, l, o);
   }
 }
 
@@ -1314,11 +1459,15 @@ cudaError_t kp_run(const CUtensorMap& tk, const CUtensorMap& tv, const KpArgs& a
     e = cudaGetLastError();
     if (e != cudaSuccess || a.ws == nullptr) return e;
   }
-  cfg.gridDim = dim3(sms, KP_ROWS * (D / 8) / (KPJ_THREADS * KPJ_R));
   cfg.blockDim = dim3(KPJ_THREADS);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_prompt_join_kernel<D, SH>, a);
+  if constexpr (SH) {
+    cfg.gridDim = dim3(4 * sms);
+    return cudaLaunchKernelEx(&cfg, kv_prompt_states_kernel<D>, a, sms);
+  }
+  cfg.gridDim = dim3(sms, KP_ROWS * (D / 8) / (KPJ_THREADS * KPJ_R));
+  return cudaLaunchKernelEx(&cfg, kv_prompt_join_kernel<D>, a);
 }
 
 template <bool SH>
@@ -1363,7 +1512,7 @@ cudaError_t launch_kv_prompt(const KvAttn& q, int sms, const KvPassArgs* pass, c
     a.joins = reinterpret_cast<KpJoin*>(ws + static_cast<int64_t>(sms) * 2 * KP_ROWS * (c.d + 2) * 4);
   }
   if (pass) {
-    if (a.ws == nullptr) return cudaErrorInvalidValue;   // the caller has seen to it
+    if (a.ws == nullptr || sms > KPS_MAX_CTAS) return cudaErrorInvalidValue;
     a.v.start = pass->start;
     a.v.row_of = pass->row_of;
     a.v.cu_step = pass->cu_step;

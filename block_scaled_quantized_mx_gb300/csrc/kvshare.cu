@@ -29,12 +29,13 @@ namespace mxk {
 
 namespace {
 
-constexpr int SH_THREADS = 512;
+constexpr int SH_THREADS = 1024;
 constexpr int SH_WARPS = SH_THREADS / 32;
 constexpr int SH_CLUSTER = 8;
 constexpr int SH_MAX_REQUESTS = 16384;
-constexpr int SH_LANES = 8;                 // lanes that look after one request's row
-constexpr int SH_BATCH = 4;                 // table entries of a lane on their way together
+constexpr int SH_ROWS = 4;                  // requests that a warp looks after together,
+constexpr int SH_BATCH = 2;                 // with as many table entries of each a lane
+constexpr int SH_SPAN = 32 * SH_BATCH;      // entries of a row at once
 constexpr int SH_SMEM_FREE = 48 * 1024;     // shared memory that a launch gets unasked
 
 struct ShareArgs {
@@ -102,8 +103,7 @@ __global__ void __launch_bounds__(SH_THREADS) kv_release_kernel(const ShareArgs 
   extern __shared__ int sm_req[];           // per request: tokens before and after, pages freed
   __shared__ int sm_scan[SH_WARPS];
   __shared__ long long sm_total;
-  const int tid = threadIdx.x, lane = tid & 31, sub = lane & (SH_LANES - 1);
-  const unsigned group = ((1u << SH_LANES) - 1u) << (lane & ~(SH_LANES - 1));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x, ctas = gridDim.x, share = share_of(a.requests, ctas);
   const int first = min(a.requests, rank * share), B = min(share, a.requests - first);
   int* sm_len = sm_req;
@@ -118,53 +118,79 @@ __global__ void __launch_bounds__(SH_THREADS) kv_release_kernel(const ShareArgs 
     sm_rank[b] = 0;
   }
   __syncthreads();
-  // f(request, its row from the first entry that it loses, their number), by SH_LANES lanes
+  // A warp's requests, SH_ROWS at a time, SH_SPAN entries of each: f(u, b, entry, page) for
+  // each of them, page being -1 behind a row's last lost entry.  Neighbours, which often
+  // end together, go to different warps.  Where that is all that the warp has, the
+  // entries are read once and stay in registers over the steps.
+  int page[SH_ROWS][SH_BATCH];
+  bool kept = false;
   auto each = [&](auto f) {
-    for (int b = tid / SH_LANES; b < B; b += SH_THREADS / SH_LANES) {
-      const long long j0 = share_blocks(sm_keep[b], a.page_shift, a.width);
-      const int n = static_cast<int>(share_blocks(sm_len[b], a.page_shift, a.width) - j0);
-      if (n > 0) f(b, a.table + static_cast<long long>(first + b) * a.table_stride + j0, n);
-    }
-  };
-  // f(entry, page) for the lane's pages of such a row, several loads together
-  auto pages_of = [&](int* row, int n, auto f) {
-    for (int k0 = sub; k0 < n; k0 += SH_LANES * SH_BATCH) {
-      int page[SH_BATCH];
+    for (int base = warp; base < B; base += SH_WARPS * SH_ROWS) {
+      int b[SH_ROWS], n[SH_ROWS], most = 0;
+      int* row[SH_ROWS];
 #pragma unroll
-      for (int i = 0; i < SH_BATCH; ++i) {
-        const int k = k0 + SH_LANES * i;
-        page[i] = k < n ? row[k] : -1;
+      for (int u = 0; u < SH_ROWS; ++u) {
+        b[u] = base + u * SH_WARPS;
+        n[u] = 0;
+        row[u] = nullptr;
+        if (b[u] < B) {
+          const long long j0 = share_blocks(sm_keep[b[u]], a.page_shift, a.width);
+          n[u] = static_cast<int>(share_blocks(sm_len[b[u]], a.page_shift, a.width) - j0);
+          row[u] = a.table + static_cast<long long>(first + b[u]) * a.table_stride + j0;
+        }
+        most = max(most, n[u]);
       }
+      const bool all = B <= SH_WARPS * SH_ROWS && most <= SH_SPAN;
+      for (int k0 = 0; k0 < most; k0 += SH_SPAN) {
+        if (!(all && kept)) {
 #pragma unroll
-      for (int i = 0; i < SH_BATCH; ++i) f(row + k0 + SH_LANES * i, page[i]);
+          for (int u = 0; u < SH_ROWS; ++u)
+#pragma unroll
+            for (int i = 0; i < SH_BATCH; ++i) {
+              const int k = k0 + 32 * i + lane;
+              page[u][i] = k < n[u] ? row[u][k] : -1;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < SH_ROWS; ++u)
+          if (k0 < n[u]) f(u, b[u], row[u] + k0);
+      }
+      kept = true;
     }
   };
-  each([&](int, int* row, int n) {
-    pages_of(row, n, [&](int*, int page) {
-      if (page >= 0 && page < a.pages) atomicSub(a.refs + page, 1);
-    });
-  });
-  share_sync();
-  each([&](int b, int* row, int n) {
-    pages_of(row, n, [&](int*, int page) {
-      if (page >= 0 && page < a.pages && __ldcg(a.refs + page) < 0)
-        atomicMin(a.refs + page, -2 - (first + b));
-    });
-  });
-  share_sync();
-  each([&](int b, int* row, int n) {
-    int mine = 0;
-    pages_of(row, n, [&](int* at, int page) {
-      if (page < 0) return;
-      const int bid = -2 - (first + b);
-      if (page < a.pages && atomicCAS(a.refs + page, bid, 0) == bid)
-        ++mine;
-      else
-        *at = -1;                           // others hold it, or free it
-    });
+  auto held = [&](int p) { return p >= 0 && p < a.pages; };
+  each([&](int u, int, int*) {
 #pragma unroll
-    for (int d = SH_LANES / 2; d > 0; d >>= 1) mine += __shfl_xor_sync(group, mine, d);
-    if (sub == 0) sm_rank[b] = mine;
+    for (int i = 0; i < SH_BATCH; ++i)
+      if (held(page[u][i])) atomicSub(a.refs + page[u][i], 1);
+  });
+  share_sync();
+  each([&](int u, int b, int*) {
+    int refs[SH_BATCH];
+#pragma unroll
+    for (int i = 0; i < SH_BATCH; ++i) refs[i] = held(page[u][i]) ? __ldcg(a.refs + page[u][i]) : 0;
+#pragma unroll
+    for (int i = 0; i < SH_BATCH; ++i)
+      if (refs[i] < 0) atomicMin(a.refs + page[u][i], -2 - (first + b));
+  });
+  share_sync();
+  each([&](int u, int b, int* row) {
+    int was[SH_BATCH], mine = 0;
+    const int bid = -2 - (first + b);
+#pragma unroll
+    for (int i = 0; i < SH_BATCH; ++i) was[i] = held(page[u][i]) ? atomicCAS(a.refs + page[u][i], bid, 0) : 0;
+#pragma unroll
+    for (int i = 0; i < SH_BATCH; ++i) {
+      if (page[u][i] < 0) continue;
+      if (was[i] == bid) {
+        ++mine;
+      } else {
+        row[32 * i + lane] = -1;            // others hold it, or free it
+        page[u][i] = -1;
+      }
+    }
+    mine = __reduce_add_sync(0xFFFFFFFFu, mine);
+    if (lane == 0) sm_rank[b] += mine;
   });
   __syncthreads();
   const int per = (B + SH_THREADS - 1) / SH_THREADS;
@@ -199,26 +225,21 @@ __global__ void __launch_bounds__(SH_THREADS) kv_release_kernel(const ShareArgs 
     a.counts_out[1] = static_cast<int>(n < a.stack_size ? 0 : n - a.stack_size);
   }
   const long long top = count + total - 1 - before;
-  each([&](int b, int* row, int n) {
+  each([&](int u, int b, int* row) {
     int i_th = sm_rank[b];
-    for (int k0 = 0; k0 < n; k0 += SH_LANES * SH_BATCH) {
-      int page[SH_BATCH];
 #pragma unroll
-      for (int i = 0; i < SH_BATCH; ++i) {
-        const int k = k0 + SH_LANES * i + sub;
-        page[i] = k < n ? row[k] : -1;
+    for (int i = 0; i < SH_BATCH; ++i) {
+      const unsigned have = __ballot_sync(0xFFFFFFFFu, page[u][i] >= 0);
+      if (page[u][i] >= 0) {
+        const long long to = top - (i_th + __popc(have & ((1u << lane) - 1u)));
+        if (to < a.stack_size) a.stack[to] = page[u][i];
+        row[32 * i + lane] = -1;
       }
-#pragma unroll
-      for (int i = 0; i < SH_BATCH; ++i) {
-        const unsigned have = __ballot_sync(group, page[i] >= 0) & group;
-        if (page[i] >= 0) {
-          const long long to = top - (i_th + __popc(have & ((1u << lane) - 1u)));
-          if (to < a.stack_size) a.stack[to] = page[i];
-          row[k0 + SH_LANES * i + sub] = -1;
-        }
-        i_th += __popc(have);
-      }
+      i_th += __popc(have);
     }
+    __syncwarp();
+    if (lane == 0) sm_rank[b] = i_th;       // (the row may go on)
+    __syncwarp();
   });
   __syncwarp();
   if (ctas > 1) cluster_wait();             // nobody reads this CTA's total any more
@@ -262,21 +283,36 @@ __global__ void __launch_bounds__(SH_THREADS) kv_fork_kernel(const ShareArgs a) 
     __syncthreads();
     if (tid == 0) a.counts_out[0] = a.forks - sm_served;
   }
-  for (int b = warp; b < B; b += SH_WARPS) {
-    const int i = sm_claim[first + b];
-    if (i == NONE) continue;
-    const int n = static_cast<int>(share_blocks(sm_n[b], a.page_shift, a.width));
-    const int* from = a.table + static_cast<long long>(a.src[i]) * a.table_stride;
-    int* to = a.table + static_cast<long long>(first + b) * a.table_stride;
-    for (int k0 = lane; k0 < n; k0 += 32 * SH_BATCH) {
-      int page[SH_BATCH];
+  for (int base = warp; base < B; base += SH_WARPS * SH_ROWS) {
+    int n[SH_ROWS], most = 0;
+    const int* from[SH_ROWS];
+    int* to[SH_ROWS];
 #pragma unroll
-      for (int u = 0; u < SH_BATCH; ++u) page[u] = k0 + 32 * u < n ? from[k0 + 32 * u] : -1;
-#pragma unroll
-      for (int u = 0; u < SH_BATCH; ++u) {
-        if (k0 + 32 * u < n) to[k0 + 32 * u] = page[u];
-        if (page[u] >= 0 && page[u] < a.pages) atomicAdd(a.refs + page[u], 1);
+    for (int u = 0; u < SH_ROWS; ++u) {
+      const int b = base + u * SH_WARPS;
+      const int i = b < B ? sm_claim[first + b] : NONE;
+      n[u] = 0;
+      from[u] = to[u] = nullptr;
+      if (i != NONE) {
+        n[u] = static_cast<int>(share_blocks(sm_n[b], a.page_shift, a.width));
+        from[u] = a.table + static_cast<long long>(a.src[i]) * a.table_stride;
+        to[u] = a.table + static_cast<long long>(first + b) * a.table_stride;
       }
+      most = max(most, n[u]);
+    }
+    for (int k0 = lane; k0 < most; k0 += SH_SPAN) {
+      int page[SH_ROWS][SH_BATCH];
+#pragma unroll
+      for (int u = 0; u < SH_ROWS; ++u)
+#pragma unroll
+        for (int i = 0; i < SH_BATCH; ++i) page[u][i] = k0 + 32 * i < n[u] ? from[u][k0 + 32 * i] : -1;
+#pragma unroll
+      for (int u = 0; u < SH_ROWS; ++u)
+#pragma unroll
+        for (int i = 0; i < SH_BATCH; ++i) {
+          if (k0 + 32 * i < n[u]) to[u][k0 + 32 * i] = page[u][i];
+          if (page[u][i] >= 0 && page[u][i] < a.pages) atomicAdd(a.refs + page[u][i], 1);
+        }
     }
   }
 }
@@ -442,9 +478,9 @@ cudaError_t launch_share(void (*kern)(const ShareArgs), const ShareArgs& a, int 
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-// One CTA where its lanes have a request each at once: a cluster's barriers
+// One CTA where its warps look after all requests at once: a cluster's barriers
 // take longer than sharing out saves.
-int share_ctas(int64_t requests) { return requests <= SH_THREADS / SH_LANES ? 1 : SH_CLUSTER; }
+int share_ctas(int64_t requests) { return requests <= SH_WARPS * SH_ROWS ? 1 : SH_CLUSTER; }
 
 }  // namespace
 

@@ -24,10 +24,9 @@ namespace mxk {
 
 namespace {
 
-constexpr int RP_THREADS = 256;
-constexpr int RP_MOST_TOKENS = 4;           // of a CTA
-constexpr int RP_BATCH = 4;                 // units whose loads are in flight together
-constexpr int RP_MOST_ROT = 512;
+constexpr int RP_MOST_THREADS = 512;
+constexpr int RP_TOKENS = 4;                // of a thread, where there are many
+constexpr int RP_SMEM = 32768;              // cosines and sines of a CTA at the most
 
 // The position of token t, found by a whole warp; false: it belongs to no request.
 __device__ __forceinline__ bool rope_position(const RopeCall& c, long long t, int lane, int& pos) {
@@ -53,59 +52,69 @@ __device__ __forceinline__ uint32_t pack16x2(float lo, float hi, int bf16) {
   return bf16 ? cvt_bf16x2(lo, hi) : cvt_f16x2(lo, hi);
 }
 
-// A unit is two chunks of 8 values of one head: turned, (8 u, 8 u + rot / 2) or
-// 16 consecutive; or behind them 16 (or the last 8) that go through.
-struct RopeUnit {
-  const uint16_t* x;
-  uint16_t* y;
-  int first, second;          // elements; second < 0: there is none
-  int u;                      // among the head's turned units; -1: goes through
+// A unit is two chunks of 8 values of one head: turned, elements 8 u .. and 8 u +
+// rot / 2 .., or 16 consecutive ones; or behind them 16 (or the last 8) that go
+// through.  A thread takes the same unit of TOKENS tokens, their loads together: its
+// place in the head and the heads' strides are worked out once.  `sets` such groups
+// of tokens make a CTA where a token has few units.
+// Cosines and sines stand in shared memory as the units read them: two pairs' to 16
+// bytes, pairs 2 e and 2 e + 1 of unit u of a token at [e][u], so that a warp's
+// reads are consecutive.
+struct RopeShape {
+  int units;                  // of a token
+  int per_head;
+  int threads;                // of a set
+  int sets;
 };
 
 template <int TOKENS>
-__global__ void __launch_bounds__(RP_THREADS) rope_kernel(const RopeCall c) {
-  __shared__ float2 sm_turn[TOKENS * (RP_MOST_ROT / 2)];
-  __shared__ int sm_pos[TOKENS];
-  __shared__ int sm_live[TOKENS];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long long t0 = static_cast<long long>(blockIdx.x) * TOKENS;
-  const int turned = c.rot / 16, per_head = turned + (c.d - c.rot + 15) / 16;
-  const int per_token = (c.a.heads + c.b.heads) * per_head;
-  const int tokens = static_cast<int>(min(static_cast<long long>(TOKENS), c.tokens - t0));
-  const int units = tokens * per_token;
-  auto unit = [&](int i) {
-    RopeUnit r;
-    const int token = i / per_token, rest = i - token * per_token;
-    const int head = rest / per_head, u = rest - head * per_head;
+__global__ void __launch_bounds__(RP_MOST_THREADS, 2) rope_kernel(const RopeCall c, const RopeShape z) {
+  extern __shared__ float4 sm_turn[];       // [tokens of the CTA][4][turned units]
+  __shared__ int sm_pos[RP_MOST_THREADS];
+  __shared__ int sm_live[RP_MOST_THREADS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  const int turned = c.rot / 16;
+  const long long t0 = static_cast<long long>(blockIdx.x) * (TOKENS * z.sets);
+  const int tokens = static_cast<int>(min(static_cast<long long>(TOKENS * z.sets), c.tokens - t0));
+  const int set = tid / z.threads, in_set = tid - set * z.threads;
+  const int mine = set < z.sets ? min(TOKENS, tokens - TOKENS * set) : 0;   // (0 or less: none)
+  const uint16_t* x;
+  uint16_t* y;
+  long long x_ts, y_ts;
+  int first, second, u;                     // elements (second < 0: there is none); u < 0: goes through
+  auto enter = [&](int i) {
+    const int head = i / z.per_head;
+    u = i - head * z.per_head;
     const bool of_b = head >= c.a.heads;
     const RopeOperand& o = of_b ? c.b : c.a;
     const int h = of_b ? head - c.a.heads : head;
-    r.x = o.x + (t0 + token) * o.x_ts + h * o.x_hs;
-    r.y = o.y + (t0 + token) * o.y_ts + h * o.y_hs;
+    x_ts = o.x_ts;
+    y_ts = o.y_ts;
+    x = o.x + (t0 + TOKENS * set) * x_ts + h * o.x_hs;
+    y = o.y + (t0 + TOKENS * set) * y_ts + h * o.y_hs;
     if (u < turned) {
-      r.u = u;
-      r.first = c.neighbours ? 16 * u : 8 * u;
-      r.second = c.neighbours ? 16 * u + 8 : 8 * u + c.rot / 2;
+      first = c.neighbours ? 16 * u : 8 * u;
+      second = c.neighbours ? 16 * u + 8 : 8 * u + c.rot / 2;
     } else {
-      r.u = -1;
-      r.first = c.rot + 16 * (u - turned);
-      r.second = r.first + 8 < c.d ? r.first + 8 : -1;
+      first = c.rot + 16 * (u - turned);
+      second = first + 8 < c.d ? first + 8 : -1;
+      u = -1;
     }
-    return r;
   };
-  uint4 va[RP_BATCH], vb[RP_BATCH];
-  auto load = [&](int i0) {
+  uint4 va[TOKENS], vb[TOKENS];
+  auto load = [&] {
 #pragma unroll
-    for (int k = 0; k < RP_BATCH; ++k) {
-      const int i = i0 + k * RP_THREADS;
-      if (i >= units) break;
-      const RopeUnit r = unit(i);
-      va[k] = *reinterpret_cast<const uint4*>(r.x + r.first);
-      if (r.second >= 0) vb[k] = *reinterpret_cast<const uint4*>(r.x + r.second);
-    }
+    for (int t = 0; t < TOKENS; ++t)
+      if (t < mine) {
+        va[t] = __ldcs(reinterpret_cast<const uint4*>(x + t * x_ts + first));
+        if (second >= 0) vb[t] = __ldcs(reinterpret_cast<const uint4*>(x + t * x_ts + second));
+      }
   };
-  load(tid);
-  for (int t = warp; t < tokens; t += RP_THREADS / 32) {
+  if (in_set < z.units) {
+    enter(in_set);
+    load();
+  }
+  for (int t = warp; t < tokens; t += warps) {
     int pos = 0;
     const bool live = rope_position(c, t0 + t, lane, pos);
     if (lane == 0) {
@@ -115,49 +124,65 @@ __global__ void __launch_bounds__(RP_THREADS) rope_kernel(const RopeCall c) {
   }
   __syncthreads();
   const int pairs = c.rot / 2;
-  for (int i = tid; i < tokens * pairs; i += RP_THREADS) {
-    const int t = i / pairs;
-    const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(sm_pos[t])) * c.freq[i - t * pairs];
+  for (int i = tid; i < tokens * pairs; i += blockDim.x) {
+    const int t = i / pairs, p = i - t * pairs;
+    const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(sm_pos[t])) * c.freq[p];
     float s, co;
     sincospif(static_cast<float>(static_cast<int64_t>(turn)) * 1.0842021724855044e-19f, &s, &co);   // 2^-63
-    sm_turn[i] = make_float2(co * c.factor, (c.backward ? -s : s) * c.factor);
+    reinterpret_cast<float2*>(sm_turn)[2 * ((4 * t + ((p & 7) >> 1)) * turned + (p >> 3)) + (p & 1)] =
+        make_float2(co * c.factor, (c.backward ? -s : s) * c.factor);
   }
   __syncthreads();
-  for (int i0 = tid; i0 < units; i0 += RP_BATCH * RP_THREADS) {
-    if (i0 != tid) load(i0);
+  for (int i = in_set; i < z.units; i += z.threads) {
+    if (i != in_set) {
+      enter(i);
+      load();
+    }
 #pragma unroll
-    for (int k = 0; k < RP_BATCH; ++k) {
-      const int i = i0 + k * RP_THREADS;
-      if (i >= units) break;
-      const int token = i / per_token;
-      if (!sm_live[token]) continue;         // belongs to no request: left as it is
-      const RopeUnit r = unit(i);
-      if (r.u < 0) {
-        if (r.x != r.y) {
-          *reinterpret_cast<uint4*>(r.y + r.first) = va[k];
-          if (r.second >= 0) *reinterpret_cast<uint4*>(r.y + r.second) = vb[k];
+    for (int t = 0; t < TOKENS; ++t) {
+      if (t >= mine || !sm_live[TOKENS * set + t]) continue;   // of no request: left as it is
+      uint16_t* to = y + t * y_ts;
+      if (u < 0) {
+        if (x != y) {
+          *reinterpret_cast<uint4*>(to + first) = va[t];
+          if (second >= 0) *reinterpret_cast<uint4*>(to + second) = vb[t];
         }
         continue;
       }
-      const float2* turn = sm_turn + token * pairs + 8 * r.u;
-      uint32_t p[4] = {va[k].x, va[k].y, va[k].z, va[k].w}, q[4] = {vb[k].x, vb[k].y, vb[k].z, vb[k].w};
+      const float4* turn = sm_turn + 4 * (TOKENS * set + t) * turned + u;
+      uint32_t p[4] = {va[t].x, va[t].y, va[t].z, va[t].w}, q[4] = {vb[t].x, vb[t].y, vb[t].z, vb[t].w};
+      float a[8], b[8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float a0, a1, b0, b1;
-        unpack16x2(p[e], c.bf16, a0, a1);
-        unpack16x2(q[e], c.bf16, b0, b1);
+        unpack16x2(p[e], c.bf16, a[2 * e], a[2 * e + 1]);
+        unpack16x2(q[e], c.bf16, b[2 * e], b[2 * e + 1]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 s = turn[e * turned];  // of pairs 2 e and 2 e + 1
         if (c.neighbours) {
-          const float2 s = turn[e], z = turn[4 + e];
-          p[e] = pack16x2(a0 * s.x - a1 * s.y, a0 * s.y + a1 * s.x, c.bf16);
-          q[e] = pack16x2(b0 * z.x - b1 * z.y, b0 * z.y + b1 * z.x, c.bf16);
+          float* v = e < 2 ? a + 4 * e : b + 4 * (e - 2);
+          const float u0 = v[0] * s.x - v[1] * s.y, w0 = v[0] * s.y + v[1] * s.x;
+          const float u1 = v[2] * s.z - v[3] * s.w, w1 = v[2] * s.w + v[3] * s.z;
+          v[0] = u0;
+          v[1] = w0;
+          v[2] = u1;
+          v[3] = w1;
         } else {
-          const float2 s = turn[2 * e], z = turn[2 * e + 1];
-          p[e] = pack16x2(a0 * s.x - b0 * s.y, a1 * z.x - b1 * z.y, c.bf16);
-          q[e] = pack16x2(a0 * s.y + b0 * s.x, a1 * z.y + b1 * z.x, c.bf16);
+          const float u0 = a[2 * e] * s.x - b[2 * e] * s.y, u1 = a[2 * e + 1] * s.z - b[2 * e + 1] * s.w;
+          b[2 * e] = a[2 * e] * s.y + b[2 * e] * s.x;
+          b[2 * e + 1] = a[2 * e + 1] * s.w + b[2 * e + 1] * s.z;
+          a[2 * e] = u0;
+          a[2 * e + 1] = u1;
         }
       }
-      *reinterpret_cast<uint4*>(r.y + r.first) = make_uint4(p[0], p[1], p[2], p[3]);
-      *reinterpret_cast<uint4*>(r.y + r.second) = make_uint4(q[0], q[1], q[2], q[3]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        p[e] = pack16x2(a[2 * e], a[2 * e + 1], c.bf16);
+        q[e] = pack16x2(b[2 * e], b[2 * e + 1], c.bf16);
+      }
+      *reinterpret_cast<uint4*>(to + first) = make_uint4(p[0], p[1], p[2], p[3]);
+      *reinterpret_cast<uint4*>(to + second) = make_uint4(q[0], q[1], q[2], q[3]);
     }
   }
 }
@@ -165,13 +190,32 @@ __global__ void __launch_bounds__(RP_THREADS) rope_kernel(const RopeCall c) {
 }  // namespace
 
 cudaError_t launch_rope(const RopeCall& c, cudaStream_t st) {
-  // a token to a CTA where that leaves no SM with more than a few
-  if (c.tokens <= 4 * 152) {
-    rope_kernel<1><<<static_cast<unsigned>(c.tokens), RP_THREADS, 0, st>>>(c);
-  } else {
-    const long long ctas = (c.tokens + RP_MOST_TOKENS - 1) / RP_MOST_TOKENS;
-    rope_kernel<RP_MOST_TOKENS><<<static_cast<unsigned>(ctas), RP_THREADS, 0, st>>>(c);
+  RopeShape z;
+  const int turned = c.rot / 16;
+  z.per_head = turned + (c.d - c.rot + 15) / 16;
+  const long long units = static_cast<long long>(c.a.heads + c.b.heads) * z.per_head;
+  z.units = static_cast<int>(units);
+  // a token's units in as few equal rounds as there must be
+  const long long rounds = (units + RP_MOST_THREADS - 1) / RP_MOST_THREADS;
+  z.threads = static_cast<int>((units + rounds - 1) / rounds);
+  // one token a thread where four would leave SMs idle
+  const bool many = c.tokens > 4 * 152;
+  const int per = many ? RP_TOKENS : 1;
+  const int fits = RP_SMEM / (per * turned * 64);
+  z.sets = 1;
+  if (many) {
+    z.sets = 256 / z.threads;
+    if (z.sets > fits) z.sets = fits;
+    if (z.sets < 1) z.sets = 1;
   }
+  const int threads = (z.threads * z.sets + 31) / 32 * 32;
+  const long long of_cta = static_cast<long long>(per) * z.sets;
+  const unsigned ctas = static_cast<unsigned>((c.tokens + of_cta - 1) / of_cta);
+  const size_t smem = static_cast<size_t>(of_cta) * turned * 64;
+  if (many)
+    rope_kernel<RP_TOKENS><<<ctas, threads, smem, st>>>(c, z);
+  else
+    rope_kernel<1><<<ctas, threads, smem, st>>>(c, z);
   return cudaGetLastError();
 }
 
