@@ -98,28 +98,44 @@ size_t kv_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t d
 cudaError_t launch_kv_attention(const KvAttn& a, cudaStream_t st);
 unsigned fetch_and_clear_status_kv(cudaError_t* err);
 
-// Shared prefixes (kvshared.cu).  The keys that a group of requests has in common are
-// attended to by all of the group's rows in one pass, which leaves each row's state -- O
-// before the division, the reference m and the sum l -- in memory, a row for each (token,
-// query head); a second pass, over each request's own keys, takes it up.  Which of the
-// two a launch is:
-enum KvPass : int { KV_OWN = 0, KV_PREFIX = 1 };
-struct KvState {
+// Shared prefixes (kvshared.cu).  The attention kernels' SH variants take a list of
+// entries instead of requests: the rows of a group over its prefix, or a request's rows
+// over its keys behind the prefix.  Each row that has both leaves its state -- O before the
+// division, the reference m and the sum l -- of either in memory, a row for each (token, query
+// head): whole where a unit is not cut, or in the parts of the workspace; rec says where.
+struct KvEntry {
+  int q0, q1;                  // rows of Q
+  int len;                     // keys up to here
+  int start;                   // the first key
+  int row;                     // of the table
+  int prefix;                  // the rows of a group: all of them see all of the keys
+  int pad[2];
+};
+// rec of a row: {its first part's slot, the CTA that has it, the parts (0: the state is
+// whole), the row in the unit and flags}.  Part i > 0 stands in slot 2 (CTA + i).
+constexpr int KV_REC_PREFIX = 1 << 16;      // the row has a prefix's state besides
+constexpr int KV_REC_DONE = 1 << 17;        // the row is written
+struct KvStates {
   float* o;                    // rows x d
   float2* ml;                  // rows: m, l
-  int pass;
+  int4* rec;                   // rows
 };
-// What a pass needs besides (or instead of) the call's arguments: KvAttn's cu, lens,
-// requests and max_q are the pass's.
 struct KvPassArgs {
-  const int* start;            // each request's first key; null: 0
-  const int* row_of;           // each request's row of the table; null: its own
-  int cu_step;                 // a request's rows: cu[b * cu_step] .. cu[b * cu_step + 1]
-  KvState state;
+  const KvEntry* list;
+  int64_t entries;
+  KvStates prefix, own;
 };
-// One of the passes: launched as a programmatic dependent, with the workspace's bytes below.
-size_t kv_pass_workspace_bytes(int64_t group, int64_t d, int64_t max_q);
-cudaError_t launch_kv_pass(const KvAttn& a, const KvPassArgs& pass, cudaStream_t st);
+// Which kernel a pass takes: rows of a unit 8 or 16 (kvattn.cu) or 256 (kvprompt.cu),
+// for entries of so many rows a cache head (and keys).
+int kv_pass_unit(int64_t rows);
+int kv_pass_prefix_unit(int64_t rows, int64_t keys);
+int kv_pass_ctas(int unit, int sms);
+size_t kv_pass_workspace_bytes(int unit, int64_t d, int sms);
+int kv_sm_count();
+// Launched as a programmatic dependent; `wait`: what it reads was written by the kernel
+// before it.  KvAttn: Q, cache, table and O, and the pass's workspace.
+cudaError_t launch_kv_pass(const KvAttn& a, const KvPassArgs& pass, int unit, bool wait, int sms,
+                           cudaStream_t st);
 
 // The call: requests groups[g] .. groups[g + 1] - 1 share their first shared[g] tokens.
 struct KvGroups {
@@ -135,7 +151,7 @@ cudaError_t launch_kv_attention_shared(const KvAttn& a, const KvGroups& g, cudaS
 // kv_prompt_max_requests() requests.
 int64_t kv_prompt_max_requests();
 size_t kv_prompt_workspace_bytes(int64_t d, int sms);
-cudaError_t launch_kv_prompt(const KvAttn& a, int sms, const KvPassArgs* pass, cudaStream_t st);
+cudaError_t launch_kv_prompt(const KvAttn& a, int sms, const KvPassArgs* pass, bool wait, cudaStream_t st);
 unsigned fetch_and_clear_status_kvp(cudaError_t* err);
 
 }  // namespace mxk

@@ -28,10 +28,7 @@ struct KvView {
   int capacity;                // tokens a table row holds
   int causal;
   int window;                  // 0: none
-  // Of the passes over shared prefixes (the kernels' SH variants) alone:
-  const int* start;            // each request's first key; null: 0
-  const int* row_of;           // each request's row of the table; null: its own
-  int cu_step;                 // a request's rows: cu[b * cu_step] .. cu[b * cu_step + 1]
+  const KvEntry* list;         // SH: the entries, in the requests' place
 };
 
 inline KvView kv_view(const KvAttn& q) {
@@ -64,27 +61,35 @@ struct KvReq {
 };
 struct KvShReq : KvReq {
   int start;                   // the first key
+  int row;                     // of the table
+  int prefix;
 };
 
 template <bool SH>
 __device__ __forceinline__ auto kv_request(const KvView& v, int b) {
   std::conditional_t<SH, KvShReq, KvReq> r;
   long long s, e;
+  int len;
   if constexpr (SH) {
-    // (another kernel of the same call may have written these: around L1)
-    s = __ldcg(v.cu + static_cast<long long>(b) * v.cu_step);
-    e = __ldcg(v.cu + static_cast<long long>(b) * v.cu_step + 1);
-    const int start = v.start ? __ldcg(v.start + b) : 0;
-    r.start = start < 0 ? 0 : (start > v.capacity ? v.capacity : start);
+    // (another kernel of the same call wrote these: around L1)
+    const int4* entry = reinterpret_cast<const int4*>(v.list + b);
+    const int4 x = __ldcg(entry);
+    const int2 y = __ldcg(reinterpret_cast<const int2*>(entry + 1));
+    s = x.x;
+    e = x.y;
+    len = x.z;
+    r.start = x.w < 0 ? 0 : (x.w > v.capacity ? v.capacity : x.w);
+    r.row = y.x;
+    r.prefix = y.y;
   } else {
     s = v.cu[b];
     e = v.cu[b + 1];
+    len = v.lens[b];
   }
   s = s < 0 ? 0 : (s > v.tokens ? v.tokens : s);
   e = e < s ? s : (e > v.tokens ? v.tokens : e);
   r.q0 = s;
   r.n = static_cast<int>(e - s);
-  const int len = SH ? __ldcg(v.lens + b) : v.lens[b];
   r.len = len < 0 ? 0 : (len > v.capacity ? v.capacity : len);
   return r;
 }
@@ -100,8 +105,13 @@ __device__ __forceinline__ int kv_first_key(const KvView& v, const KvReq& r, int
   const long long p = static_cast<long long>(r.len) - r.n + i + 1 - v.window;
   return p > 0 ? static_cast<int>(p) : 0;
 }
-__device__ __forceinline__ int kv_end_key(const KvView& v, const KvReq& r, int i) {
-  if (!v.causal) return r.len;
+__device__ __forceinline__ bool kv_sees_all(const KvView& v, const KvShReq& r) {
+  return !v.causal || r.prefix;
+}
+__device__ __forceinline__ bool kv_sees_all(const KvView& v, const KvReq&) { return !v.causal; }
+template <class Req>
+__device__ __forceinline__ int kv_end_key(const KvView& v, const Req& r, int i) {
+  if (kv_sees_all(v, r)) return r.len;
   const int p = r.len - r.n + i + 1;
   return p > 0 ? p : 0;
 }
@@ -154,14 +164,9 @@ __device__ __forceinline__ float kv_inverse(float sum, bool saw_keys) {
   return sum != 0.0f ? 1.0f / sum : saw_keys ? __uint_as_float(0x7FC00000u) : 0.0f;
 }
 
-// The two states' weights, for the sum of their O's divided by the sum of their l's.
-__device__ __forceinline__ void kv_join_states(float2 a, float2 b, float& wa, float& wb) {
-  const float t = fmaxf(a.x, b.x);
-  wa = a.x == t ? 1.0f : ex2_approx(a.x - t);
-  wb = b.x == t ? 1.0f : ex2_approx(b.x - t);
-  const float inv = kv_inverse(fmaf(wa, a.y, wb * b.y), t != -INFINITY);
-  wa *= inv;
-  wb *= inv;
+// A row's place among the states.
+__device__ __forceinline__ long long kv_state_row(const KvView& v, long long token, int qh) {
+  return token * (static_cast<long long>(v.heads) * v.group) + qh;
 }
 
 // The exponents of P.  A row's weights are 2^(x_j - m), and V's pages have scales

@@ -81,6 +81,12 @@ constexpr int ka_tk() {
   return D == 64 ? 256 : 128;
 }
 
+// Entries of a unit besides its tiles, for the time it takes to begin and end one.
+template <bool SH>
+constexpr int ka_over() {
+  return SH ? 2 : 1;
+}
+
 // CTAs per SM of the 8-row (NR = 1) and the 16-row (NR = 2) kernel.
 template <int NR>
 constexpr int ka_ctas_per_sm() {
@@ -92,7 +98,7 @@ template <int ROWS, bool SH>
 struct KaSeg;
 template <int ROWS>
 struct KaSeg<ROWS, false> {
-  int tile, count;             // first key tile, number (0: no more segments)
+  int key0, count;             // first key, number of tiles (0: no more segments)
   int len;                     // the request's length
   int live;                    // rows of the unit that exist
   int all_lo, all_hi;          // keys that every live row sees: no mask needed
@@ -105,25 +111,20 @@ struct KaSeg<ROWS, false> {
 };
 template <int ROWS>
 struct KaSeg<ROWS, true> : KaSeg<ROWS, false> {
-  int row[ROWS];               // the row's state
-  int has_state;               // a prefix went before
+  int row[ROWS];               // the row's place among the states
+  int to;                      // KA_TO_O, or whose states are written
 };
+enum { KA_TO_O = 0, KA_TO_OWN = 1, KA_TO_PREFIX = 2 };
 
 // A unit that begins in this CTA's stretch and goes on in others': what the
 // joining kernel needs (live 0: there is none).
-template <int ROWS, bool SH>
-struct KaJoin;
 template <int ROWS>
-struct KaJoin<ROWS, false> {
+struct KaJoin {
   int live;                    // rows
   int parts;                   // CTAs that share it: this one and the next ones
   int first_slot;              // this CTA's slot; the others use their first
-  int has_state;
+  int pad;
   long long out[ROWS];         // the rows' first elements of O
-};
-template <int ROWS>
-struct KaJoin<ROWS, true> : KaJoin<ROWS, false> {
-  int row[ROWS];               // the rows' states
 };
 
 template <int D, int NR, bool SH>
@@ -161,8 +162,9 @@ struct KaArgs {
   int o_dtype;
   float scale_log2e;
   float* ws;                   // two slots per CTA: [rows][D] of O, then m[rows], l[rows]
-  uint8_t* joins;              // one KaJoin per CTA, behind the slots
-  KvState state;               // SH
+  uint8_t* joins;              // one KaJoin per CTA, behind the slots (not SH)
+  KvStates prefix, own;        // SH
+  int wait;                    // SH: the kernel before this one wrote the list
 };
 
 __device__ __forceinline__ void ka_timeout(volatile int* abort, unsigned site) {
@@ -189,8 +191,8 @@ __device__ __forceinline__ long long ka_div(long long a, long long b) {
 template <bool SH>
 struct KaReq {
   std::conditional_t<SH, KvShReq, KvReq> r;
-  int tiles;                   // key tiles of each of its units, and one for its overhead
-  int tile0;                   // its first tile
+  int tiles;                   // key tiles of each of its units, and ka_over() for their overhead
+  int key0;                    // the first key of its first tile
   int row_tiles;
   long long units;             // row tiles x cache heads; 0: nothing for this kernel
 };
@@ -200,17 +202,19 @@ __device__ __forceinline__ KaReq<SH> ka_request(const KaArgs& a, int b) {
   KaReq<SH> q;
   q.r = kv_request<SH>(a.v, b);
   const long long rows = static_cast<long long>(q.r.n) * a.v.group;
+  // a window's first tile is one of the request's; behind a prefix tiles begin with its
+  // last page, so that as few as possible hold the request's own keys
   const int first = kv_first_key(a.v, q.r, 0);
-  q.tile0 = first / TK;
-  q.tiles = 1 + max(1, (q.r.len + TK - 1) / TK - q.tile0);
+  q.key0 = SH ? (first >> a.v.page_shift) << a.v.page_shift : first / TK * TK;
+  q.tiles = ka_over<SH>() + max(1, (q.r.len - q.key0 + TK - 1) / TK);
   q.row_tiles = static_cast<int>((rows + ROWS - 1) / ROWS);
   q.units = static_cast<long long>(q.row_tiles) * a.v.heads;
   return q;
 }
 
 // The walk over one CTA's stretch of the list.  Each unit stands in it with
-// its tiles behind one entry more, for the time it takes to begin and end a
-// unit (about that of a tile): without it a stretch of many short units took
+// its tiles behind ka_over() entries more, for the time it takes to begin and end a
+// unit (about that of a tile): without one a stretch of many short units took
 // 68 us where the median took 43 (48 requests of 0 to 6000 keys, window 2048).
 template <int ROWS, int TK, bool SH>
 struct KaWalk {
@@ -219,7 +223,7 @@ struct KaWalk {
   int b;
   KaReq<SH> q;
   // the current segment
-  int head, row_tile, tile, count;
+  int head, row_tile, key0, count;
   bool begins, ends;
   long long unit_start, unit_end;   // the unit's first tile's entry, its end
 
@@ -231,18 +235,20 @@ struct KaWalk {
         q = ka_request<ROWS, TK, SH>(a, b);
       }
       const long long u = ka_div(w - base, q.tiles);
-      int t = static_cast<int>((w - base) - u * q.tiles);   // 0: the extra entry
-      if (t == 0) {
-        t = 1;
-        if (++w >= w1) return false;          // the unit's tiles are the next CTA's
+      constexpr int OVER = ka_over<SH>();
+      int t = static_cast<int>((w - base) - u * q.tiles);   // below OVER: an extra entry
+      if (t < OVER) {
+        w += OVER - t;
+        t = OVER;
+        if (w >= w1) return false;            // the unit's tiles are the next CTA's
       }
       row_tile = static_cast<int>(ka_div(u, a.v.heads));
       head = static_cast<int>(u - static_cast<long long>(row_tile) * a.v.heads);
-      unit_start = base + u * q.tiles + 1;
-      unit_end = unit_start + q.tiles - 1;
-      tile = q.tile0 + t - 1;
+      unit_start = base + u * q.tiles + OVER;
+      unit_end = unit_start + q.tiles - OVER;
+      key0 = q.key0 + (t - OVER) * TK;
       count = static_cast<int>(min(static_cast<long long>(q.tiles - t), w1 - w));
-      begins = t == 1;
+      begins = t == OVER;
       ends = t + count == q.tiles;
       w += count;
       return true;
@@ -285,7 +291,6 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
   using L = KaSmem<D, NR, SH>;
   constexpr int ROWS = L::ROWS, TK = L::TK, KW = TK / KA_WARPS, KS = KW / 16;
   using Seg = KaSeg<ROWS, SH>;
-  using Join = KaJoin<ROWS, SH>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -314,11 +319,11 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
-  // The prefix pass reads what the plan wrote; the other one's launch follows all of
-  // that, and it waits for the prefixes' states where it needs them (and before it
-  // ends, for what comes after it).
+  // SH: the plan is the kernel before this one, or the one before a prefixes' pass that
+  // lets this one begin only when it has seen the plan itself; that pass's results are waited
+  // for at the end, for the kernel behind this one.
   if constexpr (SH)
-    if (a.state.pass == KV_PREFIX) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (a.wait) asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- the list: its length, and where this CTA's stretch begins
   const int per = (a.v.requests + KA_THREADS - 1) / KA_THREADS;
   const int rb0 = min(a.v.requests, tid * per), rb1 = min(a.v.requests, rb0 + per);
@@ -343,10 +348,10 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
   }
   const long long ctas = min(static_cast<long long>(gridDim.x), total);
   const long long cta = blockIdx.x;
-  Join* join = reinterpret_cast<Join*>(a.joins) + cta;
+  KaJoin<ROWS>* join = SH ? nullptr : reinterpret_cast<KaJoin<ROWS>*>(a.joins) + cta;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (cta >= ctas) {                         // the whole CTA: nothing was started
-    if (a.ws != nullptr && tid == 0) join->live = 0;
+    if (!SH && a.ws != nullptr && tid == 0) join->live = 0;
     if constexpr (SH) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
@@ -383,7 +388,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
       // units stay whole: the CTA in whose stretch a unit begins takes all of it
       const long long t = walk.q.tiles;
       walk.w = walk.base + (w0 - walk.base + t - 1) / t * t;   // may be the next request's first
-    } else if (lane == 0) {
+    } else if (!SH && lane == 0) {
       join->live = 0;
     }
     const int g = lane >> 2, t4 = lane & 3;
@@ -433,8 +438,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
         }
       }
       int table_row = walk.b;
-      if constexpr (SH)
-        if (a.v.row_of) table_row = __ldcg(a.v.row_of + walk.b);
+      if constexpr (SH) table_row = rq.row;
       const int* row = a.v.table + static_cast<long long>(table_row) * a.v.table_stride;
       // A tile's pages: the first MAX_PAGES lanes look after their keys, the next
       // after their values.  A page's id is -1 where the request has none and for an id
@@ -445,7 +449,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
       const int first_key = kv_first_key(a.v, rq, walk.row_tile * ROWS / a.v.group);
       const uint8_t* scales = is_v ? a.v.v_scales : a.v.k_scales;
       auto page_of = [&](int i) {
-        const int key0 = (walk.tile + i) * TK;
+        const int key0 = walk.key0 + i * TK;
         int id = -1;
         if (i < walk.count && lane < 2 * L::MAX_PAGES && slot < per_tile &&
             kv_follows(a.v, rq, first_key, key0 + (slot << shift)))
@@ -560,12 +564,11 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
           seg->lo[rr] = lo;
           seg->hi[rr] = hi;
           seg->out[rr] = out;
-          if constexpr (SH)
-            seg->row[rr] = static_cast<int>((rq.q0 + token) * (a.v.heads * a.v.group) + qh);
+          if constexpr (SH) seg->row[rr] = static_cast<int>(kv_state_row(a.v, rq.q0 + token, qh));
         }
         if constexpr (SH) {
-          const int own = static_cast<int>((rq.q0 + token) * (a.v.heads * a.v.group) + qh);
-          const int of = __shfl_sync(0xFFFFFFFFu, own, 4 * (lane & 7));
+          const int of = __shfl_sync(0xFFFFFFFFu, static_cast<int>(kv_state_row(a.v, rq.q0 + token, qh)),
+                                     4 * (lane & 7));
           if ((lane >> 3) == nr) row_of_lane = of;
         }
         // lane r of the warp keeps row r's
@@ -577,7 +580,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
       any_lo = __reduce_min_sync(0xFFFFFFFFu, any_lo);
       any_hi = __reduce_max_sync(0xFFFFFFFFu, any_hi);
       if (lane == 0) {
-        seg->tile = walk.tile;
+        seg->key0 = walk.key0;
         seg->count = walk.count;
         seg->len = rq.len;
         seg->live = min(ROWS, rows - walk.row_tile * ROWS);
@@ -588,22 +591,31 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
         seg->part = !(walk.begins && walk.ends);
         // the CTA's first segment and its last can be parts
         seg->slot = static_cast<int>(2 * cta + (first ? 0 : 1));
-        if constexpr (SH) seg->has_state = rq.start > 0;
+        if constexpr (SH) seg->to = rq.prefix ? KA_TO_PREFIX : rq.start > 0 ? KA_TO_OWN : KA_TO_O;
       }
       // the unit goes on in other CTAs: say what joins it
-      if (walk.begins && !walk.ends) {
+      const int live = min(ROWS, rows - walk.row_tile * ROWS);
+      auto parts = [&] {
+        const long long last = walk.unit_end - 1, edge = longer * (share + 1);
+        const long long c1 = last < edge ? ka_div(last, share + 1) : longer + ka_div(last - edge, share);
+        return static_cast<int>(c1 - cta + 1);
+      };
+      const int part_slot = static_cast<int>(2 * cta + (first ? 0 : 1));
+      if constexpr (SH) {
+        if (walk.begins && lane < live) {
+          int flags = lane;
+          if (!rq.prefix && rq.start > 0) flags |= KV_REC_PREFIX;
+          if (!rq.prefix && rq.start == 0 && walk.ends) flags |= KV_REC_DONE;
+          (rq.prefix ? a.prefix : a.own).rec[row_of_lane] =
+              make_int4(part_slot, static_cast<int>(cta), walk.ends ? 0 : parts(), flags);
+        }
+      } else if (walk.begins && !walk.ends) {
         if (lane == 0) {
-          join->live = min(ROWS, rows - walk.row_tile * ROWS);
-          const long long last = walk.unit_end - 1, edge = longer * (share + 1);
-          const long long c1 =
-              last < edge ? ka_div(last, share + 1) : longer + ka_div(last - edge, share);
-          join->parts = static_cast<int>(c1 - cta + 1);
-          join->first_slot = static_cast<int>(2 * cta + (first ? 0 : 1));
-          if constexpr (SH) join->has_state = rq.start > 0;
+          join->live = live;
+          join->parts = parts();
+          join->first_slot = part_slot;
         }
         if (lane < ROWS) join->out[lane] = out_of_lane;
-        if constexpr (SH)
-          if (lane < ROWS) join->row[lane] = row_of_lane;
       }
       first = false;
       __syncwarp();
@@ -644,7 +656,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
     const Seg* seg = reinterpret_cast<const Seg*>(gbase + L::SEG_OFF + ss * L::SEG_BYTES);
     const int count = seg->count;
     if (count == 0) break;
-    const int tile0 = seg->tile, len = seg->len;
+    const int seg_key0 = seg->key0, len = seg->len;
     const int all_lo = seg->all_lo, all_hi = seg->all_hi, any_lo = seg->any_lo, any_hi = seg->any_hi;
     // The lane's rows of S^T are 8 nr + 2 t + e.  B fragments of Q, and the rows'
     // factors: with 16 rows read for each tile, where keeping them cost spills
@@ -702,7 +714,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
         ok = false;
       }
       ok = __all_sync(0xFFFFFFFFu, ok);
-      const int key0 = (tile0 + i) * TK + warp * KW;
+      const int key0 = seg_key0 + i * TK + warp * KW;
       if (ok && key0 < any_hi && key0 + KW > any_lo) {
         const uint32_t kt = base + st * 2 * L::TILE;
         const uint32_t vt = kt + L::TILE;
@@ -937,13 +949,9 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
     }
     const bool part = seg->part;
     const int live = seg->live;
-    // SH: the rows' states are what is written, or are to be joined with these
-    bool to_state = false, from_state = false;
-    if constexpr (SH) {
-      to_state = !part && a.state.pass == KV_PREFIX;
-      from_state = !part && a.state.pass == KV_OWN && seg->has_state;
-      if (from_state) asm volatile("griddepcontrol.wait;" ::: "memory");
-    }
+    KvStates states{};                       // SH: whole states, where it is they that are written
+    if constexpr (SH)
+      if (!part && seg->to != KA_TO_O) states = seg->to == KA_TO_PREFIX ? a.prefix : a.own;
     float* slot = a.ws + static_cast<long long>(seg->slot) * (ROWS * (D + 2));
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
@@ -961,19 +969,15 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
       for (int w = 0; w < KA_WARPS; ++w) {
         lsum += sm_l[w * ROWS + rr] * ex2_approx(mv[w].x - M);
       }
-      const bool saw = max(seg->lo[rr], seg->tile * TK) < min(seg->hi[rr], (seg->tile + seg->count) * TK);
-      if (!part && !to_state && !from_state) unit0 *= kv_inverse(lsum, saw);
+      const bool saw = max(seg->lo[rr], seg_key0) < min(seg->hi[rr], seg_key0 + seg->count * TK);
+      if (!part && states.o == nullptr) unit0 *= kv_inverse(lsum, saw);
       if (!saw) M = -INFINITY;
       const long long out = seg->out[rr];
       float* state = nullptr;
-      float w_state = 0.0f, w_own = 1.0f;
       if constexpr (SH)
-        if (adds && (to_state || from_state)) {
-          state = a.state.o + static_cast<long long>(seg->row[rr]) * D;
-          if (from_state)
-            kv_join_states(__ldcg(a.state.ml + seg->row[rr]), make_float2(M, lsum), w_state, w_own);
-          else if (c8 == 0)
-            a.state.ml[seg->row[rr]] = make_float2(M, lsum);
+        if (adds && states.o != nullptr) {
+          state = states.o + static_cast<long long>(seg->row[rr]) * D;
+          if (c8 == 0) states.ml[seg->row[rr]] = make_float2(M, lsum);
         }
       // rounds over 4 columns of each of the 8 chunks
 #pragma unroll
@@ -1001,16 +1005,9 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
           s.y = s.y * unit0 * unit;
           s.z = s.z * unit0 * unit;
           s.w = s.w * unit0 * unit;
-          if (SH && from_state) {
-            const float4 p = ld_global_cg_f4(state + col);
-            s.x = s.x * w_own + p.x * w_state;
-            s.y = s.y * w_own + p.y * w_state;
-            s.z = s.z * w_own + p.z * w_state;
-            s.w = s.w * w_own + p.w * w_state;
-          }
           if (part)
             *reinterpret_cast<float4*>(slot + rr * D + col) = s;
-          else if (SH && to_state)
+          else if (SH && state != nullptr)
             *reinterpret_cast<float4*>(state + col) = s;
           else
             kv_store4(a.O, a.o_dtype, out + col, s);
@@ -1038,17 +1035,15 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
 // 52.6; 256 threads, which leave the main kernel's last CTAs less room, 58.)
 // Reads of the parts go around L1 (another kernel wrote them).
 constexpr int KJ_THREADS = 128;
-template <int D, int ROWS, bool SH>
+template <int D, int ROWS>
 __global__ void __launch_bounds__(KJ_THREADS)
-kv_join_kernel(const float* __restrict__ ws, const KaJoin<ROWS, SH>* joins, void* O, int o_dtype,
-               const KvState state) {
+kv_join_kernel(const float* __restrict__ ws, const KaJoin<ROWS>* joins, void* O, int o_dtype) {
   constexpr int BATCH = 4, GROUPS = 16;
   constexpr long long PART = ROWS * (D + 2);
   __shared__ float sm_m[KJ_THREADS], sm_l[KJ_THREADS];
   __shared__ float4 sm_acc[KJ_THREADS];
-  if constexpr (SH) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const KaJoin<ROWS, SH>* join = joins + blockIdx.x;
+  const KaJoin<ROWS>* join = joins + blockIdx.x;
   const int4 head = __ldcg(reinterpret_cast<const int4*>(join));
   const int live = head.x, n = head.y;
   if (live == 0) return;
@@ -1118,23 +1113,6 @@ kv_join_kernel(const float* __restrict__ ws, const KaJoin<ROWS, SH>* joins, void
     acc.z = fmaf(w, u.z, acc.z);
     acc.w = fmaf(w, u.w, acc.w);
   }
-  if constexpr (SH) {
-    const long long at = __ldcg(&join->row[row]);
-    if (state.pass == KV_PREFIX) {
-      *reinterpret_cast<float4*>(state.o + at * D + col) = acc;
-      if (col == 0) state.ml[at] = make_float2(t, sum);
-      return;
-    }
-    if (head.w) {
-      float wp, wo;
-      kv_join_states(__ldcg(state.ml + at), make_float2(t, sum), wp, wo);
-      const float4 p = ld_global_cg_f4(state.o + at * D + col);
-      kv_store4(O, o_dtype, out + col,
-                make_float4(acc.x * wo + p.x * wp, acc.y * wo + p.y * wp, acc.z * wo + p.z * wp,
-                            acc.w * wo + p.w * wp));
-      return;
-    }
-  }
   const float inv = kv_inverse(sum, t != -INFINITY);
   acc.x *= inv;
   acc.y *= inv;
@@ -1155,8 +1133,7 @@ int ka_sm_count() {
 int64_t ka_slot_bytes(int64_t d, int nr) { return 8 * nr * (d + 2) * 4; }
 int ka_ctas(int nr, int sms) { return (nr == 1 ? ka_ctas_per_sm<1>() : ka_ctas_per_sm<2>()) * sms; }
 size_t ka_ws_bytes(int64_t d, int nr, int sms, bool sh) {
-  const size_t join = sh ? (nr == 1 ? sizeof(KaJoin<8, true>) : sizeof(KaJoin<16, true>))
-                         : (nr == 1 ? sizeof(KaJoin<8, false>) : sizeof(KaJoin<16, false>));
+  const size_t join = sh ? 0 : nr == 1 ? sizeof(KaJoin<8>) : sizeof(KaJoin<16>);
   return static_cast<size_t>(ka_ctas(nr, sms)) * (2 * ka_slot_bytes(d, nr) + join);
 }
 
@@ -1165,7 +1142,6 @@ cudaError_t ka_run(const CUtensorMap& tk, const CUtensorMap& tv, const KaArgs& a
                    cudaStream_t st) {
   auto kern = kv_attention_kernel<FMT, D, NR, SH>;
   using L = KaSmem<D, NR, SH>;
-  using Join = KaJoin<8 * NR, SH>;
   static std::atomic<bool> attr_set[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1187,19 +1163,17 @@ cudaError_t ka_run(const CUtensorMap& tk, const CUtensorMap& tv, const KaArgs& a
     cfg.blockDim = dim3(KA_THREADS);
     cfg.dynamicSmemBytes = L::ALLOC;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kern, tk, tv, a);
-    if (e != cudaSuccess) return e;
+    return cudaLaunchKernelEx(&cfg, kern, tk, tv, a);
   } else {
     kern<<<ctas, KA_THREADS, L::ALLOC, st>>>(tk, tv, a);
     e = cudaGetLastError();
     if (e != cudaSuccess || a.ws == nullptr) return e;
+    cfg.gridDim = dim3(ctas, D / 32);
+    cfg.blockDim = dim3(KJ_THREADS);
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, 8 * NR>, static_cast<const float*>(a.ws),
+                              reinterpret_cast<const KaJoin<8 * NR>*>(a.joins), a.O, a.o_dtype);
   }
-  cfg.gridDim = dim3(ctas, D / 32);
-  cfg.blockDim = dim3(KJ_THREADS);
-  cfg.dynamicSmemBytes = 0;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, 8 * NR, SH>, static_cast<const float*>(a.ws),
-                            reinterpret_cast<const Join*>(a.joins), a.O, a.o_dtype, a.state);
 }
 
 template <int FMT, bool SH>
@@ -1211,7 +1185,8 @@ cudaError_t ka_run_f(int64_t d, int nr, const CUtensorMap& tk, const CUtensorMap
 }
 
 template <bool SH>
-cudaError_t ka_launch(const KvAttn& q, const KvPassArgs* pass, int sms, cudaStream_t st) {
+cudaError_t ka_launch(const KvAttn& q, const KvPassArgs* pass, int nr, bool wait, int sms,
+                      cudaStream_t st) {
   const KvCache& c = q.cache;
   KaArgs a{};
   a.v = kv_view(q);
@@ -1225,13 +1200,12 @@ cudaError_t ka_launch(const KvAttn& q, const KvPassArgs* pass, int sms, cudaStre
   a.o_dtype = q.o_dtype;
   a.scale_log2e = q.scale * 1.4426950408889634f;
   if constexpr (SH) {
-    a.v.start = pass->start;
-    a.v.row_of = pass->row_of;
-    a.v.cu_step = pass->cu_step;
-    a.state = pass->state;
+    a.v.list = pass->list;
+    a.v.requests = static_cast<int>(pass->entries);
+    a.prefix = pass->prefix;
+    a.own = pass->own;
+    a.wait = wait;
   }
-  // eight rows where the rows that one request has for a cache head fit
-  const int nr = q.max_q * a.v.group <= 8 ? 1 : 2;
   if (q.ws && q.ws_bytes >= ka_ws_bytes(c.d, nr, sms, SH)) {
     a.ws = static_cast<float*>(q.ws);
     a.joins = static_cast<uint8_t*>(q.ws) + ka_ctas(nr, sms) * 2 * ka_slot_bytes(c.d, nr);
@@ -1264,15 +1238,14 @@ namespace {
 constexpr int64_t KA_MOST_ROWS = 32;
 bool many_rows(int64_t max_q, int64_t group) { return max_q * group > KA_MOST_ROWS; }
 
-size_t few_rows_bytes(int64_t d, int sms, bool sh) {
-  return std::max(ka_ws_bytes(d, 1, sms, sh), ka_ws_bytes(d, 2, sms, sh));
-}
+// eight rows where the rows that one request has for a cache head fit
+int few_rows_nr(int64_t rows) { return rows <= 8 ? 1 : 2; }
 
 }  // namespace
 
 size_t kv_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t d, int64_t max_q) {
   const int sms = ka_sm_count();
-  const size_t few = few_rows_bytes(d, sms, false);
+  const size_t few = std::max(ka_ws_bytes(d, 1, sms, false), ka_ws_bytes(d, 2, sms, false));
   return many_rows(max_q, q_heads / kv_heads) ? std::max(few, kv_prompt_workspace_bytes(d, sms)) : few;
 }
 
@@ -1280,22 +1253,36 @@ cudaError_t launch_kv_attention(const KvAttn& q, cudaStream_t st) {
   const int sms = ka_sm_count();
   if (sms <= 0) return cudaErrorInvalidValue;
   if (many_rows(q.max_q, q.q_heads / q.cache.heads) && q.requests <= kv_prompt_max_requests())
-    return launch_kv_prompt(q, sms, nullptr, st);
-  return ka_launch<false>(q, nullptr, sms, st);
+    return launch_kv_prompt(q, sms, nullptr, false, st);
+  return ka_launch<false>(q, nullptr, few_rows_nr(q.max_q * (q.q_heads / q.cache.heads)), false, sms, st);
 }
 
-size_t kv_pass_workspace_bytes(int64_t group, int64_t d, int64_t max_q) {
-  const int sms = ka_sm_count();
-  const size_t few = few_rows_bytes(d, sms, true);
-  const size_t n = many_rows(max_q, group) ? std::max(few, kv_prompt_workspace_bytes(d, sms)) : few;
-  return (n + 31) / 32 * 32;
+int kv_sm_count() { return ka_sm_count(); }
+
+int kv_pass_unit(int64_t rows) { return many_rows(rows, 1) ? 256 : 8 * few_rows_nr(rows); }
+
+// For a prefix's pass the rows of a group are many, but its keys may be few: the prompt
+// kernel takes longer to begin and end.  Measured with 8 cache heads of 128 values, one group
+// (this kernel against the prompt kernel, each with its join): 64 rows, 2048 keys
+// 15.5 against 23.4 us, 8192 23.4 against 29.0, 32768 56.9 against 46.5; 128 rows
+// 18.0 against 24.8, 33.7 against 30.7, 95.2 against 48.2; 256 rows 23.2 against 29.6,
+// 52.8 against 38.0; 512 rows, 512 keys 17.9 against 21.6, 2048 33.9 against 29.1.  So their
+// product decides, with the keys that a row of the table has room for.
+constexpr int64_t KA_MOST_PREFIX = 900000;
+int kv_pass_prefix_unit(int64_t rows, int64_t keys) {
+  return rows <= KA_MOST_PREFIX / std::max<int64_t>(1, keys) ? 8 * few_rows_nr(rows) : kv_pass_unit(rows);
 }
 
-cudaError_t launch_kv_pass(const KvAttn& q, const KvPassArgs& pass, cudaStream_t st) {
-  const int sms = ka_sm_count();
-  if (sms <= 0) return cudaErrorInvalidValue;
-  if (many_rows(q.max_q, q.q_heads / q.cache.heads)) return launch_kv_prompt(q, sms, &pass, st);
-  return ka_launch<true>(q, &pass, sms, st);
+int kv_pass_ctas(int unit, int sms) { return unit == 256 ? sms : ka_ctas(unit / 8, sms); }
+
+size_t kv_pass_workspace_bytes(int unit, int64_t d, int sms) {
+  return unit == 256 ? kv_prompt_workspace_bytes(d, sms) : ka_ws_bytes(d, unit / 8, sms, true);
+}
+
+cudaError_t launch_kv_pass(const KvAttn& q, const KvPassArgs& pass, int unit, bool wait, int sms,
+                           cudaStream_t st) {
+  if (unit == 256) return launch_kv_prompt(q, sms, &pass, wait, st);
+  return ka_launch<true>(q, &pass, unit / 8, wait, sms, st);
 }
 
 unsigned fetch_and_clear_status_kv(cudaError_t* err) {

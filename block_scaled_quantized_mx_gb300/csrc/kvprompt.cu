@@ -103,7 +103,9 @@ struct KpSeg {
   int row0;                                // the unit's first row
   int head;
   int slot;                                // workspace slot, -1: not a part
-  int start;                               // SH: the request's first key
+  int start;                               // SH: the entry's first key
+  int prefix;                              // SH
+  int rec;                                 // SH: the unit's parts (0: whole) if it begins here, else -1
 };
 
 // A unit that begins in this CTA's stretch and goes on in others'.
@@ -113,7 +115,7 @@ struct KpJoin {
   int first_slot;                          // this CTA's slot; the others use their first
   int head;
   int row0;
-  int has_state;                           // SH: a prefix went before
+  int pad;
   long long q0;
 };
 
@@ -223,7 +225,8 @@ struct KpArgs {
   float* ws;                               // two slots per CTA: O as [D / 8][256 rows][8], m[256], l[256];
                                            // 32-byte aligned
   KpJoin* joins;                           // one per CTA
-  KvState state;                           // SH
+  KvStates prefix, own;                    // SH
+  int wait;                                // SH: the kernel before this one wrote the list
 };
 
 __device__ __forceinline__ void kp_timeout(volatile int* abort, unsigned site) {
@@ -377,11 +380,12 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::MISC_OFF);
   volatile int* abort = reinterpret_cast<volatile int*>(gbase + L::MISC_OFF + 4);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // The prefix pass reads what the plan wrote, before others may follow; the other
-  // one's launch follows all of that, and it waits for the prefixes' states where it
-  // needs them (and before it ends, for what comes after it).
+  // SH: the plan is the kernel before this one (which is waited for before others may
+  // follow), or the one before a prefixes' pass that lets this one begin only when it has
+  // seen the plan itself; that pass's results are waited for at the end, for the kernel
+  // behind this one.
   if constexpr (SH)
-    if (a.state.pass == KV_PREFIX) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (a.wait) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- the list: row tiles of each request, then entries of each row tile
@@ -558,16 +562,20 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             s->q0 = walk->r.q0;
             s->row0 = walk->rt * KP_ROWS;
             s->head = walk->head;
-            if constexpr (SH) s->start = walk->r.start;
             const int slot = 2 * static_cast<int>(blockIdx.x) + (first_seg ? 0 : 1);
             s->slot = walk->begins && walk->ends ? -1 : slot;
-            if (walk->begins && !walk->ends) {
+            const int parts =
+                walk->ends ? 0 : static_cast<int>((walk->unit_end * ctas - 1) / total - blockIdx.x + 1);
+            if constexpr (SH) {
+              s->start = walk->r.start;
+              s->prefix = walk->r.prefix;
+              s->rec = walk->begins ? parts : -1;
+            } else if (walk->begins && !walk->ends) {
               KpJoin* j = a.joins + blockIdx.x;
               j->live = min(KP_ROWS, walk->r.n * a.v.group - walk->rt * KP_ROWS);
-              j->parts = static_cast<int>((walk->unit_end * ctas - 1) / total - blockIdx.x + 1);
+              j->parts = parts;
               j->first_slot = slot;
               j->head = walk->head;
-              if constexpr (SH) j->has_state = walk->r.start > 0;
               j->row0 = walk->rt * KP_ROWS;
               j->q0 = walk->r.q0;
             }
@@ -580,8 +588,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         const int count = walk->count, block0 = walk->block, head = walk->head;
         const Req rq = walk->r;
         int table_row = walk->b;
-        if constexpr (SH)
-          if (a.v.row_of) table_row = __ldcg(a.v.row_of + table_row);
+        if constexpr (SH) table_row = rq.row;
         const int* row = a.v.table + static_cast<long long>(table_row) * a.v.table_stride;
         const int shift = a.v.page_shift;
         const int first_key = kv_first_key(a.v, rq, walk->rt * KP_ROWS / a.v.group);
@@ -865,7 +872,10 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       if (next_count != 0) {
         // this thread's row: Q to f16, its bounds and factor
         Req rq;
-        if constexpr (SH) rq.start = segs[ss].start;
+        if constexpr (SH) {
+          rq.start = segs[ss].start;
+          rq.prefix = segs[ss].prefix;
+        }
         rq.q0 = segs[ss].q0;
         rq.n = segs[ss].n;
         rq.len = segs[ss].len;
@@ -935,22 +945,21 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         // rows of O 32 bytes at a time where they are that aligned
         const bool by32 = ((reinterpret_cast<uintptr_t>(a.O) |
                             static_cast<uintptr_t>(out * (a.o_dtype == DT_F32 ? 4 : 2))) & 31) == 0;
-        // SH: the rows' states are what is written, or are to be joined with these
-        bool to_state = false;
-        float* state = nullptr;
-        float w_state = 0.0f, w_own = 1.0f;
+        float* state = nullptr;              // SH: the row's whole state, where it is what is written
         if constexpr (SH) {
-          to_state = !part && a.state.pass == KV_PREFIX;
-          const bool from_state = !part && a.state.pass == KV_OWN && sg->start > 0;
-          const long long at = (sg->q0 + token) * (static_cast<long long>(a.v.heads) * a.v.group) +
-                               sg->head * a.v.group + row - token * a.v.group;
-          if (from_state) asm volatile("griddepcontrol.wait;" ::: "memory");
-          if ((to_state || from_state) && live) {
-            state = a.state.o + at * D;
-            if (from_state)
-              kv_join_states(__ldcg(a.state.ml + at), make_float2(saw ? m : -INFINITY, l), w_state, w_own);
-            else
-              a.state.ml[at] = make_float2(saw ? m : -INFINITY, l);
+          const bool of_prefix = sg->prefix != 0, has_prefix = !of_prefix && sg->start > 0;
+          const KvStates& states = of_prefix ? a.prefix : a.own;
+          const long long at =
+              kv_state_row(a.v, sg->q0 + token, sg->head * a.v.group + row - token * a.v.group);
+          if (live && sg->rec >= 0) {
+            int flags = urow;
+            if (has_prefix) flags |= KV_REC_PREFIX;
+            if (!of_prefix && !has_prefix && sg->rec == 0) flags |= KV_REC_DONE;
+            states.rec[at] = make_int4(sg->slot, static_cast<int>(blockIdx.x), sg->rec, flags);
+          }
+          if (!part && live && (of_prefix || has_prefix)) {
+            state = states.o + at * D;
+            states.ml[at] = make_float2(saw ? m : -INFINITY, l);
           }
         }
         const float f = part || (SH && state) ? unit0 : unit0 * kv_inverse(l, saw);
@@ -963,21 +972,11 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f * unit);
           if constexpr (SH) {
-            if (to_state) {
+            if (state) {
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 st_global_v8(state + 32 * c + 8 * e, *reinterpret_cast<const uint32_t(*)[8]>(o + 8 * e));
               continue;
-            }
-            if (state) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 p = ld_global_cg_f4(state + 32 * c + 4 * e);
-                const float pp[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  o[4 * e + i] = __float_as_uint(__uint_as_float(o[4 * e + i]) * w_own + pp[i] * w_state);
-              }
             }
           }
           if (part) {
@@ -1256,171 +1255,6 @@ kv_prompt_join_kernel(const KpArgs a) {
   }
 }
 
-// The same for the passes over shared prefixes, whose units may be few and their parts
-// many -- 256 rows of 8 cache heads over 152 SMs make 8 units of 20 parts -- so that a CTA
-// per CTA of the main kernel leaves most of them without work.  Here the units are listed
-// first, and the CTAs share out pieces of 8 KPJ_R x 4 rows x 64 columns, a few rows a warp;
-// or, of units of more than KPS_FEW parts, of one warp's rows, whose parts the warps share
-// and join in shared memory, in order.
-constexpr int KPS_WARPS = KPJ_THREADS / 32;
-constexpr int KPS_MAX_CTAS = 512;              // of the main kernel
-constexpr int KPS_FEW = 4;
-template <int D>
-__global__ void __launch_bounds__(KPJ_THREADS)
-kv_prompt_states_kernel(const KpArgs a, const int main_ctas) {
-  __shared__ int sm_first[KPS_MAX_CTAS];       // per CTA of the main kernel: its unit's first piece
-  __shared__ int sm_scan[KPS_WARPS];
-  __shared__ float sm_acc[KPS_WARPS][KPJ_R][32][9];
-  __shared__ float2 sm_ml[KPS_WARPS][KPJ_R][32];
-  constexpr int COLS = D / 64;
-  constexpr long long PART = KP_ROWS * (D + 2);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  auto rows_of = [](int parts) { return 4 * KPJ_R * (parts > KPS_FEW ? 1 : KPS_WARPS); };
-  auto pieces_of = [&](int live, int parts) { return (live + rows_of(parts) - 1) / rows_of(parts) * COLS; };
-  // ---- the units' pieces
-  int at = 0;
-  for (int c0 = 0; c0 < main_ctas; c0 += KPJ_THREADS) {
-    const int c = c0 + tid;
-    int n = 0;
-    if (c < main_ctas) {
-      const int live = __ldcg(&a.joins[c].live);
-      if (live > 0) n = pieces_of(live, __ldcg(&a.joins[c].parts));
-    }
-    int s = n;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int u = __shfl_up_sync(0xFFFFFFFFu, s, d);
-      if (lane >= d) s += u;
-    }
-    if (lane == 31) sm_scan[warp] = s;
-    __syncthreads();
-    int before = at;
-    for (int w = 0; w < KPS_WARPS; ++w) {
-      if (w < warp) before += sm_scan[w];
-      at += sm_scan[w];
-    }
-    if (c < main_ctas) sm_first[c] = before + s - n;
-    __syncthreads();
-  }
-  const int total = at;
-  for (int piece = blockIdx.x; piece < total; piece += gridDim.x) {
-    // the last unit that begins at or before it and has pieces: of equal starts the last
-    int lo = 0, hi = main_ctas - 1;
-    while (lo < hi) {
-      const int m = (lo + hi + 1) >> 1;
-      if (sm_first[m] <= piece) lo = m; else hi = m - 1;
-    }
-    const KpJoin* join = a.joins + lo;
-    const int live = __ldcg(&join->live), n = __ldcg(&join->parts);
-    const int in = piece - sm_first[lo];
-    const bool many = n > KPS_FEW;
-    const int row0 = __ldcg(&join->row0), head = __ldcg(&join->head);
-    const long long q0 = __ldcg(&join->q0);
-    const bool to_state = a.state.pass == KV_PREFIX;
-    const bool from_state = !to_state && __ldcg(&join->has_state);
-    const int r0 = in / COLS * rows_of(n) + (many ? 0 : 4 * KPJ_R * warp) + (lane & 3);
-    const int col = 64 * (in % COLS) + 8 * (lane >> 2);
-    const float* first = a.ws + __ldcg(&join->first_slot) * PART;
-    const float* rest = a.ws + 2ll * lo * PART;
-    float top[KPJ_R], sum[KPJ_R], acc[KPJ_R][8];
-#pragma unroll
-    for (int i = 0; i < KPJ_R; ++i) {
-      top[i] = -INFINITY;
-      sum[i] = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[i][e] = 0.0f;
-    }
-#pragma unroll 2
-    for (int p = many ? warp : 0; p < n; p += many ? KPS_WARPS : 1) {
-      const float* part = p == 0 ? first : rest + 2 * p * PART;
-      float mp[KPJ_R], lp[KPJ_R], v[KPJ_R][8];
-#pragma unroll
-      for (int i = 0; i < KPJ_R; ++i) {
-        const int r = min(r0 + 4 * i, live - 1);         // (a row too many is not stored)
-        mp[i] = __ldcg(part + KP_ROWS * D + r);
-        lp[i] = __ldcg(part + KP_ROWS * (D + 1) + r);
-        ld_global_cg_v8(part + (col / 8 * KP_ROWS + r) * 8, v[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < KPJ_R; ++i) {
-        const float t = fmaxf(top[i], mp[i]);
-        const float before = top[i] == t ? 1.0f : ex2_approx(top[i] - t);
-        const float w = mp[i] == t ? 1.0f : ex2_approx(mp[i] - t);
-        top[i] = t;
-        sum[i] = fmaf(w, lp[i], sum[i] * before);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[i][e] = fmaf(w, v[i][e], acc[i][e] * before);
-      }
-    }
-    // N columns from `col` of the unit's row r, as (t, l, o) has them
-    auto finish = [&](int r, int col, float t, float l, auto& o) {
-      constexpr int N = sizeof(o) / sizeof(float);
-      const int row = row0 + r, token = row / a.v.group;
-      const int qh = head * a.v.group + row - token * a.v.group;
-      const long long state = (q0 + token) * (static_cast<long long>(a.v.heads) * a.v.group) + qh;
-      float* so = a.state.o + state * D + col;
-      float wp = 0.0f, wo = 1.0f;
-      if (to_state) {
-        if (col == 0) a.state.ml[state] = make_float2(t, l);
-      } else if (from_state) {
-        kv_join_states(__ldcg(a.state.ml + state), make_float2(t, l), wp, wo);
-      } else {
-        wo = kv_inverse(l, t != -INFINITY);
-      }
-#pragma unroll
-      for (int e = 0; e < N; e += 2) {
-        float2 v = make_float2(o[e] * wo, o[e + 1] * wo);
-        if (from_state) {
-          const float2 p = __ldcg(reinterpret_cast<const float2*>(so + e));
-          v.x = fmaf(p.x, wp, v.x);
-          v.y = fmaf(p.y, wp, v.y);
-        }
-        const long long out = (q0 + token) * a.o_ts + qh * a.o_hs + col + e;
-        if (to_state)
-          *reinterpret_cast<float2*>(so + e) = v;
-        else if (a.o_dtype == DT_F32)
-          *reinterpret_cast<float2*>(static_cast<float*>(a.O) + out) = v;
-        else
-          *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.O) + out) =
-              a.o_dtype == DT_BF16 ? cvt_bf16x2(v.x, v.y) : cvt_f16x2(v.x, v.y);
-      }
-    };
-    if (!many) {
-#pragma unroll
-      for (int i = 0; i < KPJ_R; ++i)
-        if (r0 + 4 * i < live) finish(r0 + 4 * i, col, top[i], sum[i], acc[i]);
-      continue;
-    }
-    __syncthreads();                         // the shared arrays are free
-#pragma unroll
-    for (int i = 0; i < KPJ_R; ++i) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sm_acc[warp][i][lane][e] = acc[i][e];
-      sm_ml[warp][i][lane] = make_float2(top[i], sum[i]);
-    }
-    __syncthreads();
-    // a thread takes two columns of the 8 of one lane
-    static_assert(KPJ_THREADS == KPJ_R * 32 * 4, "two of eight columns a thread");
-    const int i = tid >> 7, of = (tid >> 2) & 31, e = 2 * (tid & 3);
-    const int r = in / COLS * rows_of(n) + (of & 3) + 4 * i;
-    if (r >= live) continue;
-    float t = -INFINITY, l = 0.0f, o[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int w = 0; w < KPS_WARPS; ++w) t = fmaxf(t, sm_ml[w][i][of].x);
-#pragma unroll
-    for (int w = 0; w < KPS_WARPS; ++w) {
-      const float2 ml = sm_ml[w][i][of];
-      const float wgt = ml.x == t ? 1.0f : ex2_approx(ml.x - t);
-      l = fmaf(wgt, ml.y, l);
-      o[0] = fmaf(wgt, sm_acc[w][i][of][e], o[0]);
-      o[1] = fmaf(wgt, sm_acc[w][i][of][e + 1], o[1]);
-    }
-    finish(r, 64 * (in % COLS) + 8 * (of >> 2) + e, t, l, o);
-  }
-}
-
 template <int FMT, int D, bool SH>
 cudaError_t kp_run(const CUtensorMap& tk, const CUtensorMap& tv, const KpArgs& a, int sms,
                    cudaStream_t st) {
@@ -1452,22 +1286,16 @@ cudaError_t kp_run(const CUtensorMap& tk, const CUtensorMap& tv, const KpArgs& a
     cfg.blockDim = dim3(KP_THREADS);
     cfg.dynamicSmemBytes = L::ALLOC;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kern, tk, tv, a);
-    if (e != cudaSuccess) return e;
+    return cudaLaunchKernelEx(&cfg, kern, tk, tv, a);
   } else {
     kern<<<sms, KP_THREADS, L::ALLOC, st>>>(tk, tv, a);
     e = cudaGetLastError();
     if (e != cudaSuccess || a.ws == nullptr) return e;
+    cfg.gridDim = dim3(sms, KP_ROWS * (D / 8) / (KPJ_THREADS * KPJ_R));
+    cfg.blockDim = dim3(KPJ_THREADS);
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_prompt_join_kernel<D>, a);
   }
-  cfg.blockDim = dim3(KPJ_THREADS);
-  cfg.dynamicSmemBytes = 0;
-  cfg.numAttrs = 1;
-  if constexpr (SH) {
-    cfg.gridDim = dim3(4 * sms);
-    return cudaLaunchKernelEx(&cfg, kv_prompt_states_kernel<D>, a, sms);
-  }
-  cfg.gridDim = dim3(sms, KP_ROWS * (D / 8) / (KPJ_THREADS * KPJ_R));
-  return cudaLaunchKernelEx(&cfg, kv_prompt_join_kernel<D>, a);
 }
 
 template <bool SH>
@@ -1492,7 +1320,7 @@ size_t kv_prompt_workspace_bytes(int64_t d, int sms) {
   return static_cast<size_t>(sms) * (2 * KP_ROWS * (d + 2) * 4 + sizeof(KpJoin)) + 16;
 }
 
-cudaError_t launch_kv_prompt(const KvAttn& q, int sms, const KvPassArgs* pass, cudaStream_t st) {
+cudaError_t launch_kv_prompt(const KvAttn& q, int sms, const KvPassArgs* pass, bool wait, cudaStream_t st) {
   const KvCache& c = q.cache;
   KpArgs a{};
   a.v = kv_view(q);
@@ -1512,11 +1340,12 @@ cudaError_t launch_kv_prompt(const KvAttn& q, int sms, const KvPassArgs* pass, c
     a.joins = reinterpret_cast<KpJoin*>(ws + static_cast<int64_t>(sms) * 2 * KP_ROWS * (c.d + 2) * 4);
   }
   if (pass) {
-    if (a.ws == nullptr || sms > KPS_MAX_CTAS) return cudaErrorInvalidValue;
-    a.v.start = pass->start;
-    a.v.row_of = pass->row_of;
-    a.v.cu_step = pass->cu_step;
-    a.state = pass->state;
+    if (a.ws == nullptr) return cudaErrorInvalidValue;   // the caller has seen to it
+    a.v.list = pass->list;
+    a.v.requests = static_cast<int>(pass->entries);
+    a.prefix = pass->prefix;
+    a.own = pass->own;
+    a.wait = wait;
   }
   CUtensorMap tk, tv;
   if (!kv_tensor_map(&tk, c.k, c) || !kv_tensor_map(&tv, c.v, c)) return cudaErrorInvalidValue;

@@ -118,10 +118,10 @@ __global__ void __launch_bounds__(SH_THREADS) kv_release_kernel(const ShareArgs 
     sm_rank[b] = 0;
   }
   __syncthreads();
-  // A warp's requests, SH_ROWS at a time, SH_SPAN entries of each: f(u, b, entry, page) for
-  // each of them, page being -1 behind a row's last lost entry.  Neighbours, which often
-  // end together, go to different warps.  Where that is all that the warp has, the
-  // entries are read once and stay in registers over the steps.
+  // A warp's requests, SH_ROWS at a time, SH_SPAN entries of each, in page[][] (-1 behind a
+  // row's last lost entry): f(the requests, their rows from the first of those entries).
+  // Neighbours, which often end together, go to different warps.  Where that is all
+  // that the warp has, the entries are read once and stay in registers over the steps.
   int page[SH_ROWS][SH_BATCH];
   bool kept = false;
   auto each = [&](auto f) {
@@ -151,46 +151,61 @@ __global__ void __launch_bounds__(SH_THREADS) kv_release_kernel(const ShareArgs 
               page[u][i] = k < n[u] ? row[u][k] : -1;
             }
         }
+        f(b, row);
 #pragma unroll
-        for (int u = 0; u < SH_ROWS; ++u)
-          if (k0 < n[u]) f(u, b[u], row[u] + k0);
+        for (int u = 0; u < SH_ROWS; ++u) row[u] += SH_SPAN;
       }
       kept = true;
     }
   };
   auto held = [&](int p) { return p >= 0 && p < a.pages; };
-  each([&](int u, int, int*) {
+  using Ints = int (&)[SH_ROWS];
+  using Rows = int* (&)[SH_ROWS];
+  each([&](Ints, Rows) {
 #pragma unroll
-    for (int i = 0; i < SH_BATCH; ++i)
-      if (held(page[u][i])) atomicSub(a.refs + page[u][i], 1);
+    for (int u = 0; u < SH_ROWS; ++u)
+#pragma unroll
+      for (int i = 0; i < SH_BATCH; ++i)
+        if (held(page[u][i])) atomicSub(a.refs + page[u][i], 1);
   });
   share_sync();
-  each([&](int u, int b, int*) {
-    int refs[SH_BATCH];
+  each([&](Ints b, Rows) {
+    int refs[SH_ROWS][SH_BATCH];
 #pragma unroll
-    for (int i = 0; i < SH_BATCH; ++i) refs[i] = held(page[u][i]) ? __ldcg(a.refs + page[u][i]) : 0;
+    for (int u = 0; u < SH_ROWS; ++u)
 #pragma unroll
-    for (int i = 0; i < SH_BATCH; ++i)
-      if (refs[i] < 0) atomicMin(a.refs + page[u][i], -2 - (first + b));
+      for (int i = 0; i < SH_BATCH; ++i)
+        refs[u][i] = held(page[u][i]) ? __ldcg(a.refs + page[u][i]) : 0;
+#pragma unroll
+    for (int u = 0; u < SH_ROWS; ++u)
+#pragma unroll
+      for (int i = 0; i < SH_BATCH; ++i)
+        if (refs[u][i] < 0) atomicMin(a.refs + page[u][i], -2 - (first + b[u]));
   });
   share_sync();
-  each([&](int u, int b, int* row) {
-    int was[SH_BATCH], mine = 0;
-    const int bid = -2 - (first + b);
+  each([&](Ints b, Rows row) {
+    int was[SH_ROWS][SH_BATCH];
 #pragma unroll
-    for (int i = 0; i < SH_BATCH; ++i) was[i] = held(page[u][i]) ? atomicCAS(a.refs + page[u][i], bid, 0) : 0;
+    for (int u = 0; u < SH_ROWS; ++u)
 #pragma unroll
-    for (int i = 0; i < SH_BATCH; ++i) {
-      if (page[u][i] < 0) continue;
-      if (was[i] == bid) {
-        ++mine;
-      } else {
-        row[32 * i + lane] = -1;            // others hold it, or free it
-        page[u][i] = -1;
+      for (int i = 0; i < SH_BATCH; ++i)
+        was[u][i] = held(page[u][i]) ? atomicCAS(a.refs + page[u][i], -2 - (first + b[u]), 0) : 0;
+#pragma unroll
+    for (int u = 0; u < SH_ROWS; ++u) {
+      int mine = 0;
+#pragma unroll
+      for (int i = 0; i < SH_BATCH; ++i) {
+        if (page[u][i] < 0) continue;
+        if (was[u][i] == -2 - (first + b[u])) {
+          ++mine;
+        } else {
+          row[u][32 * i + lane] = -1;       // others hold it, or free it
+          page[u][i] = -1;
+        }
       }
+      mine = __reduce_add_sync(0xFFFFFFFFu, mine);
+      if (lane == 0 && mine) sm_rank[b[u]] += mine;
     }
-    mine = __reduce_add_sync(0xFFFFFFFFu, mine);
-    if (lane == 0) sm_rank[b] += mine;
   });
   __syncthreads();
   const int per = (B + SH_THREADS - 1) / SH_THREADS;
@@ -225,21 +240,25 @@ __global__ void __launch_bounds__(SH_THREADS) kv_release_kernel(const ShareArgs 
     a.counts_out[1] = static_cast<int>(n < a.stack_size ? 0 : n - a.stack_size);
   }
   const long long top = count + total - 1 - before;
-  each([&](int u, int b, int* row) {
-    int i_th = sm_rank[b];
+  each([&](Ints b, Rows row) {
 #pragma unroll
-    for (int i = 0; i < SH_BATCH; ++i) {
-      const unsigned have = __ballot_sync(0xFFFFFFFFu, page[u][i] >= 0);
-      if (page[u][i] >= 0) {
-        const long long to = top - (i_th + __popc(have & ((1u << lane) - 1u)));
-        if (to < a.stack_size) a.stack[to] = page[u][i];
-        row[32 * i + lane] = -1;
+    for (int u = 0; u < SH_ROWS; ++u) {
+      if (b[u] >= B) break;
+      int i_th = sm_rank[b[u]];
+#pragma unroll
+      for (int i = 0; i < SH_BATCH; ++i) {
+        const unsigned have = __ballot_sync(0xFFFFFFFFu, page[u][i] >= 0);
+        if (page[u][i] >= 0) {
+          const long long to = top - (i_th + __popc(have & ((1u << lane) - 1u)));
+          if (to < a.stack_size) a.stack[to] = page[u][i];
+          row[u][32 * i + lane] = -1;
+        }
+        i_th += __popc(have);
       }
-      i_th += __popc(have);
+      __syncwarp();
+      if (lane == 0) sm_rank[b[u]] = i_th;  // (the row may go on)
+      __syncwarp();
     }
-    __syncwarp();
-    if (lane == 0) sm_rank[b] = i_th;       // (the row may go on)
-    __syncwarp();
   });
   __syncwarp();
   if (ctas > 1) cluster_wait();             // nobody reads this CTA's total any more

@@ -4,21 +4,25 @@
 // With the keys of a row in two sets, P (the prefix) and S (its own),
 //   o = (w_P O_P + w_S O_S) / (w_P l_P + w_S l_S),  w_i = 2^(m_i - max(m_P, m_S)),
 // O_i = sum_j 2^(x_j - m_i) v_j and l_i = sum_j 2^(x_j - m_i) over the set's keys: the
-// identity behind the running softmax.  So three steps, each the next one's
-// programmatic dependency:
-//   plan     how much of each prefix its group's rows of the table agree on and all of its
-//            rows may see, and those rows (consecutive requests' are consecutive) -- a few
-//            integers;
-//   prefix   the kernels of kvattn.cu or kvprompt.cu with a group in a request's place:
-//            all of its rows, over the prefix; (O, m, l) per row are left in memory;
-//   own      the same kernels over each request's keys behind the prefix; who writes a
-//            row takes the prefix's (O, m, l) up.
-// Precision: as those kernels have it; (O, m, l) and their joining are fp32.
+// identity behind the running softmax, and the same for the parts of a set.  Three or four
+// steps, each the next one's programmatic dependency:
+//   plan   how much of each prefix its group's rows of the table agree on and all of its
+//          rows may see, and a list for the kernels of kvattn.cu and kvprompt.cu: an
+//          entry for each group (all of its rows, which are consecutive, over the prefix)
+//          and one for each request (its rows over its keys behind the prefix);
+//   pass   one of those kernels over the list, or one over each half of it, where the rows
+//          of groups and of requests want different ones.  Rows without a prefix are
+//          written, unless their unit is cut; the others leave (O, m, l) in memory, in
+//          as many parts as CTAs shared their units;
+//   join   each such row from the parts of both sets.
+// Precision: as those kernels have it; (O, m, l) and their joining are fp32, in a fixed
+// order.
 #include <algorithm>
 #include <cstdint>
 
 #include "common.cuh"
 #include "kv_common.cuh"
+#include "kv_kernel.cuh"
 #include "ptx.cuh"
 
 namespace mxk {
@@ -28,8 +32,10 @@ namespace {
 constexpr int SP_THREADS = 1024;
 constexpr int SP_WARPS = SP_THREADS / 32;
 constexpr int SP_MAX = 16384;               // requests, and groups
-constexpr int SP_CLUSTER = 8;               // CTAs to a group, where there are few
+// CTAs to a group where its rows of the table are long, and the groups few
+constexpr int SP_CLUSTER = 8;
 constexpr int SP_MANY_GROUPS = 64;
+constexpr int64_t SP_ENTRIES = 4096;        // of the table, for one CTA
 constexpr int SP_BATCH = 8;                 // table entries of a lane on their way together
 
 struct PlanArgs {
@@ -40,22 +46,21 @@ struct PlanArgs {
   const int* table;
   long long table_stride;
   int requests;
+  int n;                      // groups
   int capacity;               // tokens a table row holds
   int page_shift;
-  int* start;                 // per request: keys of its group's prefix, 0 where it has none
-  int* rows;                  // per group: its rows' first and end
-  int* plens;                 // per group: its prefix's keys
-  int* row_of;                // per group: the request in whose row of the table the prefix is found
+  KvEntry* list;              // n for the groups, then the requests'
 };
 
-__device__ __forceinline__ int plan_reduce(int v, int* sm, bool least) {
-  v = least ? __reduce_min_sync(0xFFFFFFFFu, v) : __reduce_max_sync(0xFFFFFFFFu, v);
-  __syncthreads();                          // sm is free
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+// The least a and the sum of b over the block's threads.  `sm`: of this call alone.
+__device__ __forceinline__ void plan_reduce(int& a, int& b, int2* sm) {
+  const int la = __reduce_min_sync(0xFFFFFFFFu, a), sb = __reduce_add_sync(0xFFFFFFFFu, b);
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = make_int2(la, sb);
   __syncthreads();
-  v = sm[threadIdx.x & 31];
+  const int2 v = sm[threadIdx.x & 31];
   static_assert(SP_WARPS == 32, "a lane for each warp");
-  return least ? __reduce_min_sync(0xFFFFFFFFu, v) : __reduce_max_sync(0xFFFFFFFFu, v);
+  a = __reduce_min_sync(0xFFFFFFFFu, v.x);
+  b = __reduce_add_sync(0xFFFFFFFFu, v.y);
 }
 
 // One group to a CTA or to a cluster.  Its requests are groups[g] .. groups[g + 1] - 1,
@@ -63,15 +68,17 @@ __device__ __forceinline__ int plan_reduce(int v, int* sm, bool least) {
 // `shared` says, what stands in front of all its rows, and what the rows of the table agree on,
 // whichever is least: a wrong word about a prefix costs time, not the answer.
 __global__ void __launch_bounds__(SP_THREADS) kv_plan_kernel(const PlanArgs a) {
-  __shared__ int sm[SP_WARPS];
+  __shared__ int2 sm[3][SP_WARPS];
   __shared__ int sm_agree;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, B = a.requests;
   const int rank = blockIdx.x, ctas = gridDim.x, g = blockIdx.y;
-  int top = 0;
-  for (int i = tid; i <= g; i += SP_THREADS) top = max(top, max(0, min(a.groups[i], B)));
-  const int r0 = plan_reduce(top, sm, false);
-  const int r1 = max(r0, max(0, min(a.groups[g + 1], B)));
+  int r0 = 0, none = 0;
+  for (int i = tid; i <= g; i += SP_THREADS) r0 = min(r0, -max(0, min(a.groups[i], B)));
+  const int edge = max(0, min(a.groups[g + 1], B));
+  plan_reduce(r0, none, sm[0]);
+  r0 = -r0;
+  const int r1 = max(r0, edge);
   // the tokens that stand in front of every row of the group
   int most = 0x7FFFFFFF, with_rows = 0;
   for (int b = r0 + tid; b < r1; b += SP_THREADS) {
@@ -81,8 +88,9 @@ __global__ void __launch_bounds__(SP_THREADS) kv_plan_kernel(const PlanArgs a) {
       ++with_rows;
     }
   }
-  most = min(plan_reduce(most, sm, true), a.shared[g]);
-  if (plan_reduce(with_rows, sm, false) < 2 && __syncthreads_count(with_rows) < 2) most = 0;
+  const int said = a.shared[g];
+  plan_reduce(most, with_rows, sm[1]);
+  most = with_rows < 2 ? 0 : min(most, said);
   // the first entry on which a row of the table differs from the group's first
   const int pages = most <= 0 ? 0 : static_cast<int>((most + (1ll << a.page_shift) - 1) >> a.page_shift);
   const int* first = a.table + r0 * a.table_stride;
@@ -106,7 +114,7 @@ __global__ void __launch_bounds__(SP_THREADS) kv_plan_kernel(const PlanArgs a) {
     for (int u = SP_BATCH - 1; u >= 0; --u)
       if (own[u] != ref[u]) agree = min(agree, j0 + 32 * u);
   }
-  agree = plan_reduce(agree, sm, true);
+  plan_reduce(agree, none, sm[2]);
   if (ctas > 1) {
     if (tid == 0) sm_agree = agree;
     cluster_sync();
@@ -115,34 +123,169 @@ __global__ void __launch_bounds__(SP_THREADS) kv_plan_kernel(const PlanArgs a) {
     cluster_arrive();
   }
   const int keys = agree < pages ? agree << a.page_shift : max(0, most);
+  auto entry = [&](int i, int q0, int q1, int len, int start, int row, int prefix) {
+    int4* e = reinterpret_cast<int4*>(a.list + i);
+    e[0] = make_int4(q0, q1, len, start);
+    e[1] = make_int4(row, prefix, 0, 0);
+  };
+  auto request = [&](int b, int start) { entry(a.n + b, a.cu[b], a.cu[b + 1], a.lens[b], start, b, 0); };
   if (rank == 0) {
-    if (tid == 0) {
-      const int q0 = a.cu[r0];
-      a.rows[2 * g] = q0;
-      a.rows[2 * g + 1] = keys > 0 ? a.cu[r1] : q0;
-      a.plens[g] = keys;
-      a.row_of[g] = r0;
-    }
-    for (int b = r0 + tid; b < r1; b += SP_THREADS) a.start[b] = keys;
+    if (tid == 0) entry(g, a.cu[r0], keys > 0 ? a.cu[r1] : a.cu[r0], keys, 0, r0, 1);
+    for (int b = r0 + tid; b < r1; b += SP_THREADS) request(b, keys);
     // requests of no group
     if (g == 0)
-      for (int b = tid; b < r0; b += SP_THREADS) a.start[b] = 0;
-    if (g == gridDim.y - 1)
-      for (int b = r1 + tid; b < B; b += SP_THREADS) a.start[b] = 0;
+      for (int b = tid; b < r0; b += SP_THREADS) request(b, 0);
+    if (g == a.n - 1)
+      for (int b = r1 + tid; b < B; b += SP_THREADS) request(b, 0);
   }
   __syncwarp();
   if (ctas > 1) cluster_wait();             // nobody reads this CTA's word any more
 }
 
+// The parts of one set: where a pass's kernel (rows of a unit, CTAs) left them.
+struct JoinSet {
+  KvStates states;
+  const float* parts;
+  int unit;
+  int ctas;
+};
+struct JoinArgs {
+  JoinSet prefix, own;
+  const int* cu;
+  int requests;
+  long long rows;             // tokens x q_heads
+  int q_heads;
+  void* O;
+  int o_dtype;
+  long long o_ts, o_hs;
+};
+
+constexpr int SJ_THREADS = 256, SJ_LANES = 4, SJ_BATCH = 3;
+
+// SJ_LANES lanes take eight columns of a row, each every SJ_LANES-th of its parts --
+// the prefix's, then its own -- SJ_BATCH of them with their loads together, and meet by
+// shuffles.  The parts' reads bound it: 64 rows of 32 heads behind 8192 keys have 20
+// parts a row, 20 MB from L2.
+template <int D>
+__global__ void __launch_bounds__(SJ_THREADS) kv_join_states_kernel(const JoinArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, k = tid & (SJ_LANES - 1);
+  const long long at = (static_cast<long long>(blockIdx.x) * SJ_THREADS + tid) / SJ_LANES;
+  const long long row = at / (D / 8);
+  const int col = 8 * static_cast<int>(at % (D / 8));
+  if (row >= a.rows) return;                // (SJ_LANES lanes alike)
+  const long long token = row / a.q_heads;
+  const int head = static_cast<int>(row - token * a.q_heads);
+  if (token < a.cu[0] || token >= a.cu[a.requests]) return;   // of no request: left as it is
+  const int4 own = __ldcg(a.own.states.rec + row);
+  if (own.w & KV_REC_DONE) return;
+  const bool has_prefix = (own.w & KV_REC_PREFIX) != 0;
+  const int4 pre = has_prefix ? __ldcg(a.prefix.states.rec + row) : make_int4(0, 0, 0, 0);
+  // (offsets that go up and down may leave a row without a word of this call's)
+  auto sound = [](const int4& r, const JoinSet& s) {
+    return r.z == 0 || (r.z > 1 && r.y >= 0 && r.y + r.z <= s.ctas && r.x >= 0 && r.x < 2 * s.ctas &&
+                        (r.w & 0xFFFF) < s.unit);
+  };
+  if (!sound(own, a.own) || !sound(pre, a.prefix)) return;
+  const int n_pre = has_prefix ? max(1, pre.z) : 0, n = n_pre + max(1, own.z);
+  auto read = [&](int i, float& m, float& l, float (&v)[8]) {
+    const bool of_prefix = i < n_pre;
+    const JoinSet& s = of_prefix ? a.prefix : a.own;
+    const int4 r = of_prefix ? pre : own;
+    const int p = of_prefix ? i : i - n_pre, rr = r.w & 0xFFFF;
+    if (r.z == 0) {
+      const float2 ml = __ldcg(s.states.ml + row);
+      m = ml.x;
+      l = ml.y;
+      ld_global_cg_v8(s.states.o + row * D + col, v);
+    } else {
+      const int slot = p == 0 ? r.x : 2 * (r.y + p);
+      const float* part = s.parts + static_cast<long long>(slot) * s.unit * (D + 2);
+      m = __ldcg(part + s.unit * D + rr);
+      l = __ldcg(part + s.unit * (D + 1) + rr);
+      // the prompt kernel's parts are [8 columns][row][column]
+      const float* o = s.unit == 256 ? part + (col / 8 * 256 + rr) * 8 : part + rr * D + col;
+      if ((reinterpret_cast<uintptr_t>(o) & 31) == 0) {
+        ld_global_cg_v8(o, v);
+      } else {
+        const float4 x = ld_global_cg_f4(o), y = ld_global_cg_f4(o + 4);
+        v[0] = x.x;
+        v[1] = x.y;
+        v[2] = x.z;
+        v[3] = x.w;
+        v[4] = y.x;
+        v[5] = y.y;
+        v[6] = y.z;
+        v[7] = y.w;
+      }
+    }
+  };
+  float top = -INFINITY, sum = 0.0f, acc[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+  auto add = [&](float m, float l, const float (&v)[8]) {
+    const float t = fmaxf(top, m);
+    const float before = top == t ? 1.0f : ex2_approx(top - t);
+    const float w = m == t ? 1.0f : ex2_approx(m - t);
+    top = t;
+    sum = fmaf(w, l, sum * before);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, v[e], acc[e] * before);
+  };
+  for (int i0 = k; i0 < n; i0 += SJ_LANES * SJ_BATCH) {
+    float m[SJ_BATCH], l[SJ_BATCH], v[SJ_BATCH][8];
+#pragma unroll
+    for (int u = 0; u < SJ_BATCH; ++u)
+      if (i0 + SJ_LANES * u < n) read(i0 + SJ_LANES * u, m[u], l[u], v[u]);
+#pragma unroll
+    for (int u = 0; u < SJ_BATCH; ++u)
+      if (i0 + SJ_LANES * u < n) add(m[u], l[u], v[u]);
+  }
+  const unsigned lanes = ((1u << SJ_LANES) - 1u) << (tid & 31 & ~(SJ_LANES - 1));
+#pragma unroll
+  for (int d = 1; d < SJ_LANES; d <<= 1) {
+    // both of two lanes add the lower one's first: the same bits in both
+    float m = __shfl_xor_sync(lanes, top, d), l = __shfl_xor_sync(lanes, sum, d);
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __shfl_xor_sync(lanes, acc[e], d);
+    if (k & d) {
+      const float mt = top, lt = sum;
+      top = m;
+      sum = l;
+      m = mt;
+      l = lt;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = acc[e];
+        acc[e] = v[e];
+        v[e] = x;
+      }
+    }
+    add(m, l, v);
+  }
+  if (k != 0) return;
+  const float inv = kv_inverse(sum, top != -INFINITY);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[e] *= inv;
+  kv_store8(a.O, a.o_dtype, token * a.o_ts + head * a.o_hs + col, acc);
+}
+
 int64_t up32(int64_t n) { return (n + 31) / 32 * 32; }
 
-// The workspace: the plan's integers, the rows' states, the two passes' scratch.
+// The workspace: the list, the rows' states of both sets, the passes' parts.
 struct Layout {
-  int64_t start, rows, plens, row_of, o, ml, prefix, own, total;
+  int64_t list, o[2], ml[2], rec[2], parts[2], total;
 };
-// rows of a group at the most: with one group all tokens
+// Room for either kernel that the rows may want, so that less of anything never needs
+// more.
+int64_t parts_bytes(int64_t rows, int64_t d, int sms) {
+  size_t n = std::max(kv_pass_workspace_bytes(8, d, sms), kv_pass_workspace_bytes(16, d, sms));
+  if (kv_pass_unit(rows) == 256) n = std::max(n, kv_pass_workspace_bytes(256, d, sms));
+  return static_cast<int64_t>(n);
+}
 Layout layout_of(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t max_q,
-                 int64_t requests, int64_t groups) {
+                 int64_t requests, int64_t groups, int sms) {
   Layout l;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -150,35 +293,60 @@ Layout layout_of(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d, i
     at += up32(bytes);
     return here;
   };
-  l.start = take(4 * requests);
-  l.rows = take(8 * groups);
-  l.plens = take(4 * groups);
-  l.row_of = take(4 * groups);
-  l.o = take(4 * tokens * q_heads * d);
-  l.ml = take(8 * tokens * q_heads);
-  l.prefix = take(static_cast<int64_t>(kv_pass_workspace_bytes(q_heads / kv_heads, d, tokens)));
-  l.own = take(static_cast<int64_t>(kv_pass_workspace_bytes(q_heads / kv_heads, d, max_q)));
+  const int64_t group = q_heads / kv_heads;
+  l.list = take(static_cast<int64_t>(sizeof(KvEntry)) * (requests + groups));
+  for (int i = 0; i < 2; ++i) {
+    l.o[i] = take(4 * tokens * q_heads * d);
+    l.ml[i] = take(8 * tokens * q_heads);
+    l.rec[i] = take(16 * tokens * q_heads);
+    l.parts[i] = take(parts_bytes((i == 0 ? tokens : max_q) * group, d, sms));
+  }
   l.total = at;
   return l;
+}
+
+template <class... Args, class... Given>
+cudaError_t launch_dependent(void (*kern)(Args...), dim3 grid, int threads, bool dependent, int cluster,
+                             cudaStream_t st, const Given&... given) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  if (dependent) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, given...);
 }
 
 }  // namespace
 
 size_t kv_attention_shared_workspace_bytes(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d,
                                            int64_t max_q, int64_t requests, int64_t groups) {
-  if (requests > SP_MAX || groups > SP_MAX) return 0;
+  const int sms = kv_sm_count();
+  if (sms <= 0 || requests > SP_MAX || groups > SP_MAX) return 0;
   // (16 bytes to bring a workspace that begins at a 16-byte boundary to a 32-byte one)
-  return static_cast<size_t>(layout_of(tokens, q_heads, kv_heads, d, max_q, requests, groups).total + 16);
+  return static_cast<size_t>(layout_of(tokens, q_heads, kv_heads, d, max_q, requests, groups, sms).total + 16);
 }
 
 cudaError_t launch_kv_attention_shared(const KvAttn& q, const KvGroups& g, cudaStream_t st) {
-  const int64_t kv_heads = q.cache.heads;
-  const size_t need = kv_attention_shared_workspace_bytes(q.tokens, q.q_heads, kv_heads, q.cache.d, q.max_q,
+  const KvCache& c = q.cache;
+  const int sms = kv_sm_count();
+  const size_t need = kv_attention_shared_workspace_bytes(q.tokens, q.q_heads, c.heads, c.d, q.max_q,
                                                           q.requests, g.n);
   // without groups or room for the states: each request for itself
   if (g.n == 0 || need == 0 || q.ws == nullptr || q.ws_bytes < need) return launch_kv_attention(q, st);
-  const Layout l = layout_of(q.tokens, q.q_heads, kv_heads, q.cache.d, q.max_q, q.requests, g.n);
+  const Layout l = layout_of(q.tokens, q.q_heads, c.heads, c.d, q.max_q, q.requests, g.n, sms);
   char* ws = static_cast<char*>(q.ws) + (reinterpret_cast<uintptr_t>(q.ws) & 16);
+  KvEntry* list = reinterpret_cast<KvEntry*>(ws + l.list);
   PlanArgs p{};
   p.lens = q.lens;
   p.cu = q.cu;
@@ -186,53 +354,68 @@ cudaError_t launch_kv_attention_shared(const KvAttn& q, const KvGroups& g, cudaS
   p.shared = g.shared;
   p.table = q.table;
   p.table_stride = q.table_stride;
-  p.page_shift = kv_page_shift(q.cache.page);
   p.requests = static_cast<int>(q.requests);
-  const int64_t most = q.width << kv_page_shift(q.cache.page);
+  p.n = static_cast<int>(g.n);
+  const int64_t most = q.width << kv_page_shift(c.page);
   p.capacity = static_cast<int>(most < 0x7FFFFF00 ? most : 0x7FFFFF00);
-  p.start = reinterpret_cast<int*>(ws + l.start);
-  p.rows = reinterpret_cast<int*>(ws + l.rows);
-  p.plens = reinterpret_cast<int*>(ws + l.plens);
-  p.row_of = reinterpret_cast<int*>(ws + l.row_of);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(g.n > SP_MANY_GROUPS ? 1 : SP_CLUSTER, static_cast<unsigned>(g.n));
-  cfg.blockDim = dim3(SP_THREADS);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cfg.gridDim.x;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kv_plan_kernel, p);
+  p.page_shift = kv_page_shift(c.page);
+  p.list = list;
+  const bool alone = g.n > SP_MANY_GROUPS || q.requests * q.width <= SP_ENTRIES * g.n;
+  const int cluster = alone ? 1 : SP_CLUSTER;
+  cudaError_t e = launch_dependent(kv_plan_kernel, dim3(static_cast<unsigned>(cluster), static_cast<unsigned>(g.n)),
+                                   SP_THREADS, false, cluster, st, p);
   if (e != cudaSuccess) return e;
+  JoinArgs j{};
+  JoinSet* sets[2] = {&j.prefix, &j.own};
+  for (int i = 0; i < 2; ++i) {
+    sets[i]->states.o = reinterpret_cast<float*>(ws + l.o[i]);
+    sets[i]->states.ml = reinterpret_cast<float2*>(ws + l.ml[i]);
+    sets[i]->states.rec = reinterpret_cast<int4*>(ws + l.rec[i]);
+    sets[i]->parts = reinterpret_cast<const float*>(ws + l.parts[i]);
+  }
+  // Which kernels: one for both where their units are alike, or the group's rows make two of
+  // the requests' units at most.
+  const int64_t group = q.q_heads / c.heads;
+  const int64_t rows = std::max<int64_t>(1, q.tokens / g.n) * group;
+  j.prefix.unit = kv_pass_prefix_unit(rows, most);
+  j.own.unit = kv_pass_unit(q.max_q * group);
+  const bool one = j.own.unit != 256 && j.prefix.unit != 256 &&
+                   (j.own.unit == j.prefix.unit || rows <= 2 * j.own.unit);
+  if (one) j.prefix.unit = j.own.unit;
+  for (int i = 0; i < 2; ++i) sets[i]->ctas = kv_pass_ctas(sets[i]->unit, sms);
   KvPassArgs pass{};
-  pass.state.o = reinterpret_cast<float*>(ws + l.o);
-  pass.state.ml = reinterpret_cast<float2*>(ws + l.ml);
-  // prefixes: a group in a request's place, whose rows all see all of its keys
+  pass.prefix = j.prefix.states;
+  pass.own = j.own.states;
   KvAttn a = q;
-  a.cu = p.rows;
-  a.lens = p.plens;
-  a.requests = g.n;
-  a.max_q = std::max<int64_t>(1, q.tokens / g.n);
-  a.causal = 0;
-  a.o_ts = a.o_hs = 0;                      // O is not written
-  a.ws = ws + l.prefix;
-  a.ws_bytes = static_cast<size_t>(l.own - l.prefix);
-  pass.row_of = p.row_of;
-  pass.cu_step = 2;
-  pass.state.pass = KV_PREFIX;
-  e = launch_kv_pass(a, pass, st);
-  if (e != cudaSuccess) return e;
-  a = q;
-  a.ws = ws + l.own;
-  a.ws_bytes = static_cast<size_t>(l.total - l.own);
-  pass.start = p.start;
-  pass.row_of = nullptr;
-  pass.cu_step = 1;
-  pass.state.pass = KV_OWN;
-  return launch_kv_pass(a, pass, st);
+  a.window = 0;
+  if (one) {
+    j.prefix.parts = j.own.parts;
+    pass.list = list;
+    pass.entries = g.n + q.requests;
+  } else {
+    pass.list = list;
+    pass.entries = g.n;
+    a.ws = ws + l.parts[0];
+    a.ws_bytes = static_cast<size_t>(kv_pass_workspace_bytes(j.prefix.unit, c.d, sms));
+    if ((e = launch_kv_pass(a, pass, j.prefix.unit, true, sms, st)) != cudaSuccess) return e;
+    pass.list = list + g.n;
+    pass.entries = q.requests;
+  }
+  a.ws = ws + l.parts[1];
+  a.ws_bytes = static_cast<size_t>(kv_pass_workspace_bytes(j.own.unit, c.d, sms));
+  if ((e = launch_kv_pass(a, pass, j.own.unit, one, sms, st)) != cudaSuccess) return e;
+  j.cu = q.cu;
+  j.requests = static_cast<int>(q.requests);
+  j.rows = q.tokens * q.q_heads;
+  j.q_heads = static_cast<int>(q.q_heads);
+  j.O = q.O;
+  j.o_dtype = q.o_dtype;
+  j.o_ts = q.o_ts;
+  j.o_hs = q.o_hs;
+  const int64_t lanes = j.rows * (c.d / 8) * SJ_LANES;
+  const dim3 grid(static_cast<unsigned>((lanes + SJ_THREADS - 1) / SJ_THREADS));
+  return c.d == 64 ? launch_dependent(kv_join_states_kernel<64>, grid, SJ_THREADS, true, 1, st, j)
+                   : launch_dependent(kv_join_states_kernel<128>, grid, SJ_THREADS, true, 1, st, j);
 }
 
 }  // namespace mxk
