@@ -52,8 +52,7 @@ inline KvView kv_view(const KvAttn& q) {
   return v;
 }
 
-// One request: its rows of Q (first, count) and its length.  Whatever the
-// arrays hold, the rows lie in Q and the length in the table.
+// One request: its rows of Q (first, count) and its length.
 struct KvReq {
   long long q0;
   int n;
@@ -65,33 +64,41 @@ struct KvShReq : KvReq {
   int prefix;
 };
 
-template <bool SH>
-__device__ __forceinline__ auto kv_request(const KvView& v, int b) {
-  std::conditional_t<SH, KvShReq, KvReq> r;
-  long long s, e;
-  int len;
-  if constexpr (SH) {
-    // (another kernel of the same call wrote these: around L1)
-    const int4* entry = reinterpret_cast<const int4*>(v.list + b);
-    const int4 x = __ldcg(entry);
-    const int2 y = __ldcg(reinterpret_cast<const int2*>(entry + 1));
-    s = x.x;
-    e = x.y;
-    len = x.z;
-    r.start = x.w < 0 ? 0 : (x.w > v.capacity ? v.capacity : x.w);
-    r.row = y.x;
-    r.prefix = y.y;
-  } else {
-    s = v.cu[b];
-    e = v.cu[b + 1];
-    len = v.lens[b];
-  }
+// Whatever the arrays hold, the rows lie in Q and the keys in the table.
+template <class Req>
+__device__ __forceinline__ void kv_clip(const KvView& v, Req& r, long long s, long long e, int len) {
   s = s < 0 ? 0 : (s > v.tokens ? v.tokens : s);
   e = e < s ? s : (e > v.tokens ? v.tokens : e);
   r.q0 = s;
   r.n = static_cast<int>(e - s);
   r.len = len < 0 ? 0 : (len > v.capacity ? v.capacity : len);
+}
+
+__device__ __forceinline__ KvReq kv_request(const KvView& v, int b) {
+  KvReq r;
+  kv_clip(v, r, v.cu[b], v.cu[b + 1], v.lens[b]);
   return r;
+}
+
+// An entry of the list, as its first 16 bytes and the next 8 have it.
+__device__ __forceinline__ KvShReq kv_entry(const KvView& v, int4 x, int2 y) {
+  KvShReq r;
+  kv_clip(v, r, x.x, x.y, x.z);
+  r.start = x.w < 0 ? 0 : (x.w > v.capacity ? v.capacity : x.w);
+  r.row = y.x;
+  r.prefix = y.y;
+  return r;
+}
+
+template <bool SH>
+__device__ __forceinline__ auto kv_request_of(const KvView& v, int b) {
+  if constexpr (SH) {
+    // (another kernel of the same call wrote these: around L1)
+    const int4* entry = reinterpret_cast<const int4*>(v.list + b);
+    return kv_entry(v, __ldcg(entry), __ldcg(reinterpret_cast<const int2*>(entry + 1)));
+  } else {
+    return kv_request(v, b);
+  }
 }
 
 // Token i of a request stands at position len - n + i and sees keys

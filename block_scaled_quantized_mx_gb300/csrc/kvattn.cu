@@ -81,6 +81,9 @@ constexpr int ka_tk() {
   return D == 64 ? 256 : 128;
 }
 
+// SH: entries of a CTA at the least.
+constexpr int KA_LEAST = 3;
+
 // Entries of a unit besides its tiles, for the time it takes to begin and end one.
 template <bool SH>
 constexpr int ka_over() {
@@ -200,7 +203,7 @@ struct KaReq {
 template <int ROWS, int TK, bool SH>
 __device__ __forceinline__ KaReq<SH> ka_request(const KaArgs& a, int b) {
   KaReq<SH> q;
-  q.r = kv_request<SH>(a.v, b);
+  q.r = kv_request_of<SH>(a.v, b);
   const long long rows = static_cast<long long>(q.r.n) * a.v.group;
   // a window's first tile is one of the request's; behind a prefix tiles begin with its
   // last page, so that as few as possible hold the request's own keys
@@ -321,7 +324,8 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
   }
   // SH: the plan is the kernel before this one, or the one before a prefixes' pass that
   // lets this one begin only when it has seen the plan itself; that pass's results are waited
-  // for at the end, for the kernel behind this one.
+  // for by the last CTA at its end, for the kernel behind this one (the others leave, for the
+  // CTAs that wait for their SMs).
   if constexpr (SH)
     if (a.wait) asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- the list: its length, and where this CTA's stretch begins
@@ -346,13 +350,14 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
     if (i < warp) before += sm_scan[i];
     total += sm_scan[i];
   }
-  const long long ctas = min(static_cast<long long>(gridDim.x), total);
+  // SH: the CTAs that there is little for leave their SMs to the next kernel's at once
+  const long long ctas = min(static_cast<long long>(gridDim.x), SH ? max(1ll, ka_div(total, KA_LEAST)) : total);
   const long long cta = blockIdx.x;
   KaJoin<ROWS>* join = SH ? nullptr : reinterpret_cast<KaJoin<ROWS>*>(a.joins) + cta;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (cta >= ctas) {                         // the whole CTA: nothing was started
+  if (cta >= ctas || total == 0) {           // the whole CTA: nothing was started
     if (!SH && a.ws != nullptr && tid == 0) join->live = 0;
-    if constexpr (SH) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (SH && blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
   // the first `longer` CTAs take one entry more than the others
@@ -630,7 +635,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
              clock64() - t0 < MXK_WAIT_LIMIT_CYCLES) {
       }
     }
-    if constexpr (SH) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (SH && blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
 

@@ -80,6 +80,11 @@ constexpr int KP_OVER = 4;
 constexpr int KP_PG = 8;                   // blocks whose page data is kept
 constexpr int KP_STAGES = 2;               // f16 tiles of K, and of V
 constexpr int KP_MAX_REQUESTS = 16384;
+constexpr int KP_KEPT = 1024;              // entries of the list that a CTA keeps at first
+// SH: entries of a CTA at the least.  A few blocks more on fewer SMs, the others being left
+// to the next kernel's CTAs at once, take less time than both kernels one after the
+// other: beginning and ending one takes as long as four blocks.
+constexpr int KP_LEAST = 6;
 
 // One block: the scales of each 16 of its keys, and what there is of it.
 struct KpPages {
@@ -148,7 +153,7 @@ struct KpWalk {
   long long unit_start, unit_end;
 
   __device__ __forceinline__ void enter(const KvView& v) {   // b, rt -> the rest
-    r = kv_request<SH>(v, b);
+    r = kv_request_of<SH>(v, b);
     tiles = kp_row_tiles(v, r);
     if (rt < tiles) blocks = kp_blocks(v, r, rt, block0);
   }
@@ -211,7 +216,8 @@ struct KpSmem {
   static constexpr int TOTAL = WALK_OFF + static_cast<int>(sizeof(KpWalk<SH>));
   static constexpr int ALLOC = TOTAL + 1024;
   static_assert(ALLOC <= 232448, "shared memory budget");
-  static_assert(PG_OFF >= KP_MAX_REQUESTS * 4, "the plan's array fits in the operand tiles");
+  static_assert(PG_OFF >= KP_MAX_REQUESTS * 4 + KP_KEPT * static_cast<int>(sizeof(KvEntry)),
+                "the plan's arrays fit in the operand tiles");
 };
 
 struct KpArgs {
@@ -382,8 +388,8 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // SH: the plan is the kernel before this one (which is waited for before others may
   // follow), or the one before a prefixes' pass that lets this one begin only when it has
-  // seen the plan itself; that pass's results are waited for at the end, for the kernel
-  // behind this one.
+  // seen the plan itself; that pass's results are waited for by the last CTA at its end, for
+  // the kernel behind this one (the others leave, for the CTAs that wait for their SMs).
   if constexpr (SH)
     if (a.wait) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -396,15 +402,28 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     int* sm_rt = reinterpret_cast<int*>(gbase);                        // requests + 1
     long long* sm_scan = reinterpret_cast<long long*>(gbase + L::PG_OFF);
     const int B = a.v.requests;
+    // SH: the entries are read once, where there is room for them
+    int4* sm_entry = reinterpret_cast<int4*>(gbase + KP_MAX_REQUESTS * 4);
+    const bool kept = SH && B <= KP_KEPT;
+    if (kept) {
+      for (int i = tid; i < 2 * B; i += KP_THREADS)
+        sm_entry[i] = __ldcg(reinterpret_cast<const int4*>(a.v.list) + i);
+      __syncthreads();
+    }
+    auto request = [&](int b) -> Req {
+      if constexpr (SH)
+        if (kept) return kv_entry(a.v, sm_entry[2 * b], make_int2(sm_entry[2 * b + 1].x, sm_entry[2 * b + 1].y));
+      return kv_request_of<SH>(a.v, b);
+    };
     const KvTileList list(a.v.tokens, a.v.group, KP_ROWS, B);
     const int per = (B + KP_THREADS - 1) / KP_THREADS;
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
     long long mine = 0, tiles;
-    for (int b = b0; b < b1; ++b) mine += kp_row_tiles(a.v, kv_request<SH>(a.v, b));
+    for (int b = b0; b < b1; ++b) mine += kp_row_tiles(a.v, request(b));
     long long at = kp_scan(mine, sm_scan, tiles);
     for (int b = b0; b < b1; ++b) {
       sm_rt[b] = list.start(at);
-      at += kp_row_tiles(a.v, kv_request<SH>(a.v, b));
+      at += kp_row_tiles(a.v, request(b));
     }
     tiles = list.clip(tiles);
     __syncthreads();
@@ -414,12 +433,12 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     auto each = [&](auto f) {
       if (f0 >= f1) return;
       int b = KvTileList::request(sm_rt, B, f0);
-      Req r = kv_request<SH>(a.v, b);
+      Req r = request(b);
       int rt = static_cast<int>(f0 - sm_rt[b]), n = kp_row_tiles(a.v, r);
       for (long long i = f0; i < f1; ++i, ++rt) {
         while (rt >= n) {
           rt = 0;
-          r = kv_request<SH>(a.v, ++b);
+          r = request(++b);
           n = kp_row_tiles(a.v, r);
         }
         if (!f(b, rt, r)) return;
@@ -432,9 +451,9 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       return true;
     });
     long long before = kp_scan(mine, sm_scan, total);
-    ctas = min(static_cast<long long>(gridDim.x), total);
+    ctas = min(static_cast<long long>(gridDim.x), SH ? max(1ll, total / KP_LEAST) : total);
     w0 = total * blockIdx.x / max(1ll, ctas);
-    if (blockIdx.x < ctas && w0 >= before && w0 < before + mine) {
+    if (blockIdx.x < ctas && total > 0 && w0 >= before && w0 < before + mine) {
       long long p = before;
       each([&](int b, int rt, const Req& r) {
         int first;
@@ -463,8 +482,8 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     __syncthreads();
     KpJoin* join = a.joins ? a.joins + blockIdx.x : nullptr;
     if (tid == 0 && join) join->live = 0;
-    if (blockIdx.x >= ctas) {                // the whole CTA: nothing was started
-      if constexpr (SH) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blockIdx.x >= ctas || total == 0) {  // the whole CTA: nothing was started
+      if (SH && blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
       return;
     }
   }
@@ -619,6 +638,28 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           id2 = page_of(j + 2);
           scales_of(id1);
           const long long unit = id >= 0 ? static_cast<long long>(id) * a.v.heads + head : 0;
+          // the codes: a box per page, by the lane of its first 16 keys
+          const bool loads = id >= 0 && ((16 * lane) & ((1 << shift) - 1)) == 0;
+          const unsigned boxes = __popc(__ballot_sync(0xFFFFFFFFu, loads));
+          auto codes = [&](int kv) {
+            const int slot = raw_it % L::RAW;
+            if (!mbar_wait(bar_raw_empty + 8 * slot, ((raw_it / L::RAW) & 1) ^ 1, abort)) {
+              if (lane == 0) kp_timeout(abort, 0x5e);
+              return false;
+            }
+            const uint32_t full = bar_raw + 8 * slot;
+            if (lane == 0) mbar_arrive_expect_tx(full, boxes * (D << shift));
+            __syncwarp();
+            if (loads)
+              tma_load_2d(base + L::RAW_OFF + slot * L::RAW_BYTES + 16 * lane * D,
+                          kv ? &tmV : &tmK, full, 0, static_cast<int>(unit << shift));
+            ++raw_it;
+            return true;
+          };
+          // K's are on their way before the scales are waited for; V's slot may be one that
+          // the block before still needs, and nobody waits for it with that block's data
+          ok = codes(0);
+          if (!ok) break;
           float kf = __uint_as_float(0x7FC00000u);
           float ve = 0.0f;
           if (kc != 0xFFu && vc != 0xFFu) {
@@ -646,25 +687,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           ++bt;
           held = true;
           if (j + 1 < count) release(1);       // (of the last one: when the next segment is known)
-          // the codes: a box per page, by the lane of its first 16 keys
-          const bool loads = id >= 0 && ((16 * lane) & ((1 << shift) - 1)) == 0;
-          const unsigned boxes = __popc(__ballot_sync(0xFFFFFFFFu, loads));
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            const int slot = raw_it % L::RAW;
-            if (!mbar_wait(bar_raw_empty + 8 * slot, ((raw_it / L::RAW) & 1) ^ 1, abort)) {
-              if (lane == 0) kp_timeout(abort, 0x5e);
-              ok = false;
-              break;
-            }
-            const uint32_t full = bar_raw + 8 * slot;
-            if (lane == 0) mbar_arrive_expect_tx(full, boxes * (D << shift));
-            __syncwarp();
-            if (loads)
-              tma_load_2d(base + L::RAW_OFF + slot * L::RAW_BYTES + 16 * lane * D,
-                          kv ? &tmV : &tmK, full, 0, static_cast<int>(unit << shift));
-            ++raw_it;
-          }
+          ok = codes(1);
           if (!ok) break;
         }
       }
@@ -1184,7 +1207,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     tc_fence_after();
     tmem_dealloc_cg<1>(tmem_base, KP_TMEM_COLS);
   }
-  if constexpr (SH) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (SH && blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Join the parts of the unit that begins in CTA blockIdx.x's stretch, in CTA

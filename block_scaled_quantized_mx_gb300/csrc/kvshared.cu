@@ -35,7 +35,7 @@ constexpr int SP_MAX = 16384;               // requests, and groups
 // CTAs to a group where its rows of the table are long, and the groups few
 constexpr int SP_CLUSTER = 8;
 constexpr int SP_MANY_GROUPS = 64;
-constexpr int64_t SP_ENTRIES = 4096;        // of the table, for one CTA
+constexpr int64_t SP_ENTRIES = 16384;       // of the table, for one CTA
 constexpr int SP_BATCH = 8;                 // table entries of a lane on their way together
 
 struct PlanArgs {
