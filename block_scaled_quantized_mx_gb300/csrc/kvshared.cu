@@ -160,13 +160,15 @@ struct JoinArgs {
   long long o_ts, o_hs;
 };
 
-constexpr int SJ_THREADS = 256, SJ_LANES = 4, SJ_BATCH = 3;
+constexpr int SJ_THREADS = 256, SJ_BATCH = 3;
+constexpr int64_t SJ_FEW_ROWS = 4096;
 
 // SJ_LANES lanes take eight columns of a row, each every SJ_LANES-th of its parts --
 // the prefix's, then its own -- SJ_BATCH of them with their loads together, and meet by
-// shuffles.  The parts' reads bound it: 64 rows of 32 heads behind 8192 keys have 20
-// parts a row, 20 MB from L2.
-template <int D>
+// shuffles.  Four lanes where the rows are few: their parts then are many (64 rows of 32
+// heads behind 8192 keys have 12 a row), and the wait for one read after the other bounds it; one
+// lane where the rows fill the SMs (16384 rows of 5 parts: 25 us with four).
+template <int D, int SJ_LANES>
 __global__ void __launch_bounds__(SJ_THREADS) kv_join_states_kernel(const JoinArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, k = tid & (SJ_LANES - 1);
@@ -412,10 +414,11 @@ cudaError_t launch_kv_attention_shared(const KvAttn& q, const KvGroups& g, cudaS
   j.o_dtype = q.o_dtype;
   j.o_ts = q.o_ts;
   j.o_hs = q.o_hs;
-  const int64_t lanes = j.rows * (c.d / 8) * SJ_LANES;
-  const dim3 grid(static_cast<unsigned>((lanes + SJ_THREADS - 1) / SJ_THREADS));
-  return c.d == 64 ? launch_dependent(kv_join_states_kernel<64>, grid, SJ_THREADS, true, 1, st, j)
-                   : launch_dependent(kv_join_states_kernel<128>, grid, SJ_THREADS, true, 1, st, j);
+  const int lanes = j.rows <= SJ_FEW_ROWS ? 4 : 1;
+  const dim3 grid(static_cast<unsigned>((j.rows * (c.d / 8) * lanes + SJ_THREADS - 1) / SJ_THREADS));
+  auto kern = c.d == 64 ? (lanes == 4 ? kv_join_states_kernel<64, 4> : kv_join_states_kernel<64, 1>)
+                        : (lanes == 4 ? kv_join_states_kernel<128, 4> : kv_join_states_kernel<128, 1>);
+  return launch_dependent(kern, grid, SJ_THREADS, true, 1, st, j);
 }
 
 }  // namespace mxk
