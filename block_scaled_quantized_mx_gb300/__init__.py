@@ -51,7 +51,8 @@ EXPORTS = ("mx_data_bytes", "mx_scale_bytes", "mx_quantize", "mx_gemm",
            "mx_kv_attention_workspace_bytes", "mx_kv_attention",
            "mx_rmsnorm_quantize", "mx_dequantize", "mx_rope",
            "mx_kv_fork", "mx_kv_own", "mx_kv_release",
-           "mx_kv_attention_shared_workspace_bytes", "mx_kv_attention_shared")
+           "mx_kv_attention_shared_workspace_bytes", "mx_kv_attention_shared",
+           "mx_set_shared_bytes")
 
 
 class MXError(RuntimeError):
@@ -212,6 +213,8 @@ def lib() -> ctypes.CDLL:
                                          i64, p, p, i64, i64, p, p, i64, p, i32,
                                          i64, i64, i32, ctypes.c_float, p, sz,
                                          p]
+    L.mx_set_shared_bytes.restype = i32
+    L.mx_set_shared_bytes.argtypes = [i64]
     _lib = L
     return L
 
@@ -1256,3 +1259,9 @@ def set_tile_width(tbn: int) -> None:
     """Fix the GEMMs' output-tile width (128 or 256) for later calls, or let
     the library pick it per shape (0, the default)."""
     _check(lib().mx_set_tile_width(int(tbn)), "mx_set_tile_width")
+
+
+def set_shared_bytes(nbytes: int) -> None:
+    """The bytes of reads that sharing a prefix must save for
+    mx_kv_attention_shared to do it: 0 for always, -1 for the default."""
+    _check(lib().mx_set_shared_bytes(int(nbytes)), "mx_set_shared_bytes")

@@ -802,5 +802,11 @@ mx_status mx_set_tile_width(int32_t tbn) {
   return MX_OK;
 }
 
+mx_status mx_set_shared_bytes(int64_t bytes) {
+  if (bytes < -1) return MX_ERR_INVALID_ARG;
+  mxk::kv_set_shared_bytes(bytes);
+  return MX_OK;
+}
+
 }  // extern "C"
 #pragma GCC visibility pop

@@ -146,6 +146,7 @@ struct KvGroups {
 size_t kv_attention_shared_workspace_bytes(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d,
                                            int64_t max_q, int64_t requests, int64_t groups);
 cudaError_t launch_kv_attention_shared(const KvAttn& a, const KvGroups& g, cudaStream_t st);
+void kv_set_shared_bytes(int64_t bytes);    // negative: the default
 
 // Its kernel for many rows per request (kvprompt.cu), up to
 // kv_prompt_max_requests() requests.

@@ -18,6 +18,7 @@
 // Precision: as those kernels have it; (O, m, l) and their joining are fp32, in a fixed
 // order.
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "common.cuh"
@@ -38,6 +39,15 @@ constexpr int SP_MANY_GROUPS = 64;
 constexpr int64_t SP_ENTRIES = 16384;       // of the table, for one CTA
 constexpr int SP_BATCH = 8;                 // table entries of a lane on their way together
 
+// A prefix is worth a pass where it saves this many bytes of reads.  They come from L2
+// for all requests but one, so that mx_kv_attention loses little by short ones.  Measured
+// with 8 cache heads of 128 values, one group (shared against mx_kv_attention; bytes saved):
+// 4 requests, 8192 keys 19.5 against 16.6 us (50 MB), 32768 37.8 against 36.9 (201);
+// 16 requests, 2048 keys 23.0 against 16.9 (63), 8192 31.5 against 34.0 (252); 64 requests,
+// 512 keys 32.3 against 18.9 (66), 2048 36.0 against 37.4 (264), 8192 42.6 against 109 (1057).
+constexpr int64_t SP_WORTH = 200 << 20;
+std::atomic<int64_t> g_worth{SP_WORTH};
+
 struct PlanArgs {
   const int* lens;
   const int* cu;
@@ -49,6 +59,7 @@ struct PlanArgs {
   int n;                      // groups
   int capacity;               // tokens a table row holds
   int page_shift;
+  long long worth;            // keys times requests that are spared them, to be shared at all
   KvEntry* list;              // n for the groups, then the requests'
 };
 
@@ -66,7 +77,8 @@ __device__ __forceinline__ void plan_reduce(int& a, int& b, int2* sm) {
 // One group to a CTA or to a cluster.  Its requests are groups[g] .. groups[g + 1] - 1,
 // offsets taken in order: one below an earlier one counts as that one.  Its prefix is what
 // `shared` says, what stands in front of all its rows, and what the rows of the table agree on,
-// whichever is least: a wrong word about a prefix costs time, not the answer.
+// whichever is least (a wrong word about a prefix costs time, not the answer); or
+// nothing, if that is too little for a pass.
 __global__ void __launch_bounds__(SP_THREADS) kv_plan_kernel(const PlanArgs a) {
   __shared__ int2 sm[3][SP_WARPS];
   __shared__ int sm_agree;
@@ -122,7 +134,8 @@ __global__ void __launch_bounds__(SP_THREADS) kv_plan_kernel(const PlanArgs a) {
     agree = __reduce_min_sync(0xFFFFFFFFu, agree);
     cluster_arrive();
   }
-  const int keys = agree < pages ? agree << a.page_shift : max(0, most);
+  int keys = agree < pages ? agree << a.page_shift : max(0, most);
+  if (static_cast<long long>(keys) * (with_rows - 1) < a.worth) keys = 0;
   auto entry = [&](int i, int q0, int q1, int len, int start, int row, int prefix) {
     int4* e = reinterpret_cast<int4*>(a.list + i);
     e[0] = make_int4(q0, q1, len, start);
@@ -331,6 +344,10 @@ cudaError_t launch_dependent(void (*kern)(Args...), dim3 grid, int threads, bool
 
 }  // namespace
 
+void kv_set_shared_bytes(int64_t bytes) {
+  g_worth.store(bytes < 0 ? SP_WORTH : bytes, std::memory_order_relaxed);
+}
+
 size_t kv_attention_shared_workspace_bytes(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d,
                                            int64_t max_q, int64_t requests, int64_t groups) {
   const int sms = kv_sm_count();
@@ -344,8 +361,13 @@ cudaError_t launch_kv_attention_shared(const KvAttn& q, const KvGroups& g, cudaS
   const int sms = kv_sm_count();
   const size_t need = kv_attention_shared_workspace_bytes(q.tokens, q.q_heads, c.heads, c.d, q.max_q,
                                                           q.requests, g.n);
-  // without groups or room for the states: each request for itself
-  if (g.n == 0 || need == 0 || q.ws == nullptr || q.ws_bytes < need) return launch_kv_attention(q, st);
+  // Without groups or room for the states, or where not even prefixes as long as the table
+  // would be worth a pass: each request for itself.
+  const int64_t most = q.width << kv_page_shift(c.page);
+  const int64_t bytes = 2 * c.heads * c.d, worth = g_worth.load(std::memory_order_relaxed);
+  if (g.n == 0 || need == 0 || q.ws == nullptr || q.ws_bytes < need ||
+      (q.requests - g.n) * most < worth / bytes)
+    return launch_kv_attention(q, st);
   const Layout l = layout_of(q.tokens, q.q_heads, c.heads, c.d, q.max_q, q.requests, g.n, sms);
   char* ws = static_cast<char*>(q.ws) + (reinterpret_cast<uintptr_t>(q.ws) & 16);
   KvEntry* list = reinterpret_cast<KvEntry*>(ws + l.list);
@@ -358,7 +380,7 @@ cudaError_t launch_kv_attention_shared(const KvAttn& q, const KvGroups& g, cudaS
   p.table_stride = q.table_stride;
   p.requests = static_cast<int>(q.requests);
   p.n = static_cast<int>(g.n);
-  const int64_t most = q.width << kv_page_shift(c.page);
+  p.worth = worth / bytes / g.n;            // (as if the groups were alike)
   p.capacity = static_cast<int>(most < 0x7FFFFF00 ? most : 0x7FFFFF00);
   p.page_shift = kv_page_shift(c.page);
   p.list = list;

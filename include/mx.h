@@ -740,7 +740,8 @@ mx_status mx_kv_attention(const void* Q, int32_t dtype, int64_t tokens, int64_t 
  *   shared     device, int32, n_groups entries: how many of its first tokens a group's
  *              requests have in common, or more.  Shared are those in front of the first page
  *              on which the requests' rows of the table differ, and in front of all of
- *              the group's rows: any value gives the right results
+ *              the group's rows: any value gives the right results.  (Prefixes that
+ *              are not worth it are not shared: mx_set_shared_bytes.)
  *   workspace  as for mx_kv_attention, at least mx_kv_attention_shared_workspace_bytes()
  *              bytes, which grow with each argument; NULL or a smaller size, or no groups:
  *              every request reads its keys itself, as mx_kv_attention does
@@ -798,6 +799,13 @@ int32_t mx_version(void);
  * Process-wide: set it while no other thread launches GEMMs.  Returns
  * MX_ERR_INVALID_ARG for any other value. */
 mx_status mx_set_tile_width(int32_t tbn);
+
+/* Tuning and testing knob: mx_kv_attention_shared shares a prefix where that
+ * saves at least this many bytes of reads (keys and values of the prefix, times the
+ * requests that are spared them); 0: always, -1 (the default): 200 MiB, below which it
+ * takes longer than mx_kv_attention.  Process-wide: set it while no other thread makes that
+ * call.  Returns MX_ERR_INVALID_ARG for other negative values. */
+mx_status mx_set_shared_bytes(int64_t bytes);
 
 #ifdef __cplusplus
 }

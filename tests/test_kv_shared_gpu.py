@@ -15,7 +15,9 @@ BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
 @pytest.fixture(scope="module", autouse=True)
 def _built():
     mx.build()
-    mx.lib()
+    mx.set_shared_bytes(0)                       # short prefixes are shared too
+    yield
+    mx.set_shared_bytes(-1)
 
 
 def _i32(x):
@@ -273,3 +275,28 @@ def test_a_workspace_of_exactly_the_size_at_a_16_byte_boundary():
 def test_serving_sizes(requests, q):
     b = Batch([(2048, [(q + (37 * i) % 256, q) for i in range(requests)])], 32, 8, 128, 64, seed=11)
     b.check(b.run())
+
+
+def test_prefixes_that_are_not_worth_it():
+    """By default a short prefix is read by each request for itself: with a table too short for any other
+    the call is mx_kv_attention; behind a wide table the bits are those of entries without prefixes."""
+    b = Batch(CASES[2][0], *CASES[2][1:], seed=2)
+    plain = mx.mx_kv_attention(b.q.cuda(), b.cache, _i32(b.table), _i32(b.lens), _i32(b.cu), b.most,
+                               workspace=b.workspace())
+    wide = Batch(CASES[2][0], *CASES[2][1:], seed=2)
+    wide.table = np.concatenate([b.table, np.full((len(b.lens), 200000 // 32), -1, np.int32)], 1)
+    none = wide.run(shared=[0], out_dtype=F32)
+    try:
+        mx.set_shared_bytes(-1)
+        assert torch.equal(b.run(), plain)
+        assert torch.equal(wide.run(out_dtype=F32), none)
+    finally:
+        mx.set_shared_bytes(0)
+    got = wide.run(out_dtype=F32)                # shared, and so summed in another order
+    assert not torch.equal(got, none)
+    wide.check(got)
+
+
+def test_the_knob_refuses():
+    with pytest.raises(mx.MXError):
+        mx.set_shared_bytes(-2)
