@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(SH_THREADS) kv_release_kernel(const ShareArgs 
         if (held(page[u][i])) atomicSub(a.refs + page[u][i], 1);
   });
   share_sync();
-  each([&](Ints b, Rows) {
+  each([&](Ints b, Rows row) {
     int refs[SH_ROWS][SH_BATCH];
 #pragma unroll
     for (int u = 0; u < SH_ROWS; ++u)
@@ -179,8 +179,15 @@ __global__ void __launch_bounds__(SH_THREADS) kv_release_kernel(const ShareArgs 
 #pragma unroll
     for (int u = 0; u < SH_ROWS; ++u)
 #pragma unroll
-      for (int i = 0; i < SH_BATCH; ++i)
-        if (refs[u][i] < 0) atomicMin(a.refs + page[u][i], -2 - (first + b[u]));
+      for (int i = 0; i < SH_BATCH; ++i) {
+        if (page[u][i] < 0) continue;
+        if (refs[u][i] < 0) {
+          atomicMin(a.refs + page[u][i], -2 - (first + b[u]));
+        } else {
+          row[u][32 * i + lane] = -1;       // others hold it (or it is none)
+          page[u][i] = -1;
+        }
+      }
   });
   share_sync();
   each([&](Ints b, Rows row) {
@@ -189,7 +196,7 @@ __global__ void __launch_bounds__(SH_THREADS) kv_release_kernel(const ShareArgs 
     for (int u = 0; u < SH_ROWS; ++u)
 #pragma unroll
       for (int i = 0; i < SH_BATCH; ++i)
-        was[u][i] = held(page[u][i]) ? atomicCAS(a.refs + page[u][i], -2 - (first + b[u]), 0) : 0;
+        was[u][i] = page[u][i] >= 0 ? atomicCAS(a.refs + page[u][i], -2 - (first + b[u]), 0) : 0;
 #pragma unroll
     for (int u = 0; u < SH_ROWS; ++u) {
       int mine = 0;
@@ -199,7 +206,7 @@ __global__ void __launch_bounds__(SH_THREADS) kv_release_kernel(const ShareArgs 
         if (was[u][i] == -2 - (first + b[u])) {
           ++mine;
         } else {
-          row[u][32 * i + lane] = -1;       // others hold it, or free it
+          row[u][32 * i + lane] = -1;       // another request frees it
           page[u][i] = -1;
         }
       }

@@ -25,7 +25,7 @@ namespace mxk {
 namespace {
 
 constexpr int RP_MOST_THREADS = 512;
-constexpr int RP_TOKENS = 4;                // of a thread, where there are many
+constexpr int RP_TOKENS = 2;                // of a thread, where there are many
 constexpr int RP_SMEM = 32768;              // cosines and sines of a CTA at the most
 
 // The position of token t, found by a whole warp; false: it belongs to no request.
@@ -106,8 +106,8 @@ __global__ void __launch_bounds__(RP_MOST_THREADS, 2) rope_kernel(const RopeCall
 #pragma unroll
     for (int t = 0; t < TOKENS; ++t)
       if (t < mine) {
-        va[t] = __ldcs(reinterpret_cast<const uint4*>(x + t * x_ts + first));
-        if (second >= 0) vb[t] = __ldcs(reinterpret_cast<const uint4*>(x + t * x_ts + second));
+        va[t] = *reinterpret_cast<const uint4*>(x + t * x_ts + first);
+        if (second >= 0) vb[t] = *reinterpret_cast<const uint4*>(x + t * x_ts + second);
       }
   };
   if (in_set < z.units) {
@@ -198,7 +198,7 @@ cudaError_t launch_rope(const RopeCall& c, cudaStream_t st) {
   // a token's units in as few equal rounds as there must be
   const long long rounds = (units + RP_MOST_THREADS - 1) / RP_MOST_THREADS;
   z.threads = static_cast<int>((units + rounds - 1) / rounds);
-  // one token a thread where four would leave SMs idle
+  // one token a thread where two would leave SMs idle
   const bool many = c.tokens > 4 * 152;
   const int per = many ? RP_TOKENS : 1;
   const int fits = RP_SMEM / (per * turned * 64);
