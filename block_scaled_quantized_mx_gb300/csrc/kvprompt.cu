@@ -386,6 +386,41 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::MISC_OFF);
   volatile int* abort = reinterpret_cast<volatile int*>(gbase + L::MISC_OFF + 4);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto set_up = [&] {
+    if (tid == 0) {
+      for (int i = 0; i < KP_STAGES; ++i) {
+        mbar_init(bar_k + 8 * i, 4);
+        mbar_init(bar_v + 8 * i, 4);
+        mbar_init(bar_k_empty + 8 * i, 2);
+        mbar_init(bar_v_empty + 8 * i, 2);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(bar_q + 8 * i, 4);
+        mbar_init(bar_o_done + 8 * i, 1);
+        mbar_init(bar_s_full + 16 * i, 1);
+        mbar_init(bar_s_full + 16 * i + 8, 1);
+        mbar_init(bar_p_full + 16 * i, 4);
+        mbar_init(bar_p_full + 16 * i + 8, 4);
+        mbar_init(bar_seg + 8 * i, 1);
+        mbar_init(bar_seg_empty + 8 * i, 10);
+      }
+      for (int i = 0; i < KP_PG; ++i) {
+        mbar_init(bar_pg + 8 * i, 1);
+        mbar_init(bar_pg_empty + 8 * i, 12);
+      }
+      for (int i = 0; i < L::RAW; ++i) {
+        mbar_init(bar_raw + 8 * i, 1);
+        mbar_init(bar_raw_empty + 8 * i, 4);
+      }
+      *abort = 0;
+      fence_mbar_init();
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
+    }
+    if (warp == 1) tmem_alloc_cg<1>(smem_u32(tmem_slot), KP_TMEM_COLS);
+  };
+  // (SH: beside the plan, whose launch this one follows at once)
+  if constexpr (SH) set_up();
   // SH: the plan is the kernel before this one (which is waited for before others may
   // follow), or the one before a prefixes' pass that lets this one begin only when it has
   // seen the plan itself; that pass's results are waited for by the last CTA at its end, for
@@ -483,6 +518,10 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     KpJoin* join = a.joins ? a.joins + blockIdx.x : nullptr;
     if (tid == 0 && join) join->live = 0;
     if (blockIdx.x >= ctas || total == 0) {  // the whole CTA: nothing was started
+      if (SH && warp == 1) {                 // (but for its tensor memory)
+        tc_fence_after();
+        tmem_dealloc_cg<1>(*tmem_slot, KP_TMEM_COLS);
+      }
       if (SH && blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
       return;
     }
@@ -491,37 +530,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   fence_proxy_async_smem();
   __syncthreads();
 
-  if (tid == 0) {
-    for (int i = 0; i < KP_STAGES; ++i) {
-      mbar_init(bar_k + 8 * i, 4);
-      mbar_init(bar_v + 8 * i, 4);
-      mbar_init(bar_k_empty + 8 * i, 2);
-      mbar_init(bar_v_empty + 8 * i, 2);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar_q + 8 * i, 4);
-      mbar_init(bar_o_done + 8 * i, 1);
-      mbar_init(bar_s_full + 16 * i, 1);
-      mbar_init(bar_s_full + 16 * i + 8, 1);
-      mbar_init(bar_p_full + 16 * i, 4);
-      mbar_init(bar_p_full + 16 * i + 8, 4);
-      mbar_init(bar_seg + 8 * i, 1);
-      mbar_init(bar_seg_empty + 8 * i, 10);
-    }
-    for (int i = 0; i < KP_PG; ++i) {
-      mbar_init(bar_pg + 8 * i, 1);
-      mbar_init(bar_pg_empty + 8 * i, 12);
-    }
-    for (int i = 0; i < L::RAW; ++i) {
-      mbar_init(bar_raw + 8 * i, 1);
-      mbar_init(bar_raw_empty + 8 * i, 4);
-    }
-    *abort = 0;
-    fence_mbar_init();
-    prefetch_tmap(&tmK);
-    prefetch_tmap(&tmV);
-  }
-  if (warp == 1) tmem_alloc_cg<1>(smem_u32(tmem_slot), KP_TMEM_COLS);
+  if constexpr (!SH) set_up();
   __syncwarp();
   tc_fence_before();
   __syncthreads();

@@ -191,11 +191,14 @@ __global__ void __launch_bounds__(SJ_THREADS) kv_join_states_kernel(const JoinAr
   if (row >= a.rows) return;                // (SJ_LANES lanes alike)
   const long long token = row / a.q_heads;
   const int head = static_cast<int>(row - token * a.q_heads);
-  if (token < a.cu[0] || token >= a.cu[a.requests]) return;   // of no request: left as it is
+  // (all of these at once: each is a read from L2)
   const int4 own = __ldcg(a.own.states.rec + row);
+  int4 pre = __ldcg(a.prefix.states.rec + row);
+  const int first = a.cu[0], end = a.cu[a.requests];
+  if (token < first || token >= end) return;   // of no request: left as it is
   if (own.w & KV_REC_DONE) return;
   const bool has_prefix = (own.w & KV_REC_PREFIX) != 0;
-  const int4 pre = has_prefix ? __ldcg(a.prefix.states.rec + row) : make_int4(0, 0, 0, 0);
+  if (!has_prefix) pre = make_int4(0, 0, 0, 0);
   // (offsets that go up and down may leave a row without a word of this call's)
   auto sound = [](const int4& r, const JoinSet& s) {
     return r.z == 0 || (r.z > 1 && r.y >= 0 && r.y + r.z <= s.ctas && r.x >= 0 && r.x < 2 * s.ctas &&
