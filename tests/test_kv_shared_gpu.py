@@ -300,3 +300,81 @@ def test_prefixes_that_are_not_worth_it():
 def test_the_knob_refuses():
     with pytest.raises(mx.MXError):
         mx.set_shared_bytes(-2)
+
+
+@pytest.mark.parametrize("case,max_q", [(2, 0), (4, 1), (4, 500), (7, 3), (0, 300)])
+def test_any_max_q_gives_the_same_answer(case, max_q):
+    """max_q picks the kernels; the rows are what cu says."""
+    b = Batch(*CASES[case], seed=case)
+    T, hq, d = b.q.shape
+    n = mx.kv_attention_shared_workspace_bytes(T, hq, b.heads, d, max(1, max_q), len(b.lens), len(b.common))
+    b.most = max_q
+    b.check(b.run(ws=torch.empty(n, dtype=torch.uint8, device="cuda")))
+
+
+@pytest.mark.parametrize("groups,each", [(63, 3), (65, 2), (200, 2)])
+def test_many_groups(groups, each):
+    b = Batch([(32 + 16 * (g % 3), [(1 + (7 * g + i) % 30, 1 + (g + i) % 2) for i in range(each)]) for g in range(groups)],
+              2, 1, 64, 16, seed=groups)
+    b.check(b.run())
+
+
+def test_a_table_with_room_for_far_more():
+    """The plan's cluster looks the rows over; other rules between the kernels."""
+    b = Batch(CASES[4][0], 8, 2, 128, 64, seed=12)
+    want = b.run()
+    b.table = np.concatenate([b.table, np.full((len(b.lens), 3000), -1, np.int32)], 1)
+    b.check(b.run())
+    for at in (0, 5, 10):                        # what the rows agree on ends early, in one of them
+        t = Batch(CASES[4][0], 8, 2, 128, 64, seed=12)
+        other, mine = t.table[13, at], int(np.setdiff1d(np.arange(len(t.planes[0])), t.table)[0])   # a free page
+        for p in t.planes:
+            p[mine] = p[other]
+        t.table[13, at] = mine
+        t.table = np.concatenate([t.table, np.full((len(t.lens), 3000), -1, np.int32)], 1)
+        t.cache = mx.KVCache(*[torch.from_numpy(p).cuda() for p in t.planes], t.fmt)
+        got = t.run()
+        t.check(got)
+        assert ((got.double() - want.double()).abs() <= 2.0 ** -6 * want.double().abs().amax()).all()
+
+
+def test_pages_behind_four_gib():
+    """The same pages at the end of a cache of 4.3 GB of keys: the same bits, and copies."""
+    b = Batch([(320, [(20, 1), (64, 1), (1, 2)])], 16, 8, 128, 64, seed=5)
+    want = b.run()
+    pages, small = 66000, b.cache
+    n = small.k.shape[0]
+    big = mx.empty_kv_cache(b.fmt, pages, 8, 64, 128)
+    for t, s in ((big.k, small.k), (big.v, small.v), (big.k_scales, small.k_scales), (big.v_scales, small.v_scales)):
+        t[pages - n:] = s
+    b.cache, b.table = big, np.where(b.table >= 0, b.table + pages - n, -1).astype(np.int32)
+    assert torch.equal(b.run(), want)
+    # a request that holds another's last page there writes a copy of it, on the first page and the last
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    page = int(b.table[0, 5])
+    refs[page] = 2
+    table = _i32(np.stack([b.table[0], b.table[0], b.table[0]]))
+    free = [0, int(np.setdiff1d(np.arange(pages - n, pages), b.table)[-1])]
+    own = mx.mx_kv_own(big, _i32([340] * 3), _i32([1, 1, 0]), table, _i32(free), _i32([2]), refs)
+    assert own.copies.tolist() == [[page, free[1], 20], [page, free[0], 20], [-1] * 3] and refs[page] == 0
+    for p in free:
+        assert torch.equal(big.k[p, :, :20], big.k[page, :, :20]) and torch.equal(big.v[p, :, :20], big.v[page, :, :20])
+        assert torch.equal(big.k_scales[p], big.k_scales[page]) and torch.equal(big.v_scales[p], big.v_scales[page])
+    assert mx.mx_last_error() == 0
+
+
+def test_two_streams_at_once():
+    """Calls with workspaces of their own leave each other alone."""
+    bs = [Batch(*CASES[c], seed=c) for c in (4, 7)]
+    want = [b.run() for b in bs]
+    args = [((b.q.cuda(), b.cache, _i32(b.table), _i32(b.lens), _i32(b.cu), b.most, _i32(b.edges), _i32(b.common)), b.workspace())
+            for b in bs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(mx.mx_kv_attention_shared(*args[i][0], workspace=args[i][1]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i in range(2) for o in got[i])
