@@ -11,7 +11,12 @@
 //            holder lets it go, and counts as freed by the last of the requests (in
 //            their order) that do so in one call
 // fork and release move a few KB and own's plan less: launches and chains of
-// dependent reads bound them, HBM own's copies.
+// dependent reads bound them, HBM own's copies (L2, where several requests copy one
+// page).
+// Measured, release + fork + own with its copies: 16 samples of a prompt of 1000 tokens 19 us;
+// eight samples of each of 64 prompts of up to 4096 tokens 40 us, about 15, 6, 7 and 10 of
+// them.  (release with eight lanes a row and its entries read again in each step took 27, with
+// every dropped page's holder settled by an atomic 18.)
 //
 // Who is the last of several holders must not hang on the order of atomics.  So
 // counts go down first; a page whose count is then negative has lost its last holder, and

@@ -14,6 +14,11 @@
 // once per token for all heads and both operands, into shared memory; the values' loads
 // are on their way meanwhile.  A token's request is found in cu by a warp, 32
 // offsets a step.
+// Measured: 8192 tokens, 32 + 8 heads of 128: 31 us, 5.3 TB/s, 0.79 of the copy rate: what is
+// left is the wait for the tokens' positions, three reads from L2 one after the other, before
+// the first value is turned; 64 tokens 2.8 us.  (A thread with 1, 2, 3, 4 and 8 tokens 31.6,
+// 31.4, 30.0, 31.9 and 44 us, the differences being the last wave's; a grid that stays, with
+// three tokens ahead, 31.9, and small calls slower.)
 #include <cstdint>
 
 #include "common.cuh"
