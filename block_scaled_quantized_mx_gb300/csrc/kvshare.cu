@@ -152,8 +152,8 @@ __global__ void __launch_bounds__(SH_THREADS) kv_release_kernel(const ShareArgs 
           for (int u = 0; u < SH_ROWS; ++u)
 #pragma unroll
             for (int i = 0; i < SH_BATCH; ++i) {
-              const int k = k0 + 32 * i + lane;
-              page[u][i] = k < n[u] ? row[u][k] : -1;
+              const int k = 32 * i + lane;   // (row[u] has moved on by k0)
+              page[u][i] = k0 + k < n[u] ? row[u][k] : -1;
             }
         }
         f(b, row);

@@ -46,6 +46,9 @@ def own(lens, new, table, stack, count, refs, page):
             refs[held[b]] -= 1
             copies[b] = [held[b], to, lens[b] % page]
             table[b, lens[b] // page] = to
+    for b in keeper:                             # nobody else holds his page but those refused a copy
+        p = held[b]
+        refs[p] = sum(out[w] == 0 for w in writers[p] if w != b)
     return out, copies, [count - used, refused]
 
 

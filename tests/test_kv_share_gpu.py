@@ -98,7 +98,8 @@ class Pool:
         assert [max(0, h - 1) for h in held] == self.refs
 
 
-@pytest.mark.parametrize("B,width,page", [(3, 5, 16), (40, 9, 32), (64, 3, 128), (65, 40, 64), (700, 12, 16)])
+@pytest.mark.parametrize("B,width,page", [(3, 5, 16), (40, 9, 32), (64, 3, 128), (65, 40, 64), (700, 12, 16), (20, 200, 16),
+                                          (300, 90, 16)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_a_life_of_shared_pages(B, width, page, in_place):
     p = Pool(B, width, B * width // 2 + 9, page, seed=B)
@@ -224,3 +225,57 @@ def test_captured_and_replayed():
         graph.replay()
         assert [t.tolist() for t in (f.lens, o.new_tokens, o.copies, o.counts, r.lens, r.counts)] == want
         assert all(torch.equal(before[k], g[k]) for k in ("table", "refs", "lens"))
+
+
+@pytest.mark.parametrize("B,width", [(1, 9), (64, 70), (700, 40), (3000, 90)])
+def test_release_without_sharing_is_truncate(B, width):
+    rng = np.random.default_rng(B)
+    page, pages = 16, B * width + 7
+    lens = rng.integers(0, width * page + 1, B)
+    keep = np.where(rng.random(B) < 0.1, -5, lens - rng.choice([0, 1, 3, 40, 10 ** 6], B))
+    table = np.full((B, width), -1, np.int32)
+    ids, at = rng.permutation(pages), 0
+    for b, n in enumerate(lens):
+        m = -(-n // page)
+        table[b, :m] = np.where(rng.random(m) < 0.2, -1, ids[at:at + m])
+        at += m
+    stack = np.concatenate([ids[at:], np.full(at, -9)])
+    got = []
+    for refs in (None, torch.zeros(pages, dtype=torch.int32, device="cuda")):
+        t, s, count = _i32(table), _i32(stack), _i32([pages - at])
+        if refs is None:
+            cut = mx.mx_kv_truncate(_i32(lens), _i32(keep), t, s, count, page)
+        else:
+            cut = mx.mx_kv_release(_i32(lens), _i32(keep), t, s, count, refs, page)
+            assert (refs == 0).all()
+        got.append((t, s, cut.lens, cut.counts))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_no_requests():
+    none, table = _i32([]), torch.zeros(0, 4, dtype=torch.int32, device="cuda")
+    p = Pool(1, 1, 3, 16)
+    assert mx.mx_kv_release(none, none, table, p.g["stack"], p.g["count"], p.g["refs"], 16).counts.tolist() == [3, 0]
+    assert mx.mx_kv_fork(none, none, none, none, table, p.g["refs"], 16).counts.tolist() == [0]
+    assert mx.mx_kv_fork(none, _i32([0]), _i32([1]), _i32([1]), table, p.g["refs"], 16).counts.tolist() == [1]
+    own = mx.mx_kv_own(p.cache, none, none, table, p.g["stack"], p.g["count"], p.g["refs"])
+    assert own.counts.tolist() == [3, 0] and own.copies.shape == (0, 3)
+
+
+def test_counts_that_say_too_much_or_too_little():
+    """A stack count outside the stack is clipped; a page whose holders are more than its count says is freed
+    once, by the last of them, and copied for all but him."""
+    table, refs = _i32([[2, 3], [2, 3], [2, 4]]), _i32([0, 0, 1, 0, 0])
+    stack = _i32([0, 1, -9, -9, -9])
+    cut = mx.mx_kv_release(_i32([32, 32, 32]), _i32([0, 0, 0]), table, stack, _i32([2]), refs, 16)
+    assert cut.counts.tolist() == [5, 0] and (refs == 0).all()
+    # freed: 3 by request 1, 2 then 4 by request 2
+    assert stack.tolist() == [0, 1, 4, 2, 3]
+    cut = mx.mx_kv_release(_i32([0]), _i32([0]), _i32([[-1, -1]]), stack, _i32([99]), refs, 16)
+    assert cut.counts.tolist() == [5, 0]
+    p = Pool(3, 2, 6, 16)
+    p.extend([20, 0, 0])
+    p.fork([0, 0], [1, 2], [20, 20])
+    p.refs[int(p.table[0, 1])] = 1
+    p.g["refs"][int(p.table[0, 1])] = 1
+    p.own([1, 1, 1])
