@@ -16,6 +16,7 @@ import ctypes
 import functools
 import math
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -190,12 +191,11 @@ def lib() -> ctypes.CDLL:
                                   ctypes.c_float, p, sz, p]
     L.mx_rmsnorm_quantize.restype = i32
     L.mx_rmsnorm_quantize.argtypes = [p, i32, i64, p, i32, i64, p,
-                                      ctypes.c_float, p, i64, pt, p]
+                                      ctypes.c_float, p, i64, p, p]
     L.mx_dequantize.restype = i32
-    L.mx_dequantize.argtypes = [pt, p, i32, i64, p]
-    pr = ctypes.POINTER(CRopeOperand)
+    L.mx_dequantize.argtypes = [p, p, i32, i64, p]
     L.mx_rope.restype = i32
-    L.mx_rope.argtypes = [pr, pr, i32, i64, i64, p, i64, ctypes.c_float, p, p,
+    L.mx_rope.argtypes = [p, p, i32, i64, i64, p, i64, ctypes.c_float, p, p,
                           p, i64, i32, i32, p]
     L.mx_kv_fork.restype = i32
     L.mx_kv_fork.argtypes = [p, i64, p, p, p, i64, p, i64, i64, p, i64, i32, p,
@@ -644,10 +644,10 @@ def mx_rmsnorm_quantize(X: torch.Tensor, weight: torch.Tensor, fmt: int,
     else:
         _check_mx(out, "out", fmt, rows, K)
         _one_gpu(X, out.data, out.scales)
-    ct = CMXTensor(out.data.data_ptr(), out.scales.data_ptr(), fmt, rows, K)
+    ct = _mx_struct(out.data.data_ptr(), out.scales.data_ptr(), fmt, rows, K)
     _check(lib().mx_rmsnorm_quantize(
-        px, xdt, ldx, pr, rdt, ldr, weight.data_ptr(), eps, po, ldo,
-        ctypes.byref(ct), _stream_on(stream, dev)), "mx_rmsnorm_quantize")
+        px, xdt, ldx, pr, rdt, ldr, weight.data_ptr(), eps, po, ldo, ct,
+        _stream_on(stream, dev)), "mx_rmsnorm_quantize")
     return out, residual_out
 
 
@@ -666,8 +666,8 @@ def mx_dequantize(A: MXTensor, out_dtype=torch.float32,
     else:
         _check_out(out, rows, K, out_dtype)
         ld = out.stride(0)
-    ca = A.c()
-    _check(lib().mx_dequantize(ctypes.byref(ca), out.data_ptr(), dt, ld,
+    ct = _mx_struct(A.data.data_ptr(), A.scales.data_ptr(), A.fmt, rows, K)
+    _check(lib().mx_dequantize(ct, out.data_ptr(), dt, ld,
                                _stream_on(stream, dev)), "mx_dequantize")
     return out
 
@@ -714,19 +714,25 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "parts",
     return Rope(torch.tensor(turns, dtype=torch.int64, device=device), by)
 
 
+# The C structs of small calls, as bytes (a ctypes.Structure takes three times as
+# long to make).
+_rope_struct = struct.Struct("PPqqqqq").pack       # struct mx_rope_operand
+_mx_struct = struct.Struct("PPiqq").pack           # struct mx_tensor
+
+
 def _rope_operand(x: torch.Tensor, y: torch.Tensor | None, name: str, empty):
-    """The struct of a tensor to turn, and its output."""
+    """Type, shape, output and C struct of a tensor to turn."""
     dt, shape, xt, xh = _kv_tensor(x, name)
     if y is None:
-        _, h, d = shape
+        T, h, d = shape
         yt, yh = h * d, d
-        y = empty(tuple(shape), (yt, yh, 1), x.dtype)
+        y = empty((T, h, d), (yt, yh, 1), x.dtype)
     else:
         ydt, yshape, yt, yh = _kv_tensor(y, "out")
         if ydt != dt or yshape != shape:
             raise ValueError(f"out must have {name}'s shape and type")
-    return dt, y, CRopeOperand(x.data_ptr(), y.data_ptr(), shape[1], xt, xh, yt,
-                               yh)
+    return dt, shape, y, _rope_struct(x.data_ptr(), y.data_ptr(), shape[1], xt,
+                                      xh, yt, yh)
 
 
 def mx_rope(Q: torch.Tensor, K: torch.Tensor | None, rope: Rope,
@@ -750,14 +756,12 @@ def mx_rope(Q: torch.Tensor, K: torch.Tensor | None, rope: Rope,
         raise ValueError("out must hold an output for each of Q and K")
     dev = _one_gpu(Q, K, freq, positions, lens, cu, oq, ok)
     empty = _empty(dev)
-    dt, oq, a = _rope_operand(Q, oq, "Q", empty)
-    T, _, d = Q.shape
+    dt, (T, _, d), oq, a = _rope_operand(Q, oq, "Q", empty)
     b = None
     if K is not None:
-        kdt, ok, cb = _rope_operand(K, ok, "K", empty)
-        if kdt != dt or K.shape[0] != T or K.shape[2] != d:
+        kdt, (kT, _, kd), ok, b = _rope_operand(K, ok, "K", empty)
+        if kdt != dt or kT != T or kd != d:
             raise ValueError("Q and K must have one type, tokens and d")
-        b = ctypes.byref(cb)
     requests, p_pos, p_lens, p_cu = 0, None, None, None
     if positions is not None:
         p_pos = _int32(positions, "positions", T)
@@ -767,7 +771,7 @@ def mx_rope(Q: torch.Tensor, K: torch.Tensor | None, rope: Rope,
         requests = lens.shape[0]
         p_lens, p_cu = _int32(lens, "lens"), _int32(cu, "cu", requests + 1)
     _check(lib().mx_rope(
-        ctypes.byref(a), b, dt, T, d, freq.data_ptr(), 2 * freq.shape[0],
+        a, b, dt, T, d, freq.data_ptr(), 2 * freq.shape[0],
         rope.factor, p_pos, p_lens, p_cu, requests, 1 if neighbours else 0,
         1 if backward else 0, _stream_on(stream, dev)), "mx_rope")
     return oq, ok

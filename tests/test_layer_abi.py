@@ -107,3 +107,10 @@ def test_restatement_by_hand():
     # a quarter turn each position: (1, 0) -> (0, 1) -> (-1, 0)
     x = np.tile([1.0, 0.0], (3, 1, 1))
     assert np.allclose(_layer.rope(x, [0, 1, 2], [1 << 62], 2)[:, 0], [[1, 0], [0, 1], [-1, 0]])
+
+
+def test_packed_structs_are_the_c_structs():
+    a = mx.CRopeOperand(1, 2, 3, 4, 5, 6, 7)
+    assert bytes(a) == mx._rope_struct(1, 2, 3, 4, 5, 6, 7)
+    t = mx.CMXTensor(1, 2, 3, 4, 5)
+    assert bytes(t) == mx._mx_struct(1, 2, 3, 4, 5)
