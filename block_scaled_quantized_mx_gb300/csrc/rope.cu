@@ -14,11 +14,12 @@
 // once per token for all heads and both operands, into shared memory; the values' loads
 // are on their way meanwhile.  A token's request is found in cu by a warp, 32
 // offsets a step.
-// Measured: 8192 tokens, 32 + 8 heads of 128: 31 us, 5.3 TB/s, 0.79 of the copy rate: what is
-// left is the wait for the tokens' positions, three reads from L2 one after the other, before
-// the first value is turned; 64 tokens 2.8 us.  (A thread with 1, 2, 3, 4 and 8 tokens 31.6,
-// 31.4, 30.0, 31.9 and 44 us, the differences being the last wave's; a grid that stays, with
-// three tokens ahead, 31.9, and small calls slower.)
+// Measured, 32 + 8 heads of 128: 8192 tokens 30 us, 5.6 TB/s, 0.82 of the copy rate, 17000
+// tokens 57 us, 0.90: what is left is the wait for the tokens' positions, three reads from L2
+// one after the other, before the first value is turned; 64 tokens 2.8 us.  (A thread with 2,
+// 3, 4 and 8 tokens: 8192 tokens 31.7, 30.0, 32.1 and 44 us, 17000 60.8, 56.9 and 58.5; a grid
+// that stays, with three tokens ahead, 31.9, and small calls slower; a request's offset, end and
+// length read together 20.0 -> 19.7 at 4800 tokens but 56.9 -> 59.2 at 17000.)
 #include <cstdint>
 
 #include "common.cuh"
@@ -30,7 +31,7 @@ namespace mxk {
 namespace {
 
 constexpr int RP_MOST_THREADS = 512;
-constexpr int RP_TOKENS = 2;                // of a thread, where there are many
+constexpr int RP_TOKENS = 3;                // of a thread, where there are many
 constexpr int RP_SMEM = 32768;              // cosines and sines of a CTA at the most
 
 // The position of token t, found by a whole warp; false: it belongs to no request.
@@ -203,7 +204,7 @@ cudaError_t launch_rope(const RopeCall& c, cudaStream_t st) {
   // a token's units in as few equal rounds as there must be
   const long long rounds = (units + RP_MOST_THREADS - 1) / RP_MOST_THREADS;
   z.threads = static_cast<int>((units + rounds - 1) / rounds);
-  // one token a thread where two would leave SMs idle
+  // one token a thread where three would leave SMs idle
   const bool many = c.tokens > 4 * 152;
   const int per = many ? RP_TOKENS : 1;
   const int fits = RP_SMEM / (per * turned * 64);
