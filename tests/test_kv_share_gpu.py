@@ -279,3 +279,22 @@ def test_counts_that_say_too_much_or_too_little():
     p.refs[int(p.table[0, 1])] = 1
     p.g["refs"][int(p.table[0, 1])] = 1
     p.own([1, 1, 1])
+
+
+def test_strided_tables_and_a_stream_argument():
+    a, b = Pool(6, 5, 40, 16, seed=3), Pool(6, 5, 40, 16, seed=3)
+    wide = torch.full((6, 9), 77, dtype=torch.int32, device="cuda")
+    wide[:, 2:7] = b.g["table"]
+    b.g["table"] = wide[:, 2:7]
+    side = torch.cuda.Stream()
+    for p, s in ((a, None), (b, side)):
+        p.extend([50, 0, 20, 0, 0, 0])
+        torch.cuda.synchronize()
+        kw = dict(stream=s)
+        f = mx.mx_kv_fork(p.g["lens"], _i32([0, 2, 0]), _i32([1, 3, 5]), _i32([50, 20, 33]), p.g["table"], p.g["refs"], 16, **kw)
+        o = mx.mx_kv_own(p.cache, f.lens, _i32([1, 1, 1, 1, 0, 1]), p.g["table"], p.g["stack"], p.g["count"], p.g["refs"], **kw)
+        r = mx.mx_kv_release(f.lens, _i32([17, 0, 20, 20, 0, 9]), p.g["table"], p.g["stack"], o.counts, p.g["refs"], 16, **kw)
+        torch.cuda.synchronize()
+        p.got = f.lens, o.new_tokens, o.copies, o.counts, r.lens, r.counts, p.g["table"], p.g["refs"], p.cache.k, p.cache.v, p.cache.k_scales
+    assert all(torch.equal(x, y) for x, y in zip(a.got, b.got))
+    assert (wide[:, :2] == 77).all() and (wide[:, 7:] == 77).all()

@@ -378,3 +378,33 @@ def test_two_streams_at_once():
                 got[i].append(mx.mx_kv_attention_shared(*args[i][0], workspace=args[i][1]))
     torch.cuda.synchronize()
     assert all(torch.equal(o, want[i]) for i in range(2) for o in got[i])
+
+
+@pytest.mark.parametrize("case", [2, 4, 6, 7])
+@pytest.mark.parametrize("scale", [-0.11, 0.0, 0.3])
+def test_any_scale(case, scale):
+    b = Batch(*CASES[case], seed=case + 30)
+    b.check(b.run(scale=scale, out_dtype=F32), scale=scale)
+
+
+@pytest.mark.parametrize("hq,heads,d", [(5, 1, 128), (16, 1, 64), (20, 4, 64), (3, 3, 128)])
+def test_groups_of_heads(hq, heads, d):
+    b = Batch([(160, [(33, 1), (7, 2), (64, 3)]), (96, [(1, 1)] * 30)], hq, heads, d, 32, seed=hq)
+    b.check(b.run())
+
+
+def test_a_strided_table_and_a_stream_argument():
+    b = Batch(*CASES[6], seed=21)
+    want = b.run()
+    wide = torch.full((len(b.lens), 64), 12345, dtype=torch.int32, device="cuda")
+    wide[:, :b.width] = _i32(b.table)
+    side = torch.cuda.Stream()
+    args = (b.q.cuda(), b.cache, wide[:, :b.width], _i32(b.lens), _i32(b.cu), b.most, _i32(b.edges), _i32(b.common))
+    ws, out = b.workspace(), torch.empty_like(want)
+    torch.cuda.synchronize()
+    for s in (side, side.cuda_stream):
+        out.zero_()
+        torch.cuda.synchronize()
+        mx.mx_kv_attention_shared(*args, out=out, workspace=ws, stream=s)
+        side.synchronize()
+        assert torch.equal(out, want)

@@ -185,3 +185,35 @@ def test_values_return_what_was_quantized():
     x[:, ::32] = 1.75                            # every block's scale the same
     for fmt in (mx.E4M3, mx.INT8):
         assert torch.equal(mx.mx_dequantize(mx.mx_quantize(x, fmt)), x)
+
+
+def test_operands_that_do_not_fit():
+    x, w = torch.randn(4, 64, device="cuda"), torch.ones(64, device="cuda")
+    r = torch.randn(4, 64, device="cuda")
+    for bad in (lambda: mx.mx_rmsnorm_quantize(x, w, mx.INT8), lambda: mx.mx_rmsnorm_quantize(x[:, :48], w[:48], mx.E4M3),
+                lambda: mx.mx_rmsnorm_quantize(x, w, mx.E4M3, residual=r[:3]), lambda: mx.mx_rmsnorm_quantize(x, w, mx.E4M3, residual_out=r),
+                lambda: mx.mx_rmsnorm_quantize(x, w, mx.E4M3, residual=r, residual_out=r.half()),
+                lambda: mx.mx_rmsnorm_quantize(x, w, mx.E4M3, out=mx.empty_mx(mx.E5M2, 4, 64)),
+                lambda: mx.mx_rmsnorm_quantize(x, w.cpu(), mx.E4M3), lambda: mx.mx_dequantize(mx.empty_mx(mx.E4M3, 4, 64), torch.float64)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(mx.MXError):
+        mx.mx_rmsnorm_quantize(x, w, mx.E4M3, eps=0.0)
+    with pytest.raises(mx.MXError):
+        mx.mx_rmsnorm_quantize(torch.zeros(1, 32800, device="cuda"), torch.ones(32800, device="cuda"), mx.E4M3)
+
+
+def test_no_rows_and_a_stream_argument():
+    w = torch.ones(64, device="cuda")
+    q, h = mx.mx_rmsnorm_quantize(torch.zeros(0, 64, device="cuda"), w, mx.E4M3, residual=torch.zeros(0, 64, device="cuda"))
+    assert q.outer == 0 and h.shape == (0, 64) and mx.mx_dequantize(q).shape == (0, 64)
+    x, r, w = _inputs(50, 512, F16, F16)
+    want, hw = mx.mx_rmsnorm_quantize(x, w, mx.E5M2, residual=r)
+    vw = mx.mx_dequantize(want, BF16)
+    out, ho, vo = mx.empty_mx(mx.E5M2, 50, 512), torch.empty_like(r), torch.empty_like(vw)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    mx.mx_rmsnorm_quantize(x, w, mx.E5M2, residual=r, out=out, residual_out=ho, stream=side)
+    mx.mx_dequantize(out, BF16, out=vo, stream=side)
+    side.synchronize()
+    assert torch.equal(out.data, want.data) and torch.equal(out.scales, want.scales) and torch.equal(ho, hw) and torch.equal(vo, vw)

@@ -151,3 +151,33 @@ def test_captured():
     out.zero_()
     graph.replay()
     assert torch.equal(out, want)
+
+
+def test_outputs_with_strides_and_a_stream_argument():
+    T, pos = 70, np.arange(70) * 13
+    q, k = torch.randn(T, 4, 64, device="cuda").half(), torch.randn(T, 2, 64, device="cuda").half()
+    rope = mx.rope_frequencies(64)
+    wide = torch.full((T, 3, 6, 72), 5.0, dtype=torch.float16, device="cuda")
+    oq, ok = wide[:, 0, :4, :64], wide[:, 2, 1:3, 8:]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    mx.mx_rope(q, k, rope, positions=_i32(pos), out=(oq, ok), stream=side)
+    side.synchronize()
+    _check(oq, q, pos, rope)
+    _check(ok, k, pos, rope)
+    assert (wide[:, 1] == 5).all() and (wide[:, 0, 4:] == 5).all() and (wide[:, 0, :4, 64:] == 5).all() and (wide[:, 2, 1:3, :8] == 5).all()
+
+
+def test_operands_that_do_not_fit():
+    q, rope = torch.randn(4, 2, 64, device="cuda").half(), mx.rope_frequencies(64)
+    pos = _i32([0, 1, 2, 3])
+    for bad in (lambda: mx.mx_rope(q, q.bfloat16(), rope, positions=pos), lambda: mx.mx_rope(q, q[:3], rope, positions=pos),
+                lambda: mx.mx_rope(q, None, rope, positions=pos[:3]), lambda: mx.mx_rope(q, None, rope),
+                lambda: mx.mx_rope(q, None, rope, positions=pos, out=(q, q)), lambda: mx.mx_rope(q, q, rope, positions=pos, out=(q, None)),
+                lambda: mx.mx_rope(q.float(), None, rope, positions=pos), lambda: mx.mx_rope(q, None, rope, positions=pos.long())):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(mx.MXError):              # more values than a head has
+        mx.mx_rope(q, None, mx.rope_frequencies(128), positions=pos)
+    with pytest.raises(mx.MXError):              # rows that lie on one another
+        mx.mx_rope(q[:1].expand(4, 2, 64), None, rope, positions=pos)
