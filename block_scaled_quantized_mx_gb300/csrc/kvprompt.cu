@@ -918,39 +918,65 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         next_lo = next_live ? kv_first_key(a.v, rq, token) : 0;
         next_hi = next_live ? kv_end_key(a.v, rq, token) : 0;
         if (next_works) {
-          uint32_t w[D / 2];
-          const uint16_t* src = a.Q + (rq.q0 + token) * a.q_ts + qh * a.q_hs;
+          // The warp's rows go to shared memory as they are, in whole lines that are all on
+          // their way together (lanes with a row each touch 32 lines a load, and take
+          // 3 us to issue them), and each thread converts its own there, in short loops: code that a
+          // unit runs once costs its fetch.
+          const unsigned long long src = next_live
+              ? reinterpret_cast<unsigned long long>(a.Q + (rq.q0 + token) * a.q_ts + qh * a.q_hs) : 0ull;
+          const int r = 32 * quarter + lane;
+          const uint32_t q_base = base + L::Q_OFF + t * L::Q_BYTES;
+          auto place = [&](int row, int c) {
+            return q_base + row * 128 + (c >> 3) * L::REGION + (((c & 7) ^ (row & 7)) << 4);
+          };
+          auto chunk = [&](int c) { return place(r, c); };
+          {
+            constexpr int LANES = D / 8, ROWS = 32 / LANES, IT = 32 / ROWS;
+            const int c = lane & (LANES - 1), sub = lane / LANES;
+            uint4 v[IT];
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (next_live) v = *reinterpret_cast<const uint4*>(src + 8 * c);
-            w[4 * c] = v.x;
-            w[4 * c + 1] = v.y;
-            w[4 * c + 2] = v.z;
-            w[4 * c + 3] = v.w;
+            for (int i = 0; i < IT; ++i) {
+              const unsigned long long from = __shfl_sync(0xFFFFFFFFu, src, ROWS * i + sub);
+              v[i] = make_uint4(0, 0, 0, 0);
+              if (from) v[i] = reinterpret_cast<const uint4*>(from)[c];
+            }
+#pragma unroll
+            for (int i = 0; i < IT; ++i)
+              st_shared_v4(place(32 * quarter + ROWS * i + sub, c), v[i].x, v[i].y, v[i].z, v[i].w);
           }
+          __syncwarp();
+          const bool turned = a.scale_log2e < 0.0f;
           if (a.bf16) {
             uint32_t top = 0;
+#pragma unroll 4
+            for (int c = 0; c < D / 8; ++c) {
+              const uint4 v = ld_shared_v4(chunk(c));
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int e = 0; e < D / 2; ++e)
-              top = max(top, max((w[e] << 16) & 0x7FFFFFFFu, w[e] & 0x7FFF0000u));
+              for (int e = 0; e < 4; ++e)
+                top = max(top, max((w[e] << 16) & 0x7FFFFFFFu, w[e] & 0x7FFF0000u));
+            }
             float down;
             kv_row_factors(top, down, up);
-            if (a.scale_log2e < 0.0f) down = -down;
+            if (turned) down = -down;
+#pragma unroll 4
+            for (int c = 0; c < D / 8; ++c) {
+              const uint4 v = ld_shared_v4(chunk(c));
+              uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int e = 0; e < D / 2; ++e)
-              w[e] = cvt_f16x2(__uint_as_float(w[e] << 16) * down,
-                               __uint_as_float(w[e] & 0xFFFF0000u) * down);
-          } else if (a.scale_log2e < 0.0f) {
-#pragma unroll
-            for (int e = 0; e < D / 2; ++e) w[e] ^= 0x80008000u;
+              for (int e = 0; e < 4; ++e)
+                w[e] = cvt_f16x2(__uint_as_float(w[e] << 16) * down,
+                                 __uint_as_float(w[e] & 0xFFFF0000u) * down);
+              st_shared_v4(chunk(c), w[0], w[1], w[2], w[3]);
+            }
+          } else if (turned) {
+#pragma unroll 1
+            for (int c = 0; c < D / 8; ++c) {
+              const uint4 v = ld_shared_v4(chunk(c));
+              st_shared_v4(chunk(c), v.x ^ 0x80008000u, v.y ^ 0x80008000u, v.z ^ 0x80008000u,
+                           v.w ^ 0x80008000u);
+            }
           }
-          const int r = 32 * quarter + lane;
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c)
-            st_shared_v4(base + L::Q_OFF + t * L::Q_BYTES + (c >> 3) * L::REGION + r * 128 +
-                             (((c & 7) ^ (r & 7)) << 4),
-                         w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_q + 8 * t);

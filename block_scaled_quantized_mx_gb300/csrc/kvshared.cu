@@ -96,20 +96,26 @@ __global__ void __launch_bounds__(SP_THREADS) kv_plan_kernel(const PlanArgs a) {
   const int rank = blockIdx.x, ctas = gridDim.x, g = blockIdx.y;
   int r0 = 0, none = 0;
   for (int i = tid; i <= g; i += SP_THREADS) r0 = min(r0, -max(0, min(a.groups[i], B)));
-  const int edge = max(0, min(a.groups[g + 1], B));
+  const int edge = max(0, min(a.groups[g + 1], B)), said = a.shared[g];
+  // (with the offsets, before it is known which requests matter: the tokens in front of
+  // a request's rows)
+  auto in_front = [&](int b) {
+    const int n = a.cu[b + 1] - a.cu[b];
+    return n > 0 ? max(0, min(a.lens[b], a.capacity)) - n : 0x7FFFFFFF;
+  };
+  const int mine = tid < B ? in_front(tid) : 0x7FFFFFFF;
   plan_reduce(r0, none, sm[0]);
   r0 = -r0;
   const int r1 = max(r0, edge);
   // the tokens that stand in front of every row of the group
   int most = 0x7FFFFFFF, with_rows = 0;
-  for (int b = r0 + tid; b < r1; b += SP_THREADS) {
-    const int n = a.cu[b + 1] - a.cu[b];
-    if (n > 0) {
-      most = min(most, max(0, min(a.lens[b], a.capacity)) - n);
-      ++with_rows;
-    }
-  }
-  const int said = a.shared[g];
+  auto count = [&](int tokens) {
+    most = min(most, tokens);
+    with_rows += tokens != 0x7FFFFFFF;
+  };
+  if (tid >= r0 && tid < r1) count(mine);
+  for (int b = tid + SP_THREADS; b < r1; b += SP_THREADS)
+    if (b >= r0) count(in_front(b));
   plan_reduce(most, with_rows, sm[1]);
   most = with_rows < 2 ? 0 : min(most, said);
   // the first entry on which a row of the table differs from the group's first
