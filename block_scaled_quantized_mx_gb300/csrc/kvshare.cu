@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(SH_THREADS) kv_release_kernel(const ShareArgs 
   extern __shared__ int sm_req[];           // per request: tokens before and after, pages freed
   __shared__ int sm_scan[SH_WARPS];
   __shared__ long long sm_total;
+  wait_for_stream();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x, ctas = gridDim.x, share = share_of(a.requests, ctas);
   const int first = min(a.requests, rank * share), B = min(share, a.requests - first);
@@ -280,6 +281,7 @@ __global__ void __launch_bounds__(SH_THREADS) kv_fork_kernel(const ShareArgs a) 
   extern __shared__ int sm_claim[];         // per request: the fork that makes it, or none
   __shared__ int sm_served;
   constexpr int NONE = 0x7FFFFFFF;
+  wait_for_stream();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x, ctas = gridDim.x, share = share_of(a.requests, ctas);
   const int first = min(a.requests, rank * share), B = min(share, a.requests - first);
@@ -354,6 +356,7 @@ __global__ void __launch_bounds__(SH_THREADS) kv_own_kernel(const ShareArgs a) {
                                             // hold it (-1: none), -2 - that for its keeper
   __shared__ int sm_scan[SH_WARPS];
   __shared__ int sm_cut, sm_served, sm_refused;
+  wait_for_stream();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the copies' CTAs may come and wait
   const int tid = threadIdx.x, B = a.requests, P = 1 << a.page_shift;
   const int per = (B + SH_THREADS - 1) / SH_THREADS;
@@ -448,7 +451,7 @@ __global__ void __launch_bounds__(SH_THREADS) kv_own_kernel(const ShareArgs a) {
 constexpr int CP_THREADS = 256, CP_BATCH = 4;
 __global__ void __launch_bounds__(CP_THREADS)
 kv_copy_kernel(const KvCache c, const int* copies, int heads_per_cta, int page_shift, int d_shift) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_stream();
   const int* job = copies + 3ll * blockIdx.x;
   const int from = __ldcg(job), to = __ldcg(job + 1), tokens = __ldcg(job + 2);
   if (from < 0 || to < 0 || from >= c.pages || to >= c.pages) return;
@@ -494,19 +497,7 @@ cudaError_t launch_share(void (*kern)(const ShareArgs), const ShareArgs& a, int 
       if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
     }
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(SH_THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  return launch_early(kern, dim3(static_cast<unsigned>(ctas)), SH_THREADS, smem, ctas, st, a);
 }
 
 // One CTA where its warps look after all requests at once: a cluster's barriers
@@ -584,17 +575,9 @@ cudaError_t launch_kv_own(const KvCache& c, const KvShare& q, cudaStream_t st) {
   // if every request were to copy
   int64_t per = 1;
   while (per < c.heads && a.requests * 2 * (c.heads / per) > 1216) per *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.requests), static_cast<unsigned>((c.heads + per - 1) / per), 2);
-  cfg.blockDim = dim3(CP_THREADS);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_copy_kernel, c, static_cast<const int*>(q.copies), static_cast<int>(per),
-                            a.page_shift, c.d == 64 ? 6 : 7);
+  const dim3 grid(static_cast<unsigned>(a.requests), static_cast<unsigned>((c.heads + per - 1) / per), 2);
+  return launch_early(kv_copy_kernel, grid, CP_THREADS, 0, 1, st, c, static_cast<const int*>(q.copies),
+                      static_cast<int>(per), a.page_shift, c.d == 64 ? 6 : 7);
 }
 
 }  // namespace mxk

@@ -91,6 +91,7 @@ __device__ __forceinline__ void plan_reduce(int& a, int& b, int2* sm) {
 __global__ void __launch_bounds__(SP_THREADS) kv_plan_kernel(const PlanArgs a) {
   __shared__ int2 sm[3][SP_WARPS];
   __shared__ int sm_agree;
+  wait_for_stream();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, B = a.requests;
   const int rank = blockIdx.x, ctas = gridDim.x, g = blockIdx.y;
@@ -198,7 +199,7 @@ constexpr int64_t SJ_FEW_ROWS = 4096;
 // lane where the rows fill the SMs (16384 rows of 5 parts: 25 us with four).
 template <int D, int SJ_LANES>
 __global__ void __launch_bounds__(SJ_THREADS) kv_join_states_kernel(const JoinArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_stream();
   const int tid = threadIdx.x, k = tid & (SJ_LANES - 1);
   const long long at = (static_cast<long long>(blockIdx.x) * SJ_THREADS + tid) / SJ_LANES;
   const long long row = at / (D / 8);
@@ -338,28 +339,6 @@ Layout layout_of(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d, i
   return l;
 }
 
-template <class... Args, class... Given>
-cudaError_t launch_dependent(void (*kern)(Args...), dim3 grid, int threads, bool dependent, int cluster,
-                             cudaStream_t st, const Given&... given) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  if (dependent) {
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-  } else {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-  }
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, given...);
-}
-
 }  // namespace
 
 void kv_set_shared_bytes(int64_t bytes) {
@@ -404,8 +383,8 @@ cudaError_t launch_kv_attention_shared(const KvAttn& q, const KvGroups& g, cudaS
   p.list = list;
   const bool alone = g.n > SP_MANY_GROUPS || q.requests * q.width <= SP_ENTRIES * g.n;
   const int cluster = alone ? 1 : SP_CLUSTER;
-  cudaError_t e = launch_dependent(kv_plan_kernel, dim3(static_cast<unsigned>(cluster), static_cast<unsigned>(g.n)),
-                                   SP_THREADS, false, cluster, st, p);
+  cudaError_t e = launch_early(kv_plan_kernel, dim3(static_cast<unsigned>(cluster), static_cast<unsigned>(g.n)),
+                               SP_THREADS, 0, cluster, st, p);
   if (e != cudaSuccess) return e;
   JoinArgs j{};
   JoinSet* sets[2] = {&j.prefix, &j.own};
@@ -458,7 +437,7 @@ cudaError_t launch_kv_attention_shared(const KvAttn& q, const KvGroups& g, cudaS
   const dim3 grid(static_cast<unsigned>((j.rows * (c.d / 8) * lanes + SJ_THREADS - 1) / SJ_THREADS));
   auto kern = c.d == 64 ? (lanes == 4 ? kv_join_states_kernel<64, 4> : kv_join_states_kernel<64, 1>)
                         : (lanes == 4 ? kv_join_states_kernel<128, 4> : kv_join_states_kernel<128, 1>);
-  return launch_dependent(kern, grid, SJ_THREADS, true, 1, st, j);
+  return launch_early(kern, grid, SJ_THREADS, 0, 1, st, j);
 }
 
 }  // namespace mxk

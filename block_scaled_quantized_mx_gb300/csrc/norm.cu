@@ -12,8 +12,8 @@
 // block of 32 is four lanes' values, so its maximum takes two shuffles; four
 // blocks' scales, one 32-bit word of the row's atom, take two more.  The sum is
 // added in a fixed order.
-// Measured: 8192 x 8192, bf16 with a bf16 residual, E4M3: 77 us, 6.1 TB/s, 0.90 of the copy
-// rate; 4097 x 5120, bf16 with an fp32 residual, E2M1: 38 us, 0.87; 64 x 4096: 2.9 us, a launch
+// Measured: 8192 x 8192, bf16 with a bf16 residual, E4M3: 76 us, 6.2 TB/s, 0.91 of the copy
+// rate; 4097 x 5120, bf16 with an fp32 residual, E2M1: 37 us, 0.88; 64 x 4096: 2.4 us, a launch
 // and two dependent reads.  The values of 8192 x 8192 E4M3 codes as bf16: 32 us, 0.94.
 //
 // Precision: h, the sum of squares (each thread's, then by halves within a warp, then
@@ -109,6 +109,7 @@ __global__ void __launch_bounds__(CH <= 2 ? 1024 : 512) rmsnorm_quantize_kernel(
   __shared__ float sm_sum[64];
   const long long row = blockIdx.x;
   const int lane = threadIdx.x & 31;
+  wait_for_stream();
   if (row >= a.rows) {                       // rows that pad the last atom: scales 0
     for (int c = 16 * threadIdx.x; c < a.chunks; c += 16 * blockDim.x)
       *reinterpret_cast<uint32_t*>(a.sf + sf_offset(row, c / 4, a.k_atoms)) = 0u;
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(CH <= 2 ? 1024 : 512) rmsnorm_quantize_kernel(
     uint32_t top = 0;
     if (c < a.chunks) {
       const float4* w = reinterpret_cast<const float4*>(a.w) + 2 * c;
-      const float4 w0 = __ldg(w), w1 = __ldg(w + 1);
+      const float4 w0 = w[0], w1 = w[1];
       const float ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -209,14 +210,13 @@ __global__ void __launch_bounds__(CH <= 2 ? 1024 : 512) rmsnorm_quantize_kernel(
 }
 
 template <int XW, int RW>
-cudaError_t norm_run(const NormArgs& a, long long ctas, int ch, int threads, cudaStream_t st) {
+cudaError_t norm_run(const NormArgs& a, unsigned ctas, int ch, int threads, cudaStream_t st) {
   switch (ch) {
-    case 1: rmsnorm_quantize_kernel<XW, RW, 1><<<ctas, threads, 0, st>>>(a); break;
-    case 2: rmsnorm_quantize_kernel<XW, RW, 2><<<ctas, threads, 0, st>>>(a); break;
-    case 4: rmsnorm_quantize_kernel<XW, RW, 4><<<ctas, threads, 0, st>>>(a); break;
-    default: rmsnorm_quantize_kernel<XW, RW, 8><<<ctas, threads, 0, st>>>(a); break;
+    case 1: return launch_early(rmsnorm_quantize_kernel<XW, RW, 1>, ctas, threads, 0, 1, st, a);
+    case 2: return launch_early(rmsnorm_quantize_kernel<XW, RW, 2>, ctas, threads, 0, 1, st, a);
+    case 4: return launch_early(rmsnorm_quantize_kernel<XW, RW, 4>, ctas, threads, 0, 1, st, a);
+    default: return launch_early(rmsnorm_quantize_kernel<XW, RW, 8>, ctas, threads, 0, 1, st, a);
   }
-  return cudaGetLastError();
 }
 
 // ------------------------------------------------------------------ values
@@ -253,6 +253,7 @@ template <int FMT>
 __global__ void __launch_bounds__(DQ_THREADS) dequantize_kernel(const DequantArgs a) {
   constexpr int BITS = FMT == FMT_INT2 ? 2 : (FMT == FMT_E2M1 || FMT == FMT_INT4) ? 4 : 8;
   const long long u0 = static_cast<long long>(blockIdx.x) * (DQ_THREADS * DQ_BATCH) + threadIdx.x;
+  wait_for_stream();
   uint32_t w[DQ_BATCH][4];
   uint32_t scale[DQ_BATCH];
   long long row[DQ_BATCH];
@@ -339,7 +340,7 @@ cudaError_t launch_rmsnorm_quantize(const void* x, int x_dtype, int64_t x_ld, co
   a.k_atoms = sf_k_atoms(K);
   a.data = static_cast<uint8_t*>(data);
   a.sf = sf;
-  const long long ctas = sf_row_atoms(rows) * SF_ATOM_ROWS;
+  const unsigned ctas = static_cast<unsigned>(sf_row_atoms(rows) * SF_ATOM_ROWS);
   // As few chunks a thread as 1024 threads allow where the rows do not fill the
   // SMs (a row's time is what counts); where they do, about 256 threads (8192 rows of
   // 8192 with 1, 2, 4 and 8 chunks 104, 95, 77 and 96 us; 4097 of 5120, fp32 residual,
@@ -371,14 +372,13 @@ cudaError_t launch_dequantize(int fmt, const void* data, const uint8_t* sf, int6
   if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   const unsigned grid = static_cast<unsigned>(ctas);
   switch (fmt) {
-    case FMT_E4M3: dequantize_kernel<FMT_E4M3><<<grid, DQ_THREADS, 0, st>>>(a); break;
-    case FMT_E5M2: dequantize_kernel<FMT_E5M2><<<grid, DQ_THREADS, 0, st>>>(a); break;
-    case FMT_E2M1: dequantize_kernel<FMT_E2M1><<<grid, DQ_THREADS, 0, st>>>(a); break;
-    case FMT_INT8: dequantize_kernel<FMT_INT8><<<grid, DQ_THREADS, 0, st>>>(a); break;
-    case FMT_INT4: dequantize_kernel<FMT_INT4><<<grid, DQ_THREADS, 0, st>>>(a); break;
-    default: dequantize_kernel<FMT_INT2><<<grid, DQ_THREADS, 0, st>>>(a); break;
+    case FMT_E4M3: return launch_early(dequantize_kernel<FMT_E4M3>, grid, DQ_THREADS, 0, 1, st, a);
+    case FMT_E5M2: return launch_early(dequantize_kernel<FMT_E5M2>, grid, DQ_THREADS, 0, 1, st, a);
+    case FMT_E2M1: return launch_early(dequantize_kernel<FMT_E2M1>, grid, DQ_THREADS, 0, 1, st, a);
+    case FMT_INT8: return launch_early(dequantize_kernel<FMT_INT8>, grid, DQ_THREADS, 0, 1, st, a);
+    case FMT_INT4: return launch_early(dequantize_kernel<FMT_INT4>, grid, DQ_THREADS, 0, 1, st, a);
+    default: return launch_early(dequantize_kernel<FMT_INT2>, grid, DQ_THREADS, 0, 1, st, a);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace mxk

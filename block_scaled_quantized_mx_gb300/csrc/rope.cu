@@ -16,7 +16,7 @@
 // offsets a step.
 // Measured, 32 + 8 heads of 128: 8192 tokens 30 us, 5.6 TB/s, 0.82 of the copy rate, 17000
 // tokens 57 us, 0.90: what is left is the wait for the tokens' positions, three reads from L2
-// one after the other, before the first value is turned; 64 tokens 2.8 us.  (A thread with 2,
+// one after the other, before the first value is turned; 64 tokens 2.4 us.  (A thread with 2,
 // 3, 4 and 8 tokens: 8192 tokens 31.7, 30.0, 32.1 and 44 us, 17000 60.8, 56.9 and 58.5; a grid
 // that stays, with three tokens ahead, 31.9, and small calls slower; a request's offset, end and
 // length read together 20.0 -> 19.7 at 4800 tokens but 56.9 -> 59.2 at 17000.)
@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(RP_MOST_THREADS, 2) rope_kernel(const RopeCall
       u = -1;
     }
   };
+  wait_for_stream();
   uint4 va[TOKENS], vb[TOKENS];
   auto load = [&] {
 #pragma unroll
@@ -219,10 +220,8 @@ cudaError_t launch_rope(const RopeCall& c, cudaStream_t st) {
   const unsigned ctas = static_cast<unsigned>((c.tokens + of_cta - 1) / of_cta);
   const size_t smem = static_cast<size_t>(of_cta) * turned * 64;
   if (many)
-    rope_kernel<RP_TOKENS><<<ctas, threads, smem, st>>>(c, z);
-  else
-    rope_kernel<1><<<ctas, threads, smem, st>>>(c, z);
-  return cudaGetLastError();
+    return launch_early(rope_kernel<RP_TOKENS>, ctas, threads, smem, 1, st, c, z);
+  return launch_early(rope_kernel<1>, ctas, threads, smem, 1, st, c, z);
 }
 
 }  // namespace mxk
