@@ -14,7 +14,7 @@
 // dependent reads bound them, HBM own's copies (L2, where several requests copy one
 // page).
 // Measured, release + fork + own with its copies: 16 samples of a prompt of 1000 tokens 19 us;
-// eight samples of each of 64 prompts of up to 4096 tokens 40 us, about 15, 6, 7 and 10 of
+// eight samples of each of 64 prompts of up to 4096 tokens 36 us, about 13, 5, 7 and 10 of
 // them.  (release with eight lanes a row and its entries read again in each step took 27, with
 // every dropped page's holder settled by an atomic 18.)
 //
@@ -36,7 +36,7 @@ namespace {
 
 constexpr int SH_THREADS = 1024;
 constexpr int SH_WARPS = SH_THREADS / 32;
-constexpr int SH_CLUSTER = 8;
+constexpr int SH_CLUSTER = 8, SH_WIDE = 16; // CTAs, where there are many requests
 constexpr int SH_MAX_REQUESTS = 16384;
 constexpr int SH_ROWS = 4;                  // requests that a warp looks after together,
 constexpr int SH_BATCH = 2;                 // with as many table entries of each a lane
@@ -501,8 +501,36 @@ cudaError_t launch_share(void (*kern)(const ShareArgs), const ShareArgs& a, int 
 }
 
 // One CTA where its warps look after all requests at once: a cluster's barriers
-// take longer than sharing out saves.
-int share_ctas(int64_t requests) { return requests <= SH_WARPS * SH_ROWS ? 1 : SH_CLUSTER; }
+// take longer than sharing out saves.  16 where that is fewer rows for each warp and the
+// device has room for such a cluster (more than the 8 that every device of this
+// architecture holds): eight samples of each of 18, 25, 36, 64, 128 and 256 prompts take
+// 22.9, 24.3, 27.1, 35.7, 50.6 and 84.3 us, with 8 CTAs 22.4, 24.4, 27.8, 38.2, 60.4 and 99.7.
+int share_ctas(void (*kern)(const ShareArgs), int64_t requests, std::atomic<int> (&most)[64]) {
+  if (requests <= SH_WARPS * SH_ROWS) return 1;
+  int dev = 0;
+  if (requests <= SH_CLUSTER * SH_WARPS || cudaGetDevice(&dev) != cudaSuccess || dev >= 64)
+    return SH_CLUSTER;
+  int ctas = most[dev].load(std::memory_order_relaxed);
+  if (ctas == 0) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = SH_WIDE;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(SH_WIDE);
+    cfg.blockDim = dim3(SH_THREADS);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    const bool wide =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) == cudaSuccess && clusters > 0;
+    if (!wide) cudaGetLastError();
+    ctas = wide ? SH_WIDE : SH_CLUSTER;
+    most[dev].store(ctas, std::memory_order_relaxed);
+  }
+  return ctas;
+}
 
 }  // namespace
 
@@ -522,8 +550,9 @@ cudaError_t launch_kv_release(const KvShare& q, cudaStream_t st) {
   a.requests = static_cast<int>(q.requests);
   a.lens_out = q.lens_out;
   a.counts_out = q.counts_out;
-  const int ctas = share_ctas(q.requests);
   static std::atomic<bool> set[64] = {};
+  static std::atomic<int> most[64] = {};
+  const int ctas = share_ctas(kv_release_kernel, q.requests, most);
   static_assert(3 * SH_MAX_REQUESTS / SH_CLUSTER * sizeof(int) <= SH_SMEM_FREE, "");
   return launch_share(kv_release_kernel, a, ctas, 3 * share_of(a.requests, ctas) * sizeof(int), 0, set, st);
 }
@@ -544,8 +573,9 @@ cudaError_t launch_kv_fork(const KvShare& q, cudaStream_t st) {
   a.requests = static_cast<int>(q.requests);
   a.lens_out = q.lens_out;
   a.counts_out = q.counts_out;
-  const int ctas = share_ctas(q.requests);
   static std::atomic<bool> set[64] = {};
+  static std::atomic<int> most[64] = {};
+  const int ctas = share_ctas(kv_fork_kernel, q.requests, most);
   return launch_share(kv_fork_kernel, a, ctas, (a.requests + share_of(a.requests, ctas)) * sizeof(int),
                       (SH_MAX_REQUESTS + SH_MAX_REQUESTS / SH_CLUSTER) * sizeof(int), set, st);
 }
