@@ -109,7 +109,7 @@ struct KvEntry {
   int start;                   // the first key
   int row;                     // of the table
   int prefix;                  // the rows of a group: all of them see all of the keys
-  int pad[2];
+  float prefix_time, own_time; // of a group, in SM-microseconds: for how many SMs each pass gets
 };
 // rec of a row: {its first part's slot, the CTA that has it, the parts (0: the state is
 // whole), the row in the unit and flags}.  Part i > 0 stands in slot 2 (CTA + i).
@@ -124,7 +124,10 @@ struct KvPassArgs {
   const KvEntry* list;
   int64_t entries;
   KvStates prefix, own;
+  const KvEntry* groups;       // two passes beside one another: whose times share the SMs out
+  int n_groups;                // (0: each pass takes what it finds)
 };
+constexpr int KV_SPLIT_GROUPS = 64;         // at the most: a lane reads two
 // Which kernel a pass takes: rows of a unit 8 or 16 (kvattn.cu) or 256 (kvprompt.cu),
 // for entries of so many rows a cache head (and keys).
 int kv_pass_unit(int64_t rows);

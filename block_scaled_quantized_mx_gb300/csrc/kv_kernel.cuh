@@ -123,6 +123,32 @@ __device__ __forceinline__ int kv_end_key(const KvView& v, const Req& r, int i) 
   return p > 0 ? p : 0;
 }
 
+// The SMs that a prefixes' pass takes when the requests' pass runs beside it on the others: P
+// such that both end together, lag + A / P = B / (sms - P), where A and B are what the plan
+// expects of them in SM-microseconds and `lag` what the prefixes' pass takes longer to
+// begin and end.  An even number, of a grid whose CTAs come in clusters of two: a pair of SMs
+// with one of the prompt kernel's CTAs and some of the other pass's is slow at both (128 x 4 drafts
+// behind 32768 tokens: 266 and 250 us for the pairs of one kind, 383 and 331 for a mixed
+// one).  0: there are no prefixes.  For a whole warp.
+__device__ __forceinline__ int kv_split(const KvEntry* groups, int n, int sms) {
+  constexpr float lag = 5.0f;
+  float A = 0.0f, B = 0.0f;
+  for (int i = threadIdx.x & 31; i < n; i += 32) {
+    const float2 t = __ldcg(reinterpret_cast<const float2*>(&groups[i].prefix_time));
+    A += t.x;
+    B += t.y;
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    A += __shfl_xor_sync(0xFFFFFFFFu, A, d);
+    B += __shfl_xor_sync(0xFFFFFFFFu, B, d);
+  }
+  if (!(A > 0.0f)) return 0;
+  const float p = lag * sms - A - B, q = sqrtf(p * p + 4.0f * lag * A * sms);
+  const float x = p > 0.0f ? (p + q) / (2.0f * lag) : 2.0f * A * sms / (q - p);
+  return max(2, min(sms - 2, static_cast<int>(x) & ~1));
+}
+
 // The list of all requests' row tiles (`rows` rows each), and the request of a
 // tile in it.  Starts are kept in 32 bits.  Rows of Q that belong to one request
 // each make `most` tiles at most, a last one that is not full for every request

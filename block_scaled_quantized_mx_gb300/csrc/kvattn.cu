@@ -168,6 +168,8 @@ struct KaArgs {
   uint8_t* joins;              // one KaJoin per CTA, behind the slots (not SH)
   KvStates prefix, own;        // SH
   int wait;                    // SH: the kernel before this one wrote the list
+  const KvEntry* groups;       // SH: the SMs are shared out by kv_split
+  int n_groups;
 };
 
 __device__ __forceinline__ void ka_timeout(volatile int* abort, unsigned site) {
@@ -328,6 +330,13 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
   // CTAs that wait for their SMs).
   if constexpr (SH)
     if (a.wait) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // SH: beside a prefixes' pass as many CTAs as its SMs leave room for
+  long long room = gridDim.x;
+  if constexpr (SH)
+    if (a.n_groups > 0) {
+      const int sms = gridDim.x / ka_ctas_per_sm<NR>();
+      room = (sms - kv_split(a.groups, a.n_groups, sms)) * ka_ctas_per_sm<NR>();
+    }
   // ---- the list: its length, and where this CTA's stretch begins
   const int per = (a.v.requests + KA_THREADS - 1) / KA_THREADS;
   const int rb0 = min(a.v.requests, tid * per), rb1 = min(a.v.requests, rb0 + per);
@@ -351,7 +360,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
     total += sm_scan[i];
   }
   // SH: the CTAs that there is little for leave their SMs to the next kernel's at once
-  const long long ctas = min(static_cast<long long>(gridDim.x), SH ? max(1ll, ka_div(total, KA_LEAST)) : total);
+  const long long ctas = min(room, SH ? max(1ll, ka_div(total, KA_LEAST)) : total);
   const long long cta = blockIdx.x;
   KaJoin<ROWS>* join = SH ? nullptr : reinterpret_cast<KaJoin<ROWS>*>(a.joins) + cta;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1210,6 +1219,8 @@ cudaError_t ka_launch(const KvAttn& q, const KvPassArgs* pass, int nr, bool wait
     a.prefix = pass->prefix;
     a.own = pass->own;
     a.wait = wait;
+    a.groups = pass->groups;
+    a.n_groups = pass->n_groups;
   }
   if (q.ws && q.ws_bytes >= ka_ws_bytes(c.d, nr, sms, SH)) {
     a.ws = static_cast<float*>(q.ws);

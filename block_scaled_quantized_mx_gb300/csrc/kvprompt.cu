@@ -81,7 +81,8 @@ constexpr int KP_PG = 8;                   // blocks whose page data is kept
 constexpr int KP_STAGES = 2;               // f16 tiles of K, and of V
 constexpr int KP_MAX_REQUESTS = 16384;
 constexpr int KP_KEPT = 1024;              // entries of the list that a CTA keeps at first
-// SH: entries of a CTA at the least.  A few blocks more on fewer SMs, the others being left
+// SH: entries of a CTA at the least, where kv_split does not say how many CTAs there
+// are.  A few blocks more on fewer SMs, the others being left
 // to the next kernel's CTAs at once, take less time than both kernels one after the
 // other: beginning and ending one takes as long as four blocks.
 constexpr int KP_LEAST = 6;
@@ -233,6 +234,8 @@ struct KpArgs {
   KpJoin* joins;                           // one per CTA
   KvStates prefix, own;                    // SH
   int wait;                                // SH: the kernel before this one wrote the list
+  const KvEntry* groups;                   // SH: the SMs are shared out by kv_split
+  int n_groups;
 };
 
 __device__ __forceinline__ void kp_timeout(volatile int* abort, unsigned site) {
@@ -429,6 +432,10 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     if (a.wait) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+  int split = 0;
+  if constexpr (SH)
+    if (a.n_groups > 0) split = kv_split(a.groups, a.n_groups, gridDim.x);
+
   // ---- the list: row tiles of each request, then entries of each row tile
   // (in the operand regions, which nothing uses yet)
   KpWalk<SH>* walk = reinterpret_cast<KpWalk<SH>*>(gbase + L::WALK_OFF);   // warp 0's, kept by lane 0
@@ -487,6 +494,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     });
     long long before = kp_scan(mine, sm_scan, total);
     ctas = min(static_cast<long long>(gridDim.x), SH ? max(1ll, total / KP_LEAST) : total);
+    if (SH && split > 0) ctas = min(total, static_cast<long long>(split));
     w0 = total * blockIdx.x / max(1ll, ctas);
     if (blockIdx.x < ctas && total > 0 && w0 >= before && w0 < before + mine) {
       long long p = before;
@@ -1333,17 +1341,22 @@ cudaError_t kp_run(const CUtensorMap& tk, const CUtensorMap& tv, const KpArgs& a
       return cudaErrorInvalidConfiguration;
     if (dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
   }
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = st;
   cfg.attrs = attr;
   if constexpr (SH) {
-    cfg.gridDim = dim3(sms);
+    // (kv_split: a cluster of two gets a pair of SMs, so that the next pass has whole pairs)
+    const int pair = a.n_groups > 0 && sms > 1 ? 2 : 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = pair;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(sms / pair * pair);
     cfg.blockDim = dim3(KP_THREADS);
     cfg.dynamicSmemBytes = L::ALLOC;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, tk, tv, a);
   } else {
     kern<<<sms, KP_THREADS, L::ALLOC, st>>>(tk, tv, a);
@@ -1404,6 +1417,8 @@ cudaError_t launch_kv_prompt(const KvAttn& q, int sms, const KvPassArgs* pass, b
     a.prefix = pass->prefix;
     a.own = pass->own;
     a.wait = wait;
+    a.groups = pass->groups;
+    a.n_groups = pass->n_groups;
   }
   CUtensorMap tk, tv;
   if (!kv_tensor_map(&tk, c.k, c) || !kv_tensor_map(&tv, c.v, c)) return cudaErrorInvalidValue;

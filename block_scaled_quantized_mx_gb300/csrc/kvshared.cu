@@ -57,6 +57,17 @@ constexpr int SP_BATCH = 8;                 // table entries of a lane on their 
 constexpr int64_t SP_WORTH = 200 << 20;
 std::atomic<int64_t> g_worth{SP_WORTH};
 
+// SM-microseconds of an entry of either pass, for sharing the SMs out between them (a unit's
+// blocks of 128 keys and four more; its tiles and two more).  Fitted where one or the other
+// bounded the whole, with 8 cache heads, 16 to 256 requests of up to 2048 tokens, 52 to 140 SMs
+// for prefixes of 2048 to 32768: 1.8 to 2.0, with 64 values 1.54 to 1.63; 0.35 to 0.41 and 0.8 to
+// 0.95 with 8 and 16 rows a unit; int8 codes 1.0 to 1.2 of that.  (With the requests' pass on
+// the SMs that six entries a CTA left, 64 requests behind 8192 tokens took 48 us instead of 43,
+// up to 2048 of their own behind 16384 77 instead of 62, 128 x 4 drafts behind 32768 297
+// instead of 283.)
+constexpr float SP_PREFIX_128 = 1.9f, SP_PREFIX_64 = 1.6f;
+constexpr float SP_OWN_8 = 0.4f, SP_OWN_16 = 0.9f, SP_OWN_INT8 = 1.1f;
+
 struct PlanArgs {
   const int* lens;
   const int* cu;
@@ -70,6 +81,11 @@ struct PlanArgs {
   int page_shift;
   long long worth;            // keys times requests that are spared them, to be shared at all
   KvEntry* list;              // n for the groups, then the requests'
+  // what the passes are expected to take, where they run beside one another (split)
+  int split;
+  int heads, group;           // of the cache, query heads of each
+  int own_rows, own_tile;     // of the requests' pass: rows of a unit, keys of a tile
+  float own_entry, prefix_entry;   // SM-microseconds of a tile, of a block of 256 rows
 };
 
 // The least a and the sum of b over the block's threads.  `sm`: of this call alone.
@@ -83,6 +99,18 @@ __device__ __forceinline__ void plan_reduce(int& a, int& b, int2* sm) {
   b = __reduce_add_sync(0xFFFFFFFFu, v.y);
 }
 
+// The sum over the block's threads, in a fixed order.
+__device__ __forceinline__ float plan_sum(float v, float* sm) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = sm[threadIdx.x & 31];
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+  return v;
+}
+
 // One group to a CTA or to a cluster.  Its requests are groups[g] .. groups[g + 1] - 1,
 // offsets taken in order: one below an earlier one counts as that one.  Its prefix is what
 // `shared` says, what stands in front of all its rows, and what the rows of the table agree on,
@@ -91,6 +119,7 @@ __device__ __forceinline__ void plan_reduce(int& a, int& b, int2* sm) {
 __global__ void __launch_bounds__(SP_THREADS) kv_plan_kernel(const PlanArgs a) {
   __shared__ int2 sm[3][SP_WARPS];
   __shared__ int sm_agree;
+  __shared__ float sm_own[SP_WARPS];
   wait_for_stream();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, B = a.requests;
@@ -152,20 +181,39 @@ __global__ void __launch_bounds__(SP_THREADS) kv_plan_kernel(const PlanArgs a) {
   }
   int keys = agree < pages ? agree << a.page_shift : max(0, most);
   if (static_cast<long long>(keys) * (with_rows - 1) < a.worth) keys = 0;
-  auto entry = [&](int i, int q0, int q1, int len, int start, int row, int prefix) {
+  auto entry = [&](int i, int q0, int q1, int len, int start, int row, int prefix, float t0, float t1) {
     int4* e = reinterpret_cast<int4*>(a.list + i);
     e[0] = make_int4(q0, q1, len, start);
-    e[1] = make_int4(row, prefix, 0, 0);
+    e[1] = make_int4(row, prefix, __float_as_int(t0), __float_as_int(t1));
   };
-  auto request = [&](int b, int start) { entry(a.n + b, a.cu[b], a.cu[b + 1], a.lens[b], start, b, 0); };
+  float own = 0.0f;                         // entries of the requests' pass
+  auto request = [&](int b, int start) {
+    const int q0 = a.cu[b], q1 = a.cu[b + 1], len = a.lens[b];
+    entry(a.n + b, q0, q1, len, start, b, 0, 0.0f, 0.0f);
+    if (a.split && q1 > q0) {
+      const int from = start >> a.page_shift << a.page_shift;
+      const int tiles = max(1, (max(0, min(len, a.capacity) - from) + a.own_tile - 1) / a.own_tile);
+      own += ceilf(static_cast<float>(q1 - q0) * a.group / a.own_rows) * (2 + tiles);
+    }
+  };
   if (rank == 0) {
-    if (tid == 0) entry(g, a.cu[r0], keys > 0 ? a.cu[r1] : a.cu[r0], keys, 0, r0, 1);
     for (int b = r0 + tid; b < r1; b += SP_THREADS) request(b, keys);
     // requests of no group
     if (g == 0)
       for (int b = tid; b < r0; b += SP_THREADS) request(b, 0);
     if (g == a.n - 1)
       for (int b = r1 + tid; b < B; b += SP_THREADS) request(b, 0);
+    float prefix = 0.0f;
+    if (a.split) {
+      own = plan_sum(own, sm_own);
+      // a block's 256 rows in halves: one alone takes 0.74 of the time of both
+      const float rows = static_cast<float>(a.cu[r1] - a.cu[r0]) * a.group, full = floorf(rows / 256.0f);
+      const float rest = rows - 256.0f * full;
+      prefix = (full + (rest > 128.0f ? 1.0f : rest > 0.0f ? 0.74f : 0.0f)) * (4 + (keys + 127) / 128);
+    }
+    if (tid == 0)
+      entry(g, a.cu[r0], keys > 0 ? a.cu[r1] : a.cu[r0], keys, 0, r0, 1,
+            keys > 0 ? prefix * a.heads * a.prefix_entry : 0.0f, own * a.heads * a.own_entry);
   }
   __syncwarp();
   if (ctas > 1) cluster_wait();             // nobody reads this CTA's word any more
@@ -368,6 +416,15 @@ cudaError_t launch_kv_attention_shared(const KvAttn& q, const KvGroups& g, cudaS
   const Layout l = layout_of(q.tokens, q.q_heads, c.heads, c.d, q.max_q, q.requests, g.n, sms);
   char* ws = static_cast<char*>(q.ws) + (reinterpret_cast<uintptr_t>(q.ws) & 16);
   KvEntry* list = reinterpret_cast<KvEntry*>(ws + l.list);
+  // Which kernels: one for both where their units are alike, or the group's rows make two of
+  // the requests' units at most.
+  const int64_t group = q.q_heads / c.heads;
+  const int64_t rows = std::max<int64_t>(1, q.tokens / g.n) * group;
+  int prefix_unit = kv_pass_prefix_unit(rows, most);
+  const int own_unit = kv_pass_unit(q.max_q * group);
+  const bool one = own_unit != 256 && prefix_unit != 256 &&
+                   (own_unit == prefix_unit || rows <= 2 * own_unit);
+  if (one) prefix_unit = own_unit;
   PlanArgs p{};
   p.lens = q.lens;
   p.cu = q.cu;
@@ -381,6 +438,13 @@ cudaError_t launch_kv_attention_shared(const KvAttn& q, const KvGroups& g, cudaS
   p.capacity = static_cast<int>(most < 0x7FFFFF00 ? most : 0x7FFFFF00);
   p.page_shift = kv_page_shift(c.page);
   p.list = list;
+  p.split = !one && prefix_unit == 256 && own_unit != 256 && g.n <= KV_SPLIT_GROUPS;
+  p.heads = static_cast<int>(c.heads);
+  p.group = static_cast<int>(group);
+  p.own_rows = own_unit;
+  p.own_tile = c.d == 64 ? 256 : 128;
+  p.own_entry = (own_unit == 8 ? SP_OWN_8 : SP_OWN_16) * (c.fmt == FMT_INT8 ? SP_OWN_INT8 : 1.0f);
+  p.prefix_entry = c.d == 64 ? SP_PREFIX_64 : SP_PREFIX_128;
   const bool alone = g.n > SP_MANY_GROUPS || q.requests * q.width <= SP_ENTRIES * g.n;
   const int cluster = alone ? 1 : SP_CLUSTER;
   cudaError_t e = launch_early(kv_plan_kernel, dim3(static_cast<unsigned>(cluster), static_cast<unsigned>(g.n)),
@@ -394,19 +458,14 @@ cudaError_t launch_kv_attention_shared(const KvAttn& q, const KvGroups& g, cudaS
     sets[i]->states.rec = reinterpret_cast<int4*>(ws + l.rec[i]);
     sets[i]->parts = reinterpret_cast<const float*>(ws + l.parts[i]);
   }
-  // Which kernels: one for both where their units are alike, or the group's rows make two of
-  // the requests' units at most.
-  const int64_t group = q.q_heads / c.heads;
-  const int64_t rows = std::max<int64_t>(1, q.tokens / g.n) * group;
-  j.prefix.unit = kv_pass_prefix_unit(rows, most);
-  j.own.unit = kv_pass_unit(q.max_q * group);
-  const bool one = j.own.unit != 256 && j.prefix.unit != 256 &&
-                   (j.own.unit == j.prefix.unit || rows <= 2 * j.own.unit);
-  if (one) j.prefix.unit = j.own.unit;
+  j.prefix.unit = prefix_unit;
+  j.own.unit = own_unit;
   for (int i = 0; i < 2; ++i) sets[i]->ctas = kv_pass_ctas(sets[i]->unit, sms);
   KvPassArgs pass{};
   pass.prefix = j.prefix.states;
   pass.own = j.own.states;
+  pass.groups = list;
+  pass.n_groups = p.split ? static_cast<int>(g.n) : 0;
   KvAttn a = q;
   a.window = 0;
   if (one) {
