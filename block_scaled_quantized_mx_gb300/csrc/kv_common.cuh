@@ -127,11 +127,10 @@ struct KvPassArgs {
   const KvEntry* groups;       // two passes beside one another: whose times share the SMs out
   int n_groups;                // (0: each pass takes what it finds)
 };
-constexpr int KV_SPLIT_GROUPS = 64;         // at the most: a lane reads two
+constexpr int KV_SPLIT_GROUPS = 512;        // at the most: a lane reads 16
 // Which kernel a pass takes: rows of a unit 8 or 16 (kvattn.cu) or 256 (kvprompt.cu),
-// for entries of so many rows a cache head (and keys).
+// for entries of so many rows a cache head.
 int kv_pass_unit(int64_t rows);
-int kv_pass_prefix_unit(int64_t rows, int64_t keys);
 int kv_pass_ctas(int unit, int sms);
 size_t kv_pass_workspace_bytes(int unit, int64_t d, int sms);
 int kv_sm_count();

@@ -1275,19 +1275,11 @@ cudaError_t launch_kv_attention(const KvAttn& q, cudaStream_t st) {
 
 int kv_sm_count() { return ka_sm_count(); }
 
+// (A prefix's pass by the same rule.  Measured with 8 cache heads of 128 values, one group, up to
+// 512 tokens of each request's own: this kernel against the prompt kernel, each with the
+// requests' pass: 48 rows, 4096 keys 28.0 against 26.4 us, 16384 41 against 36; 64 rows, 2048 keys 27.7
+// against 25.5, 16384 46 against 36; 256 rows, 512 keys 35 against 28, 2048 42 against 35.)
 int kv_pass_unit(int64_t rows) { return many_rows(rows, 1) ? 256 : 8 * few_rows_nr(rows); }
-
-// For a prefix's pass the rows of a group are many, but its keys may be few: the prompt
-// kernel takes longer to begin and end.  Measured with 8 cache heads of 128 values, one group
-// (this kernel against the prompt kernel, each with its join): 64 rows, 2048 keys
-// 15.5 against 23.4 us, 8192 23.4 against 29.0, 32768 56.9 against 46.5; 128 rows
-// 18.0 against 24.8, 33.7 against 30.7, 95.2 against 48.2; 256 rows 23.2 against 29.6,
-// 52.8 against 38.0; 512 rows, 512 keys 17.9 against 21.6, 2048 33.9 against 29.1.  So their
-// product decides, with the keys that a row of the table has room for.
-constexpr int64_t KA_MOST_PREFIX = 900000;
-int kv_pass_prefix_unit(int64_t rows, int64_t keys) {
-  return rows <= KA_MOST_PREFIX / std::max<int64_t>(1, keys) ? 8 * few_rows_nr(rows) : kv_pass_unit(rows);
-}
 
 int kv_pass_ctas(int unit, int sms) { return unit == 256 ? sms : ka_ctas(unit / 8, sms); }
 

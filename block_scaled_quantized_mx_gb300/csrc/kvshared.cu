@@ -50,11 +50,11 @@ constexpr int SP_BATCH = 8;                 // table entries of a lane on their 
 
 // A prefix is worth a pass where it saves this many bytes of reads.  They come from L2
 // for all requests but one, so that mx_kv_attention loses little by short ones.  Measured
-// with 8 cache heads of 128 values, one group (shared against mx_kv_attention; bytes saved):
-// 4 requests, 8192 keys 19.5 against 16.6 us (50 MB), 32768 37.8 against 36.9 (201);
-// 16 requests, 2048 keys 23.0 against 16.9 (63), 8192 31.5 against 34.0 (252); 64 requests,
-// 512 keys 32.3 against 18.9 (66), 2048 36.0 against 37.4 (264), 8192 42.6 against 109 (1057).
-constexpr int64_t SP_WORTH = 200 << 20;
+// with 8 cache heads of 128 values, one group (shared against mx_kv_attention; MiB saved):
+// 4 requests, 8192 keys 19.5 against 16.6 us (48); 16, 2048 keys 25.5 against 17.1 (60), 4096
+// 27.1 against 23.4 (120), 8192 30 against 36 (240); 64, 512 keys 28 against 20 (63), 1024 29 against
+// 27 (126), 2048 35 against 42 (252), 8192 43 against 113 (1008); 64 values 29 against 35 (184).
+constexpr int64_t SP_WORTH = 150 << 20;
 std::atomic<int64_t> g_worth{SP_WORTH};
 
 // SM-microseconds of an entry of either pass, for sharing the SMs out between them (a unit's
@@ -420,7 +420,7 @@ cudaError_t launch_kv_attention_shared(const KvAttn& q, const KvGroups& g, cudaS
   // the requests' units at most.
   const int64_t group = q.q_heads / c.heads;
   const int64_t rows = std::max<int64_t>(1, q.tokens / g.n) * group;
-  int prefix_unit = kv_pass_prefix_unit(rows, most);
+  int prefix_unit = kv_pass_unit(rows);
   const int own_unit = kv_pass_unit(q.max_q * group);
   const bool one = own_unit != 256 && prefix_unit != 256 &&
                    (own_unit == prefix_unit || rows <= 2 * own_unit);
