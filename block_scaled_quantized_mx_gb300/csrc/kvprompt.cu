@@ -434,7 +434,10 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 
   int split = 0;
   if constexpr (SH)
-    if (a.n_groups > 0) split = kv_split(a.groups, a.n_groups, gridDim.x);
+    if (a.n_groups > 0) {
+      split = kv_split(a.groups, a.n_groups, gridDim.x);
+      if (!a.wait && split > 0) split = gridDim.x - split;   // the requests' pass
+    }
 
   // ---- the list: row tiles of each request, then entries of each row tile
   // (in the operand regions, which nothing uses yet)

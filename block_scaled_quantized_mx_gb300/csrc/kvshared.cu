@@ -56,6 +56,12 @@ constexpr int SP_BATCH = 8;                 // table entries of a lane on their 
 // 27 (126), 2048 35 against 42 (252), 8192 43 against 113 (1008); 64 values 29 against 35 (184).
 constexpr int64_t SP_WORTH = 150 << 20;
 std::atomic<int64_t> g_worth{SP_WORTH};
+// Nor is it where the requests' rows fill the prompt kernel's units of 256 by themselves: its time
+// is then that of the products, which sharing does not save.  Rows of each request, on the average;
+// measured (32 requests behind 4096 tokens; shared against mx_kv_attention): 36 rows 55 against
+// 109 us, 64 70 against 111, 128 106 against 114, 256 185 against 146; behind 8192, one cache
+// head to eight, 128 rows 164 against 202; 64 behind 8192, 256 rows 544 against 469.
+constexpr int64_t SP_MOST_ROWS = 192;
 
 // SM-microseconds of an entry of either pass, for sharing the SMs out between them (a unit's
 // blocks of 128 keys and four more; its tiles and two more).  Fitted where one or the other
@@ -109,6 +115,13 @@ __device__ __forceinline__ float plan_sum(float v, float* sm) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
   return v;
+}
+
+// The prompt kernel's units of so many rows.  Their 256 rows go in halves: one alone takes
+// 0.74 of the time of both.
+__device__ __forceinline__ float plan_units_256(float rows) {
+  const float full = floorf(rows / 256.0f), rest = rows - 256.0f * full;
+  return full + (rest > 128.0f ? 1.0f : rest > 0.0f ? 0.74f : 0.0f);
 }
 
 // One group to a CTA or to a cluster.  Its requests are groups[g] .. groups[g + 1] - 1,
@@ -193,7 +206,8 @@ __global__ void __launch_bounds__(SP_THREADS) kv_plan_kernel(const PlanArgs a) {
     if (a.split && q1 > q0) {
       const int from = start >> a.page_shift << a.page_shift;
       const int tiles = max(1, (max(0, min(len, a.capacity) - from) + a.own_tile - 1) / a.own_tile);
-      own += ceilf(static_cast<float>(q1 - q0) * a.group / a.own_rows) * (2 + tiles);
+      const float rows = static_cast<float>(q1 - q0) * a.group;
+      own += a.own_rows == 256 ? plan_units_256(rows) * (4 + tiles) : ceilf(rows / a.own_rows) * (2 + tiles);
     }
   };
   if (rank == 0) {
@@ -206,10 +220,7 @@ __global__ void __launch_bounds__(SP_THREADS) kv_plan_kernel(const PlanArgs a) {
     float prefix = 0.0f;
     if (a.split) {
       own = plan_sum(own, sm_own);
-      // a block's 256 rows in halves: one alone takes 0.74 of the time of both
-      const float rows = static_cast<float>(a.cu[r1] - a.cu[r0]) * a.group, full = floorf(rows / 256.0f);
-      const float rest = rows - 256.0f * full;
-      prefix = (full + (rest > 128.0f ? 1.0f : rest > 0.0f ? 0.74f : 0.0f)) * (4 + (keys + 127) / 128);
+      prefix = plan_units_256(static_cast<float>(a.cu[r1] - a.cu[r0]) * a.group) * (4 + (keys + 127) / 128);
     }
     if (tid == 0)
       entry(g, a.cu[r0], keys > 0 ? a.cu[r1] : a.cu[r0], keys, 0, r0, 1,
@@ -407,11 +418,12 @@ cudaError_t launch_kv_attention_shared(const KvAttn& q, const KvGroups& g, cudaS
   const size_t need = kv_attention_shared_workspace_bytes(q.tokens, q.q_heads, c.heads, c.d, q.max_q,
                                                           q.requests, g.n);
   // Without groups or room for the states, or where not even prefixes as long as the table
-  // would be worth a pass: each request for itself.
+  // would be worth a pass, or the requests' rows are many: each request for itself.
   const int64_t most = q.width << kv_page_shift(c.page);
   const int64_t bytes = 2 * c.heads * c.d, worth = g_worth.load(std::memory_order_relaxed);
   if (g.n == 0 || need == 0 || q.ws == nullptr || q.ws_bytes < need ||
-      (q.requests - g.n) * most < worth / bytes)
+      (q.requests - g.n) * most < worth / bytes ||
+      (worth > 0 && q.tokens * (q.q_heads / c.heads) > SP_MOST_ROWS * q.requests))
     return launch_kv_attention(q, st);
   const Layout l = layout_of(q.tokens, q.q_heads, c.heads, c.d, q.max_q, q.requests, g.n, sms);
   char* ws = static_cast<char*>(q.ws) + (reinterpret_cast<uintptr_t>(q.ws) & 16);
@@ -438,13 +450,14 @@ cudaError_t launch_kv_attention_shared(const KvAttn& q, const KvGroups& g, cudaS
   p.capacity = static_cast<int>(most < 0x7FFFFF00 ? most : 0x7FFFFF00);
   p.page_shift = kv_page_shift(c.page);
   p.list = list;
-  p.split = !one && prefix_unit == 256 && own_unit != 256 && g.n <= KV_SPLIT_GROUPS;
+  p.split = !one && prefix_unit == 256 && g.n <= KV_SPLIT_GROUPS;
   p.heads = static_cast<int>(c.heads);
   p.group = static_cast<int>(group);
   p.own_rows = own_unit;
-  p.own_tile = c.d == 64 ? 256 : 128;
-  p.own_entry = (own_unit == 8 ? SP_OWN_8 : SP_OWN_16) * (c.fmt == FMT_INT8 ? SP_OWN_INT8 : 1.0f);
+  p.own_tile = c.d == 64 && own_unit != 256 ? 256 : 128;
   p.prefix_entry = c.d == 64 ? SP_PREFIX_64 : SP_PREFIX_128;
+  p.own_entry = own_unit == 256 ? p.prefix_entry
+                                : (own_unit == 8 ? SP_OWN_8 : SP_OWN_16) * (c.fmt == FMT_INT8 ? SP_OWN_INT8 : 1.0f);
   const bool alone = g.n > SP_MANY_GROUPS || q.requests * q.width <= SP_ENTRIES * g.n;
   const int cluster = alone ? 1 : SP_CLUSTER;
   cudaError_t e = launch_early(kv_plan_kernel, dim3(static_cast<unsigned>(cluster), static_cast<unsigned>(g.n)),

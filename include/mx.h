@@ -803,7 +803,8 @@ mx_status mx_set_tile_width(int32_t tbn);
 /* Tuning and testing knob: mx_kv_attention_shared shares a prefix where that
  * saves at least this many bytes of reads (keys and values of the prefix, times the
  * requests that are spared them); 0: always, -1 (the default): 150 MiB, below which it
- * takes longer than mx_kv_attention.  Process-wide: set it while no other thread makes that
+ * takes longer than mx_kv_attention.  Unless always, not where the requests have more
+ * than 192 rows for a cache head on the average either.  Process-wide: set it while no other thread makes that
  * call.  Returns MX_ERR_INVALID_ARG for other negative values. */
 mx_status mx_set_shared_bytes(int64_t bytes);
 

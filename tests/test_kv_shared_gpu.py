@@ -408,3 +408,20 @@ def test_a_strided_table_and_a_stream_argument():
         mx.mx_kv_attention_shared(*args, out=out, workspace=ws, stream=s)
         side.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("rows,shares", [(150, True), (260, False)])
+def test_requests_with_rows_of_their_own_for_whole_units(rows, shares):
+    """By default requests of many rows each are left to themselves, however much they have in common."""
+    b = Batch([(96000, [(rows + 9 * i, rows) for i in range(15)])], 1, 1, 64, 128, seed=21)
+    plain = mx.mx_kv_attention(b.q.cuda(), b.cache, _i32(b.table), _i32(b.lens), _i32(b.cu), b.most,
+                               workspace=b.workspace(), out_dtype=F32)
+    assert plain.isfinite().all()
+    try:
+        mx.set_shared_bytes(-1)
+        got = b.run(out_dtype=F32)
+    finally:
+        mx.set_shared_bytes(0)
+    assert torch.equal(got, plain) == (not shares)
+    # each weight is off by 2^-11 of itself at most in either, the rest by far less: twice their sum
+    assert (got - plain).abs().max() <= 2.0 ** -9 * 448 * 2.0 ** (int(b.planes[3].max()) - 127)
