@@ -571,7 +571,7 @@ def _one_gpu(*tensors) -> int:
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError("operands must be CUDA tensors of one GPU")
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != torch._C._cuda_getDevice():   # (a tensor of its means CUDA is up)
         raise ValueError("operands must be CUDA tensors of the current GPU")
     return dev
 

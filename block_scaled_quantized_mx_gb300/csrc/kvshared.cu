@@ -20,12 +20,13 @@
 // Bound: HBM for the own keys, the tensor rate or HBM for the prefix; between them the four
 // launches.  Measured with 32 heads on 8 cache heads of 128, E4M3 (mx_kv_attention,
 // for which a prefix that fits in L2 comes from there): 64 requests behind 8192 tokens with up to 512
-// of their own 47 us (113), of which the plan takes 4.5, the prefix's pass up to 35 with the
-// own one beside it, the join 5; 128 requests with four drafts behind 32768 tokens, E5M2, 298 us
-// (1300), 225 of them the prompt kernel at 0.62 of the bf16 rate; 16 groups of eight behind up
+// of their own 43 us (113), of which the plan takes 3.5, both passes, side by side, 27, the
+// join 6.5; 128 requests with four drafts behind 32768 tokens, E5M2, 283 us (1300), 266 of them the
+// prompt kernel on 128 SMs, at 0.62 of their bf16 rate; 16 groups of eight behind up
 // to 3000 tokens, 16 heads of 64, int8, pages of 16, 52 us (120).
 // (With a join for each pass, the own pass taking the prefix's states up as it wrote: 58, 315,
-// 82; with the prefix's pass on all SMs and the own one behind it: 50.)
+// 82; with the prefix's pass on all SMs and the own one behind it: 50; with the own one
+// on the SMs that are left by six entries a CTA: 48, 297.)
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
