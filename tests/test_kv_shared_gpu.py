@@ -425,3 +425,10 @@ def test_requests_with_rows_of_their_own_for_whole_units(rows, shares):
     assert torch.equal(got, plain) == (not shares)
     # each weight is off by 2^-11 of itself at most in either, the rest by far less: twice their sum
     assert (got - plain).abs().max() <= 2.0 ** -9 * 448 * 2.0 ** (int(b.planes[3].max()) - 127)
+
+
+@pytest.mark.parametrize("groups", [70, 600])
+def test_many_groups_of_many_rows(groups):
+    """More groups than a lane of the prompt kernel's pass looks at once, and more than it looks at at all."""
+    b = Batch([(20 + g % 40, [(20 + g % 7, 20), (25 + g % 11, 17)]) for g in range(groups)], 1, 1, 64, 16, seed=groups)
+    b.check(b.run())
