@@ -23,7 +23,7 @@
 // of their own 43 us (113), of which the plan takes 3.5, both passes, side by side, 27, the
 // join 6.5; 128 requests with four drafts behind 32768 tokens, E5M2, 283 us (1300), 266 of them the
 // prompt kernel on 128 SMs, at 0.62 of their bf16 rate; 16 groups of eight behind up
-// to 3000 tokens, 16 heads of 64, int8, pages of 16, 52 us (120).
+// to 3000 tokens, 16 heads of 64, int8, pages of 16, 48.5 us (120).
 // (With a join for each pass, the own pass taking the prefix's states up as it wrote: 58, 315,
 // 82; with the prefix's pass on all SMs and the own one behind it: 50; with the own one
 // on the SMs that are left by six entries a CTA: 48, 297.)
@@ -68,12 +68,12 @@ constexpr int64_t SP_MOST_ROWS = 192;
 // blocks of 128 keys and four more; its tiles and two more).  Fitted where one or the other
 // bounded the whole, with 8 cache heads, 16 to 256 requests of up to 2048 tokens, 52 to 140 SMs
 // for prefixes of 2048 to 32768: 1.8 to 2.0, with 64 values 1.54 to 1.63; 0.35 to 0.41 and 0.8 to
-// 0.95 with 8 and 16 rows a unit; int8 codes 1.0 to 1.2 of that.  (With the requests' pass on
+// 0.95 with 8 and 16 rows a unit, with 64 values about 0.7 of that; int8 codes 1.0 to 1.2.  (With the requests' pass on
 // the SMs that six entries a CTA left, 64 requests behind 8192 tokens took 48 us instead of 43,
 // up to 2048 of their own behind 16384 77 instead of 62, 128 x 4 drafts behind 32768 297
 // instead of 283.)
 constexpr float SP_PREFIX_128 = 1.9f, SP_PREFIX_64 = 1.6f;
-constexpr float SP_OWN_8 = 0.4f, SP_OWN_16 = 0.9f, SP_OWN_INT8 = 1.1f;
+constexpr float SP_OWN_8 = 0.4f, SP_OWN_16 = 0.9f, SP_OWN_INT8 = 1.1f, SP_OWN_64 = 0.7f;
 
 struct PlanArgs {
   const int* lens;
@@ -91,7 +91,7 @@ struct PlanArgs {
   // what the passes are expected to take, where they run beside one another (split)
   int split;
   int heads, group;           // of the cache, query heads of each
-  int own_rows, own_tile;     // of the requests' pass: rows of a unit, keys of a tile
+  int own_rows;               // of a unit of the requests' pass
   float own_entry, prefix_entry;   // SM-microseconds of a tile, of a block of 256 rows
 };
 
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(SP_THREADS) kv_plan_kernel(const PlanArgs a) {
     entry(a.n + b, q0, q1, len, start, b, 0, 0.0f, 0.0f);
     if (a.split && q1 > q0) {
       const int from = start >> a.page_shift << a.page_shift;
-      const int tiles = max(1, (max(0, min(len, a.capacity) - from) + a.own_tile - 1) / a.own_tile);
+      const int tiles = max(1, (max(0, min(len, a.capacity) - from) + 127) / 128);
       const float rows = static_cast<float>(q1 - q0) * a.group;
       own += a.own_rows == 256 ? plan_units_256(rows) * (4 + tiles) : ceilf(rows / a.own_rows) * (2 + tiles);
     }
@@ -455,10 +455,9 @@ cudaError_t launch_kv_attention_shared(const KvAttn& q, const KvGroups& g, cudaS
   p.heads = static_cast<int>(c.heads);
   p.group = static_cast<int>(group);
   p.own_rows = own_unit;
-  p.own_tile = c.d == 64 && own_unit != 256 ? 256 : 128;
   p.prefix_entry = c.d == 64 ? SP_PREFIX_64 : SP_PREFIX_128;
   p.own_entry = own_unit == 256 ? p.prefix_entry
-                                : (own_unit == 8 ? SP_OWN_8 : SP_OWN_16) * (c.fmt == FMT_INT8 ? SP_OWN_INT8 : 1.0f);
+                                : (own_unit == 8 ? SP_OWN_8 : SP_OWN_16) * (c.d == 64 ? SP_OWN_64 : 1.0f) * (c.fmt == FMT_INT8 ? SP_OWN_INT8 : 1.0f);
   const bool alone = g.n > SP_MANY_GROUPS || q.requests * q.width <= SP_ENTRIES * g.n;
   const int cluster = alone ? 1 : SP_CLUSTER;
   cudaError_t e = launch_early(kv_plan_kernel, dim3(static_cast<unsigned>(cluster), static_cast<unsigned>(g.n)),
