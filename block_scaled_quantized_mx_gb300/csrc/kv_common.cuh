@@ -131,7 +131,7 @@ constexpr int KV_SPLIT_GROUPS = 512;        // at the most: a lane reads 16
 // Which kernel a pass takes: rows of a unit 8 or 16 (kvattn.cu) or 256 (kvprompt.cu),
 // for entries of so many rows a cache head.
 int kv_pass_unit(int64_t rows);
-int kv_pass_ctas(int unit, int sms);
+int kv_pass_ctas(int unit, int64_t d, int sms);
 size_t kv_pass_workspace_bytes(int unit, int64_t d, int sms);
 int kv_sm_count();
 // Launched as a programmatic dependent; `wait`: what it reads was written by the kernel

@@ -77,7 +77,7 @@ constexpr int KA_RED = 36;                 // floats per row of the staging: 32,
 // Keys per tile: 16 KB of codes of K and as many of V.  (128 keys of 64 values a
 // tile left each warp 32 short keys between two waits.)  SH: 128 at either size, as the keys
 // behind a prefix are few and rarely fill a larger tile (16 groups of eight, up to 300 of their own
-// behind 3000, heads of 64: 48.5 against 51.5 us; up to 2000 89.1 against 88.4).
+// behind 3000, heads of 64: 48.5 against 51.5 us with three CTAs an SM).
 template <int D, bool SH>
 constexpr int ka_tk() {
   return D == 64 && !SH ? 256 : 128;
@@ -92,10 +92,12 @@ constexpr int ka_over() {
   return SH ? 2 : 1;
 }
 
-// CTAs per SM of the 8-row (NR = 1) and the 16-row (NR = 2) kernel.
-template <int NR>
+// CTAs per SM of the 8-row (NR = 1) and the 16-row (NR = 2) kernel.  SH, whose units are
+// short, with heads of 64: one more, with two tiles in flight each instead of four (16 groups of
+// eight, up to 300 of their own behind 3000: 44.3 against 48.5 us; 64 groups 141 against 162).
+template <int D, int NR, bool SH>
 constexpr int ka_ctas_per_sm() {
-  return NR == 1 ? 3 : 2;
+  return (NR == 1 ? 3 : 2) + (SH && D == 64 ? 1 : 0);
 }
 
 // What the producer says about a segment: one CTA's part of a unit.
@@ -138,7 +140,7 @@ struct KaSmem {
   static constexpr int TK = ka_tk<D, SH>();
   static constexpr int MAX_PAGES = TK / 16;            // pages in a tile
   static constexpr int TILE = TK * D;                  // codes of one tile of K or V
-  static constexpr int RING = NR == 1 ? 65536 : 98304;
+  static constexpr int RING = SH && D == 64 ? (NR == 1 ? 32768 : 49152) : NR == 1 ? 65536 : 98304;
   static constexpr int STAGES = RING / (2 * TILE);
   // staging of the warps' O: [warp][8 rows][KA_RED]
   static constexpr int RED_OFF = RING;
@@ -155,7 +157,7 @@ struct KaSmem {
   static constexpr int MISC_OFF = BAR_OFF + STAGES * 16 + 32;
   static constexpr int TOTAL = MISC_OFF + 128;
   static constexpr int ALLOC = TOTAL + 1024;
-  static_assert(ka_ctas_per_sm<NR>() * (ALLOC + 1024) <= 233472, "CTAs per SM");
+  static_assert(ka_ctas_per_sm<D, NR, SH>() * (ALLOC + 1024) <= 233472, "CTAs per SM");
 };
 
 struct KaArgs {
@@ -292,7 +294,7 @@ __device__ __forceinline__ bool ka_all(bool v) {
 }
 
 template <int FMT, int D, int NR, bool SH>
-__global__ void __launch_bounds__(KA_THREADS, ka_ctas_per_sm<NR>())
+__global__ void __launch_bounds__(KA_THREADS, ka_ctas_per_sm<D, NR, SH>())
 kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const KaArgs a) {
   using L = KaSmem<D, NR, SH>;
@@ -336,8 +338,8 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
   long long room = gridDim.x;
   if constexpr (SH)
     if (a.n_groups > 0) {
-      const int sms = gridDim.x / ka_ctas_per_sm<NR>();
-      room = (sms - kv_split(a.groups, a.n_groups, sms)) * ka_ctas_per_sm<NR>();
+      const int sms = gridDim.x / ka_ctas_per_sm<D, NR, SH>();
+      room = (sms - kv_split(a.groups, a.n_groups, sms)) * ka_ctas_per_sm<D, NR, SH>();
     }
   // ---- the list: its length, and where this CTA's stretch begins
   const int per = (a.v.requests + KA_THREADS - 1) / KA_THREADS;
@@ -1147,10 +1149,15 @@ int ka_sm_count() {
 // The workspace of a launch: two slots per CTA (rows x (d + 2) floats), then
 // a KaJoin per CTA.
 int64_t ka_slot_bytes(int64_t d, int nr) { return 8 * nr * (d + 2) * 4; }
-int ka_ctas(int nr, int sms) { return (nr == 1 ? ka_ctas_per_sm<1>() : ka_ctas_per_sm<2>()) * sms; }
+template <int D, bool SH>
+int ka_ctas_of(int nr) { return nr == 1 ? ka_ctas_per_sm<D, 1, SH>() : ka_ctas_per_sm<D, 2, SH>(); }
+int ka_ctas(int64_t d, int nr, bool sh, int sms) {
+  return sms * (d == 64 ? (sh ? ka_ctas_of<64, true>(nr) : ka_ctas_of<64, false>(nr))
+                        : (sh ? ka_ctas_of<128, true>(nr) : ka_ctas_of<128, false>(nr)));
+}
 size_t ka_ws_bytes(int64_t d, int nr, int sms, bool sh) {
   const size_t join = sh ? 0 : nr == 1 ? sizeof(KaJoin<8>) : sizeof(KaJoin<16>);
-  return static_cast<size_t>(ka_ctas(nr, sms)) * (2 * ka_slot_bytes(d, nr) + join);
+  return static_cast<size_t>(ka_ctas(d, nr, sh, sms)) * (2 * ka_slot_bytes(d, nr) + join);
 }
 
 template <int FMT, int D, int NR, bool SH>
@@ -1167,7 +1174,7 @@ cudaError_t ka_run(const CUtensorMap& tk, const CUtensorMap& tv, const KaArgs& a
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
   }
-  const int ctas = ka_ctas(NR, sms);
+  const int ctas = ka_ctas_per_sm<D, NR, SH>() * sms;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1226,7 +1233,7 @@ cudaError_t ka_launch(const KvAttn& q, const KvPassArgs* pass, int nr, bool wait
   }
   if (q.ws && q.ws_bytes >= ka_ws_bytes(c.d, nr, sms, SH)) {
     a.ws = static_cast<float*>(q.ws);
-    a.joins = static_cast<uint8_t*>(q.ws) + ka_ctas(nr, sms) * 2 * ka_slot_bytes(c.d, nr);
+    a.joins = static_cast<uint8_t*>(q.ws) + ka_ctas(c.d, nr, SH, sms) * 2 * ka_slot_bytes(c.d, nr);
   } else if (SH) {
     return cudaErrorInvalidValue;             // the caller has seen to it
   }
@@ -1283,7 +1290,7 @@ int kv_sm_count() { return ka_sm_count(); }
 // against 25.5, 16384 46 against 36; 256 rows, 512 keys 35 against 28, 2048 42 against 35.)
 int kv_pass_unit(int64_t rows) { return many_rows(rows, 1) ? 256 : 8 * few_rows_nr(rows); }
 
-int kv_pass_ctas(int unit, int sms) { return unit == 256 ? sms : ka_ctas(unit / 8, sms); }
+int kv_pass_ctas(int unit, int64_t d, int sms) { return unit == 256 ? sms : ka_ctas(d, unit / 8, true, sms); }
 
 size_t kv_pass_workspace_bytes(int unit, int64_t d, int sms) {
   return unit == 256 ? kv_prompt_workspace_bytes(d, sms) : ka_ws_bytes(d, unit / 8, sms, true);

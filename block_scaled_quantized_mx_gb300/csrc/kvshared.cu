@@ -23,7 +23,7 @@
 // of their own 43 us (113), of which the plan takes 3.5, both passes, side by side, 27, the
 // join 6.5; 128 requests with four drafts behind 32768 tokens, E5M2, 283 us (1300), 266 of them the
 // prompt kernel on 128 SMs, at 0.62 of their bf16 rate; 16 groups of eight behind up
-// to 3000 tokens, 16 heads of 64, int8, pages of 16, 48.5 us (120).
+// to 3000 tokens, 16 heads of 64, int8, pages of 16, 44 us (120).
 // (With a join for each pass, the own pass taking the prefix's states up as it wrote: 58, 315,
 // 82; with the prefix's pass on all SMs and the own one behind it: 50; with the own one
 // on the SMs that are left by six entries a CTA: 48, 297.)
@@ -473,7 +473,7 @@ cudaError_t launch_kv_attention_shared(const KvAttn& q, const KvGroups& g, cudaS
   }
   j.prefix.unit = prefix_unit;
   j.own.unit = own_unit;
-  for (int i = 0; i < 2; ++i) sets[i]->ctas = kv_pass_ctas(sets[i]->unit, sms);
+  for (int i = 0; i < 2; ++i) sets[i]->ctas = kv_pass_ctas(sets[i]->unit, c.d, sms);
   KvPassArgs pass{};
   pass.prefix = j.prefix.states;
   pass.own = j.own.states;
