@@ -421,10 +421,12 @@ cudaError_t launch_kv_attention_shared(const KvAttn& q, const KvGroups& g, cudaS
   // Without groups or room for the states, or where not even prefixes as long as the table
   // would be worth a pass, or the requests' rows are many: each request for itself.
   const int64_t most = q.width << kv_page_shift(c.page);
+  // (Q may have room for more rows than the requests have)
+  const int64_t tokens = std::min(q.tokens, std::max<int64_t>(1, q.max_q) * q.requests);
   const int64_t bytes = 2 * c.heads * c.d, worth = g_worth.load(std::memory_order_relaxed);
   if (g.n == 0 || need == 0 || q.ws == nullptr || q.ws_bytes < need ||
       (q.requests - g.n) * most < worth / bytes ||
-      (worth > 0 && q.tokens * (q.q_heads / c.heads) > SP_MOST_ROWS * q.requests))
+      (worth > 0 && tokens * (q.q_heads / c.heads) > SP_MOST_ROWS * q.requests))
     return launch_kv_attention(q, st);
   const Layout l = layout_of(q.tokens, q.q_heads, c.heads, c.d, q.max_q, q.requests, g.n, sms);
   char* ws = static_cast<char*>(q.ws) + (reinterpret_cast<uintptr_t>(q.ws) & 16);
@@ -432,7 +434,7 @@ cudaError_t launch_kv_attention_shared(const KvAttn& q, const KvGroups& g, cudaS
   // Which kernels: one for both where their units are alike, or the group's rows make two of
   // the requests' units at most.
   const int64_t group = q.q_heads / c.heads;
-  const int64_t rows = std::max<int64_t>(1, q.tokens / g.n) * group;
+  const int64_t rows = std::max<int64_t>(1, tokens / g.n) * group;
   int prefix_unit = kv_pass_unit(rows);
   const int own_unit = kv_pass_unit(q.max_q * group);
   const bool one = own_unit != 256 && prefix_unit != 256 &&

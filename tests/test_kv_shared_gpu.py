@@ -432,3 +432,29 @@ def test_many_groups_of_many_rows(groups):
     """More groups than a lane of the prompt kernel's pass looks at once, and more than it looks at at all."""
     b = Batch([(20 + g % 40, [(20 + g % 7, 20), (25 + g % 11, 17)]) for g in range(groups)], 1, 1, 64, 16, seed=groups)
     b.check(b.run())
+
+
+def test_a_q_with_room_for_more():
+    """Rows behind the last request's choose no kernel and are not written; by default a prefix is shared
+    all the same."""
+    b = Batch([(96000, [(1 + 3 * i, 1) for i in range(15)])], 4, 1, 64, 128, seed=23)
+    T = b.q.shape[0]
+    q = torch.cat([b.q, torch.full((1500, 4, 64), float("nan"), dtype=BF16)]).cuda()
+    n = mx.kv_attention_shared_workspace_bytes(T + 1500, 4, 1, 64, 1, 15, 1)
+    args = (b.cache, _i32(b.table), _i32(b.lens), _i32(b.cu), 1)
+
+    def run(shared):
+        out = torch.full((T + 1500, 4, 64), 7.0, device="cuda")
+        mx.mx_kv_attention_shared(q, *args, _i32([0, 15]), _i32([shared]), out=out,
+                                  workspace=torch.empty(n, dtype=torch.uint8, device="cuda"))
+        assert (out[T:] == 7.0).all()
+        return out[:T]
+
+    always = run(10 ** 9)
+    try:
+        mx.set_shared_bytes(-1)
+        got, none = run(10 ** 9), run(0)
+    finally:
+        mx.set_shared_bytes(0)
+    assert torch.equal(got, always) and not torch.equal(got, none)
+    b.check(got)
