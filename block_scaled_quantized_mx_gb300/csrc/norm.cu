@@ -12,15 +12,17 @@
 // block of 32 is four lanes' values, so its maximum takes two shuffles; four
 // blocks' scales, one 32-bit word of the row's atom, take two more.  The sum is
 // added in a fixed order.
-// Measured: 8192 x 8192, bf16 with a bf16 residual, E4M3: 76 us, 6.2 TB/s, 0.91 of the copy
+// Measured: 8192 x 8192, bf16 with a bf16 residual, E4M3: 77 us, 6.1 TB/s, 0.90 of the copy
 // rate; 4097 x 5120, bf16 with an fp32 residual, E2M1: 37 us, 0.88; 64 x 4096: 2.4 us, a launch
 // and two dependent reads.  The values of 8192 x 8192 E4M3 codes as bf16: 32 us, 0.94.
 //
 // Precision: h, the sum of squares (each thread's, then by halves within a warp, then
 // the warps in order) and y are fp32; r' alone is rounded to its type.  Squares that
-// overflow (|h| from 2^64 / sqrt(K) on) are summed again from h * 2^-100.  eps is
-// 1e-30 at least, so that squares too small for fp32 do not matter beside it.
+// overflow (|h| from 2^64 / sqrt(K) on) are summed again, with eps, in units of 2^144; h itself
+// is not scaled, so that what is small beside them keeps its bits.  eps is 1e-30 at least, so
+// that squares too small for fp32 do not matter beside it.
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "layer_common.cuh"
@@ -102,6 +104,13 @@ __device__ __forceinline__ void store_codes(uint8_t* data, long long at, const f
     *reinterpret_cast<uint2*>(data + at) = make_uint2(a, b);
 }
 
+// The largest of a, |b| and |c|, a NaN if one of them is.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // XW, RW: what a chunk of x and of r takes (RW 0: there is no r); CH: chunks a
 // thread.
 template <int XW, int RW, int CH>
@@ -161,33 +170,51 @@ __global__ void __launch_bounds__(CH <= 2 ? 1024 : 512) rmsnorm_quantize_kernel(
   sum = row_sum(sum, sm_sum);
   float f = __frsqrt_rn(sum / K + a.eps);
   if (!(sum <= 3.402823466e38f)) {           // the whole CTA
+    constexpr float unit = 2.1175824e-22f;   // 2^-72
     sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < CH; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        h[i][e] *= 7.888609052e-31f;         // 2^-100; eps is nothing beside such squares
-        sum = fmaf(h[i][e], h[i][e], sum);
-      }
-    f = __frsqrt_rn(row_sum(sum, sm_sum + 32) / K);
+      for (int e = 0; e < 8; ++e) sum = fmaf(h[i][e] * unit, h[i][e] * unit, sum);
+    // (2^-128 at least, where a subnormal still has 21 bits; 0 beside an infinity)
+    f = __frsqrt_rn(row_sum(sum, sm_sum + 32) / K + a.eps * unit * unit) * unit;
   }
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = threadIdx.x + i * blockDim.x;
     float y[8];
-    uint32_t top = 0;
-    if (c < a.chunks) {
-      const float4* w = reinterpret_cast<const float4*>(a.w) + 2 * c;
-      const float4 w0 = w[0], w1 = w[1];
-      const float ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+    // y of the chunk, and the largest |y| of its block.  FAR: not by way of an h f below the
+    // normal numbers, from where a weight may bring the product back.
+    auto normed = [&](auto far, float& heaviest) {
+      constexpr bool FAR = decltype(far)::value;
+      float most = 0.0f;
+      heaviest = 0.0f;
+      if (c < a.chunks) {
+        const float4* w = reinterpret_cast<const float4*>(a.w) + 2 * c;
+        const float4 w0 = w[0], w1 = w[1];
+        const float ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        y[e] = h[i][e] * f * ww[e];
-        top = max(top, abs_bits(y[e]));
+        for (int e = 0; e < 8; ++e) {
+          const float n = h[i][e] * f;
+          y[e] = n * ww[e];
+          if (FAR && fabsf(n) < 1.17549435e-38f && h[i][e] != 0.0f) y[e] = h[i][e] * (f * ww[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          most = max3_abs(most, y[e], y[e + 1]);
+          if (!FAR) heaviest = max3_abs(heaviest, ww[e], ww[e + 1]);
+        }
       }
-    }
-    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      uint32_t top = __float_as_uint(most);
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      return max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    };
+    // Such an h f is off by 2^-150, y by 2^-90 under a weight of 2^60: 2^-27 of the smallest step
+    // of a code in a block whose largest y is 2^-32.
+    float heaviest;
+    uint32_t top = normed(std::false_type{}, heaviest);
+    if (__any_sync(0xFFFFFFFFu, c < a.chunks && (top < 0x2F800000u || !(heaviest < 1.1529215e18f))))
+      top = normed(std::true_type{}, heaviest);
     uint32_t code;
     float inv;
     block_scale(top, emax_of_fmt(a.fmt), code, inv);

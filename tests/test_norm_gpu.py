@@ -103,6 +103,49 @@ def test_rows_of_zeros_large_and_small_values():
         assert (mx.mx_dequantize(q)[0] == 0).all()
 
 
+def test_small_values_in_rows_whose_squares_overflow():
+    """y of what stands beside values of 2^64 and more is as exact as any: normal fp32 values under normal
+    scales, however far below the row's largest (the bound's roundings and no other: factors of two are exact)."""
+    K = 256
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(7, K, generator=g, device="cuda")
+    x[0] *= 2.0 ** -30
+    x[1] *= 2.0 ** -51
+    x[2] *= torch.exp2(torch.arange(K, device="cuda") / 2 - 60)
+    x[3] *= 2.0 ** 20
+    x[4] *= 2.0 ** -58
+    x[5] *= 2.0 ** 40
+    x[6] *= 2.0 ** -20
+    x[0, 0] = x[1, 77] = x[3, 200] = 2.0 ** 64
+    x[2, 255] = x[5, 31] = 3.0e38
+    x[4, 128] = x[6, 3] = 2.0 ** 66
+    w = 1 + 0.3 * torch.randn(K, generator=g, device="cuda")
+    w[64:96] *= 2.0 ** 30
+    w[96:128] *= 2.0 ** -14
+    for fmt in (mx.E4M3, mx.E5M2, mx.E2M1):
+        q, _ = mx.mx_rmsnorm_quantize(x, w, fmt, eps=1e-6)
+        _check(q, x, None, w, 1e-6, fmt, None)
+        r = x.flip(1).contiguous()
+        q, h = mx.mx_rmsnorm_quantize(x, w, fmt, residual=r, eps=1e-6)
+        _check(q, x, r, w, 1e-6, fmt, h)
+
+
+@pytest.mark.parametrize("rows,K", [(3, 64), (2, 4096), (3, 32768)])
+def test_large_eps(rows, K):
+    """eps counts whatever the squares do: mean squares of 4e34, whose sum overflows at 32768 values, beside an
+    eps of the same size; and rows that a large eps divides down to 2^-90 and weights bring back."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.randn(rows, K, generator=g, device="cuda") * 2e17
+    w = 1 + 0.3 * torch.randn(K, generator=g, device="cuda")
+    for eps in (1e34, 1e36, 3e38):
+        q, _ = mx.mx_rmsnorm_quantize(x, w, mx.E4M3, eps=eps)
+        _check(q, x, None, w, eps, mx.E4M3, None)
+    small = x * 2.0 ** -140
+    for up in (2.0 ** 60, 2.0 ** 100):
+        q, _ = mx.mx_rmsnorm_quantize(small, w * up, mx.E5M2, eps=3e38)
+        _check(q, small, None, w * up, 3e38, mx.E5M2, None)
+
+
 def test_nan_and_infinity_stay_in_their_rows():
     x = torch.randn(4, 256, device="cuda")
     x[1, 40], x[2, 100] = float("nan"), float("inf")
