@@ -95,15 +95,17 @@ struct PlanArgs {
   float own_entry, prefix_entry;   // SM-microseconds of a tile, of a block of 256 rows
 };
 
-// The least a and the sum of b over the block's threads.  `sm`: of this call alone.
-__device__ __forceinline__ void plan_reduce(int& a, int& b, int2* sm) {
+// The least a and c and the sum of b over the block's threads.  `sm`: of this call alone.
+__device__ __forceinline__ void plan_reduce(int& a, int& b, int& c, int4* sm) {
   const int la = __reduce_min_sync(0xFFFFFFFFu, a), sb = __reduce_add_sync(0xFFFFFFFFu, b);
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = make_int2(la, sb);
+  const int lc = __reduce_min_sync(0xFFFFFFFFu, c);
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = make_int4(la, sb, lc, 0);
   __syncthreads();
-  const int2 v = sm[threadIdx.x & 31];
+  const int4 v = sm[threadIdx.x & 31];
   static_assert(SP_WARPS == 32, "a lane for each warp");
   a = __reduce_min_sync(0xFFFFFFFFu, v.x);
   b = __reduce_add_sync(0xFFFFFFFFu, v.y);
+  c = __reduce_min_sync(0xFFFFFFFFu, v.z);
 }
 
 // The sum over the block's threads, in a fixed order.
@@ -127,11 +129,12 @@ __device__ __forceinline__ float plan_units_256(float rows) {
 
 // One group to a CTA or to a cluster.  Its requests are groups[g] .. groups[g + 1] - 1,
 // offsets taken in order: one below an earlier one counts as that one.  Its prefix is what
-// `shared` says, what stands in front of all its rows, and what the rows of the table agree on,
-// whichever is least (a wrong word about a prefix costs time, not the answer); or
-// nothing, if that is too little for a pass.
+// `shared` says, what stands in front of all its rows, and what the rows of the table of its
+// requests that have rows agree on, whichever is least (a wrong word about a prefix costs
+// time, not the answer); or nothing, if that is too little for a pass.  A request without
+// rows, which may have ended and hold nothing, has no say.
 __global__ void __launch_bounds__(SP_THREADS) kv_plan_kernel(const PlanArgs a) {
-  __shared__ int2 sm[3][SP_WARPS];
+  __shared__ int4 sm[3][SP_WARPS];
   __shared__ int sm_agree;
   __shared__ float sm_own[SP_WARPS];
   wait_for_stream();
@@ -148,30 +151,33 @@ __global__ void __launch_bounds__(SP_THREADS) kv_plan_kernel(const PlanArgs a) {
     return n > 0 ? max(0, min(a.lens[b], a.capacity)) - n : 0x7FFFFFFF;
   };
   const int mine = tid < B ? in_front(tid) : 0x7FFFFFFF;
-  plan_reduce(r0, none, sm[0]);
+  plan_reduce(r0, none, none, sm[0]);
   r0 = -r0;
   const int r1 = max(r0, edge);
-  // the tokens that stand in front of every row of the group
-  int most = 0x7FFFFFFF, with_rows = 0;
-  auto count = [&](int tokens) {
+  // the tokens that stand in front of every row of the group, and its first request with rows
+  int most = 0x7FFFFFFF, with_rows = 0, lead = 0x7FFFFFFF;
+  auto count = [&](int b, int tokens) {
+    if (tokens == 0x7FFFFFFF) return;
     most = min(most, tokens);
-    with_rows += tokens != 0x7FFFFFFF;
+    lead = min(lead, b);
+    ++with_rows;
   };
-  if (tid >= r0 && tid < r1) count(mine);
+  if (tid >= r0 && tid < r1) count(tid, mine);
   for (int b = tid + SP_THREADS; b < r1; b += SP_THREADS)
-    if (b >= r0) count(in_front(b));
-  plan_reduce(most, with_rows, sm[1]);
+    if (b >= r0) count(b, in_front(b));
+  plan_reduce(most, with_rows, lead, sm[1]);
   most = with_rows < 2 ? 0 : min(most, said);
-  // the first entry on which a row of the table differs from the group's first
+  // the first entry on which a row of the table differs from that request's
   const int pages = most <= 0 ? 0 : static_cast<int>((most + (1ll << a.page_shift) - 1) >> a.page_shift);
-  const int* first = a.table + r0 * a.table_stride;
+  const int* first = a.table + (pages > 0 ? lead : 0) * a.table_stride;
   const int chunks = (pages + 32 * SP_BATCH - 1) / (32 * SP_BATCH);
   int agree = pages;
-  for (long long i = rank * SP_WARPS + (tid >> 5); i < static_cast<long long>(chunks) * (r1 - r0 - 1);
+  for (long long i = rank * SP_WARPS + (tid >> 5); i < static_cast<long long>(chunks) * (r1 - 1 - lead);
        i += ctas * SP_WARPS) {
-    const int b = r0 + 1 + static_cast<int>(i / chunks);
+    const int b = lead + 1 + static_cast<int>(i / chunks);
     const int j0 = static_cast<int>(i % chunks) * 32 * SP_BATCH + lane;
     const int* row = a.table + b * a.table_stride;
+    const bool has_rows = a.cu[b + 1] > a.cu[b];   // (read with the entries)
     int own[SP_BATCH], ref[SP_BATCH];
 #pragma unroll
     for (int u = 0; u < SP_BATCH; ++u) {
@@ -183,9 +189,9 @@ __global__ void __launch_bounds__(SP_THREADS) kv_plan_kernel(const PlanArgs a) {
     }
 #pragma unroll
     for (int u = SP_BATCH - 1; u >= 0; --u)
-      if (own[u] != ref[u]) agree = min(agree, j0 + 32 * u);
+      if (has_rows && own[u] != ref[u]) agree = min(agree, j0 + 32 * u);
   }
-  plan_reduce(agree, none, sm[2]);
+  plan_reduce(agree, none, none, sm[2]);
   if (ctas > 1) {
     if (tid == 0) sm_agree = agree;
     cluster_sync();
@@ -224,7 +230,7 @@ __global__ void __launch_bounds__(SP_THREADS) kv_plan_kernel(const PlanArgs a) {
       prefix = plan_units_256(static_cast<float>(a.cu[r1] - a.cu[r0]) * a.group) * (4 + (keys + 127) / 128);
     }
     if (tid == 0)
-      entry(g, a.cu[r0], keys > 0 ? a.cu[r1] : a.cu[r0], keys, 0, r0, 1,
+      entry(g, a.cu[r0], keys > 0 ? a.cu[r1] : a.cu[r0], keys, 0, keys > 0 ? lead : r0, 1,
             keys > 0 ? prefix * a.heads * a.prefix_entry : 0.0f, own * a.heads * a.own_entry);
   }
   __syncwarp();

@@ -739,8 +739,9 @@ mx_status mx_kv_attention(const void* Q, int32_t dtype, int64_t tokens, int64_t 
  *              first group and behind the last share nothing
  *   shared     device, int32, n_groups entries: how many of its first tokens a group's
  *              requests have in common, or more.  Shared are those in front of the first page
- *              on which the requests' rows of the table differ, and in front of all of
- *              the group's rows: any value gives the right results.  (Prefixes that
+ *              on which the rows of the table of requests that have rows of Q differ, and in
+ *              front of all of the group's rows: any value gives the right results, and a
+ *              request that adds no tokens, or has ended, has no say.  (Prefixes that
  *              are not worth it are not shared: mx_set_shared_bytes.)
  *   workspace  as for mx_kv_attention, at least mx_kv_attention_shared_workspace_bytes()
  *              bytes, which grow with each argument; NULL or a smaller size, or no groups:

@@ -458,3 +458,31 @@ def test_a_q_with_room_for_more():
         mx.set_shared_bytes(0)
     assert torch.equal(got, always) and not torch.equal(got, none)
     b.check(got)
+
+
+@pytest.mark.parametrize("ended", [[0], [2], [4], [0, 2, 4], [0, 1]])
+@pytest.mark.parametrize("left", [-1, 10 ** 6])
+def test_requests_without_rows_take_no_sharing_away(ended, left):
+    """Requests that have ended, whose rows of the table hold no page or whatever stood there: the others' bits are
+    those of a call in which the pages are still in place, and not those without sharing."""
+    each = [(17, 1), (200, 1), (33, 2), (64, 1), (40, 4), (9, 1)]
+    b = Batch([(300, [(n, 0 if i in ended else r) for i, (n, r) in enumerate(each)])], 6, 2, 128, 32, mx.E5M2, F16, seed=31)
+    want, none = b.run(out_dtype=F32), b.run(shared=[0], out_dtype=F32)
+    assert not torch.equal(want, none)
+    for i in ended:
+        b.table[i], b.lens[i] = left, 0
+    got = b.run(out_dtype=F32)
+    b.check(got)
+    assert torch.equal(got, want)
+
+
+def test_a_group_with_one_request_that_has_rows():
+    b = Batch([(300, [(17, 0), (200, 3), (33, 0)]), (0, [(90, 1)])], 4, 2, 64, 32, seed=32)
+    b.table[[0, 2]] = -1
+    b.lens[0] = b.lens[2] = 0
+    b.check(b.run())
+    b.cu[:] = 0                                  # nobody has
+    b.q = b.q[:1]
+    out = torch.full((1, 4, 64), 7.0, device="cuda")
+    b.run(out=out, out_dtype=F32)
+    assert (out == 7.0).all() and mx.mx_last_error() == 0
