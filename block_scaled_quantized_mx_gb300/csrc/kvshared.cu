@@ -86,7 +86,7 @@ struct PlanArgs {
   int n;                      // groups
   int capacity;               // tokens a table row holds
   int page_shift;
-  long long worth;            // keys times requests that are spared them, to be shared at all
+  long long worth;            // keys times requests that are spared them, of all groups, to be shared at all
   KvEntry* list;              // n for the groups, then the requests'
   // what the passes are expected to take, where they run beside one another (split)
   int split;
@@ -141,8 +141,13 @@ __global__ void __launch_bounds__(SP_THREADS) kv_plan_kernel(const PlanArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, B = a.requests;
   const int rank = blockIdx.x, ctas = gridDim.x, g = blockIdx.y;
-  int r0 = 0, none = 0;
-  for (int i = tid; i <= g; i += SP_THREADS) r0 = min(r0, -max(0, min(a.groups[i], B)));
+  int r0 = 0, several = 0, none = 0;         // several: groups of two requests or more
+#pragma unroll 1                              // (unrolled, its code took 0.3 us to fetch)
+  for (int i = tid; i < a.n; i += SP_THREADS) {
+    const int from = max(0, min(a.groups[i], B)), to = max(0, min(a.groups[i + 1], B));
+    if (i <= g) r0 = min(r0, -from);
+    several += to - from >= 2;
+  }
   const int edge = max(0, min(a.groups[g + 1], B)), said = a.shared[g];
   // (with the offsets, before it is known which requests matter: the tokens in front of
   // a request's rows)
@@ -151,7 +156,7 @@ __global__ void __launch_bounds__(SP_THREADS) kv_plan_kernel(const PlanArgs a) {
     return n > 0 ? max(0, min(a.lens[b], a.capacity)) - n : 0x7FFFFFFF;
   };
   const int mine = tid < B ? in_front(tid) : 0x7FFFFFFF;
-  plan_reduce(r0, none, none, sm[0]);
+  plan_reduce(r0, several, none, sm[0]);
   r0 = -r0;
   const int r1 = max(r0, edge);
   // the tokens that stand in front of every row of the group, and its first request with rows
@@ -200,7 +205,8 @@ __global__ void __launch_bounds__(SP_THREADS) kv_plan_kernel(const PlanArgs a) {
     cluster_arrive();
   }
   int keys = agree < pages ? agree << a.page_shift : max(0, most);
-  if (static_cast<long long>(keys) * (with_rows - 1) < a.worth) keys = 0;
+  // (what is asked of all, as if the groups that can share anything were alike)
+  if (static_cast<long long>(keys) * (with_rows - 1) * max(1, several) < a.worth) keys = 0;
   auto entry = [&](int i, int q0, int q1, int len, int start, int row, int prefix, float t0, float t1) {
     int4* e = reinterpret_cast<int4*>(a.list + i);
     e[0] = make_int4(q0, q1, len, start);
@@ -425,14 +431,15 @@ cudaError_t launch_kv_attention_shared(const KvAttn& q, const KvGroups& g, cudaS
   const size_t need = kv_attention_shared_workspace_bytes(q.tokens, q.q_heads, c.heads, c.d, q.max_q,
                                                           q.requests, g.n);
   // Without groups or room for the states, or where not even prefixes as long as the table
-  // would be worth a pass, or the requests' rows are many: each request for itself.
+  // would be worth a pass (groups may be empty: one of all requests spares most), or the
+  // requests' rows are many: each request for itself.
   const int64_t most = q.width << kv_page_shift(c.page);
   // (Q may have room for more rows than the requests have)
   const int64_t tokens = std::min(q.tokens, std::max<int64_t>(1, q.max_q) * q.requests);
   const int64_t bytes = 2 * c.heads * c.d, worth = g_worth.load(std::memory_order_relaxed);
   if (g.n == 0 || need == 0 || q.ws == nullptr || q.ws_bytes < need ||
-      (q.requests - g.n) * most < worth / bytes ||
-      (worth > 0 && tokens * (q.q_heads / c.heads) > SP_MOST_ROWS * q.requests))
+      (worth > 0 && ((q.requests - 1) * most < worth / bytes ||
+                     tokens * (q.q_heads / c.heads) > SP_MOST_ROWS * q.requests)))
     return launch_kv_attention(q, st);
   const Layout l = layout_of(q.tokens, q.q_heads, c.heads, c.d, q.max_q, q.requests, g.n, sms);
   char* ws = static_cast<char*>(q.ws) + (reinterpret_cast<uintptr_t>(q.ws) & 16);
@@ -455,7 +462,7 @@ cudaError_t launch_kv_attention_shared(const KvAttn& q, const KvGroups& g, cudaS
   p.table_stride = q.table_stride;
   p.requests = static_cast<int>(q.requests);
   p.n = static_cast<int>(g.n);
-  p.worth = worth / bytes / g.n;            // (as if the groups were alike)
+  p.worth = worth / bytes;
   p.capacity = static_cast<int>(most < 0x7FFFFF00 ? most : 0x7FFFFF00);
   p.page_shift = kv_page_shift(c.page);
   p.list = list;

@@ -736,7 +736,9 @@ mx_status mx_kv_attention(const void* Q, int32_t dtype, int64_t tokens, int64_t 
  *   groups     device, int32, n_groups + 1 entries: group g is the requests groups[g] ..
  *              groups[g + 1] - 1.  Offsets outside 0 .. requests count as the nearest of
  *              the two, one below an earlier one as that one; requests in front of the
- *              first group and behind the last share nothing
+ *              first group and behind the last share nothing.  Groups may be empty, but the
+ *              kernels are picked as if they were alike: n_groups is best the number of
+ *              those that there are
  *   shared     device, int32, n_groups entries: how many of its first tokens a group's
  *              requests have in common, or more.  Shared are those in front of the first page
  *              on which the rows of the table of requests that have rows of Q differ, and in
@@ -801,12 +803,13 @@ int32_t mx_version(void);
  * MX_ERR_INVALID_ARG for any other value. */
 mx_status mx_set_tile_width(int32_t tbn);
 
-/* Tuning and testing knob: mx_kv_attention_shared shares a prefix where that
+/* Tuning and testing knob: mx_kv_attention_shared shares prefixes where that
  * saves at least this many bytes of reads (keys and values of the prefix, times the
- * requests that are spared them); 0: always, -1 (the default): 150 MiB, below which it
+ * requests that are spared them; of several groups with two requests or more each is asked
+ * for its even part); 0: always, -1 (the default): 150 MiB, below which it
  * takes longer than mx_kv_attention.  Unless always, not where the requests have more
- * than 192 rows for a cache head on the average either.  Process-wide: set it while no other thread makes that
- * call.  Returns MX_ERR_INVALID_ARG for other negative values. */
+ * than 192 rows for a cache head on the average either.  Process-wide: set it while no
+ * other thread makes that call.  Returns MX_ERR_INVALID_ARG for other negative values. */
 mx_status mx_set_shared_bytes(int64_t bytes);
 
 #ifdef __cplusplus
