@@ -1182,7 +1182,7 @@ def kv_attention_shared_workspace_bytes(tokens: int, q_heads: int, heads: int,
                                         d: int, max_q: int, requests: int,
                                         groups: int) -> int:
     """Bytes of workspace with which mx_kv_attention_shared reads a group's
-    common keys once; they grow with each argument."""
+    common keys once; they grow with each argument but heads."""
     return int(lib().mx_kv_attention_shared_workspace_bytes(
         tokens, q_heads, heads, d, max_q, requests, groups))
 

@@ -746,8 +746,9 @@ mx_status mx_kv_attention(const void* Q, int32_t dtype, int64_t tokens, int64_t 
  *              request that adds no tokens, or has ended, has no say.  (Prefixes that
  *              are not worth it are not shared: mx_set_shared_bytes.)
  *   workspace  as for mx_kv_attention, at least mx_kv_attention_shared_workspace_bytes()
- *              bytes, which grow with each argument; NULL or a smaller size, or no groups:
- *              every request reads its keys itself, as mx_kv_attention does
+ *              bytes, which grow with each argument but `heads` (fewer cache heads have
+ *              more rows each); NULL or a smaller size, or no groups: every request reads
+ *              its keys itself, as mx_kv_attention does
  * requests and n_groups up to 16384, tokens * q_heads below 2^31.  The other arguments,
  * results and bounds are those of mx_kv_attention, whose last bits may differ.
  */

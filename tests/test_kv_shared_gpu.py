@@ -530,3 +530,19 @@ def test_small_groups_do_not_make_a_prefix_worth_it():
     b = Batch([(40000, [(1 + 3 * i, 1) for i in range(15)]), (0, [(40, 1), (9, 1)])] + [(0, [(30, 1)])] * 6, 4, 1, 64, 128, seed=35)
     got, none = _by_default(b, b.edges, [10 ** 9] * 8)
     assert torch.equal(got, none)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_workspace_grows_with_each_argument_but_heads(d):
+    size = mx.kv_attention_shared_workspace_bytes
+    least = dict(tokens=1, q_heads=8, heads=4, d=d, max_q=1, requests=1, groups=1)
+    steps = dict(tokens=[1, 2, 4, 15, 16, 17, 31, 300], q_heads=[4, 8, 12, 32, 64, 128, 256], max_q=[1, 3, 8, 9, 16, 17, 40],
+                 requests=[1, 2, 100, 16384], groups=[1, 5, 100, 16384])
+    for others in (least, dict(least, tokens=40), dict(least, max_q=20), dict(least, q_heads=64, tokens=7, max_q=3)):
+        for name, values in steps.items():
+            n = [size(**dict(others, **{name: v})) for v in values]
+            assert min(n) > 0 and n == sorted(n)
+        assert size(**dict(others, d=64)) < size(**dict(others, d=128))
+    # fewer cache heads are more rows to each, for which another kernel wants other room
+    n = [size(16, 32, h, d, 1, 4, 1) for h in (1, 2, 8, 32)]
+    assert n == sorted(n, reverse=True) and n[0] > n[-1]
