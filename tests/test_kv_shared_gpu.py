@@ -546,3 +546,44 @@ def test_the_workspace_grows_with_each_argument_but_heads(d):
     # fewer cache heads are more rows to each, for which another kernel wants other room
     n = [size(16, 32, h, d, 1, 4, 1) for h in (1, 2, 8, 32)]
     assert n == sorted(n, reverse=True) and n[0] > n[-1]
+
+
+def test_many_rows_whose_own_keys_weigh():
+    """By default, both passes by the prompt kernel side by side: requests of 150 rows whose own keys, and the prefix's
+    last ones, take about half of the softmax, some rows of them against 64 bits.  Of a row's keys, the one at its
+    own position weighs 2^-9 or more, where the bound allows 2^-11: a mask that is off by one is seen."""
+    n, common, rows = 12, 16384, 150
+    b = Batch([(common, [(rows + 9 * i, rows) for i in range(n)])], 4, 4, 128, 128, seed=36, spread=0.5)
+    k, v, ks, vs = [t.copy() for t in b.planes]
+    ks[:] = 127 - 9                              # |k| < 1
+    k[..., 0] = 0
+    k[b.table[0, common // 128 - 1], :, -5:, 0] = 0x7E
+    for i in range(n):
+        k[b.table[i, common // 128:-(-b.lens[i] // 128)], ..., 0] = 0x7E      # 448 * 2^-9
+    b.q *= 0.25                                  # scores of 0.1 or so
+    b.q[..., 0] = 57.0                           # and 57 * 0.875 / sqrt(128) = 4.4 for those keys: 82 times the weight
+    b.planes = k, v, ks, vs
+    b.cache = mx.KVCache(*[torch.from_numpy(t).cuda() for t in b.planes], b.fmt)
+    plain = mx.mx_kv_attention(b.q.cuda(), b.cache, _i32(b.table), _i32(b.lens), _i32(b.cu), b.most,
+                               workspace=b.workspace(), out_dtype=F32)
+    try:
+        mx.set_shared_bytes(-1)
+        got = b.run(out_dtype=F32)
+    finally:
+        mx.set_shared_bytes(0)
+    assert not torch.equal(got, plain)           # it was shared
+    some = [(r, i) for r in (0, 1, 7, 11) for i in (0, 1, 63, 127, 128, 149)]
+    at = [int(b.cu[r]) + i for r, i in some]
+    lens = np.array([b.lens[r] - rows + i + 1 for r, i in some])
+    table, one = b.table[[r for r, _ in some]], np.arange(len(some) + 1)
+
+    def exact(lens):
+        return _kv.attention(b.q[at].double().numpy(), *b.planes, b.fmt, table, lens, one, 128 ** -0.5)
+
+    e = exact(lens)
+    bound = _kv.bound(*e, F32)
+    for out in (got, plain):
+        assert (np.abs(out[at].double().cpu().numpy() - e[0]) <= bound).all()
+    for other in (lens - 1, np.full_like(lens, common)):      # without a row's last key, and without all of its own
+        assert (np.abs(exact(other)[0] - e[0]) > bound).any(2).all()
+    assert mx.mx_last_error() == 0
