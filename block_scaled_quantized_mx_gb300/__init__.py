@@ -689,7 +689,8 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "parts",
       base    the base raised so that the slowest pair's is divided by factor
       parts   pairs that turn `fast` times or more in `original` positions keep
               theirs, those that turn `slow` times or less have it divided, in
-              between in proportion; cosines and sines times 1 + 0.1 ln factor"""
+              between in proportion; cosines and sines times 1 + 0.1 ln factor
+    Computed in doubles: a frequency is within 2^-52 turns of this."""
     if rot < 16 or rot % 16:
         raise ValueError("rot must be a multiple of 16")
     if not base > 1.0 or not 1.0 <= factor < math.inf:

@@ -7,8 +7,9 @@
 //
 // Angles.  A frequency is a number of turns for each position, kept as a whole
 // number of 2^-64 turns: position * freq in 64 bits that wrap is then the angle
-// modulo one turn, exactly, at any position (of freq itself 2^-65 turns are lost, at
-// position 2^31 2^-34).  What is left is in [-1/2, 1/2) turns, where fp32 serves.
+// modulo one turn, exactly, at any position.  (Of a frequency itself 2^-65 turns are lost where
+// freq is the nearest whole number; mx.rope_frequencies computes in doubles, within 2^-52 turns, at
+// position 2^20 2^-32, at 2^31 2^-21.)  What is left is in [-1/2, 1/2) turns, where fp32 serves.
 //
 // Bound: HBM, each value read and written once.  Cosines and sines are computed
 // once per token for all heads and both operands, into shared memory; the values' loads

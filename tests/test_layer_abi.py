@@ -2,6 +2,7 @@
 the host before any launch, the binding's checks, and the tests' restatement
 against hand values."""
 import ctypes
+import decimal
 import math
 
 import numpy as np
@@ -97,6 +98,46 @@ def test_frequencies_by_hand():
     assert f.factor == 1.0 and f.freq[0].item() == round(2.0 ** 64 / (2 * math.pi)) and f.freq.numel() == 8
     g = mx.rope_frequencies(16, 10000.0, "linear", 4.0, device="cpu")
     assert all(abs(4 * b - a) <= 4096 for a, b in zip(f.freq.tolist(), g.freq.tolist()))
+
+
+def _quarter_turns(bits):
+    """pi / 4 times 2^bits, by Machin's formula in whole numbers."""
+    def arctan(n):
+        term, total, k = (1 << (bits + 40)) // n, 0, 0
+        while term:
+            total += (-1) ** k * term // (2 * k + 1)
+            term, k = term // (n * n), k + 1
+        return total
+    return (4 * arctan(5) - arctan(239)) >> 40
+
+
+@pytest.mark.parametrize("rot,base,scaling,factor", [
+    (16, 10000.0, "parts", 1.0), (64, 10000.0, "linear", 8.0), (128, 500000.0, "linear", 3.0), (256, 2.0, "linear", 1.0),
+    (16, 10000.0, "base", 128.0), (64, 500000.0, "parts", 8.0), (128, 10000.0, "parts", 4.0)])
+def test_frequencies_against_roots(rot, base, scaling, factor):
+    """Powers of base^(-2 / rot) as repeated square roots, in 60 digits.  The library's are doubles: of
+    x = base^(-2 i / rot) the exponent's rounding costs ln(1 / x) 2^-53 of itself, the power two and the base (raised)
+    one, a scaling three at most, 2 pi and the division two.  x (8 + ln(1 / x)) is 8 at most: 8 / 2 pi 2^-53 turns, less
+    than 2^-52."""
+    D, before = decimal.Decimal, decimal.getcontext().prec
+    decimal.getcontext().prec = 60
+    two_pi = D(8 * _quarter_turns(200)) / (1 << 200)
+    b = D(base)
+    if scaling == "base":                        # 128^(16 / 14) = 2^8
+        b *= 256
+    step, k = b, rot // 2
+    while k > 1:
+        step, k = step.sqrt(), k // 2
+    want = [step ** -i for i in range(rot // 2)]
+    if scaling == "linear":
+        want = [x / D(factor) for x in want]
+    if scaling == "parts":
+        keep = [min(D(1), max(D(0), (8192 * x / two_pi - 1) / 31)) for x in want]
+        want = [x * a + x / D(factor) * (1 - a) for x, a in zip(want, keep)]
+    got = mx.rope_frequencies(rot, base, scaling, factor, original=8192, device="cpu").freq.tolist()
+    off = [abs(D(g) - x / two_pi * 2 ** 64) for g, x in zip(got, want)]
+    decimal.getcontext().prec = before
+    assert len(got) == rot // 2 and max(off) <= 2 ** 12
 
 
 def test_restatement_by_hand():
