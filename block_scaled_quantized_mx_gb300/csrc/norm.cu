@@ -369,9 +369,10 @@ cudaError_t launch_rmsnorm_quantize(const void* x, int x_dtype, int64_t x_ld, co
   a.sf = sf;
   const unsigned ctas = static_cast<unsigned>(sf_row_atoms(rows) * SF_ATOM_ROWS);
   // As few chunks a thread as 1024 threads allow where the rows do not fill the
-  // SMs (a row's time is what counts); where they do, about 256 threads (8192 rows of
+  // SMs (a row's time is what counts); where they do, one to 2048 values, two below
+  // 8192, four to 16384, so that longer rows have 130 to 512 threads (8192 rows of
   // 8192 with 1, 2, 4 and 8 chunks 104, 95, 77 and 96 us; 4097 of 5120, fp32 residual,
-  // 39, 38, 41 and 50).
+  // 39, 38, 41 and 50; where two and four cross between those widths is not measured).
   const bool few = rows <= 2 * 152;
   int ch = a.chunks <= 256 ? 1 : a.chunks < 1024 ? 2 : a.chunks <= 2048 ? 4 : 8;
   if (few && a.chunks <= 2048) ch = a.chunks <= 1024 ? 1 : 2;

@@ -76,7 +76,7 @@ class Server:
         (int32, on the GPU); x: the new tokens' hidden states, request by
         request; most_new: the most any request adds.  fork: (src, dst, tokens),
         requests that begin as copies of others' first tokens; groups: offsets of requests
-        that may have a prefix in common.  Returns the layer's output for the new tokens, and
+        that may have a prefix in common, which stand side by side.  Returns the layer's output for the new tokens, and
         what the attention saw."""
         cut = mx.mx_kv_release(self.lens, keep, self.table, self.stack, self.counts, self.refs,
                                self.page)

@@ -448,9 +448,9 @@ mx_status mx_rmsnorm_quantize(const void* X, int32_t x_dtype, int64_t ldx, const
 
 /*
  * mx_dequantize -- the values of an MX tensor of any format as a plain outer x K
- * row-major matrix: code * scale, exact in fp32 and rounded to nearest even in the
- * 16-bit types (bf16 holds every value of every format for scales 2^-110 .. 2^110);
- * NaN under a scale of 0xFF.
+ * row-major matrix: code * scale, exact in fp32 (infinite where that is beyond it) and
+ * rounded to nearest even in the 16-bit types (bf16 holds every value of every format for
+ * scales 2^-110 .. 2^110); NaN under a scale of 0xFF.
  *
  *   out    device, dtype (any mx_dtype), 16-byte aligned; ld >= K, a multiple of
  *          16 bytes
@@ -747,8 +747,9 @@ mx_status mx_kv_attention(const void* Q, int32_t dtype, int64_t tokens, int64_t 
  *              are not worth it are not shared: mx_set_shared_bytes.)
  *   workspace  as for mx_kv_attention, at least mx_kv_attention_shared_workspace_bytes()
  *              bytes, which grow with each argument but `heads` (fewer cache heads have
- *              more rows each); NULL or a smaller size, or no groups: every request reads
- *              its keys itself, as mx_kv_attention does
+ *              more rows each): 8 d + 48 for each row of Q and query head, whether it will
+ *              share anything or not, and up to 84 MB; NULL or a smaller size, or no groups:
+ *              every request reads its keys itself, as mx_kv_attention does
  * requests and n_groups up to 16384, tokens * q_heads below 2^31.  The other arguments,
  * results and bounds are those of mx_kv_attention, whose last bits may differ.
  */
