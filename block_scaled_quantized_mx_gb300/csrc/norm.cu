@@ -197,7 +197,10 @@ __global__ void __launch_bounds__(CH <= 2 ? 1024 : 512) rmsnorm_quantize_kernel(
         for (int e = 0; e < 8; ++e) {
           const float n = h[i][e] * f;
           y[e] = n * ww[e];
-          if (FAR && fabsf(n) < 1.17549435e-38f && h[i][e] != 0.0f) y[e] = h[i][e] * (f * ww[e]);
+          if (FAR && fabsf(n) < 1.17549435e-38f && h[i][e] != 0.0f) {
+            const float by = f * ww[e];      // (beyond fp32 for a subnormal h under 2^105 and more)
+            if (fabsf(by) <= 3.402823466e38f) y[e] = h[i][e] * by;
+          }
         }
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {

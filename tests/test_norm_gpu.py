@@ -146,6 +146,18 @@ def test_large_eps(rows, K):
         _check(q, small, None, w * up, 3e38, mx.E5M2, None)
 
 
+def test_subnormal_values_under_huge_weights():
+    """h f is sqrt(2) 2^-127, with 22 bits, and y sqrt(2) 2^-19 under a weight of 2^108: f w is beyond fp32, y is not."""
+    x = torch.full((2, 64), 2.0 ** -22, device="cuda")
+    x[:, 32:] = 2.0 ** -149
+    x[1, ::2] *= -1
+    w = torch.ones(64, device="cuda")
+    w[32:] = 2.0 ** 108
+    for fmt in (mx.E4M3, mx.E5M2, mx.E2M1):
+        q, _ = mx.mx_rmsnorm_quantize(x, w, fmt, eps=1e-30)
+        _check(q, x, None, w, 1e-30, fmt, None)
+
+
 def test_nan_and_infinity_stay_in_their_rows():
     x = torch.randn(4, 256, device="cuda")
     x[1, 40], x[2, 100] = float("nan"), float("inf")
